@@ -376,6 +376,76 @@ la_status la_layer_decode_step(const void* x, const void* Wqkv, const void* Wo, 
                                void* workspace, size_t workspace_bytes, la_stream_t stream);
 
 /*
+ * Position rotation with an optional per-head RMS norm, in the pass that takes
+ * queries and keys from the token-major projection to the head-major layout of
+ * the attention entries ("Why Replace Attention? The Softmax Bottleneck and the
+ * Path to Linear Time", section 7.2, step 1, leaves the linear maps of the
+ * token's hidden state as the attention's inputs; norm and rotation sit between
+ * the two). The pages have no counterpart; the definitions, for a row x of D
+ * values (one token, one head):
+ *   u = w x / sqrt(mean(x^2) + eps)   (norm != 0; w = 1 when null), else u = x
+ *   pair i of the first 2 `pairs` values of u, (a, b) ->
+ *     (a cos t - b sin t, b cos t + a sin t),  t = pos[b, n, axis_i] inv_freq_i
+ *   the values past them pass unrotated.
+ * Pairs are (i, i + pairs) in LA_ROPE_HALVES, (2i, 2i + 1) in
+ * LA_ROPE_INTERLEAVED. Each pair belongs to one of 1 to LA_ROPE_MAX_AXES position
+ * axes: one axis for text, rows and columns for images, time, height and width
+ * for video.
+ *
+ * la_rope_table fills the HOST array table[2 * pairs] from inv_freq (radians per
+ * position, finite) and axis (null: all 0): entry i is (inv_freq_i / 2 pi as a
+ * whole number of 2^-64 turns, axis_i). pos * step modulo 2^64 is then the
+ * angle's fraction of a turn, without loss for any int32 position. The caller
+ * copies the table to the device (16-byte aligned) once.
+ */
+#define LA_ROPE_MAX_AXES 4
+enum { LA_ROPE_HALVES = 0, LA_ROPE_INTERLEAVED = 1 };
+
+la_status la_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int axes,
+                        int64_t* table);
+
+/*
+ * Forward. q: rows of [B, N, Hq, D] with batch stride q_batch and token stride
+ * q_token in elements (heads D apart: the projection's own layout); k the same
+ * with Hk heads. qo: [B, Hq, N, D], ko: [B, Hk, N, D], contiguous. wq, wk: [D] in
+ * dtype dt, nullable. pos: [B, N, axes] int32. Hq or Hk may be 0 (its pointers
+ * are then ignored). Arithmetic, statistics and angles are fp32 from exact
+ * angles; each output is rounded once. 1 <= D <= 128, 2 pairs <= D.
+ *  - D a multiple of 8, pairs a multiple of 4 and 16-byte aligned rows run the
+ *    vector kernels, anything else one warp per row.
+ *  - A table entry whose axis is >= axes uses the last axis.
+ *  - Outputs must not overlap inputs. Needs no workspace; asynchronous on `stream`.
+ */
+la_status la_qk_norm_rope_fwd(const void* q, int64_t q_batch, int64_t q_token, const void* k,
+                              int64_t k_batch, int64_t k_token, const void* wq, const void* wk,
+                              const int32_t* pos, int axes, const int64_t* table, int pairs,
+                              void* qo, void* ko, int B, int N, int Hq, int Hk, int D, la_dtype dt,
+                              int norm, float eps, int layout, la_stream_t stream);
+
+/*
+ * Backward: from dqo = dL/dqo and dko = dL/dko (contiguous, head-major) writes
+ * dq and dk (rows of [B, N, H, D] with their own batch and token strides, which
+ * may be column ranges of one projection gradient; rows must not overlap:
+ * LA_ERR_INVALID_ARG) and, with the norm, dwq, dwk [D] float32 (nullable). With
+ * g = R^T dout (rotation by -t), r = 1 / sqrt(mean(x^2) + eps):
+ *   dw = sum over rows of g r x,   dx = r w g - x r^3 mean(w g x)   (dx = g without the norm).
+ * Sums are fp32 in a fixed order: the same inputs give the same bits.
+ *  - q, k may be null when norm == 0.
+ *  - workspace (norm only): la_qk_norm_rope_bwd_workspace_size() bytes, 256-byte
+ *    aligned; it needs no initialisation.
+ */
+la_status la_qk_norm_rope_bwd_workspace_size(int B, int N, int Hq, int Hk, int D, size_t* bytes);
+
+la_status la_qk_norm_rope_bwd(const void* q, int64_t q_batch, int64_t q_token, const void* k,
+                              int64_t k_batch, int64_t k_token, const void* wq, const void* wk,
+                              const int32_t* pos, int axes, const int64_t* table, int pairs,
+                              const void* dqo, const void* dko, void* dq, int64_t dq_batch,
+                              int64_t dq_token, void* dk, int64_t dk_batch, int64_t dk_token,
+                              float* dwq, float* dwk, int B, int N, int Hq, int Hk, int D,
+                              la_dtype dt, int norm, float eps, int layout, void* workspace,
+                              size_t workspace_bytes, la_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the workspace status word.
  * Returns LA_OK, LA_ERR_TIMEOUT (a bounded wait expired in an earlier call
  * that used this workspace) or LA_ERR_CUDA.

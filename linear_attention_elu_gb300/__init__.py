@@ -9,6 +9,7 @@ device memory and streams.
 Importing the package loads the library and fails loudly if it has not been
 built (``python linear_attention_elu_gb300/build.py``).
 """
+import contextlib
 import ctypes
 import os
 
@@ -24,13 +25,16 @@ __all__ = [
     "la_causal_bwd", "LA_OP_CAUSAL_BWD", "la_noncausal_bwd", "LA_OP_NONCAUSAL_BWD",
     "LA_PHI_ELU1", "LA_PHI_IDENTITY", "la_positive_random_features", "LA_OP_LAYER_DECODE",
     "la_layer_decode_step", "la_causal_fwd_noalloc", "la_noalloc_query_status",
-    "la_noalloc_set_wait_limit", "library_path",
+    "la_noalloc_set_wait_limit", "library_path", "LA_ROPE_MAX_AXES", "la_rope_table",
+    "la_qk_norm_rope_fwd", "la_qk_norm_rope_bwd", "la_qk_norm_rope_bwd_workspace_size",
+    "qk_norm_rope_workspace",
 ]
 
 LA_F32, LA_BF16 = 0, 1
 LA_OP_NONCAUSAL, LA_OP_CAUSAL, LA_OP_DECODE, LA_OP_CAUSAL_BWD, LA_OP_NONCAUSAL_BWD = 0, 1, 2, 3, 4
 LA_OP_LAYER_DECODE = 5
 LA_PHI_ELU1, LA_PHI_IDENTITY = 0, 1
+LA_ROPE_HALVES, LA_ROPE_INTERLEAVED, LA_ROPE_MAX_AXES = 0, 1, 4
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_WORKSPACE, LA_ERR_CUDA, LA_ERR_TIMEOUT = 0, 1, 2, 3, 4, 5
 
 _DTYPES = {torch.float32: LA_F32, torch.bfloat16: LA_BF16}
@@ -101,6 +105,16 @@ def _load():
     lib.la_noalloc_set_wait_limit.restype = I
     lib.la_layer_decode_step.argtypes = [P, P, P, P, P, P, I, I, I, I, F, P, Z, P]
     lib.la_layer_decode_step.restype = I
+    lib.la_rope_table.argtypes = [P, P, I, I, P]
+    lib.la_rope_table.restype = I
+    lib.la_qk_norm_rope_fwd.argtypes = [P, L, L, P, L, L, P, P, P, I, P, I, P, P, I, I, I, I, I, I,
+                                        I, F, I, P]
+    lib.la_qk_norm_rope_fwd.restype = I
+    lib.la_qk_norm_rope_bwd_workspace_size.argtypes = [I, I, I, I, I, ctypes.POINTER(Z)]
+    lib.la_qk_norm_rope_bwd_workspace_size.restype = I
+    lib.la_qk_norm_rope_bwd.argtypes = [P, L, L, P, L, L, P, P, P, I, P, I, P, P, P, L, L, P, L, L,
+                                        P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
+    lib.la_qk_norm_rope_bwd.restype = I
     lib.la_query_status.argtypes = [P, P]
     lib.la_query_status.restype = I
     return lib
@@ -450,6 +464,173 @@ def la_layer_decode_step(x, Wqkv, Wo, S, z, H, y=None, eps=1e-6, ws=None, stream
                                      _stream(stream)),
            "la_layer_decode_step")
     return y
+
+
+def _scope(dev, stream):
+    """Context in which a call on tensors of `dev` allocates and launches: that device, and the
+    given stream (so that what the call allocates belongs to the stream that uses it)."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _same_cuda(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must be on one CUDA device")
+
+
+def _token_rows(t, what, heads):
+    """(batch stride, token stride) of a [B, N, heads, D] tensor whose heads are D apart and whose
+    D values are adjacent (a column range of a projection, for instance)."""
+    B, N, H, D = t.shape
+    sb, sn, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{what}: the {heads} of a token must be adjacent [.., H, D] values "
+                         f"(strides {t.stride()})")
+    return sb, sn
+
+
+def la_rope_table(inv_freq, axis=None, device="cuda"):
+    """Table of the position rotation: int64 [pairs, 2] on `device`, one (step, axis) per pair.
+
+    inv_freq: radians per position of each rotated pair (a sequence or CPU tensor of float64);
+    axis: the position axis of each pair (default: all 0)."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    if f.dim() != 1:
+        raise ValueError("inv_freq must be one-dimensional")
+    ax = None
+    if axis is not None:
+        ax = torch.as_tensor(axis, device="cpu").to(torch.int32).contiguous()
+        if ax.shape != f.shape:
+            raise ValueError("axis must have one entry per pair")
+    table = torch.empty(f.numel(), 2, dtype=torch.int64)
+    _check(_lib.la_rope_table(_ptr(f), _ptr(ax), f.numel(), LA_ROPE_MAX_AXES, _ptr(table)),
+           "la_rope_table")
+    return table.to(device)
+
+
+def _rope_args(q, k, pos, table, wq, wk, norm):
+    """Checks shared by both directions; returns (B, N, Hq, Hk, D, axes)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    for t in (q, k):
+        if t is not None and (t.dim() != 4 or t.shape[:2] != ref.shape[:2] or t.shape[3] != ref.shape[3]):
+            raise ValueError("expected q [B,N,Hq,D] and k [B,N,Hk,D]")
+        if t is not None and t.dtype != ref.dtype:
+            raise TypeError("q and k must share one dtype")
+    _dt(ref)
+    if not ref.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    B, N, _, D = ref.shape
+    for w in (wq, wk):
+        if w is None:
+            continue
+        if not norm:
+            raise ValueError("norm weights need norm=True")
+        if tuple(w.shape) != (D,) or w.dtype != ref.dtype or not w.is_contiguous():
+            raise ValueError("norm weights must be contiguous [D] in q's dtype")
+    if pos.dtype != torch.int32 or not pos.is_contiguous() or tuple(pos.shape[:2]) != (B, N) \
+            or pos.dim() not in (2, 3):
+        raise ValueError("pos must be contiguous int32 [B,N] or [B,N,axes]")
+    axes = pos.shape[2] if pos.dim() == 3 else 1
+    if table.dtype != torch.int64 or table.dim() != 2 or table.shape[1] != 2 or not table.is_contiguous():
+        raise ValueError("table must come from la_rope_table (int64 [pairs, 2])")
+    _same_cuda(ref.device, q, k, pos, table, wq, wk)
+    return B, N, q.shape[2] if q is not None else 0, k.shape[2] if k is not None else 0, D, axes
+
+
+def _head_major(t, B, H, N, D, like, what):
+    if tuple(t.shape) != (B, H, N, D) or t.dtype != like.dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous [B,H,N,D] = {(B, H, N, D)} in q's dtype")
+
+
+def la_qk_norm_rope_fwd(q, k, pos, table, wq=None, wk=None, norm=True, eps=1e-6, interleaved=False,
+                        qo=None, ko=None, stream=None):
+    """Per-head RMS norm (norm=True) and position rotation of q [B,N,Hq,D] and k [B,N,Hk,D].
+
+    q and k may be column ranges of one projection; either may be None. pos: int32 [B,N] or
+    [B,N,axes]; table: la_rope_table. Returns (qo [B,Hq,N,D], ko [B,Hk,N,D]), head-major, ready
+    for the attention entries."""
+    B, N, Hq, Hk, D, axes = _rope_args(q, k, pos, table, wq, wk, norm)
+    ref = q if q is not None else k
+    qs = _token_rows(q, "q", "heads") if q is not None else (0, 0)
+    ks = _token_rows(k, "k", "heads") if k is not None else (0, 0)
+    with _scope(ref.device, stream):
+        if qo is None and q is not None:
+            qo = torch.empty((B, Hq, N, D), dtype=ref.dtype, device=ref.device)
+        if ko is None and k is not None:
+            ko = torch.empty((B, Hk, N, D), dtype=ref.dtype, device=ref.device)
+        for t, H, what in ((qo, Hq, "qo"), (ko, Hk, "ko")):
+            if t is not None:
+                _head_major(t, B, H, N, D, ref, what)
+        _same_cuda(ref.device, qo, ko)
+        _check(_lib.la_qk_norm_rope_fwd(_ptr(q), qs[0], qs[1], _ptr(k), ks[0], ks[1], _ptr(wq),
+                                        _ptr(wk), _ptr(pos), axes, _ptr(table), table.shape[0],
+                                        _ptr(qo), _ptr(ko), B, N, Hq, Hk, D, _dt(ref),
+                                        1 if norm else 0, float(eps), 1 if interleaved else 0,
+                                        _stream(stream)),
+               "la_qk_norm_rope_fwd")
+    return qo, ko
+
+
+def la_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hk, D):
+    """Workspace bytes of la_qk_norm_rope_bwd with the norm."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.la_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hk, D, ctypes.byref(n)),
+           "la_qk_norm_rope_bwd_workspace_size")
+    return int(n.value)
+
+
+def qk_norm_rope_workspace(B, N, Hq, Hk, D, device=None):
+    """Allocates (through PyTorch) the workspace of la_qk_norm_rope_bwd; it needs no initialisation."""
+    n = la_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hk, D)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, wq=None, wk=None, norm=True, eps=1e-6,
+                        interleaved=False, dq=None, dk=None, ws=None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) of sum(qo * dqo) + sum(ko * dko) of la_qk_norm_rope_fwd.
+
+    dq [B,N,Hq,D] and dk [B,N,Hk,D] may be given as column ranges of one projection gradient.
+    dwq, dwk are float32 [D], None without the norm (or without weights of that side)."""
+    B, N, Hq, Hk, D, axes = _rope_args(q, k, pos, table, wq, wk, norm)
+    ref = q if q is not None else k
+    qs = _token_rows(q, "q", "heads") if q is not None else (0, 0)
+    ks = _token_rows(k, "k", "heads") if k is not None else (0, 0)
+    for t, x, H, what in ((dqo, q, Hq, "dqo"), (dko, k, Hk, "dko")):
+        if (t is None) != (x is None):
+            raise ValueError(f"{what} must be given exactly when its input is")
+        if t is not None:
+            _head_major(t, B, H, N, D, ref, what)
+    with _scope(ref.device, stream):
+        dq = torch.empty((B, N, Hq, D), dtype=ref.dtype, device=ref.device) if dq is None and q is not None else dq
+        dk = torch.empty((B, N, Hk, D), dtype=ref.dtype, device=ref.device) if dk is None and k is not None else dk
+        for t, x, what in ((dq, q, "dq"), (dk, k, "dk")):
+            if t is not None and (x is None or t.shape != x.shape or t.dtype != ref.dtype):
+                raise ValueError(f"{what} must be shaped and typed like its input")
+        dqs = _token_rows(dq, "dq", "heads") if dq is not None else (0, 0)
+        dks = _token_rows(dk, "dk", "heads") if dk is not None else (0, 0)
+        dwq = torch.empty(D, dtype=torch.float32, device=ref.device) if wq is not None else None
+        dwk = torch.empty(D, dtype=torch.float32, device=ref.device) if wk is not None else None
+        if ws is None and norm:
+            ws = qk_norm_rope_workspace(B, N, Hq, Hk, D, ref.device)
+        _same_cuda(ref.device, dqo, dko, dq, dk, ws)
+        _check(_lib.la_qk_norm_rope_bwd(_ptr(q), qs[0], qs[1], _ptr(k), ks[0], ks[1], _ptr(wq),
+                                        _ptr(wk), _ptr(pos), axes, _ptr(table), table.shape[0],
+                                        _ptr(dqo), _ptr(dko), _ptr(dq), dqs[0], dqs[1], _ptr(dk),
+                                        dks[0], dks[1], _ptr(dwq), _ptr(dwk), B, N, Hq, Hk, D,
+                                        _dt(ref), 1 if norm else 0, float(eps),
+                                        1 if interleaved else 0, _ptr(ws),
+                                        ws.numel() * ws.element_size() if ws is not None else 0,
+                                        _stream(stream)),
+               "la_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
 
 
 def la_query_status(ws, stream=None):

@@ -1,0 +1,722 @@
+// Per-head RMS norm of queries and keys and the position rotation, in the pass
+// that takes them from the token-major projection [B, N, H, D] to the
+// head-major layout [B, H, N, D] of the attention entries; and its backward.
+//
+// Forward, per row x (one token of one head), with r = 1 / sqrt(mean x^2 + eps):
+//   u = r w x (or x without the norm);  a rotated pair (a, b) of u becomes
+//   (a cos t - b sin t, b cos t + a sin t),  t = pos[axis_i] f_i.
+// Backward, from g_out: g = R^T g_out (the rotation by -t),
+//   dw = sum over rows of g r x,   dx = r (w g) - x r^3 mean(w g x).
+//
+// Angles. A pair's table entry holds its frequency as a whole number of 2^-64
+// turns, so pos * step modulo 2^64 is the angle's fraction of a turn, exact for
+// every position (wrap-around is the reduction modulo 2 pi); its top 32 bits go
+// through sincospif. No table over positions, no loss for far tokens.
+//
+// What bounds it: every value is read once and written once (the backward also
+// reads the gradient), two dozen operations each: HBM bandwidth. A group of D/8
+// lanes owns one token and walks its heads, so the angles are computed once per
+// token, and each lane moves 16-byte (fp32: 32-byte) pieces of whole rows; the
+// stores of neighbouring groups are neighbouring rows of one head. Weights are
+// folded into the cos and sin registers. Statistics and sums are fp32.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+
+namespace la {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// One of q and k: rows at x + b bs + n ts + h D (backward: the gradient dx
+// written at the same kind of address), head-major rows at o + ((b H + h) N + n) D.
+struct Side {
+    const void* x;
+    int64_t x_bs, x_ts;
+    const void* w;        // [D] or null
+    void* y;              // forward: head-major output; backward: dx
+    int64_t y_bs, y_ts;   // backward only
+    const void* go;       // backward: head-major gradient of the output
+    int H;
+};
+
+struct Args {
+    Side s[2];
+    const int32_t* pos;       // [B, N, axes]
+    const longlong2* table;   // [R]: (step in 2^-64 turns, axis)
+    float* partial;           // backward with the norm: [blocks][2][D]
+    int64_t tokens;           // B N
+    int axes, R, N, D, norm, heads_per_block;
+    float eps;
+};
+
+template <typename T> struct Raw8;   // eight consecutive values of a row as stored
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(tcc::pack_bf16(f[0], f[1]), tcc::pack_bf16(f[2], f[3]),
+                       tcc::pack_bf16(f[4], f[5]), tcc::pack_bf16(f[6], f[7]));
+    }
+    // The partner values of lane l: half h of the row piece comes from lane src[h],
+    // whose halves are swapped when `swap` (R not a multiple of 8).
+    __device__ __forceinline__ Raw8 partner(const int (&src)[2], bool swap) const {
+        Raw8 r;
+        const uint32_t a = swap ? v.z : v.x, b = swap ? v.w : v.y;
+        const uint32_t c = swap ? v.x : v.z, d = swap ? v.y : v.w;
+        r.v.x = __shfl_sync(0xffffffffu, a, src[0]);
+        r.v.y = __shfl_sync(0xffffffffu, b, src[0]);
+        r.v.z = __shfl_sync(0xffffffffu, c, src[1]);
+        r.v.w = __shfl_sync(0xffffffffu, d, src[1]);
+        return r;
+    }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ Raw8 partner(const int (&src)[2], bool swap) const {
+        const float4 lo = swap ? b : a, hi = swap ? a : b;
+        Raw8 r;
+        r.a.x = __shfl_sync(0xffffffffu, lo.x, src[0]);
+        r.a.y = __shfl_sync(0xffffffffu, lo.y, src[0]);
+        r.a.z = __shfl_sync(0xffffffffu, lo.z, src[0]);
+        r.a.w = __shfl_sync(0xffffffffu, lo.w, src[0]);
+        r.b.x = __shfl_sync(0xffffffffu, hi.x, src[1]);
+        r.b.y = __shfl_sync(0xffffffffu, hi.y, src[1]);
+        r.b.z = __shfl_sync(0xffffffffu, hi.z, src[1]);
+        r.b.w = __shfl_sync(0xffffffffu, hi.w, src[1]);
+        return r;
+    }
+};
+
+// cos and sin of pair i at token t. A pair whose axis is past the last given one
+// takes the last, so no position is read out of range.
+__device__ __forceinline__ void pair_angle(const Args& a, int64_t t, int i, float* c, float* s) {
+    const longlong2 e = __ldg(a.table + i);
+    const int ax = min(max((int)e.y, 0), a.axes - 1);
+    const uint64_t turn = (uint64_t)(int64_t)__ldg(a.pos + t * a.axes + ax) * (uint64_t)e.x;
+    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, s, c);   // 2^-31 half-turns
+}
+
+// Rotation of a lane's eight values: out = x c + partner s (s carries the sign).
+// Lanes past the rotated features get c = 1, s = 0 and must use a zero partner.
+template <bool kInter>
+__device__ __forceinline__ void lane_angles(const Args& a, int64_t t, int l, float (&c)[8],
+                                            float (&s)[8]) {
+    if (8 * l >= 2 * a.R) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
+        return;
+    }
+    if constexpr (kInter) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float cc, ss;
+            pair_angle(a, t, 4 * l + j / 2, &cc, &ss);
+            c[j] = c[j + 1] = cc;
+            s[j] = -ss;
+            s[j + 1] = ss;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = 8 * l + j;
+            const bool low = e < a.R;
+            float ss;
+            pair_angle(a, t, low ? e : e - a.R, &c[j], &ss);
+            s[j] = low ? -ss : ss;
+        }
+    }
+}
+
+// Source lanes (within the warp) of the partner halves, half layout.
+__device__ __forceinline__ void partner_lanes(int R, int l, int group_base, int (&src)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = 8 * l + 4 * h;
+        const int p = e < R ? e + R : (e < 2 * R ? e - R : e);
+        src[h] = group_base + (p >> 3);
+    }
+}
+
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The partner's values of x: in the lane itself (pairs 2i, 2i + 1) or by shuffle.
+template <bool kInter, typename T>
+__device__ __forceinline__ void partner_values(const Raw8<T>& raw, const float (&x)[8],
+                                               const int (&src)[2], bool swap, bool rot,
+                                               float (&p)[8]) {
+    if constexpr (kInter) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = x[j ^ 1];
+    } else {
+        raw.partner(src, swap).get(p);
+    }
+    if (!rot) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = 0.f;
+    }
+}
+
+// Forward. kLanes: lanes per row (D / 8 rounded up to a power of two; the lanes
+// past D / 8 carry zeros). blockIdx.y: a range of the Hq + Hk heads.
+template <typename T, int kLanes, bool kInter>
+__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ Args a) {
+    constexpr int kRows = kThreads / kLanes, kU = 4;   // heads in flight per group
+    const int l = threadIdx.x % kLanes;
+    const int64_t t_raw = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
+    const bool live = t_raw < a.tokens && 8 * l < a.D;
+    const int64_t t = min(t_raw, a.tokens - 1);
+    const int64_t b = t / a.N, n = t - b * a.N;
+    const bool rot = 8 * l < 2 * a.R, swap = (a.R & 4) != 0;
+    int src[2];
+    partner_lanes(a.R, l, (threadIdx.x & 31) & ~(kLanes - 1), src);
+    float c[8], s[8];
+    lane_angles<kInter>(a, t, l, c, s);
+    const int h_begin = blockIdx.y * a.heads_per_block, h_end = h_begin + a.heads_per_block;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const Side& sd = a.s[side];
+        const int off = side ? a.s[0].H : 0;
+        const int h0 = max(h_begin - off, 0), h1 = min(h_end - off, sd.H);
+        if (h0 >= h1) continue;
+        // Weights folded into the rotation: c w and s w_partner.
+        float cw[8], sw[8];
+        if (sd.w != nullptr) {
+            Raw8<T> wr;
+            wr.zero();
+            if (8 * l < a.D) wr.load(static_cast<const T*>(sd.w) + 8 * l);
+            float w[8], wp[8];
+            wr.get(w);
+            partner_values<kInter>(wr, w, src, swap, rot, wp);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cw[j] = c[j] * w[j], sw[j] = s[j] * wp[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cw[j] = c[j], sw[j] = s[j];
+        }
+        const T* xp = static_cast<const T*>(sd.x) + b * sd.x_bs + n * sd.x_ts + 8 * l;
+        T* yp = static_cast<T*>(sd.y) + (b * sd.H * a.N + n) * a.D + 8 * l;
+        for (int h = h0; h < h1; h += kU) {
+            Raw8<T> raw[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                raw[u].zero();
+                if (live && h + u < h1) raw[u].load(xp + (int64_t)(h + u) * a.D);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                float x[8], p[8], r = 1.f;
+                raw[u].get(x);
+                partner_values<kInter>(raw[u], x, src, swap, rot, p);
+                if (a.norm) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+                    r = rsqrtf(group_sum<kLanes>(ss) / (float)a.D + a.eps);
+                }
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = r * fmaf(x[j], cw[j], p[j] * sw[j]);
+                if (live && h + u < h1) Raw8<T>::store(yp + (int64_t)(h + u) * a.N * a.D, y);
+            }
+        }
+    }
+}
+
+// Adds a block's per-lane dw sums (v[8] for features 8l .. 8l + 7 of every row
+// group) in a fixed order and writes D floats at out.
+template <int kLanes>
+__device__ __forceinline__ void block_dw(float (&v)[8], float (*red)[kMaxDim], int l, int D,
+                                         float* out) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane < kLanes && 8 * l < D)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) red[warp][8 * l + j] = v[j];
+    __syncthreads();
+    if ((int)threadIdx.x < D) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) t += red[w][threadIdx.x];
+        out[threadIdx.x] = t;
+    }
+    __syncthreads();
+}
+
+// Backward. A block walks token tiles blockIdx.x, + gridDim.x, ..., so that dw
+// leaves as one partial row per block.
+template <typename T, int kLanes, bool kInter, bool kNorm>
+__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constant__ Args a) {
+    constexpr int kRows = kThreads / kLanes, kU = 2;
+    const int l = threadIdx.x % kLanes;
+    const bool rot = 8 * l < 2 * a.R, swap = (a.R & 4) != 0;
+    int src[2];
+    partner_lanes(a.R, l, (threadIdx.x & 31) & ~(kLanes - 1), src);
+    const int h_begin = blockIdx.y * a.heads_per_block, h_end = h_begin + a.heads_per_block;
+    const int64_t tiles = (a.tokens + kRows - 1) / kRows;
+    float dw[2][8] = {};
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t t_raw = tile * kRows + threadIdx.x / kLanes;
+        const bool live = t_raw < a.tokens && 8 * l < a.D;
+        const int64_t t = min(t_raw, a.tokens - 1);
+        const int64_t b = t / a.N, n = t - b * a.N;
+        float c[8], s[8];
+        lane_angles<kInter>(a, t, l, c, s);
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const Side& sd = a.s[side];
+            const int off = side ? a.s[0].H : 0;
+            const int h0 = max(h_begin - off, 0), h1 = min(h_end - off, sd.H);
+            if (h0 >= h1) continue;
+            float w[8];
+            if (kNorm && sd.w != nullptr && 8 * l < a.D) {
+                Raw8<T> wr;
+                wr.load(static_cast<const T*>(sd.w) + 8 * l);
+                wr.get(w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 1.f;
+            }
+            const T* gp = static_cast<const T*>(sd.go) + (b * sd.H * a.N + n) * a.D + 8 * l;
+            const T* xp = kNorm ? static_cast<const T*>(sd.x) + b * sd.x_bs + n * sd.x_ts + 8 * l : nullptr;
+            T* yp = static_cast<T*>(sd.y) + b * sd.y_bs + n * sd.y_ts + 8 * l;
+            for (int h = h0; h < h1; h += kU) {
+                Raw8<T> graw[kU], xraw[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    graw[u].zero();
+                    xraw[u].zero();
+                    if (live && h + u < h1) {
+                        graw[u].load(gp + (int64_t)(h + u) * a.N * a.D);
+                        if (kNorm) xraw[u].load(xp + (int64_t)(h + u) * a.D);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    float go[8], p[8], g[8], y[8];
+                    graw[u].get(go);
+                    partner_values<kInter>(graw[u], go, src, swap, rot, p);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) g[j] = fmaf(go[j], c[j], -p[j] * s[j]);
+                    if constexpr (kNorm) {
+                        float x[8], ss = 0.f, dot = 0.f;
+                        xraw[u].get(x);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            ss = fmaf(x[j], x[j], ss);
+                            dot = fmaf(g[j] * w[j], x[j], dot);
+                        }
+                        ss = group_sum<kLanes>(ss);
+                        dot = group_sum<kLanes>(dot);
+                        const float r = rsqrtf(ss / (float)a.D + a.eps);
+                        const float k = r * r * r * (dot / (float)a.D);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            y[j] = fmaf(r * w[j], g[j], -k * x[j]);
+                            dw[side][j] = fmaf(g[j] * r, x[j], dw[side][j]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) y[j] = g[j];
+                    }
+                    if (live && h + u < h1) Raw8<T>::store(yp + (int64_t)(h + u) * a.D, y);
+                }
+            }
+        }
+    }
+    if constexpr (kNorm) {
+        __shared__ float red[kThreads / 32][kMaxDim];
+        float* out = a.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.D;
+        block_dw<kLanes>(dw[0], red, l, a.D, out);
+        block_dw<kLanes>(dw[1], red, l, a.D, out + a.D);
+    }
+}
+
+// Any D, R, stride and alignment: one warp per row, lane i owning features
+// i, i + 32, ...; partners through shared memory. Rows are walked token-major
+// so that a warp's dw sums stay in registers.
+template <typename T, bool kBwd>
+__global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ Args a, int inter) {
+    constexpr int kWarps = kThreads / 32, kE = kMaxDim / 32;
+    __shared__ float buf[kWarps][kMaxDim];
+    __shared__ float red[kWarps][kMaxDim];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* row = buf[warp];
+    float dw[2][kE] = {};
+    for (int side = 0; side < 2; ++side) {
+        const Side& sd = a.s[side];
+        const int64_t rows = a.tokens * sd.H;
+        for (int64_t i = (int64_t)blockIdx.x * kWarps + warp; i < rows; i += (int64_t)gridDim.x * kWarps) {
+            const int64_t t = i / sd.H;
+            const int h = (int)(i - t * sd.H);
+            const int64_t b = t / a.N, n = t - b * a.N;
+            const int64_t hm = ((b * sd.H + h) * a.N + n) * a.D;   // head-major row
+            const T* xr = static_cast<const T*>(sd.x) + b * sd.x_bs + n * sd.x_ts + (int64_t)h * a.D;
+            float x[kE], w[kE], v[kE];
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                const int e = lane + 32 * j;
+                const bool in = e < a.D;
+                x[j] = in && (!kBwd || a.norm) ? to_f(xr[e]) : 0.f;
+                w[j] = in && sd.w ? to_f(static_cast<const T*>(sd.w)[e]) : 1.f;
+                ss = fmaf(x[j], x[j], ss);
+                v[j] = kBwd ? (in ? to_f(static_cast<const T*>(sd.go)[hm + e]) : 0.f) : x[j];
+            }
+            const float r = a.norm ? rsqrtf(group_sum<32>(ss) / (float)a.D + a.eps) : 1.f;
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                const int e = lane + 32 * j;
+                if (!kBwd) v[j] *= r * w[j];
+                if (e < a.D) row[e] = v[j];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                const int e = lane + 32 * j;
+                if (e >= 2 * a.R) continue;
+                const bool low = inter ? (e & 1) == 0 : e < a.R;
+                const int pr = inter ? e >> 1 : (low ? e : e - a.R);
+                const int pe = inter ? e ^ 1 : (low ? e + a.R : e - a.R);
+                float c, s;
+                pair_angle(a, t, pr, &c, &s);
+                if (low != kBwd) s = -s;
+                v[j] = fmaf(v[j], c, row[pe] * s);
+            }
+            __syncwarp();
+            if (!kBwd) {
+#pragma unroll
+                for (int j = 0; j < kE; ++j)
+                    if (lane + 32 * j < a.D)
+                        static_cast<T*>(sd.y)[hm + lane + 32 * j] = from_f<T>(v[j]);
+            } else {
+                T* yr = static_cast<T*>(sd.y) + b * sd.y_bs + n * sd.y_ts + (int64_t)h * a.D;
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < kE; ++j) dot = fmaf(v[j] * w[j], x[j], dot);
+                const float k = a.norm ? r * r * r * (group_sum<32>(dot) / (float)a.D) : 0.f;
+#pragma unroll
+                for (int j = 0; j < kE; ++j) {
+                    const int e = lane + 32 * j;
+                    if (e >= a.D) continue;
+                    yr[e] = from_f<T>(a.norm ? fmaf(r * w[j], v[j], -k * x[j]) : v[j]);
+                    if (side == 0) dw[0][j] = fmaf(v[j] * r, x[j], dw[0][j]);
+                    else dw[1][j] = fmaf(v[j] * r, x[j], dw[1][j]);
+                }
+            }
+        }
+    }
+    if (kBwd && a.norm) {
+        for (int side = 0; side < 2; ++side) {
+#pragma unroll
+            for (int j = 0; j < kE; ++j) red[warp][lane + 32 * j] = side ? dw[1][j] : dw[0][j];
+            __syncthreads();
+            if ((int)threadIdx.x < a.D) {
+                float t = 0.f;
+                for (int i = 0; i < kWarps; ++i) t += red[i][threadIdx.x];
+                a.partial[((int64_t)blockIdx.x * 2 + side) * a.D + threadIdx.x] = t;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// dw[side][d] = sum over blocks of partial[block][side][d], in a fixed order.
+// A block sums 32 columns: thread (x, y) the rows y, y + 8, ...
+__global__ void __launch_bounds__(256) rope_dw_kernel(const float* __restrict__ partial, int blocks,
+                                                      int D, float* dwq, float* dwk) {
+    tcc::pdl_wait();
+    __shared__ float red[8][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + x;   // of 2 D
+    float t = 0.f;
+    if (col < 2 * D)
+        for (int i = y; i < blocks; i += 8) t += partial[(int64_t)i * 2 * D + col];
+    red[y][x] = t;
+    __syncthreads();
+    if (y == 0 && col < 2 * D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) t += red[i][x];
+        float* out = col < D ? dwq : dwk;
+        if (out) out[col < D ? col : col - D] = t;
+    }
+}
+
+// Blocks of the backward: four per SM, each walking token tiles; fewer when
+// there are fewer tiles. Bounds the partial sums' workspace.
+constexpr int kBwdBlocksPerSm = 4;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The vector kernels need whole 16-byte pieces: eight values per lane for bf16
+// (two pieces for fp32), and partner groups of four values.
+bool vector_ok(const Args& a, size_t eb, bool bwd) {
+    if (a.D % 8 || a.R % 4) return false;
+    for (const Side& s : a.s) {
+        if (s.H == 0) continue;
+        if (!aligned16(s.y) || (s.w && !aligned16(s.w))) return false;
+        if (s.x && (!aligned16(s.x) || (s.x_bs * (int64_t)eb) % 16 || (s.x_ts * (int64_t)eb) % 16))
+            return false;
+        if (bwd && (!aligned16(s.go) || (s.y_bs * (int64_t)eb) % 16 || (s.y_ts * (int64_t)eb) % 16))
+            return false;
+    }
+    return true;
+}
+
+int lanes_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : 16; }
+
+// Heads walked by one block: all of a token's heads share its angles, but with
+// few tokens the heads are spread over blocks until the SMs have two each.
+int heads_per_block(int64_t tiles, int heads) {
+    int per = heads;
+    while (per > 1 && tiles * ((heads + per - 1) / per) < 2 * tcc::sm_count()) per = (per + 1) / 2;
+    return per;
+}
+
+template <typename T, int kLanes>
+cudaError_t fwd_vec(Args& a, bool inter, cudaStream_t st) {
+    const int64_t tiles = (a.tokens + kThreads / kLanes - 1) / (kThreads / kLanes);
+    const int heads = a.s[0].H + a.s[1].H;
+    a.heads_per_block = heads_per_block(tiles, heads);
+    const dim3 grid((unsigned)tiles, (heads + a.heads_per_block - 1) / a.heads_per_block);
+    if (inter) rope_fwd_kernel<T, kLanes, true><<<grid, kThreads, 0, st>>>(a);
+    else rope_fwd_kernel<T, kLanes, false><<<grid, kThreads, 0, st>>>(a);
+    return cudaPeekAtLastError();
+}
+
+template <typename T, int kLanes>
+cudaError_t bwd_vec(Args& a, bool inter, int* blocks, cudaStream_t st) {
+    const int64_t tiles = (a.tokens + kThreads / kLanes - 1) / (kThreads / kLanes);
+    const int heads = a.s[0].H + a.s[1].H;
+    const int64_t most = (int64_t)kBwdBlocksPerSm * tcc::sm_count();
+    a.heads_per_block = heads_per_block(tiles, heads);
+    const int gy = (heads + a.heads_per_block - 1) / a.heads_per_block;
+    const int64_t gx = tiles < most / gy ? tiles : (most / gy > 0 ? most / gy : 1);
+    const dim3 grid((unsigned)gx, gy);
+    *blocks = (int)(gx * gy);
+    if (a.norm) {
+        if (inter) rope_bwd_kernel<T, kLanes, true, true><<<grid, kThreads, 0, st>>>(a);
+        else rope_bwd_kernel<T, kLanes, false, true><<<grid, kThreads, 0, st>>>(a);
+    } else {
+        if (inter) rope_bwd_kernel<T, kLanes, true, false><<<grid, kThreads, 0, st>>>(a);
+        else rope_bwd_kernel<T, kLanes, false, false><<<grid, kThreads, 0, st>>>(a);
+    }
+    return cudaPeekAtLastError();
+}
+
+template <typename T>
+cudaError_t run(Args& a, bool bwd, bool inter, int* blocks, cudaStream_t st) {
+    if (vector_ok(a, sizeof(T), bwd)) {
+        switch (lanes_of(a.D)) {
+            case 4: return bwd ? bwd_vec<T, 4>(a, inter, blocks, st) : fwd_vec<T, 4>(a, inter, st);
+            case 8: return bwd ? bwd_vec<T, 8>(a, inter, blocks, st) : fwd_vec<T, 8>(a, inter, st);
+            default: return bwd ? bwd_vec<T, 16>(a, inter, blocks, st) : fwd_vec<T, 16>(a, inter, st);
+        }
+    }
+    const int64_t rows = a.tokens * (a.s[0].H > a.s[1].H ? a.s[0].H : a.s[1].H);
+    const int64_t want = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t most = (int64_t)kBwdBlocksPerSm * tcc::sm_count();
+    const int grid = (int)(want < most ? want : most);
+    *blocks = grid;
+    if (bwd) rope_any_kernel<T, true><<<grid, kThreads, 0, st>>>(a, inter);
+    else rope_any_kernel<T, false><<<grid, kThreads, 0, st>>>(a, inter);
+    return cudaPeekAtLastError();
+}
+
+bool elem_aligned(const void* p, la_dtype dt) {
+    return (reinterpret_cast<uintptr_t>(p) & (dt == LA_BF16 ? 1 : 3)) == 0;
+}
+
+la_status check_shape(int B, int N, int Hq, int Hk, int D, la_dtype dt, const int32_t* pos, int axes,
+                      const int64_t* table, int pairs, float eps, int layout) {
+    if (B < 0 || N < 0 || Hq < 0 || Hk < 0 || D < 1) return LA_ERR_INVALID_ARG;
+    if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (pairs < 0 || 2 * (int64_t)pairs > D || axes < 1) return LA_ERR_INVALID_ARG;
+    if (layout != LA_ROPE_HALVES && layout != LA_ROPE_INTERLEAVED) return LA_ERR_INVALID_ARG;
+    if (!isfinite(eps) || eps < 0.f) return LA_ERR_INVALID_ARG;
+    if (D > kMaxDim || axes > LA_ROPE_MAX_AXES) return LA_ERR_UNSUPPORTED;
+    // A token's heads map to grid.y, and tokens to 31-bit block counts.
+    if ((int64_t)Hq + Hk > 65535 || (int64_t)B * N > (int64_t)1 << 31) return LA_ERR_UNSUPPORTED;
+    if ((int64_t)B * N == 0 || Hq + Hk == 0) return LA_OK;
+    if (pairs > 0) {
+        if (!pos || !table || (reinterpret_cast<uintptr_t>(pos) & 3)) return LA_ERR_INVALID_ARG;
+        if (!aligned16(table)) return LA_ERR_INVALID_ARG;
+    }
+    return LA_OK;
+}
+
+// Rows of `out` (batch stride bs, token stride ts, H D values each) must not overlap.
+bool rows_disjoint(int B, int N, int64_t row, int64_t bs, int64_t ts) {
+    if (B <= 1 && N <= 1) return true;
+    if (B <= 1) return ts >= row;
+    if (N <= 1) return bs >= row;
+    return (ts >= row && bs >= (N - 1) * ts + row) || (bs >= row && ts >= (B - 1) * bs + row);
+}
+
+}  // namespace
+
+}  // namespace la
+
+extern "C" {
+
+la_status la_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int axes,
+                        int64_t* table) {
+    if (pairs < 0 || axes < 1 || (pairs > 0 && (!inv_freq || !table))) return LA_ERR_INVALID_ARG;
+    if (axes > LA_ROPE_MAX_AXES) return LA_ERR_UNSUPPORTED;
+    for (int i = 0; i < pairs; ++i) {
+        if (!isfinite(inv_freq[i])) return LA_ERR_INVALID_ARG;
+        const int ax = axis ? axis[i] : 0;
+        if (ax < 0 || ax >= axes) return LA_ERR_INVALID_ARG;
+        // Whole turns per position fall away; the rest as a multiple of 2^-64,
+        // in two exact steps (32 bits each) of the double's fraction.
+        double turns = inv_freq[i] * 0.15915494309189535;   // 1 / (2 pi)
+        turns -= floor(turns);
+        if (turns >= 1.0) turns = 0.0;
+        const double hi = floor(turns * 4294967296.0);
+        const double lo = (turns * 4294967296.0 - hi) * 4294967296.0;
+        const uint64_t step = ((uint64_t)hi << 32) + (uint64_t)llrint(lo);
+        table[2 * i] = (int64_t)step;
+        table[2 * i + 1] = ax;
+    }
+    return LA_OK;
+}
+
+la_status la_qk_norm_rope_fwd(const void* q, int64_t q_batch, int64_t q_token, const void* k,
+                              int64_t k_batch, int64_t k_token, const void* wq, const void* wk,
+                              const int32_t* pos, int axes, const int64_t* table, int pairs,
+                              void* qo, void* ko, int B, int N, int Hq, int Hk, int D, la_dtype dt,
+                              int norm, float eps, int layout, la_stream_t stream) {
+    la_status s = la::check_shape(B, N, Hq, Hk, D, dt, pos, axes, table, pairs, eps, layout);
+    if (s != LA_OK) return s;
+    if ((wq || wk) && !norm) return LA_ERR_INVALID_ARG;
+    const int64_t tokens = (int64_t)B * N;
+    if (tokens == 0 || Hq + Hk == 0) return LA_OK;
+    la::Args a = {};
+    a.s[0] = {q, q_batch, q_token, wq, qo, 0, 0, nullptr, Hq};
+    a.s[1] = {k, k_batch, k_token, wk, ko, 0, 0, nullptr, Hk};
+    for (const la::Side& sd : a.s)
+        if (sd.H > 0 && (!sd.x || !sd.y || !la::elem_aligned(sd.x, dt) || !la::elem_aligned(sd.y, dt) ||
+                         !la::elem_aligned(sd.w, dt)))
+            return LA_ERR_INVALID_ARG;
+    a.pos = pos;
+    a.table = reinterpret_cast<const longlong2*>(table);
+    a.tokens = tokens;
+    a.axes = axes, a.R = pairs, a.N = N, a.D = D, a.norm = norm ? 1 : 0, a.eps = eps;
+    int blocks = 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = dt == LA_BF16
+                              ? la::run<__nv_bfloat16>(a, false, layout == LA_ROPE_INTERLEAVED, &blocks, st)
+                              : la::run<float>(a, false, layout == LA_ROPE_INTERLEAVED, &blocks, st);
+    return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+la_status la_qk_norm_rope_bwd_workspace_size(int B, int N, int Hq, int Hk, int D, size_t* bytes) {
+    if (!bytes || B < 0 || N < 0 || Hq < 0 || Hk < 0 || D < 1) return LA_ERR_INVALID_ARG;
+    if (D > la::kMaxDim || (int64_t)Hq + Hk > 65535) return LA_ERR_UNSUPPORTED;
+    // One [2, D] row of partial weight gradients per block: at most four blocks
+    // per SM, or one per head range when there are more head ranges than that.
+    const int64_t most = (int64_t)la::kBwdBlocksPerSm * la::tcc::sm_count();
+    const int64_t blocks = most > (int64_t)Hq + Hk ? most : (int64_t)Hq + Hk;
+    *bytes = (size_t)(blocks * 2 * D * 4 + 255) / 256 * 256;
+    return LA_OK;
+}
+
+la_status la_qk_norm_rope_bwd(const void* q, int64_t q_batch, int64_t q_token, const void* k,
+                              int64_t k_batch, int64_t k_token, const void* wq, const void* wk,
+                              const int32_t* pos, int axes, const int64_t* table, int pairs,
+                              const void* dqo, const void* dko, void* dq, int64_t dq_batch,
+                              int64_t dq_token, void* dk, int64_t dk_batch, int64_t dk_token,
+                              float* dwq, float* dwk, int B, int N, int Hq, int Hk, int D,
+                              la_dtype dt, int norm, float eps, int layout, void* workspace,
+                              size_t workspace_bytes, la_stream_t stream) {
+    la_status s = la::check_shape(B, N, Hq, Hk, D, dt, pos, axes, table, pairs, eps, layout);
+    if (s != LA_OK) return s;
+    if ((wq || wk || dwq || dwk) && !norm) return LA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(dwq) & 3) || (reinterpret_cast<uintptr_t>(dwk) & 3))
+        return LA_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    const int64_t tokens = (int64_t)B * N;
+    if (tokens == 0 || Hq + Hk == 0) {
+        // No rows: the weight gradients are zero.
+        if (dwq && cudaMemsetAsync(dwq, 0, (size_t)D * 4, st)) return LA_ERR_CUDA;
+        if (dwk && cudaMemsetAsync(dwk, 0, (size_t)D * 4, st)) return LA_ERR_CUDA;
+        return LA_OK;
+    }
+    la::Args a = {};
+    a.s[0] = {norm ? q : nullptr, q_batch, q_token, wq, dq, dq_batch, dq_token, dqo, Hq};
+    a.s[1] = {norm ? k : nullptr, k_batch, k_token, wk, dk, dk_batch, dk_token, dko, Hk};
+    for (const la::Side& sd : a.s) {
+        if (sd.H == 0) continue;
+        if ((norm && !sd.x) || !sd.y || !sd.go || !la::elem_aligned(sd.x, dt) ||
+            !la::elem_aligned(sd.y, dt) || !la::elem_aligned(sd.go, dt) || !la::elem_aligned(sd.w, dt))
+            return LA_ERR_INVALID_ARG;
+        if (!la::rows_disjoint(B, N, (int64_t)sd.H * D, sd.y_bs, sd.y_ts)) return LA_ERR_INVALID_ARG;
+    }
+    if (norm) {
+        size_t need = 0;
+        if ((s = la_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hk, D, &need)) != LA_OK) return s;
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
+            return LA_ERR_WORKSPACE;
+    }
+    a.pos = pos;
+    a.table = reinterpret_cast<const longlong2*>(table);
+    a.partial = static_cast<float*>(workspace);
+    a.tokens = tokens;
+    a.axes = axes, a.R = pairs, a.N = N, a.D = D, a.norm = norm ? 1 : 0, a.eps = eps;
+    int blocks = 0;
+    cudaError_t e = dt == LA_BF16
+                        ? la::run<__nv_bfloat16>(a, true, layout == LA_ROPE_INTERLEAVED, &blocks, st)
+                        : la::run<float>(a, true, layout == LA_ROPE_INTERLEAVED, &blocks, st);
+    if (e != cudaSuccess) return LA_ERR_CUDA;
+    if (norm && (dwq || dwk)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((2 * D + 31) / 32);
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, la::rope_dw_kernel, (const float*)workspace, blocks, D, dwq, dwk);
+        if (e != cudaSuccess) return LA_ERR_CUDA;
+    }
+    return LA_OK;
+}
+
+}  // extern "C"
