@@ -72,7 +72,8 @@ typedef enum {
     LA_OP_DECODE = 2,
     LA_OP_CAUSAL_BWD = 3,
     LA_OP_NONCAUSAL_BWD = 4,
-    LA_OP_LAYER_DECODE = 5
+    LA_OP_LAYER_DECODE = 5,
+    LA_OP_SELECTIVE_SCAN = 6   /* Dk = S, Dv = P */
 } la_op;
 
 /*
@@ -444,6 +445,80 @@ la_status la_qk_norm_rope_bwd(const void* q, int64_t q_batch, int64_t q_token, c
                               float* dwq, float* dwk, int B, int N, int Hq, int Hk, int D,
                               la_dtype dt, int norm, float eps, int layout, void* workspace,
                               size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * Short causal depthwise convolution over tokens, the local mixing of the
+ * projections in front of a recurrent layer (no counterpart in the pages; it
+ * feeds la_selective_scan_fwd, and the attention entries as well). Per channel c:
+ *   y_t = act(bias_c + sum_{k < W} w[c, k] x[t - W + 1 + k, c]),  act = silu or identity.
+ *  - x: rows of [B, N, C] with batch stride x_batch and token stride x_token in
+ *    elements (C adjacent values: a column range of a projection); y the same
+ *    with its own strides (rows must not overlap); w [C, W], bias [C] (nullable),
+ *    dtype dt, W in {2, 3, 4}. fp32 sums, one rounding.
+ *  - state0 [B, W - 1, C] (nullable: zero): the inputs before the first token;
+ *    state_out [B, W - 1, C] (nullable) receives the last W - 1 inputs. They must
+ *    not overlap (LA_ERR_INVALID_ARG).
+ *  - lengths [B] int32, device (nullable): sequence b has lengths[b] tokens
+ *    (clamped to 0..N). Rows past it are neither read nor written.
+ *  - y must not overlap x. Whole, aligned 16-byte pieces run the vector kernel.
+ *  - Needs no workspace; asynchronous on `stream`.
+ * la_short_conv_step: one token per sequence, x and y rows of [B, C]; state
+ * [B, W - 1, C] is read and shifted by one row in place.
+ */
+la_status la_short_conv_fwd(const void* x, int64_t x_batch, int64_t x_token, const void* w,
+                            const void* bias, int silu, const int32_t* lengths, const void* state0,
+                            void* state_out, void* y, int64_t y_batch, int64_t y_token, int B,
+                            int N, int C, int W, la_dtype dt, la_stream_t stream);
+la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, const void* bias,
+                             int silu, void* state, void* y, int64_t y_batch, int B, int C, int W,
+                             la_dtype dt, la_stream_t stream);
+
+/*
+ * Selective state space scan: causal linear attention without feature map and
+ * denominator whose state decays by a factor per token and head ("Why Replace
+ * Attention? The Softmax Bottleneck and the Path to Linear Time", section 7.2,
+ * steps 1-4, is the recurrence without the decay; queries are C, keys are
+ * d B, values are x, and the state has the layout of la_decode_step's S). Per
+ * head h of group g = h / (H / G):
+ *   d_t = softplus(step_t + step_bias_h)  (softplus != 0; else step_t + step_bias_h)
+ *   S_t = exp(d_t A_h) S_{t-1} + d_t B_t x_t^T
+ *   y_t = (C_t^T S_t + D_h x_t) silu(z_t)   (D null: 0; z null: factor 1)
+ *  - x, z, y: rows of [B, N, H, P] with batch and token strides in elements (the
+ *    H P values of a token adjacent); step: rows of [B, N, H]; Bm, Cm: rows of
+ *    [B, N, G, S]; all dtype dt, so that they can be column ranges of the
+ *    projection and of la_short_conv_fwd's output. H a multiple of G; 1 <= S,
+ *    P <= 128; B H <= 65535.
+ *  - A, D, step_bias: [H] float32; A is the (negative) rate itself. d_t A_h <= 0 is
+ *    expected (the state must not grow); nothing checks it.
+ *  - S0 [B, H, S, P] float32 (nullable: zero): state before the first token; S_out
+ *    (nullable): state after the last. S_out == S0 updates it in place; any other
+ *    overlap is LA_ERR_INVALID_ARG.
+ *  - lengths [B] int32, device (nullable): sequence b has lengths[b] tokens
+ *    (clamped to 0..N); rows past it are neither read nor written, and a sequence
+ *    of no tokens keeps its state.
+ *  - y must not overlap an input, and its rows must not overlap one another.
+ *  - workspace: la_workspace_size(LA_OP_SELECTIVE_SCAN, B, H, N, S, P, dt, ...)
+ *    bytes, 256-byte aligned, initialised once with la_workspace_init. Calls that
+ *    overlap in time need workspaces of their own.
+ * la_selective_scan_step: one token per sequence (x, z, y rows of [B, H, P], step
+ * of [B, H], Bm, Cm of [B, G, S], batch strides only), S [B, H, S, P] float32
+ * updated in place, 16-byte aligned; needs no workspace.
+ */
+la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token, const void* step,
+                                int64_t step_batch, int64_t step_token, const float* A,
+                                const void* Bm, int64_t b_batch, int64_t b_token, const void* Cm,
+                                int64_t c_batch, int64_t c_token, const float* D, const void* z,
+                                int64_t z_batch, int64_t z_token, const float* step_bias,
+                                int softplus, const int32_t* lengths, const float* S0,
+                                float* S_out, void* y, int64_t y_batch, int64_t y_token, int B,
+                                int H, int G, int N, int S, int P, la_dtype dt, void* workspace,
+                                size_t workspace_bytes, la_stream_t stream);
+la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* step,
+                                 int64_t step_batch, const float* A, const void* Bm,
+                                 int64_t b_batch, const void* Cm, int64_t c_batch, const float* D,
+                                 const void* z, int64_t z_batch, const float* step_bias,
+                                 int softplus, float* S_inout, void* y, int64_t y_batch, int B,
+                                 int H, int G, int S, int P, la_dtype dt, la_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears the workspace status word.

@@ -27,12 +27,13 @@ __all__ = [
     "la_layer_decode_step", "la_causal_fwd_noalloc", "la_noalloc_query_status",
     "la_noalloc_set_wait_limit", "library_path", "LA_ROPE_MAX_AXES", "la_rope_table",
     "la_qk_norm_rope_fwd", "la_qk_norm_rope_bwd", "la_qk_norm_rope_bwd_workspace_size",
-    "qk_norm_rope_workspace",
+    "qk_norm_rope_workspace", "la_short_conv_fwd", "la_short_conv_step",
+    "LA_OP_SELECTIVE_SCAN", "la_selective_scan_fwd", "la_selective_scan_step",
 ]
 
 LA_F32, LA_BF16 = 0, 1
 LA_OP_NONCAUSAL, LA_OP_CAUSAL, LA_OP_DECODE, LA_OP_CAUSAL_BWD, LA_OP_NONCAUSAL_BWD = 0, 1, 2, 3, 4
-LA_OP_LAYER_DECODE = 5
+LA_OP_LAYER_DECODE, LA_OP_SELECTIVE_SCAN = 5, 6
 LA_PHI_ELU1, LA_PHI_IDENTITY = 0, 1
 LA_ROPE_HALVES, LA_ROPE_INTERLEAVED, LA_ROPE_MAX_AXES = 0, 1, 4
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_WORKSPACE, LA_ERR_CUDA, LA_ERR_TIMEOUT = 0, 1, 2, 3, 4, 5
@@ -115,6 +116,16 @@ def _load():
     lib.la_qk_norm_rope_bwd.argtypes = [P, L, L, P, L, L, P, P, P, I, P, I, P, P, P, L, L, P, L, L,
                                         P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
     lib.la_qk_norm_rope_bwd.restype = I
+    lib.la_short_conv_fwd.argtypes = [P, L, L, P, P, I, P, P, P, P, L, L, I, I, I, I, I, P]
+    lib.la_short_conv_fwd.restype = I
+    lib.la_short_conv_step.argtypes = [P, L, P, P, I, P, P, L, I, I, I, I, P]
+    lib.la_short_conv_step.restype = I
+    lib.la_selective_scan_fwd.argtypes = [P, L, L, P, L, L, P, P, L, L, P, L, L, P, P, L, L, P, I, P,
+                                          P, P, P, L, L, I, I, I, I, I, I, I, P, Z, P]
+    lib.la_selective_scan_fwd.restype = I
+    lib.la_selective_scan_step.argtypes = [P, L, P, L, P, P, L, P, L, P, P, L, P, I, P, P, L, I, I, I,
+                                           I, I, I, P]
+    lib.la_selective_scan_step.restype = I
     lib.la_query_status.argtypes = [P, P]
     lib.la_query_status.restype = I
     return lib
@@ -631,6 +642,172 @@ def la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, wq=None, wk=None, norm=True,
                                         _stream(stream)),
                "la_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
+
+
+def _conv_args(x, w, bias, dims):
+    if x.dim() != dims or w.dim() != 2 or w.shape[0] != x.shape[-1] or (x.stride(-1) != 1 and x.shape[-1] > 1):
+        raise ValueError("expected x [B,N,C] (one token: [B,C]) with adjacent channels and w [C,W]")
+    _dt(x)
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    C, W = w.shape
+    for t, shape, what in ((w, (C, W), "w"), (bias, (C,), "bias")):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != x.dtype or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous {shape} in x's dtype")
+    return C, W
+
+
+def _conv_state(t, B, C, W, x, what):
+    if t is not None and (tuple(t.shape) != (B, W - 1, C) or t.dtype != x.dtype or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous [B,W-1,C] = {(B, W - 1, C)} in x's dtype")
+
+
+def _out_rows(y, x, what="y"):
+    if y.shape != x.shape or y.dtype != x.dtype or (y.stride(-1) != 1 and y.shape[-1] > 1):
+        raise ValueError(f"{what} must be shaped and typed like x, with adjacent channels")
+
+
+def _check_lengths(lengths, B):
+    if lengths is not None and (lengths.dtype != torch.int32 or tuple(lengths.shape) != (B,)
+                                or not lengths.is_contiguous()):
+        raise ValueError("lengths must be contiguous int32 [B]")
+
+
+def la_short_conv_fwd(x, w, bias=None, silu=True, lengths=None, state0=None, state_out=None, y=None,
+                      return_state=False, stream=None):
+    """Causal depthwise convolution of x [B,N,C] (strided rows allowed) with w [C,W], W in 2..4.
+
+    state0 [B,W-1,C]: the inputs before the first token; the last W - 1 inputs go to state_out
+    (allocated with return_state=True). lengths (int32 [B]): rows past them are left as they are.
+    Returns y, or (y, state_out) with return_state=True."""
+    C, W = _conv_args(x, w, bias, 3)
+    B, N, _ = x.shape
+    _conv_state(state0, B, C, W, x, "state0")
+    _check_lengths(lengths, B)
+    with _scope(x.device, stream):
+        if y is None:
+            y = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+        if state_out is None and return_state:
+            state_out = torch.empty((B, W - 1, C), dtype=x.dtype, device=x.device)
+        _out_rows(y, x)
+        _conv_state(state_out, B, C, W, x, "state_out")
+        _same_cuda(x.device, w, bias, lengths, state0, state_out, y)
+        _check(_lib.la_short_conv_fwd(_ptr(x), x.stride(0), x.stride(1), _ptr(w), _ptr(bias),
+                                      1 if silu else 0, _ptr(lengths), _ptr(state0), _ptr(state_out),
+                                      _ptr(y), y.stride(0), y.stride(1), B, N, C, W, _dt(x),
+                                      _stream(stream)),
+               "la_short_conv_fwd")
+    return (y, state_out) if return_state else y
+
+
+def la_short_conv_step(x, w, state, bias=None, silu=True, y=None, stream=None):
+    """One token of the convolution: x [B,C] -> y [B,C]; state [B,W-1,C] is shifted in place."""
+    C, W = _conv_args(x, w, bias, 2)
+    B = x.shape[0]
+    _conv_state(state, B, C, W, x, "state")
+    with _scope(x.device, stream):
+        if y is None:
+            y = torch.empty((B, C), dtype=x.dtype, device=x.device)
+        _out_rows(y, x)
+        _same_cuda(x.device, w, bias, state, y)
+        _check(_lib.la_short_conv_step(_ptr(x), x.stride(0), _ptr(w), _ptr(bias), 1 if silu else 0,
+                                       _ptr(state), _ptr(y), y.stride(0), B, C, W, _dt(x),
+                                       _stream(stream)),
+               "la_short_conv_step")
+    return y
+
+
+def _inner_adjacent(t, what, inner):
+    """The last `inner` dimensions of t are adjacent values."""
+    want = 1
+    for size, stride in zip(reversed(t.shape[-inner:]), reversed(t.stride()[-inner:])):
+        if size > 1 and stride != want:
+            raise ValueError(f"{what}: a token's values must be adjacent (strides {t.stride()})")
+        want *= size
+
+
+def _scan_args(x, step, A, Bm, Cm, D, z, step_bias, lead):
+    """Checks shared by the prompt (lead = 2: [B,N,..]) and the step (lead = 1: [B,..])."""
+    dims = "[B,N,H,P]" if lead == 2 else "[B,H,P]"
+    if x.dim() != lead + 2 or Bm.dim() != lead + 2 or Cm.shape != Bm.shape or \
+            Bm.shape[:lead] != x.shape[:lead] or step.shape != x.shape[:-1] or \
+            (z is not None and z.shape != x.shape):
+        raise ValueError(f"expected x (and z) {dims}, step one value per head, Bm and Cm with [G,S] per token")
+    for t in (step, Bm, Cm, z):
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError("x, step, Bm, Cm and z must share one dtype")
+    _dt(x)
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    H, P = x.shape[-2:]
+    for t, what in ((A, "A"), (D, "D"), (step_bias, "dt_bias")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H,) or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous float32 [H]")
+    if A is None:
+        raise ValueError("A must be given")
+    for t, what, inner in ((x, "x", 2), (step, "step", 1), (Bm, "Bm", 2), (Cm, "Cm", 2), (z, "z", 2)):
+        if t is not None:
+            _inner_adjacent(t, what, inner)
+    return x.shape[0], H, P, Bm.shape[-2], Bm.shape[-1]
+
+
+def _f32_state(t, shape, what):
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous float32 with shape {shape}")
+
+
+def la_selective_scan_fwd(x, step, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True,
+                          lengths=None, S0=None, S_out=None, y=None, ws=None, stream=None):
+    """Selective scan of x [B,N,H,P] with step sizes [B,N,H], rates A [H], Bm, Cm [B,N,G,S].
+
+    y_t = (C_t^T S_t + D x_t) silu(z_t) with S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T and
+    d_t = softplus(step_t + dt_bias). S0, S_out [B,H,S,P] float32 (S_out may be S0). lengths
+    (int32 [B]): rows past them are left as they are. Token rows may be strided (column ranges of
+    a projection). Returns y [B,N,H,P]."""
+    B, H, P, G, S = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 2)
+    N = x.shape[1]
+    _f32_state(S0, (B, H, S, P), "S0")
+    _f32_state(S_out, (B, H, S, P), "S_out")
+    _check_lengths(lengths, B)
+    with _scope(x.device, stream):
+        if y is None:
+            y = torch.empty((B, N, H, P), dtype=x.dtype, device=x.device)
+        if y.shape != x.shape or y.dtype != x.dtype:
+            raise ValueError("y must be shaped and typed like x")
+        _inner_adjacent(y, "y", 2)
+        if ws is None:
+            ws = workspace(LA_OP_SELECTIVE_SCAN, B, H, N, S, P, x.dtype, x.device, stream)
+        _same_cuda(x.device, step, A, Bm, Cm, D, z, dt_bias, lengths, S0, S_out, y, ws)
+        zs = z.stride() if z is not None else (0, 0)
+        xs, ss, bs, cs, ys = x.stride(), step.stride(), Bm.stride(), Cm.stride(), y.stride()
+        _check(_lib.la_selective_scan_fwd(
+            _ptr(x), xs[0], xs[1], _ptr(step), ss[0], ss[1], _ptr(A), _ptr(Bm), bs[0], bs[1], _ptr(Cm),
+            cs[0], cs[1], _ptr(D), _ptr(z), zs[0], zs[1], _ptr(dt_bias), 1 if softplus else 0,
+            _ptr(lengths), _ptr(S0), _ptr(S_out), _ptr(y), ys[0], ys[1], B, H, G, N, S, P, _dt(x),
+            _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "la_selective_scan_fwd")
+    return y
+
+
+def la_selective_scan_step(x, step, A, Bm, Cm, S, D=None, z=None, dt_bias=None, softplus=True,
+                           y=None, stream=None):
+    """One token of the scan: x [B,H,P], step [B,H], Bm, Cm [B,G,S]; S [B,H,S,P] in place."""
+    B, H, P, G, Sn = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 1)
+    if S is None:
+        raise ValueError("S must be given")
+    _f32_state(S, (B, H, Sn, P), "S")
+    with _scope(x.device, stream):
+        if y is None:
+            y = torch.empty((B, H, P), dtype=x.dtype, device=x.device)
+        if y.shape != x.shape or y.dtype != x.dtype:
+            raise ValueError("y must be shaped and typed like x")
+        _inner_adjacent(y, "y", 2)
+        _same_cuda(x.device, step, A, Bm, Cm, D, z, dt_bias, S, y)
+        _check(_lib.la_selective_scan_step(
+            _ptr(x), x.stride(0), _ptr(step), step.stride(0), _ptr(A), _ptr(Bm), Bm.stride(0), _ptr(Cm),
+            Cm.stride(0), _ptr(D), _ptr(z), z.stride(0) if z is not None else 0, _ptr(dt_bias),
+            1 if softplus else 0, _ptr(S), _ptr(y), y.stride(0), B, H, G, Sn, P, _dt(x),
+            _stream(stream)), "la_selective_scan_step")
+    return y
 
 
 def la_query_status(ws, stream=None):

@@ -52,6 +52,8 @@ size_t body_bytes(la_op op, int B, int H, int N, int Dk, int Dv, la_dtype dt) {
             return la::simt_bwd_workspace(BH, N, Dk, Dv);
         case LA_OP_LAYER_DECODE:
             return la::layer_workspace(B, H, Dk, dt);
+        case LA_OP_SELECTIVE_SCAN:
+            return la::scan_workspace(BH, N, Dk, Dv);
         default:
             return 0;
     }
@@ -149,7 +151,8 @@ la_status la_workspace_size(la_op op, int B, int H, int N, int Dk, int Dv, la_dt
                             size_t* bytes) {
     if (!bytes) return LA_ERR_INVALID_ARG;
     if (op != LA_OP_CAUSAL && op != LA_OP_NONCAUSAL && op != LA_OP_DECODE &&
-        op != LA_OP_CAUSAL_BWD && op != LA_OP_NONCAUSAL_BWD && op != LA_OP_LAYER_DECODE)
+        op != LA_OP_CAUSAL_BWD && op != LA_OP_NONCAUSAL_BWD && op != LA_OP_LAYER_DECODE &&
+        op != LA_OP_SELECTIVE_SCAN)
         return LA_ERR_INVALID_ARG;
     const bool one_token = op == LA_OP_DECODE || op == LA_OP_LAYER_DECODE;
     la_status s = check_common(B, H, one_token ? 1 : N, Dk, Dv, dt);
@@ -174,7 +177,8 @@ la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtyp
                           int* launches) {
     if (!launches) return LA_ERR_INVALID_ARG;
     if (op != LA_OP_CAUSAL && op != LA_OP_NONCAUSAL && op != LA_OP_DECODE &&
-        op != LA_OP_CAUSAL_BWD && op != LA_OP_NONCAUSAL_BWD && op != LA_OP_LAYER_DECODE)
+        op != LA_OP_CAUSAL_BWD && op != LA_OP_NONCAUSAL_BWD && op != LA_OP_LAYER_DECODE &&
+        op != LA_OP_SELECTIVE_SCAN)
         return LA_ERR_INVALID_ARG;
     const bool one_token = op == LA_OP_DECODE || op == LA_OP_LAYER_DECODE;
     la_status s = check_common(B, H, one_token ? 1 : N, Dk, Dv, dt);
@@ -188,6 +192,8 @@ la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtyp
         *launches = 3;                           // two projections and the decode step
     else if (one_token)
         *launches = 1;
+    else if (op == LA_OP_SELECTIVE_SCAN)
+        *launches = la::scan_launches(BH, N);
     else if (op == LA_OP_CAUSAL_BWD || op == LA_OP_NONCAUSAL_BWD)
         *launches = 5;
     else if (op == LA_OP_CAUSAL && la::tc_causal_supported(Dk, Dv, dt))

@@ -40,6 +40,9 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
     return __float2bfloat16_rn(x);
 }
 
+// v sigmoid(v) in fp32 (hardware exponential and division, a few 2^-24 relative).
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+
 // Workspace header (first 256 bytes of every workspace).
 struct WsHeader {
     uint32_t status;     // 0 = ok, else an la_status code set by a kernel

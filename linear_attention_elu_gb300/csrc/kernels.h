@@ -97,6 +97,19 @@ cudaError_t tc_bwd(const void* q, const void* k, const void* v, const void* dout
 // Layer decode step (csrc/layer.cu): workspace bytes after the header.
 size_t layer_workspace(int B, int H, int D, la_dtype dt);
 
+// Selective scan (csrc/scan.cu): workspace bytes after the header, launches.
+size_t scan_workspace(int64_t BH, int N, int S, int P);
+int scan_launches(int64_t BH, int N);
+
+// Whether the rows of an output (`row` values each, batch stride bs, token stride
+// ts) are disjoint.
+inline bool rows_disjoint(int B, int N, int64_t row, int64_t bs, int64_t ts) {
+    if (B <= 1 && N <= 1) return true;
+    if (B <= 1) return ts >= row;
+    if (N <= 1) return bs >= row;
+    return (ts >= row && bs >= (N - 1) * ts + row) || (bs >= row && ts >= (B - 1) * bs + row);
+}
+
 // Y = X W, row-major X [rows, K], W [K, N], Y [rows, N], fp32 accumulation
 // (csrc/gemm.cu): tcgen05 for bf16 with K, N multiples of 8, fp32 FMA otherwise.
 // A bounded wait that runs out is recorded in the header at ws_header.

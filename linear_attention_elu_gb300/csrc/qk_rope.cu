@@ -580,14 +580,6 @@ la_status check_shape(int B, int N, int Hq, int Hk, int D, la_dtype dt, const in
     return LA_OK;
 }
 
-// Rows of `out` (batch stride bs, token stride ts, H D values each) must not overlap.
-bool rows_disjoint(int B, int N, int64_t row, int64_t bs, int64_t ts) {
-    if (B <= 1 && N <= 1) return true;
-    if (B <= 1) return ts >= row;
-    if (N <= 1) return bs >= row;
-    return (ts >= row && bs >= (N - 1) * ts + row) || (bs >= row && ts >= (B - 1) * bs + row);
-}
-
 }  // namespace
 
 }  // namespace la

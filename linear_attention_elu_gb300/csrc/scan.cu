@@ -1,0 +1,464 @@
+// Selective state space scan, per head (b, h) with its group's B and C:
+//   d_t = softplus(step_t + bias_h) (or step_t + bias_h),   a_t = exp(d_t A_h)
+//   S_t = a_t S_{t-1} + d_t B_t x_t^T,   y_t = C_t^T S_t + D_h x_t,   y_t *= silu(z_t)
+// i.e. causal linear attention ("Why Replace Attention? The Softmax Bottleneck
+// and the Path to Linear Time", section 7.2, steps 1-4) with q = C, k = d B,
+// v = x, no feature map and no denominator, and a decay of the state per token.
+//
+// This file: the recurrence on the CUDA cores in fp32 (any type, size, stride),
+// the single-token step, the scan over segments, and the entry points. bf16
+// with whole 16-byte rows runs on the tensor cores instead (csrc/scan_tc.cu).
+//
+// The recurrence keeps the state in registers: a warp owns 8 columns of one
+// head, its 32 lanes 8 row groups x 4 column pairs, so a lane holds R rows
+// (R = S / 8) of two columns, as packed fp32 row pairs. A token costs three
+// packed operations per row pair (decay, update, read): the FP32 pipe bounds it.
+// Eight tokens' reads are then summed over the row groups by a butterfly that
+// halves the tokens at each step (14 shuffles for 8 tokens x 2 columns). With too
+// few heads for the SMs a sequence is cut into segments: a first pass gives each
+// segment's own end state and total decay, a scan chains them, and the second
+// pass starts each segment from its state.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "scan.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+
+using namespace scan;
+
+namespace {
+
+constexpr int kTok = 16;               // tokens staged per tile
+
+__device__ __forceinline__ uint64_t pk(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+    return x + y;
+}
+
+// Staged floats per token and operand: 8 row groups of R rows, padded so that
+// the groups' vector loads fall into different banks.
+template <int R> constexpr int kGroupStride = R >= 8 ? R + 4 : R;
+
+// Grid: (segments, B H). Block: one warp per 8 columns of the head.
+// kState: only the segment's end state from zero and its decay (first pass).
+template <typename T, int R, bool kState>
+__global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int kG = kGroupStride<R>, kRow = 8 * kG;
+    extern __shared__ float smem[];
+    float* bs = smem;                                   // [kTok][kRow]
+    float* cs = bs + kTok * kRow;                       // [kTok][kRow]
+    float* xs = cs + kTok * kRow;                       // [kTok][cols]
+    const int cols = blockDim.x / 4;                    // P rounded up to a multiple of 8
+    float* ds = xs + kTok * cols;                       // [kTok]
+    float* as = ds + kTok;                              // [kTok]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rg = lane & 7, col = 8 * warp + 2 * (lane >> 3);
+    const int seg = blockIdx.x, h = blockIdx.y % a.H;
+    const int64_t b = blockIdx.y / a.H, bh = blockIdx.y;
+    const int grp = h / (a.H / a.G);
+    const int n = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
+    const int t0 = seg * a.seg_len, t1 = min(t0 + a.seg_len, n);
+    const T* x = static_cast<const T*>(a.x) + b * a.x_bs + (int64_t)h * a.P;
+    const T* z = a.z ? static_cast<const T*>(a.z) + b * a.z_bs + (int64_t)h * a.P : nullptr;
+    const T* Bm = static_cast<const T*>(a.Bm) + b * a.b_bs + (int64_t)grp * a.S;
+    const T* Cm = static_cast<const T*>(a.Cm) + b * a.c_bs + (int64_t)grp * a.S;
+    const T* st = static_cast<const T*>(a.step) + b * a.step_bs + h;
+    T* y = static_cast<T*>(a.y) + b * a.y_bs + (int64_t)h * a.P;
+    const float A = a.A[h], bias = a.step_bias ? a.step_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+
+    // The state: rows rg R .. rg R + R - 1 of columns col, col + 1.
+    uint64_t s[2][R / 2];
+    const float* from = kState ? nullptr : (a.nseg > 1 ? a.seeds + (bh * a.nseg + seg) * a.S * a.P
+                                                       : (a.S0 ? a.S0 + bh * a.S * a.P : nullptr));
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < R / 2; ++i) {
+            const int r = rg * R + 2 * i;
+            float v[2] = {0.f, 0.f};
+            if (from && col + c < a.P) {
+                if (r < a.S) v[0] = from[(int64_t)r * a.P + col + c];
+                if (r + 1 < a.S) v[1] = from[(int64_t)(r + 1) * a.P + col + c];
+            }
+            s[c][i] = pk(v[0], v[1]);
+        }
+    float decay = 0.f;                                  // sum of d A over the segment (first pass)
+
+    for (int tile = t0; tile < t1; tile += kTok) {
+        const int m = min(kTok, t1 - tile);
+        __syncthreads();
+        for (int i = tid; i < kTok * 8 * R; i += blockDim.x) {
+            const int t = i / (8 * R), r = i % (8 * R);
+            const bool in = t < m && r < a.S;
+            const int at = t * kRow + (r / R) * kG + r % R;
+            bs[at] = in ? to_f(Bm[(int64_t)(tile + t) * a.b_ts + r]) : 0.f;
+            if (!kState) cs[at] = in ? to_f(Cm[(int64_t)(tile + t) * a.c_ts + r]) : 0.f;
+        }
+        for (int i = tid; i < kTok * cols; i += blockDim.x) {
+            const int t = i / cols, p = i - t * cols;
+            xs[i] = t < m && p < a.P ? to_f(x[(int64_t)(tile + t) * a.x_ts + p]) : 0.f;
+        }
+        if (tid < kTok) {
+            // A token past the end decays by 1 and adds nothing.
+            const float d = tid < m ? step_size(to_f(st[(int64_t)(tile + tid) * a.step_ts]) + bias, a.softplus) : 0.f;
+            ds[tid] = d;
+            as[tid] = expf(d * A);
+        }
+        __syncthreads();
+        if (kState && tid == 0)
+            for (int t = 0; t < m; ++t) decay += ds[t] * A;
+#pragma unroll 1
+        for (int half = 0; half < kTok && half < m; half += 8) {
+            float acc[8][2];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const int tt = half + t;
+                const float d = ds[tt], at = as[tt];
+                const uint64_t a2 = pk(at, at);
+                const float2 xv = *reinterpret_cast<const float2*>(xs + tt * cols + col);
+                const uint64_t x0 = pk(d * xv.x, d * xv.x), x1 = pk(d * xv.y, d * xv.y);
+                const float* bp = bs + tt * kRow + rg * kG;
+                const float* cp = cs + tt * kRow + rg * kG;
+                uint64_t y0 = 0, y1 = 0;
+#pragma unroll
+                for (int i = 0; i < R / 2; ++i) {
+                    uint64_t bb, cc = 0;
+                    if constexpr (R >= 4) {             // two pairs per 16-byte load
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(bp + (i & ~1) * 2);
+                        bb = (i & 1) ? v.y : v.x;
+                        if (!kState) {
+                            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cp + (i & ~1) * 2);
+                            cc = (i & 1) ? w.y : w.x;
+                        }
+                    } else {
+                        bb = *reinterpret_cast<const uint64_t*>(bp + 2 * i);
+                        if (!kState) cc = *reinterpret_cast<const uint64_t*>(cp + 2 * i);
+                    }
+                    s[0][i] = fma2(bb, x0, mul2(a2, s[0][i]));
+                    s[1][i] = fma2(bb, x1, mul2(a2, s[1][i]));
+                    if (!kState) {
+                        y0 = fma2(cc, s[0][i], y0);
+                        y1 = fma2(cc, s[1][i], y1);
+                    }
+                }
+                if (!kState) acc[t][0] = sum2(y0), acc[t][1] = sum2(y1);
+            }
+            if constexpr (!kState) {
+                // Sum over the 8 row groups (lane bits 0-2): each step keeps half of the
+                // tokens, so lane rg ends with token rg of the eight.
+#pragma unroll
+                for (int bit = 2; bit >= 0; --bit) {
+                    const int keep = 1 << bit;
+                    const bool up = (rg & keep) != 0;
+#pragma unroll
+                    for (int t = 0; t < keep; ++t)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float send = up ? acc[t][c] : acc[t + keep][c];
+                            const float mine = up ? acc[t + keep][c] : acc[t][c];
+                            acc[t][c] = mine + __shfl_xor_sync(0xffffffffu, send, keep);
+                        }
+                }
+                const int tt = half + rg;
+                if (tt < m) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (col + c >= a.P) continue;
+                        float v = fmaf(Dh, xs[tt * cols + col + c], acc[0][c]);
+                        if (z) v *= silu(to_f(z[(int64_t)(tile + tt) * a.z_ts + col + c]));
+                        y[(int64_t)(tile + tt) * a.y_ts + col + c] = from_f<T>(v);
+                    }
+                }
+            }
+        }
+    }
+    float* to = kState ? a.seeds + (bh * a.nseg + seg) * a.S * a.P
+                       : (seg == a.nseg - 1 && a.S_out ? a.S_out + bh * a.S * a.P : nullptr);
+    if (to) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (col + c >= a.P) continue;
+#pragma unroll
+            for (int i = 0; i < R / 2; ++i) {
+                const int r = rg * R + 2 * i;
+                float lo, hi;
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(s[c][i]));
+                if (r < a.S) to[(int64_t)r * a.P + col + c] = lo;
+                if (r + 1 < a.S) to[(int64_t)(r + 1) * a.P + col + c] = hi;
+            }
+        }
+    }
+    if (kState && tid == 0) a.seg_decay[bh * a.nseg + seg] = decay;
+}
+
+// In place over a head's segments: the end states (from zero) become the states
+// that the segments start from, seed_0 = S0, seed_{i+1} = exp(decay_i) seed_i + end_i.
+__global__ void __launch_bounds__(256) seed_kernel(const __grid_constant__ ScanArgs a) {
+    const int64_t bh = blockIdx.y;
+    const int e = blockIdx.x * 256 + threadIdx.x, E = a.S * a.P;
+    if (e >= E) return;
+    float carry = a.S0 ? a.S0[bh * E + e] : 0.f;
+    float* p = a.seeds + bh * a.nseg * E + e;
+    for (int i0 = 0; i0 < a.nseg; i0 += 8) {
+        float end[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i0 + u < a.nseg) end[u] = p[(int64_t)(i0 + u) * E];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (i0 + u >= a.nseg) break;
+            p[(int64_t)(i0 + u) * E] = carry;
+            carry = fmaf(expf(a.seg_decay[bh * a.nseg + i0 + u]), carry, end[u]);
+        }
+    }
+}
+
+// One token per sequence, the state updated in place. It is read and written
+// once (8 bytes per element against a handful of operations): HBM bandwidth
+// bounds it. A block owns one head; a thread owns kV columns of every
+// rows-per-pass-th row and keeps kU rows in flight.
+template <typename T, int kV>
+__global__ void __launch_bounds__(256) scan_step_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int kU = 8;
+    __shared__ float bs[kMaxDim], cs[kMaxDim];
+    __shared__ float red[256 * kV];
+    const int tid = threadIdx.x;
+    const int64_t bh = blockIdx.x, b = bh / a.H;
+    const int h = (int)(bh - b * a.H), grp = h / (a.H / a.G);
+    const int lpr = (a.P + kV - 1) / kV, rpp = 256 / lpr;   // lanes per row, rows per pass
+    const int r0 = tid / lpr, c0 = (tid - r0 * lpr) * kV;
+    const bool mine = r0 < rpp;
+    float* S = a.S_out + bh * a.S * a.P + c0;
+    float s[kU][kV];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int r = base + u * rpp + r0;
+            if (!mine || r >= a.S) continue;
+            if constexpr (kV == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(S + (int64_t)r * a.P);
+                s[u][0] = v.x, s[u][1] = v.y, s[u][2] = v.z, s[u][3] = v.w;
+            } else {
+                s[u][0] = S[(int64_t)r * a.P];
+            }
+        }
+    };
+    load(0);
+    const T* xp = static_cast<const T*>(a.x) + b * a.x_bs + (int64_t)h * a.P;
+    if (tid < a.S) {
+        bs[tid] = to_f(static_cast<const T*>(a.Bm)[b * a.b_bs + (int64_t)grp * a.S + tid]);
+        cs[tid] = to_f(static_cast<const T*>(a.Cm)[b * a.c_bs + (int64_t)grp * a.S + tid]);
+    }
+    const float d = step_size(to_f(static_cast<const T*>(a.step)[b * a.step_bs + h]) +
+                                  (a.step_bias ? a.step_bias[h] : 0.f), a.softplus);
+    const float decay = expf(d * a.A[h]);
+    float xd[kV], acc[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) xd[v] = mine ? d * to_f(xp[c0 + v]) : 0.f, acc[v] = 0.f;
+    __syncthreads();
+    for (int base = 0; base < a.S; base += kU * rpp) {
+        if (base > 0) load(base);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int r = base + u * rpp + r0;
+            if (!mine || r >= a.S) continue;
+            const float br = bs[r], cr = cs[r];
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                s[u][v] = fmaf(br, xd[v], decay * s[u][v]);
+                acc[v] = fmaf(cr, s[u][v], acc[v]);
+            }
+            if constexpr (kV == 4)
+                *reinterpret_cast<float4*>(S + (int64_t)r * a.P) = make_float4(s[u][0], s[u][1], s[u][2], s[u][3]);
+            else
+                S[(int64_t)r * a.P] = s[u][0];
+        }
+    }
+    if (mine)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) red[r0 * a.P + c0 + v] = acc[v];
+    __syncthreads();
+    if (tid < a.P) {
+        float v = 0.f;
+        for (int r = 0; r < rpp; ++r) v += red[r * a.P + tid];
+        v = fmaf(a.D ? a.D[h] : 0.f, to_f(xp[tid]), v);
+        if (a.z) v *= silu(to_f(static_cast<const T*>(a.z)[b * a.z_bs + (int64_t)h * a.P + tid]));
+        static_cast<T*>(a.y)[b * a.y_bs + (int64_t)h * a.P + tid] = from_f<T>(v);
+    }
+}
+
+template <typename T, int R>
+cudaError_t recurrence(const ScanArgs& a, int64_t BH, cudaStream_t st) {
+    const int warps = (a.P + 7) / 8;
+    const size_t smem = sizeof(float) * (size_t)(kTok * (2 * 8 * kGroupStride<R> + 8 * warps) + 2 * kTok);
+    const dim3 grid(a.nseg, (unsigned)BH);
+    if (a.nseg > 1) {
+        scan_kernel<T, R, true><<<grid, 32 * warps, smem, st>>>(a);
+        cudaError_t e = launch_seeds(a, BH, st);
+        if (e != cudaSuccess) return e;
+    }
+    scan_kernel<T, R, false><<<grid, 32 * warps, smem, st>>>(a);
+    return cudaPeekAtLastError();
+}
+
+template <typename T>
+cudaError_t recurrence_by_size(const ScanArgs& a, int64_t BH, cudaStream_t st) {
+    if (a.S <= 16) return recurrence<T, 2>(a, BH, st);
+    if (a.S <= 32) return recurrence<T, 4>(a, BH, st);
+    if (a.S <= 64) return recurrence<T, 8>(a, BH, st);
+    return recurrence<T, 16>(a, BH, st);
+}
+
+template <typename T>
+cudaError_t step(const ScanArgs& a, int64_t BH, cudaStream_t st) {
+    if (a.P % 4 == 0) scan_step_kernel<T, 4><<<(unsigned)BH, 256, 0, st>>>(a);
+    else scan_step_kernel<T, 1><<<(unsigned)BH, 256, 0, st>>>(a);
+    return cudaPeekAtLastError();
+}
+
+la_status check_shape(int B, int H, int G, int N, int S, int P, la_dtype dt) {
+    if (B < 0 || H < 0 || N < 0 || G < 1 || S < 1 || P < 1) return LA_ERR_INVALID_ARG;
+    if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (H % G) return LA_ERR_INVALID_ARG;
+    if (S > kMaxDim || P > kMaxDim) return LA_ERR_UNSUPPORTED;
+    if ((int64_t)B * H > 65535) return LA_ERR_UNSUPPORTED;   // heads map to grid.y
+    return LA_OK;
+}
+
+bool bad(const void* p, la_dtype dt) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (dt == LA_BF16 ? 1 : 3));
+}
+
+bool bad4(const void* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
+
+}  // namespace
+
+namespace scan {
+
+// Segments of the recurrence: one while there are two blocks per SM or fewer
+// than two stretches of 64 tokens; else as many as fill two blocks per SM.
+int recurrence_segments(int64_t BH, int N) {
+    const int64_t want = 2 * (int64_t)tcc::sm_count() / (BH > 0 ? BH : 1);
+    const int64_t most = N / 64;
+    const int64_t n = want < most ? want : most;
+    return n < 2 ? 1 : (int)n;
+}
+
+cudaError_t launch_seeds(const ScanArgs& a, int64_t BH, cudaStream_t st) {
+    seed_kernel<<<dim3((a.S * a.P + 255) / 256, (unsigned)BH), 256, 0, st>>>(a);
+    return cudaPeekAtLastError();
+}
+
+}  // namespace scan
+
+size_t scan_workspace(int64_t BH, int N, int S, int P) {
+    const int n = recurrence_segments(BH, N);
+    return n > 1 ? (size_t)BH * n * ((size_t)S * P + 1) * sizeof(float) : 0;
+}
+
+int scan_launches(int64_t BH, int N) { return recurrence_segments(BH, N) > 1 ? 3 : 1; }
+
+}  // namespace la
+
+extern "C" {
+
+la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token, const void* step,
+                                int64_t step_batch, int64_t step_token, const float* A,
+                                const void* Bm, int64_t b_batch, int64_t b_token, const void* Cm,
+                                int64_t c_batch, int64_t c_token, const float* D, const void* z,
+                                int64_t z_batch, int64_t z_token, const float* step_bias,
+                                int softplus, const int32_t* lengths, const float* S0,
+                                float* S_out, void* y, int64_t y_batch, int64_t y_token, int B,
+                                int H, int G, int N, int S, int P, la_dtype dt, void* workspace,
+                                size_t workspace_bytes, la_stream_t stream) {
+    la_status s = la::check_shape(B, H, G, N, S, P, dt);
+    if (s != LA_OK) return s;
+    const int64_t BH = (int64_t)B * H;
+    if (BH == 0) return LA_OK;
+    if (la::bad4(S0) || la::bad4(S_out) || la::bad4(lengths) || la::bad4(D) || la::bad4(step_bias) ||
+        la::bad4(A) || !A)
+        return LA_ERR_INVALID_ARG;
+    // The final state may replace the initial one, but not overlap it otherwise.
+    const size_t state = sizeof(float) * (size_t)BH * S * P;
+    if (S0 && S_out && S0 != S_out) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(S0), q = reinterpret_cast<uintptr_t>(S_out);
+        if (p < q + state && q < p + state) return LA_ERR_INVALID_ARG;
+    }
+    cudaStream_t st = (cudaStream_t)stream;
+    if (N == 0) {
+        if (!S_out || S_out == S0) return LA_OK;
+        const cudaError_t e = S0 ? cudaMemcpyAsync(S_out, S0, state, cudaMemcpyDeviceToDevice, st)
+                                 : cudaMemsetAsync(S_out, 0, state, st);
+        return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    }
+    if (la::bad(x, dt) || la::bad(step, dt) || la::bad(Bm, dt) || la::bad(Cm, dt) || la::bad(y, dt) ||
+        (z && la::bad(z, dt)) || y == x || (z && y == z))
+        return LA_ERR_INVALID_ARG;
+    if (!la::rows_disjoint(B, N, (int64_t)H * P, y_batch, y_token)) return LA_ERR_INVALID_ARG;
+    const size_t need = sizeof(la::WsHeader) + la::scan_workspace(BH, N, S, P);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
+        return LA_ERR_WORKSPACE;
+    la::scan::ScanArgs a = {};
+    a.x = x, a.x_bs = x_batch, a.x_ts = x_token;
+    a.step = step, a.step_bs = step_batch, a.step_ts = step_token;
+    a.Bm = Bm, a.b_bs = b_batch, a.b_ts = b_token;
+    a.Cm = Cm, a.c_bs = c_batch, a.c_ts = c_token;
+    a.z = z, a.z_bs = z_batch, a.z_ts = z_token;
+    a.y = y, a.y_bs = y_batch, a.y_ts = y_token;
+    a.A = A, a.D = D, a.step_bias = step_bias, a.lengths = lengths, a.S0 = S0, a.S_out = S_out;
+    a.N = N, a.H = H, a.G = G, a.S = S, a.P = P, a.softplus = softplus ? 1 : 0;
+    a.nseg = la::scan::recurrence_segments(BH, N);
+    a.seg_len = (N + a.nseg - 1) / a.nseg;
+    a.seeds = reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(la::WsHeader));
+    a.seg_decay = a.seeds + (size_t)BH * a.nseg * S * P;
+    const cudaError_t e = dt == LA_BF16 ? la::recurrence_by_size<__nv_bfloat16>(a, BH, st)
+                                        : la::recurrence_by_size<float>(a, BH, st);
+    return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* step,
+                                 int64_t step_batch, const float* A, const void* Bm,
+                                 int64_t b_batch, const void* Cm, int64_t c_batch, const float* D,
+                                 const void* z, int64_t z_batch, const float* step_bias,
+                                 int softplus, float* S_inout, void* y, int64_t y_batch, int B,
+                                 int H, int G, int S, int P, la_dtype dt, la_stream_t stream) {
+    la_status s = la::check_shape(B, H, G, 1, S, P, dt);
+    if (s != LA_OK) return s;
+    const int64_t BH = (int64_t)B * H;
+    if (BH == 0) return LA_OK;
+    if (la::bad(x, dt) || la::bad(step, dt) || la::bad(Bm, dt) || la::bad(Cm, dt) || la::bad(y, dt) ||
+        (z && la::bad(z, dt)) || !A || la::bad4(A) || la::bad4(D) || la::bad4(step_bias) || !S_inout ||
+        (reinterpret_cast<uintptr_t>(S_inout) & 15))
+        return LA_ERR_INVALID_ARG;
+    if (!la::rows_disjoint(B, 1, (int64_t)H * P, y_batch, 0)) return LA_ERR_INVALID_ARG;
+    la::scan::ScanArgs a = {};
+    a.x = x, a.x_bs = x_batch, a.step = step, a.step_bs = step_batch, a.Bm = Bm, a.b_bs = b_batch;
+    a.Cm = Cm, a.c_bs = c_batch, a.z = z, a.z_bs = z_batch, a.y = y, a.y_bs = y_batch;
+    a.A = A, a.D = D, a.step_bias = step_bias, a.S_out = S_inout;
+    a.N = 1, a.H = H, a.G = G, a.S = S, a.P = P, a.softplus = softplus ? 1 : 0;
+    const cudaError_t e = dt == LA_BF16 ? la::step<__nv_bfloat16>(a, BH, (cudaStream_t)stream)
+                                        : la::step<float>(a, BH, (cudaStream_t)stream);
+    return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+}  // extern "C"

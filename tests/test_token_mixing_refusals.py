@@ -92,3 +92,102 @@ def test_rope_wrappers_refuse_before_any_launch(la):
         la.la_qk_norm_rope_fwd(None, None, pos, table)
     with pytest.raises(TypeError):
         la.la_qk_norm_rope_fwd(q, q.double(), pos, table)
+
+
+def conv_fwd(la, **kw):
+    a = dict(x=F, xb=1000, xt=64, w=F, bias=F, silu=1, lengths=None, s0=F, s1=F + (1 << 19), y=F + 16, yb=1000,
+             yt=64, B=2, N=4, C=64, W=4, dt=1, stream=None)
+    a.update(kw)
+    return la._lib.la_short_conv_fwd(*a.values())
+
+
+def conv_step(la, **kw):
+    a = dict(x=F, xb=64, w=F, bias=F, silu=1, state=F, y=F, yb=64, B=2, C=64, W=4, dt=1, stream=None)
+    a.update(kw)
+    return la._lib.la_short_conv_step(*a.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), BAD), (dict(w=None), BAD), (dict(y=None), BAD), (dict(y=F), BAD), (dict(x=F + 1), BAD),
+    (dict(bias=F + 1), BAD), (dict(lengths=F + 2), BAD), (dict(s1=F + 64), BAD), (dict(yt=32), BAD),
+    (dict(yb=100), BAD), (dict(W=5), UNSUP), (dict(W=1), UNSUP), (dict(W=0), BAD), (dict(C=0), BAD),
+    (dict(dt=3), BAD), (dict(N=-1), BAD), (dict(B=1 << 20, N=1 << 20), UNSUP), (dict(B=0, x=None), 0),
+])
+def test_conv_forward_refuses(la, kw, want):
+    assert conv_fwd(la, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(state=None), BAD), (dict(x=None), BAD), (dict(y=F + 1), BAD), (dict(W=8), UNSUP), (dict(yb=63), BAD),
+    (dict(C=-1), BAD), (dict(B=0, x=None), 0),
+])
+def test_conv_step_refuses(la, kw, want):
+    assert conv_step(la, **kw) == want
+
+
+def test_conv_wrappers_refuse_before_any_launch(la):
+    x, w = torch.zeros(2, 4, 64), torch.zeros(64, 4)
+    with pytest.raises(ValueError):                       # host tensors
+        la.la_short_conv_fwd(x, w)
+    with pytest.raises(ValueError):
+        la.la_short_conv_fwd(x, torch.zeros(32, 4))
+    with pytest.raises(TypeError):
+        la.la_short_conv_step(torch.zeros(2, 64).half(), w, torch.zeros(2, 3, 64))
+
+
+def scan_fwd(la, **kw):
+    a = dict(x=F, xb=1 << 14, xt=128, step=F, sb=8, st=2, A=F, Bm=F, bb=256, bt=64, Cm=F, cb=256, ct=64, D=F, z=F,
+             zb=1 << 14, zt=128, bias=F, softplus=1, lengths=None, S0=F, S_out=F, y=F + 16, yb=512, yt=128, B=2, H=2,
+             G=1, N=4, S=64, P=64, dt=1, ws=F, wsb=1 << 30, stream=None)
+    a.update(kw)
+    return la._lib.la_selective_scan_fwd(*a.values())
+
+
+def scan_step(la, **kw):
+    a = dict(x=F, xb=128, step=F, sb=2, A=F, Bm=F, bb=64, Cm=F, cb=64, D=F, z=F, zb=128, bias=F, softplus=1, S=F, y=F,
+             yb=128, B=2, H=2, G=1, Sn=64, P=64, dt=1, stream=None)
+    a.update(kw)
+    return la._lib.la_selective_scan_step(*a.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), BAD), (dict(A=None), BAD), (dict(Bm=F + 1), BAD), (dict(Cm=None), BAD), (dict(step=None), BAD),
+    (dict(y=None), BAD), (dict(y=F), BAD), (dict(z=F + 16), BAD), (dict(S_out=F + 64), BAD), (dict(S0=F + 2), BAD),
+    (dict(D=F + 2), BAD), (dict(lengths=F + 1), BAD), (dict(yt=64), BAD), (dict(yb=500), BAD),
+    (dict(G=0), BAD), (dict(H=3, G=2), BAD), (dict(S=0), BAD), (dict(P=-1), BAD), (dict(dt=2), BAD),
+    (dict(S=129), UNSUP), (dict(P=192), UNSUP), (dict(B=40000), UNSUP), (dict(ws=None), WS), (dict(ws=F + 8), WS),
+    (dict(wsb=255), WS), (dict(B=0, x=None), 0), (dict(H=0, x=None), 0), (dict(N=0, x=None, y=None), 0),
+])
+def test_scan_forward_refuses(la, kw, want):
+    assert scan_fwd(la, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(S=None), BAD), (dict(S=F + 4), BAD), (dict(x=None), BAD), (dict(y=F + 1), BAD), (dict(A=None), BAD),
+    (dict(yb=100), BAD), (dict(H=3, G=2), BAD), (dict(Sn=200), UNSUP), (dict(B=0, x=None), 0),
+])
+def test_scan_step_refuses(la, kw, want):
+    assert scan_step(la, **kw) == want
+
+
+def test_scan_workspace_and_launches(la):
+    assert la.la_workspace_size(la.LA_OP_SELECTIVE_SCAN, 2, 64, 0, 128, 64, la.LA_BF16) == 256
+    assert la.la_workspace_size(la.LA_OP_SELECTIVE_SCAN, 1, 8, 8192, 128, 64, la.LA_BF16) % 256 == 0
+    assert la.la_launch_count(la.LA_OP_SELECTIVE_SCAN, 1, 8, 0, 128, 64, la.LA_BF16) == 0
+    for N in (1, 60):                                     # too short to be cut into segments
+        assert la.la_launch_count(la.LA_OP_SELECTIVE_SCAN, 1, 1, N, 64, 64, la.LA_F32) == 1
+    with pytest.raises(la.LinAttnError):
+        la.la_workspace_size(la.LA_OP_SELECTIVE_SCAN, 1, 8, 64, 129, 64, la.LA_BF16)
+
+
+def test_scan_wrappers_refuse_before_any_launch(la):
+    x, step, A = torch.zeros(2, 4, 2, 64), torch.zeros(2, 4, 2), -torch.ones(2)
+    Bm = torch.zeros(2, 4, 1, 64)
+    with pytest.raises(ValueError):                       # host tensors
+        la.la_selective_scan_fwd(x, step, A, Bm, Bm)
+    with pytest.raises(ValueError):
+        la.la_selective_scan_fwd(x, step[:, :3], A, Bm, Bm)
+    with pytest.raises(TypeError):
+        la.la_selective_scan_fwd(x, step.bfloat16(), A, Bm, Bm)
+    with pytest.raises(ValueError):
+        la.la_selective_scan_step(x[:, 0], step[:, 0], A, Bm[:, 0], Bm[:, 0], None)
