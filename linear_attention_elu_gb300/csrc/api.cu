@@ -53,7 +53,7 @@ size_t body_bytes(la_op op, int B, int H, int N, int Dk, int Dv, la_dtype dt) {
         case LA_OP_LAYER_DECODE:
             return la::layer_workspace(B, H, Dk, dt);
         case LA_OP_SELECTIVE_SCAN:
-            return la::scan_workspace(BH, N, Dk, Dv);
+            return la::scan_workspace(B, H, N, Dk, Dv, dt);
         default:
             return 0;
     }
@@ -193,7 +193,7 @@ la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtyp
     else if (one_token)
         *launches = 1;
     else if (op == LA_OP_SELECTIVE_SCAN)
-        *launches = la::scan_launches(BH, N);
+        *launches = la::scan_launches(B, H, N, Dk, Dv, dt);
     else if (op == LA_OP_CAUSAL_BWD || op == LA_OP_NONCAUSAL_BWD)
         *launches = 5;
     else if (op == LA_OP_CAUSAL && la::tc_causal_supported(Dk, Dv, dt))

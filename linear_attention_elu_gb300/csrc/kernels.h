@@ -98,8 +98,8 @@ cudaError_t tc_bwd(const void* q, const void* k, const void* v, const void* dout
 size_t layer_workspace(int B, int H, int D, la_dtype dt);
 
 // Selective scan (csrc/scan.cu): workspace bytes after the header, launches.
-size_t scan_workspace(int64_t BH, int N, int S, int P);
-int scan_launches(int64_t BH, int N);
+size_t scan_workspace(int B, int H, int N, int S, int P, la_dtype dt);
+int scan_launches(int B, int H, int N, int S, int P, la_dtype dt);
 
 // Whether the rows of an output (`row` values each, batch stride bs, token stride
 // ts) are disjoint.

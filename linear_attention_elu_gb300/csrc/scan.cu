@@ -371,12 +371,31 @@ cudaError_t launch_seeds(const ScanArgs& a, int64_t BH, cudaStream_t st) {
 
 }  // namespace scan
 
-size_t scan_workspace(int64_t BH, int N, int S, int P) {
-    const int n = recurrence_segments(BH, N);
+namespace {
+
+bool tc_widths(int S, int P, la_dtype dt) { return dt == LA_BF16 && S % 8 == 0 && P % 8 == 0; }
+
+}  // namespace
+
+// Enough for either path (rows that are not aligned take the recurrence) and for
+// every number of groups, on which the tensor-core path's segments depend.
+size_t scan_workspace(int B, int H, int N, int S, int P, la_dtype dt) {
+    const int64_t BH = (int64_t)B * H;
+    int n = recurrence_segments(BH, N);
+    if (tc_widths(S, P, dt))
+        for (int g = 1; (int64_t)g * g <= H; ++g) {
+            if (H % g) continue;
+            const int x = tc_segments(B, H, g, N, P), y = tc_segments(B, H, H / g, N, P);
+            n = x > n ? x : n;
+            n = y > n ? y : n;
+        }
     return n > 1 ? (size_t)BH * n * ((size_t)S * P + 1) * sizeof(float) : 0;
 }
 
-int scan_launches(int64_t BH, int N) { return recurrence_segments(BH, N) > 1 ? 3 : 1; }
+int scan_launches(int B, int H, int N, int S, int P, la_dtype dt) {
+    const int n = tc_widths(S, P, dt) ? tc_segments(B, H, 1, N, P) : recurrence_segments((int64_t)B * H, N);
+    return n > 1 ? 3 : 1;
+}
 
 }  // namespace la
 
@@ -415,9 +434,6 @@ la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token,
         (z && la::bad(z, dt)) || y == x || (z && y == z))
         return LA_ERR_INVALID_ARG;
     if (!la::rows_disjoint(B, N, (int64_t)H * P, y_batch, y_token)) return LA_ERR_INVALID_ARG;
-    const size_t need = sizeof(la::WsHeader) + la::scan_workspace(BH, N, S, P);
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
-        return LA_ERR_WORKSPACE;
     la::scan::ScanArgs a = {};
     a.x = x, a.x_bs = x_batch, a.x_ts = x_token;
     a.step = step, a.step_bs = step_batch, a.step_ts = step_token;
@@ -427,12 +443,18 @@ la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token,
     a.y = y, a.y_bs = y_batch, a.y_ts = y_token;
     a.A = A, a.D = D, a.step_bias = step_bias, a.lengths = lengths, a.S0 = S0, a.S_out = S_out;
     a.N = N, a.H = H, a.G = G, a.S = S, a.P = P, a.softplus = softplus ? 1 : 0;
-    a.nseg = la::scan::recurrence_segments(BH, N);
+    const bool tc = la::scan::tc_supported(a, B, dt);
+    a.nseg = tc ? la::scan::tc_segments(B, H, G, N, P) : la::scan::recurrence_segments(BH, N);
     a.seg_len = (N + a.nseg - 1) / a.nseg;
+    const size_t need = sizeof(la::WsHeader) +
+                        (a.nseg > 1 ? (size_t)BH * a.nseg * ((size_t)S * P + 1) * sizeof(float) : 0);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
+        return LA_ERR_WORKSPACE;
     a.seeds = reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(la::WsHeader));
     a.seg_decay = a.seeds + (size_t)BH * a.nseg * S * P;
-    const cudaError_t e = dt == LA_BF16 ? la::recurrence_by_size<__nv_bfloat16>(a, BH, st)
-                                        : la::recurrence_by_size<float>(a, BH, st);
+    const cudaError_t e = tc ? la::scan::tc_scan(a, B, workspace, st)
+                          : dt == LA_BF16 ? la::recurrence_by_size<__nv_bfloat16>(a, BH, st)
+                                          : la::recurrence_by_size<float>(a, BH, st);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "linattn.h"
+
 namespace la {
 namespace scan {
 
@@ -27,6 +29,12 @@ struct ScanArgs {
 __device__ __forceinline__ float step_size(float v, int softplus) {
     return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
 }
+
+// Tensor-core path (csrc/scan_tc.cu): whether these arguments can take it, its
+// segments, and the launches.
+bool tc_supported(const ScanArgs& a, int B, la_dtype dt);
+int tc_segments(int64_t B, int H, int G, int N, int P);
+cudaError_t tc_scan(ScanArgs& a, int B, void* ws_header, cudaStream_t st);
 
 int recurrence_segments(int64_t BH, int N);
 cudaError_t launch_seeds(const ScanArgs& a, int64_t BH, cudaStream_t st);

@@ -231,3 +231,21 @@ def test_convolution_and_scan_together(la, dt):
     assert (np.abs(to_f64(u) - u64) <= 2.0 ** -20 * mag + (2.0 ** -8 * np.abs(u64) if dt == "bf16" else 0)).all()
     q = dict(p, step=step, z=z, S0=None, **cut(u, 2))
     check(torch.cat(ys, 1), S_out, oracle(q), N + 3, S, dt)
+
+
+@pytest.mark.parametrize("N,H", [(300, 2), (4096, 2)])
+def test_withheld_loads_time_out_and_the_context_survives(la, N, H):
+    # The header's test hook withholds the loads: every bounded wait runs out, the call
+    # ends and the status says so (one launch, and the segmented form).
+    p = problem(1, N, H, 1, 128, 64, "bf16", 12)
+    ws = la.workspace(la.LA_OP_SELECTIVE_SCAN, 1, H, N, 128, 64, torch.bfloat16)
+    hdr = ws[:256].view(torch.int32)
+    hdr[4], hdr[5] = 2000, 1               # 2 ms, withhold
+    la.la_selective_scan_fwd(**p, ws=ws)
+    assert la.la_query_status(ws) == la.LA_ERR_TIMEOUT
+    la.la_workspace_init(ws)
+    S_out = torch.empty(1, H, 128, 64, device="cuda")
+    y = la.la_selective_scan_fwd(**p, S_out=S_out, ws=ws)
+    assert la.la_query_status(ws) == la.LA_OK
+    if N < 1000:
+        check(y, S_out, oracle(p), N, 128, "bf16")
