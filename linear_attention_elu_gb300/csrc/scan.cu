@@ -213,9 +213,15 @@ __global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanA
 
 // In place over a head's segments: the end states (from zero) become the states
 // that the segments start from, seed_0 = S0, seed_{i+1} = exp(decay_i) seed_i + end_i.
-__global__ void __launch_bounds__(256) seed_kernel(const __grid_constant__ ScanArgs a) {
+// A thread chains one element (reads and writes of a segment are whole rows of
+// threads), eight segments in flight; the decays' exponentials are shared.
+constexpr int kMaxSegments = 512;
+__global__ void __launch_bounds__(128) seed_kernel(const __grid_constant__ ScanArgs a) {
+    __shared__ float f[kMaxSegments];
     const int64_t bh = blockIdx.y;
-    const int e = blockIdx.x * 256 + threadIdx.x, E = a.S * a.P;
+    for (int i = threadIdx.x; i < a.nseg; i += 128) f[i] = expf(a.seg_decay[bh * a.nseg + i]);
+    __syncthreads();
+    const int e = blockIdx.x * 128 + threadIdx.x, E = a.S * a.P;
     if (e >= E) return;
     float carry = a.S0 ? a.S0[bh * E + e] : 0.f;
     float* p = a.seeds + bh * a.nseg * E + e;
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(256) seed_kernel(const __grid_constant__ ScanA
         for (int u = 0; u < 8; ++u) {
             if (i0 + u >= a.nseg) break;
             p[(int64_t)(i0 + u) * E] = carry;
-            carry = fmaf(expf(a.seg_decay[bh * a.nseg + i0 + u]), carry, end[u]);
+            carry = fmaf(f[i0 + u], carry, end[u]);
         }
     }
 }
@@ -360,12 +366,13 @@ namespace scan {
 int recurrence_segments(int64_t BH, int N) {
     const int64_t want = 2 * (int64_t)tcc::sm_count() / (BH > 0 ? BH : 1);
     const int64_t most = N / 64;
-    const int64_t n = want < most ? want : most;
+    int64_t n = want < most ? want : most;
+    n = n < kMaxSegments ? n : kMaxSegments;
     return n < 2 ? 1 : (int)n;
 }
 
 cudaError_t launch_seeds(const ScanArgs& a, int64_t BH, cudaStream_t st) {
-    seed_kernel<<<dim3((a.S * a.P + 255) / 256, (unsigned)BH), 256, 0, st>>>(a);
+    seed_kernel<<<dim3((a.S * a.P + 127) / 128, (unsigned)BH), 128, 0, st>>>(a);
     return cudaPeekAtLastError();
 }
 

@@ -25,9 +25,28 @@ struct ScanArgs {
     int nseg, seg_len;
 };
 
-// softplus(v) = max(v, 0) + log(1 + e^-|v|), or v as it is.
+// softplus(v) = max(v, 0) + log(1 + e^-|v|), or v as it is. With e = e^-|v| the
+// logarithm is 2 artanh(s), s = e / (2 + e) <= 1/3, by its odd power series to s^13
+// (truncation below 2^-26 of the value), which keeps small step sizes accurate
+// relative to themselves; e^-|v| is 2^t with the rounding of t = -|v| log2 e put back.
 __device__ __forceinline__ float step_size(float v, int softplus) {
-    return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
+    if (!softplus) return v;
+    constexpr float kL = 1.44269502162933349609375f, kLLo = 1.925963033500011e-8f;   // log2 e
+    const float x = -fabsf(v), t = x * kL;
+    const float r = fmaf(x, kL, -t) + x * kLLo;
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fmaf(e, r * 0.6931471805599453f, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(2.f + e));
+    const float s = e * q, u = s * s;
+    float p = 1.f / 13.f;
+    p = fmaf(p, u, 1.f / 11.f);
+    p = fmaf(p, u, 1.f / 9.f);
+    p = fmaf(p, u, 1.f / 7.f);
+    p = fmaf(p, u, 1.f / 5.f);
+    p = fmaf(p, u, 1.f / 3.f);
+    p = fmaf(p, u, 1.f);
+    return fmaxf(v, 0.f) + 2.f * s * p;
 }
 
 // Tensor-core path (csrc/scan_tc.cu): whether these arguments can take it, its

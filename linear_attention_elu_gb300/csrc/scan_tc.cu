@@ -22,13 +22,22 @@
 // score; the weights of (4) come from sums taken from the chunk's end, so that a
 // small exponent is not a difference of two large ones.
 //
-// Roles (20 warps, one CTA per SM): TMA; MMA issue; two warps that turn step
-// sizes into decays (one per unit); and four warpgroups over the 128 rows: scores
-// to P, state, weighted values, output. All hand-offs are mbarriers; every wait is
-// bounded. Sequences are cut into segments when there are too few units for the
-// SMs: the first pass streams (4) alone, in reverse order of chunks so that the
-// weights reach to the segment's end and nothing has to be rescaled; seeds are
-// chained by csrc/scan.cu and the second pass starts from them.
+// Schedule (20 warps, one CTA per SM). An item is one chunk of one unit. Sixteen
+// warps share every step of an item, a warp owning 32 rows x 16 columns (32 x 32
+// of the scores): state to bf16 and scaled, output of the item before, weighted
+// values, scores to P. They run the same code at the same time: an earlier form
+// with a warpgroup per step spent 8,000 cycles an item against 3,000, each role
+// waiting on its own instruction fetches and hand-offs. One thread then issues
+// (2), (3), (4) of the item (and (1) of the next chunk), which run under the next
+// item's steps. Four more warps: TMA loads, MMA issue, step sizes to decays, and
+// the output slots (gate in, output in place, TMA store). All hand-offs are
+// mbarriers; every wait is bounded. Sequences are cut into segments when there are
+// too few units for the SMs: the first pass streams (4) alone, in reverse order of
+// chunks so that the weights reach to the segment's end and nothing has to be
+// rescaled; seeds are chained by csrc/scan.cu and the second pass starts from them.
+// What bounds it: shared memory. Operands of the products (196 KB an item, their A
+// tiles once per 64 columns), TMA and the steps move some 400 KB per item at 128
+// bytes a cycle, against 49 KB of HBM traffic.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -57,8 +66,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // One unit's decays over a chunk, exponents in base 2.
 struct Decay {
     float cum[kC];      // l_t: sum up to and including t
-    float d[kC];        // step sizes (0 past the sequence's end)
-    float w[kC];        // d_t 2^(l_end - l_t)
+    float d[kC];        // step sizes, 0 past the sequence's end (not folded into an exponent:
+                        // next to a large l their logarithm would lose its digits)
+    float w[kC];        // d_t 2^(l_end - l_t), 0 past the end
     float total;        // 2^l_end
     float pad[3];
 };
@@ -73,27 +83,31 @@ struct Units {
 constexpr uint32_t kTmSc = 0, kTmP = 128, kTmY1 = 256, kTmY2 = 320, kTmSt = 384;
 
 struct Misc {
-    uint64_t bc_full[2], bc_empty[2], x_full[2], x_empty[2], dt_full[kDtRing], dt_empty[kDtRing];
-    uint64_t sc_full, sc_empty, p_full[2], p_empty[2], xw_full, xw_empty, sb_full, sb_empty;
-    uint64_t st_full[2], y_full, y_empty, drain;
+    uint64_t c_full, c_empty, b_full[2], b_empty[2], x_full[2], x_empty[2], dt_full[kDtRing], dt_empty[kDtRing];
+    uint64_t slot_ready[2], y_staged[2], sc_full, item_ready, read_done, y_full, state_done, drain;
     uint32_t tmem_slot;
 };
 
-// Shared memory of the main kernel, from a 1024-byte boundary.
+// Shared memory of the main kernel, from a 1024-byte boundary. B is double
+// buffered; C, which the read of the state frees half an item earlier, is not: its
+// 32 KB hold the output slots instead (gate in, output in place, TMA store).
 template <int kT> struct Smem {
-    static constexpr uint32_t kStage = 2 * kT * kTile;         // C tiles, then B tiles
-    static constexpr uint32_t kX = 2 * kStage;
+    static constexpr uint32_t kC0 = 0, kB0 = kT * kTile;
+    static constexpr uint32_t kX = 3 * kT * kTile;
     static constexpr uint32_t kXw = kX + 2 * kTile;            // value, remainder
-    static constexpr uint32_t kSb = kXw + 2 * kTile;           // bf16 state, 64 kT rows
+    static constexpr uint32_t kOut = kXw + 2 * kTile;          // gate, then output
+    static constexpr uint32_t kSb = kOut + 2 * kTile;          // bf16 state, 64 kT rows
     static constexpr uint32_t kDt = kSb + kT * 64 * 128;
-    static constexpr uint32_t kCol = kDt + kDtRing * sizeof(Decay);   // column factors per P warp
-    static constexpr uint32_t kMisc = kCol + 4 * 96 * 4;
+    static constexpr uint32_t kCol = kDt + (kDtRing * sizeof(Decay) + 127) / 128 * 128;
+    static constexpr uint32_t kMisc = kCol + 16 * 32 * 4;      // 32 column factors per warp
     static constexpr uint32_t kEnd = kMisc + sizeof(Misc);
     static constexpr size_t kBytes = 1024 + kEnd;
 };
 static_assert(Smem<2>::kBytes <= 227 * 1024, "main kernel's shared memory");
 
 constexpr int kThreads = 640;
+constexpr int kWork = 16;              // warps that share the items' steps; then TMA, MMA, decays, slots
+constexpr int kAhead = 3;              // items between a tile's L2 prefetch and its load
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -201,12 +215,14 @@ __device__ __forceinline__ void decays(const ScanArgs& a, const Place& pl, int c
     suf[0] = suf[1] + l[1];
 }
 
-// Row `row` of the weighted values: hi = bf16(w x), lo = bf16(w x - hi).
-__device__ __forceinline__ void weigh_row(const uint8_t* x, uint8_t* hi, uint8_t* lo, int row, float w) {
+// Pieces j0 .. j1 - 1 (8 values each) of row `row` of the weighted values:
+// hi = bf16(w x), lo = bf16(w x - hi).
+__device__ __forceinline__ void weigh_row(const uint8_t* x, uint8_t* hi, uint8_t* lo, int row, float w, int j0,
+                                          int j1) {
     const uint64_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
     const uint32_t base = row * 128;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
+#pragma unroll 4
+    for (int j = j0; j < j1; ++j) {
         const uint32_t off = base + ((j ^ (row & 7)) << 4);
         const uint4 v = *reinterpret_cast<const uint4*>(x + off);
         const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -228,56 +244,65 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
     for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(tile + row * 128 + j * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// (4): state += B^T (hi + lo), issued by one thread. The second 64-row atom of the
-// A operand is the next tile (for kT = 1 whatever tile follows: those lanes are unused).
-__device__ __forceinline__ void issue_state(uint32_t dst, uint32_t bt, uint32_t hi, uint32_t lo, bool fresh) {
-    const uint32_t id = idesc_bf16_f32(128, 64, true, true);
+// Descriptor of the 16-row (or 16-column) step k of an operand whose first one is d:
+// only the start address (in 16-byte units) moves.
+__device__ __forceinline__ uint64_t step_desc(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+// Operand with rows of 64 values along M or N (one row per k): steps of 16 rows.
+__device__ __forceinline__ uint64_t rows_desc(uint32_t tile) { return smem_desc(tile, kTile, 1024, kSwizzle128B); }
+// K-major operand (64 k per row of a tile, tiles kTile apart): steps of 16 k.
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile) { return smem_desc(tile, 16, 1024, kSwizzle128B); }
+__device__ __forceinline__ uint64_t kmajor_step(uint64_t d, int k) {
+    return step_desc(d, (k >> 2) * kTile + (k & 3) * 32);
+}
+
+// (4): state += B^T (hi + lo), issued by one thread; lo is the tile after hi. The second
+// 64-row atom of the A operand is the tile after B's (for kT = 1 whatever tile follows:
+// those lanes are unused).
+__device__ __forceinline__ void issue_state(uint32_t dst, uint64_t bt, uint64_t hi, bool fresh) {
+    constexpr uint32_t id = idesc_bf16_f32(128, 64, true, true);
 #pragma unroll
     for (int part = 0; part < 2; ++part)
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k)
-            mma_bf16(dst, smem_desc(bt + k * 2048, kTile, 1024, kSwizzle128B),
-                     smem_desc((part ? lo : hi) + k * 2048, 1024, 1024, kSwizzle128B), id,
+            mma_bf16(dst, step_desc(bt, k * 2048), step_desc(hi, part * kTile + k * 2048), id,
                      (fresh && part == 0 && k == 0) ? 0u : 1u);
 }
 
-// `pieces` times 8 gate values of a row, zeros past them: 16-byte loads where the
-// rows are aligned, else one value at a time.
-__device__ __forceinline__ void load_gate(const __nv_bfloat16* p, int pieces, bool vec, uint4 (&z)[8]) {
+// Eight gate values of a row that is not 16-byte aligned.
+__device__ __forceinline__ uint4 load_gate(const __nv_bfloat16* p) {
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        z[j] = make_uint4(0, 0, 0, 0);
-        if (j >= pieces) continue;
-        if (vec) {
-            z[j] = __ldg(reinterpret_cast<const uint4*>(p) + j);
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const unsigned short lo = __ldg(reinterpret_cast<const unsigned short*>(p) + 8 * j + 2 * k);
-                const unsigned short hi = __ldg(reinterpret_cast<const unsigned short*>(p) + 8 * j + 2 * k + 1);
-                w[k] = (uint32_t)lo | ((uint32_t)hi << 16);
-            }
-            z[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
+    for (int k = 0; k < 4; ++k) w[k] = (uint32_t)__ldg(h + 2 * k) | ((uint32_t)__ldg(h + 2 * k + 1) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// z / (1 + e^-z) of two packed bf16 values. e^-z overflows to infinity and its
+// reciprocal is then 0: the limit.
+__device__ __forceinline__ uint64_t gate2(uint32_t z) {
+    const uint64_t v = bf2(z);
+    float t0, t1, r0, r1;
+    unpk2(mul2(v, pk2(-kLog2e, -kLog2e)), &t0, &t1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(1.f + ex2(t0)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(1.f + ex2(t1)));
+    return mul2(v, pk2(r0, r1));
 }
 
 template <int kT>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap bmap,
-               const __grid_constant__ CUtensorMap cmap, const __grid_constant__ ScanArgs a,
+               const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap zmap,
+               const __grid_constant__ CUtensorMap ymap, const __grid_constant__ ScanArgs a,
                const __grid_constant__ Units un, WsHeader* hdr) {
     using L = Smem<kT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     Decay* dts = reinterpret_cast<Decay*>(base + L::kDt);
-    uint8_t* sb = base + L::kSb;
-    uint8_t *xw_hi = base + L::kXw, *xw_lo = xw_hi + kTile;
-    auto ctile = [&](int s) { return base + s * L::kStage; };
-    auto btile = [&](int s) { return base + s * L::kStage + kT * kTile; };
+    auto btile = [&](int s) { return base + L::kB0 + s * kT * kTile; };
     auto xtile = [&](int n) { return base + L::kX + (n & 1) * kTile; };
+    auto oslot = [&](int n) { return base + L::kOut + (n & 1) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Place pl = place(a, un);
     const bool last_seg = pl.seg == a.nseg - 1;
@@ -286,37 +311,37 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&m.bc_full[s], 1);
-            mbar_init(&m.bc_empty[s], 1);
+            mbar_init(&m.b_full[s], 1);
+            mbar_init(&m.b_empty[s], 1);
             mbar_init(&m.x_full[s], 1);
-            mbar_init(&m.x_empty[s], 9);      // weights, output (4 warps each), (3)
-            mbar_init(&m.p_full[s], 4);
-            mbar_init(&m.p_empty[s], 1);
-            mbar_init(&m.st_full[s], 1);
+            mbar_init(&m.x_empty[s], kWork);
+            mbar_init(&m.slot_ready[s], 1);
+            mbar_init(&m.y_staged[s], kWork);
         }
         for (int s = 0; s < kDtRing; ++s) {
             mbar_init(&m.dt_full[s], 1);
-            mbar_init(&m.dt_empty[s], 12 + 2 * kT);
+            mbar_init(&m.dt_empty[s], kWork);
         }
+        mbar_init(&m.c_full, 1);
+        mbar_init(&m.c_empty, 1);
         mbar_init(&m.sc_full, 1);
-        mbar_init(&m.sc_empty, 4);
-        mbar_init(&m.xw_full, 4);
-        mbar_init(&m.xw_empty, 1);
-        mbar_init(&m.sb_full, 2 * kT);
-        mbar_init(&m.sb_empty, 1);
+        mbar_init(&m.item_ready, kWork);
+        mbar_init(&m.read_done, 1);
         mbar_init(&m.y_full, 1);
-        mbar_init(&m.y_empty, 4);
+        mbar_init(&m.state_done, 1);
         mbar_init(&m.drain, 1);
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == kWork + 1) {
         tmem_alloc(&m.tmem_slot, 512);
         tmem_relinquish();
     }
-    if (warp == 0 && lane == 0) {
+    if (warp == kWork && lane == 0) {
         tma_prefetch_desc(&xmap);
         tma_prefetch_desc(&bmap);
         tma_prefetch_desc(&cmap);
+        tma_prefetch_desc(&zmap);
+        tma_prefetch_desc(&ymap);
     }
     tc_fence_before();
     __syncthreads();
@@ -324,400 +349,399 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     const uint32_t tmem = m.tmem_slot;
     const uint32_t max_spin = hdr->max_spin;
     const bool hold = hdr->hold_item != 0;                 // test hook: loads never issued
-    const int q = warp & 3, row = 32 * q + lane;           // TMEM lane quarter, tile row
-    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    // The last chunk of a ragged sequence is stored row by row.
+    auto by_rows = [&](int i) { return pl.n < a.N && (pl.c0 + i + 1) * kC > pl.n; };
     bool ok = true;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ TMA
+    if (warp == kWork) {
+        // ------------------------------------------------------------ TMA loads
         if (lane == 0) {
-            int i = 0, n = 0;
-            for (; i < pl.nc && ok && !hold; ++i) {
-                const int s = i & 1, t = (pl.c0 + i) * kC;
-                if (i >= 2 && !(ok = mbar_wait(&m.bc_empty[s], ((i >> 1) - 1) & 1, max_spin))) break;
-                mbar_arrive_expect_tx(&m.bc_full[s], 2 * kT * kTile);
-#pragma unroll
-                for (int k = 0; k < kT; ++k) {
-                    tma_load_4d(ctile(s) + k * kTile, &cmap, &m.bc_full[s], 64 * k, pl.g, t, pl.b);
-                    tma_load_4d(btile(s) + k * kTile, &bmap, &m.bc_full[s], 64 * k, pl.g, t, pl.b);
+            int i = 0, n = 0, c = 0;                       // chunks of B, value tiles, chunks of C issued
+            auto load_x = [&](int u, int t) -> bool {
+                if (n >= 2 && !mbar_wait(&m.x_empty[n & 1], ((n >> 1) - 1) & 1, max_spin)) return false;
+                // The value and gate tiles after this one come to L2 ahead of their use.
+                const int ia = i + (u + kAhead) / nu, ua = (u + kAhead) % nu;
+                if (ia < pl.nc) {
+                    const int ta = (pl.c0 + ia) * kC, ha = pl.head(a, un, ua), pa = pl.col0(un, ua);
+                    tma_prefetch_4d(&xmap, pa, ha, ta, pl.b);
+                    if (un.gate_vec) tma_prefetch_4d(&zmap, pa, ha, ta, pl.b);
                 }
-                for (int u = 0; u < nu; ++u, ++n) {
-                    if (n >= 2 && !(ok = mbar_wait(&m.x_empty[n & 1], ((n >> 1) - 1) & 1, max_spin))) break;
-                    mbar_arrive_expect_tx(&m.x_full[n & 1], kTile);
-                    tma_load_4d(xtile(n), &xmap, &m.x_full[n & 1], pl.col0(un, u), pl.head(a, un, u), t, pl.b);
-                }
-            }
-            // Every issued load (i chunks, n value tiles) lands before the CTA exits.
-            for (int j = max(i - 2, 0); j < i; ++j) mbar_wait(&m.bc_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
-            for (int j = max(n - 2, 0); j < n; ++j) mbar_wait(&m.x_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            const uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
-            const uint32_t id_y = idesc_bf16_f32(128, 64, false, true);
-            const uint32_t sba = smem_u32(sb), hia = smem_u32(xw_hi), loa = smem_u32(xw_lo);
-            auto scores = [&](int i) -> bool {
-                if (!mbar_wait(&m.bc_full[i & 1], (i >> 1) & 1, max_spin) ||
-                    (i >= 1 && !mbar_wait(&m.sc_empty, (i - 1) & 1, max_spin)))
-                    return false;
-                tc_fence_after();
-                const uint32_t ca = smem_u32(ctile(i & 1)), ba = smem_u32(btile(i & 1));
-#pragma unroll
-                for (int k = 0; k < 4 * kT; ++k) {
-                    const uint32_t off = (k >> 2) * kTile + (k & 3) * 32;
-                    mma_bf16(tmem + kTmSc, smem_desc(ca + off, 16, 1024, kSwizzle128B),
-                             smem_desc(ba + off, 16, 1024, kSwizzle128B), id_sc, k > 0);
-                }
-                mma_commit(&m.sc_full);
+                mbar_arrive_expect_tx(&m.x_full[n & 1], kTile);
+                tma_load_4d(xtile(n), &xmap, &m.x_full[n & 1], pl.col0(un, u), pl.head(a, un, u), t, pl.b);
+                ++n;
                 return true;
             };
-            if (pl.nc > 0) ok = scores(0);
-            for (int n = 0, i = 0, u = 0; n < items && ok; ++n) {
-                const int s = i & 1;
-                const uint32_t ca = smem_u32(ctile(s)), ba = smem_u32(btile(s)), xa = smem_u32(xtile(n));
-                // (2)
-                if (!(ok = mbar_wait(&m.sb_full, n & 1, max_spin) &&
-                           (n < 1 || mbar_wait(&m.y_empty, (n - 1) & 1, max_spin))))
-                    break;
-                tc_fence_after();
+            while (i < pl.nc && ok && !hold) {
+                const int s = i & 1, t = (pl.c0 + i) * kC;
+                if (i >= 2 && !(ok = mbar_wait(&m.b_empty[s], ((i >> 1) - 1) & 1, max_spin))) break;
+                mbar_arrive_expect_tx(&m.b_full[s], kT * kTile);
 #pragma unroll
-                for (int k = 0; k < 4 * kT; ++k)
-                    mma_bf16(tmem + kTmY2, smem_desc(ca + (k >> 2) * kTile + (k & 3) * 32, 16, 1024, kSwizzle128B),
-                             smem_desc(sba + k * 2048, 1024, 1024, kSwizzle128B), id_y, k > 0);
-                mma_commit(&m.sb_empty);
-                // (1) of the next chunk as soon as this chunk's scores have been read.
-                if (u == nu - 1 && i + 1 < pl.nc && !(ok = scores(i + 1))) break;
-                // (3)
-                if (!(ok = mbar_wait(&m.p_full[n & 1], (n >> 1) & 1, max_spin) &&
-                           mbar_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin)))
+                for (int k = 0; k < kT; ++k)
+                    tma_load_4d(btile(s) + k * kTile, &bmap, &m.b_full[s], 64 * k, pl.g, t, pl.b);
+                // C is free once the chunk before has been read from the state for its last unit.
+                ok = load_x(0, t) && (i < 1 || mbar_wait(&m.c_empty, (i - 1) & 1, max_spin));
+                if (ok) {
+                    mbar_arrive_expect_tx(&m.c_full, kT * kTile);
+#pragma unroll
+                    for (int k = 0; k < kT; ++k)
+                        tma_load_4d(base + L::kC0 + k * kTile, &cmap, &m.c_full, 64 * k, pl.g, t, pl.b);
+                    ++c;
+                    ok = nu < 2 || load_x(1, t);
+                }
+                ++i;
+            }
+            // Every issued load lands before the CTA exits.
+            for (int j = max(i - 2, 0); j < i; ++j) mbar_wait(&m.b_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
+            if (c > 0) mbar_wait(&m.c_full, (c - 1) & 1, kDefaultMaxSpin);
+            for (int j = max(n - 2, 0); j < n; ++j) mbar_wait(&m.x_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
+        }
+    } else if (warp == kWork + 1) {
+        // ------------------------------------------------------------ MMA
+        // The whole warp walks the loop (its values stay uniform), one lane issues.
+        constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t id_y = idesc_bf16_f32(128, 64, false, true);
+        const uint32_t base_a = smem_u32(base);
+        const uint64_t ca0 = kmajor_desc(base_a + L::kC0), bk0 = kmajor_desc(base_a + L::kB0);
+        const uint64_t br0 = rows_desc(base_a + L::kB0), x0 = rows_desc(base_a + L::kX);
+        const uint64_t sb0 = rows_desc(base_a + L::kSb), xw0 = rows_desc(base_a + L::kXw);
+        const bool leader = lane == 0;
+        for (int n = 0, i = 0, u = 0; n < items; ++n) {
+            if (u == 0) {                      // (1); the items before it have read the old scores
+                if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin) && warp_wait(&m.c_full, i & 1, max_spin)))
                     break;
-                // Rows past a ragged end are cleared by the weights' warps first.
-                const bool ragged = a.lengths && (pl.c0 + i + 1) * kC > pl.n;
-                if (ragged && !(ok = mbar_wait(&m.xw_full, n & 1, max_spin))) break;
                 tc_fence_after();
+                if (leader) {
+                    const uint64_t ba = step_desc(bk0, (i & 1) * kT * kTile);
+#pragma unroll
+                    for (int k = 0; k < 4 * kT; ++k)
+                        mma_bf16(tmem + kTmSc, kmajor_step(ca0, k), kmajor_step(ba, k), id_sc, k > 0);
+                    mma_commit(&m.sc_full);
+                }
+                __syncwarp();
+            }
+            if (!(ok = warp_wait(&m.item_ready, n & 1, max_spin))) break;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4 * kT; ++k)                                        // (2)
+                    mma_bf16(tmem + kTmY2, kmajor_step(ca0, k), step_desc(sb0, k * 2048), id_y, k > 0);
+                mma_commit(&m.read_done);
+                if (u == nu - 1) mma_commit(&m.c_empty);
+                const uint64_t xa = step_desc(x0, (n & 1) * kTile);
                 const uint32_t pt = tmem + kTmP + 64 * (n & 1);
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k)
-                    mma_bf16_ts(tmem + kTmY1, pt + 8 * k, smem_desc(xa + k * 2048, 1024, 1024, kSwizzle128B),
-                                id_y, k > 0);
-                mma_commit(&m.p_empty[n & 1]);
-                mma_commit(&m.x_empty[n & 1]);
+                for (int k = 0; k < kC / 16; ++k)                                       // (3)
+                    mma_bf16_ts(tmem + kTmY1, pt + 8 * k, step_desc(xa, k * 2048), id_y, k > 0);
                 mma_commit(&m.y_full);
-                // (4)
-                if (!(ok = mbar_wait(&m.xw_full, n & 1, max_spin))) break;
-                tc_fence_after();
-                issue_state(tmem + kTmSt + 64 * u, ba, hia, loa, false);
-                mma_commit(&m.xw_empty);
-                mma_commit(&m.st_full[u]);
-                if (++u == nu) {
-                    mma_commit(&m.bc_empty[s]);
-                    u = 0;
-                    ++i;
-                }
+                issue_state(tmem + kTmSt + 64 * u, step_desc(br0, (i & 1) * kT * kTile), xw0, false);  // (4)
+                mma_commit(&m.state_done);
+                if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
+            __syncwarp();
+            if (++u == nu) u = 0, ++i;
+        }
+        if (leader) {
             mma_commit(&m.drain);              // every issued MMA completes before TMEM is released
             ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
         }
-    } else if (warp < 4) {
-        // ------------------------------------------------------------ decays, unit warp - 2
-        const int u = warp - 2;
-        if (u < nu && pl.nc > 0) {
-            const int h = pl.head(a, un, u);
-            const float A2 = a.A[h] * kLog2e, bias = a.step_bias ? a.step_bias[h] : 0.f;
-            float raw[4];
-            load_steps(a, pl, h, pl.c0, raw);
-            for (int i = 0; i < pl.nc; ++i) {
-                const int n = i * nu + u, slot = n % kDtRing;
-                float next[4] = {};
-                if (i + 1 < pl.nc) load_steps(a, pl, h, pl.c0 + i + 1, next);
-                float d[4], cum[4], suf[4], total;
-                decays(a, pl, pl.c0 + i, A2, bias, raw, d, cum, suf, &total);
-                if (n >= kDtRing && !(ok = warp_wait(&m.dt_empty[slot], (n / kDtRing - 1) & 1, max_spin))) break;
-                Decay& o = dts[slot];
-                *reinterpret_cast<float4*>(o.cum + 4 * lane) = make_float4(cum[0], cum[1], cum[2], cum[3]);
-                *reinterpret_cast<float4*>(o.d + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
-                *reinterpret_cast<float4*>(o.w + 4 * lane) =
-                    make_float4(d[0] * exp2f(suf[0]), d[1] * exp2f(suf[1]), d[2] * exp2f(suf[2]), d[3] * exp2f(suf[3]));
-                if (lane == 0) o.total = exp2f(total);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&m.dt_full[slot]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) raw[k] = next[k];
-            }
-        }
-    } else if (warp < 8) {
-        // ------------------------------------------------------------ scores -> P
-        float* col = reinterpret_cast<float*>(base + L::kCol) + q * 96;
-        // Blocks above the diagonal are zero in both buffers, once.
-        {
-            const uint32_t z[16] = {};
-            for (int b = q + 1; b < 4; ++b) {
-                tmem_st16(tmem + lanes + kTmP + 16 * b, z);
-                tmem_st16(tmem + lanes + kTmP + 64 + 16 * b, z);
-            }
-            tmem_st_wait();
-        }
+        __syncwarp();
+    } else if (warp == kWork + 2) {
+        // ------------------------------------------------------------ step sizes to decays
+        const int h0 = pl.head(a, un, 0), h1 = pl.head(a, un, nu - 1);
+        const float A0 = a.A[h0] * kLog2e, A1 = a.A[h1] * kLog2e;
+        const float b0 = a.step_bias ? a.step_bias[h0] : 0.f, b1 = a.step_bias ? a.step_bias[h1] : 0.f;
+        float raw[4];
+        if (items > 0) load_steps(a, pl, h0, pl.c0, raw);
         for (int n = 0, i = 0, u = 0; n < items; ++n) {
-            const int slot = n % kDtRing;
-            if (!(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin))) break;
-            const Decay& dc = dts[slot];
-            const float ci = dc.cum[row];
-            const float cm = q ? dc.cum[32 * q - 1] : 0.f;
-            for (int b = 0; b < q; ++b)
-                col[32 * b + lane] = ex2(cm - dc.cum[32 * b + lane]) * dc.d[32 * b + lane];
+            const int slot = n % kDtRing, in = u + 1 == nu ? i + 1 : i, next_u = u + 1 == nu ? 0 : 1;
+            float next[4] = {};
+            if (n + 1 < items) load_steps(a, pl, next_u ? h1 : h0, pl.c0 + in, next);
+            float d[4], cum[4], suf[4], total;
+            decays(a, pl, pl.c0 + i, u ? A1 : A0, u ? b1 : b0, raw, d, cum, suf, &total);
+            if (n >= kDtRing && !(ok = warp_wait(&m.dt_empty[slot], (n / kDtRing - 1) & 1, max_spin))) break;
+            Decay& o = dts[slot];
+            *reinterpret_cast<float4*>(o.cum + 4 * lane) = make_float4(cum[0], cum[1], cum[2], cum[3]);
+            *reinterpret_cast<float4*>(o.d + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4*>(o.w + 4 * lane) =
+                make_float4(d[0] * ex2(suf[0]), d[1] * ex2(suf[1]), d[2] * ex2(suf[2]), d[3] * ex2(suf[3]));
+            if (lane == 0) o.total = ex2(total);
             __syncwarp();
-            const float ri = ex2(ci - cm);
-            const uint64_t r2 = pk2(ri, ri);
-            if (u == 0 && !(ok = warp_wait(&m.sc_full, i & 1, max_spin))) break;
-            if (n >= 2 && !(ok = warp_wait(&m.p_empty[n & 1], ((n >> 1) - 1) & 1, max_spin))) break;
-            tc_fence_after();
-            const uint32_t src = tmem + lanes + kTmSc, dst = tmem + lanes + kTmP + 64 * (n & 1);
-            for (int b = 0; b < q; ++b) {
-                uint32_t s0[16], s1[16], p[16];
-                tmem_ld16(src + 32 * b, s0);
-                tmem_ld16(src + 32 * b + 16, s1);
-                tmem_ld_wait();
+            if (lane == 0) mbar_arrive(&m.dt_full[slot]);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 f = *reinterpret_cast<const float4*>(col + 32 * b + 2 * e);
-                    const uint32_t* s = e < 8 ? s0 + 2 * e : s1 + 2 * e - 16;
-                    p[e] = pack2(mul2(mul2(pk2(__uint_as_float(s[0]), __uint_as_float(s[1])), pk2(f.x, f.y)), r2));
-                    p[e + 1] = pack2(mul2(mul2(pk2(__uint_as_float(s[2]), __uint_as_float(s[3])), pk2(f.z, f.w)), r2));
-                }
-                tmem_st16(dst + 16 * b, p);
-            }
-            {
-                uint32_t s0[16], s1[16], p[16];
-                tmem_ld16(src + 32 * q, s0);
-                tmem_ld16(src + 32 * q + 16, s1);
-                tmem_ld_wait();
-                if (u == nu - 1) {             // the chunk's scores have been read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&m.sc_empty);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 l = *reinterpret_cast<const float4*>(dc.cum + 32 * q + 2 * e);
-                    const float4 d = *reinterpret_cast<const float4*>(dc.d + 32 * q + 2 * e);
-                    const uint32_t* s = e < 8 ? s0 + 2 * e : s1 + 2 * e - 16;
-                    const float lj[4] = {l.x, l.y, l.z, l.w}, dj[4] = {d.x, d.y, d.z, d.w};
-                    float v[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = 2 * e + k <= lane ? __uint_as_float(s[k]) * (ex2(ci - lj[k]) * dj[k]) : 0.f;
-                    p[e] = pack_bf16(v[0], v[1]);
-                    p[e + 1] = pack_bf16(v[2], v[3]);
-                }
-                tmem_st16(dst + 16 * q, p);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&m.p_full[n & 1]);
-                mbar_arrive(&m.dt_empty[slot]);
-            }
-            if (++u == nu) u = 0, ++i;
+            for (int k = 0; k < 4; ++k) raw[k] = next[k];
+            i = in, u = next_u;
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------------------ state
-        if (q < 2 * kT) {
-            const int64_t head_state = (int64_t)a.S * a.P;
-            // The state before the first chunk: row `row` of each unit.
-            for (int u = 0; u < nu; ++u) {
-                const int64_t bh = (int64_t)pl.b * a.H + pl.head(a, un, u);
-                const float* from = a.nseg > 1 ? a.seeds + (bh * a.nseg + pl.seg) * head_state
-                                               : (a.S0 ? a.S0 + bh * head_state : nullptr);
-                const int p0 = pl.col0(un, u), np = min(64, a.P - p0);
-                const float* r = from && row < a.S ? from + (int64_t)row * a.P + p0 : nullptr;
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        const uint4 x = r && c + k < np ? *reinterpret_cast<const uint4*>(r + c + k) : make_uint4(0, 0, 0, 0);
-                        v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
-                    }
-                    tmem_st16(tmem + lanes + kTmSt + 64 * u + c, v);
+    } else if (warp == kWork + 3) {
+        // ------------------------------------------------------------ output slots
+        if (lane == 0) {
+            const bool gate = un.gate_vec != 0;
+            int opened = 0;
+            // Slot of the next item: its gate on the way, or just free.
+            auto open_slot = [&](int i, int u) {
+                uint64_t* bar = &m.slot_ready[opened & 1];
+                if (gate) {
+                    mbar_arrive_expect_tx(bar, kTile);
+                    tma_load_4d(oslot(opened), &zmap, bar, pl.col0(un, u), pl.head(a, un, u), (pl.c0 + i) * kC, pl.b);
+                } else {
+                    mbar_arrive(bar);
                 }
-            }
-            tmem_st_wait();
+                ++opened;
+            };
+            for (int n = 0; n < 2 && n < items && !hold; ++n) open_slot(n / nu, n % nu);
             for (int n = 0, i = 0, u = 0; n < items; ++n) {
-                const int slot = n % kDtRing;
-                if (!(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin) &&
-                           (i < 1 || warp_wait(&m.st_full[u], (i - 1) & 1, max_spin)) &&
-                           (n < 1 || warp_wait(&m.sb_empty, (n - 1) & 1, max_spin))))
-                    break;
-                tc_fence_after();
-                const float f = dts[slot].total;
-                const uint64_t f2 = pk2(f, f);
-                const uint32_t st = tmem + lanes + kTmSt + 64 * u;
+                if (!(ok = mbar_wait(&m.y_staged[n & 1], (n >> 1) & 1, max_spin))) break;
+                if (!by_rows(i)) {
+                    tma_store_4d(&ymap, oslot(n), pl.col0(un, u), pl.head(a, un, u), (pl.c0 + i) * kC, pl.b);
+                    tma_store_commit();
+                    tma_store_wait_read<0>();
+                }
+                if (n + 2 < items) open_slot((n + 2) / nu, (n + 2) % nu);
+                if (++u == nu) u = 0, ++i;
+            }
+            // Every gate that was asked for lands before the CTA exits.
+            for (int j = max(opened - 2, 0); j < opened; ++j)
+                mbar_wait(&m.slot_ready[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
+        }
+    } else {
+        // ------------------------------------------------------------ the items' steps
+        const int q = warp & 3, g = warp >> 2, row = 32 * q + lane;   // TMEM lane quarter, column group
+        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        const int64_t head_state = (int64_t)a.S * a.P;
+        const bool has_state = q < 2 * kT, gated = a.z != nullptr, tma_gate = un.gate_vec != 0;
+        float* col = reinterpret_cast<float*>(base + L::kCol) + 32 * warp;
+        uint8_t* sb = base + L::kSb;
+        // This lane's two 16-byte pieces of columns 16 g .. 16 g + 15 in a swizzled tile.
+        const uint32_t pc0 = row * 128 + (((2 * g) ^ (row & 7)) << 4), pc1 = row * 128 + (((2 * g + 1) ^ (row & 7)) << 4);
+        if (g > q) {                           // blocks above the diagonal are zero in both P buffers
+            const uint32_t z[16] = {};
+            tmem_st16(tmem + lanes + kTmP + 16 * g, z);
+            tmem_st16(tmem + lanes + kTmP + 64 + 16 * g, z);
+            tmem_st_wait();
+        }
+        float Du[2];
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t v[2][16];
-                    tmem_ld16(st + c, v[0]);
-                    tmem_ld16(st + c + 16, v[1]);
+        for (int u = 0; u < 2; ++u) {
+            const int h = pl.head(a, un, min(u, nu - 1)), c0 = pl.col0(un, min(u, nu - 1)) + 16 * g;
+            Du[u] = a.D ? a.D[h] : 0.f;
+            if (!has_state || u >= nu) continue;
+            // The state before the first chunk.
+            const int64_t bh = (int64_t)pl.b * a.H + h;
+            const float* from = a.nseg > 1 ? a.seeds + (bh * a.nseg + pl.seg) * head_state
+                                           : (a.S0 ? a.S0 + bh * head_state : nullptr);
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                const uint4 x = from && row < a.S && c0 + k < a.P
+                                    ? *reinterpret_cast<const uint4*>(from + (int64_t)row * a.P + c0 + k)
+                                    : make_uint4(0, 0, 0, 0);
+                v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
+            }
+            tmem_st16(tmem + lanes + kTmSt + 64 * u + 16 * g, v);
+            tmem_st_wait();
+        }
+        for (int n = 0, i = 0, u = 0; n <= items; ++n) {
+            const int slot = n % kDtRing;
+            const Decay& dc = dts[slot];
+            if (n < items && !(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin))) break;
+            // Scores to P first, except at a chunk's start, where (1) is still under way.
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                if ((pass == 0) == (u != 0)) {
+                    // ------------------------------------------------ scores to P
+                    if (n == items || g > q) continue;
+                    const uint32_t dst = tmem + lanes + kTmP + 64 * (n & 1) + 16 * g;
+                    const float ci = dc.cum[row];
+                    if (g < q) col[lane] = ex2(dc.cum[32 * q - 1] - dc.cum[32 * g + lane]) * dc.d[32 * g + lane];
+                    __syncwarp();
+                    if (!(ok = warp_wait(&m.sc_full, i & 1, max_spin))) break;
+                    tc_fence_after();
+                    uint32_t s[2][16], p[16];
+                    tmem_ld16(tmem + lanes + kTmSc + 32 * g, s[0]);
+                    tmem_ld16(tmem + lanes + kTmSc + 32 * g + 16, s[1]);
                     tmem_ld_wait();
+                    if (g < q) {
+                        const float ri = ex2(ci - dc.cum[32 * q - 1]);
+                        const uint64_t r2 = pk2(ri, ri);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t h[8];
+                        for (int e = 0; e < 16; e += 2) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(col + 2 * e);
+                            const uint32_t* v = &s[e >> 3][2 * (e & 7)];
+                            p[e] = pack2(mul2(mul2(pk2(__uint_as_float(v[0]), __uint_as_float(v[1])), f.x), r2));
+                            p[e + 1] = pack2(mul2(mul2(pk2(__uint_as_float(v[2]), __uint_as_float(v[3])), f.y), r2));
+                        }
+                    } else {
+                        // The diagonal block: an exponential per score; pairs past the row's own
+                        // token are cleared as bits (their products may be anything).
+                        const uint64_t c2 = pk2(ci, ci), minus = pk2(-1.f, -1.f);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dc.cum + 32 * q + 2 * e);
+                            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(dc.d + 32 * q + 2 * e);
+                            const uint32_t* v = &s[e >> 3][2 * (e & 7)];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float t0, t1;
+                                unpk2(fma2(k ? l.y : l.x, minus, c2), &t0, &t1);
+                                const uint64_t f = mul2(pk2(ex2(t0), ex2(t1)), k ? d.y : d.x);
+                                const uint32_t w = pack2(mul2(f, pk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]))));
+                                const int j = 2 * (e + k);
+                                p[e + k] = j < lane ? w : (j == lane ? w & 0xFFFFu : 0u);
+                            }
+                        }
+                    }
+                    tmem_st16(dst, p);
+                    tmem_st_wait();
+                    continue;
+                }
+                // ---------------------------------------------------- state: bf16 for (2), scaled for (4)
+                if (n < items) {
+                    if (n > 0 && !(ok = warp_wait(&m.read_done, (n - 1) & 1, max_spin))) break;
+                    if (nu == 1 && n > 0 && !(ok = warp_wait(&m.state_done, (n - 1) & 1, max_spin))) break;
+                    if (has_state) {
+                        tc_fence_after();
+                        const uint32_t st = tmem + lanes + kTmSt + 64 * u + 16 * g;
+                        const float f = dc.total;
+                        const uint64_t f2 = pk2(f, f);
+                        uint32_t v[16], h[8];
+                        tmem_ld16(st, v);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const uint64_t x = pk2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1]));
-                            h[e] = row < a.S ? pack2(x) : 0u;
+                            const uint64_t x = pk2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                            h[e] = row < a.S ? pack2(x) : 0u;   // padding rows never reach the read
                             float lo, hi;
                             unpk2(mul2(x, f2), &lo, &hi);
-                            v[k][2 * e] = __float_as_uint(lo);
-                            v[k][2 * e + 1] = __float_as_uint(hi);
+                            v[2 * e] = __float_as_uint(lo);
+                            v[2 * e + 1] = __float_as_uint(hi);
                         }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<uint4*>(sb + sw128_offset(row, c + 16 * k + 8 * e)) =
-                                make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
-                        tmem_st16(st + c + 16 * k, v[k]);
+                        *reinterpret_cast<uint4*>(sb + pc0) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(sb + pc1) = make_uint4(h[4], h[5], h[6], h[7]);
+                        tmem_st16(st, v);
+                        tmem_st_wait();
                     }
                 }
-                tmem_st_wait();
+                // ---------------------------------------------------- output of the item before
+                if (n > 0) {
+                    const int pn = n - 1, pu = u == 0 ? nu - 1 : u - 1, pi = u == 0 ? i - 1 : i;
+                    const int ps = pn % kDtRing;
+                    const float Dh = pu ? Du[1] : Du[0], e = ex2(dts[ps].cum[row]);
+                    const uint64_t D2 = pk2(Dh, Dh), e2 = pk2(e, e);
+                    const uint4 xv[2] = {*reinterpret_cast<const uint4*>(xtile(pn) + pc0),
+                                         *reinterpret_cast<const uint4*>(xtile(pn) + pc1)};
+                    if (!(ok = warp_wait(&m.slot_ready[pn & 1], (pn >> 1) & 1, max_spin) &&
+                               warp_wait(&m.y_full, pn & 1, max_spin)))
+                        break;
+                    tc_fence_after();
+                    uint32_t y1[16], y2[16];
+                    tmem_ld16(tmem + lanes + kTmY1 + 16 * g, y1);
+                    tmem_ld16(tmem + lanes + kTmY2 + 16 * g, y2);
+                    tmem_ld_wait();
+                    const int t = (pl.c0 + pi) * kC + row, h = pl.head(a, un, pu), c0 = pl.col0(un, pu) + 16 * g;
+                    const bool rows = by_rows(pi);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint4* at = reinterpret_cast<uint4*>(oslot(pn) + (j ? pc1 : pc0));
+                        const uint32_t xs[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+                        const bool live = t < pl.n && c0 + 8 * j < a.P;
+                        uint4 z = make_uint4(0, 0, 0, 0);
+                        if (gated) {
+                            if (tma_gate) z = *at;
+                            else if (live)
+                                z = load_gate(static_cast<const __nv_bfloat16*>(a.z) + pl.b * a.z_bs + (int64_t)t * a.z_ts +
+                                              (int64_t)h * a.P + c0 + 8 * j);
+                        }
+                        const uint32_t zs[4] = {z.x, z.y, z.z, z.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int f = 8 * j + 2 * k;
+                            uint64_t v = fma2(e2, pk2(__uint_as_float(y2[f]), __uint_as_float(y2[f + 1])),
+                                              pk2(__uint_as_float(y1[f]), __uint_as_float(y1[f + 1])));
+                            v = fma2(D2, bf2(xs[k]), v);
+                            if (gated) v = mul2(v, gate2(zs[k]));
+                            o[k] = pack2(v);
+                        }
+                        if (!rows)
+                            *at = make_uint4(o[0], o[1], o[2], o[3]);
+                        else if (live)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + pl.b * a.y_bs + (int64_t)t * a.y_ts +
+                                                      (int64_t)h * a.P + c0 + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    fence_proxy_async_smem();              // the store reads the slot
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&m.y_staged[pn & 1]);
+                        mbar_arrive(&m.x_empty[pn & 1]);
+                        mbar_arrive(&m.dt_empty[ps]);
+                    }
+                }
+                // ---------------------------------------------------- weighted values
+                if (n < items) {
+                    if (!(ok = warp_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin) &&
+                               (n < 1 || warp_wait(&m.state_done, (n - 1) & 1, max_spin))))
+                        break;
+                    // Rows at or past a ragged end may hold anything: they are cleared in x, and in
+                    // B for (4). (1) may read such rows of B, whose scores no kept row uses.
+                    if (a.lengths && (pl.c0 + i + 1) * kC > pl.n) {       // uniform over the block
+                        if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin))) break;
+                        if ((pl.c0 + i) * kC + row >= pl.n) {
+                            *reinterpret_cast<uint4*>(xtile(n) + pc0) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(xtile(n) + pc1) = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < kT && u == 0; ++k) {
+                                *reinterpret_cast<uint4*>(btile(i & 1) + k * kTile + pc0) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(btile(i & 1) + k * kTile + pc1) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                    }
+                    weigh_row(xtile(n), base + L::kXw, base + L::kXw + kTile, row, dc.w[row], 2 * g, 2 * g + 2);
+                }
+            }
+            if (!ok) break;
+            if (n < items) {
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&m.sb_full);
-                    mbar_arrive(&m.dt_empty[slot]);
-                }
+                if (lane == 0) mbar_arrive(&m.item_ready);
                 if (++u == nu) u = 0, ++i;
             }
-            // The final state.
-            if (ok && last_seg && a.S_out) {
-                for (int u = 0; u < nu && ok; ++u) {
-                    if (pl.nc > 0 && !(ok = warp_wait(&m.st_full[u], (pl.nc - 1) & 1, max_spin))) break;
-                    tc_fence_after();
-                    const int64_t bh = (int64_t)pl.b * a.H + pl.head(a, un, u);
-                    const int p0 = pl.col0(un, u), np = min(64, a.P - p0);
-                    float* r = a.S_out + bh * head_state + (int64_t)row * a.P + p0;
-#pragma unroll
-                    for (int c = 0; c < 64; c += 16) {
-                        uint32_t v[16];
-                        tmem_ld16(tmem + lanes + kTmSt + 64 * u + c, v);
-                        tmem_ld_wait();
-                        if (row >= a.S) continue;
-#pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            if (c + k < np)
-                                *reinterpret_cast<uint4*>(r + c + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                    }
-                }
-            }
         }
-    } else if (warp < 16) {
-        // ------------------------------------------------------------ weighted values
-        for (int n = 0, i = 0, u = 0; n < items; ++n) {
-            const int slot = n % kDtRing;
-            if (!(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin) &&
-                       warp_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin) &&
-                       (n < 1 || warp_wait(&m.xw_empty, (n - 1) & 1, max_spin))))
-                break;
-            // Rows at or past a ragged end may hold anything: they are cleared in x, and in B
-            // for (4). (1) may read such rows of B, whose scores no kept row uses.
-            if (a.lengths && (pl.c0 + i + 1) * kC > pl.n) {        // uniform over the block
-                if (!(ok = warp_wait(&m.bc_full[i & 1], (i >> 1) & 1, max_spin))) break;
-                if ((pl.c0 + i) * kC + row >= pl.n) {
-                    zero_row(xtile(n), row);
-                    for (int k = 0; k < kT && u == 0; ++k) zero_row(btile(i & 1) + k * kTile, row);
+        // The final state.
+        if (ok && last_seg && a.S_out && has_state) {
+            if (items == 0 || (ok = warp_wait(&m.state_done, (items - 1) & 1, max_spin))) {
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u >= nu) break;
+                    const int c0 = pl.col0(un, u) + 16 * g;
+                    uint32_t v[16];
+                    tmem_ld16(tmem + lanes + kTmSt + 64 * u + 16 * g, v);
+                    tmem_ld_wait();
+                    float* to = a.S_out + ((int64_t)pl.b * a.H + pl.head(a, un, u)) * head_state + (int64_t)row * a.P + c0;
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4)
+                        if (row < a.S && c0 + k < a.P)
+                            *reinterpret_cast<uint4*>(to + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                 }
             }
-            weigh_row(xtile(n), xw_hi, xw_lo, row, dts[slot].w[row]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&m.xw_full);
-                mbar_arrive(&m.x_empty[n & 1]);
-                mbar_arrive(&m.dt_empty[slot]);
-            }
-            if (++u == nu) u = 0, ++i;
-        }
-    } else {
-        // ------------------------------------------------------------ output
-        for (int n = 0, i = 0, u = 0; n < items; ++n) {
-            const int slot = n % kDtRing;
-            const int t = (pl.c0 + i) * kC + row, h = pl.head(a, un, u), p0 = pl.col0(un, u);
-            const int pieces = min(64, a.P - p0) >> 3;
-            const bool live = t < pl.n;
-            const __nv_bfloat16* zr = static_cast<const __nv_bfloat16*>(a.z) + pl.b * a.z_bs +
-                                      (int64_t)t * a.z_ts + (int64_t)h * a.P + p0;
-            __nv_bfloat16* yr = static_cast<__nv_bfloat16*>(a.y) + pl.b * a.y_bs + (int64_t)t * a.y_ts +
-                                (int64_t)h * a.P + p0;
-            uint4 z[8];
-            if (a.z) load_gate(zr, live ? pieces : 0, un.gate_vec != 0, z);
-            const float Dh = a.D ? a.D[h] : 0.f;
-            const uint64_t D2 = pk2(Dh, Dh);
-            if (!(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin) &&
-                       warp_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin) &&
-                       warp_wait(&m.y_full, n & 1, max_spin)))
-                break;
-            tc_fence_after();
-            const float e = ex2(dts[slot].cum[row]);
-            const uint64_t e2 = pk2(e, e);
-            const uint8_t* xr = xtile(n) + row * 128;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t y1[16], y2[16];
-                tmem_ld16(tmem + lanes + kTmY1 + 16 * c, y1);
-                tmem_ld16(tmem + lanes + kTmY2 + 16 * c, y2);
-                tmem_ld_wait();
-                if (c == 3) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&m.y_empty);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int piece = 2 * c + j;
-                    const uint4 xv = *reinterpret_cast<const uint4*>(xr + ((piece ^ (row & 7)) << 4));
-                    const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-                    const uint32_t zs[4] = {z[piece].x, z[piece].y, z[piece].z, z[piece].w};
-                    uint32_t out[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int at = 8 * j + 2 * k;
-                        uint64_t v = fma2(e2, pk2(__uint_as_float(y2[at]), __uint_as_float(y2[at + 1])),
-                                          pk2(__uint_as_float(y1[at]), __uint_as_float(y1[at + 1])));
-                        v = fma2(D2, bf2(xs[k]), v);
-                        if (a.z) {
-                            const float z0 = __uint_as_float(zs[k] << 16), z1 = __uint_as_float(zs[k] & 0xFFFF0000u);
-                            v = mul2(v, pk2(silu(z0), silu(z1)));
-                        }
-                        out[k] = pack2(v);
-                    }
-                    if (live && piece < pieces)
-                        reinterpret_cast<uint4*>(yr)[piece] = make_uint4(out[0], out[1], out[2], out[3]);
-                }
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&m.x_empty[n & 1]);
-                mbar_arrive(&m.dt_empty[slot]);
-            }
-            if (++u == nu) u = 0, ++i;
         }
     }
     if (!ok) report_timeout(hdr);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == kWork + 1) tmem_dealloc(tmem, 512);
 }
 
 // First pass over segments: end state from zero, sum over the segment of
 // B_j (d_j e^{l(end) - l_j} x_j)^T, and the segment's total decay. Chunks run from
 // the last to the first; the weights carry the sum of the chunks after them.
-// Warps: TMA, MMA, decays (two), then two weight groups of four that alternate.
-constexpr int kSumThreads = 384;
+// Warps: TMA, MMA, decays (two), then four weight groups of four: two items at a
+// time, half of the columns each (one group per item left the pass waiting for
+// its weights).
+constexpr int kSumThreads = 640, kSumRing = 4;
 
 struct SumMisc {
-    uint64_t b_full[2], b_empty[2], x_full[4], x_empty[4], dt_full[kDtRing], dt_empty[kDtRing];
+    uint64_t b_full[2], b_empty[2], x_full[4], x_empty[4], dt_full[kSumRing], dt_empty[kSumRing];
     uint64_t xw_full[2], xw_empty[2], drain;
     uint32_t tmem_slot;
 };
@@ -726,7 +750,7 @@ template <int kT> struct SumSmem {
     static constexpr uint32_t kX = 2 * kT * kTile;
     static constexpr uint32_t kXw = kX + 4 * kTile;
     static constexpr uint32_t kW = kXw + 4 * kTile;
-    static constexpr uint32_t kMisc = kW + kDtRing * kC * 4;
+    static constexpr uint32_t kMisc = kW + kSumRing * kC * 4;
     static constexpr size_t kBytes = 1024 + kMisc + sizeof(SumMisc);
 };
 
@@ -751,14 +775,14 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.b_full[s], 1);
             mbar_init(&m.b_empty[s], 1);
-            mbar_init(&m.xw_full[s], 4);
+            mbar_init(&m.xw_full[s], 8);
             mbar_init(&m.xw_empty[s], 1);
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(&m.x_full[s], 1);
-            mbar_init(&m.x_empty[s], 4);
+            mbar_init(&m.x_empty[s], 8);
             mbar_init(&m.dt_full[s], 1);
-            mbar_init(&m.dt_empty[s], 4);
+            mbar_init(&m.dt_empty[s], 8);
         }
         mbar_init(&m.drain, 1);
         fence_mbar_init();
@@ -796,24 +820,26 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
             for (int j = max(n - 4, 0); j < n; ++j) mbar_wait(&m.x_full[j & 3], (j >> 2) & 1, kDefaultMaxSpin);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            for (int n = 0, i = 0, u = 0; n < items; ++n) {
-                if (!(ok = mbar_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin) &&
-                           mbar_wait(&m.xw_full[n & 1], (n >> 1) & 1, max_spin)))
-                    break;
-                tc_fence_after();
-                const uint32_t xw = smem_u32(xwtile(n));
-                issue_state(tmem + 64 * u, smem_u32(btile(i & 1)), xw, xw + kTile, i == 0);
+        const uint32_t base_a = smem_u32(base);
+        const uint64_t br0 = rows_desc(base_a), xw0 = rows_desc(base_a + L::kXw);
+        for (int n = 0, i = 0, u = 0; n < items; ++n) {
+            if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin) &&
+                       warp_wait(&m.xw_full[n & 1], (n >> 1) & 1, max_spin)))
+                break;
+            tc_fence_after();
+            if (lane == 0) {
+                issue_state(tmem + 64 * u, step_desc(br0, (i & 1) * kT * kTile), step_desc(xw0, (n & 1) * 2 * kTile), i == 0);
                 mma_commit(&m.xw_empty[n & 1]);
-                if (++u == nu) {
-                    mma_commit(&m.b_empty[i & 1]);
-                    u = 0;
-                    ++i;
-                }
+                if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
+            __syncwarp();
+            if (++u == nu) u = 0, ++i;
+        }
+        if (lane == 0) {
             mma_commit(&m.drain);
             ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
         }
+        __syncwarp();
     } else if (warp < 4) {
         const int u = warp - 2;
         if (u < nu) {
@@ -822,15 +848,15 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
             float raw[4] = {}, after = 0.f;            // after: sum over the chunks behind
             if (pl.nc > 0) load_steps(a, pl, h, c_last, raw);
             for (int i = 0; i < pl.nc; ++i) {
-                const int n = i * nu + u, slot = n % kDtRing;
+                const int n = i * nu + u, slot = n % kSumRing;
                 float next[4] = {};
                 if (i + 1 < pl.nc) load_steps(a, pl, h, c_last - i - 1, next);
                 float d[4], cum[4], suf[4], total;
                 decays(a, pl, c_last - i, A2, bias, raw, d, cum, suf, &total);
-                if (n >= kDtRing && !(ok = warp_wait(&m.dt_empty[slot], (n / kDtRing - 1) & 1, max_spin))) break;
+                if (n >= kSumRing && !(ok = warp_wait(&m.dt_empty[slot], (n / kSumRing - 1) & 1, max_spin))) break;
                 *reinterpret_cast<float4*>(wts + slot * kC + 4 * lane) =
-                    make_float4(d[0] * exp2f(suf[0] + after), d[1] * exp2f(suf[1] + after),
-                                d[2] * exp2f(suf[2] + after), d[3] * exp2f(suf[3] + after));
+                    make_float4(d[0] * ex2(suf[0] + after), d[1] * ex2(suf[1] + after),
+                                d[2] * ex2(suf[2] + after), d[3] * ex2(suf[3] + after));
                 after += total;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.dt_full[slot]);
@@ -841,21 +867,21 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
                 a.seg_decay[((int64_t)pl.b * a.H + h) * a.nseg + pl.seg] = after * kLn2;
         }
     } else {
-        const int grp = (warp - 4) >> 2;
-        for (int n = grp; n < items; n += 2) {
-            const int slot = n % kDtRing, i = n / nu, u = n - i * nu;
-            if (!(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin) &&
+        const int grp = (warp - 4) >> 2, half = grp >> 1;
+        for (int n = grp & 1; n < items; n += 2) {
+            const int slot = n % kSumRing, i = n / nu, u = n - i * nu;
+            if (!(ok = warp_wait(&m.dt_full[slot], (n / kSumRing) & 1, max_spin) &&
                        warp_wait(&m.x_full[n & 3], (n >> 2) & 1, max_spin) &&
                        (n < 2 || warp_wait(&m.xw_empty[n & 1], ((n >> 1) - 1) & 1, max_spin))))
                 break;
             if (a.lengths && (c_last - i + 1) * kC > pl.n) {
                 if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin))) break;
-                if ((c_last - i) * kC + row >= pl.n) {
+                if ((c_last - i) * kC + row >= pl.n) {     // both halves write the same zeros
                     zero_row(xtile(n), row);
                     for (int k = 0; k < kT && u == 0; ++k) zero_row(btile(i & 1) + k * kTile, row);
                 }
             }
-            weigh_row(xtile(n), xwtile(n), xwtile(n) + kTile, row, wts[slot * kC + row]);
+            weigh_row(xtile(n), xwtile(n), xwtile(n) + kTile, row, wts[slot * kC + row], 4 * half, 4 * half + 4);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -919,8 +945,8 @@ Units units_of(int H, int G, int P) {
 
 // CTAs run in waves over the SMs, so the number of segments is the one whose
 // waves times chunks is least. In units of one chunk of the main pass: a CTA
-// spends about two on starting and ending, the first pass 0.4 per chunk, and
-// two further launches about two.
+// spends about two on starting and ending, the first pass 0.4 per chunk, two
+// further launches about two, and chaining the segments' states 0.2 per segment.
 int pick_segments(int64_t ctas, int N) {
     const int nch = (N + kC - 1) / kC, sms = sm_count();
     int best = 1;
@@ -929,14 +955,14 @@ int pick_segments(int64_t ctas, int N) {
         const int cps = (nch + n - 1) / n;
         if ((nch + cps - 1) / cps != n) continue;      // the same split with empty segments
         const double waves = (double)((ctas * n + sms - 1) / sms);
-        const double cost = waves * (cps + 2.0) + (n > 1 ? waves * (0.4 * cps + 1.5) + 2.0 : 0.0);
+        const double cost = waves * (cps + 2.0) + (n > 1 ? waves * (0.4 * cps + 1.5) + 2.0 + 0.2 * n : 0.0);
         if (cost < least) least = cost, best = n;
     }
     return best;
 }
 
 template <int kT>
-cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorMap& cm, const ScanArgs& a,
+cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorMap& cm, const CUtensorMap& zm, const CUtensorMap& ym, const ScanArgs& a,
                    const Units& un, int B, WsHeader* hdr, cudaStream_t st) {
     static std::atomic<int> optin[kMaxDevices], optin_sums[kMaxDevices];
     cudaError_t e = ensure_smem_optin(scan_tc_kernel<kT>, (int)Smem<kT>::kBytes, optin);
@@ -949,7 +975,7 @@ cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorM
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         if ((e = launch_seeds(a, (int64_t)B * a.H, st)) != cudaSuccess) return e;
     }
-    scan_tc_kernel<kT><<<grid, kThreads, Smem<kT>::kBytes, st>>>(xm, bm, cm, a, un, hdr);
+    scan_tc_kernel<kT><<<grid, kThreads, Smem<kT>::kBytes, st>>>(xm, bm, cm, zm, ym, a, un, hdr);
     return cudaPeekAtLastError();
 }
 
@@ -979,15 +1005,19 @@ cudaError_t tc_scan(ScanArgs& a, int B, void* ws_header, cudaStream_t st) {
     Units un = units_of(a.H, a.G, a.P);
     const int nch = (a.N + kC - 1) / kC;
     un.cps = (nch + a.nseg - 1) / a.nseg;
-    un.gate_vec = (reinterpret_cast<uintptr_t>(a.z) & 15) == 0 && (a.N == 1 || a.z_ts % 8 == 0) &&
-                  (B == 1 || a.z_bs % 8 == 0);
-    CUtensorMap xm, bm, cm;
+    un.gate_vec = a.z && (reinterpret_cast<uintptr_t>(a.z) & 15) == 0 &&
+                  (a.N == 1 || (a.z_ts > 0 && a.z_ts % 8 == 0)) && (B == 1 || (a.z_bs > 0 && a.z_bs % 8 == 0)) &&
+                  a.z_ts < (int64_t)1 << 38 && a.z_bs < (int64_t)1 << 38;
+    CUtensorMap xm, bm, cm, zm, ym;
     if (!encode_rows(&xm, a.x, a.P, a.H, a.N, B, a.x_ts, a.x_bs) ||
         !encode_rows(&bm, a.Bm, a.S, a.G, a.N, B, a.b_ts, a.b_bs) ||
-        !encode_rows(&cm, a.Cm, a.S, a.G, a.N, B, a.c_ts, a.c_bs))
+        !encode_rows(&cm, a.Cm, a.S, a.G, a.N, B, a.c_ts, a.c_bs) ||
+        !encode_rows(&ym, a.y, a.P, a.H, a.N, B, a.y_ts, a.y_bs))
         return cudaErrorInvalidValue;
+    zm = xm;                                               // unused without an aligned gate
+    if (un.gate_vec && !encode_rows(&zm, a.z, a.P, a.H, a.N, B, a.z_ts, a.z_bs)) return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
-    return a.S <= 64 ? launch<1>(xm, bm, cm, a, un, B, hdr, st) : launch<2>(xm, bm, cm, a, un, B, hdr, st);
+    return a.S <= 64 ? launch<1>(xm, bm, cm, zm, ym, a, un, B, hdr, st) : launch<2>(xm, bm, cm, zm, ym, a, un, B, hdr, st);
 }
 
 }  // namespace scan
