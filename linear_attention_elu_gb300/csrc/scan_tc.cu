@@ -215,26 +215,15 @@ __device__ __forceinline__ void decays(const ScanArgs& a, const Place& pl, int c
     suf[0] = suf[1] + l[1];
 }
 
-// Pieces j0 .. j1 - 1 (8 values each) of row `row` of the weighted values:
-// hi = bf16(w x), lo = bf16(w x - hi).
-__device__ __forceinline__ void weigh_row(const uint8_t* x, uint8_t* hi, uint8_t* lo, int row, float w, int j0,
-                                          int j1) {
+// Sixteen weighted values: hi = bf16(w x), lo = bf16(w x - hi).
+__device__ __forceinline__ void weigh16(uint4 a, uint4 b, float w, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
     const uint64_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
-    const uint32_t base = row * 128;
-#pragma unroll 4
-    for (int j = j0; j < j1; ++j) {
-        const uint32_t off = base + ((j ^ (row & 7)) << 4);
-        const uint4 v = *reinterpret_cast<const uint4*>(x + off);
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t h[4], l[4];
+    const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint64_t p = mul2(bf2(in[k]), w2);
-            h[k] = pack2(p);
-            l[k] = pack2(fma2(bf2(h[k]), minus, p));
-        }
-        *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    for (int k = 0; k < 8; ++k) {
+        const uint64_t p = mul2(bf2(in[k]), w2);
+        hi[k] = pack2(p);
+        lo[k] = pack2(fma2(bf2(hi[k]), minus, p));
     }
 }
 
@@ -276,6 +265,28 @@ __device__ __forceinline__ uint4 load_gate(const __nv_bfloat16* p) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = (uint32_t)__ldg(h + 2 * k) | ((uint32_t)__ldg(h + 2 * k + 1) << 16);
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Columns c .. c + 15 of unit u's output row t, to global memory (ragged ends).
+__device__ __noinline__ void put_row(const ScanArgs& a, const Place& pl, const Units& un, int u, int t, int c,
+                                     uint4 o0, uint4 o1) {
+    c += pl.col0(un, u);
+    if (t >= pl.n || c >= a.P) return;
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + pl.b * a.y_bs + (int64_t)t * a.y_ts +
+                       (int64_t)pl.head(a, un, u) * a.P + c;
+    *reinterpret_cast<uint4*>(y) = o0;
+    if (c + 8 < a.P) *reinterpret_cast<uint4*>(y + 8) = o1;
+}
+
+// The same columns of a gate row that the TMA cannot fetch, to its two pieces of the slot.
+__device__ __noinline__ void put_gate(const ScanArgs& a, const Place& pl, const Units& un, int u, int t, int c,
+                                      uint8_t* slot, uint32_t pc0, uint32_t pc1) {
+    c += pl.col0(un, u);
+    const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(a.z) + pl.b * a.z_bs + (int64_t)t * a.z_ts +
+                             (int64_t)pl.head(a, un, u) * a.P + c;
+    const bool in = t < pl.n;
+    *reinterpret_cast<uint4*>(slot + pc0) = in && c < a.P ? load_gate(z) : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(slot + pc1) = in && c + 8 < a.P ? load_gate(z + 8) : make_uint4(0, 0, 0, 0);
 }
 
 // z / (1 + e^-z) of two packed bf16 values. e^-z overflows to infinity and its
@@ -549,19 +560,19 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                 if ((pass == 0) == (u != 0)) {
                     // ------------------------------------------------ scores to P
                     if (n == items || g > q) continue;
-                    const uint32_t dst = tmem + lanes + kTmP + 64 * (n & 1) + 16 * g;
-                    const float ci = dc.cum[row];
-                    if (g < q) col[lane] = ex2(dc.cum[32 * q - 1] - dc.cum[32 * g + lane]) * dc.d[32 * g + lane];
-                    __syncwarp();
-                    if (!(ok = warp_wait(&m.sc_full, i & 1, max_spin))) break;
+                    if (u == 0 && !(ok = warp_wait(&m.sc_full, i & 1, max_spin))) break;
                     tc_fence_after();
                     uint32_t s[2][16], p[16];
                     tmem_ld16(tmem + lanes + kTmSc + 32 * g, s[0]);
                     tmem_ld16(tmem + lanes + kTmSc + 32 * g + 16, s[1]);
-                    tmem_ld_wait();
+                    const float ci = dc.cum[row];
                     if (g < q) {
-                        const float ri = ex2(ci - dc.cum[32 * q - 1]);
+                        const float cm = dc.cum[32 * q - 1];
+                        col[lane] = ex2(cm - dc.cum[32 * g + lane]) * dc.d[32 * g + lane];
+                        __syncwarp();
+                        const float ri = ex2(ci - cm);
                         const uint64_t r2 = pk2(ri, ri);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(col + 2 * e);
@@ -573,6 +584,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                         // The diagonal block: an exponential per score; pairs past the row's own
                         // token are cleared as bits (their products may be anything).
                         const uint64_t c2 = pk2(ci, ci), minus = pk2(-1.f, -1.f);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dc.cum + 32 * q + 2 * e);
@@ -589,42 +601,43 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                             }
                         }
                     }
-                    tmem_st16(dst, p);
-                    tmem_st_wait();
+                    tmem_st16(tmem + lanes + kTmP + 64 * (n & 1) + 16 * g, p);
                     continue;
                 }
                 // ---------------------------------------------------- state: bf16 for (2), scaled for (4)
                 if (n < items) {
-                    if (n > 0 && !(ok = warp_wait(&m.read_done, (n - 1) & 1, max_spin))) break;
-                    if (nu == 1 && n > 0 && !(ok = warp_wait(&m.state_done, (n - 1) & 1, max_spin))) break;
+                    if (n > 0 && !(ok = warp_wait(&m.read_done, (n - 1) & 1, max_spin) &&
+                                        (nu == 2 || warp_wait(&m.state_done, (n - 1) & 1, max_spin))))
+                        break;
                     if (has_state) {
                         tc_fence_after();
                         const uint32_t st = tmem + lanes + kTmSt + 64 * u + 16 * g;
-                        const float f = dc.total;
-                        const uint64_t f2 = pk2(f, f);
                         uint32_t v[16], h[8];
                         tmem_ld16(st, v);
+                        const float f = dc.total;
+                        const uint64_t f2 = pk2(f, f);
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const uint64_t x = pk2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-                            h[e] = row < a.S ? pack2(x) : 0u;   // padding rows never reach the read
+                            h[e] = pack2(x);
                             float lo, hi;
                             unpk2(mul2(x, f2), &lo, &hi);
                             v[2 * e] = __float_as_uint(lo);
                             v[2 * e + 1] = __float_as_uint(hi);
                         }
+                        tmem_st16(st, v);
+                        if (row >= a.S)                    // padding rows never reach the read
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) h[e] = 0u;
                         *reinterpret_cast<uint4*>(sb + pc0) = make_uint4(h[0], h[1], h[2], h[3]);
                         *reinterpret_cast<uint4*>(sb + pc1) = make_uint4(h[4], h[5], h[6], h[7]);
-                        tmem_st16(st, v);
-                        tmem_st_wait();
                     }
                 }
                 // ---------------------------------------------------- output of the item before
                 if (n > 0) {
                     const int pn = n - 1, pu = u == 0 ? nu - 1 : u - 1, pi = u == 0 ? i - 1 : i;
-                    const int ps = pn % kDtRing;
-                    const float Dh = pu ? Du[1] : Du[0], e = ex2(dts[ps].cum[row]);
+                    const float Dh = pu ? Du[1] : Du[0], e = ex2(dts[pn % kDtRing].cum[row]);
                     const uint64_t D2 = pk2(Dh, Dh), e2 = pk2(e, e);
                     const uint4 xv[2] = {*reinterpret_cast<const uint4*>(xtile(pn) + pc0),
                                          *reinterpret_cast<const uint4*>(xtile(pn) + pc1)};
@@ -632,54 +645,42 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                                warp_wait(&m.y_full, pn & 1, max_spin)))
                         break;
                     tc_fence_after();
+                    if (lane == 0) mbar_arrive(&m.x_empty[pn & 1]);   // (3) and this warp are done with x
                     uint32_t y1[16], y2[16];
                     tmem_ld16(tmem + lanes + kTmY1 + 16 * g, y1);
                     tmem_ld16(tmem + lanes + kTmY2 + 16 * g, y2);
-                    tmem_ld_wait();
-                    const int t = (pl.c0 + pi) * kC + row, h = pl.head(a, un, pu), c0 = pl.col0(un, pu) + 16 * g;
-                    const bool rows = by_rows(pi);
+                    uint64_t gt[8];
+                    if (gated) {
+                        if (!tma_gate) put_gate(a, pl, un, pu, (pl.c0 + pi) * kC + row, 16 * g, oslot(pn), pc0, pc1);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint4* at = reinterpret_cast<uint4*>(oslot(pn) + (j ? pc1 : pc0));
-                        const uint32_t xs[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
-                        const bool live = t < pl.n && c0 + 8 * j < a.P;
-                        uint4 z = make_uint4(0, 0, 0, 0);
-                        if (gated) {
-                            if (tma_gate) z = *at;
-                            else if (live)
-                                z = load_gate(static_cast<const __nv_bfloat16*>(a.z) + pl.b * a.z_bs + (int64_t)t * a.z_ts +
-                                              (int64_t)h * a.P + c0 + 8 * j);
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 z = *reinterpret_cast<const uint4*>(oslot(pn) + (j ? pc1 : pc0));
+                            gt[4 * j] = gate2(z.x), gt[4 * j + 1] = gate2(z.y);
+                            gt[4 * j + 2] = gate2(z.z), gt[4 * j + 3] = gate2(z.w);
                         }
-                        const uint32_t zs[4] = {z.x, z.y, z.z, z.w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int f = 8 * j + 2 * k;
-                            uint64_t v = fma2(e2, pk2(__uint_as_float(y2[f]), __uint_as_float(y2[f + 1])),
-                                              pk2(__uint_as_float(y1[f]), __uint_as_float(y1[f + 1])));
-                            v = fma2(D2, bf2(xs[k]), v);
-                            if (gated) v = mul2(v, gate2(zs[k]));
-                            o[k] = pack2(v);
-                        }
-                        if (!rows)
-                            *at = make_uint4(o[0], o[1], o[2], o[3]);
-                        else if (live)
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + pl.b * a.y_bs + (int64_t)t * a.y_ts +
-                                                      (int64_t)h * a.P + c0 + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                    fence_proxy_async_smem();              // the store reads the slot
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&m.y_staged[pn & 1]);
-                        mbar_arrive(&m.x_empty[pn & 1]);
-                        mbar_arrive(&m.dt_empty[ps]);
+                    tmem_ld_wait();
+                    uint32_t o[8];
+#pragma unroll
+                    for (int f = 0; f < 8; ++f) {
+                        const uint4 x = xv[f >> 2];
+                        const uint32_t xs = (f & 3) == 0 ? x.x : (f & 3) == 1 ? x.y : (f & 3) == 2 ? x.z : x.w;
+                        uint64_t v = fma2(e2, pk2(__uint_as_float(y2[2 * f]), __uint_as_float(y2[2 * f + 1])),
+                                          pk2(__uint_as_float(y1[2 * f]), __uint_as_float(y1[2 * f + 1])));
+                        v = fma2(D2, bf2(xs), v);
+                        o[f] = pack2(gated ? mul2(v, gt[f]) : v);
+                    }
+                    const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
+                    if (!by_rows(pi)) {
+                        *reinterpret_cast<uint4*>(oslot(pn) + pc0) = o0;
+                        *reinterpret_cast<uint4*>(oslot(pn) + pc1) = o1;
+                    } else {
+                        put_row(a, pl, un, pu, (pl.c0 + pi) * kC + row, 16 * g, o0, o1);
                     }
                 }
                 // ---------------------------------------------------- weighted values
                 if (n < items) {
-                    if (!(ok = warp_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin) &&
-                               (n < 1 || warp_wait(&m.state_done, (n - 1) & 1, max_spin))))
-                        break;
+                    if (!(ok = warp_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin))) break;
                     // Rows at or past a ragged end may hold anything: they are cleared in x, and in
                     // B for (4). (1) may read such rows of B, whose scores no kept row uses.
                     if (a.lengths && (pl.c0 + i + 1) * kC > pl.n) {       // uniform over the block
@@ -693,17 +694,31 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                             }
                         }
                     }
-                    weigh_row(xtile(n), base + L::kXw, base + L::kXw + kTile, row, dc.w[row], 2 * g, 2 * g + 2);
+                    uint32_t wh[8], wl[8];
+                    weigh16(*reinterpret_cast<const uint4*>(xtile(n) + pc0), *reinterpret_cast<const uint4*>(xtile(n) + pc1),
+                            dc.w[row], wh, wl);
+                    if (n > 0 && !(ok = warp_wait(&m.state_done, (n - 1) & 1, max_spin))) break;
+                    uint8_t* hi = base + L::kXw;
+                    *reinterpret_cast<uint4*>(hi + pc0) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                    *reinterpret_cast<uint4*>(hi + pc1) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
+                    *reinterpret_cast<uint4*>(hi + kTile + pc0) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+                    *reinterpret_cast<uint4*>(hi + kTile + pc1) = make_uint4(wl[4], wl[5], wl[6], wl[7]);
                 }
             }
             if (!ok) break;
-            if (n < items) {
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&m.item_ready);
-                if (++u == nu) u = 0, ++i;
+            // What this warp stored is ready for the tensor cores and the TMA.
+            tmem_st_wait();
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (n < items) mbar_arrive(&m.item_ready);
+                if (n > 0) {
+                    mbar_arrive(&m.y_staged[(n - 1) & 1]);
+                    mbar_arrive(&m.dt_empty[(n - 1) % kDtRing]);
+                }
             }
+            if (n < items && ++u == nu) u = 0, ++i;
         }
         // The final state.
         if (ok && last_seg && a.S_out && has_state) {
@@ -810,7 +825,12 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
 #pragma unroll
                 for (int k = 0; k < kT; ++k)
                     tma_load_4d(btile(s) + k * kTile, &bmap, &m.b_full[s], 64 * k, pl.g, t, pl.b);
+                if (i + 2 < pl.nc)                         // to L2 ahead of its load
+#pragma unroll
+                    for (int k = 0; k < kT; ++k) tma_prefetch_4d(&bmap, 64 * k, pl.g, t - 2 * kC, pl.b);
                 for (int u = 0; u < nu; ++u, ++n) {
+                    if (i + 3 < pl.nc)
+                        tma_prefetch_4d(&xmap, pl.col0(un, u), pl.head(a, un, u), t - 3 * kC, pl.b);
                     if (n >= 4 && !(ok = mbar_wait(&m.x_empty[n & 3], ((n >> 2) - 1) & 1, max_spin))) break;
                     mbar_arrive_expect_tx(&m.x_full[n & 3], kTile);
                     tma_load_4d(xtile(n), &xmap, &m.x_full[n & 3], pl.col0(un, u), pl.head(a, un, u), t, pl.b);
@@ -881,7 +901,17 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
                     for (int k = 0; k < kT && u == 0; ++k) zero_row(btile(i & 1) + k * kTile, row);
                 }
             }
-            weigh_row(xtile(n), xwtile(n), xwtile(n) + kTile, row, wts[slot * kC + row], 4 * half, 4 * half + 4);
+#pragma unroll
+            for (int j = 4 * half; j < 4 * half + 4; j += 2) {
+                const uint32_t o0 = row * 128 + ((j ^ (row & 7)) << 4), o1 = row * 128 + (((j + 1) ^ (row & 7)) << 4);
+                uint32_t h[8], l[8];
+                weigh16(*reinterpret_cast<const uint4*>(xtile(n) + o0), *reinterpret_cast<const uint4*>(xtile(n) + o1),
+                        wts[slot * kC + row], h, l);
+                *reinterpret_cast<uint4*>(xwtile(n) + o0) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(xwtile(n) + o1) = make_uint4(h[4], h[5], h[6], h[7]);
+                *reinterpret_cast<uint4*>(xwtile(n) + kTile + o0) = make_uint4(l[0], l[1], l[2], l[3]);
+                *reinterpret_cast<uint4*>(xwtile(n) + kTile + o1) = make_uint4(l[4], l[5], l[6], l[7]);
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
