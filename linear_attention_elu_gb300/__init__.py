@@ -477,33 +477,54 @@ def la_layer_decode_step(x, Wqkv, Wo, S, z, H, y=None, eps=1e-6, ws=None, stream
     return y
 
 
-def _scope(dev, stream):
-    """Context in which a call on tensors of `dev` allocates and launches: that device, and the
-    given stream (so that what the call allocates belongs to the stream that uses it)."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+_NO_SCOPE = contextlib.nullcontext()
+# The stream handle alone: the Stream object that torch.cuda.current_stream() builds
+# costs a call more than the rest of its argument handling.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same_cuda(dev, *ts):
+def _device_of(t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return index
+
+
+def _same_device(index, *ts):
     for t in ts:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors must be on one CUDA device")
 
 
-def _token_rows(t, what, heads):
-    """(batch stride, token stride) of a [B, N, heads, D] tensor whose heads are D apart and whose
-    D values are adjacent (a column range of a projection, for instance)."""
-    B, N, H, D = t.shape
-    sb, sn, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{what}: the {heads} of a token must be adjacent [.., H, D] values "
-                         f"(strides {t.stride()})")
-    return sb, sn
+def _scope(index, stream):
+    """Context in which a call on tensors of device `index` allocates and launches: that device,
+    and the given stream (so that what the call allocates belongs to the stream that uses it)."""
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        return torch.cuda.stream(stream)
+    return _NO_SCOPE if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _inner_adjacent(t, what, inner):
+    """Strides of t, whose last `inner` dimensions must be adjacent values (a column range of a
+    projection's rows, for instance)."""
+    strides = t.stride()
+    if not t.is_contiguous():
+        want = 1
+        for size, stride in zip(reversed(t.shape[-inner:]), reversed(strides[-inner:])):
+            if size > 1 and stride != want:
+                raise ValueError(f"{what}: a token's values must be adjacent (strides {strides})")
+            want *= size
+    return strides
 
 
 def la_rope_table(inv_freq, axis=None, device="cuda"):
@@ -520,44 +541,51 @@ def la_rope_table(inv_freq, axis=None, device="cuda"):
         if ax.shape != f.shape:
             raise ValueError("axis must have one entry per pair")
     table = torch.empty(f.numel(), 2, dtype=torch.int64)
-    _check(_lib.la_rope_table(_ptr(f), _ptr(ax), f.numel(), LA_ROPE_MAX_AXES, _ptr(table)),
+    _check(_lib.la_rope_table(_addr(f), _addr(ax), f.numel(), LA_ROPE_MAX_AXES, _addr(table)),
            "la_rope_table")
     return table.to(device)
 
 
 def _rope_args(q, k, pos, table, wq, wk, norm):
-    """Checks shared by both directions; returns (B, N, Hq, Hk, D, axes)."""
+    """Checks shared by both directions; returns (device index, B, N, Hq, Hk, D, axes)."""
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    for t in (q, k):
-        if t is not None and (t.dim() != 4 or t.shape[:2] != ref.shape[:2] or t.shape[3] != ref.shape[3]):
+    shape, dtype = ref.shape, ref.dtype
+    if len(shape) != 4:
+        raise ValueError("expected q [B,N,Hq,D] and k [B,N,Hk,D]")
+    B, N, Hq, D = shape
+    Hk = Hq
+    if q is None:
+        Hq = 0
+    elif k is None:
+        Hk = 0
+    else:
+        if k.dim() != 4 or k.shape[0] != B or k.shape[1] != N or k.shape[3] != D:
             raise ValueError("expected q [B,N,Hq,D] and k [B,N,Hk,D]")
-        if t is not None and t.dtype != ref.dtype:
+        if k.dtype != dtype:
             raise TypeError("q and k must share one dtype")
-    _dt(ref)
-    if not ref.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    B, N, _, D = ref.shape
+        Hk = k.shape[2]
+    index = _device_of(ref)
     for w in (wq, wk):
         if w is None:
             continue
         if not norm:
             raise ValueError("norm weights need norm=True")
-        if tuple(w.shape) != (D,) or w.dtype != ref.dtype or not w.is_contiguous():
+        if w.dtype != dtype or w.dim() != 1 or w.shape[0] != D or not w.is_contiguous():
             raise ValueError("norm weights must be contiguous [D] in q's dtype")
-    if pos.dtype != torch.int32 or not pos.is_contiguous() or tuple(pos.shape[:2]) != (B, N) \
-            or pos.dim() not in (2, 3):
+    pshape = pos.shape
+    if pos.dtype != torch.int32 or not pos.is_contiguous() or len(pshape) not in (2, 3) or pshape[0] != B \
+            or pshape[1] != N:
         raise ValueError("pos must be contiguous int32 [B,N] or [B,N,axes]")
-    axes = pos.shape[2] if pos.dim() == 3 else 1
     if table.dtype != torch.int64 or table.dim() != 2 or table.shape[1] != 2 or not table.is_contiguous():
         raise ValueError("table must come from la_rope_table (int64 [pairs, 2])")
-    _same_cuda(ref.device, q, k, pos, table, wq, wk)
-    return B, N, q.shape[2] if q is not None else 0, k.shape[2] if k is not None else 0, D, axes
+    _same_device(index, k, pos, table, wq, wk)
+    return index, B, N, Hq, Hk, D, pshape[2] if len(pshape) == 3 else 1
 
 
 def _head_major(t, B, H, N, D, like, what):
-    if tuple(t.shape) != (B, H, N, D) or t.dtype != like.dtype or not t.is_contiguous():
+    if t.shape != (B, H, N, D) or t.dtype != like.dtype or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous [B,H,N,D] = {(B, H, N, D)} in q's dtype")
 
 
@@ -568,25 +596,26 @@ def la_qk_norm_rope_fwd(q, k, pos, table, wq=None, wk=None, norm=True, eps=1e-6,
     q and k may be column ranges of one projection; either may be None. pos: int32 [B,N] or
     [B,N,axes]; table: la_rope_table. Returns (qo [B,Hq,N,D], ko [B,Hk,N,D]), head-major, ready
     for the attention entries."""
-    B, N, Hq, Hk, D, axes = _rope_args(q, k, pos, table, wq, wk, norm)
+    index, B, N, Hq, Hk, D, axes = _rope_args(q, k, pos, table, wq, wk, norm)
     ref = q if q is not None else k
-    qs = _token_rows(q, "q", "heads") if q is not None else (0, 0)
-    ks = _token_rows(k, "k", "heads") if k is not None else (0, 0)
-    with _scope(ref.device, stream):
-        if qo is None and q is not None:
-            qo = torch.empty((B, Hq, N, D), dtype=ref.dtype, device=ref.device)
-        if ko is None and k is not None:
-            ko = torch.empty((B, Hk, N, D), dtype=ref.dtype, device=ref.device)
-        for t, H, what in ((qo, Hq, "qo"), (ko, Hk, "ko")):
-            if t is not None:
-                _head_major(t, B, H, N, D, ref, what)
-        _same_cuda(ref.device, qo, ko)
-        _check(_lib.la_qk_norm_rope_fwd(_ptr(q), qs[0], qs[1], _ptr(k), ks[0], ks[1], _ptr(wq),
-                                        _ptr(wk), _ptr(pos), axes, _ptr(table), table.shape[0],
-                                        _ptr(qo), _ptr(ko), B, N, Hq, Hk, D, _dt(ref),
-                                        1 if norm else 0, float(eps), 1 if interleaved else 0,
-                                        _stream(stream)),
-               "la_qk_norm_rope_fwd")
+    qs = _inner_adjacent(q, "q", 2) if q is not None else (0, 0)
+    ks = _inner_adjacent(k, "k", 2) if k is not None else (0, 0)
+    with _scope(index, stream):
+        if q is not None:
+            if qo is None:
+                qo = torch.empty((B, Hq, N, D), dtype=ref.dtype, device=ref.device)
+            else:
+                _head_major(qo, B, Hq, N, D, ref, "qo")
+        if k is not None:
+            if ko is None:
+                ko = torch.empty((B, Hk, N, D), dtype=ref.dtype, device=ref.device)
+            else:
+                _head_major(ko, B, Hk, N, D, ref, "ko")
+        _same_device(index, qo, ko)
+        _check(_lib.la_qk_norm_rope_fwd(
+            _addr(q), qs[0], qs[1], _addr(k), ks[0], ks[1], _addr(wq), _addr(wk), pos.data_ptr(), axes,
+            table.data_ptr(), table.shape[0], _addr(qo), _addr(ko), B, N, Hq, Hk, D, _dt(ref),
+            1 if norm else 0, eps, 1 if interleaved else 0, _raw_stream(index)), "la_qk_norm_rope_fwd")
     return qo, ko
 
 
@@ -601,7 +630,7 @@ def la_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hk, D):
 def qk_norm_rope_workspace(B, N, Hq, Hk, D, device=None):
     """Allocates (through PyTorch) the workspace of la_qk_norm_rope_bwd; it needs no initialisation."""
     n = la_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hk, D)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(max(n, 256), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, wq=None, wk=None, norm=True, eps=1e-6,
@@ -610,65 +639,66 @@ def la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, wq=None, wk=None, norm=True,
 
     dq [B,N,Hq,D] and dk [B,N,Hk,D] may be given as column ranges of one projection gradient.
     dwq, dwk are float32 [D], None without the norm (or without weights of that side)."""
-    B, N, Hq, Hk, D, axes = _rope_args(q, k, pos, table, wq, wk, norm)
+    index, B, N, Hq, Hk, D, axes = _rope_args(q, k, pos, table, wq, wk, norm)
     ref = q if q is not None else k
-    qs = _token_rows(q, "q", "heads") if q is not None else (0, 0)
-    ks = _token_rows(k, "k", "heads") if k is not None else (0, 0)
+    qs = _inner_adjacent(q, "q", 2) if q is not None else (0, 0)
+    ks = _inner_adjacent(k, "k", 2) if k is not None else (0, 0)
     for t, x, H, what in ((dqo, q, Hq, "dqo"), (dko, k, Hk, "dko")):
         if (t is None) != (x is None):
             raise ValueError(f"{what} must be given exactly when its input is")
         if t is not None:
             _head_major(t, B, H, N, D, ref, what)
-    with _scope(ref.device, stream):
-        dq = torch.empty((B, N, Hq, D), dtype=ref.dtype, device=ref.device) if dq is None and q is not None else dq
-        dk = torch.empty((B, N, Hk, D), dtype=ref.dtype, device=ref.device) if dk is None and k is not None else dk
+    with _scope(index, stream):
+        if dq is None and q is not None:
+            dq = torch.empty((B, N, Hq, D), dtype=ref.dtype, device=ref.device)
+        if dk is None and k is not None:
+            dk = torch.empty((B, N, Hk, D), dtype=ref.dtype, device=ref.device)
         for t, x, what in ((dq, q, "dq"), (dk, k, "dk")):
             if t is not None and (x is None or t.shape != x.shape or t.dtype != ref.dtype):
                 raise ValueError(f"{what} must be shaped and typed like its input")
-        dqs = _token_rows(dq, "dq", "heads") if dq is not None else (0, 0)
-        dks = _token_rows(dk, "dk", "heads") if dk is not None else (0, 0)
+        dqs = _inner_adjacent(dq, "dq", 2) if dq is not None else (0, 0)
+        dks = _inner_adjacent(dk, "dk", 2) if dk is not None else (0, 0)
         dwq = torch.empty(D, dtype=torch.float32, device=ref.device) if wq is not None else None
         dwk = torch.empty(D, dtype=torch.float32, device=ref.device) if wk is not None else None
         if ws is None and norm:
             ws = qk_norm_rope_workspace(B, N, Hq, Hk, D, ref.device)
-        _same_cuda(ref.device, dqo, dko, dq, dk, ws)
-        _check(_lib.la_qk_norm_rope_bwd(_ptr(q), qs[0], qs[1], _ptr(k), ks[0], ks[1], _ptr(wq),
-                                        _ptr(wk), _ptr(pos), axes, _ptr(table), table.shape[0],
-                                        _ptr(dqo), _ptr(dko), _ptr(dq), dqs[0], dqs[1], _ptr(dk),
-                                        dks[0], dks[1], _ptr(dwq), _ptr(dwk), B, N, Hq, Hk, D,
-                                        _dt(ref), 1 if norm else 0, float(eps),
-                                        1 if interleaved else 0, _ptr(ws),
-                                        ws.numel() * ws.element_size() if ws is not None else 0,
-                                        _stream(stream)),
-               "la_qk_norm_rope_bwd")
+        _same_device(index, dqo, dko, dq, dk, ws)
+        _check(_lib.la_qk_norm_rope_bwd(
+            _addr(q), qs[0], qs[1], _addr(k), ks[0], ks[1], _addr(wq), _addr(wk), pos.data_ptr(), axes,
+            table.data_ptr(), table.shape[0], _addr(dqo), _addr(dko), _addr(dq), dqs[0], dqs[1], _addr(dk),
+            dks[0], dks[1], _addr(dwq), _addr(dwk), B, N, Hq, Hk, D, _dt(ref), 1 if norm else 0, eps,
+            1 if interleaved else 0, _addr(ws), _bytes(ws), _raw_stream(index)), "la_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
 def _conv_args(x, w, bias, dims):
-    if x.dim() != dims or w.dim() != 2 or w.shape[0] != x.shape[-1] or (x.stride(-1) != 1 and x.shape[-1] > 1):
-        raise ValueError("expected x [B,N,C] (one token: [B,C]) with adjacent channels and w [C,W]")
+    """Checks shared by the prompt and the step; returns (device index, x's strides, C, W)."""
+    wshape, dtype = w.shape, x.dtype
+    if x.dim() != dims or len(wshape) != 2 or wshape[0] != x.shape[-1]:
+        raise ValueError("expected x [B,N,C] (one token: [B,C]) and w [C,W]")
     _dt(x)
-    if not x.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    C, W = w.shape
-    for t, shape, what in ((w, (C, W), "w"), (bias, (C,), "bias")):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != x.dtype or not t.is_contiguous()):
-            raise ValueError(f"{what} must be contiguous {shape} in x's dtype")
-    return C, W
+    index = _device_of(x)
+    if w.dtype != dtype or not w.is_contiguous():
+        raise ValueError("w must be contiguous [C,W] in x's dtype")
+    if bias is not None and (bias.dtype != dtype or bias.dim() != 1 or bias.shape[0] != wshape[0]
+                             or not bias.is_contiguous()):
+        raise ValueError("bias must be contiguous [C] in x's dtype")
+    return index, _inner_adjacent(x, "x", 1), wshape[0], wshape[1]
 
 
 def _conv_state(t, B, C, W, x, what):
-    if t is not None and (tuple(t.shape) != (B, W - 1, C) or t.dtype != x.dtype or not t.is_contiguous()):
+    if t is not None and (t.shape != (B, W - 1, C) or t.dtype != x.dtype or not t.is_contiguous()):
         raise ValueError(f"{what} must be contiguous [B,W-1,C] = {(B, W - 1, C)} in x's dtype")
 
 
-def _out_rows(y, x, what="y"):
-    if y.shape != x.shape or y.dtype != x.dtype or (y.stride(-1) != 1 and y.shape[-1] > 1):
-        raise ValueError(f"{what} must be shaped and typed like x, with adjacent channels")
+def _like(y, x, inner):
+    if y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError("y must be shaped and typed like x")
+    return _inner_adjacent(y, "y", inner)
 
 
 def _check_lengths(lengths, B):
-    if lengths is not None and (lengths.dtype != torch.int32 or tuple(lengths.shape) != (B,)
+    if lengths is not None and (lengths.dtype != torch.int32 or lengths.shape != (B,)
                                 or not lengths.is_contiguous()):
         raise ValueError("lengths must be contiguous int32 [B]")
 
@@ -680,79 +710,70 @@ def la_short_conv_fwd(x, w, bias=None, silu=True, lengths=None, state0=None, sta
     state0 [B,W-1,C]: the inputs before the first token; the last W - 1 inputs go to state_out
     (allocated with return_state=True). lengths (int32 [B]): rows past them are left as they are.
     Returns y, or (y, state_out) with return_state=True."""
-    C, W = _conv_args(x, w, bias, 3)
+    index, xs, C, W = _conv_args(x, w, bias, 3)
     B, N, _ = x.shape
     _conv_state(state0, B, C, W, x, "state0")
     _check_lengths(lengths, B)
-    with _scope(x.device, stream):
+    with _scope(index, stream):
         if y is None:
             y = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
         if state_out is None and return_state:
             state_out = torch.empty((B, W - 1, C), dtype=x.dtype, device=x.device)
-        _out_rows(y, x)
+        ys = _like(y, x, 1)
         _conv_state(state_out, B, C, W, x, "state_out")
-        _same_cuda(x.device, w, bias, lengths, state0, state_out, y)
-        _check(_lib.la_short_conv_fwd(_ptr(x), x.stride(0), x.stride(1), _ptr(w), _ptr(bias),
-                                      1 if silu else 0, _ptr(lengths), _ptr(state0), _ptr(state_out),
-                                      _ptr(y), y.stride(0), y.stride(1), B, N, C, W, _dt(x),
-                                      _stream(stream)),
-               "la_short_conv_fwd")
+        _same_device(index, w, bias, lengths, state0, state_out, y)
+        _check(_lib.la_short_conv_fwd(
+            x.data_ptr(), xs[0], xs[1], w.data_ptr(), _addr(bias), 1 if silu else 0, _addr(lengths),
+            _addr(state0), _addr(state_out), y.data_ptr(), ys[0], ys[1], B, N, C, W, _dt(x),
+            _raw_stream(index)), "la_short_conv_fwd")
     return (y, state_out) if return_state else y
 
 
 def la_short_conv_step(x, w, state, bias=None, silu=True, y=None, stream=None):
     """One token of the convolution: x [B,C] -> y [B,C]; state [B,W-1,C] is shifted in place."""
-    C, W = _conv_args(x, w, bias, 2)
+    index, xs, C, W = _conv_args(x, w, bias, 2)
     B = x.shape[0]
+    if state is None:
+        raise ValueError("state must be given")
     _conv_state(state, B, C, W, x, "state")
-    with _scope(x.device, stream):
+    with _scope(index, stream):
         if y is None:
             y = torch.empty((B, C), dtype=x.dtype, device=x.device)
-        _out_rows(y, x)
-        _same_cuda(x.device, w, bias, state, y)
-        _check(_lib.la_short_conv_step(_ptr(x), x.stride(0), _ptr(w), _ptr(bias), 1 if silu else 0,
-                                       _ptr(state), _ptr(y), y.stride(0), B, C, W, _dt(x),
-                                       _stream(stream)),
-               "la_short_conv_step")
+            ys = (C, 1)
+        else:
+            ys = _like(y, x, 1)
+        _same_device(index, w, bias, state, y)
+        _check(_lib.la_short_conv_step(
+            x.data_ptr(), xs[0], w.data_ptr(), _addr(bias), 1 if silu else 0, state.data_ptr(), y.data_ptr(),
+            ys[0], B, C, W, _dt(x), _raw_stream(index)), "la_short_conv_step")
     return y
 
 
-def _inner_adjacent(t, what, inner):
-    """The last `inner` dimensions of t are adjacent values."""
-    want = 1
-    for size, stride in zip(reversed(t.shape[-inner:]), reversed(t.stride()[-inner:])):
-        if size > 1 and stride != want:
-            raise ValueError(f"{what}: a token's values must be adjacent (strides {t.stride()})")
-        want *= size
-
-
 def _scan_args(x, step, A, Bm, Cm, D, z, step_bias, lead):
-    """Checks shared by the prompt (lead = 2: [B,N,..]) and the step (lead = 1: [B,..])."""
-    dims = "[B,N,H,P]" if lead == 2 else "[B,H,P]"
-    if x.dim() != lead + 2 or Bm.dim() != lead + 2 or Cm.shape != Bm.shape or \
-            Bm.shape[:lead] != x.shape[:lead] or step.shape != x.shape[:-1] or \
-            (z is not None and z.shape != x.shape):
+    """Checks shared by the prompt (lead = 2: [B,N,..]) and the step (lead = 1: [B,..]); returns
+    (device index, shape of x, G, S)."""
+    xshape, bshape, dtype = x.shape, Bm.shape, x.dtype
+    if len(xshape) != lead + 2 or len(bshape) != lead + 2 or Cm.shape != bshape or \
+            bshape[:lead] != xshape[:lead] or step.shape != xshape[:-1] or \
+            (z is not None and z.shape != xshape):
+        dims = "[B,N,H,P]" if lead == 2 else "[B,H,P]"
         raise ValueError(f"expected x (and z) {dims}, step one value per head, Bm and Cm with [G,S] per token")
-    for t in (step, Bm, Cm, z):
-        if t is not None and t.dtype != x.dtype:
-            raise TypeError("x, step, Bm, Cm and z must share one dtype")
+    if step.dtype != dtype or Bm.dtype != dtype or Cm.dtype != dtype or (z is not None and z.dtype != dtype):
+        raise TypeError("x, step, Bm, Cm and z must share one dtype")
     _dt(x)
-    if not x.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    H, P = x.shape[-2:]
-    for t, what in ((A, "A"), (D, "D"), (step_bias, "dt_bias")):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H,) or not t.is_contiguous()):
-            raise ValueError(f"{what} must be contiguous float32 [H]")
+    index = _device_of(x)
     if A is None:
         raise ValueError("A must be given")
-    for t, what, inner in ((x, "x", 2), (step, "step", 1), (Bm, "Bm", 2), (Cm, "Cm", 2), (z, "z", 2)):
-        if t is not None:
-            _inner_adjacent(t, what, inner)
-    return x.shape[0], H, P, Bm.shape[-2], Bm.shape[-1]
+    for t, what in ((A, "A"), (D, "D"), (step_bias, "dt_bias")):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != xshape[-2]
+                              or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous float32 [H]")
+    _same_device(index, step, A, Bm, Cm, D, z, step_bias)
+    return index, xshape, bshape[-2], bshape[-1]
 
 
 def _f32_state(t, shape, what):
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what} must be contiguous float32 with shape {shape}")
 
 
@@ -764,49 +785,47 @@ def la_selective_scan_fwd(x, step, A, Bm, Cm, D=None, z=None, dt_bias=None, soft
     d_t = softplus(step_t + dt_bias). S0, S_out [B,H,S,P] float32 (S_out may be S0). lengths
     (int32 [B]): rows past them are left as they are. Token rows may be strided (column ranges of
     a projection). Returns y [B,N,H,P]."""
-    B, H, P, G, S = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 2)
-    N = x.shape[1]
+    index, (B, N, H, P), G, S = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 2)
     _f32_state(S0, (B, H, S, P), "S0")
     _f32_state(S_out, (B, H, S, P), "S_out")
     _check_lengths(lengths, B)
-    with _scope(x.device, stream):
+    xs, ss = _inner_adjacent(x, "x", 2), _inner_adjacent(step, "step", 1)
+    bs, cs = _inner_adjacent(Bm, "Bm", 2), _inner_adjacent(Cm, "Cm", 2)
+    zs = _inner_adjacent(z, "z", 2) if z is not None else (0, 0)
+    with _scope(index, stream):
         if y is None:
             y = torch.empty((B, N, H, P), dtype=x.dtype, device=x.device)
-        if y.shape != x.shape or y.dtype != x.dtype:
-            raise ValueError("y must be shaped and typed like x")
-        _inner_adjacent(y, "y", 2)
+        ys = _like(y, x, 2)
         if ws is None:
-            ws = workspace(LA_OP_SELECTIVE_SCAN, B, H, N, S, P, x.dtype, x.device, stream)
-        _same_cuda(x.device, step, A, Bm, Cm, D, z, dt_bias, lengths, S0, S_out, y, ws)
-        zs = z.stride() if z is not None else (0, 0)
-        xs, ss, bs, cs, ys = x.stride(), step.stride(), Bm.stride(), Cm.stride(), y.stride()
+            ws = workspace(LA_OP_SELECTIVE_SCAN, B, H, N, S, P, x.dtype, x.device)
+        _same_device(index, lengths, S0, S_out, y, ws)
         _check(_lib.la_selective_scan_fwd(
-            _ptr(x), xs[0], xs[1], _ptr(step), ss[0], ss[1], _ptr(A), _ptr(Bm), bs[0], bs[1], _ptr(Cm),
-            cs[0], cs[1], _ptr(D), _ptr(z), zs[0], zs[1], _ptr(dt_bias), 1 if softplus else 0,
-            _ptr(lengths), _ptr(S0), _ptr(S_out), _ptr(y), ys[0], ys[1], B, H, G, N, S, P, _dt(x),
-            _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "la_selective_scan_fwd")
+            x.data_ptr(), xs[0], xs[1], step.data_ptr(), ss[0], ss[1], A.data_ptr(), Bm.data_ptr(), bs[0],
+            bs[1], Cm.data_ptr(), cs[0], cs[1], _addr(D), _addr(z), zs[0], zs[1], _addr(dt_bias),
+            1 if softplus else 0, _addr(lengths), _addr(S0), _addr(S_out), y.data_ptr(), ys[0], ys[1], B, H,
+            G, N, S, P, _dt(x), ws.data_ptr(), _bytes(ws), _raw_stream(index)), "la_selective_scan_fwd")
     return y
 
 
 def la_selective_scan_step(x, step, A, Bm, Cm, S, D=None, z=None, dt_bias=None, softplus=True,
                            y=None, stream=None):
     """One token of the scan: x [B,H,P], step [B,H], Bm, Cm [B,G,S]; S [B,H,S,P] in place."""
-    B, H, P, G, Sn = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 1)
+    index, (B, H, P), G, Sn = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 1)
     if S is None:
         raise ValueError("S must be given")
     _f32_state(S, (B, H, Sn, P), "S")
-    with _scope(x.device, stream):
+    xs, ss = _inner_adjacent(x, "x", 2), _inner_adjacent(step, "step", 1)
+    bs, cs = _inner_adjacent(Bm, "Bm", 2), _inner_adjacent(Cm, "Cm", 2)
+    zs = _inner_adjacent(z, "z", 2) if z is not None else (0,)
+    with _scope(index, stream):
         if y is None:
             y = torch.empty((B, H, P), dtype=x.dtype, device=x.device)
-        if y.shape != x.shape or y.dtype != x.dtype:
-            raise ValueError("y must be shaped and typed like x")
-        _inner_adjacent(y, "y", 2)
-        _same_cuda(x.device, step, A, Bm, Cm, D, z, dt_bias, S, y)
+        ys = _like(y, x, 2)
+        _same_device(index, S, y)
         _check(_lib.la_selective_scan_step(
-            _ptr(x), x.stride(0), _ptr(step), step.stride(0), _ptr(A), _ptr(Bm), Bm.stride(0), _ptr(Cm),
-            Cm.stride(0), _ptr(D), _ptr(z), z.stride(0) if z is not None else 0, _ptr(dt_bias),
-            1 if softplus else 0, _ptr(S), _ptr(y), y.stride(0), B, H, G, Sn, P, _dt(x),
-            _stream(stream)), "la_selective_scan_step")
+            x.data_ptr(), xs[0], step.data_ptr(), ss[0], A.data_ptr(), Bm.data_ptr(), bs[0], Cm.data_ptr(),
+            cs[0], _addr(D), _addr(z), zs[0], _addr(dt_bias), 1 if softplus else 0, S.data_ptr(),
+            y.data_ptr(), ys[0], B, H, G, Sn, P, _dt(x), _raw_stream(index)), "la_selective_scan_step")
     return y
 
 
