@@ -51,7 +51,7 @@ struct Args {
     float* partial;           // backward with the norm: [blocks][2][D]
     int64_t tokens;           // B N
     int axes, R, N, D, norm, heads_per_block;
-    float eps;
+    float eps, inv_D;
 };
 
 template <typename T> struct Raw8;   // eight consecutive values of a row as stored
@@ -76,12 +76,12 @@ template <> struct Raw8<__nv_bfloat16> {
     // whose halves are swapped when `swap` (R not a multiple of 8).
     __device__ __forceinline__ Raw8 partner(const int (&src)[2], bool swap) const {
         Raw8 r;
-        const uint32_t a = swap ? v.z : v.x, b = swap ? v.w : v.y;
-        const uint32_t c = swap ? v.x : v.z, d = swap ? v.y : v.w;
-        r.v.x = __shfl_sync(0xffffffffu, a, src[0]);
-        r.v.y = __shfl_sync(0xffffffffu, b, src[0]);
-        r.v.z = __shfl_sync(0xffffffffu, c, src[1]);
-        r.v.w = __shfl_sync(0xffffffffu, d, src[1]);
+        uint4 t = v;
+        if (swap) t = make_uint4(v.z, v.w, v.x, v.y);      // uniform over the grid
+        r.v.x = __shfl_sync(0xffffffffu, t.x, src[0]);
+        r.v.y = __shfl_sync(0xffffffffu, t.y, src[0]);
+        r.v.z = __shfl_sync(0xffffffffu, t.z, src[1]);
+        r.v.w = __shfl_sync(0xffffffffu, t.w, src[1]);
         return r;
     }
 };
@@ -191,8 +191,11 @@ __device__ __forceinline__ void partner_values(const Raw8<T>& raw, const float (
 
 // Forward. kLanes: lanes per row (D / 8 rounded up to a power of two; the lanes
 // past D / 8 carry zeros). blockIdx.y: a range of the Hq + Hk heads.
+// Four blocks of 256 threads per SM for bf16 (B=16 N=8192 H=8+8 D=128: 220 us, two
+// blocks 293), two for fp32, whose pieces need twice the registers (16 images of
+// 32 x 32: 28 us, four blocks 32).
 template <typename T, int kLanes, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) rope_fwd_kernel(const __grid_constant__ Args a) {
     constexpr int kRows = kThreads / kLanes, kU = 4;   // heads in flight per group
     const int l = threadIdx.x % kLanes;
     const int64_t t_raw = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const __grid_constan
                     float ss = 0.f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-                    r = rsqrtf(group_sum<kLanes>(ss) / (float)a.D + a.eps);
+                    r = rsqrtf(group_sum<kLanes>(ss) * a.inv_D + a.eps);
                 }
                 float y[8];
 #pragma unroll
@@ -281,7 +284,7 @@ __device__ __forceinline__ void block_dw(float (&v)[8], float (*red)[kMaxDim], i
 // Backward. A block walks token tiles blockIdx.x, + gridDim.x, ..., so that dw
 // leaves as one partial row per block.
 template <typename T, int kLanes, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_bwd_kernel(const __grid_constant__ Args a) {
     constexpr int kRows = kThreads / kLanes, kU = 2;
     const int l = threadIdx.x % kLanes;
     const bool rot = 8 * l < 2 * a.R, swap = (a.R & 4) != 0;
@@ -343,8 +346,8 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constan
                         }
                         ss = group_sum<kLanes>(ss);
                         dot = group_sum<kLanes>(dot);
-                        const float r = rsqrtf(ss / (float)a.D + a.eps);
-                        const float k = r * r * r * (dot / (float)a.D);
+                        const float r = rsqrtf(ss * a.inv_D + a.eps);
+                        const float k = r * r * r * (dot * a.inv_D);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             y[j] = fmaf(r * w[j], g[j], -k * x[j]);
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
                 ss = fmaf(x[j], x[j], ss);
                 v[j] = kBwd ? (in ? to_f(static_cast<const T*>(sd.go)[hm + e]) : 0.f) : x[j];
             }
-            const float r = a.norm ? rsqrtf(group_sum<32>(ss) / (float)a.D + a.eps) : 1.f;
+            const float r = a.norm ? rsqrtf(group_sum<32>(ss) * a.inv_D + a.eps) : 1.f;
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 const int e = lane + 32 * j;
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
                 float dot = 0.f;
 #pragma unroll
                 for (int j = 0; j < kE; ++j) dot = fmaf(v[j] * w[j], x[j], dot);
-                const float k = a.norm ? r * r * r * (group_sum<32>(dot) / (float)a.D) : 0.f;
+                const float k = a.norm ? r * r * r * (group_sum<32>(dot) * a.inv_D) : 0.f;
 #pragma unroll
                 for (int j = 0; j < kE; ++j) {
                     const int e = lane + 32 * j;
@@ -628,7 +631,7 @@ la_status la_qk_norm_rope_fwd(const void* q, int64_t q_batch, int64_t q_token, c
     a.pos = pos;
     a.table = reinterpret_cast<const longlong2*>(table);
     a.tokens = tokens;
-    a.axes = axes, a.R = pairs, a.N = N, a.D = D, a.norm = norm ? 1 : 0, a.eps = eps;
+    a.axes = axes, a.R = pairs, a.N = N, a.D = D, a.norm = norm ? 1 : 0, a.eps = eps, a.inv_D = 1.f / (float)D;
     int blocks = 0;
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = dt == LA_BF16
@@ -689,7 +692,7 @@ la_status la_qk_norm_rope_bwd(const void* q, int64_t q_batch, int64_t q_token, c
     a.table = reinterpret_cast<const longlong2*>(table);
     a.partial = static_cast<float*>(workspace);
     a.tokens = tokens;
-    a.axes = axes, a.R = pairs, a.N = N, a.D = D, a.norm = norm ? 1 : 0, a.eps = eps;
+    a.axes = axes, a.R = pairs, a.N = N, a.D = D, a.norm = norm ? 1 : 0, a.eps = eps, a.inv_D = 1.f / (float)D;
     int blocks = 0;
     cudaError_t e = dt == LA_BF16
                         ? la::run<__nv_bfloat16>(a, true, layout == LA_ROPE_INTERLEAVED, &blocks, st)

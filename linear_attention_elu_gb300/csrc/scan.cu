@@ -9,17 +9,23 @@
 // the single-token step, the scan over segments, and the entry points. bf16
 // with whole 16-byte rows runs on the tensor cores instead (csrc/scan_tc.cu).
 //
-// The recurrence keeps the state in registers: a warp owns 8 columns of one
-// head, its 32 lanes 8 row groups x 4 column pairs, so a lane holds R rows
-// (R = S / 8) of two columns, as packed fp32 row pairs. A token costs three
-// packed operations per row pair (decay, update, read): the FP32 pipe bounds it.
-// Eight tokens' reads are then summed over the row groups by a butterfly that
-// halves the tokens at each step (14 shuffles for 8 tokens x 2 columns). With too
-// few heads for the SMs a sequence is cut into segments: a first pass gives each
-// segment's own end state and total decay, a scan chains them, and the second
-// pass starts each segment from its state.
+// The recurrence keeps the state in registers: a warp owns 4 kW columns of one
+// head, its 32 lanes 8 row groups x 4 column groups, so a lane holds R = S / 8 rows
+// of kW columns, as packed fp32 row pairs. What bounds it is the FP32 pipe, so the
+// decay is taken out of the inner loop: within eight tokens the state is kept
+// divided by the decay since their start (the update's weight is d_t e^{-l_t}, the
+// read is multiplied by e^{l_t}), two operations per element and token instead of
+// three, and multiplied through once at the end. Where eight tokens decay by more
+// than e^-40 the plain form runs instead. The eight tokens' reads are summed over
+// the row groups by a butterfly that halves the tokens at each step. With too few
+// heads for the SMs a sequence is cut into segments: a first pass gives each
+// segment's own end state (one operation per element and token: walked backwards,
+// the weights reach to the segment's end) and total decay, a scan chains them, and
+// the second pass starts each segment from its state.
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -32,7 +38,7 @@ using namespace scan;
 
 namespace {
 
-constexpr int kTok = 16;               // tokens staged per tile
+constexpr int kTok = 32;               // tokens staged per tile
 
 __device__ __forceinline__ uint64_t pk(float lo, float hi) {
     uint64_t r;
@@ -57,27 +63,49 @@ __device__ __forceinline__ float sum2(uint64_t a) {
 
 // Staged floats per token and operand: 8 row groups of R rows, padded so that
 // the groups' vector loads fall into different banks.
-template <int R> constexpr int kGroupStride = R >= 8 ? R + 4 : R;
+template <int R> constexpr int kGroupStride = R == 8 || R == 16 ? R + 4 : R;
 
-// Grid: (segments, B H). Block: one warp per 8 columns of the head.
+// Per-token factors of a tile.
+struct Factors {
+    float w[kTok];       // weight of the update: d e^{-l} (plain form: d; first pass: d e^{sum to the end})
+    float a[kTok];       // e^l, l summed from the start of the token's eight (plain form: e^{d A})
+    float plain[kTok / 8];   // != 0: these eight tokens take the plain form
+};
+
+// 2 kPairs rows of one lane at p, as packed pairs.
+template <int kPairs>
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[kPairs]) {
+    if constexpr (kPairs % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < kPairs; i += 2) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
+            v[i] = t.x, v[i + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) v[i] = *reinterpret_cast<const uint64_t*>(p + 2 * i);
+    }
+}
+
+// Grid: (segments, B H). Block: one warp per 4 kW columns of the head.
 // kState: only the segment's end state from zero and its decay (first pass).
-template <typename T, int R, bool kState>
-__global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int kG = kGroupStride<R>, kRow = 8 * kG;
+template <typename T, int R, int kW, bool kState>
+__global__ void __launch_bounds__(32 * kMaxDim / (4 * kW)) scan_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int kG = kGroupStride<R>, kRow = 8 * kG, kP = R / 2;
+    constexpr int kJ = (8 * R + 31) / 32, kB = R <= 8 ? 8 : 4;
     extern __shared__ float smem[];
+    __shared__ Factors fac;
+    const int cols = blockDim.x / 8 * kW;               // P rounded up to whole warps
     float* bs = smem;                                   // [kTok][kRow]
-    float* cs = bs + kTok * kRow;                       // [kTok][kRow]
-    float* xs = cs + kTok * kRow;                       // [kTok][cols]
-    const int cols = blockDim.x / 4;                    // P rounded up to a multiple of 8
-    float* ds = xs + kTok * cols;                       // [kTok]
-    float* as = ds + kTok;                              // [kTok]
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rg = lane & 7, col = 8 * warp + 2 * (lane >> 3);
+    float* xs = bs + kTok * kRow;                       // [kTok][cols]
+    float* cs = xs + kTok * cols;                       // [kTok][kRow], second pass
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int rg = lane & 7, col = 4 * kW * warp + kW * (lane >> 3);
     const int seg = blockIdx.x, h = blockIdx.y % a.H;
     const int64_t b = blockIdx.y / a.H, bh = blockIdx.y;
     const int grp = h / (a.H / a.G);
     const int n = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
-    const int t0 = seg * a.seg_len, t1 = min(t0 + a.seg_len, n);
+    const int t0 = min(seg * a.seg_len, n), t1 = min(t0 + a.seg_len, n);
     const T* x = static_cast<const T*>(a.x) + b * a.x_bs + (int64_t)h * a.P;
     const T* z = a.z ? static_cast<const T*>(a.z) + b * a.z_bs + (int64_t)h * a.P : nullptr;
     const T* Bm = static_cast<const T*>(a.Bm) + b * a.b_bs + (int64_t)grp * a.S;
@@ -86,14 +114,18 @@ __global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanA
     T* y = static_cast<T*>(a.y) + b * a.y_bs + (int64_t)h * a.P;
     const float A = a.A[h], bias = a.step_bias ? a.step_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
 
-    // The state: rows rg R .. rg R + R - 1 of columns col, col + 1.
-    uint64_t s[2][R / 2];
+    // The second pass is a programmatic dependent of the chaining kernel (the wait is a
+    // no-op in any other launch).
+    tcc::pdl_launch_dependents();
+    tcc::pdl_wait();
+    // The state: rows rg R .. rg R + R - 1 of columns col .. col + kW - 1.
+    uint64_t s[kW][kP];
     const float* from = kState ? nullptr : (a.nseg > 1 ? a.seeds + (bh * a.nseg + seg) * a.S * a.P
                                                        : (a.S0 ? a.S0 + bh * a.S * a.P : nullptr));
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < kW; ++c)
 #pragma unroll
-        for (int i = 0; i < R / 2; ++i) {
+        for (int i = 0; i < kP; ++i) {
             const int r = rg * R + 2 * i;
             float v[2] = {0.f, 0.f};
             if (from && col + c < a.P) {
@@ -102,68 +134,141 @@ __global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanA
             }
             s[c][i] = pk(v[0], v[1]);
         }
-    float decay = 0.f;                                  // sum of d A over the segment (first pass)
+    float behind = 0.f;                                 // first pass: sum of d A over the tiles behind
 
-    for (int tile = t0; tile < t1; tile += kTok) {
-        const int m = min(kTok, t1 - tile);
+    const int tiles = (t1 - t0 + kTok - 1) / kTok;
+    for (int k = 0; k < tiles; ++k) {
+        const int tile = t0 + (kState ? tiles - 1 - k : k) * kTok, m = min(kTok, t1 - tile);
         __syncthreads();
-        for (int i = tid; i < kTok * 8 * R; i += blockDim.x) {
-            const int t = i / (8 * R), r = i % (8 * R);
-            const bool in = t < m && r < a.S;
-            const int at = t * kRow + (r / R) * kG + r % R;
-            bs[at] = in ? to_f(Bm[(int64_t)(tile + t) * a.b_ts + r]) : 0.f;
-            if (!kState) cs[at] = in ? to_f(Cm[(int64_t)(tile + t) * a.c_ts + r]) : 0.f;
+        // A warp stages every nw-th token, a lane 32 columns apart; kB tokens' loads are
+        // all in flight before the first store (one wait on memory per tile and block).
+        for (int tb = warp; tb < kTok; tb += kB * nw) {
+            float vb[kJ][kB], vc[kJ][kB], vx[4][kB];
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                const int t = tb + u * nw;
+                const bool in = t < m;
+                const T* pb = Bm + (int64_t)(tile + t) * a.b_ts;
+                const T* pc = Cm + (int64_t)(tile + t) * a.c_ts;
+                const T* px = x + (int64_t)(tile + t) * a.x_ts;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int r = lane + 32 * j;
+                    vb[j][u] = in && r < a.S ? to_f(pb[r]) : 0.f;
+                    if (!kState) vc[j][u] = in && r < a.S ? to_f(pc[r]) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int p = lane + 32 * j;
+                    vx[j][u] = in && p < a.P ? to_f(px[p]) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                const int t = tb + u * nw;
+                if (t >= kTok) break;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int r = lane + 32 * j;
+                    if (8 * R < 32 * kJ && r >= 8 * R) continue;
+                    const int at = t * kRow + (r / R) * kG + r % R;
+                    bs[at] = vb[j][u];
+                    if (!kState) cs[at] = vc[j][u];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (lane + 32 * j < cols) xs[t * cols + lane + 32 * j] = vx[j][u];
+            }
         }
-        for (int i = tid; i < kTok * cols; i += blockDim.x) {
-            const int t = i / cols, p = i - t * cols;
-            xs[i] = t < m && p < a.P ? to_f(x[(int64_t)(tile + t) * a.x_ts + p]) : 0.f;
-        }
-        if (tid < kTok) {
-            // A token past the end decays by 1 and adds nothing.
-            const float d = tid < m ? step_size(to_f(st[(int64_t)(tile + tid) * a.step_ts]) + bias, a.softplus) : 0.f;
-            ds[tid] = d;
-            as[tid] = expf(d * A);
+        if (warp == 0) {
+            // One token per lane. A token past the end decays by 1 and adds nothing.
+            const float d = lane < m ? step_size(to_f(st[(int64_t)(tile + lane) * a.step_ts]) + bias, a.softplus) : 0.f;
+            float l = d * A;
+            const float own = l;
+            if constexpr (kState) {
+                // Sum over the tokens after this one, up to the segment's end.
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float u = __shfl_down_sync(0xffffffffu, l, o);
+                    if (lane + o < 32) l += u;
+                }
+                const float total = __shfl_sync(0xffffffffu, l, 0);
+                float after = __shfl_down_sync(0xffffffffu, l, 1);
+                if (lane == 31) after = 0.f;
+                fac.w[lane] = d * expf(after + behind);
+                behind += total;
+            } else {
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    const float u = __shfl_up_sync(0xffffffffu, l, o, 8);
+                    if ((lane & 7) >= o) l += u;
+                }
+                const float end = __shfl_sync(0xffffffffu, l, 7, 8);
+                const bool plain = !(fabsf(end) < 40.f);
+                fac.w[lane] = plain ? d : d * expf(-l);
+                fac.a[lane] = expf(plain ? own : l);
+                if ((lane & 7) == 0) fac.plain[lane >> 3] = plain ? 1.f : 0.f;
+            }
         }
         __syncthreads();
-        if (kState && tid == 0)
-            for (int t = 0; t < m; ++t) decay += ds[t] * A;
 #pragma unroll 1
         for (int half = 0; half < kTok && half < m; half += 8) {
-            float acc[8][2];
+            if constexpr (kState) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const int tt = half + t;
-                const float d = ds[tt], at = as[tt];
-                const uint64_t a2 = pk(at, at);
-                const float2 xv = *reinterpret_cast<const float2*>(xs + tt * cols + col);
-                const uint64_t x0 = pk(d * xv.x, d * xv.x), x1 = pk(d * xv.y, d * xv.y);
-                const float* bp = bs + tt * kRow + rg * kG;
-                const float* cp = cs + tt * kRow + rg * kG;
-                uint64_t y0 = 0, y1 = 0;
+                for (int t = 0; t < 8; ++t) {
+                    const int tt = half + t;
+                    const float w = fac.w[tt];
+                    const float* xv = xs + tt * cols + col;
+                    uint64_t bb[kP];
+                    load_pairs<kP>(bs + tt * kRow + rg * kG, bb);
 #pragma unroll
-                for (int i = 0; i < R / 2; ++i) {
-                    uint64_t bb, cc = 0;
-                    if constexpr (R >= 4) {             // two pairs per 16-byte load
-                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(bp + (i & ~1) * 2);
-                        bb = (i & 1) ? v.y : v.x;
-                        if (!kState) {
-                            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cp + (i & ~1) * 2);
-                            cc = (i & 1) ? w.y : w.x;
-                        }
-                    } else {
-                        bb = *reinterpret_cast<const uint64_t*>(bp + 2 * i);
-                        if (!kState) cc = *reinterpret_cast<const uint64_t*>(cp + 2 * i);
-                    }
-                    s[0][i] = fma2(bb, x0, mul2(a2, s[0][i]));
-                    s[1][i] = fma2(bb, x1, mul2(a2, s[1][i]));
-                    if (!kState) {
-                        y0 = fma2(cc, s[0][i], y0);
-                        y1 = fma2(cc, s[1][i], y1);
+                    for (int c = 0; c < kW; ++c) {
+                        const float v = w * xv[c];
+                        const uint64_t x2 = pk(v, v);
+#pragma unroll
+                        for (int i = 0; i < kP; ++i) s[c][i] = fma2(bb[i], x2, s[c][i]);
                     }
                 }
-                if (!kState) acc[t][0] = sum2(y0), acc[t][1] = sum2(y1);
-            }
-            if constexpr (!kState) {
+            } else {
+                const bool plain = fac.plain[half >> 3] != 0.f;
+                float acc[8][kW];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const int tt = half + t;
+                    const float w = fac.w[tt];
+                    const float* xv = xs + tt * cols + col;
+                    if (plain) {
+                        const float at = fac.a[tt];
+                        const uint64_t a2 = pk(at, at);
+#pragma unroll
+                        for (int c = 0; c < kW; ++c)
+#pragma unroll
+                            for (int i = 0; i < kP; ++i) s[c][i] = mul2(a2, s[c][i]);
+                    }
+                    uint64_t bb[kP], cc[kP];
+                    load_pairs<kP>(bs + tt * kRow + rg * kG, bb);
+                    load_pairs<kP>(cs + tt * kRow + rg * kG, cc);
+#pragma unroll
+                    for (int c = 0; c < kW; ++c) {
+                        const float v = w * xv[c];
+                        const uint64_t x2 = pk(v, v);
+                        uint64_t y2 = 0;
+#pragma unroll
+                        for (int i = 0; i < kP; ++i) {
+                            s[c][i] = fma2(bb[i], x2, s[c][i]);
+                            y2 = fma2(cc[i], s[c][i], y2);
+                        }
+                        acc[t][c] = sum2(y2);
+                    }
+                }
+                if (!plain) {
+                    const float at = fac.a[half + 7];
+                    const uint64_t a2 = pk(at, at);
+#pragma unroll
+                    for (int c = 0; c < kW; ++c)
+#pragma unroll
+                        for (int i = 0; i < kP; ++i) s[c][i] = mul2(a2, s[c][i]);
+                }
                 // Sum over the 8 row groups (lane bits 0-2): each step keeps half of the
                 // tokens, so lane rg ends with token rg of the eight.
 #pragma unroll
@@ -173,7 +278,7 @@ __global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanA
 #pragma unroll
                     for (int t = 0; t < keep; ++t)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
+                        for (int c = 0; c < kW; ++c) {
                             const float send = up ? acc[t][c] : acc[t + keep][c];
                             const float mine = up ? acc[t + keep][c] : acc[t][c];
                             acc[t][c] = mine + __shfl_xor_sync(0xffffffffu, send, keep);
@@ -181,10 +286,11 @@ __global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanA
                 }
                 const int tt = half + rg;
                 if (tt < m) {
+                    const float at = plain ? 1.f : fac.a[tt];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < kW; ++c) {
                         if (col + c >= a.P) continue;
-                        float v = fmaf(Dh, xs[tt * cols + col + c], acc[0][c]);
+                        float v = fmaf(at, acc[0][c], Dh * xs[tt * cols + col + c]);
                         if (z) v *= silu(to_f(z[(int64_t)(tile + tt) * a.z_ts + col + c]));
                         y[(int64_t)(tile + tt) * a.y_ts + col + c] = from_f<T>(v);
                     }
@@ -196,10 +302,10 @@ __global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanA
                        : (seg == a.nseg - 1 && a.S_out ? a.S_out + bh * a.S * a.P : nullptr);
     if (to) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kW; ++c) {
             if (col + c >= a.P) continue;
 #pragma unroll
-            for (int i = 0; i < R / 2; ++i) {
+            for (int i = 0; i < kP; ++i) {
                 const int r = rg * R + 2 * i;
                 float lo, hi;
                 asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(s[c][i]));
@@ -208,30 +314,32 @@ __global__ void __launch_bounds__(512) scan_kernel(const __grid_constant__ ScanA
             }
         }
     }
-    if (kState && tid == 0) a.seg_decay[bh * a.nseg + seg] = decay;
+    if (kState && tid == 0) a.seg_decay[bh * a.nseg + seg] = behind;
 }
 
 // In place over a head's segments: the end states (from zero) become the states
 // that the segments start from, seed_0 = S0, seed_{i+1} = exp(decay_i) seed_i + end_i.
 // A thread chains one element (reads and writes of a segment are whole rows of
-// threads), eight segments in flight; the decays' exponentials are shared.
+// threads), sixteen segments in flight; the decays' exponentials are shared.
 constexpr int kMaxSegments = 512;
 __global__ void __launch_bounds__(128) seed_kernel(const __grid_constant__ ScanArgs a) {
     __shared__ float f[kMaxSegments];
     const int64_t bh = blockIdx.y;
+    tcc::pdl_launch_dependents();
+    tcc::pdl_wait();
     for (int i = threadIdx.x; i < a.nseg; i += 128) f[i] = expf(a.seg_decay[bh * a.nseg + i]);
     __syncthreads();
     const int e = blockIdx.x * 128 + threadIdx.x, E = a.S * a.P;
     if (e >= E) return;
     float carry = a.S0 ? a.S0[bh * E + e] : 0.f;
     float* p = a.seeds + bh * a.nseg * E + e;
-    for (int i0 = 0; i0 < a.nseg; i0 += 8) {
-        float end[8];
+    for (int i0 = 0; i0 < a.nseg; i0 += 16) {
+        float end[16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < 16; ++u)
             if (i0 + u < a.nseg) end[u] = p[(int64_t)(i0 + u) * E];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 16; ++u) {
             if (i0 + u >= a.nseg) break;
             p[(int64_t)(i0 + u) * E] = carry;
             carry = fmaf(f[i0 + u], carry, end[u]);
@@ -313,26 +421,42 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const __grid_constant__ 
     }
 }
 
-template <typename T, int R>
+template <typename T, int R, int kW>
 cudaError_t recurrence(const ScanArgs& a, int64_t BH, cudaStream_t st) {
-    const int warps = (a.P + 7) / 8;
-    const size_t smem = sizeof(float) * (size_t)(kTok * (2 * 8 * kGroupStride<R> + 8 * warps) + 2 * kTok);
+    const int warps = (a.P + 4 * kW - 1) / (4 * kW);
+    const size_t row = sizeof(float) * kTok * 8 * kGroupStride<R>, x = sizeof(float) * (size_t)kTok * 4 * kW * warps;
+    const size_t smem = 2 * row + x;
+    static std::atomic<int> optin[tcc::kMaxDevices];
+    // The largest head needs more than the 48 KB that need no opting in.
+    cudaError_t e = tcc::ensure_smem_optin(scan_kernel<T, R, kW, false>,
+                                           (int)(sizeof(float) * kTok * (16 * kGroupStride<R> + kMaxDim)), optin);
+    if (e != cudaSuccess) return e;
     const dim3 grid(a.nseg, (unsigned)BH);
     if (a.nseg > 1) {
-        scan_kernel<T, R, true><<<grid, 32 * warps, smem, st>>>(a);
-        cudaError_t e = launch_seeds(a, BH, st);
-        if (e != cudaSuccess) return e;
+        scan_kernel<T, R, kW, true><<<grid, 32 * warps, row + x, st>>>(a);
+        if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
+        if ((e = launch_seeds(a, BH, st)) != cudaSuccess) return e;
     }
-    scan_kernel<T, R, false><<<grid, 32 * warps, smem, st>>>(a);
-    return cudaPeekAtLastError();
+    return launch_after(scan_kernel<T, R, kW, false>, grid, 32 * warps, smem, st, a.nseg > 1, a);
+}
+
+// Four columns per lane share each row's B and C. Two for heads of at most 8
+// columns, which would leave half of the lanes idle, and for states of more than 64
+// rows, whose lanes would hold 48 to 64 values (254 registers with 16 rows).
+template <typename T, int R>
+cudaError_t recurrence_by_width(const ScanArgs& a, int64_t BH, cudaStream_t st) {
+    if constexpr (R <= 8)
+        if (a.P > 8) return recurrence<T, R, 4>(a, BH, st);
+    return recurrence<T, R, 2>(a, BH, st);
 }
 
 template <typename T>
 cudaError_t recurrence_by_size(const ScanArgs& a, int64_t BH, cudaStream_t st) {
-    if (a.S <= 16) return recurrence<T, 2>(a, BH, st);
-    if (a.S <= 32) return recurrence<T, 4>(a, BH, st);
-    if (a.S <= 64) return recurrence<T, 8>(a, BH, st);
-    return recurrence<T, 16>(a, BH, st);
+    if (a.S <= 16) return recurrence_by_width<T, 2>(a, BH, st);
+    if (a.S <= 32) return recurrence_by_width<T, 4>(a, BH, st);
+    if (a.S <= 64) return recurrence_by_width<T, 8>(a, BH, st);
+    if (a.S <= 96) return recurrence_by_width<T, 12>(a, BH, st);
+    return recurrence_by_width<T, 16>(a, BH, st);
 }
 
 template <typename T>
@@ -361,10 +485,10 @@ bool bad4(const void* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
 
 namespace scan {
 
-// Segments of the recurrence: one while there are two blocks per SM or fewer
-// than two stretches of 64 tokens; else as many as fill two blocks per SM.
+// Segments of the recurrence: one while there are three blocks per SM or fewer
+// than two stretches of 64 tokens; else as many as fill three blocks per SM.
 int recurrence_segments(int64_t BH, int N) {
-    const int64_t want = 2 * (int64_t)tcc::sm_count() / (BH > 0 ? BH : 1);
+    const int64_t want = 3 * (int64_t)tcc::sm_count() / (BH > 0 ? BH : 1);
     const int64_t most = N / 64;
     int64_t n = want < most ? want : most;
     n = n < kMaxSegments ? n : kMaxSegments;
@@ -372,8 +496,7 @@ int recurrence_segments(int64_t BH, int N) {
 }
 
 cudaError_t launch_seeds(const ScanArgs& a, int64_t BH, cudaStream_t st) {
-    seed_kernel<<<dim3((a.S * a.P + 127) / 128, (unsigned)BH), 128, 0, st>>>(a);
-    return cudaPeekAtLastError();
+    return launch_after(seed_kernel, dim3((a.S * a.P + 127) / 128, (unsigned)BH), 128, 0, st, true, a);
 }
 
 }  // namespace scan

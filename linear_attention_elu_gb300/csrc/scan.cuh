@@ -55,6 +55,24 @@ bool tc_supported(const ScanArgs& a, int B, la_dtype dt);
 int tc_segments(int64_t B, int H, int G, int N, int P);
 cudaError_t tc_scan(ScanArgs& a, int B, void* ws_header, cudaStream_t st);
 
+// Launches a kernel, with `dependent` as a programmatic dependent of the one before
+// it in the stream (it must call griddepcontrol.wait before it reads that one's results).
+template <typename... P, typename... V>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         bool dependent, V&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 int recurrence_segments(int64_t BH, int N);
 cudaError_t launch_seeds(const ScanArgs& a, int64_t BH, cudaStream_t st);
 

@@ -317,7 +317,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Place pl = place(a, un);
     const bool last_seg = pl.seg == a.nseg - 1;
-    if (pl.nc == 0 && !(last_seg && a.S_out)) return;
+    if (pl.nc == 0 && !(last_seg && a.S_out)) {
+        pdl_wait();                            // a dependent launch never ends before what it follows
+        return;
+    }
     const int nu = pl.nu, items = pl.nc * nu;
 
     if (tid == 0) {
@@ -357,6 +360,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // The second pass is a programmatic dependent of the chaining kernel: everything above
+    // touches no global memory but the lengths.
+    pdl_wait();
     const uint32_t tmem = m.tmem_slot;
     const uint32_t max_spin = hdr->max_spin;
     const bool hold = hdr->hold_item != 0;                 // test hook: loads never issued
@@ -809,6 +815,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();
     const uint32_t tmem = m.tmem_slot;
     const uint32_t max_spin = hdr->max_spin;
     const bool hold = hdr->hold_item != 0;                 // test hook: loads never issued
@@ -1005,8 +1012,7 @@ cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorM
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         if ((e = launch_seeds(a, (int64_t)B * a.H, st)) != cudaSuccess) return e;
     }
-    scan_tc_kernel<kT><<<grid, kThreads, Smem<kT>::kBytes, st>>>(xm, bm, cm, zm, ym, a, un, hdr);
-    return cudaPeekAtLastError();
+    return launch_after(scan_tc_kernel<kT>, grid, kThreads, Smem<kT>::kBytes, st, a.nseg > 1, xm, bm, cm, zm, ym, a, un, hdr);
 }
 
 }  // namespace
