@@ -82,9 +82,12 @@ struct Units {
 // TMEM columns of the main kernel.
 constexpr uint32_t kTmSc = 0, kTmP = 128, kTmY1 = 256, kTmY2 = 320, kTmSt = 384;
 
+// Barriers of items are kept per item parity: a group of warps sees every second
+// item, and one that skipped phases of a barrier could take an earlier phase's
+// parity for its own.
 struct Misc {
     uint64_t c_full, c_empty, b_full[2], b_empty[2], x_full[2], x_empty[2], dt_full[kDtRing], dt_empty[kDtRing];
-    uint64_t slot_ready[2], y_staged[2], sc_full, item_ready, read_done, y_full, state_done, drain;
+    uint64_t slot_ready[2], y_staged[2], sc_full[2], item_ready, read_done[2], y_full[2], state_done[2], drain;
     uint32_t tmem_slot;
 };
 
@@ -99,14 +102,16 @@ template <int kT> struct Smem {
     static constexpr uint32_t kSb = kOut + 2 * kTile;          // bf16 state, 64 kT rows
     static constexpr uint32_t kDt = kSb + kT * 64 * 128;
     static constexpr uint32_t kCol = kDt + (kDtRing * sizeof(Decay) + 127) / 128 * 128;
-    static constexpr uint32_t kMisc = kCol + 16 * 32 * 4;      // 32 column factors per warp
+    static constexpr uint32_t kMask = kCol + 16 * 32 * 4;      // 32 column factors per warp
+    static constexpr uint32_t kMisc = kMask + 32 * 16 * 4;     // diagonal block: 16 words of pairs per row
     static constexpr uint32_t kEnd = kMisc + sizeof(Misc);
     static constexpr size_t kBytes = 1024 + kEnd;
 };
 static_assert(Smem<2>::kBytes <= 227 * 1024, "main kernel's shared memory");
 
 constexpr int kThreads = 640;
-constexpr int kWork = 16;              // warps that share the items' steps; then TMA, MMA, decays, slots
+constexpr int kWork = 16;              // warps of the items' steps (two groups); then TMA, MMA, decays, slots
+constexpr int kGroup = kWork / 2;
 constexpr int kAhead = 3;              // items between a tile's L2 prefetch and its load
 
 __device__ __forceinline__ float ex2(float x) {
@@ -300,7 +305,7 @@ __device__ __forceinline__ uint64_t gate2(uint32_t z) {
     return mul2(v, pk2(r0, r1));
 }
 
-template <int kT>
+template <int kT, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap zmap,
@@ -328,21 +333,21 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             mbar_init(&m.b_full[s], 1);
             mbar_init(&m.b_empty[s], 1);
             mbar_init(&m.x_full[s], 1);
-            mbar_init(&m.x_empty[s], kWork);
+            mbar_init(&m.x_empty[s], kGroup);
             mbar_init(&m.slot_ready[s], 1);
-            mbar_init(&m.y_staged[s], kWork);
+            mbar_init(&m.y_staged[s], kGroup);
+            mbar_init(&m.sc_full[s], 1);
+            mbar_init(&m.read_done[s], 1);
+            mbar_init(&m.y_full[s], 1);
+            mbar_init(&m.state_done[s], 1);
         }
         for (int s = 0; s < kDtRing; ++s) {
             mbar_init(&m.dt_full[s], 1);
-            mbar_init(&m.dt_empty[s], kWork);
+            mbar_init(&m.dt_empty[s], kGroup);
         }
         mbar_init(&m.c_full, 1);
         mbar_init(&m.c_empty, 1);
-        mbar_init(&m.sc_full, 1);
         mbar_init(&m.item_ready, kWork);
-        mbar_init(&m.read_done, 1);
-        mbar_init(&m.y_full, 1);
-        mbar_init(&m.state_done, 1);
         mbar_init(&m.drain, 1);
         fence_mbar_init();
     }
@@ -366,8 +371,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     const uint32_t tmem = m.tmem_slot;
     const uint32_t max_spin = hdr->max_spin;
     const bool hold = hdr->hold_item != 0;                 // test hook: loads never issued
-    // The last chunk of a ragged sequence is stored row by row.
-    auto by_rows = [&](int i) { return pl.n < a.N && (pl.c0 + i + 1) * kC > pl.n; };
+    // The last chunk of a ragged sequence is stored row by row: its number, or -1.
+    const int by_rows = pl.n < a.N && (pl.c0 + pl.nc) * kC > pl.n ? pl.nc - 1 : -1;
     bool ok = true;
 
     if (warp == kWork) {
@@ -432,7 +437,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 #pragma unroll
                     for (int k = 0; k < 4 * kT; ++k)
                         mma_bf16(tmem + kTmSc, kmajor_step(ca0, k), kmajor_step(ba, k), id_sc, k > 0);
-                    mma_commit(&m.sc_full);
+                    mma_commit(&m.sc_full[i & 1]);
                 }
                 __syncwarp();
             }
@@ -442,16 +447,16 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 #pragma unroll
                 for (int k = 0; k < 4 * kT; ++k)                                        // (2)
                     mma_bf16(tmem + kTmY2, kmajor_step(ca0, k), step_desc(sb0, k * 2048), id_y, k > 0);
-                mma_commit(&m.read_done);
+                mma_commit(&m.read_done[n & 1]);
                 if (u == nu - 1) mma_commit(&m.c_empty);
                 const uint64_t xa = step_desc(x0, (n & 1) * kTile);
                 const uint32_t pt = tmem + kTmP + 64 * (n & 1);
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k)                                       // (3)
                     mma_bf16_ts(tmem + kTmY1, pt + 8 * k, step_desc(xa, k * 2048), id_y, k > 0);
-                mma_commit(&m.y_full);
+                mma_commit(&m.y_full[n & 1]);
                 issue_state(tmem + kTmSt + 64 * u, step_desc(br0, (i & 1) * kT * kTile), xw0, false);  // (4)
-                mma_commit(&m.state_done);
+                mma_commit(&m.state_done[n & 1]);
                 if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
             __syncwarp();
@@ -507,7 +512,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             for (int n = 0; n < 2 && n < items && !hold; ++n) open_slot(n / nu, n % nu);
             for (int n = 0, i = 0, u = 0; n < items; ++n) {
                 if (!(ok = mbar_wait(&m.y_staged[n & 1], (n >> 1) & 1, max_spin))) break;
-                if (!by_rows(i)) {
+                if (i != by_rows) {
                     tma_store_4d(&ymap, oslot(n), pl.col0(un, u), pl.head(a, un, u), (pl.c0 + i) * kC, pl.b);
                     tma_store_commit();
                     tma_store_wait_read<0>();
@@ -521,107 +526,128 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         }
     } else {
         // ------------------------------------------------------------ the items' steps
-        const int q = warp & 3, g = warp >> 2, row = 32 * q + lane;   // TMEM lane quarter, column group
+        // Group (item mod 2) of eight warps; a warp's TMEM lane quarter, half of the columns.
+        const int grp = warp >> 3, q = warp & 3, g = (warp >> 2) & 1, row = 32 * q + lane;
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         const int64_t head_state = (int64_t)a.S * a.P;
-        const bool has_state = q < 2 * kT, gated = a.z != nullptr, tma_gate = un.gate_vec != 0;
+        const bool has_state = q < 2 * kT;
         float* col = reinterpret_cast<float*>(base + L::kCol) + 32 * warp;
+        const uint32_t* mask = reinterpret_cast<const uint32_t*>(base + L::kMask) + 16 * lane;
         uint8_t* sb = base + L::kSb;
-        // This lane's two 16-byte pieces of columns 16 g .. 16 g + 15 in a swizzled tile.
-        const uint32_t pc0 = row * 128 + (((2 * g) ^ (row & 7)) << 4), pc1 = row * 128 + (((2 * g + 1) ^ (row & 7)) << 4);
-        if (g > q) {                           // blocks above the diagonal are zero in both P buffers
-            const uint32_t z[16] = {};
-            tmem_st16(tmem + lanes + kTmP + 16 * g, z);
-            tmem_st16(tmem + lanes + kTmP + 64 + 16 * g, z);
-            tmem_st_wait();
-        }
+        const uint32_t ptm = tmem + lanes + kTmP + 64 * grp;
+        // Byte offset of this row's 16-byte piece j (columns 8 j ..) in a swizzled tile.
+        auto piece = [&](int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); };
+        if (warp < 4)                          // pairs 2e, 2e + 1 up to the row's own token
+            for (int e = warp; e < 16; e += 4)
+                reinterpret_cast<uint32_t*>(base + L::kMask)[16 * lane + e] =
+                    2 * e < lane ? 0xFFFFFFFFu : (2 * e == lane ? 0xFFFFu : 0u);
+        for (int b = g; b < 4; b += 2)         // blocks above the diagonal stay zero
+            if (b > q) {
+                const uint32_t z[16] = {};
+                tmem_st16(ptm + 16 * b, z);
+            }
         float Du[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int h = pl.head(a, un, min(u, nu - 1)), c0 = pl.col0(un, min(u, nu - 1)) + 16 * g;
+            const int h = pl.head(a, un, min(u, nu - 1));
             Du[u] = a.D ? a.D[h] : 0.f;
-            if (!has_state || u >= nu) continue;
-            // The state before the first chunk.
+            // The state before the first chunk (group u writes unit u's).
+            if (!has_state || u >= nu || u != grp) continue;
             const int64_t bh = (int64_t)pl.b * a.H + h;
             const float* from = a.nseg > 1 ? a.seeds + (bh * a.nseg + pl.seg) * head_state
                                            : (a.S0 ? a.S0 + bh * head_state : nullptr);
-            uint32_t v[16];
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 16) {
+                const int c0 = pl.col0(un, u) + 32 * g + c;
+                uint32_t v[16];
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                const uint4 x = from && row < a.S && c0 + k < a.P
-                                    ? *reinterpret_cast<const uint4*>(from + (int64_t)row * a.P + c0 + k)
-                                    : make_uint4(0, 0, 0, 0);
-                v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
+                for (int k = 0; k < 16; k += 4) {
+                    const uint4 x = from && row < a.S && c0 + k < a.P
+                                        ? *reinterpret_cast<const uint4*>(from + (int64_t)row * a.P + c0 + k)
+                                        : make_uint4(0, 0, 0, 0);
+                    v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
+                }
+                tmem_st16(tmem + lanes + kTmSt + 64 * u + 32 * g + c, v);
             }
-            tmem_st16(tmem + lanes + kTmSt + 64 * u + 16 * g, v);
-            tmem_st_wait();
         }
-        for (int n = 0, i = 0, u = 0; n <= items; ++n) {
-            const int slot = n % kDtRing;
+        tmem_st_wait();
+        named_bar(1, 32 * kWork);              // the mask table
+        tc_fence_before();
+        // An item is issued when its own group has prepared it and the other group has
+        // taken the output of the item before (for the first item there is none).
+        if (grp == 1 && lane == 0) mbar_arrive(&m.item_ready);
+        for (int n = grp; n < items; n += 2) {
+            const int slot = n % kDtRing, i = n / nu, u = n - i * nu, s1 = (n - 1) & 1, ph1 = ((n - 1) >> 1) & 1;
             const Decay& dc = dts[slot];
-            if (n < items && !(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin))) break;
+            if (!(ok = warp_wait(&m.dt_full[slot], (n / kDtRing) & 1, max_spin))) break;
             // Scores to P first, except at a chunk's start, where (1) is still under way.
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
                 if ((pass == 0) == (u != 0)) {
                     // ------------------------------------------------ scores to P
-                    if (n == items || g > q) continue;
-                    if (u == 0 && !(ok = warp_wait(&m.sc_full, i & 1, max_spin))) break;
+                    if (!(ok = warp_wait(&m.sc_full[i & 1], (i >> 1) & 1, max_spin))) break;
                     tc_fence_after();
-                    uint32_t s[2][16], p[16];
-                    tmem_ld16(tmem + lanes + kTmSc + 32 * g, s[0]);
-                    tmem_ld16(tmem + lanes + kTmSc + 32 * g + 16, s[1]);
                     const float ci = dc.cum[row];
-                    if (g < q) {
-                        const float cm = dc.cum[32 * q - 1];
-                        col[lane] = ex2(cm - dc.cum[32 * g + lane]) * dc.d[32 * g + lane];
-                        __syncwarp();
-                        const float ri = ex2(ci - cm);
-                        const uint64_t r2 = pk2(ri, ri);
-                        tmem_ld_wait();
+#pragma unroll 1
+                    for (int b = g; b <= q; b += 2) {
+                        uint32_t s[2][16], p[16];
+                        tmem_ld16(tmem + lanes + kTmSc + 32 * b, s[0]);
+                        tmem_ld16(tmem + lanes + kTmSc + 32 * b + 16, s[1]);
+                        if (b < q) {
+                            const float cm = dc.cum[32 * q - 1];
+                            col[lane] = ex2(cm - dc.cum[32 * b + lane]) * dc.d[32 * b + lane];
+                            __syncwarp();
+                            const float ri = ex2(ci - cm);
+                            const uint64_t r2 = pk2(ri, ri);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(col + 2 * e);
-                            const uint32_t* v = &s[e >> 3][2 * (e & 7)];
-                            p[e] = pack2(mul2(mul2(pk2(__uint_as_float(v[0]), __uint_as_float(v[1])), f.x), r2));
-                            p[e + 1] = pack2(mul2(mul2(pk2(__uint_as_float(v[2]), __uint_as_float(v[3])), f.y), r2));
-                        }
-                    } else {
-                        // The diagonal block: an exponential per score; pairs past the row's own
-                        // token are cleared as bits (their products may be anything).
-                        const uint64_t c2 = pk2(ci, ci), minus = pk2(-1.f, -1.f);
-                        tmem_ld_wait();
+                            for (int e = 0; e < 16; e += 2) {
+                                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(col + 2 * e);
+                                const uint32_t* v = &s[e >> 3][2 * (e & 7)];
+                                p[e] = pack2(mul2(mul2(pk2(__uint_as_float(v[0]), __uint_as_float(v[1])), f.x), r2));
+                                p[e + 1] = pack2(mul2(mul2(pk2(__uint_as_float(v[2]), __uint_as_float(v[3])), f.y), r2));
+                            }
+                            __syncwarp();                  // the factors have been read
+                        } else {
+                            // The diagonal block: an exponential per score; pairs past the row's
+                            // own token are cleared as bits (their products may be anything).
+                            const uint64_t c2 = pk2(ci, ci), minus = pk2(-1.f, -1.f);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dc.cum + 32 * q + 2 * e);
-                            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(dc.d + 32 * q + 2 * e);
-                            const uint32_t* v = &s[e >> 3][2 * (e & 7)];
+                            for (int e = 0; e < 16; e += 2) {
+                                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dc.cum + 32 * q + 2 * e);
+                                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(dc.d + 32 * q + 2 * e);
+                                const uint2 mk = *reinterpret_cast<const uint2*>(mask + e);
+                                const uint32_t* v = &s[e >> 3][2 * (e & 7)];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float t0, t1;
-                                unpk2(fma2(k ? l.y : l.x, minus, c2), &t0, &t1);
-                                const uint64_t f = mul2(pk2(ex2(t0), ex2(t1)), k ? d.y : d.x);
-                                const uint32_t w = pack2(mul2(f, pk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]))));
-                                const int j = 2 * (e + k);
-                                p[e + k] = j < lane ? w : (j == lane ? w & 0xFFFFu : 0u);
+                                for (int k = 0; k < 2; ++k) {
+                                    float t0, t1;
+                                    unpk2(fma2(k ? l.y : l.x, minus, c2), &t0, &t1);
+                                    const uint64_t f = mul2(pk2(ex2(t0), ex2(t1)), k ? d.y : d.x);
+                                    p[e + k] = pack2(mul2(f, pk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])))) &
+                                               (k ? mk.y : mk.x);
+                                }
                             }
                         }
+                        tmem_st16(ptm + 16 * b, p);
                     }
-                    tmem_st16(tmem + lanes + kTmP + 64 * (n & 1) + 16 * g, p);
                     continue;
                 }
                 // ---------------------------------------------------- state: bf16 for (2), scaled for (4)
-                if (n < items) {
-                    if (n > 0 && !(ok = warp_wait(&m.read_done, (n - 1) & 1, max_spin) &&
-                                        (nu == 2 || warp_wait(&m.state_done, (n - 1) & 1, max_spin))))
-                        break;
-                    if (has_state) {
-                        tc_fence_after();
-                        const uint32_t st = tmem + lanes + kTmSt + 64 * u + 16 * g;
+                // (2) of the item before has read the bf16 state; with two units it was issued
+                // after (4) of this unit's last item, so that one is done as well.
+                if (n > 0 && !(ok = warp_wait(&m.read_done[s1], ph1, max_spin) &&
+                                    (nu == 2 || warp_wait(&m.state_done[s1], ph1, max_spin))))
+                    break;
+                if (has_state) {
+                    tc_fence_after();
+                    const float f = dc.total;
+                    const uint64_t f2 = pk2(f, f);
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t at = tmem + lanes + kTmSt + 64 * u + 32 * g + 16 * c;
                         uint32_t v[16], h[8];
-                        tmem_ld16(st, v);
-                        const float f = dc.total;
-                        const uint64_t f2 = pk2(f, f);
+                        tmem_ld16(at, v);
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -632,112 +658,120 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                             v[2 * e] = __float_as_uint(lo);
                             v[2 * e + 1] = __float_as_uint(hi);
                         }
-                        tmem_st16(st, v);
+                        tmem_st16(at, v);
                         if (row >= a.S)                    // padding rows never reach the read
 #pragma unroll
                             for (int e = 0; e < 8; ++e) h[e] = 0u;
-                        *reinterpret_cast<uint4*>(sb + pc0) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4*>(sb + pc1) = make_uint4(h[4], h[5], h[6], h[7]);
-                    }
-                }
-                // ---------------------------------------------------- output of the item before
-                if (n > 0) {
-                    const int pn = n - 1, pu = u == 0 ? nu - 1 : u - 1, pi = u == 0 ? i - 1 : i;
-                    const float Dh = pu ? Du[1] : Du[0], e = ex2(dts[pn % kDtRing].cum[row]);
-                    const uint64_t D2 = pk2(Dh, Dh), e2 = pk2(e, e);
-                    const uint4 xv[2] = {*reinterpret_cast<const uint4*>(xtile(pn) + pc0),
-                                         *reinterpret_cast<const uint4*>(xtile(pn) + pc1)};
-                    if (!(ok = warp_wait(&m.slot_ready[pn & 1], (pn >> 1) & 1, max_spin) &&
-                               warp_wait(&m.y_full, pn & 1, max_spin)))
-                        break;
-                    tc_fence_after();
-                    if (lane == 0) mbar_arrive(&m.x_empty[pn & 1]);   // (3) and this warp are done with x
-                    uint32_t y1[16], y2[16];
-                    tmem_ld16(tmem + lanes + kTmY1 + 16 * g, y1);
-                    tmem_ld16(tmem + lanes + kTmY2 + 16 * g, y2);
-                    uint64_t gt[8];
-                    if (gated) {
-                        if (!tma_gate) put_gate(a, pl, un, pu, (pl.c0 + pi) * kC + row, 16 * g, oslot(pn), pc0, pc1);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint4 z = *reinterpret_cast<const uint4*>(oslot(pn) + (j ? pc1 : pc0));
-                            gt[4 * j] = gate2(z.x), gt[4 * j + 1] = gate2(z.y);
-                            gt[4 * j + 2] = gate2(z.z), gt[4 * j + 3] = gate2(z.w);
-                        }
-                    }
-                    tmem_ld_wait();
-                    uint32_t o[8];
-#pragma unroll
-                    for (int f = 0; f < 8; ++f) {
-                        const uint4 x = xv[f >> 2];
-                        const uint32_t xs = (f & 3) == 0 ? x.x : (f & 3) == 1 ? x.y : (f & 3) == 2 ? x.z : x.w;
-                        uint64_t v = fma2(e2, pk2(__uint_as_float(y2[2 * f]), __uint_as_float(y2[2 * f + 1])),
-                                          pk2(__uint_as_float(y1[2 * f]), __uint_as_float(y1[2 * f + 1])));
-                        v = fma2(D2, bf2(xs), v);
-                        o[f] = pack2(gated ? mul2(v, gt[f]) : v);
-                    }
-                    const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
-                    if (!by_rows(pi)) {
-                        *reinterpret_cast<uint4*>(oslot(pn) + pc0) = o0;
-                        *reinterpret_cast<uint4*>(oslot(pn) + pc1) = o1;
-                    } else {
-                        put_row(a, pl, un, pu, (pl.c0 + pi) * kC + row, 16 * g, o0, o1);
+                        *reinterpret_cast<uint4*>(sb + piece(4 * g + 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(sb + piece(4 * g + 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
                 }
                 // ---------------------------------------------------- weighted values
-                if (n < items) {
-                    if (!(ok = warp_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin))) break;
-                    // Rows at or past a ragged end may hold anything: they are cleared in x, and in
-                    // B for (4). (1) may read such rows of B, whose scores no kept row uses.
-                    if (a.lengths && (pl.c0 + i + 1) * kC > pl.n) {       // uniform over the block
-                        if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin))) break;
-                        if ((pl.c0 + i) * kC + row >= pl.n) {
-                            *reinterpret_cast<uint4*>(xtile(n) + pc0) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4*>(xtile(n) + pc1) = make_uint4(0, 0, 0, 0);
-                            for (int k = 0; k < kT && u == 0; ++k) {
-                                *reinterpret_cast<uint4*>(btile(i & 1) + k * kTile + pc0) = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4*>(btile(i & 1) + k * kTile + pc1) = make_uint4(0, 0, 0, 0);
-                            }
+                if (!(ok = warp_wait(&m.x_full[n & 1], (n >> 1) & 1, max_spin) &&
+                           (n == 0 || warp_wait(&m.state_done[s1], ph1, max_spin))))
+                    break;
+                // Rows at or past a ragged end may hold anything: they are cleared in x, and in
+                // B for (4). (1) may read such rows of B, whose scores no kept row uses.
+                if (i == by_rows) {
+                    if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin))) break;
+                    if ((pl.c0 + i) * kC + row >= pl.n)
+                        for (int j = 4 * g; j < 4 * g + 4; ++j) {
+                            *reinterpret_cast<uint4*>(xtile(n) + piece(j)) = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < kT; ++k)
+                                *reinterpret_cast<uint4*>(btile(i & 1) + k * kTile + piece(j)) = make_uint4(0, 0, 0, 0);
                         }
-                    }
-                    uint32_t wh[8], wl[8];
-                    weigh16(*reinterpret_cast<const uint4*>(xtile(n) + pc0), *reinterpret_cast<const uint4*>(xtile(n) + pc1),
-                            dc.w[row], wh, wl);
-                    if (n > 0 && !(ok = warp_wait(&m.state_done, (n - 1) & 1, max_spin))) break;
+                }
+                const float w = dc.w[row];
+#pragma unroll 1
+                for (int j = 4 * g; j < 4 * g + 4; j += 2) {
+                    const uint32_t o0 = piece(j), o1 = piece(j + 1);
                     uint8_t* hi = base + L::kXw;
-                    *reinterpret_cast<uint4*>(hi + pc0) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-                    *reinterpret_cast<uint4*>(hi + pc1) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
-                    *reinterpret_cast<uint4*>(hi + kTile + pc0) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-                    *reinterpret_cast<uint4*>(hi + kTile + pc1) = make_uint4(wl[4], wl[5], wl[6], wl[7]);
+                    uint32_t wh[8], wl[8];
+                    weigh16(*reinterpret_cast<const uint4*>(xtile(n) + o0), *reinterpret_cast<const uint4*>(xtile(n) + o1), w,
+                            wh, wl);
+                    *reinterpret_cast<uint4*>(hi + o0) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                    *reinterpret_cast<uint4*>(hi + o1) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
+                    *reinterpret_cast<uint4*>(hi + kTile + o0) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+                    *reinterpret_cast<uint4*>(hi + kTile + o1) = make_uint4(wl[4], wl[5], wl[6], wl[7]);
                 }
             }
             if (!ok) break;
-            // What this warp stored is ready for the tensor cores and the TMA.
+            // What this warp stored is ready for the tensor cores.
             tmem_st_wait();
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if (n < items) mbar_arrive(&m.item_ready);
-                if (n > 0) {
-                    mbar_arrive(&m.y_staged[(n - 1) & 1]);
-                    mbar_arrive(&m.dt_empty[(n - 1) % kDtRing]);
+            if (lane == 0) mbar_arrive(&m.item_ready);
+            // -------------------------------------------------------- output
+            const float Dh = u ? Du[1] : Du[0], e = ex2(dc.cum[row]);
+            const uint64_t D2 = pk2(Dh, Dh), e2 = pk2(e, e);
+            if (!(ok = warp_wait(&m.slot_ready[n & 1], (n >> 1) & 1, max_spin) &&
+                       warp_wait(&m.y_full[n & 1], (n >> 1) & 1, max_spin)))
+                break;
+            tc_fence_after();
+            if (kGated && un.gate_vec == 0) {
+                put_gate(a, pl, un, u, (pl.c0 + i) * kC + row, 32 * g, oslot(n), piece(4 * g), piece(4 * g + 1));
+                put_gate(a, pl, un, u, (pl.c0 + i) * kC + row, 32 * g + 16, oslot(n), piece(4 * g + 2), piece(4 * g + 3));
+            }
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {                  // 16 columns at a time
+                const uint32_t o0 = piece(4 * g + 2 * c), o1 = piece(4 * g + 2 * c + 1);
+                const uint32_t ty = tmem + lanes + kTmY1 + 32 * g + 16 * c;
+                uint32_t y1[16], y2[16];
+                tmem_ld16(ty, y1);
+                tmem_ld16(ty + (kTmY2 - kTmY1), y2);
+                const uint4 xa = *reinterpret_cast<const uint4*>(xtile(n) + o0), xb = *reinterpret_cast<const uint4*>(xtile(n) + o1);
+                const uint32_t xs[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+                uint64_t gt[8];
+                if constexpr (kGated) {
+                    const uint4 za = *reinterpret_cast<const uint4*>(oslot(n) + o0), zb = *reinterpret_cast<const uint4*>(oslot(n) + o1);
+                    const uint32_t zs[8] = {za.x, za.y, za.z, za.w, zb.x, zb.y, zb.z, zb.w};
+#pragma unroll
+                    for (int f = 0; f < 8; ++f) gt[f] = gate2(zs[f]);
+                }
+                tmem_ld_wait();
+                if (c == 1) {
+                    // Y and x are free: the next item may be issued, the tile after it loaded.
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&m.item_ready);
+                        mbar_arrive(&m.x_empty[n & 1]);
+                        mbar_arrive(&m.dt_empty[slot]);
+                    }
+                }
+                uint32_t o[8];
+#pragma unroll
+                for (int f = 0; f < 8; ++f) {
+                    uint64_t v = fma2(e2, pk2(__uint_as_float(y2[2 * f]), __uint_as_float(y2[2 * f + 1])),
+                                      pk2(__uint_as_float(y1[2 * f]), __uint_as_float(y1[2 * f + 1])));
+                    v = fma2(D2, bf2(xs[f]), v);
+                    if constexpr (kGated) v = mul2(v, gt[f]);
+                    o[f] = pack2(v);
+                }
+                const uint4 p0 = make_uint4(o[0], o[1], o[2], o[3]), p1 = make_uint4(o[4], o[5], o[6], o[7]);
+                if (i != by_rows) {
+                    *reinterpret_cast<uint4*>(oslot(n) + o0) = p0;
+                    *reinterpret_cast<uint4*>(oslot(n) + o1) = p1;
+                } else {
+                    put_row(a, pl, un, u, (pl.c0 + i) * kC + row, 32 * g + 16 * c, p0, p1);
                 }
             }
-            if (n < items && ++u == nu) u = 0, ++i;
+            fence_proxy_async_smem();                      // the store reads the slot
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.y_staged[n & 1]);
         }
-        // The final state.
-        if (ok && last_seg && a.S_out && has_state) {
-            if (items == 0 || (ok = warp_wait(&m.state_done, (items - 1) & 1, max_spin))) {
+        // The final state (group u writes unit u's).
+        if (ok && last_seg && a.S_out && has_state && grp < nu) {
+            if (items == 0 || (ok = warp_wait(&m.state_done[(items - 1) & 1], ((items - 1) >> 1) & 1, max_spin))) {
                 tc_fence_after();
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (u >= nu) break;
-                    const int c0 = pl.col0(un, u) + 16 * g;
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                    const int c0 = pl.col0(un, grp) + 32 * g + c;
                     uint32_t v[16];
-                    tmem_ld16(tmem + lanes + kTmSt + 64 * u + 16 * g, v);
+                    tmem_ld16(tmem + lanes + kTmSt + 64 * grp + 32 * g + c, v);
                     tmem_ld_wait();
-                    float* to = a.S_out + ((int64_t)pl.b * a.H + pl.head(a, un, u)) * head_state + (int64_t)row * a.P + c0;
+                    float* to = a.S_out + ((int64_t)pl.b * a.H + pl.head(a, un, grp)) * head_state + (int64_t)row * a.P + c0;
 #pragma unroll
                     for (int k = 0; k < 16; k += 4)
                         if (row < a.S && c0 + k < a.P)
@@ -998,11 +1032,11 @@ int pick_segments(int64_t ctas, int N) {
     return best;
 }
 
-template <int kT>
-cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorMap& cm, const CUtensorMap& zm, const CUtensorMap& ym, const ScanArgs& a,
-                   const Units& un, int B, WsHeader* hdr, cudaStream_t st) {
+template <int kT, bool kGated>
+cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorMap& cm, const CUtensorMap& zm,
+                   const CUtensorMap& ym, const ScanArgs& a, const Units& un, int B, WsHeader* hdr, cudaStream_t st) {
     static std::atomic<int> optin[kMaxDevices], optin_sums[kMaxDevices];
-    cudaError_t e = ensure_smem_optin(scan_tc_kernel<kT>, (int)Smem<kT>::kBytes, optin);
+    cudaError_t e = ensure_smem_optin(scan_tc_kernel<kT, kGated>, (int)Smem<kT>::kBytes, optin);
     if (e != cudaSuccess) return e;
     const dim3 grid(un.pairs * a.G, a.nseg, B);
     if (a.nseg > 1) {
@@ -1012,7 +1046,8 @@ cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorM
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         if ((e = launch_seeds(a, (int64_t)B * a.H, st)) != cudaSuccess) return e;
     }
-    return launch_after(scan_tc_kernel<kT>, grid, kThreads, Smem<kT>::kBytes, st, a.nseg > 1, xm, bm, cm, zm, ym, a, un, hdr);
+    return launch_after(scan_tc_kernel<kT, kGated>, grid, kThreads, Smem<kT>::kBytes, st, a.nseg > 1, xm, bm, cm, zm,
+                        ym, a, un, hdr);
 }
 
 }  // namespace
@@ -1053,7 +1088,11 @@ cudaError_t tc_scan(ScanArgs& a, int B, void* ws_header, cudaStream_t st) {
     zm = xm;                                               // unused without an aligned gate
     if (un.gate_vec && !encode_rows(&zm, a.z, a.P, a.H, a.N, B, a.z_ts, a.z_bs)) return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
-    return a.S <= 64 ? launch<1>(xm, bm, cm, zm, ym, a, un, B, hdr, st) : launch<2>(xm, bm, cm, zm, ym, a, un, B, hdr, st);
+    if (a.S <= 64)
+        return a.z ? launch<1, true>(xm, bm, cm, zm, ym, a, un, B, hdr, st)
+                   : launch<1, false>(xm, bm, cm, zm, ym, a, un, B, hdr, st);
+    return a.z ? launch<2, true>(xm, bm, cm, zm, ym, a, un, B, hdr, st)
+               : launch<2, false>(xm, bm, cm, zm, ym, a, un, B, hdr, st);
 }
 
 }  // namespace scan
