@@ -74,7 +74,8 @@ struct Decay {
 };
 
 struct Units {
-    int pairs, units, blocks;   // CTAs per group, units per group, 64-column blocks per head
+    int ctas, units, blocks;    // CTAs per group, units per group, 64-column blocks per head
+    int per;                    // units per CTA, 1 or 2
     int cps;                    // chunks per segment
     int gate_vec;               // z rows are 16-byte aligned
 };
@@ -163,12 +164,12 @@ struct Place {
 
 __device__ __forceinline__ Place place(const ScanArgs& a, const Units& un) {
     Place p;
-    const int pair = blockIdx.x % un.pairs;
-    p.g = blockIdx.x / un.pairs;
+    const int cta = blockIdx.x % un.ctas;
+    p.g = blockIdx.x / un.ctas;
     p.seg = blockIdx.y;
     p.b = blockIdx.z;
-    p.unit0 = 2 * pair;
-    p.nu = min(2, un.units - p.unit0);
+    p.unit0 = un.per * cta;
+    p.nu = min(un.per, un.units - p.unit0);
     p.n = a.lengths ? min(max(a.lengths[p.b], 0), a.N) : a.N;
     p.c0 = p.seg * un.cps;
     p.nc = min(max((p.n + kC - 1) / kC - p.c0, 0), un.cps);
@@ -532,14 +533,14 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         const int64_t head_state = (int64_t)a.S * a.P;
         const bool has_state = q < 2 * kT;
         float* col = reinterpret_cast<float*>(base + L::kCol) + 32 * warp;
-        const uint32_t* mask = reinterpret_cast<const uint32_t*>(base + L::kMask) + 16 * lane;
+        const uint2* mask = reinterpret_cast<const uint2*>(base + L::kMask) + lane;   // [e / 2][lane]
         uint8_t* sb = base + L::kSb;
         const uint32_t ptm = tmem + lanes + kTmP + 64 * grp;
         // Byte offset of this row's 16-byte piece j (columns 8 j ..) in a swizzled tile.
         auto piece = [&](int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); };
         if (warp < 4)                          // pairs 2e, 2e + 1 up to the row's own token
             for (int e = warp; e < 16; e += 4)
-                reinterpret_cast<uint32_t*>(base + L::kMask)[16 * lane + e] =
+                reinterpret_cast<uint32_t*>(base + L::kMask)[64 * (e >> 1) + 2 * lane + (e & 1)] =
                     2 * e < lane ? 0xFFFFFFFFu : (2 * e == lane ? 0xFFFFu : 0u);
         for (int b = g; b < 4; b += 2)         // blocks above the diagonal stay zero
             if (b > q) {
@@ -617,7 +618,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                             for (int e = 0; e < 16; e += 2) {
                                 const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dc.cum + 32 * q + 2 * e);
                                 const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(dc.d + 32 * q + 2 * e);
-                                const uint2 mk = *reinterpret_cast<const uint2*>(mask + e);
+                                const uint2 mk = mask[16 * e];   // 32 (e / 2)
                                 const uint32_t* v = &s[e >> 3][2 * (e & 7)];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
@@ -790,6 +791,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 // First pass over segments: end state from zero, sum over the segment of
 // B_j (d_j e^{l(end) - l_j} x_j)^T, and the segment's total decay. Chunks run from
 // the last to the first; the weights carry the sum of the chunks after them.
+// Here the product is taken transposed, (w x)^T B with value and remainder as the two
+// halves of one 128-row operand: D rows 0-63 + rows 64-127, S columns. That reads 64 KB
+// of operands per item instead of the main pass's 96 (which has no TMEM left for it).
 // Warps: TMA, MMA, decays (two), then four weight groups of four: two items at a
 // time, half of the columns each (one group per item left the pass waiting for
 // its weights).
@@ -843,7 +847,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(&m.tmem_slot, 128);
+        tmem_alloc(&m.tmem_slot, 128 * kT);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -881,6 +885,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
             for (int j = max(n - 4, 0); j < n; ++j) mbar_wait(&m.x_full[j & 3], (j >> 2) & 1, kDefaultMaxSpin);
         }
     } else if (warp == 1) {
+        constexpr uint32_t id = idesc_bf16_f32(128, 64 * kT, true, true);
         const uint32_t base_a = smem_u32(base);
         const uint64_t br0 = rows_desc(base_a), xw0 = rows_desc(base_a + L::kXw);
         for (int n = 0, i = 0, u = 0; n < items; ++n) {
@@ -889,7 +894,10 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
                 break;
             tc_fence_after();
             if (lane == 0) {
-                issue_state(tmem + 64 * u, step_desc(br0, (i & 1) * kT * kTile), step_desc(xw0, (n & 1) * 2 * kTile), i == 0);
+                const uint64_t bt = step_desc(br0, (i & 1) * kT * kTile), xw = step_desc(xw0, (n & 1) * 2 * kTile);
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k)
+                    mma_bf16(tmem + 64 * kT * u, step_desc(xw, k * 2048), step_desc(bt, k * 2048), id, i > 0 || k > 0);
                 mma_commit(&m.xw_empty[n & 1]);
                 if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
@@ -961,23 +969,35 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
                 mbar_arrive(&m.dt_empty[slot]);
             }
         }
-        if (grp == 0 && ok && (pl.nc == 0 || (ok = warp_wait(&m.drain, 0, max_spin)))) {
+        // The state of unit u: value part (lanes p) plus remainder part (lanes 64 + p), one
+        // state row per column. The upper lane quarters hand theirs over through shared
+        // memory (the operand tiles are free by then), 32 state rows at a time and group.
+        ok = pl.nc == 0 || (ok && warp_wait(&m.drain, 0, max_spin));
+        ok = named_bar_and(1, 512, ok);
+        if (ok) {
             tc_fence_after();
+            const uint32_t lanes = (uint32_t)(32 * q) << 16;
+            float* stage = reinterpret_cast<float*>(base) + grp * 32 * 64;       // [32 state rows][64 values]
             for (int u = 0; u < nu; ++u) {
                 const int64_t bh = (int64_t)pl.b * a.H + pl.head(a, un, u);
-                const int p0 = pl.col0(un, u), np = min(64, a.P - p0);
-                float* r = a.seeds + (bh * a.nseg + pl.seg) * head_state + (int64_t)row * a.P + p0;
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + 64 * u + c, v);
+                const int p0 = pl.col0(un, u), p = 32 * (q & 1) + lane;
+                float* to = a.seeds + (bh * a.nseg + pl.seg) * head_state + p0 + p;
+                for (int s0 = 32 * grp; s0 < 64 * kT; s0 += 128) {               // a group: 32 state rows of 128
+                    uint32_t v[2][16];
+                    tmem_ld16(tmem + lanes + 64 * kT * u + s0, v[0]);
+                    tmem_ld16(tmem + lanes + 64 * kT * u + s0 + 16, v[1]);
                     tmem_ld_wait();
-                    if (row >= a.S) continue;
+                    if (q >= 2)
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4)
-                        if (c + k < np)
-                            *reinterpret_cast<uint4*>(r + c + k) =
-                                pl.nc > 0 ? make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]) : make_uint4(0, 0, 0, 0);
+                        for (int k = 0; k < 32; ++k) stage[k * 64 + p] = __uint_as_float(v[k >> 4][k & 15]);
+                    named_bar(2 + grp, 128);
+                    if (q < 2 && p0 + p < a.P)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (s0 + k < a.S)
+                                to[(int64_t)(s0 + k) * a.P] =
+                                    pl.nc > 0 ? __uint_as_float(v[k >> 4][k & 15]) + stage[k * 64 + p] : 0.f;
+                    named_bar(2 + grp, 128);
                 }
             }
         }
@@ -986,7 +1006,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 128);
+    if (warp == 1) tmem_dealloc(tmem, 128 * kT);
 }
 
 // Rows [B, N, outer, inner] of bf16 as a 4-D map with boxes of 64 values x 128 tokens;
@@ -1006,28 +1026,39 @@ bool encode_rows(CUtensorMap* map, const void* p, int inner, int outer, int N, i
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-Units units_of(int H, int G, int P) {
+Units units_of(int H, int G, int P, int per) {
     Units un = {};
     un.blocks = (P + 63) / 64;
     un.units = (G > 0 ? H / G : H) * un.blocks;
-    un.pairs = (un.units + 1) / 2;
+    un.per = per;
+    un.ctas = (un.units + per - 1) / per;
     return un;
 }
 
-// CTAs run in waves over the SMs, so the number of segments is the one whose
-// waves times chunks is least. In units of one chunk of the main pass: a CTA
-// spends about two on starting and ending, the first pass 0.4 per chunk, two
-// further launches about two, and chaining the segments' states 0.2 per segment.
-int pick_segments(int64_t ctas, int N) {
+// How the work is cut: two units per CTA share (1) and the loads of B and C, one
+// spreads few heads over more SMs; segments spread long sequences. CTAs run in
+// waves over the SMs, so the cut is the one whose waves times chunks is least. In
+// units of one chunk of two units (about 5 us): a chunk of one unit 0.65, starting
+// and ending a CTA 1.3, the first pass 0.35 per chunk, and with segments two
+// further launches and the chaining 1 + 0.1 per segment.
+struct Cut {
+    int per, nseg;
+};
+Cut pick_cut(int64_t groups, int units, int N) {
     const int nch = (N + kC - 1) / kC, sms = sm_count();
-    int best = 1;
+    Cut best = {2, 1};
     double least = 1e30;
-    for (int n = 1; n <= 64 && n <= nch; ++n) {
-        const int cps = (nch + n - 1) / n;
-        if ((nch + cps - 1) / cps != n) continue;      // the same split with empty segments
-        const double waves = (double)((ctas * n + sms - 1) / sms);
-        const double cost = waves * (cps + 2.0) + (n > 1 ? waves * (0.4 * cps + 1.5) + 2.0 + 0.2 * n : 0.0);
-        if (cost < least) least = cost, best = n;
+    for (int per = 2; per >= 1; --per) {
+        const int64_t ctas = groups * ((units + per - 1) / per);
+        const double chunk = per == 2 && units > 1 ? 1.0 : 0.65;
+        for (int n = 1; n <= 64 && n <= nch; ++n) {
+            const int cps = (nch + n - 1) / n;
+            if ((nch + cps - 1) / cps != n) continue;      // the same split with empty segments
+            const double waves = (double)((ctas * n + sms - 1) / sms);
+            const double cost = waves * (cps * chunk + 1.3) +
+                                (n > 1 ? waves * (0.35 * cps * chunk + 1.0) + 1.0 + 0.1 * n : 0.0);
+            if (cost < least) least = cost, best = {per, n};
+        }
     }
     return best;
 }
@@ -1038,7 +1069,7 @@ cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorM
     static std::atomic<int> optin[kMaxDevices], optin_sums[kMaxDevices];
     cudaError_t e = ensure_smem_optin(scan_tc_kernel<kT, kGated>, (int)Smem<kT>::kBytes, optin);
     if (e != cudaSuccess) return e;
-    const dim3 grid(un.pairs * a.G, a.nseg, B);
+    const dim3 grid(un.ctas * a.G, a.nseg, B);
     if (a.nseg > 1) {
         e = ensure_smem_optin(scan_sums_kernel<kT>, (int)SumSmem<kT>::kBytes, optin_sums);
         if (e != cudaSuccess) return e;
@@ -1068,12 +1099,12 @@ bool tc_supported(const ScanArgs& a, int B, la_dtype dt) {
 }
 
 int tc_segments(int64_t B, int H, int G, int N, int P) {
-    const Units un = units_of(H, G, P);
-    return pick_segments(B * G * un.pairs, N);
+    return pick_cut(B * G, units_of(H, G, P, 1).units, N).nseg;
 }
 
 cudaError_t tc_scan(ScanArgs& a, int B, void* ws_header, cudaStream_t st) {
-    Units un = units_of(a.H, a.G, a.P);
+    Units un = units_of(a.H, a.G, a.P, 1);
+    un = units_of(a.H, a.G, a.P, pick_cut((int64_t)B * a.G, un.units, a.N).per);
     const int nch = (a.N + kC - 1) / kC;
     un.cps = (nch + a.nseg - 1) / a.nseg;
     un.gate_vec = a.z && (reinterpret_cast<uintptr_t>(a.z) & 15) == 0 &&
