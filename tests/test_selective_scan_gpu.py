@@ -249,3 +249,91 @@ def test_withheld_loads_time_out_and_the_context_survives(la, N, H):
     assert la.la_query_status(ws) == la.LA_OK
     if N < 1000:
         check(y, S_out, oracle(p), N, 128, "bf16")
+
+
+MANY = [
+    # B, N, H, G, S, P: enough units for two per CTA
+    (1, 140, 304, 1, 64, 16),
+    (1, 300, 303, 1, 64, 64),          # the last CTA has one unit
+    (2, 129, 152, 2, 128, 128),        # both units of a CTA belong to one head
+    (1, 700, 306, 2, 16, 8),           # odd unit counts per group
+]
+
+
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("shape", MANY)
+def test_many_heads_match_oracle(la, shape, gate):
+    B, N, H, G, S, P = shape
+    p = problem(B, N, H, G, S, P, "bf16", N + H)
+    if not gate:
+        p["z"] = None
+    S_out = torch.empty(B, H, S, P, device="cuda")
+    y = la.la_selective_scan_fwd(**p, S_out=S_out)
+    torch.cuda.synchronize()
+    check(y, S_out, oracle(p), N, S, "bf16")
+
+
+def test_many_heads_ragged(la):
+    n = [260, 0, 129]
+    B, N, H, S, P = len(n), 300, 104, 64, 64
+    p = problem(B, N, H, 1, S, P, "bf16", 14)
+    for b in range(B):
+        for k in ("x", "Bm", "Cm", "step", "z"):
+            p[k][b, n[b]:] = float("inf")
+    y = torch.full((B, N, H, P), 5.0, dtype=torch.bfloat16, device="cuda")
+    state = p["S0"].clone()
+    la.la_selective_scan_fwd(**dict(p, S0=state), lengths=torch.tensor(n, dtype=torch.int32, device="cuda"),
+                             S_out=state, y=y)
+    torch.cuda.synchronize()
+    for b in range(B):
+        assert (y[b, n[b]:] == 5).all(), b
+        q = {k: (v[b:b + 1, :n[b]] if k in ("x", "Bm", "Cm", "step", "z") else v) for k, v in p.items()}
+        q["S0"] = p["S0"][b:b + 1]
+        check(y[b:b + 1, :n[b]], state[b:b + 1], oracle(q), max(n[b], 1), S, "bf16")
+    assert torch.equal(state[1], p["S0"][1])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_segments_equal_pieces(la, dt):
+    # A sequence long enough to be cut into segments against the same sequence in two
+    # calls through the state: both within the bounds of their own sums.
+    p = problem(1, 2600, 8, 1, 64, 64, dt, 15, small=True)
+    S_out = torch.empty(1, 8, 64, 64, device="cuda")
+    y = la.la_selective_scan_fwd(**p, S_out=S_out)
+    state, outs = p["S0"].clone(), []
+    for a, b in ((0, 1001), (1001, 2600)):
+        q = {k: (v[:, a:b] if k in ("x", "Bm", "Cm", "step", "z") else v) for k, v in p.items()}
+        outs.append(la.la_selective_scan_fwd(**dict(q, S0=state), S_out=state))
+    torch.cuda.synchronize()
+    ref = oracle(p)
+    check(y, S_out, ref, 2600, 64, dt)
+    check(torch.cat(outs, 1), state, ref, 2600, 64, dt)
+
+
+def test_two_calls_on_two_streams(la):
+    # Two calls in flight at once, each with its own workspace, equal the calls alone.
+    ps = [problem(1, 1500, 4, 1, 128, 64, "bf16", s) for s in (16, 17)]
+    alone = [la.la_selective_scan_fwd(**p) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    outs = [la.la_selective_scan_fwd(**p, stream=s) for p, s in zip(ps, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, outs):
+        assert torch.equal(a, b)
+
+
+def test_shared_batch_inputs(la):
+    # B and C expanded over the batch (stride 0) and a batch that is a slice of a larger one.
+    p = problem(3, 70, 4, 1, 64, 64, "bf16", 18)
+    p["Bm"], p["Cm"] = (p[k][:1].expand(3, -1, -1, -1) for k in ("Bm", "Cm"))
+    S_out = torch.empty(3, 4, 64, 64, device="cuda")
+    y = la.la_selective_scan_fwd(**p, S_out=S_out)
+    torch.cuda.synchronize()
+    check(y, S_out, oracle(p), 70, 64, "bf16")
+    q = problem(4, 150, 2, 1, 128, 64, "bf16", 19)
+    q = {k: (v[::2, 10:140] if k in ("x", "Bm", "Cm", "step", "z") else v[::2].contiguous() if k == "S0" else v)
+         for k, v in q.items()}
+    S_out = torch.empty(2, 2, 128, 64, device="cuda")
+    y = la.la_selective_scan_fwd(**q, S_out=S_out)
+    torch.cuda.synchronize()
+    check(y, S_out, oracle(q), 130, 128, "bf16")
