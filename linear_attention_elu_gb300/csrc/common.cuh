@@ -40,16 +40,6 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
     return __float2bfloat16_rn(x);
 }
 
-// v sigmoid(v) = v / (1 + e^-v) in fp32: hardware exponential and reciprocal (a few
-// 2^-23 relative for |v| of order 1, |v| 2^-24 in the exponent beyond). e^-v overflows
-// to infinity below -88.7, and its reciprocal is then 0: the limit.
-__device__ __forceinline__ float silu(float v) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return v * r;
-}
-
 // Workspace header (first 256 bytes of every workspace).
 struct WsHeader {
     uint32_t status;     // 0 = ok, else an la_status code set by a kernel

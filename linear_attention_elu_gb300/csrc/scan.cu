@@ -29,6 +29,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mixing.cuh"
 #include "scan.cuh"
 #include "tc_common.cuh"
 

@@ -22,22 +22,27 @@
 // score; the weights of (4) come from sums taken from the chunk's end, so that a
 // small exponent is not a difference of two large ones.
 //
-// Schedule (20 warps, one CTA per SM). An item is one chunk of one unit. Sixteen
-// warps share every step of an item, a warp owning 32 rows x 16 columns (32 x 32
-// of the scores): state to bf16 and scaled, output of the item before, weighted
-// values, scores to P. They run the same code at the same time: an earlier form
-// with a warpgroup per step spent 8,000 cycles an item against 3,000, each role
-// waiting on its own instruction fetches and hand-offs. One thread then issues
-// (2), (3), (4) of the item (and (1) of the next chunk), which run under the next
-// item's steps. Four more warps: TMA loads, MMA issue, step sizes to decays, and
-// the output slots (gate in, output in place, TMA store). All hand-offs are
-// mbarriers; every wait is bounded. Sequences are cut into segments when there are
-// too few units for the SMs: the first pass streams (4) alone, in reverse order of
-// chunks so that the weights reach to the segment's end and nothing has to be
-// rescaled; seeds are chained by csrc/scan.cu and the second pass starts from them.
-// What bounds it: shared memory. Operands of the products (196 KB an item, their A
-// tiles once per 64 columns), TMA and the steps move some 400 KB per item at 128
-// bytes a cycle, against 49 KB of HBM traffic.
+// Schedule (20 warps, one CTA per SM). An item is one chunk of one unit. Two groups
+// of eight warps alternate items; a warp owns 32 rows and half of the columns. A
+// group prepares its item (scores to P, state to bf16 and scaled, weighted values),
+// hands it over, and writes its output while the other group prepares the next. One
+// thread issues (2), (3), (4) of an item, and (1) of the next chunk, which run under
+// the groups' steps. The other warps: TMA loads, step sizes to decays, and the output
+// slots (gate in, output in place, TMA store). All hand-offs are mbarriers; every wait
+// is bounded. Loops over columns are kept rolled: the steps' code competes for the
+// instruction cache (the output step unrolled twice cost 6 % of the call).
+// Measured on B=1 N=65536 H=32 P=64 S=128 with a gate, 126 us of HBM time: a form with
+// one warpgroup per step ran 470 us, all sixteen warps on one item 312, two groups 294.
+// A second issuing thread, the products issued by predicate instead of by branch, and
+// x kept in registers from the weights to the output all measured slower.
+// Sequences are cut into segments when there are too few units for the SMs: the first
+// pass streams (4) alone, in reverse order of chunks so that the weights reach to the
+// segment's end and nothing has to be rescaled (99 us of the call); seeds are chained by
+// csrc/scan.cu (12 us) and the second pass starts from them.
+// What bounds it: the groups' instructions (about 9,700 a warp-item of 128 tokens x 64
+// values, 42 % of the issue slots, each warp waiting on its own chain of TMEM reads,
+// exponentials and hand-offs) next to the products' operand reads from shared memory
+// (196 KB an item at 128 bytes a cycle).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -46,6 +51,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mixing.cuh"
 #include "scan.cuh"
 #include "tc_common.cuh"
 #include "tc_util.cuh"

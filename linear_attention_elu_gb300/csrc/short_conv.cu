@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mixing.cuh"
 #include "tc_common.cuh"
 
 namespace la {
