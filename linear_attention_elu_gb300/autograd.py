@@ -6,6 +6,9 @@ run in the library's kernels).
     o.backward(g)                                   # la_causal_bwd fills q.grad, k.grad, v.grad
     qo, ko = qk_norm_rope(q, k, pos, table, wq, wk) # q: [B,N,Hq,D], k: [B,N,Hk,D], head-major out
 
+Either of q and k of qk_norm_rope may be None. A training step captured into a CUDA
+graph calls the library's backward entries (la_*_bwd) itself.
+
 The attention backward takes Dk, Dv <= 64 (the library refuses wider heads with
 LA_ERR_UNSUPPORTED). Gradients have the inputs' dtype.
 """
@@ -52,8 +55,10 @@ class _QkNormRope(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dqo, dko):
         q, k, pos, table, wq, wk = ctx.saved_tensors
-        dq, dk, dwq, dwk = la_qk_norm_rope_bwd(q, k, dqo.contiguous(), dko.contiguous(), pos, table,
-                                               wq=wq, wk=wk, **ctx.how)
+        # A side that was not given has no gradient (one whose output was not used gets zeros).
+        dqo = None if q is None else dqo.contiguous()
+        dko = None if k is None else dko.contiguous()
+        dq, dk, dwq, dwk = la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, wq=wq, wk=wk, **ctx.how)
         return (dq, dk, None, None, dwq.to(wq.dtype) if wq is not None else None,
                 dwk.to(wk.dtype) if wk is not None else None, None, None, None)
 

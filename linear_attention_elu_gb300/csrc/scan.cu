@@ -88,6 +88,23 @@ __device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[kPairs]
     }
 }
 
+// kW adjacent values at p (8- or 16-byte aligned).
+template <int kW>
+__device__ __forceinline__ void load_values(const float* p, float (&v)[kW]) {
+    if constexpr (kW == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(p);
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else {
+        const float2 t = *reinterpret_cast<const float2*>(p);
+        v[0] = t.x, v[1] = t.y;
+    }
+}
+
+// Columns per lane: four share each row's B and C; two for heads of at most 8
+// columns, which would leave half of the lanes idle, and for states of more than 64
+// rows, whose lanes would hold 48 to 64 values (254 registers with 16 rows).
+int lane_columns(int S, int P) { return S > 64 || P <= 8 ? 2 : 4; }
+
 // Grid: (segments, B H). Block: one warp per 4 kW columns of the head.
 // kState: only the segment's end state from zero and its decay (first pass).
 template <typename T, int R, int kW, bool kState>
@@ -219,7 +236,8 @@ __global__ void __launch_bounds__(32 * kMaxDim / (4 * kW)) scan_kernel(const __g
                 for (int t = 0; t < 8; ++t) {
                     const int tt = half + t;
                     const float w = fac.w[tt];
-                    const float* xv = xs + tt * cols + col;
+                    float xv[kW];
+                    load_values<kW>(xs + tt * cols + col, xv);
                     uint64_t bb[kP];
                     load_pairs<kP>(bs + tt * kRow + rg * kG, bb);
 #pragma unroll
@@ -237,7 +255,8 @@ __global__ void __launch_bounds__(32 * kMaxDim / (4 * kW)) scan_kernel(const __g
                 for (int t = 0; t < 8; ++t) {
                     const int tt = half + t;
                     const float w = fac.w[tt];
-                    const float* xv = xs + tt * cols + col;
+                    float xv[kW];
+                    load_values<kW>(xs + tt * cols + col, xv);
                     if (plain) {
                         const float at = fac.a[tt];
                         const uint64_t a2 = pk(at, at);
@@ -253,11 +272,11 @@ __global__ void __launch_bounds__(32 * kMaxDim / (4 * kW)) scan_kernel(const __g
                     for (int c = 0; c < kW; ++c) {
                         const float v = w * xv[c];
                         const uint64_t x2 = pk(v, v);
-                        uint64_t y2 = 0;
+                        uint64_t y2;
 #pragma unroll
                         for (int i = 0; i < kP; ++i) {
                             s[c][i] = fma2(bb[i], x2, s[c][i]);
-                            y2 = fma2(cc[i], s[c][i], y2);
+                            y2 = i == 0 ? mul2(cc[0], s[c][0]) : fma2(cc[i], s[c][i], y2);
                         }
                         acc[t][c] = sum2(y2);
                     }
@@ -441,13 +460,10 @@ cudaError_t recurrence(const ScanArgs& a, int64_t BH, cudaStream_t st) {
     return launch_after(scan_kernel<T, R, kW, false>, grid, 32 * warps, smem, st, a.nseg > 1, a);
 }
 
-// Four columns per lane share each row's B and C. Two for heads of at most 8
-// columns, which would leave half of the lanes idle, and for states of more than 64
-// rows, whose lanes would hold 48 to 64 values (254 registers with 16 rows).
 template <typename T, int R>
 cudaError_t recurrence_by_width(const ScanArgs& a, int64_t BH, cudaStream_t st) {
     if constexpr (R <= 8)
-        if (a.P > 8) return recurrence<T, R, 4>(a, BH, st);
+        if (lane_columns(a.S, a.P) == 4) return recurrence<T, R, 4>(a, BH, st);
     return recurrence<T, R, 2>(a, BH, st);
 }
 
@@ -486,10 +502,14 @@ bool bad4(const void* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
 
 namespace scan {
 
-// Segments of the recurrence: one while there are three blocks per SM or fewer
-// than two stretches of 64 tokens; else as many as fill three blocks per SM.
-int recurrence_segments(int64_t BH, int N) {
-    const int64_t want = 3 * (int64_t)tcc::sm_count() / (BH > 0 ? BH : 1);
+// Segments of the recurrence: one while there are twelve warps per SM or fewer than
+// two stretches of 64 tokens; else as many as give each SM twelve warps in whole
+// blocks (B=2 N=4000 H=8 P=64: S=64, three blocks of four warps 78 us, two 98, four
+// 93; S=128, two blocks of eight warps 143, three 157). Segments of whole tiles left
+// the SMs unevenly loaded (95 us).
+int recurrence_segments(int64_t BH, int N, int S, int P) {
+    const int columns = 4 * lane_columns(S, P), warps = (P + columns - 1) / columns;
+    const int64_t want = (int64_t)((12 + warps - 1) / warps) * tcc::sm_count() / (BH > 0 ? BH : 1);
     const int64_t most = N / 64;
     int64_t n = want < most ? want : most;
     n = n < kMaxSegments ? n : kMaxSegments;
@@ -512,7 +532,7 @@ bool tc_widths(int S, int P, la_dtype dt) { return dt == LA_BF16 && S % 8 == 0 &
 // every number of groups, on which the tensor-core path's segments depend.
 size_t scan_workspace(int B, int H, int N, int S, int P, la_dtype dt) {
     const int64_t BH = (int64_t)B * H;
-    int n = recurrence_segments(BH, N);
+    int n = recurrence_segments(BH, N, S, P);
     if (tc_widths(S, P, dt))
         for (int g = 1; (int64_t)g * g <= H; ++g) {
             if (H % g) continue;
@@ -524,7 +544,7 @@ size_t scan_workspace(int B, int H, int N, int S, int P, la_dtype dt) {
 }
 
 int scan_launches(int B, int H, int N, int S, int P, la_dtype dt) {
-    const int n = tc_widths(S, P, dt) ? tc_segments(B, H, 1, N, P) : recurrence_segments((int64_t)B * H, N);
+    const int n = tc_widths(S, P, dt) ? tc_segments(B, H, 1, N, P) : recurrence_segments((int64_t)B * H, N, S, P);
     return n > 1 ? 3 : 1;
 }
 
@@ -575,8 +595,8 @@ la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token,
     a.A = A, a.D = D, a.step_bias = step_bias, a.lengths = lengths, a.S0 = S0, a.S_out = S_out;
     a.N = N, a.H = H, a.G = G, a.S = S, a.P = P, a.softplus = softplus ? 1 : 0;
     const bool tc = la::scan::tc_supported(a, B, dt);
-    a.nseg = tc ? la::scan::tc_segments(B, H, G, N, P) : la::scan::recurrence_segments(BH, N);
-    a.seg_len = (N + a.nseg - 1) / a.nseg;
+    a.nseg = tc ? la::scan::tc_segments(B, H, G, N, P) : la::scan::recurrence_segments(BH, N, S, P);
+    a.seg_len = (N + a.nseg - 1) / a.nseg;                 // of the recurrence
     const size_t need = sizeof(la::WsHeader) +
                         (a.nseg > 1 ? (size_t)BH * a.nseg * ((size_t)S * P + 1) * sizeof(float) : 0);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)

@@ -73,7 +73,7 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-int recurrence_segments(int64_t BH, int N);
+int recurrence_segments(int64_t BH, int N, int S, int P);
 cudaError_t launch_seeds(const ScanArgs& a, int64_t BH, cudaStream_t st);
 
 }  // namespace scan

@@ -186,3 +186,28 @@ def test_autograd_feeds_linear_attention(la):
     assert torch.allclose(proj.grad, ref, rtol=1e-4, atol=1e-5)
     assert torch.allclose(wq.grad, dwq, rtol=1e-4, atol=1e-4)
     assert torch.allclose(wk.grad, dwk, rtol=1e-4, atol=1e-4)
+
+
+@pytest.mark.parametrize("given", ["q", "k", "unused"])
+def test_autograd_of_one_side(la, given):
+    # One side alone, and both with only one output used.
+    from linear_attention_elu_gb300.autograd import qk_norm_rope
+    q, k, pos, f, ax, wq, wk, _ = problem(2, 9, 4, 2, 64, 32, 1, "f32", 9)
+    table, pos = la.la_rope_table(f, ax), pos.cuda()
+    q, k, wq, wk = (t.clone().requires_grad_() for t in (q, k, wq, wk))
+    if given == "q":
+        qo, ko = qk_norm_rope(q, None, pos, table, wq)
+        assert ko is None
+    elif given == "k":
+        qo, ko = qk_norm_rope(None, k, pos, table, None, wk)
+        assert qo is None
+    else:
+        qo, ko = qk_norm_rope(q, k, pos, table, wq, wk)
+    out, x, w = (ko, k, wk) if given == "k" else (qo, q, wq)
+    go = torch.randn_like(out)
+    out.backward(go)
+    rx, rw = tm.norm_rope_bwd(to_f64(x), to_f64(w), to_f64(go), pos.cpu().numpy(), f, ax)
+    assert np.allclose(to_f64(x.grad), rx, rtol=0, atol=2.0 ** -18 * np.abs(rx).max())
+    assert np.allclose(to_f64(w.grad), rw, rtol=0, atol=2.0 ** -16 * np.abs(rw).max())
+    if given == "unused":
+        assert (k.grad == 0).all() and (wk.grad == 0).all()
