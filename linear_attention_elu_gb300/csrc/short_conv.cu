@@ -4,12 +4,13 @@
 // rows) and for single tokens (the state shifted in place).
 //
 // What bounds it: each value is read once and written once, W multiply-adds and
-// one silu each: HBM bandwidth. A thread owns one 16-byte piece of a row (8 bf16
-// or 4 fp32 channels) and walks kTok consecutive tokens with the last W - 1 rows
-// in registers, so a row is read again only by the neighbouring thread of the
-// next token group (W - 1 rows in kTok, from L2). Channels that are not whole
-// 16-byte pieces, or rows that are not aligned, run the same kernel one channel
-// per thread. Sums are fp32.
+// one silu each: HBM bandwidth, with the silus' exponentials and reciprocals close
+// behind (142 M of them in 31 us at B=4 N=4096 C=4352). A thread owns one 16-byte
+// piece of a row (8 bf16 or 4 fp32 channels) and walks consecutive tokens with the
+// last W - 1 rows in registers, so a row is read again only by the neighbouring
+// thread of the next token group (W - 1 rows in 64 at best, from L2). Channels that are not
+// whole 16-byte pieces, or rows that are not aligned, take one channel per thread.
+// Sums are fp32.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -96,9 +97,100 @@ __device__ __forceinline__ void emit(const float (&w)[kW][kV], const float (&bia
     store_v<T, kV>(out, y);
 }
 
+// Input row t of sequence b, or row t + W - 1 of the state before the first token.
 template <typename T, int kV, int kW>
-__global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(const __grid_constant__ ConvArgs a) {
+__device__ __forceinline__ void input_row(const ConvArgs& a, const T* x, int b, int c0, int t, float (&f)[kV]) {
+    if (t >= 0) {
+        load_v<T, kV>(x + t * a.x_ts, f);
+    } else if (a.s0) {
+        load_v<T, kV>(static_cast<const T*>(a.s0) + ((int64_t)b * (kW - 1) + t + kW - 1) * a.C + c0, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) f[j] = 0.f;
+    }
+}
+
+// The last W - 1 of n rows (and of the state before them) to the state after.
+template <typename T, int kV, int kW>
+__device__ __forceinline__ void write_state(const ConvArgs& a, const T* x, int b, int c0, int n) {
+    T* s1 = static_cast<T*>(a.s1) + (int64_t)b * (kW - 1) * a.C + c0;
+#pragma unroll
+    for (int k = 0; k < kW - 1; ++k) {
+        float f[kV];
+        input_row<T, kV, kW>(a, x, b, c0, n - (kW - 1) + k, f);
+        store_v<T, kV>(s1 + (int64_t)k * a.C, f);
+    }
+}
+
+// Any channel count and alignment: one channel per thread.
+template <typename T, int kW>
+__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs a) {
     constexpr int kAhead = 4;                              // rows in flight
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t bg = id / a.C;
+    const int c0 = (int)(id - bg * a.C);
+    const int b = (int)(bg / a.groups), g = (int)(bg - (int64_t)b * a.groups);
+    if (b >= a.B) return;
+    const int n = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
+    const T* x = static_cast<const T*>(a.x) + b * a.x_bs + c0;
+    if (g == 0 && a.s1) write_state<T, 1, kW>(a, x, b, c0, n);
+    const int t0 = g * a.tok, t1 = min(t0 + a.tok, n);
+    if (t0 >= t1) return;
+    float w[kW][1], bias[1] = {}, win[kW - 1][1];
+    load_weights<T, 1, kW>(static_cast<const T*>(a.w), c0, w);
+    if (a.bias) load_v<T, 1>(static_cast<const T*>(a.bias) + c0, bias);
+#pragma unroll
+    for (int k = 0; k < kW - 1; ++k) input_row<T, 1, kW>(a, x, b, c0, t0 - (kW - 1) + k, win[k]);
+    T* y = static_cast<T*>(a.y) + b * a.y_bs + c0;
+    for (int t = t0; t < t1; t += kAhead) {
+        float v[kAhead][1];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (t + u < t1) load_v<T, 1>(x + (t + u) * a.x_ts, v[u]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (t + u >= t1) break;
+            emit<T, 1, kW>(w, bias, win, v[u], a.silu, y + (t + u) * a.y_ts);
+#pragma unroll
+            for (int k = 0; k + 1 < kW - 1; ++k) win[k][0] = win[k + 1][0];
+            win[kW - 2][0] = v[u][0];
+        }
+    }
+}
+
+// Packed fp32 pairs: one instruction for two channels.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t a, float* lo, float* hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(a));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Rows of whole 16-byte pieces. The rows ahead are in flight in shared memory: every
+// thread copies its own pieces asynchronously into a ring of its own, so that no
+// barrier stands between the copies and their use. Two blocks per SM and rings of
+// three groups of four rows (B=4 N=4096 C=4352 bf16: 56 us; rows ahead in registers
+// instead 72, three groups of two rows 60, four of six 60; three blocks per SM, which
+// spill, 92). Two channels per instruction, as packed pairs, took 3 of the 59 us.
+constexpr int kRows = 4, kRing = 3;                    // rows per group, groups in the ring
+constexpr int kRingBytes = kRows * kRing * kThreads * 16;
+static_assert(kRingBytes <= 48 * 1024, "within the shared memory of a launch without an attribute");
+
+template <typename T, int kV, int kW>
+__global__ void __launch_bounds__(kThreads, 2) conv_ring_kernel(const __grid_constant__ ConvArgs a) {
+    constexpr int kP = kV / 2;
+    extern __shared__ uint4 ring[];                        // [kRing kRows][threads]
     const int pieces = a.C / kV;
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t bg = id / pieces;
@@ -107,51 +199,72 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(const __grid_cons
     if (b >= a.B) return;
     const int n = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
     const T* x = static_cast<const T*>(a.x) + b * a.x_bs + c0;
-    const T* s0 = a.s0 ? static_cast<const T*>(a.s0) + (int64_t)b * (kW - 1) * a.C + c0 : nullptr;
-    // Input row t, or row t + W - 1 of the state for t < 0.
-    auto row = [&](int t, float (&f)[kV]) {
-        if (t >= 0) {
-            load_v<T, kV>(x + t * a.x_ts, f);
-        } else if (s0) {
-            load_v<T, kV>(s0 + (int64_t)(t + kW - 1) * a.C, f);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kV; ++j) f[j] = 0.f;
-        }
-    };
-    if (g == 0 && a.s1) {                                  // the last W - 1 rows
-        T* s1 = static_cast<T*>(a.s1) + (int64_t)b * (kW - 1) * a.C + c0;
-#pragma unroll
-        for (int k = 0; k < kW - 1; ++k) {
-            float f[kV];
-            row(n - (kW - 1) + k, f);
-            store_v<T, kV>(s1 + (int64_t)k * a.C, f);
-        }
-    }
+    if (g == 0 && a.s1) write_state<T, kV, kW>(a, x, b, c0, n);
     const int t0 = g * a.tok, t1 = min(t0 + a.tok, n);
     if (t0 >= t1) return;
-    float w[kW][kV], bias[kV] = {}, win[kW - 1][kV];
-    load_weights<T, kV, kW>(static_cast<const T*>(a.w), c0, w);
-    if (a.bias) load_v<T, kV>(static_cast<const T*>(a.bias) + c0, bias);
+    const uint32_t slot = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
+    const T* xa = x + (int64_t)t0 * a.x_ts;
+    int left = t1 - t0;                                    // rows not yet fetched
+    auto fetch = [&](int q) {                              // the next rows into group q
 #pragma unroll
-    for (int k = 0; k < kW - 1; ++k) row(t0 - (kW - 1) + k, win[k]);
-    T* y = static_cast<T*>(a.y) + b * a.y_bs + c0;
-    for (int t = t0; t < t1; t += kAhead) {
-        float v[kAhead][kV];
+        for (int u = 0; u < kRows; ++u) {
+            if (u < left) copy16(slot + (q * kRows + u) * kThreads * 16, xa);
+            xa += a.x_ts;
+        }
+        left -= kRows;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (t + u < t1) load_v<T, kV>(x + (t + u) * a.x_ts, v[u]);
+    for (int q = 0; q < kRing - 1; ++q) fetch(q);
+    uint64_t w[kW][kP], bias[kP], win[kW - 1][kP];
+    {
+        float f[kW][kV], e[kV] = {};
+        load_weights<T, kV, kW>(static_cast<const T*>(a.w), c0, f);
+        if (a.bias) load_v<T, kV>(static_cast<const T*>(a.bias) + c0, e);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int j = 0; j < kP; ++j) {
+            bias[j] = pair_of(e[2 * j], e[2 * j + 1]);
+#pragma unroll
+            for (int k = 0; k < kW; ++k) w[k][j] = pair_of(f[k][2 * j], f[k][2 * j + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < kW - 1; ++k) {
+            input_row<T, kV, kW>(a, x, b, c0, t0 - (kW - 1) + k, e);
+#pragma unroll
+            for (int j = 0; j < kP; ++j) win[k][j] = pair_of(e[2 * j], e[2 * j + 1]);
+        }
+    }
+    T* y = static_cast<T*>(a.y) + b * a.y_bs + (int64_t)t0 * a.y_ts + c0;
+    int q = 0;
+    for (int t = t0; t < t1; t += kRows) {
+        fetch(q == 0 ? kRing - 1 : q - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        const uint4* r = ring + q * kRows * kThreads + threadIdx.x;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
             if (t + u >= t1) break;
-            emit<T, kV, kW>(w, bias, win, v[u], a.silu, y + (t + u) * a.y_ts);
+            float v[kV];
+            load_v<T, kV>(reinterpret_cast<const T*>(r + u * kThreads), v);
 #pragma unroll
-            for (int j = 0; j < kV; ++j) {
+            for (int j = 0; j < kP; ++j) {
+                const uint64_t in = pair_of(v[2 * j], v[2 * j + 1]);
+                uint64_t s = bias[j];
+#pragma unroll
+                for (int k = 0; k < kW - 1; ++k) s = fma_pair(w[k][j], win[k][j], s);
+                s = fma_pair(w[kW - 1][j], in, s);
 #pragma unroll
                 for (int k = 0; k + 1 < kW - 1; ++k) win[k][j] = win[k + 1][j];
-                win[kW - 2][j] = v[u][j];
+                win[kW - 2][j] = in;
+                split(s, &v[2 * j], &v[2 * j + 1]);
             }
+            if (a.silu) {
+#pragma unroll
+                for (int j = 0; j < kV; ++j) v[j] = silu(v[j]);
+            }
+            store_v<T, kV>(y, v);
+            y += a.y_ts;
         }
+        q = q + 1 == kRing ? 0 : q + 1;
     }
 }
 
@@ -193,16 +306,20 @@ cudaError_t launch(ConvArgs& a, bool step, cudaStream_t st) {
         conv_step_kernel<T, kV, kW><<<(unsigned)blocks, kThreads, 0, st>>>(a);
         return cudaPeekAtLastError();
     }
-    // Tokens per thread: 64 (W - 1 rows in 64 are read again, the weights are loaded
-    // once; B=4 N=4096 C=4352 bf16: 70 us, with 16 tokens 78); fewer while that would
-    // leave SMs without four blocks each.
+    // Tokens per thread: 64 (W - 1 rows in 64 are read again, and the weights are loaded
+    // once), fewer while that would leave SMs without four blocks each. B=4 N=4096 C=4352
+    // bf16 takes 32: 56 us, 16 tokens 68; C=2304 N=3000 29, 96 tokens 33.
     a.tok = 64;
     while (a.tok > 4 && (int64_t)a.B * ((a.N + a.tok - 1) / a.tok) * pieces < 4LL * kThreads * tcc::sm_count())
         a.tok /= 2;
     a.groups = (a.N + a.tok - 1) / a.tok;
     const int64_t blocks = ((int64_t)a.B * a.groups * pieces + kThreads - 1) / kThreads;
     if (blocks > 2147483647LL) return cudaErrorInvalidValue;
-    conv_fwd_kernel<T, kV, kW><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    if constexpr (kV > 1) {
+        conv_ring_kernel<T, kV, kW><<<(unsigned)blocks, kThreads, kRingBytes, st>>>(a);
+    } else {
+        conv_fwd_kernel<T, kW><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    }
     return cudaPeekAtLastError();
 }
 
