@@ -108,6 +108,8 @@ la_status la_workspace_size(la_op op, int B, int H, int N, int Dk, int Dv, la_dt
  * Number of kernel launches one call of `op` makes for this shape and dtype
  * (host-only query; `launches` is a HOST pointer). Useful for stream and
  * graph planning and for counting launches in a timed region.
+ * LA_OP_SELECTIVE_SCAN: for one group and 16-byte aligned rows; a call with more
+ * groups or unaligned rows makes one launch or three by its own cut.
  */
 la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtype dt,
                           int* launches);

@@ -31,7 +31,8 @@ struct ScanArgs {
 // relative to themselves; e^-|v| is 2^t with the rounding of t = -|v| log2 e put back.
 __device__ __forceinline__ float step_size(float v, int softplus) {
     if (!softplus) return v;
-    constexpr float kL = 1.44269502162933349609375f, kLLo = 1.925963033500011e-8f;   // log2 e
+    constexpr double kLog2e = 1.44269504088896340736;
+    constexpr float kL = (float)kLog2e, kLLo = (float)(kLog2e - (double)kL);
     const float x = -fabsf(v), t = x * kL;
     const float r = fmaf(x, kL, -t) + x * kLLo;
     float e, q;
