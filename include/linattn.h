@@ -456,7 +456,7 @@ la_status la_qk_norm_rope_bwd(const void* q, int64_t q_batch, int64_t q_token, c
  *  - x: rows of [B, N, C] with batch stride x_batch and token stride x_token in
  *    elements (C adjacent values: a column range of a projection); y the same
  *    with its own strides (rows must not overlap); w [C, W], bias [C] (nullable),
- *    dtype dt, W in {2, 3, 4}. fp32 sums, one rounding.
+ *    dtype dt, W in {2, 3, 4}; B N <= 2^30. fp32 sums, one rounding.
  *  - state0 [B, W - 1, C] (nullable: zero): the inputs before the first token;
  *    state_out [B, W - 1, C] (nullable) receives the last W - 1 inputs. They must
  *    not overlap (LA_ERR_INVALID_ARG).
@@ -489,7 +489,7 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
  *    H P values of a token adjacent); step: rows of [B, N, H]; Bm, Cm: rows of
  *    [B, N, G, S]; all dtype dt, so that they can be column ranges of the
  *    projection and of la_short_conv_fwd's output. H a multiple of G; 1 <= S,
- *    P <= 128; B H <= 65535.
+ *    P <= 128; B H <= 65535; N <= 2^30.
  *  - A, D, step_bias: [H] float32; A is the (negative) rate itself. d_t A_h <= 0 is
  *    expected (the state must not grow); nothing checks it.
  *  - S0 [B, H, S, P] float32 (nullable: zero): state before the first token; S_out

@@ -157,6 +157,7 @@ la_status la_workspace_size(la_op op, int B, int H, int N, int Dk, int Dv, la_dt
     const bool one_token = op == LA_OP_DECODE || op == LA_OP_LAYER_DECODE;
     la_status s = check_common(B, H, one_token ? 1 : N, Dk, Dv, dt);
     if (s != LA_OK) return s;
+    if (op == LA_OP_SELECTIVE_SCAN && N > la::kScanMaxTokens) return LA_ERR_UNSUPPORTED;
     if (op == LA_OP_LAYER_DECODE) {
         if (Dk != Dv) return LA_ERR_UNSUPPORTED;
         *bytes = kHeaderBytes + round_up(body_bytes(op, B, H, 1, Dk, Dv, dt), 256);
@@ -183,6 +184,7 @@ la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtyp
     const bool one_token = op == LA_OP_DECODE || op == LA_OP_LAYER_DECODE;
     la_status s = check_common(B, H, one_token ? 1 : N, Dk, Dv, dt);
     if (s != LA_OK) return s;
+    if (op == LA_OP_SELECTIVE_SCAN && N > la::kScanMaxTokens) return LA_ERR_UNSUPPORTED;
     const int64_t BH = (int64_t)B * H;
     if (BH == 0 || (!one_token && N == 0)) {
         *launches = 0;

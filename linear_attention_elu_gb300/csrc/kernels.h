@@ -97,7 +97,9 @@ cudaError_t tc_bwd(const void* q, const void* k, const void* v, const void* dout
 // Layer decode step (csrc/layer.cu): workspace bytes after the header.
 size_t layer_workspace(int B, int H, int D, la_dtype dt);
 
-// Selective scan (csrc/scan.cu): workspace bytes after the header, launches.
+// Selective scan (csrc/scan.cu): the longest sequence (its roundings to chunks and
+// segments fit an int), workspace bytes after the header, launches.
+constexpr int kScanMaxTokens = 1 << 30;
 size_t scan_workspace(int B, int H, int N, int S, int P, la_dtype dt);
 int scan_launches(int B, int H, int N, int S, int P, la_dtype dt);
 

@@ -489,6 +489,7 @@ la_status check_shape(int B, int H, int G, int N, int S, int P, la_dtype dt) {
     if (H % G) return LA_ERR_INVALID_ARG;
     if (S > kMaxDim || P > kMaxDim) return LA_ERR_UNSUPPORTED;
     if ((int64_t)B * H > 65535) return LA_ERR_UNSUPPORTED;   // heads map to grid.y
+    if (N > kScanMaxTokens) return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }
 

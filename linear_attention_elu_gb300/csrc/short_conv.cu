@@ -343,7 +343,7 @@ la_status check(int B, int N, int C, int W, la_dtype dt) {
     if (B < 0 || N < 0 || C < 1 || W < 1) return LA_ERR_INVALID_ARG;
     if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_INVALID_ARG;
     if (W < 2 || W > 4) return LA_ERR_UNSUPPORTED;
-    if ((int64_t)B * N > (int64_t)1 << 31) return LA_ERR_UNSUPPORTED;
+    if ((int64_t)B * N > (int64_t)1 << 30) return LA_ERR_UNSUPPORTED;   // token counts and their roundings fit an int
     return LA_OK;
 }
 

@@ -191,3 +191,16 @@ def test_scan_wrappers_refuse_before_any_launch(la):
         la.la_selective_scan_fwd(x, step.bfloat16(), A, Bm, Bm)
     with pytest.raises(ValueError):
         la.la_selective_scan_step(x[:, 0], step[:, 0], A, Bm[:, 0], Bm[:, 0], None)
+
+
+def test_sequences_whose_roundings_pass_an_int(la):
+    far = (1 << 30) + 1
+    assert conv_fwd(la, B=1, N=far) == UNSUP
+    assert conv_fwd(la, B=1, N=2147483647, C=1) == UNSUP
+    for N in (far, 2147483647):
+        assert scan_fwd(la, B=1, N=N) == UNSUP
+        for dt in (la.LA_F32, la.LA_BF16):
+            with pytest.raises(la.LinAttnError):
+                la.la_workspace_size(la.LA_OP_SELECTIVE_SCAN, 1, 2, N, 64, 64, dt)
+            with pytest.raises(la.LinAttnError):
+                la.la_launch_count(la.LA_OP_SELECTIVE_SCAN, 1, 2, N, 64, 64, dt)
