@@ -16,11 +16,12 @@
 // Roundings. x, B, C enter as they are. P and the state of (2) are rounded to bf16
 // once each (2^-9 relative, as the output itself). The state is held in fp32 in
 // TMEM: it is scaled there per chunk, and (4) adds w x as two bf16 terms (value and
-// remainder), which leaves 2^-17 of each term. Decays of P below the diagonal
-// 32 x 32 blocks are products of two factors <= 1 around the block row's start,
-// e^{l_i - l_m} e^{l_m - l_j}, so only the diagonal blocks take an exponential per
-// score; the weights of (4) come from sums taken from the chunk's end, so that a
-// small exponent is not a difference of two large ones.
+// remainder), which leaves at most 2^-18 of each term (states 2e-6 off in all, relative
+// to their largest entry; a third term needs 16 KB of shared memory that are not there).
+// Decays of P below the diagonal 32 x 32 blocks are products of two factors <= 1 around
+// the block row's start, e^{l_i - l_m} e^{l_m - l_j}, so only the diagonal blocks take an
+// exponential per score; the weights of (4) come from sums taken from the chunk's end, so
+// that a small exponent is not a difference of two large ones.
 //
 // Schedule (20 warps, one CTA per SM). An item is one chunk of one unit. Two groups
 // of eight warps alternate items; a warp owns 32 rows and half of the columns. A
@@ -37,7 +38,7 @@
 // x kept in registers from the weights to the output all measured slower.
 // Sequences are cut into segments when there are too few units for the SMs: the first
 // pass streams (4) alone, in reverse order of chunks so that the weights reach to the
-// segment's end and nothing has to be rescaled (99 us of the call); seeds are chained by
+// segment's end and nothing has to be rescaled (97 us of the call); seeds are chained by
 // csrc/scan.cu (12 us) and the second pass starts from them.
 // What bounds it: the groups' instructions (about 9,700 a warp-item of 128 tokens x 64
 // values, 42 % of the issue slots, each warp waiting on its own chain of TMEM reads,
@@ -802,19 +803,21 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 // of operands per item instead of the main pass's 96 (which has no TMEM left for it).
 // Warps: TMA, MMA, decays (two), then four weight groups of four: two items at a
 // time, half of the columns each (one group per item left the pass waiting for
-// its weights).
+// its weights). A value is written over its x, so that four items fit in flight
+// (two in tiles of their own: 409 against 406 us of the call).
+// What bounds it: shared memory. An item's 32 KB in by TMA, 16 KB read and 32 KB
+// written by the weight groups and 64 KB of operands are 1,152 cycles at 128 bytes
+// each; it takes about 1,500.
 constexpr int kSumThreads = 640, kSumRing = 4;
 
 struct SumMisc {
-    uint64_t b_full[2], b_empty[2], x_full[4], x_empty[4], dt_full[kSumRing], dt_empty[kSumRing];
-    uint64_t xw_full[2], xw_empty[2], drain;
+    uint64_t b_full[2], b_empty[2], x_full[4], xw_full[4], x_empty[4], dt_full[kSumRing], dt_empty[kSumRing], drain;
     uint32_t tmem_slot;
 };
 
 template <int kT> struct SumSmem {
-    static constexpr uint32_t kX = 2 * kT * kTile;
-    static constexpr uint32_t kXw = kX + 4 * kTile;
-    static constexpr uint32_t kW = kXw + 4 * kTile;
+    static constexpr uint32_t kX = 2 * kT * kTile;             // four slots: x, then its weighted value; remainder
+    static constexpr uint32_t kW = kX + 8 * kTile;
     static constexpr uint32_t kMisc = kW + kSumRing * kC * 4;
     static constexpr size_t kBytes = 1024 + kMisc + sizeof(SumMisc);
 };
@@ -829,8 +832,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
     SumMisc& m = *reinterpret_cast<SumMisc*>(base + L::kMisc);
     float* wts = reinterpret_cast<float*>(base + L::kW);
     auto btile = [&](int s) { return base + s * kT * kTile; };
-    auto xtile = [&](int n) { return base + L::kX + (n & 3) * kTile; };
-    auto xwtile = [&](int n) { return base + L::kXw + (n & 1) * 2 * kTile; };
+    auto xtile = [&](int n) { return base + L::kX + (n & 3) * 2 * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Place pl = place(a, un);
     const int nu = pl.nu, items = pl.nc * nu, c_last = pl.c0 + pl.nc - 1;
@@ -840,12 +842,11 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.b_full[s], 1);
             mbar_init(&m.b_empty[s], 1);
-            mbar_init(&m.xw_full[s], 8);
-            mbar_init(&m.xw_empty[s], 1);
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(&m.x_full[s], 1);
-            mbar_init(&m.x_empty[s], 8);
+            mbar_init(&m.xw_full[s], 8);
+            mbar_init(&m.x_empty[s], 1);
             mbar_init(&m.dt_full[s], 1);
             mbar_init(&m.dt_empty[s], 8);
         }
@@ -893,18 +894,18 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
     } else if (warp == 1) {
         constexpr uint32_t id = idesc_bf16_f32(128, 64 * kT, true, true);
         const uint32_t base_a = smem_u32(base);
-        const uint64_t br0 = rows_desc(base_a), xw0 = rows_desc(base_a + L::kXw);
+        const uint64_t br0 = rows_desc(base_a), xw0 = rows_desc(base_a + L::kX);
         for (int n = 0, i = 0, u = 0; n < items; ++n) {
             if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin) &&
-                       warp_wait(&m.xw_full[n & 1], (n >> 1) & 1, max_spin)))
+                       warp_wait(&m.xw_full[n & 3], (n >> 2) & 1, max_spin)))
                 break;
             tc_fence_after();
             if (lane == 0) {
-                const uint64_t bt = step_desc(br0, (i & 1) * kT * kTile), xw = step_desc(xw0, (n & 1) * 2 * kTile);
+                const uint64_t bt = step_desc(br0, (i & 1) * kT * kTile), xw = step_desc(xw0, (n & 3) * 2 * kTile);
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k)
                     mma_bf16(tmem + 64 * kT * u, step_desc(xw, k * 2048), step_desc(bt, k * 2048), id, i > 0 || k > 0);
-                mma_commit(&m.xw_empty[n & 1]);
+                mma_commit(&m.x_empty[n & 3]);
                 if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
             __syncwarp();
@@ -946,8 +947,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
         for (int n = grp & 1; n < items; n += 2) {
             const int slot = n % kSumRing, i = n / nu, u = n - i * nu;
             if (!(ok = warp_wait(&m.dt_full[slot], (n / kSumRing) & 1, max_spin) &&
-                       warp_wait(&m.x_full[n & 3], (n >> 2) & 1, max_spin) &&
-                       (n < 2 || warp_wait(&m.xw_empty[n & 1], ((n >> 1) - 1) & 1, max_spin))))
+                       warp_wait(&m.x_full[n & 3], (n >> 2) & 1, max_spin)))
                 break;
             if (a.lengths && (c_last - i + 1) * kC > pl.n) {
                 if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin))) break;
@@ -962,16 +962,15 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
                 uint32_t h[8], l[8];
                 weigh16(*reinterpret_cast<const uint4*>(xtile(n) + o0), *reinterpret_cast<const uint4*>(xtile(n) + o1),
                         wts[slot * kC + row], h, l);
-                *reinterpret_cast<uint4*>(xwtile(n) + o0) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(xwtile(n) + o1) = make_uint4(h[4], h[5], h[6], h[7]);
-                *reinterpret_cast<uint4*>(xwtile(n) + kTile + o0) = make_uint4(l[0], l[1], l[2], l[3]);
-                *reinterpret_cast<uint4*>(xwtile(n) + kTile + o1) = make_uint4(l[4], l[5], l[6], l[7]);
+                *reinterpret_cast<uint4*>(xtile(n) + o0) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(xtile(n) + o1) = make_uint4(h[4], h[5], h[6], h[7]);
+                *reinterpret_cast<uint4*>(xtile(n) + kTile + o0) = make_uint4(l[0], l[1], l[2], l[3]);
+                *reinterpret_cast<uint4*>(xtile(n) + kTile + o1) = make_uint4(l[4], l[5], l[6], l[7]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&m.xw_full[n & 1]);
-                mbar_arrive(&m.x_empty[n & 3]);
+                mbar_arrive(&m.xw_full[n & 3]);
                 mbar_arrive(&m.dt_empty[slot]);
             }
         }
