@@ -16,9 +16,12 @@
 // What bounds it: every value is read once and written once (the backward also
 // reads the gradient), two dozen operations each: HBM bandwidth. A group of D/8
 // lanes owns one token and walks its heads, so the angles are computed once per
-// token, and each lane moves 16-byte (fp32: 32-byte) pieces of whole rows; the
-// stores of neighbouring groups are neighbouring rows of one head. Weights are
-// folded into the cos and sin registers. Statistics and sums are fp32.
+// token; the stores of neighbouring groups are neighbouring rows of one head. A lane
+// holds both values of its pairs: eight neighbours of a row, or, for pairs (i, i + R),
+// four and their four partners (with eight neighbours there too, their partners came
+// by shuffles: B=16 N=8192 H=8+8 D=128 forward 221 us against 189). The next heads'
+// rows are in flight under the current ones. Weights are folded into the cos and sin
+// registers. Statistics and sums are fp32.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -57,7 +60,15 @@ struct Args {
 template <typename T> struct Raw8;   // eight consecutive values of a row as stored
 template <> struct Raw8<__nv_bfloat16> {
     uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    template <bool kInter>
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int o0, int o1) {
+        if constexpr (kInter) {
+            v = __ldg(reinterpret_cast<const uint4*>(p + o0));
+        } else {
+            const uint2 lo = __ldg(reinterpret_cast<const uint2*>(p + o0)), hi = __ldg(reinterpret_cast<const uint2*>(p + o1));
+            v = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+    }
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -67,53 +78,46 @@ template <> struct Raw8<__nv_bfloat16> {
             f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
-        *reinterpret_cast<uint4*>(p) =
-            make_uint4(tcc::pack_bf16(f[0], f[1]), tcc::pack_bf16(f[2], f[3]),
-                       tcc::pack_bf16(f[4], f[5]), tcc::pack_bf16(f[6], f[7]));
-    }
-    // The partner values of lane l: half h of the row piece comes from lane src[h],
-    // whose halves are swapped when `swap` (R not a multiple of 8).
-    __device__ __forceinline__ Raw8 partner(const int (&src)[2], bool swap) const {
-        Raw8 r;
-        uint4 t = v;
-        if (swap) t = make_uint4(v.z, v.w, v.x, v.y);      // uniform over the grid
-        r.v.x = __shfl_sync(0xffffffffu, t.x, src[0]);
-        r.v.y = __shfl_sync(0xffffffffu, t.y, src[0]);
-        r.v.z = __shfl_sync(0xffffffffu, t.z, src[1]);
-        r.v.w = __shfl_sync(0xffffffffu, t.w, src[1]);
-        return r;
+    template <bool kInter>
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, int o0, int o1, const float (&f)[8]) {
+        const uint4 u = make_uint4(tcc::pack_bf16(f[0], f[1]), tcc::pack_bf16(f[2], f[3]),
+                                   tcc::pack_bf16(f[4], f[5]), tcc::pack_bf16(f[6], f[7]));
+        if constexpr (kInter) {
+            *reinterpret_cast<uint4*>(p + o0) = u;
+        } else {
+            *reinterpret_cast<uint2*>(p + o0) = make_uint2(u.x, u.y);
+            *reinterpret_cast<uint2*>(p + o1) = make_uint2(u.z, u.w);
+        }
     }
 };
 template <> struct Raw8<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    template <bool kInter>
+    __device__ __forceinline__ void load(const float* p, int o0, int o1) {
+        a = __ldg(reinterpret_cast<const float4*>(p + o0));
+        b = __ldg(reinterpret_cast<const float4*>(p + o1));
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
-    static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __device__ __forceinline__ Raw8 partner(const int (&src)[2], bool swap) const {
-        const float4 lo = swap ? b : a, hi = swap ? a : b;
-        Raw8 r;
-        r.a.x = __shfl_sync(0xffffffffu, lo.x, src[0]);
-        r.a.y = __shfl_sync(0xffffffffu, lo.y, src[0]);
-        r.a.z = __shfl_sync(0xffffffffu, lo.z, src[0]);
-        r.a.w = __shfl_sync(0xffffffffu, lo.w, src[0]);
-        r.b.x = __shfl_sync(0xffffffffu, hi.x, src[1]);
-        r.b.y = __shfl_sync(0xffffffffu, hi.y, src[1]);
-        r.b.z = __shfl_sync(0xffffffffu, hi.z, src[1]);
-        r.b.w = __shfl_sync(0xffffffffu, hi.w, src[1]);
-        return r;
+    template <bool kInter>
+    static __device__ __forceinline__ void store(float* p, int o0, int o1, const float (&f)[8]) {
+        *reinterpret_cast<float4*>(p + o0) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(p + o1) = make_float4(f[4], f[5], f[6], f[7]);
     }
 };
+
+// Features of lane l: o0 .. o0 + 3 and o1 .. o1 + 3, so that a lane holds both
+// values of its pairs. Pairs (2i, 2i + 1), and features past the rotated ones: eight
+// neighbours. Pairs (i, i + R): four and their four partners.
+template <bool kInter>
+__device__ __forceinline__ void lane_features(int R, int l, int* o0, int* o1) {
+    const bool halves = !kInter && 8 * l < 2 * R;
+    *o0 = halves ? 4 * l : 8 * l;
+    *o1 = halves ? R + 4 * l : 8 * l + 4;
+}
 
 // cos and sin of pair i at token t. A pair whose axis is past the last given one
 // takes the last, so no position is read out of range.
@@ -145,23 +149,13 @@ __device__ __forceinline__ void lane_angles(const Args& a, int64_t t, int l, flo
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int e = 8 * l + j;
-            const bool low = e < a.R;
-            float ss;
-            pair_angle(a, t, low ? e : e - a.R, &c[j], &ss);
-            s[j] = low ? -ss : ss;
+        for (int j = 0; j < 4; ++j) {
+            float cc, ss;
+            pair_angle(a, t, 4 * l + j, &cc, &ss);
+            c[j] = c[j + 4] = cc;
+            s[j] = -ss;
+            s[j + 4] = ss;
         }
-    }
-}
-
-// Source lanes (within the warp) of the partner halves, half layout.
-__device__ __forceinline__ void partner_lanes(int R, int l, int group_base, int (&src)[2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int e = 8 * l + 4 * h;
-        const int p = e < R ? e + R : (e < 2 * R ? e - R : e);
-        src[h] = group_base + (p >> 3);
     }
 }
 
@@ -172,97 +166,100 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// The partner's values of x: in the lane itself (pairs 2i, 2i + 1) or by shuffle.
-template <bool kInter, typename T>
-__device__ __forceinline__ void partner_values(const Raw8<T>& raw, const float (&x)[8],
-                                               const int (&src)[2], bool swap, bool rot,
-                                               float (&p)[8]) {
-    if constexpr (kInter) {
+// The partners of a lane's values; zeros past the rotated features.
+template <bool kInter>
+__device__ __forceinline__ void partner_values(const float (&x)[8], bool rot, float (&p)[8]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = x[j ^ 1];
-    } else {
-        raw.partner(src, swap).get(p);
-    }
-    if (!rot) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = 0.f;
-    }
+    for (int j = 0; j < 8; ++j) p[j] = rot ? x[kInter ? j ^ 1 : j ^ 4] : 0.f;
 }
 
 // Forward. kLanes: lanes per row (D / 8 rounded up to a power of two; the lanes
 // past D / 8 carry zeros). blockIdx.y: a range of the Hq + Hk heads.
-// Four blocks of 256 threads per SM for bf16 (B=16 N=8192 H=8+8 D=128: 220 us, two
-// blocks 293), two for fp32, whose pieces need twice the registers (16 images of
-// 32 x 32: 28 us, four blocks 32).
+// Three blocks of 256 threads per SM for bf16 (B=16 N=8192 H=8+8 D=128: 189 us; four,
+// which spill, 210; four with two heads in flight 197), two for fp32, whose rows need
+// twice the registers (16 images of 32 x 32: 24.5 us).
 template <typename T, int kLanes, bool kInter>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) rope_fwd_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_fwd_kernel(const __grid_constant__ Args a) {
     constexpr int kRows = kThreads / kLanes, kU = 4;   // heads in flight per group
     const int l = threadIdx.x % kLanes;
     const int64_t t_raw = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
     const bool live = t_raw < a.tokens && 8 * l < a.D;
     const int64_t t = min(t_raw, a.tokens - 1);
     const int64_t b = t / a.N, n = t - b * a.N;
-    const bool rot = 8 * l < 2 * a.R, swap = (a.R & 4) != 0;
-    int src[2];
-    partner_lanes(a.R, l, (threadIdx.x & 31) & ~(kLanes - 1), src);
-    float c[8], s[8];
-    lane_angles<kInter>(a, t, l, c, s);
-    const int h_begin = blockIdx.y * a.heads_per_block, h_end = h_begin + a.heads_per_block;
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
+    const bool rot = 8 * l < 2 * a.R;
+    int o0, o1;
+    lane_features<kInter>(a.R, l, &o0, &o1);
+    const int h_begin = blockIdx.y * a.heads_per_block;
+    const int h_end = min(h_begin + a.heads_per_block, a.s[0].H + a.s[1].H);
+    // Heads h .. h + kU - 1 of q and k together, as far as they belong to one side.
+    Raw8<T> raw[kU];
+    auto fetch = [&](int h) {
+        const int side = h >= a.s[0].H;
         const Side& sd = a.s[side];
-        const int off = side ? a.s[0].H : 0;
-        const int h0 = max(h_begin - off, 0), h1 = min(h_end - off, sd.H);
-        if (h0 >= h1) continue;
-        // Weights folded into the rotation: c w and s w_partner.
-        float cw[8], sw[8];
-        if (sd.w != nullptr) {
-            Raw8<T> wr;
-            wr.zero();
-            if (8 * l < a.D) wr.load(static_cast<const T*>(sd.w) + 8 * l);
-            float w[8], wp[8];
-            wr.get(w);
-            partner_values<kInter>(wr, w, src, swap, rot, wp);
+        const int hs = side ? h - a.s[0].H : h, left = min(h_end - h, sd.H - hs);
+        const T* xp = static_cast<const T*>(sd.x) + b * sd.x_bs + n * sd.x_ts + (int64_t)hs * a.D;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) cw[j] = c[j] * w[j], sw[j] = s[j] * wp[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) cw[j] = c[j], sw[j] = s[j];
+        for (int u = 0; u < kU; ++u) {
+            raw[u].zero();
+            if (live && u < left) raw[u].template load<kInter>(xp + (int64_t)u * a.D, o0, o1);
         }
-        const T* xp = static_cast<const T*>(sd.x) + b * sd.x_bs + n * sd.x_ts + 8 * l;
-        T* yp = static_cast<T*>(sd.y) + (b * sd.H * a.N + n) * a.D + 8 * l;
-        for (int h = h0; h < h1; h += kU) {
-            Raw8<T> raw[kU];
+    };
+    fetch(h_begin);                                    // in flight under the angles
+    float c[8], s[8], cw[8], sw[8];
+    lane_angles<kInter>(a, t, l, c, s);
+    int last = -1;
+#pragma unroll 1
+    for (int h = h_begin; h < h_end;) {
+        const int side = h >= a.s[0].H;
+        const Side& sd = a.s[side];
+        const int hs = side ? h - a.s[0].H : h, left = min(min(h_end - h, sd.H - hs), kU);
+        if (side != last) {
+            // Weights folded into the rotation: c w and s w_partner.
+            last = side;
+            if (sd.w != nullptr) {
+                Raw8<T> wr;
+                wr.zero();
+                if (8 * l < a.D) wr.template load<kInter>(static_cast<const T*>(sd.w), o0, o1);
+                float w[8], wp[8];
+                wr.get(w);
+                partner_values<kInter>(w, rot, wp);
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                raw[u].zero();
-                if (live && h + u < h1) raw[u].load(xp + (int64_t)(h + u) * a.D);
+                for (int j = 0; j < 8; ++j) cw[j] = c[j] * w[j], sw[j] = s[j] * wp[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cw[j] = c[j], sw[j] = s[j];
             }
+        }
+        Raw8<T> cur[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                float x[8], p[8], r = 1.f;
-                raw[u].get(x);
-                partner_values<kInter>(raw[u], x, src, swap, rot, p);
-                if (a.norm) {
-                    float ss = 0.f;
+        for (int u = 0; u < kU; ++u) cur[u] = raw[u];
+        h += left;
+        if (h < h_end) fetch(h);                       // in flight under this batch
+        T* yp = static_cast<T*>(sd.y) + ((b * sd.H + hs) * a.N + n) * a.D;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-                    r = rsqrtf(group_sum<kLanes>(ss) * a.inv_D + a.eps);
-                }
-                float y[8];
+        for (int u = 0; u < kU; ++u) {
+            float x[8], p[8], r = 1.f;
+            cur[u].get(x);
+            partner_values<kInter>(x, rot, p);
+            if (a.norm) {
+                float ss = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = r * fmaf(x[j], cw[j], p[j] * sw[j]);
-                if (live && h + u < h1) Raw8<T>::store(yp + (int64_t)(h + u) * a.N * a.D, y);
+                for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+                r = rsqrtf(group_sum<kLanes>(ss) * a.inv_D + a.eps);
             }
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = r * fmaf(x[j], cw[j], p[j] * sw[j]);
+            if (live && u < left) Raw8<T>::template store<kInter>(yp + (int64_t)u * a.N * a.D, o0, o1, y);
         }
     }
 }
 
-// Adds a block's per-lane dw sums (v[8] for features 8l .. 8l + 7 of every row
+// Adds a block's per-lane dw sums (v[8] for a lane's eight features of every row
 // group) in a fixed order and writes D floats at out.
 template <int kLanes>
-__device__ __forceinline__ void block_dw(float (&v)[8], float (*red)[kMaxDim], int l, int D,
-                                         float* out) {
+__device__ __forceinline__ void block_dw(float (&v)[8], float (*red)[kMaxDim], int l, int o0,
+                                         int o1, int D, float* out) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -270,7 +267,7 @@ __device__ __forceinline__ void block_dw(float (&v)[8], float (*red)[kMaxDim], i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane < kLanes && 8 * l < D)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) red[warp][8 * l + j] = v[j];
+        for (int j = 0; j < 8; ++j) red[warp][j < 4 ? o0 + j : o1 + j - 4] = v[j];
     __syncthreads();
     if ((int)threadIdx.x < D) {
         float t = 0.f;
@@ -283,13 +280,17 @@ __device__ __forceinline__ void block_dw(float (&v)[8], float (*red)[kMaxDim], i
 
 // Backward. A block walks token tiles blockIdx.x, + gridDim.x, ..., so that dw
 // leaves as one partial row per block.
+// With the norm, whose weight sums fill the registers, two blocks per SM and the next
+// heads' rows in flight (B=4 N=8191 H=16+4 D=64 bf16 61 us; three blocks without the
+// rows ahead 65); without it three blocks, whose warps hide the loads by themselves
+// (B=4 N=9216 H=12+12 D=128 78 us; two blocks with the rows ahead 94).
 template <typename T, int kLanes, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_bwd_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kNorm ? 3 : 2) rope_bwd_kernel(const __grid_constant__ Args a) {
     constexpr int kRows = kThreads / kLanes, kU = 2;
     const int l = threadIdx.x % kLanes;
-    const bool rot = 8 * l < 2 * a.R, swap = (a.R & 4) != 0;
-    int src[2];
-    partner_lanes(a.R, l, (threadIdx.x & 31) & ~(kLanes - 1), src);
+    const bool rot = 8 * l < 2 * a.R;
+    int o0, o1;
+    lane_features<kInter>(a.R, l, &o0, &o1);
     const int h_begin = blockIdx.y * a.heads_per_block, h_end = h_begin + a.heads_per_block;
     const int64_t tiles = (a.tokens + kRows - 1) / kRows;
     float dw[2][8] = {};
@@ -298,47 +299,64 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_bwd_ker
         const bool live = t_raw < a.tokens && 8 * l < a.D;
         const int64_t t = min(t_raw, a.tokens - 1);
         const int64_t b = t / a.N, n = t - b * a.N;
+        // This block's heads of each side, and the rows of the next batch.
+        const int h0[2] = {min(h_begin, a.s[0].H), max(h_begin - a.s[0].H, 0)};
+        const int h1[2] = {min(h_end, a.s[0].H), min(max(h_end - a.s[0].H, 0), a.s[1].H)};
+        Raw8<T> graw[kU], xraw[kU];
+        auto fetch = [&](int side, int h) {
+            const Side& sd = a.s[side];
+            const T* gp = static_cast<const T*>(sd.go) + ((b * sd.H + h) * a.N + n) * a.D;
+            const T* xp = kNorm ? static_cast<const T*>(sd.x) + b * sd.x_bs + n * sd.x_ts + (int64_t)h * a.D
+                                : nullptr;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                graw[u].zero();
+                xraw[u].zero();
+                if (live && h + u < h1[side]) {
+                    graw[u].template load<kInter>(gp + (int64_t)u * a.N * a.D, o0, o1);
+                    if (kNorm) xraw[u].template load<kInter>(xp + (int64_t)u * a.D, o0, o1);
+                }
+            }
+        };
+        if constexpr (kNorm) {                         // in flight under the angles
+            if (h0[0] < h1[0]) fetch(0, h0[0]);
+            else if (h0[1] < h1[1]) fetch(1, h0[1]);
+        }
         float c[8], s[8];
         lane_angles<kInter>(a, t, l, c, s);
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             const Side& sd = a.s[side];
-            const int off = side ? a.s[0].H : 0;
-            const int h0 = max(h_begin - off, 0), h1 = min(h_end - off, sd.H);
-            if (h0 >= h1) continue;
+            if (h0[side] >= h1[side]) continue;
             float w[8];
             if (kNorm && sd.w != nullptr && 8 * l < a.D) {
                 Raw8<T> wr;
-                wr.load(static_cast<const T*>(sd.w) + 8 * l);
+                wr.template load<kInter>(static_cast<const T*>(sd.w), o0, o1);
                 wr.get(w);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = 1.f;
             }
-            const T* gp = static_cast<const T*>(sd.go) + (b * sd.H * a.N + n) * a.D + 8 * l;
-            const T* xp = kNorm ? static_cast<const T*>(sd.x) + b * sd.x_bs + n * sd.x_ts + 8 * l : nullptr;
-            T* yp = static_cast<T*>(sd.y) + b * sd.y_bs + n * sd.y_ts + 8 * l;
-            for (int h = h0; h < h1; h += kU) {
-                Raw8<T> graw[kU], xraw[kU];
+            T* yp = static_cast<T*>(sd.y) + b * sd.y_bs + n * sd.y_ts;
+            for (int h = h0[side]; h < h1[side]; h += kU) {
+                if constexpr (!kNorm) fetch(side, h);
+                Raw8<T> gcur[kU], xcur[kU];
 #pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    graw[u].zero();
-                    xraw[u].zero();
-                    if (live && h + u < h1) {
-                        graw[u].load(gp + (int64_t)(h + u) * a.N * a.D);
-                        if (kNorm) xraw[u].load(xp + (int64_t)(h + u) * a.D);
-                    }
+                for (int u = 0; u < kU; ++u) gcur[u] = graw[u], xcur[u] = xraw[u];
+                if constexpr (kNorm) {                 // in flight under this batch
+                    if (h + kU < h1[side]) fetch(side, h + kU);
+                    else if (side == 0 && h0[1] < h1[1]) fetch(1, h0[1]);
                 }
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     float go[8], p[8], g[8], y[8];
-                    graw[u].get(go);
-                    partner_values<kInter>(graw[u], go, src, swap, rot, p);
+                    gcur[u].get(go);
+                    partner_values<kInter>(go, rot, p);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) g[j] = fmaf(go[j], c[j], -p[j] * s[j]);
                     if constexpr (kNorm) {
                         float x[8], ss = 0.f, dot = 0.f;
-                        xraw[u].get(x);
+                        xcur[u].get(x);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             ss = fmaf(x[j], x[j], ss);
@@ -357,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_bwd_ker
 #pragma unroll
                         for (int j = 0; j < 8; ++j) y[j] = g[j];
                     }
-                    if (live && h + u < h1) Raw8<T>::store(yp + (int64_t)(h + u) * a.D, y);
+                    if (live && h + u < h1[side]) Raw8<T>::template store<kInter>(yp + (int64_t)(h + u) * a.D, o0, o1, y);
                 }
             }
         }
@@ -365,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_bwd_ker
     if constexpr (kNorm) {
         __shared__ float red[kThreads / 32][kMaxDim];
         float* out = a.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.D;
-        block_dw<kLanes>(dw[0], red, l, a.D, out);
-        block_dw<kLanes>(dw[1], red, l, a.D, out + a.D);
+        block_dw<kLanes>(dw[0], red, l, o0, o1, a.D, out);
+        block_dw<kLanes>(dw[1], red, l, o0, o1, a.D, out + a.D);
     }
 }
 

@@ -40,7 +40,7 @@
 // pass streams (4) alone, in reverse order of chunks so that the weights reach to the
 // segment's end and nothing has to be rescaled (97 us of the call); seeds are chained by
 // csrc/scan.cu (12 us) and the second pass starts from them.
-// What bounds it: the groups' instructions (about 9,700 a warp-item of 128 tokens x 64
+// What bounds it: the groups' instructions (about 9,600 of a warp an item of 128 tokens x 64
 // values, 42 % of the issue slots, each warp waiting on its own chain of TMEM reads,
 // exponentials and hand-offs) next to the products' operand reads from shared memory
 // (196 KB an item at 128 bytes a cycle).
