@@ -211,3 +211,34 @@ def test_autograd_of_one_side(la, given):
     assert np.allclose(to_f64(w.grad), rw, rtol=0, atol=2.0 ** -16 * np.abs(rw).max())
     if given == "unused":
         assert (k.grad == 0).all() and (wk.grad == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_backward_of_many_tokens(la, dt, inter):
+    # More token tiles than blocks, so that a block walks several: rows equal those of pieces
+    # bit for bit; the weight gradients are the pieces' sums. Either is an fp32 sum of the same
+    # terms in a tree of fewer than 2^7 additions deep, the pieces' five sums add five more.
+    B, N, D, step = 1, 60001, 32, 12000
+    q, k, pos, f, ax, wq, wk, g = problem(B, N, 2, 1, D, 12, 2, dt, 5)
+    table, pos = la.la_rope_table(f, ax), pos.cuda()
+    how = dict(wq=wq, wk=wk, interleaved=inter)
+    qo, ko = la.la_qk_norm_rope_fwd(q, k, pos, table, **how)
+    dqo, dko = torch.randn_like(qo), torch.randn_like(ko)
+    dq, dk, dwq, dwk = la.la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, **how)
+    sums = [torch.zeros(D, device="cuda", dtype=torch.float64) for _ in range(2)]
+    for t in range(0, N, step):
+        s = slice(t, min(t + step, N))
+        part = (q[:, s], k[:, s], pos[:, s].contiguous(), table)
+        po, ro = la.la_qk_norm_rope_fwd(*part, **how)
+        assert torch.equal(po, qo[:, :, s]) and torch.equal(ro, ko[:, :, s])
+        pq, pk, pwq, pwk = la.la_qk_norm_rope_bwd(*part[:2], dqo[:, :, s].contiguous(), dko[:, :, s].contiguous(),
+                                                  *part[2:], **how)
+        assert torch.equal(pq, dq[:, s]) and torch.equal(pk, dk[:, s])
+        sums[0] += pwq
+        sums[1] += pwk
+    for x, do, dw, want in ((q, dqo, dwq, sums[0]), (k, dko, dwk, sums[1])):
+        r = torch.rsqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
+        # |g| of a pair is at most the two gradients' magnitudes together.
+        size = (do.double().abs().amax(-1).transpose(1, 2)[..., None] * 2 * (x.double() * r).abs()).sum((0, 1, 2))
+        assert ((dw - want).abs() <= 2 * 128 * 2.0 ** -24 * size).all()

@@ -141,3 +141,24 @@ def test_extreme_values(la):
     assert y[0] == 1e4 and y[4] == 200 and abs(y[2] - 88) < 1e-4
     assert abs(y[1]) < 1e-30 and abs(y[3]) < 1e-30 and abs(y[5]) < 1e-30
     assert y[8].isnan() and torch.isfinite(y[9:]).all()
+
+
+@pytest.mark.parametrize("dt,C", [("bf16", 4096), ("f32", 2048)])
+@pytest.mark.parametrize("W", [2, 4])
+def test_long_prompts_equal_their_pieces(la, dt, C, W):
+    # Enough work that a thread walks 64 tokens; pieces of 500 tokens, which it walks 8 or
+    # fewer at a time, continued from the state: same multiply-adds in the same order, so
+    # equal bits, with ragged ends inside a group of rows and on its borders.
+    g = torch.Generator(device="cuda").manual_seed(C + W)
+    B, N = 4, 6000
+    x = torch.randn(B, N, C, generator=g, device="cuda").to(DT[dt])
+    w = torch.randn(C, W, generator=g, device="cuda").to(DT[dt])
+    n = torch.tensor([N, 5000, 4481, 63], dtype=torch.int32, device="cuda")
+    y = torch.full_like(x, 5.0)
+    y, last = la.la_short_conv_fwd(x, w, None, True, n, y=y, return_state=True)
+    state = torch.zeros(B, W - 1, C, dtype=x.dtype, device="cuda")
+    want = torch.full_like(x, 5.0)
+    for t in range(0, N, 500):
+        _, state = la.la_short_conv_fwd(x[:, t:t + 500], w, None, True, (n - t).clamp(0, 500).to(torch.int32),
+                                        state, y=want[:, t:t + 500], return_state=True)
+    assert torch.equal(y, want) and torch.equal(last, state)
