@@ -807,7 +807,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 // (two in tiles of their own: 409 against 406 us of the call).
 // What bounds it: shared memory. An item's 32 KB in by TMA, 16 KB read and 32 KB
 // written by the weight groups and 64 KB of operands are 1,152 cycles at 128 bytes
-// each; it takes about 1,500.
+// each, 1,500 as counted with barriers and factors; it takes about 1,750.
 constexpr int kSumThreads = 640, kSumRing = 4;
 
 struct SumMisc {
