@@ -29,11 +29,14 @@ struct ScanArgs {
 // logarithm is 2 artanh(s), s = e / (2 + e) <= 1/3, by its odd power series to s^13
 // (truncation below 2^-26 of the value), which keeps small step sizes accurate
 // relative to themselves; e^-|v| is 2^t with the rounding of t = -|v| log2 e put back.
+// |v| is held within 128, where e^-|v| is 0 in fp32 already: the lowest values of a type and
+// minus infinity, which mask a token, give 0 (t and its rounding would be infinities that
+// cancel to NaN). A comparison, not a minimum, so that NaN stays NaN.
 __device__ __forceinline__ float step_size(float v, int softplus) {
     if (!softplus) return v;
     constexpr double kLog2e = 1.44269504088896340736;
     constexpr float kL = (float)kLog2e, kLLo = (float)(kLog2e - (double)kL);
-    const float x = -fabsf(v), t = x * kL;
+    const float m = fabsf(v), x = m > 128.f ? -128.f : -m, t = x * kL;
     const float r = fmaf(x, kL, -t) + x * kLLo;
     float e, q;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
