@@ -364,7 +364,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kNorm ? 3 : 2) ro
                         }
                         ss = group_sum<kLanes>(ss);
                         dot = group_sum<kLanes>(dot);
-                        const float r = rsqrtf(ss * a.inv_D + a.eps);
+                        // A slot that holds no row (past the last token or head) adds nothing to the
+                        // weights' sums, without an epsilon either (0 times infinity).
+                        const bool row = t_raw < a.tokens && h + u < h1[side];
+                        const float r = row ? rsqrtf(ss * a.inv_D + a.eps) : 0.f;
                         const float k = r * r * r * (dot * a.inv_D);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
