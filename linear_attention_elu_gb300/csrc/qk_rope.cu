@@ -6,7 +6,7 @@
 //   u = r w x (or x without the norm);  a rotated pair (a, b) of u becomes
 //   (a cos t - b sin t, b cos t + a sin t),  t = pos[axis_i] f_i.
 // Backward, from g_out: g = R^T g_out (the rotation by -t),
-//   dw = sum over rows of g r x,   dx = r (w g) - x r^3 mean(w g x).
+//   dw = sum over rows of g xh,   dx = r (w g - xh mean(w g xh)),   xh = r x.
 //
 // Angles. A pair's table entry holds its frequency as a whole number of 2^-64
 // turns, so pos * step modulo 2^64 is the angle's fraction of a turn, exact for
@@ -368,11 +368,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !kNorm ? 3 : 2) ro
                         // weights' sums, without an epsilon either (0 times infinity).
                         const bool row = t_raw < a.tokens && h + u < h1[side];
                         const float r = row ? rsqrtf(ss * a.inv_D + a.eps) : 0.f;
-                        const float k = r * r * r * (dot * a.inv_D);
+                        // dx = r (w g - xh mean(w g xh)) with xh = r x of order 1: r^3 alone passes
+                        // fp32's range for rows below 1e-13.
+                        const float k = r * (r * dot * a.inv_D);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            y[j] = fmaf(r * w[j], g[j], -k * x[j]);
-                            dw[side][j] = fmaf(g[j] * r, x[j], dw[side][j]);
+                            const float xh = r * x[j];
+                            y[j] = fmaf(r * w[j], g[j], -k * xh);
+                            dw[side][j] = fmaf(g[j], xh, dw[side][j]);
                         }
                     } else {
 #pragma unroll
@@ -453,14 +456,15 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
                 float dot = 0.f;
 #pragma unroll
                 for (int j = 0; j < kE; ++j) dot = fmaf(v[j] * w[j], x[j], dot);
-                const float k = a.norm ? r * r * r * (group_sum<32>(dot) * a.inv_D) : 0.f;
+                const float k = a.norm ? r * (r * group_sum<32>(dot) * a.inv_D) : 0.f;
 #pragma unroll
                 for (int j = 0; j < kE; ++j) {
                     const int e = lane + 32 * j;
                     if (e >= a.D) continue;
-                    yr[e] = from_f<T>(a.norm ? fmaf(r * w[j], v[j], -k * x[j]) : v[j]);
-                    if (side == 0) dw[0][j] = fmaf(v[j] * r, x[j], dw[0][j]);
-                    else dw[1][j] = fmaf(v[j] * r, x[j], dw[1][j]);
+                    const float xh = r * x[j];
+                    yr[e] = from_f<T>(a.norm ? fmaf(r * w[j], v[j], -k * xh) : v[j]);
+                    if (side == 0) dw[0][j] = fmaf(v[j], xh, dw[0][j]);
+                    else dw[1][j] = fmaf(v[j], xh, dw[1][j]);
                 }
             }
         }
