@@ -18,10 +18,11 @@
 // TMEM: it is scaled there per chunk, and (4) adds w x as two bf16 terms (value and
 // remainder), which leaves at most 2^-18 of each term (states 2e-6 off in all, relative
 // to their largest entry; a third term needs 16 KB of shared memory that are not there).
-// Decays of P below the diagonal 32 x 32 blocks are products of two factors <= 1 around
-// the block row's start, e^{l_i - l_m} e^{l_m - l_j}, so only the diagonal blocks take an
-// exponential per score; the weights of (4) come from sums taken from the chunk's end, so
-// that a small exponent is not a difference of two large ones.
+// Decays of P below the diagonal 32 x 32 blocks are products of factors <= 1 (from token j
+// to its block's end, over the blocks between, from the block row's start to token i), so
+// only the diagonal blocks take an exponential per score. Each factor's exponent is a sum of
+// its own tokens; the diagonal blocks' are differences of sums from the block's start, so
+// that a small exponent is not a difference of two large ones from further back.
 //
 // Schedule (20 warps, one CTA per SM). An item is one chunk of one unit. Two groups
 // of eight warps alternate items; a warp owns 32 rows and half of the columns. A
@@ -70,12 +71,16 @@ constexpr uint32_t kTile = kTileBytes;             // [128 tokens x 64] bf16
 constexpr int kDtRing = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// One unit's decays over a chunk, exponents in base 2.
+// One unit's decays over a chunk, exponents in base 2. Sums start at every 32 tokens (the
+// blocks of the scores): after a token that decays by a large factor, a sum from the chunk's
+// start would leave no digits to the differences between the slow tokens behind it.
 struct Decay {
-    float cum[kC];      // l_t: sum up to and including t
+    float loc[kC];      // sum from the token's block's start up to and including t
     float d[kC];        // step sizes, 0 past the sequence's end (not folded into an exponent:
-                        // next to a large l their logarithm would lose its digits)
-    float w[kC];        // d_t 2^(l_end - l_t), 0 past the end
+                        // next to a large sum their logarithm would lose its digits)
+    float off[192];     // d_t 2^(sum from t to the start of block q): q = 1 32 tokens, then q = 2 64, q = 3 96
+    float w[kC];        // d_t 2^(sum over the tokens of the chunk after t), 0 past the end
+    float start[kC];    // 2^l_t
     float total;        // 2^l_end
     float pad[3];
 };
@@ -109,8 +114,7 @@ template <int kT> struct Smem {
     static constexpr uint32_t kOut = kXw + 2 * kTile;          // gate, then output
     static constexpr uint32_t kSb = kOut + 2 * kTile;          // bf16 state, 64 kT rows
     static constexpr uint32_t kDt = kSb + kT * 64 * 128;
-    static constexpr uint32_t kCol = kDt + (kDtRing * sizeof(Decay) + 127) / 128 * 128;
-    static constexpr uint32_t kMask = kCol + 16 * 32 * 4;      // 32 column factors per warp
+    static constexpr uint32_t kMask = kDt + (kDtRing * sizeof(Decay) + 127) / 128 * 128;
     static constexpr uint32_t kMisc = kMask + 32 * 16 * 4;     // diagonal block: 16 words of pairs per row
     static constexpr uint32_t kEnd = kMisc + sizeof(Misc);
     static constexpr size_t kBytes = 1024 + kEnd;
@@ -193,39 +197,51 @@ __device__ __forceinline__ void load_steps(const ScanArgs& a, const Place& pl, i
         v[k] = t + k < pl.n ? __bfloat162float(p[(int64_t)(t + k) * a.step_ts]) : 0.f;
 }
 
-// Inclusive sums from the chunk's start (cum) and exclusive sums from its end
-// (suf) of d A log2 e over the 128 tokens, and the step sizes themselves.
-__device__ __forceinline__ void decays(const ScanArgs& a, const Place& pl, int c, float A2, float bias,
-                                       const float (&raw)[4], float (&d)[4], float (&cum)[4],
-                                       float (&suf)[4], float* total) {
-    const int lane = threadIdx.x & 31, t = c * kC + 4 * lane;
+// Of d A log2 e over the 128 tokens: inclusive sums from the start of each block of 32 (loc),
+// exclusive sums from its end (suf) and the blocks' sums; and the step sizes themselves. A
+// token's exponent is held within -127, where its factor is 0 in fp32 already, so that sums
+// over a block stay below 4096 (digits of 2^-12) and never reach an infinity. A comparison,
+// so that NaN stays NaN.
+__device__ __forceinline__ void decays(const ScanArgs& a, const Place& pl, int c, float A, float bias,
+                                       const float (&raw)[4], float (&d)[4], float (&loc)[4],
+                                       float (&suf)[4], float (&blk)[4]) {
+    const int lane = threadIdx.x & 31, in = lane & 7, t = c * kC + 4 * lane;
     float l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         d[k] = t + k < pl.n ? step_size(raw[k] + bias, a.softplus) : 0.f;
-        l[k] = d[k] * A2;
+        const float e = t + k < pl.n ? d[k] * A * kLog2e : 0.f;
+        l[k] = e < -127.f ? -127.f : e;
     }
     const float own = (l[0] + l[1]) + (l[2] + l[3]);
-    float up = own, down = own;              // inclusive scans over lanes, both directions
+    float up = own, down = own;              // inclusive scans over a block's lanes, both directions
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float x = __shfl_up_sync(0xffffffffu, up, o);
-        const float y = __shfl_down_sync(0xffffffffu, down, o);
-        if (lane >= o) up += x;
-        if (lane + o < 32) down += y;
+    for (int o = 1; o < 8; o <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, up, o, 8);
+        const float y = __shfl_down_sync(0xffffffffu, down, o, 8);
+        if (in >= o) up += x;
+        if (in + o < 8) down += y;
     }
-    *total = __shfl_sync(0xffffffffu, down, 0);
-    float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
-    if (lane == 0) before = 0.f;
-    if (lane == 31) after = 0.f;
-    cum[0] = before + l[0];
-    cum[1] = cum[0] + l[1];
-    cum[2] = cum[1] + l[2];
-    cum[3] = cum[2] + l[3];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) blk[k] = __shfl_sync(0xffffffffu, down, 8 * k);
+    float before = __shfl_up_sync(0xffffffffu, up, 1, 8), after = __shfl_down_sync(0xffffffffu, down, 1, 8);
+    if (in == 0) before = 0.f;
+    if (in == 7) after = 0.f;
+    loc[0] = before + l[0];
+    loc[1] = loc[0] + l[1];
+    loc[2] = loc[1] + l[2];
+    loc[3] = loc[2] + l[3];
     suf[3] = after;
     suf[2] = suf[3] + l[3];
     suf[1] = suf[2] + l[2];
     suf[0] = suf[1] + l[1];
+}
+
+// Sums over the blocks before and after the lane's own.
+__device__ __forceinline__ void other_blocks(const float (&blk)[4], float* before, float* after) {
+    const int own = (threadIdx.x & 31) >> 3;
+    *before = (own > 0 ? blk[0] : 0.f) + (own > 1 ? blk[1] : 0.f) + (own > 2 ? blk[2] : 0.f);
+    *after = (own < 1 ? blk[1] : 0.f) + (own < 2 ? blk[2] : 0.f) + (own < 3 ? blk[3] : 0.f);
 }
 
 // Sixteen weighted values: hi = bf16(w x), lo = bf16(w x - hi).
@@ -478,7 +494,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     } else if (warp == kWork + 2) {
         // ------------------------------------------------------------ step sizes to decays
         const int h0 = pl.head(a, un, 0), h1 = pl.head(a, un, nu - 1);
-        const float A0 = a.A[h0] * kLog2e, A1 = a.A[h1] * kLog2e;
+        const float A0 = a.A[h0], A1 = a.A[h1];
         const float b0 = a.step_bias ? a.step_bias[h0] : 0.f, b1 = a.step_bias ? a.step_bias[h1] : 0.f;
         float raw[4];
         if (items > 0) load_steps(a, pl, h0, pl.c0, raw);
@@ -486,15 +502,28 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             const int slot = n % kDtRing, in = u + 1 == nu ? i + 1 : i, next_u = u + 1 == nu ? 0 : 1;
             float next[4] = {};
             if (n + 1 < items) load_steps(a, pl, next_u ? h1 : h0, pl.c0 + in, next);
-            float d[4], cum[4], suf[4], total;
-            decays(a, pl, pl.c0 + i, u ? A1 : A0, u ? b1 : b0, raw, d, cum, suf, &total);
+            float d[4], loc[4], suf[4], blk[4], before, after;
+            decays(a, pl, pl.c0 + i, u ? A1 : A0, u ? b1 : b0, raw, d, loc, suf, blk);
+            other_blocks(blk, &before, &after);
             if (n >= kDtRing && !(ok = warp_wait(&m.dt_empty[slot], (n / kDtRing - 1) & 1, max_spin))) break;
             Decay& o = dts[slot];
-            *reinterpret_cast<float4*>(o.cum + 4 * lane) = make_float4(cum[0], cum[1], cum[2], cum[3]);
+            *reinterpret_cast<float4*>(o.loc + 4 * lane) = make_float4(loc[0], loc[1], loc[2], loc[3]);
             *reinterpret_cast<float4*>(o.d + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
-            *reinterpret_cast<float4*>(o.w + 4 * lane) =
-                make_float4(d[0] * ex2(suf[0]), d[1] * ex2(suf[1]), d[2] * ex2(suf[2]), d[3] * ex2(suf[3]));
-            if (lane == 0) o.total = ex2(total);
+            // To the end of the token's block, over the blocks between, over the blocks after.
+            const float out[4] = {d[0] * ex2(suf[0]), d[1] * ex2(suf[1]), d[2] * ex2(suf[2]), d[3] * ex2(suf[3])};
+            const int own = lane >> 3;
+#pragma unroll
+            for (int q = 1; q < 4; ++q) {
+                const float f = ex2((own < 1 && q > 1 ? blk[1] : 0.f) + (own < 2 && q > 2 ? blk[2] : 0.f));
+                if (own < q)
+                    *reinterpret_cast<float4*>(o.off + 16 * q * (q - 1) + 4 * lane) =
+                        make_float4(out[0] * f, out[1] * f, out[2] * f, out[3] * f);
+            }
+            const float rest = ex2(after);
+            *reinterpret_cast<float4*>(o.w + 4 * lane) = make_float4(out[0] * rest, out[1] * rest, out[2] * rest, out[3] * rest);
+            *reinterpret_cast<float4*>(o.start + 4 * lane) =
+                make_float4(ex2(before + loc[0]), ex2(before + loc[1]), ex2(before + loc[2]), ex2(before + loc[3]));
+            if (lane == 0) o.total = ex2(blk[0] + blk[1] + blk[2] + blk[3]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&m.dt_full[slot]);
 #pragma unroll
@@ -539,7 +568,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         const int64_t head_state = (int64_t)a.S * a.P;
         const bool has_state = q < 2 * kT;
-        float* col = reinterpret_cast<float*>(base + L::kCol) + 32 * warp;
         const uint2* mask = reinterpret_cast<const uint2*>(base + L::kMask) + lane;   // [e / 2][lane]
         uint8_t* sb = base + L::kSb;
         const uint32_t ptm = tmem + lanes + kTmP + 64 * grp;
@@ -595,17 +623,15 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                     // ------------------------------------------------ scores to P
                     if (!(ok = warp_wait(&m.sc_full[i & 1], (i >> 1) & 1, max_spin))) break;
                     tc_fence_after();
-                    const float ci = dc.cum[row];
+                    const float ci = dc.loc[row];
 #pragma unroll 1
                     for (int b = g; b <= q; b += 2) {
                         uint32_t s[2][16], p[16];
                         tmem_ld16(tmem + lanes + kTmSc + 32 * b, s[0]);
                         tmem_ld16(tmem + lanes + kTmSc + 32 * b + 16, s[1]);
                         if (b < q) {
-                            const float cm = dc.cum[32 * q - 1];
-                            col[lane] = ex2(cm - dc.cum[32 * b + lane]) * dc.d[32 * b + lane];
-                            __syncwarp();
-                            const float ri = ex2(ci - cm);
+                            const float* col = dc.off + 16 * q * (q - 1) + 32 * b;
+                            const float ri = ex2(ci);
                             const uint64_t r2 = pk2(ri, ri);
                             tmem_ld_wait();
 #pragma unroll
@@ -615,7 +641,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                                 p[e] = pack2(mul2(mul2(pk2(__uint_as_float(v[0]), __uint_as_float(v[1])), f.x), r2));
                                 p[e + 1] = pack2(mul2(mul2(pk2(__uint_as_float(v[2]), __uint_as_float(v[3])), f.y), r2));
                             }
-                            __syncwarp();                  // the factors have been read
                         } else {
                             // The diagonal block: an exponential per score; pairs past the row's
                             // own token are cleared as bits (their products may be anything).
@@ -623,7 +648,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                             tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dc.cum + 32 * q + 2 * e);
+                                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dc.loc + 32 * q + 2 * e);
                                 const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(dc.d + 32 * q + 2 * e);
                                 const uint2 mk = mask[16 * e];   // 32 (e / 2)
                                 const uint32_t* v = &s[e >> 3][2 * (e & 7)];
@@ -711,7 +736,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(&m.item_ready);
             // -------------------------------------------------------- output
-            const float Dh = u ? Du[1] : Du[0], e = ex2(dc.cum[row]);
+            const float Dh = u ? Du[1] : Du[0], e = dc.start[row];
             const uint64_t D2 = pk2(Dh, Dh), e2 = pk2(e, e);
             if (!(ok = warp_wait(&m.slot_ready[n & 1], (n >> 1) & 1, max_spin) &&
                        warp_wait(&m.y_full[n & 1], (n >> 1) & 1, max_spin)))
@@ -920,20 +945,22 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
         const int u = warp - 2;
         if (u < nu) {
             const int h = pl.head(a, un, u);
-            const float A2 = a.A[h] * kLog2e, bias = a.step_bias ? a.step_bias[h] : 0.f;
+            const float A = a.A[h], bias = a.step_bias ? a.step_bias[h] : 0.f;
             float raw[4] = {}, after = 0.f;            // after: sum over the chunks behind
             if (pl.nc > 0) load_steps(a, pl, h, c_last, raw);
             for (int i = 0; i < pl.nc; ++i) {
                 const int n = i * nu + u, slot = n % kSumRing;
                 float next[4] = {};
                 if (i + 1 < pl.nc) load_steps(a, pl, h, c_last - i - 1, next);
-                float d[4], cum[4], suf[4], total;
-                decays(a, pl, c_last - i, A2, bias, raw, d, cum, suf, &total);
+                float d[4], loc[4], suf[4], blk[4], before, rest;
+                decays(a, pl, c_last - i, A, bias, raw, d, loc, suf, blk);
+                other_blocks(blk, &before, &rest);
                 if (n >= kSumRing && !(ok = warp_wait(&m.dt_empty[slot], (n / kSumRing - 1) & 1, max_spin))) break;
+                rest += after;
                 *reinterpret_cast<float4*>(wts + slot * kC + 4 * lane) =
-                    make_float4(d[0] * ex2(suf[0] + after), d[1] * ex2(suf[1] + after),
-                                d[2] * ex2(suf[2] + after), d[3] * ex2(suf[3] + after));
-                after += total;
+                    make_float4(d[0] * ex2(suf[0] + rest), d[1] * ex2(suf[1] + rest),
+                                d[2] * ex2(suf[2] + rest), d[3] * ex2(suf[3] + rest));
+                after += blk[0] + blk[1] + blk[2] + blk[3];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.dt_full[slot]);
 #pragma unroll
