@@ -85,6 +85,17 @@ struct Decay {
     float pad[3];
 };
 
+// A unit's values that are not finite. They would reach the tokens before them too: (3) adds
+// 0 x for every later token of the chunk, and 0 times an infinity is NaN. So (3) gets 0 in
+// their place, and their columns' outputs are set to NaN from their token on; the state, which
+// takes the values as they are, is not finite from there on by itself.
+struct Bad {
+    int first[64];      // per column, the first such token
+    int any;            // the first of all
+    int pad[3];
+};
+constexpr int kNone = 0x7fffffff;
+
 struct Units {
     int ctas, units, blocks;    // CTAs per group, units per group, 64-column blocks per head
     int per;                    // units per CTA, 1 or 2
@@ -115,7 +126,8 @@ template <int kT> struct Smem {
     static constexpr uint32_t kSb = kOut + 2 * kTile;          // bf16 state, 64 kT rows
     static constexpr uint32_t kDt = kSb + kT * 64 * 128;
     static constexpr uint32_t kMask = kDt + (kDtRing * sizeof(Decay) + 127) / 128 * 128;
-    static constexpr uint32_t kMisc = kMask + 32 * 16 * 4;     // diagonal block: 16 words of pairs per row
+    static constexpr uint32_t kBad = kMask + 32 * 16 * 4;      // diagonal block: 16 words of pairs per row
+    static constexpr uint32_t kMisc = kBad + 2 * sizeof(Bad);
     static constexpr uint32_t kEnd = kMisc + sizeof(Misc);
     static constexpr size_t kBytes = 1024 + kEnd;
 };
@@ -318,6 +330,36 @@ __device__ __noinline__ void put_gate(const ScanArgs& a, const Place& pl, const 
     *reinterpret_cast<uint4*>(slot + pc1) = in && c + 8 < a.P ? load_gate(z + 8) : make_uint4(0, 0, 0, 0);
 }
 
+// Columns 32 g .. of row `row` of an x tile: notes the values that are not finite, and clears them.
+__device__ __noinline__ void take_out(uint8_t* tile, int row, int g, int token, Bad* bad) {
+    for (int c = 32 * g; c < 32 * g + 32; ++c) {
+        unsigned short* v = reinterpret_cast<unsigned short*>(tile + row * 128 + (((c >> 3) ^ (row & 7)) << 4)) + (c & 7);
+        if ((*v & 0x7F80u) != 0x7F80u) continue;
+        *v = 0;
+        atomicMin(&bad->first[c], token);
+        atomicMin(&bad->any, token);
+    }
+}
+
+// Outputs of the chunk at token t0 that such values reach, set to NaN: in the output slot, or
+// (slot null) in the rows that were written one by one. One thread; a column whose first value
+// is in an earlier chunk is NaN by its state.
+__device__ __noinline__ void put_nan(const ScanArgs& a, const Place& pl, const Units& un, int u, int t0, uint8_t* slot,
+                                     const Bad* bad) {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + pl.b * a.y_bs + (int64_t)pl.head(a, un, u) * a.P + pl.col0(un, u);
+    for (int c = 0; c < 64; ++c) {
+        const int row0 = *const_cast<const volatile int*>(&bad->first[c]) - t0;
+        if (row0 < 0) continue;
+        for (int row = row0; row < kC; ++row) {
+            if (slot)
+                reinterpret_cast<unsigned short*>(slot + row * 128 + (((c >> 3) ^ (row & 7)) << 4))[c & 7] = 0x7FFF;
+            else if (t0 + row < pl.n && pl.col0(un, u) + c < a.P)
+                y[(t0 + row) * a.y_ts + c] = __ushort_as_bfloat16(0x7FFF);
+        }
+    }
+    fence_proxy_async_smem();
+}
+
 // z / (1 + e^-z) of two packed bf16 values. e^-z overflows to infinity and its
 // reciprocal is then 0: the limit.
 __device__ __forceinline__ uint64_t gate2(uint32_t z) {
@@ -340,6 +382,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     Decay* dts = reinterpret_cast<Decay*>(base + L::kDt);
+    Bad* bad = reinterpret_cast<Bad*>(base + L::kBad);
     auto btile = [&](int s) { return base + L::kB0 + s * kT * kTile; };
     auto xtile = [&](int n) { return base + L::kX + (n & 1) * kTile; };
     auto oslot = [&](int n) { return base + L::kOut + (n & 1) * kTile; };
@@ -375,6 +418,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         mbar_init(&m.drain, 1);
         fence_mbar_init();
     }
+    if (tid < 2 * (int)(sizeof(Bad) / sizeof(int))) reinterpret_cast<int*>(bad)[tid] = kNone;
     if (warp == kWork + 1) {
         tmem_alloc(&m.tmem_slot, 512);
         tmem_relinquish();
@@ -549,6 +593,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             for (int n = 0; n < 2 && n < items && !hold; ++n) open_slot(n / nu, n % nu);
             for (int n = 0, i = 0, u = 0; n < items; ++n) {
                 if (!(ok = mbar_wait(&m.y_staged[n & 1], (n >> 1) & 1, max_spin))) break;
+                if (*const_cast<volatile int*>(&bad[u].any) != kNone)
+                    put_nan(a, pl, un, u, (pl.c0 + i) * kC, i != by_rows ? oslot(n) : nullptr, bad + u);
                 if (i != by_rows) {
                     tma_store_4d(&ymap, oslot(n), pl.col0(un, u), pl.head(a, un, u), (pl.c0 + i) * kC, pl.b);
                     tma_store_commit();
@@ -715,6 +761,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                         }
                 }
                 const float w = dc.w[row];
+                uint32_t bits = 0u;
 #pragma unroll 1
                 for (int j = 4 * g; j < 4 * g + 4; j += 2) {
                     const uint32_t o0 = piece(j), o1 = piece(j + 1);
@@ -726,7 +773,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                     *reinterpret_cast<uint4*>(hi + o1) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
                     *reinterpret_cast<uint4*>(hi + kTile + o0) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
                     *reinterpret_cast<uint4*>(hi + kTile + o1) = make_uint4(wl[4], wl[5], wl[6], wl[7]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) bits |= wl[e];
                 }
+                // A value that is not finite leaves NaN as remainder. Others leave small ones: bits of
+                // theirs together make up NaN's exponent only where one is 2 or more.
+                if ((bits & 0x7F80u) == 0x7F80u || (bits & 0x7F800000u) == 0x7F800000u)
+                    take_out(xtile(n), row, g, (pl.c0 + i) * kC + row, bad + u);
             }
             if (!ok) break;
             // What this warp stored is ready for the tensor cores.
