@@ -708,15 +708,16 @@ def la_short_conv_fwd(x, w, bias=None, silu=True, lengths=None, state0=None, sta
     """Causal depthwise convolution of x [B,N,C] (strided rows allowed) with w [C,W], W in 2..4.
 
     state0 [B,W-1,C]: the inputs before the first token; the last W - 1 inputs go to state_out
-    (allocated with return_state=True). lengths (int32 [B]): rows past them are left as they are.
-    Returns y, or (y, state_out) with return_state=True."""
+    (allocated with return_state=True). lengths (int32 [B]): rows past them are left as they are
+    (zero where the call makes y). Returns y, or (y, state_out) with return_state=True."""
     index, xs, C, W = _conv_args(x, w, bias, 3)
     B, N, _ = x.shape
     _conv_state(state0, B, C, W, x, "state0")
     _check_lengths(lengths, B)
     with _scope(index, stream):
         if y is None:
-            y = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+            make = torch.empty if lengths is None else torch.zeros
+            y = make((B, N, C), dtype=x.dtype, device=x.device)
         if state_out is None and return_state:
             state_out = torch.empty((B, W - 1, C), dtype=x.dtype, device=x.device)
         ys = _like(y, x, 1)
@@ -783,8 +784,8 @@ def la_selective_scan_fwd(x, step, A, Bm, Cm, D=None, z=None, dt_bias=None, soft
 
     y_t = (C_t^T S_t + D x_t) silu(z_t) with S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T and
     d_t = softplus(step_t + dt_bias). S0, S_out [B,H,S,P] float32 (S_out may be S0). lengths
-    (int32 [B]): rows past them are left as they are. Token rows may be strided (column ranges of
-    a projection). Returns y [B,N,H,P]."""
+    (int32 [B]): rows past them are left as they are (zero where the call makes y). Token rows may
+    be strided (column ranges of a projection). Returns y [B,N,H,P]."""
     index, (B, N, H, P), G, S = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 2)
     _f32_state(S0, (B, H, S, P), "S0")
     _f32_state(S_out, (B, H, S, P), "S_out")
@@ -794,7 +795,8 @@ def la_selective_scan_fwd(x, step, A, Bm, Cm, D=None, z=None, dt_bias=None, soft
     zs = _inner_adjacent(z, "z", 2) if z is not None else (0, 0)
     with _scope(index, stream):
         if y is None:
-            y = torch.empty((B, N, H, P), dtype=x.dtype, device=x.device)
+            make = torch.empty if lengths is None else torch.zeros
+            y = make((B, N, H, P), dtype=x.dtype, device=x.device)
         ys = _like(y, x, 2)
         if ws is None:
             ws = workspace(LA_OP_SELECTIVE_SCAN, B, H, N, S, P, x.dtype, x.device)
