@@ -489,7 +489,7 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
  *    H P values of a token adjacent); step: rows of [B, N, H]; Bm, Cm: rows of
  *    [B, N, G, S]; all dtype dt, so that they can be column ranges of the
  *    projection and of la_short_conv_fwd's output. H a multiple of G; 1 <= S,
- *    P <= 128; B H <= 65535; N <= 2^30.
+ *    P <= 128; B H <= 65535 (prompts); N <= 2^30.
  *  - A, D, step_bias: [H] float32; A is the (negative) rate itself. d_t A_h <= 0 is
  *    expected (the state must not grow); nothing checks it.
  *  - S0 [B, H, S, P] float32 (nullable: zero): state before the first token; S_out

@@ -489,12 +489,14 @@ cudaError_t step(const ScanArgs& a, int64_t BH, cudaStream_t st) {
     return cudaPeekAtLastError();
 }
 
-la_status check_shape(int B, int H, int G, int N, int S, int P, la_dtype dt) {
+// most_heads: of all sequences together, the size of the grid's axis that they map to.
+constexpr int64_t kPromptHeads = 65535, kStepHeads = 2147483647;
+la_status check_shape(int B, int H, int G, int N, int S, int P, la_dtype dt, int64_t most_heads) {
     if (B < 0 || H < 0 || N < 0 || G < 1 || S < 1 || P < 1) return LA_ERR_INVALID_ARG;
     if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_INVALID_ARG;
     if (H % G) return LA_ERR_INVALID_ARG;
     if (S > kMaxDim || P > kMaxDim) return LA_ERR_UNSUPPORTED;
-    if ((int64_t)B * H > 65535) return LA_ERR_UNSUPPORTED;   // heads map to grid.y
+    if ((int64_t)B * H > most_heads) return LA_ERR_UNSUPPORTED;
     if (N > kScanMaxTokens) return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }
@@ -568,7 +570,7 @@ la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token,
                                 float* S_out, void* y, int64_t y_batch, int64_t y_token, int B,
                                 int H, int G, int N, int S, int P, la_dtype dt, void* workspace,
                                 size_t workspace_bytes, la_stream_t stream) {
-    la_status s = la::check_shape(B, H, G, N, S, P, dt);
+    la_status s = la::check_shape(B, H, G, N, S, P, dt, la::kPromptHeads);   // grid.y
     if (s != LA_OK) return s;
     const int64_t BH = (int64_t)B * H;
     if (BH == 0) return LA_OK;
@@ -622,7 +624,7 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
                                  const void* z, int64_t z_batch, const float* step_bias,
                                  int softplus, float* S_inout, void* y, int64_t y_batch, int B,
                                  int H, int G, int S, int P, la_dtype dt, la_stream_t stream) {
-    la_status s = la::check_shape(B, H, G, 1, S, P, dt);
+    la_status s = la::check_shape(B, H, G, 1, S, P, dt, la::kStepHeads);     // grid.x
     if (s != LA_OK) return s;
     const int64_t BH = (int64_t)B * H;
     if (BH == 0) return LA_OK;
