@@ -504,7 +504,7 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
  *    overlap in time need workspaces of their own.
  * la_selective_scan_step: one token per sequence (x, z, y rows of [B, H, P], step
  * of [B, H], Bm, Cm of [B, G, S], batch strides only), S [B, H, S, P] float32
- * updated in place, 16-byte aligned; needs no workspace.
+ * updated in place, 16-byte aligned where P is a multiple of 4; needs no workspace.
  */
 la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token, const void* step,
                                 int64_t step_batch, int64_t step_token, const float* A,

@@ -630,7 +630,7 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
     if (BH == 0) return LA_OK;
     if (la::bad(x, dt) || la::bad(step, dt) || la::bad(Bm, dt) || la::bad(Cm, dt) || la::bad(y, dt) ||
         (z && la::bad(z, dt)) || !A || la::bad4(A) || la::bad4(D) || la::bad4(step_bias) || !S_inout ||
-        (reinterpret_cast<uintptr_t>(S_inout) & 15))
+        (reinterpret_cast<uintptr_t>(S_inout) & (P % 4 ? 3 : 15)))   // 16-byte accesses of four columns
         return LA_ERR_INVALID_ARG;
     if (!la::rows_disjoint(B, 1, (int64_t)H * P, y_batch, 0)) return LA_ERR_INVALID_ARG;
     la::scan::ScanArgs a = {};
