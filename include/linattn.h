@@ -417,7 +417,9 @@ la_status la_rope_table(const double* inv_freq, const int32_t* axis, int pairs, 
  *  - D a multiple of 8, pairs a multiple of 4 and 16-byte aligned rows run the
  *    vector kernels, anything else one warp per row.
  *  - A table entry whose axis is >= axes uses the last axis.
- *  - Outputs must not overlap inputs. Needs no workspace; asynchronous on `stream`.
+ *  - Outputs must not overlap inputs or one another: LA_ERR_INVALID_ARG where their
+ *    addresses show it (as in the entries below). Needs no workspace; asynchronous on
+ *    `stream`.
  */
 la_status la_qk_norm_rope_fwd(const void* q, int64_t q_batch, int64_t q_token, const void* k,
                               int64_t k_batch, int64_t k_token, const void* wq, const void* wk,
@@ -434,6 +436,8 @@ la_status la_qk_norm_rope_fwd(const void* q, int64_t q_batch, int64_t q_token, c
  *   dw = sum over rows of g r x,   dx = r w g - x r^3 mean(w g x)   (dx = g without the norm).
  * Sums are fp32 in a fixed order: the same inputs give the same bits.
  *  - q, k may be null when norm == 0.
+ *  - dq and dk must not overlap an input or one another; only dq may be q itself and dk k
+ *    (the same rows).
  *  - workspace (norm only): la_qk_norm_rope_bwd_workspace_size() bytes, 256-byte
  *    aligned; it needs no initialisation.
  */
@@ -462,10 +466,12 @@ la_status la_qk_norm_rope_bwd(const void* q, int64_t q_batch, int64_t q_token, c
  *    not overlap (LA_ERR_INVALID_ARG).
  *  - lengths [B] int32, device (nullable): sequence b has lengths[b] tokens
  *    (clamped to 0..N). Rows past it are neither read nor written.
- *  - y must not overlap x. Whole, aligned 16-byte pieces run the vector kernel.
+ *  - y and state_out must not overlap an input or one another (LA_ERR_INVALID_ARG).
+ *    Whole, aligned 16-byte pieces run the vector kernel.
  *  - Needs no workspace; asynchronous on `stream`.
  * la_short_conv_step: one token per sequence, x and y rows of [B, C]; state
- * [B, W - 1, C] is read and shifted by one row in place.
+ * [B, W - 1, C] is read and shifted by one row in place. y may be x itself; nothing
+ * else may overlap y or the state.
  */
 la_status la_short_conv_fwd(const void* x, int64_t x_batch, int64_t x_token, const void* w,
                             const void* bias, int silu, const int32_t* lengths, const void* state0,
@@ -498,13 +504,15 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
  *  - lengths [B] int32, device (nullable): sequence b has lengths[b] tokens
  *    (clamped to 0..N); rows past it are neither read nor written, and a sequence
  *    of no tokens keeps its state.
- *  - y must not overlap an input, and its rows must not overlap one another.
+ *  - y and S_out must not overlap an input (but S_out == S0) or one another, and y's
+ *    rows must not overlap among themselves (LA_ERR_INVALID_ARG).
  *  - workspace: la_workspace_size(LA_OP_SELECTIVE_SCAN, B, H, N, S, P, dt, ...)
  *    bytes, 256-byte aligned, initialised once with la_workspace_init. Calls that
  *    overlap in time need workspaces of their own.
  * la_selective_scan_step: one token per sequence (x, z, y rows of [B, H, P], step
  * of [B, H], Bm, Cm of [B, G, S], batch strides only), S [B, H, S, P] float32
- * updated in place, 16-byte aligned where P is a multiple of 4; needs no workspace.
+ * updated in place, 16-byte aligned where P is a multiple of 4; needs no workspace. y may
+ * be x or z itself; nothing else may overlap y or S.
  */
 la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token, const void* step,
                                 int64_t step_batch, int64_t step_token, const float* A,

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "overlap.h"
 #include "tc_common.cuh"
 
 namespace la {
@@ -586,6 +587,24 @@ cudaError_t run(Args& a, bool bwd, bool inter, int* blocks, cudaStream_t st) {
     return cudaPeekAtLastError();
 }
 
+// What both directions read, for the checks of overlap.
+struct Operands {
+    Rows x[2], w[2], pos, table;
+};
+Operands operands(const Args& a, int B, int N, int D, la_dtype dt, const int32_t* pos, int axes, const int64_t* table,
+                  int pairs) {
+    const int64_t eb = dt == LA_BF16 ? 2 : 4;
+    Operands o;
+    for (int i = 0; i < 2; ++i) {
+        const Side& sd = a.s[i];
+        o.x[i] = rows_of(sd.H ? sd.x : nullptr, B, N, (int64_t)sd.H * D, sd.x_bs, sd.x_ts, eb);
+        o.w[i] = block_of(sd.H ? sd.w : nullptr, D * eb);
+    }
+    o.pos = block_of(pairs > 0 ? pos : nullptr, (int64_t)B * N * axes * 4);
+    o.table = block_of(pairs > 0 ? table : nullptr, (int64_t)pairs * 16);
+    return o;
+}
+
 bool elem_aligned(const void* p, la_dtype dt) {
     return (reinterpret_cast<uintptr_t>(p) & (dt == LA_BF16 ? 1 : 3)) == 0;
 }
@@ -653,6 +672,15 @@ la_status la_qk_norm_rope_fwd(const void* q, int64_t q_batch, int64_t q_token, c
         if (sd.H > 0 && (!sd.x || !sd.y || !la::elem_aligned(sd.x, dt) || !la::elem_aligned(sd.y, dt) ||
                          !la::elem_aligned(sd.w, dt)))
             return LA_ERR_INVALID_ARG;
+    {
+        const la::Operands o = la::operands(a, B, N, D, dt, pos, axes, table, pairs);
+        const int64_t eb = dt == LA_BF16 ? 2 : 4;
+        const la::Rows yq = la::block_of(Hq ? qo : nullptr, tokens * Hq * D * eb);
+        const la::Rows yk = la::block_of(Hk ? ko : nullptr, tokens * Hk * D * eb);
+        if (la::overlap(yq, yk) || la::overlaps_any(yq, {o.x[0], o.x[1], o.w[0], o.w[1], o.pos, o.table}) ||
+            la::overlaps_any(yk, {o.x[0], o.x[1], o.w[0], o.w[1], o.pos, o.table}))
+            return LA_ERR_INVALID_ARG;
+    }
     a.pos = pos;
     a.table = reinterpret_cast<const longlong2*>(table);
     a.tokens = tokens;
@@ -712,6 +740,21 @@ la_status la_qk_norm_rope_bwd(const void* q, int64_t q_batch, int64_t q_token, c
         if ((s = la_qk_norm_rope_bwd_workspace_size(B, N, Hq, Hk, D, &need)) != LA_OK) return s;
         if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
             return LA_ERR_WORKSPACE;
+    }
+    {
+        const la::Operands o = la::operands(a, B, N, D, dt, pos, axes, table, pairs);
+        const int64_t eb = dt == LA_BF16 ? 2 : 4;
+        la::Rows dx[2], go[2];
+        for (int i = 0; i < 2; ++i) {
+            const la::Side& sd = a.s[i];
+            dx[i] = la::rows_of(sd.H ? sd.y : nullptr, B, N, (int64_t)sd.H * D, sd.y_bs, sd.y_ts, eb);
+            go[i] = la::block_of(sd.H ? sd.go : nullptr, tokens * sd.H * D * eb);
+        }
+        // dx may be its x itself: the lanes that read a row's values replace them.
+        for (int i = 0; i < 2; ++i)
+            if (la::overlaps_any(dx[i], {dx[1 - i], o.x[1 - i], go[0], go[1], o.w[0], o.w[1], o.pos, o.table}) ||
+                (!la::same_rows(dx[i], o.x[i]) && la::overlap(dx[i], o.x[i])))
+                return LA_ERR_INVALID_ARG;
     }
     a.pos = pos;
     a.table = reinterpret_cast<const longlong2*>(table);

@@ -30,6 +30,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "mixing.cuh"
+#include "overlap.h"
 #include "scan.cuh"
 #include "tc_common.cuh"
 
@@ -579,10 +580,8 @@ la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token,
         return LA_ERR_INVALID_ARG;
     // The final state may replace the initial one, but not overlap it otherwise.
     const size_t state = sizeof(float) * (size_t)BH * S * P;
-    if (S0 && S_out && S0 != S_out) {
-        const uintptr_t p = reinterpret_cast<uintptr_t>(S0), q = reinterpret_cast<uintptr_t>(S_out);
-        if (p < q + state && q < p + state) return LA_ERR_INVALID_ARG;
-    }
+    const la::Rows s0 = la::block_of(S0, state), s1 = la::block_of(S_out, state);
+    if (S0 != S_out && la::overlap(s0, s1)) return LA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     if (N == 0) {
         if (!S_out || S_out == S0) return LA_OK;
@@ -591,7 +590,7 @@ la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token,
         return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
     }
     if (la::bad(x, dt) || la::bad(step, dt) || la::bad(Bm, dt) || la::bad(Cm, dt) || la::bad(y, dt) ||
-        (z && la::bad(z, dt)) || y == x || (z && y == z))
+        (z && la::bad(z, dt)))
         return LA_ERR_INVALID_ARG;
     if (!la::rows_disjoint(B, N, (int64_t)H * P, y_batch, y_token)) return LA_ERR_INVALID_ARG;
     la::scan::ScanArgs a = {};
@@ -610,6 +609,16 @@ la_status la_selective_scan_fwd(const void* x, int64_t x_batch, int64_t x_token,
                         (a.nseg > 1 ? (size_t)BH * a.nseg * ((size_t)S * P + 1) * sizeof(float) : 0);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
         return LA_ERR_WORKSPACE;
+    const int64_t eb = dt == LA_BF16 ? 2 : 4, HP = (int64_t)H * P, GS = (int64_t)G * S;
+    const la::Rows xr = la::rows_of(x, B, N, HP, x_batch, x_token, eb), zr = la::rows_of(z, B, N, HP, z_batch, z_token, eb);
+    const la::Rows dr = la::rows_of(step, B, N, H, step_batch, step_token, eb);
+    const la::Rows br = la::rows_of(Bm, B, N, GS, b_batch, b_token, eb), cr = la::rows_of(Cm, B, N, GS, c_batch, c_token, eb);
+    const la::Rows yr = la::rows_of(y, B, N, HP, y_batch, y_token, eb);
+    const la::Rows Ar = la::block_of(A, 4 * (int64_t)H), Dr = la::block_of(D, 4 * (int64_t)H);
+    const la::Rows biasr = la::block_of(step_bias, 4 * (int64_t)H), nr = la::block_of(lengths, 4 * (int64_t)B);
+    if (la::overlaps_any(yr, {xr, zr, dr, br, cr, Ar, Dr, biasr, nr, s0, s1}) ||
+        la::overlaps_any(s1, {xr, zr, dr, br, cr, Ar, Dr, biasr, nr}))
+        return LA_ERR_INVALID_ARG;
     a.seeds = reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(la::WsHeader));
     a.seg_decay = a.seeds + (size_t)BH * a.nseg * S * P;
     const cudaError_t e = tc ? la::scan::tc_scan(a, B, workspace, st)
@@ -633,6 +642,17 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
         (reinterpret_cast<uintptr_t>(S_inout) & (P % 4 ? 3 : 15)))   // 16-byte accesses of four columns
         return LA_ERR_INVALID_ARG;
     if (!la::rows_disjoint(B, 1, (int64_t)H * P, y_batch, 0)) return LA_ERR_INVALID_ARG;
+    const int64_t eb = dt == LA_BF16 ? 2 : 4, HP = (int64_t)H * P, GS = (int64_t)G * S;
+    const la::Rows xr = la::rows_of(x, B, 1, HP, x_batch, 0, eb), zr = la::rows_of(z, B, 1, HP, z_batch, 0, eb);
+    const la::Rows dr = la::rows_of(step, B, 1, H, step_batch, 0, eb), yr = la::rows_of(y, B, 1, HP, y_batch, 0, eb);
+    const la::Rows br = la::rows_of(Bm, B, 1, GS, b_batch, 0, eb), cr = la::rows_of(Cm, B, 1, GS, c_batch, 0, eb);
+    const la::Rows Ar = la::block_of(A, 4 * (int64_t)H), Dr = la::block_of(D, 4 * (int64_t)H);
+    const la::Rows biasr = la::block_of(step_bias, 4 * (int64_t)H);
+    const la::Rows sr = la::block_of(S_inout, (int64_t)(sizeof(float) * (size_t)BH * S * P));
+    // y may be x or z itself: a block reads what it replaces.
+    if (la::overlaps_any(sr, {xr, zr, dr, br, cr, Ar, Dr, biasr, yr}) || la::overlaps_any(yr, {dr, br, cr, Ar, Dr, biasr}) ||
+        (!la::same_rows(xr, yr) && la::overlap(xr, yr)) || (!la::same_rows(zr, yr) && la::overlap(zr, yr)))
+        return LA_ERR_INVALID_ARG;
     la::scan::ScanArgs a = {};
     a.x = x, a.x_bs = x_batch, a.step = step, a.step_bs = step_batch, a.Bm = Bm, a.b_bs = b_batch;
     a.Cm = Cm, a.c_bs = c_batch, a.z = z, a.z_bs = z_batch, a.y = y, a.y_bs = y_batch;

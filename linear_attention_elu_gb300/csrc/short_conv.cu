@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "mixing.cuh"
+#include "overlap.h"
 #include "tc_common.cuh"
 
 namespace la {
@@ -353,12 +354,6 @@ bool bad(const void* p, la_dtype dt) {
 
 bool bad_or_null(const void* p, la_dtype dt) { return p && bad(p, dt); }
 
-bool overlap(const void* a, const void* b, size_t n) {
-    if (!a || !b) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + n && y < x + n;
-}
-
 }  // namespace
 
 }  // namespace la
@@ -375,9 +370,11 @@ la_status la_short_conv_fwd(const void* x, int64_t x_batch, int64_t x_token, con
     if (la::bad_or_null(bias, dt) || la::bad_or_null(state0, dt) || la::bad_or_null(state_out, dt) ||
         (reinterpret_cast<uintptr_t>(lengths) & 3) || la::bad(w, dt))
         return LA_ERR_INVALID_ARG;
-    const size_t state = (size_t)B * (W - 1) * C * (dt == LA_BF16 ? 2 : 4);
+    const int64_t eb = dt == LA_BF16 ? 2 : 4;
+    const size_t state = (size_t)B * (W - 1) * C * eb;
     // Threads of other token groups may still read the old state.
-    if (la::overlap(state0, state_out, state)) return LA_ERR_INVALID_ARG;
+    const la::Rows s0 = la::block_of(state0, state), s1 = la::block_of(state_out, state);
+    if (la::overlap(s0, s1)) return LA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     if (N == 0) {
         if (!state_out) return LA_OK;
@@ -385,8 +382,12 @@ la_status la_short_conv_fwd(const void* x, int64_t x_batch, int64_t x_token, con
                                      : cudaMemsetAsync(state_out, 0, state, st);
         return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
     }
-    if (la::bad(x, dt) || la::bad(y, dt) || x == y) return LA_ERR_INVALID_ARG;
+    if (la::bad(x, dt) || la::bad(y, dt)) return LA_ERR_INVALID_ARG;
     if (!la::rows_disjoint(B, N, C, y_batch, y_token)) return LA_ERR_INVALID_ARG;
+    const la::Rows xr = la::rows_of(x, B, N, C, x_batch, x_token, eb), yr = la::rows_of(y, B, N, C, y_batch, y_token, eb);
+    const la::Rows wr = la::block_of(w, (int64_t)C * W * eb), br = la::block_of(bias, C * eb);
+    const la::Rows nr = la::block_of(lengths, 4 * (int64_t)B);
+    if (la::overlaps_any(yr, {xr, wr, br, nr, s0, s1}) || la::overlaps_any(s1, {xr, wr, br, nr})) return LA_ERR_INVALID_ARG;
     la::ConvArgs a = {};
     a.x = x, a.x_bs = x_batch, a.x_ts = x_token, a.w = w, a.bias = bias, a.s0 = state0, a.s1 = state_out;
     a.y = y, a.y_bs = y_batch, a.y_ts = y_token, a.lengths = lengths;
@@ -403,6 +404,14 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
     if (la::bad(x, dt) || la::bad(w, dt) || la::bad(state, dt) || la::bad(y, dt) || la::bad_or_null(bias, dt))
         return LA_ERR_INVALID_ARG;
     if (!la::rows_disjoint(B, 1, C, y_batch, 0)) return LA_ERR_INVALID_ARG;
+    const int64_t eb = dt == LA_BF16 ? 2 : 4;
+    const la::Rows xr = la::rows_of(x, B, 1, C, x_batch, 0, eb), yr = la::rows_of(y, B, 1, C, y_batch, 0, eb);
+    const la::Rows wr = la::block_of(w, (int64_t)C * W * eb), br = la::block_of(bias, C * eb);
+    const la::Rows sr = la::block_of(state, (int64_t)B * (W - 1) * C * eb);
+    // y may be x itself: a thread reads what it replaces.
+    if (la::overlaps_any(sr, {xr, wr, br, yr}) || la::overlaps_any(yr, {wr, br}) ||
+        (!la::same_rows(xr, yr) && la::overlap(xr, yr)))
+        return LA_ERR_INVALID_ARG;
     la::ConvArgs a = {};
     a.x = x, a.x_bs = x_batch, a.w = w, a.bias = bias, a.s1 = state, a.y = y, a.y_bs = y_batch;
     a.B = B, a.N = 1, a.C = C, a.silu = silu ? 1 : 0;
