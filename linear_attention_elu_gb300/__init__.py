@@ -638,22 +638,28 @@ def la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, wq=None, wk=None, norm=True,
     """Gradients (dq, dk, dwq, dwk) of sum(qo * dqo) + sum(ko * dko) of la_qk_norm_rope_fwd.
 
     dq [B,N,Hq,D] and dk [B,N,Hk,D] may be given as column ranges of one projection gradient.
-    dwq, dwk are float32 [D], None without the norm (or without weights of that side)."""
-    index, B, N, Hq, Hk, D, axes = _rope_args(q, k, pos, table, wq, wk, norm)
-    ref = q if q is not None else k
+    dwq, dwk are float32 [D], None without the norm (or without weights of that side). Without
+    the norm the gradient needs no inputs: q and k may be None."""
+    if norm or q is not None or k is not None:
+        for t, x, what in ((dqo, q, "dqo"), (dko, k, "dko")):
+            if (t is None) != (x is None):
+                raise ValueError(f"{what} must be given exactly when its input is")
+        qx, kx = q, k
+    else:
+        qx, kx = (t.transpose(1, 2) if t is not None and t.dim() == 4 else t for t in (dqo, dko))
+    index, B, N, Hq, Hk, D, axes = _rope_args(qx, kx, pos, table, wq, wk, norm)
+    ref = qx if qx is not None else kx
     qs = _inner_adjacent(q, "q", 2) if q is not None else (0, 0)
     ks = _inner_adjacent(k, "k", 2) if k is not None else (0, 0)
-    for t, x, H, what in ((dqo, q, Hq, "dqo"), (dko, k, Hk, "dko")):
-        if (t is None) != (x is None):
-            raise ValueError(f"{what} must be given exactly when its input is")
+    for t, H, what in ((dqo, Hq, "dqo"), (dko, Hk, "dko")):
         if t is not None:
             _head_major(t, B, H, N, D, ref, what)
     with _scope(index, stream):
-        if dq is None and q is not None:
+        if dq is None and qx is not None:
             dq = torch.empty((B, N, Hq, D), dtype=ref.dtype, device=ref.device)
-        if dk is None and k is not None:
+        if dk is None and kx is not None:
             dk = torch.empty((B, N, Hk, D), dtype=ref.dtype, device=ref.device)
-        for t, x, what in ((dq, q, "dq"), (dk, k, "dk")):
+        for t, x, what in ((dq, qx, "dq"), (dk, kx, "dk")):
             if t is not None and (x is None or t.shape != x.shape or t.dtype != ref.dtype):
                 raise ValueError(f"{what} must be shaped and typed like its input")
         dqs = _inner_adjacent(dq, "dq", 2) if dq is not None else (0, 0)

@@ -47,7 +47,9 @@ class _QkNormRope(torch.autograd.Function):
     def forward(ctx, q, k, pos, table, wq, wk, norm, eps, interleaved):
         qo, ko = la_qk_norm_rope_fwd(q, k, pos, table, wq=wq, wk=wk, norm=norm, eps=eps,
                                      interleaved=interleaved)
-        ctx.save_for_backward(q, k, pos, table, wq, wk)
+        # Without the norm the gradient needs nothing of q and k.
+        ctx.save_for_backward(*((q, k) if norm else (None, None)), pos, table, wq, wk)
+        ctx.given = q is not None, k is not None
         ctx.how = dict(norm=norm, eps=eps, interleaved=interleaved)
         return qo, ko
 
@@ -56,8 +58,8 @@ class _QkNormRope(torch.autograd.Function):
     def backward(ctx, dqo, dko):
         q, k, pos, table, wq, wk = ctx.saved_tensors
         # A side that was not given has no gradient (one whose output was not used gets zeros).
-        dqo = None if q is None else dqo.contiguous()
-        dko = None if k is None else dko.contiguous()
+        dqo = dqo.contiguous() if ctx.given[0] else None
+        dko = dko.contiguous() if ctx.given[1] else None
         dq, dk, dwq, dwk = la_qk_norm_rope_bwd(q, k, dqo, dko, pos, table, wq=wq, wk=wk, **ctx.how)
         return (dq, dk, None, None, dwq.to(wq.dtype) if wq is not None else None,
                 dwk.to(wk.dtype) if wk is not None else None, None, None, None)
