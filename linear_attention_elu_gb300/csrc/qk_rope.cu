@@ -605,6 +605,14 @@ Operands operands(const Args& a, int B, int N, int D, la_dtype dt, const int32_t
     return o;
 }
 
+// v turns modulo one, as a multiple of 2^-64: in two exact steps of 32 bits of the fraction.
+uint64_t turn_bits(double v) {
+    if (v < 0) return 0 - turn_bits(-v);
+    v -= floor(v);
+    const double hi = floor(v * 4294967296.0), lo = (v * 4294967296.0 - hi) * 4294967296.0;
+    return ((uint64_t)hi << 32) + (uint64_t)llrint(lo);
+}
+
 bool elem_aligned(const void* p, la_dtype dt) {
     return (reinterpret_cast<uintptr_t>(p) & (dt == LA_BF16 ? 1 : 3)) == 0;
 }
@@ -641,15 +649,13 @@ la_status la_rope_table(const double* inv_freq, const int32_t* axis, int pairs, 
         if (!isfinite(inv_freq[i])) return LA_ERR_INVALID_ARG;
         const int ax = axis ? axis[i] : 0;
         if (ax < 0 || ax >= axes) return LA_ERR_INVALID_ARG;
-        // Whole turns per position fall away; the rest as a multiple of 2^-64,
-        // in two exact steps (32 bits each) of the double's fraction.
-        double turns = inv_freq[i] * 0.15915494309189535;   // 1 / (2 pi)
-        turns -= floor(turns);
-        if (turns >= 1.0) turns = 0.0;
-        const double hi = floor(turns * 4294967296.0);
-        const double lo = (turns * 4294967296.0 - hi) * 4294967296.0;
-        const uint64_t step = ((uint64_t)hi << 32) + (uint64_t)llrint(lo);
-        table[2 * i] = (int64_t)step;
+        // Turns per position as the sum of two doubles (1 / (2 pi) is such a sum, the product's
+        // rounding is recovered by a fused multiply-add), so that a step is exact to its last
+        // unit: far positions multiply its error. Whole turns fall away. (volatile: the rounding
+        // is of the product as it stands, whatever the compiler contracts.)
+        const volatile double turns = inv_freq[i] * 0.15915494309189535;
+        const double rest = fma(inv_freq[i], 0.15915494309189535, -turns) + inv_freq[i] * -9.839338337591243e-18;
+        table[2 * i] = (int64_t)(la::turn_bits(turns) + la::turn_bits(rest));
         table[2 * i + 1] = ax;
     }
     return LA_OK;
