@@ -395,6 +395,13 @@ la_status la_layer_decode_step(const void* x, const void* Wqkv, const void* Wo, 
  * axes: one axis for text, rows and columns for images, time, height and width
  * for video.
  *
+ * Products of rotated rows depend on their positions' differences alone; products of
+ * elu(x) + 1 of rotated rows, which the attention entries form from these outputs, do
+ * not: phi(R_m q) . phi(R_n k) carries the positions themselves. Scores of differences
+ * come from entries without a map: LA_PHI_IDENTITY (whose denominator is then a sum of
+ * rotated products as well, which can be negative or zero), or la_selective_scan_fwd,
+ * which has neither map nor denominator (Bm and Cm of one group: k and q with one head).
+ *
  * la_rope_table fills the HOST array table[2 * pairs] from inv_freq (radians per
  * position, finite) and axis (null: all 0): entry i is (inv_freq_i / 2 pi as a
  * whole number of 2^-64 turns, axis_i). pos * step modulo 2^64 is then the
