@@ -509,8 +509,9 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
  *    (nullable): state after the last. S_out == S0 updates it in place; any other
  *    overlap is LA_ERR_INVALID_ARG.
  *  - lengths [B] int32, device (nullable): sequence b has lengths[b] tokens
- *    (clamped to 0..N); rows past it are neither read nor written, and a sequence
- *    of no tokens keeps its state.
+ *    (clamped to 0..N). Rows past it are not written and nothing in them counts,
+ *    but they may be read, in whole tiles of 128: nothing else may write them
+ *    meanwhile. A sequence of no tokens keeps its state.
  *  - y and S_out must not overlap an input (but S_out == S0) or one another, and y's
  *    rows must not overlap among themselves (LA_ERR_INVALID_ARG).
  *  - workspace: la_workspace_size(LA_OP_SELECTIVE_SCAN, B, H, N, S, P, dt, ...)
