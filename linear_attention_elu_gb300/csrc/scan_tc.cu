@@ -16,7 +16,7 @@
 // Roundings. x, B, C enter as they are. P and the state of (2) are rounded to bf16
 // once each (2^-9 relative, as the output itself). The state is held in fp32 in
 // TMEM: it is scaled there per chunk, and (4) adds w x as two bf16 terms (value and
-// remainder), which leaves at most 2^-18 of each term (states 2e-6 off in all, relative
+// remainder), which leaves at most 2^-17 of each term (states 2e-6 off in all, relative
 // to their largest entry; a third term needs 16 KB of shared memory that are not there).
 // Decays of P below the diagonal 32 x 32 blocks are products of factors <= 1 (from token j
 // to its block's end, over the blocks between, from the block row's start to token i), so
