@@ -14,7 +14,7 @@
 // so that (1) and the loads of B and C serve both, and walks a range of chunks.
 //
 // Roundings. x, B, C enter as they are. P and the state of (2) are rounded to bf16
-// once each (2^-9 relative, as the output itself). The state is held in fp32 in
+// once each (at most 2^-8 of a term, as the output itself). The state is held in fp32 in
 // TMEM: it is scaled there per chunk, and (4) adds w x as two bf16 terms (value and
 // remainder), which leaves at most 2^-17 of each term (states 2e-6 off in all, relative
 // to their largest entry; a third term needs 16 KB of shared memory that are not there).
@@ -268,7 +268,7 @@ __device__ __forceinline__ void weigh16(uint4 a, uint4 b, float w, uint32_t (&hi
     }
 }
 
-// Rows from `from` on of a [128 x 64] tile set to 0 by its four warps (thread = row).
+// One row of a [128 x 64] tile set to 0.
 __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(tile + row * 128 + j * 16) = make_uint4(0, 0, 0, 0);
@@ -289,14 +289,13 @@ __device__ __forceinline__ uint64_t kmajor_step(uint64_t d, int k) {
 // (4): state += B^T (hi + lo), issued by one thread; lo is the tile after hi. The second
 // 64-row atom of the A operand is the tile after B's (for kT = 1 whatever tile follows:
 // those lanes are unused).
-__device__ __forceinline__ void issue_state(uint32_t dst, uint64_t bt, uint64_t hi, bool fresh) {
+__device__ __forceinline__ void issue_state(uint32_t dst, uint64_t bt, uint64_t hi) {
     constexpr uint32_t id = idesc_bf16_f32(128, 64, true, true);
 #pragma unroll
     for (int part = 0; part < 2; ++part)
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k)
-            mma_bf16(dst, step_desc(bt, k * 2048), step_desc(hi, part * kTile + k * 2048), id,
-                     (fresh && part == 0 && k == 0) ? 0u : 1u);
+            mma_bf16(dst, step_desc(bt, k * 2048), step_desc(hi, part * kTile + k * 2048), id, 1u);
 }
 
 // Eight gate values of a row that is not 16-byte aligned.
@@ -523,7 +522,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                 for (int k = 0; k < kC / 16; ++k)                                       // (3)
                     mma_bf16_ts(tmem + kTmY1, pt + 8 * k, step_desc(xa, k * 2048), id_y, k > 0);
                 mma_commit(&m.y_full[n & 1]);
-                issue_state(tmem + kTmSt + 64 * u, step_desc(br0, (i & 1) * kT * kTile), xw0, false);  // (4)
+                issue_state(tmem + kTmSt + 64 * u, step_desc(br0, (i & 1) * kT * kTile), xw0);  // (4)
                 mma_commit(&m.state_done[n & 1]);
                 if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
