@@ -171,6 +171,15 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
     return pack_bf16(a, b);
 }
 
+// The warp goes on once two loaded values are in every lane's registers. Loads whose values
+// are used only later may complete after an arrival that follows them; here the TMA would
+// then overwrite what they read.
+__device__ __forceinline__ void arrived(uint32_t a, uint32_t b) {
+    asm volatile("{\n .reg .pred p, q;\n setp.eq.u32 p, %0, %1;\n vote.sync.any.pred q, p, 0xffffffff;\n}\n" ::"r"(a),
+                 "r"(b)
+                 : "memory");
+}
+
 // Bounded wait of a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit_us) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_us));
@@ -818,6 +827,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                 if (c == 1) {
                     // Y and x are free: the next item may be issued, the tile after it loaded.
                     tc_fence_before();
+                    arrived(xa.x, xb.x);
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&m.item_ready);
