@@ -506,9 +506,9 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
  *  - Arithmetic is fp32, and y is rounded once, but for bf16 with S and P multiples of
  *    8 and 16-byte aligned rows and states, which runs on the tensor cores: there the
  *    weighted scores within 128 tokens, and the state where y reads it, are rounded to
- *    bf16 as well (half a step, 2^-8, of each term, as y's own rounding), and what a
- *    token adds to the state enters as two bf16 terms (2^-17 of it). The state is held
- *    in fp32 throughout.
+ *    bf16 as well (half a step, 2^-8, of each term, as y's own rounding). The state is
+ *    held in fp32 throughout; what a token adds to it enters S_out as three bf16 terms
+ *    (2^-25 of it is left), and what only y reads as two (2^-17).
  *  - A, D, step_bias: [H] float32; A is the (negative) rate itself. d_t A_h <= 0 is
  *    expected (the state must not grow); nothing checks it.
  *  - S0 [B, H, S, P] float32 (nullable: zero): state before the first token; S_out

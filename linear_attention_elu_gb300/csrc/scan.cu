@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(32 * kMaxDim / (4 * kW)) scan_kernel(const __g
 }
 
 // In place over a head's segments: the end states (from zero) become the states
-// that the segments start from, seed_0 = S0, seed_{i+1} = exp(decay_i) seed_i + end_i.
+// that the segments start from, seed_0 = S0, seed_{i+1} = exp(decay_i) seed_i + end_i; the
+// last one's end goes to S_out (which may be S0).
 // A thread chains one element (reads and writes of a segment are whole rows of
 // threads), sixteen segments in flight; the decays' exponentials are shared.
 constexpr int kMaxSegments = 512;
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(128) seed_kernel(const __grid_constant__ ScanA
             carry = fmaf(f[i0 + u], carry, end[u]);
         }
     }
+    if (a.S_out) a.S_out[bh * E + e] = carry;
 }
 
 // One token per sequence, the state updated in place. It is read and written
@@ -462,7 +464,9 @@ cudaError_t recurrence(const ScanArgs& a, int64_t BH, cudaStream_t st) {
     if (a.nseg > 1) {
         scan_kernel<T, R, kW, true><<<grid, 32 * warps, row + x, st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
-        if ((e = launch_seeds(a, BH, st)) != cudaSuccess) return e;
+        ScanArgs chain = a;
+        chain.S_out = nullptr;                             // the second pass writes it
+        if ((e = launch_seeds(chain, BH, st)) != cudaSuccess) return e;
     }
     return launch_after(scan_kernel<T, R, kW, false>, grid, 32 * warps, smem, st, a.nseg > 1, a);
 }

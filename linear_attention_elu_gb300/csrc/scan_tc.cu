@@ -15,9 +15,10 @@
 //
 // Roundings. x, B, C enter as they are. P and the state of (2) are rounded to bf16
 // once each (at most 2^-8 of a term, as the output itself). The state is held in fp32 in
-// TMEM: it is scaled there per chunk, and (4) adds w x as two bf16 terms (value and
-// remainder), which leaves at most 2^-17 of each term (states 2e-6 off in all, relative
-// to their largest entry; a third term needs 16 KB of shared memory that are not there).
+// TMEM: it is scaled there per chunk, and (4) adds w x as bf16 terms, each the remainder of
+// those before. A state that the call returns, and those that segments start from, take
+// three (2^-25 of w x is left; states 1e-7 to 7e-7 off in all); a state that is only read
+// for y takes two (2^-17), whose tiles leave room for two output slots.
 // Decays of P below the diagonal 32 x 32 blocks are products of factors <= 1 (from token j
 // to its block's end, over the blocks between, from the block row's start to token i), so
 // only the diagonal blocks take an exponential per score. Each factor's exponent is a sum of
@@ -39,8 +40,8 @@
 // x kept in registers from the weights to the output all measured slower.
 // Sequences are cut into segments when there are too few units for the SMs: the first
 // pass streams (4) alone, in reverse order of chunks so that the weights reach to the
-// segment's end and nothing has to be rescaled (97 us of the call); seeds are chained by
-// csrc/scan.cu (12 us) and the second pass starts from them.
+// segment's end and nothing has to be rescaled; seeds are chained by csrc/scan.cu, which
+// writes the final state too, and the second pass starts from them.
 // What bounds it: the groups' instructions (about 9,600 of a warp an item of 128 tokens x 64
 // values, 42 % of the issue slots, each warp waiting on its own chain of TMEM reads,
 // exponentials and hand-offs) next to the products' operand reads from shared memory
@@ -117,13 +118,16 @@ struct Misc {
 
 // Shared memory of the main kernel, from a 1024-byte boundary. B is double
 // buffered; C, which the read of the state frees half an item earlier, is not: its
-// 32 KB hold the output slots instead (gate in, output in place, TMA store).
-template <int kT> struct Smem {
+// 32 KB hold the output slots instead (gate in, output in place, TMA store). With three
+// terms of 128 state rows there is room for one slot (B=8 N=333 H=16 S=128: 20.6 us in a
+// graph, 18.6 with two terms and two slots).
+template <int kT, int kTerms> struct Smem {
+    static constexpr int kSlots = kT * kTerms < 6 ? 2 : 1;
     static constexpr uint32_t kC0 = 0, kB0 = kT * kTile;
     static constexpr uint32_t kX = 3 * kT * kTile;
-    static constexpr uint32_t kXw = kX + 2 * kTile;            // value, remainder
-    static constexpr uint32_t kOut = kXw + 2 * kTile;          // gate, then output
-    static constexpr uint32_t kSb = kOut + 2 * kTile;          // bf16 state, 64 kT rows
+    static constexpr uint32_t kXw = kX + 2 * kTile;            // value, remainder (and its remainder)
+    static constexpr uint32_t kOut = kXw + kTerms * kTile;     // gate, then output
+    static constexpr uint32_t kSb = kOut + kSlots * kTile;     // bf16 state, 64 kT rows
     static constexpr uint32_t kDt = kSb + kT * 64 * 128;
     static constexpr uint32_t kMask = kDt + (kDtRing * sizeof(Decay) + 127) / 128 * 128;
     static constexpr uint32_t kBad = kMask + 32 * 16 * 4;      // diagonal block: 16 words of pairs per row
@@ -131,7 +135,7 @@ template <int kT> struct Smem {
     static constexpr uint32_t kEnd = kMisc + sizeof(Misc);
     static constexpr size_t kBytes = 1024 + kEnd;
 };
-static_assert(Smem<2>::kBytes <= 227 * 1024, "main kernel's shared memory");
+static_assert(Smem<2, 2>::kBytes <= 227 * 1024 && Smem<2, 3>::kBytes <= 227 * 1024, "main kernel's shared memory");
 
 constexpr int kThreads = 640;
 constexpr int kWork = 16;              // warps of the items' steps (two groups); then TMA, MMA, decays, slots
@@ -265,15 +269,18 @@ __device__ __forceinline__ void other_blocks(const float (&blk)[4], float* befor
     *after = (own < 1 ? blk[1] : 0.f) + (own < 2 ? blk[2] : 0.f) + (own < 3 ? blk[3] : 0.f);
 }
 
-// Sixteen weighted values: hi = bf16(w x), lo = bf16(w x - hi).
-__device__ __forceinline__ void weigh16(uint4 a, uint4 b, float w, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+// Sixteen weighted values: hi = bf16(w x), lo = bf16(w x - hi), last = bf16(w x - hi - lo).
+__device__ __forceinline__ void weigh16(uint4 a, uint4 b, float w, uint32_t (&hi)[8], uint32_t (&lo)[8],
+                                        uint32_t (&last)[8]) {
     const uint64_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
     const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint64_t p = mul2(bf2(in[k]), w2);
         hi[k] = pack2(p);
-        lo[k] = pack2(fma2(bf2(hi[k]), minus, p));
+        const uint64_t r = fma2(bf2(hi[k]), minus, p);
+        lo[k] = pack2(r);
+        last[k] = pack2(fma2(bf2(lo[k]), minus, r));
     }
 }
 
@@ -295,13 +302,14 @@ __device__ __forceinline__ uint64_t kmajor_step(uint64_t d, int k) {
     return step_desc(d, (k >> 2) * kTile + (k & 3) * 32);
 }
 
-// (4): state += B^T (hi + lo), issued by one thread; lo is the tile after hi. The second
+// (4): state += B^T (sum of the terms), issued by one thread; their tiles follow one another. The second
 // 64-row atom of the A operand is the tile after B's (for kT = 1 whatever tile follows:
 // those lanes are unused).
+template <int kTerms>
 __device__ __forceinline__ void issue_state(uint32_t dst, uint64_t bt, uint64_t hi) {
     constexpr uint32_t id = idesc_bf16_f32(128, 64, true, true);
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
+    for (int part = 0; part < kTerms; ++part)
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k)
             mma_bf16(dst, step_desc(bt, k * 2048), step_desc(hi, part * kTile + k * 2048), id, 1u);
@@ -379,13 +387,13 @@ __device__ __forceinline__ uint64_t gate2(uint32_t z) {
     return mul2(v, pk2(r0, r1));
 }
 
-template <int kT, bool kGated>
+template <int kT, int kTerms, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap zmap,
                const __grid_constant__ CUtensorMap ymap, const __grid_constant__ ScanArgs a,
                const __grid_constant__ Units un, WsHeader* hdr) {
-    using L = Smem<kT>;
+    using L = Smem<kT, kTerms>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
@@ -393,7 +401,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     Bad* bad = reinterpret_cast<Bad*>(base + L::kBad);
     auto btile = [&](int s) { return base + L::kB0 + s * kT * kTile; };
     auto xtile = [&](int n) { return base + L::kX + (n & 1) * kTile; };
-    auto oslot = [&](int n) { return base + L::kOut + (n & 1) * kTile; };
+    auto oslot = [&](int n) { return base + L::kOut + n % L::kSlots * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Place pl = place(a, un);
     const bool last_seg = pl.seg == a.nseg - 1;
@@ -531,7 +539,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                 for (int k = 0; k < kC / 16; ++k)                                       // (3)
                     mma_bf16_ts(tmem + kTmY1, pt + 8 * k, step_desc(xa, k * 2048), id_y, k > 0);
                 mma_commit(&m.y_full[n & 1]);
-                issue_state(tmem + kTmSt + 64 * u, step_desc(br0, (i & 1) * kT * kTile), xw0);  // (4)
+                issue_state<kTerms>(tmem + kTmSt + 64 * u, step_desc(br0, (i & 1) * kT * kTile), xw0);  // (4)
                 mma_commit(&m.state_done[n & 1]);
                 if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
@@ -598,7 +606,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                 }
                 ++opened;
             };
-            for (int n = 0; n < 2 && n < items && !hold; ++n) open_slot(n / nu, n % nu);
+            for (int n = 0; n < L::kSlots && n < items && !hold; ++n) open_slot(n / nu, n % nu);
             for (int n = 0, i = 0, u = 0; n < items; ++n) {
                 if (!(ok = mbar_wait(&m.y_staged[n & 1], (n >> 1) & 1, max_spin))) break;
                 if (*const_cast<volatile int*>(&bad[u].any) != kNone)
@@ -608,7 +616,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                     tma_store_commit();
                     tma_store_wait_read<0>();
                 }
-                if (n + 2 < items) open_slot((n + 2) / nu, (n + 2) % nu);
+                if (n + L::kSlots < items) open_slot((n + L::kSlots) / nu, (n + L::kSlots) % nu);
                 if (++u == nu) u = 0, ++i;
             }
             // Every gate that was asked for lands before the CTA exits.
@@ -774,13 +782,17 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                 for (int j = 4 * g; j < 4 * g + 4; j += 2) {
                     const uint32_t o0 = piece(j), o1 = piece(j + 1);
                     uint8_t* hi = base + L::kXw;
-                    uint32_t wh[8], wl[8];
+                    uint32_t wh[8], wl[8], wr[8];
                     weigh16(*reinterpret_cast<const uint4*>(xtile(n) + o0), *reinterpret_cast<const uint4*>(xtile(n) + o1), w,
-                            wh, wl);
+                            wh, wl, wr);
                     *reinterpret_cast<uint4*>(hi + o0) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
                     *reinterpret_cast<uint4*>(hi + o1) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
                     *reinterpret_cast<uint4*>(hi + kTile + o0) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
                     *reinterpret_cast<uint4*>(hi + kTile + o1) = make_uint4(wl[4], wl[5], wl[6], wl[7]);
+                    if constexpr (kTerms == 3) {
+                        *reinterpret_cast<uint4*>(hi + 2 * kTile + o0) = make_uint4(wr[0], wr[1], wr[2], wr[3]);
+                        *reinterpret_cast<uint4*>(hi + 2 * kTile + o1) = make_uint4(wr[4], wr[5], wr[6], wr[7]);
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) bits |= wl[e];
                 }
@@ -885,29 +897,30 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 // First pass over segments: end state from zero, sum over the segment of
 // B_j (d_j e^{l(end) - l_j} x_j)^T, and the segment's total decay. Chunks run from
 // the last to the first; the weights carry the sum of the chunks after them.
-// Here the product is taken transposed, (w x)^T B with value and remainder as the two
-// halves of one 128-row operand: D rows 0-63 + rows 64-127, S columns. That reads 64 KB
-// of operands per item instead of the main pass's 96 (which has no TMEM left for it).
+// The three terms of w x stand side by side along N, B^T [hi | lo | last], so that an item
+// reads B once: 80 KB of operands (the main pass, which has no TMEM left for it, takes the
+// terms one after another); D holds S state rows, 64 columns of each term.
 // Warps: TMA, MMA, decays (two), then four weight groups of four: two items at a
 // time, half of the columns each (one group per item left the pass waiting for
-// its weights). A value is written over its x, so that four items fit in flight
-// (two in tiles of their own: 409 against 406 us of the call).
-// What bounds it: shared memory. An item's 32 KB in by TMA, 16 KB read and 32 KB
-// written by the weight groups and 64 KB of operands are 1,152 cycles at 128 bytes
-// each, 1,500 as counted with barriers and factors; it takes about 1,750.
-constexpr int kSumThreads = 640, kSumRing = 4;
+// its weights). Four items' values and two items' terms are in flight.
+// What bounds it: shared memory. An item's 16 KB in by TMA (and 16 of B), 16 KB read and 48 KB
+// written by the weight groups and 80 KB of operands are 1,400 cycles at 128 bytes each.
+constexpr int kSumThreads = 640, kSumRing = 2, kSumX = 4, kSumW = 2, kSumN = 192;
 
 struct SumMisc {
-    uint64_t b_full[2], b_empty[2], x_full[4], xw_full[4], x_empty[4], dt_full[kSumRing], dt_empty[kSumRing], drain;
+    uint64_t b_full[2], b_empty[2], x_full[kSumX], x_empty[kSumX], w_full[kSumW], w_empty[kSumW];
+    uint64_t dt_full[kSumRing], dt_empty[kSumRing], drain;
     uint32_t tmem_slot;
 };
 
 template <int kT> struct SumSmem {
-    static constexpr uint32_t kX = 2 * kT * kTile;             // four slots: x, then its weighted value; remainder
-    static constexpr uint32_t kW = kX + 8 * kTile;
-    static constexpr uint32_t kMisc = kW + kSumRing * kC * 4;
+    static constexpr uint32_t kX = 2 * kT * kTile;
+    static constexpr uint32_t kW = kX + kSumX * kTile;         // three tiles per item
+    static constexpr uint32_t kDt = kW + kSumW * 3 * kTile;
+    static constexpr uint32_t kMisc = kDt + kSumRing * kC * 4;
     static constexpr size_t kBytes = 1024 + kMisc + sizeof(SumMisc);
 };
+static_assert(SumSmem<2>::kBytes <= 227 * 1024, "first pass's shared memory");
 
 template <int kT>
 __global__ void __launch_bounds__(kSumThreads, 1)
@@ -917,9 +930,9 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     SumMisc& m = *reinterpret_cast<SumMisc*>(base + L::kMisc);
-    float* wts = reinterpret_cast<float*>(base + L::kW);
+    float* wts = reinterpret_cast<float*>(base + L::kDt);
     auto btile = [&](int s) { return base + s * kT * kTile; };
-    auto xtile = [&](int n) { return base + L::kX + (n & 3) * 2 * kTile; };
+    auto xtile = [&](int n) { return base + L::kX + n % kSumX * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Place pl = place(a, un);
     const int nu = pl.nu, items = pl.nc * nu, c_last = pl.c0 + pl.nc - 1;
@@ -930,10 +943,15 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
             mbar_init(&m.b_full[s], 1);
             mbar_init(&m.b_empty[s], 1);
         }
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < kSumX; ++s) {
             mbar_init(&m.x_full[s], 1);
-            mbar_init(&m.xw_full[s], 8);
-            mbar_init(&m.x_empty[s], 1);
+            mbar_init(&m.x_empty[s], 8);
+        }
+        for (int s = 0; s < kSumW; ++s) {
+            mbar_init(&m.w_full[s], 8);
+            mbar_init(&m.w_empty[s], 1);
+        }
+        for (int s = 0; s < kSumRing; ++s) {
             mbar_init(&m.dt_full[s], 1);
             mbar_init(&m.dt_empty[s], 8);
         }
@@ -941,7 +959,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(&m.tmem_slot, 128 * kT);
+        tmem_alloc(&m.tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -970,29 +988,32 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
                 for (int u = 0; u < nu; ++u, ++n) {
                     if (i + 3 < pl.nc)
                         tma_prefetch_4d(&xmap, pl.col0(un, u), pl.head(a, un, u), t - 3 * kC, pl.b);
-                    if (n >= 4 && !(ok = mbar_wait(&m.x_empty[n & 3], ((n >> 2) - 1) & 1, max_spin))) break;
-                    mbar_arrive_expect_tx(&m.x_full[n & 3], kTile);
-                    tma_load_4d(xtile(n), &xmap, &m.x_full[n & 3], pl.col0(un, u), pl.head(a, un, u), t, pl.b);
+                    uint64_t* full = &m.x_full[n % kSumX];
+                    if (n >= kSumX && !(ok = mbar_wait(&m.x_empty[n % kSumX], (n / kSumX - 1) & 1, max_spin))) break;
+                    mbar_arrive_expect_tx(full, kTile);
+                    tma_load_4d(xtile(n), &xmap, full, pl.col0(un, u), pl.head(a, un, u), t, pl.b);
                 }
             }
             for (int j = max(i - 2, 0); j < i; ++j) mbar_wait(&m.b_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
-            for (int j = max(n - 4, 0); j < n; ++j) mbar_wait(&m.x_full[j & 3], (j >> 2) & 1, kDefaultMaxSpin);
+            for (int j = max(n - kSumX, 0); j < n; ++j)
+                mbar_wait(&m.x_full[j % kSumX], (j / kSumX) & 1, kDefaultMaxSpin);
         }
     } else if (warp == 1) {
-        constexpr uint32_t id = idesc_bf16_f32(128, 64 * kT, true, true);
+        constexpr uint32_t id = idesc_bf16_f32(128, kSumN, true, true);
         const uint32_t base_a = smem_u32(base);
-        const uint64_t br0 = rows_desc(base_a), xw0 = rows_desc(base_a + L::kX);
+        const uint64_t br0 = rows_desc(base_a), w0 = rows_desc(base_a + L::kW);
         for (int n = 0, i = 0, u = 0; n < items; ++n) {
             if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin) &&
-                       warp_wait(&m.xw_full[n & 3], (n >> 2) & 1, max_spin)))
+                       warp_wait(&m.w_full[n % kSumW], (n / kSumW) & 1, max_spin)))
                 break;
             tc_fence_after();
             if (lane == 0) {
-                const uint64_t bt = step_desc(br0, (i & 1) * kT * kTile), xw = step_desc(xw0, (n & 3) * 2 * kTile);
+                // (For kT = 1 the second 64-row atom of B^T is whatever tile follows: unused lanes.)
+                const uint64_t bt = step_desc(br0, (i & 1) * kT * kTile), w = step_desc(w0, n % kSumW * 3 * kTile);
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k)
-                    mma_bf16(tmem + 64 * kT * u, step_desc(xw, k * 2048), step_desc(bt, k * 2048), id, i > 0 || k > 0);
-                mma_commit(&m.x_empty[n & 3]);
+                    mma_bf16(tmem + kSumN * u, step_desc(bt, k * 2048), step_desc(w, k * 2048), id, i > 0 || k > 0);
+                mma_commit(&m.w_empty[n % kSumW]);
                 if (u == nu - 1) mma_commit(&m.b_empty[i & 1]);
             }
             __syncwarp();
@@ -1036,7 +1057,8 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
         for (int n = grp & 1; n < items; n += 2) {
             const int slot = n % kSumRing, i = n / nu, u = n - i * nu;
             if (!(ok = warp_wait(&m.dt_full[slot], (n / kSumRing) & 1, max_spin) &&
-                       warp_wait(&m.x_full[n & 3], (n >> 2) & 1, max_spin)))
+                       warp_wait(&m.x_full[n % kSumX], (n / kSumX) & 1, max_spin) &&
+                       (n < kSumW || warp_wait(&m.w_empty[n % kSumW], (n / kSumW - 1) & 1, max_spin))))
                 break;
             if (a.lengths && (c_last - i + 1) * kC > pl.n) {
                 if (!(ok = warp_wait(&m.b_full[i & 1], (i >> 1) & 1, max_spin))) break;
@@ -1045,53 +1067,50 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
                     for (int k = 0; k < kT && u == 0; ++k) zero_row(btile(i & 1) + k * kTile, row);
                 }
             }
+            uint8_t* const terms = base + L::kW + n % kSumW * 3 * kTile;
 #pragma unroll
             for (int j = 4 * half; j < 4 * half + 4; j += 2) {
                 const uint32_t o0 = row * 128 + ((j ^ (row & 7)) << 4), o1 = row * 128 + (((j + 1) ^ (row & 7)) << 4);
-                uint32_t h[8], l[8];
+                uint32_t t[3][8];
                 weigh16(*reinterpret_cast<const uint4*>(xtile(n) + o0), *reinterpret_cast<const uint4*>(xtile(n) + o1),
-                        wts[slot * kC + row], h, l);
-                *reinterpret_cast<uint4*>(xtile(n) + o0) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(xtile(n) + o1) = make_uint4(h[4], h[5], h[6], h[7]);
-                *reinterpret_cast<uint4*>(xtile(n) + kTile + o0) = make_uint4(l[0], l[1], l[2], l[3]);
-                *reinterpret_cast<uint4*>(xtile(n) + kTile + o1) = make_uint4(l[4], l[5], l[6], l[7]);
+                        wts[slot * kC + row], t[0], t[1], t[2]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    *reinterpret_cast<uint4*>(terms + k * kTile + o0) = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
+                    *reinterpret_cast<uint4*>(terms + k * kTile + o1) = make_uint4(t[k][4], t[k][5], t[k][6], t[k][7]);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&m.xw_full[n & 3]);
+                mbar_arrive(&m.w_full[n % kSumW]);
+                mbar_arrive(&m.x_empty[n % kSumX]);
                 mbar_arrive(&m.dt_empty[slot]);
             }
         }
-        // The state of unit u: value part (lanes p) plus remainder part (lanes 64 + p), one
-        // state row per column. The upper lane quarters hand theirs over through shared
-        // memory (the operand tiles are free by then), 32 state rows at a time and group.
+        // The state of unit u, the sum of the three terms: a thread has a state row, a group
+        // sixteen of its columns.
         ok = pl.nc == 0 || (ok && warp_wait(&m.drain, 0, max_spin));
-        ok = named_bar_and(1, 512, ok);
         if (ok) {
             tc_fence_after();
-            const uint32_t lanes = (uint32_t)(32 * q) << 16;
-            float* stage = reinterpret_cast<float*>(base) + grp * 32 * 64;       // [32 state rows][64 values]
-            for (int u = 0; u < nu; ++u) {
+            const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + 16 * grp;
+            for (int u = 0; u < nu && q < 2 * kT; ++u) {
                 const int64_t bh = (int64_t)pl.b * a.H + pl.head(a, un, u);
-                const int p0 = pl.col0(un, u), p = 32 * (q & 1) + lane;
-                float* to = a.seeds + (bh * a.nseg + pl.seg) * head_state + p0 + p;
-                for (int s0 = 32 * grp; s0 < 64 * kT; s0 += 128) {               // a group: 32 state rows of 128
-                    uint32_t v[2][16];
-                    tmem_ld16(tmem + lanes + 64 * kT * u + s0, v[0]);
-                    tmem_ld16(tmem + lanes + 64 * kT * u + s0 + 16, v[1]);
-                    tmem_ld_wait();
-                    if (q >= 2)
+                const int p0 = pl.col0(un, u) + 16 * grp;
+                float* to = a.seeds + (bh * a.nseg + pl.seg) * head_state + (int64_t)row * a.P + p0;
+                uint32_t v[3][16];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) stage[k * 64 + p] = __uint_as_float(v[k >> 4][k & 15]);
-                    named_bar(2 + grp, 128);
-                    if (q < 2 && p0 + p < a.P)
+                for (int k = 0; k < 3; ++k) tmem_ld16(at + kSumN * u + 64 * k, v[k]);
+                tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (s0 + k < a.S)
-                                to[(int64_t)(s0 + k) * a.P] =
-                                    pl.nc > 0 ? __uint_as_float(v[k >> 4][k & 15]) + stage[k * 64 + p] : 0.f;
-                    named_bar(2 + grp, 128);
+                for (int c = 0; c < 16; c += 4) {
+                    float f[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        f[k] = pl.nc == 0 ? 0.f
+                                          : __uint_as_float(v[0][c + k]) +
+                                                (__uint_as_float(v[1][c + k]) + __uint_as_float(v[2][c + k]));
+                    if (row < a.S && p0 + c < a.P) *reinterpret_cast<float4*>(to + c) = make_float4(f[0], f[1], f[2], f[3]);
                 }
             }
         }
@@ -1100,7 +1119,7 @@ scan_sums_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 128 * kT);
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // Rows [B, N, outer, inner] of bf16 as a 4-D map with boxes of 64 values x 128 tokens;
@@ -1157,22 +1176,36 @@ Cut pick_cut(int64_t groups, int units, int N) {
     return best;
 }
 
+template <int kT, int kTerms, bool kGated>
+cudaError_t launch_main(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorMap& cm, const CUtensorMap& zm,
+                        const CUtensorMap& ym, const ScanArgs& a, const Units& un, dim3 grid, WsHeader* hdr,
+                        cudaStream_t st) {
+    static std::atomic<int> optin[kMaxDevices];
+    constexpr size_t bytes = Smem<kT, kTerms>::kBytes;
+    const cudaError_t e = ensure_smem_optin(scan_tc_kernel<kT, kTerms, kGated>, (int)bytes, optin);
+    if (e != cudaSuccess) return e;
+    return launch_after(scan_tc_kernel<kT, kTerms, kGated>, grid, kThreads, bytes, st, a.nseg > 1, xm, bm, cm, zm, ym, a, un,
+                        hdr);
+}
+
+// The state that a call returns is summed in three terms: by the first pass and the chaining
+// where there are segments (the main pass's state serves its outputs alone then), else by the
+// main pass.
 template <int kT, bool kGated>
 cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& bm, const CUtensorMap& cm, const CUtensorMap& zm,
-                   const CUtensorMap& ym, const ScanArgs& a, const Units& un, int B, WsHeader* hdr, cudaStream_t st) {
-    static std::atomic<int> optin[kMaxDevices], optin_sums[kMaxDevices];
-    cudaError_t e = ensure_smem_optin(scan_tc_kernel<kT, kGated>, (int)Smem<kT>::kBytes, optin);
-    if (e != cudaSuccess) return e;
+                   const CUtensorMap& ym, ScanArgs a, const Units& un, int B, WsHeader* hdr, cudaStream_t st) {
     const dim3 grid(un.ctas * a.G, a.nseg, B);
     if (a.nseg > 1) {
-        e = ensure_smem_optin(scan_sums_kernel<kT>, (int)SumSmem<kT>::kBytes, optin_sums);
+        static std::atomic<int> optin[kMaxDevices];
+        cudaError_t e = ensure_smem_optin(scan_sums_kernel<kT>, (int)SumSmem<kT>::kBytes, optin);
         if (e != cudaSuccess) return e;
         scan_sums_kernel<kT><<<grid, kSumThreads, SumSmem<kT>::kBytes, st>>>(xm, bm, a, un, hdr);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         if ((e = launch_seeds(a, (int64_t)B * a.H, st)) != cudaSuccess) return e;
+        a.S_out = nullptr;
     }
-    return launch_after(scan_tc_kernel<kT, kGated>, grid, kThreads, Smem<kT>::kBytes, st, a.nseg > 1, xm, bm, cm, zm,
-                        ym, a, un, hdr);
+    return a.S_out ? launch_main<kT, 3, kGated>(xm, bm, cm, zm, ym, a, un, grid, hdr, st)
+                   : launch_main<kT, 2, kGated>(xm, bm, cm, zm, ym, a, un, grid, hdr, st);
 }
 
 }  // namespace
