@@ -11,11 +11,12 @@
 //
 // The recurrence keeps the state in registers: a warp owns 4 kW columns of one
 // head, its 32 lanes 8 row groups x 4 column groups, so a lane holds R = S / 8 rows
-// of kW columns, as packed fp32 row pairs. What bounds it is the FP32 pipe, so the
-// decay is taken out of the inner loop: within eight tokens the state is kept
-// divided by the decay since their start (the update's weight is d_t e^{-l_t}, the
-// read is multiplied by e^{l_t}), two operations per element and token instead of
-// three, and multiplied through once at the end. Where eight tokens decay by more
+// of kW columns, as packed fp32 row pairs. What bounds it are the instructions of the
+// eleven or so warps per SM that the registers leave (issue slots 56 % used in the second
+// pass, 45 % in the first, B=2 N=4000 H=8 P=S=64), so the decay is taken out of the
+// inner loop: within eight tokens the state is kept divided by the decay since their
+// start (the update's weight is d_t e^{-l_t}, the read is multiplied by e^{l_t}), two
+// operations per element and token instead of three, and multiplied through once at the end. Where eight tokens decay by more
 // than e^-40 the plain form runs instead. The eight tokens' reads are summed over
 // the row groups by a butterfly that halves the tokens at each step. With too few
 // heads for the SMs a sequence is cut into segments: a first pass gives each

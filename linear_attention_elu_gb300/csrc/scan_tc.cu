@@ -34,16 +34,17 @@
 // slots (gate in, output in place, TMA store). All hand-offs are mbarriers; every wait
 // is bounded. Loops over columns are kept rolled: the steps' code competes for the
 // instruction cache (the output step unrolled twice cost 6 % of the call).
-// Measured on B=1 N=65536 H=32 P=64 S=128 with a gate, 126 us of HBM time: a form with
-// one warpgroup per step ran 470 us, all sixteen warps on one item 312, two groups 294.
+// Measured on B=1 N=65536 H=32 P=64 S=128 with a gate, 126 us of HBM time: a form of this
+// pass with one warpgroup per step ran 470 us, all sixteen warps on one item 312, two groups
+// 290; the call 416.
 // A second issuing thread, the products issued by predicate instead of by branch, and
 // x kept in registers from the weights to the output all measured slower.
 // Sequences are cut into segments when there are too few units for the SMs: the first
 // pass streams (4) alone, in reverse order of chunks so that the weights reach to the
-// segment's end and nothing has to be rescaled; seeds are chained by csrc/scan.cu, which
+// segment's end and nothing has to be rescaled (a quarter of the call); seeds are chained by csrc/scan.cu, which
 // writes the final state too, and the second pass starts from them.
 // What bounds it: the groups' instructions (about 9,600 of a warp an item of 128 tokens x 64
-// values, 42 % of the issue slots, each warp waiting on its own chain of TMEM reads,
+// values, 44 % of the issue slots, each warp waiting on its own chain of TMEM reads,
 // exponentials and hand-offs) next to the products' operand reads from shared memory
 // (196 KB an item at 128 bytes a cycle).
 #include <cuda.h>

@@ -4,8 +4,9 @@
 // rows) and for single tokens (the state shifted in place).
 //
 // What bounds it: each value is read once and written once, W multiply-adds and
-// one silu each: HBM bandwidth, with the silus' exponentials and reciprocals close
-// behind (142 M of them in 31 us at B=4 N=4096 C=4352). A thread owns one 16-byte
+// one silu each: HBM bandwidth (76 % of the copy rate at B=4 N=4096 C=4352), with the
+// issue slots behind it (59 % used, a third of the instructions the silus'; 86 % of the
+// copy rate without them). A thread owns one 16-byte
 // piece of a row (8 bf16 or 4 fp32 channels) and walks consecutive tokens with the
 // last W - 1 rows in registers, so a row is read again only by the neighbouring
 // thread of the next token group (W - 1 rows in 64 at best, from L2). Channels that are not
