@@ -510,7 +510,10 @@ la_status la_short_conv_step(const void* x, int64_t x_batch, const void* w, cons
  *    held in fp32 throughout; what a token adds to it enters S_out as three bf16 terms
  *    (2^-25 of it is left), and what only y reads as two (2^-17).
  *  - A, D, step_bias: [H] float32; A is the (negative) rate itself. d_t A_h <= 0 is
- *    expected (the state must not grow); nothing checks it.
+ *    expected (the state must not grow); nothing checks it. With the softplus, a step
+ *    of minus infinity or of a type's lowest value masks its token: d_t = 0, the state
+ *    stays as it is (left padding, say, which lengths cannot express). An infinity or
+ *    NaN in a token's x reaches no earlier output.
  *  - S0 [B, H, S, P] float32 (nullable: zero): state before the first token; S_out
  *    (nullable): state after the last. S_out == S0 updates it in place; any other
  *    overlap is LA_ERR_INVALID_ARG.
