@@ -789,9 +789,10 @@ def la_selective_scan_fwd(x, step, A, Bm, Cm, D=None, z=None, dt_bias=None, soft
     """Selective scan of x [B,N,H,P] with step sizes [B,N,H], rates A [H], Bm, Cm [B,N,G,S].
 
     y_t = (C_t^T S_t + D x_t) silu(z_t) with S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T and
-    d_t = softplus(step_t + dt_bias); a step of minus infinity masks its token. S0, S_out [B,H,S,P] float32 (S_out may be S0). lengths
-    (int32 [B]): rows past them are left as they are (zero where the call makes y). Token rows may
-    be strided (column ranges of a projection). Returns y [B,N,H,P]."""
+    d_t = softplus(step_t + dt_bias); a step of minus infinity masks its token. S0, S_out [B,H,S,P]
+    float32 (S_out may be S0). lengths (int32 [B]): rows past them are left as they are (zero where
+    the call makes y). Token rows may be strided (column ranges of a projection). Returns y
+    [B,N,H,P]."""
     index, (B, N, H, P), G, S = _scan_args(x, step, A, Bm, Cm, D, z, dt_bias, 2)
     _f32_state(S0, (B, H, S, P), "S0")
     _f32_state(S_out, (B, H, S, P), "S_out")
