@@ -73,7 +73,9 @@ typedef enum {
     LA_OP_CAUSAL_BWD = 3,
     LA_OP_NONCAUSAL_BWD = 4,
     LA_OP_LAYER_DECODE = 5,
-    LA_OP_SELECTIVE_SCAN = 6   /* Dk = S, Dv = P */
+    LA_OP_SELECTIVE_SCAN = 6,  /* Dk = S, Dv = P */
+    LA_OP_DECAY_ATTN = 8,      /* 7 names no operation */
+    LA_OP_DECAY_ATTN_BWD = 9
 } la_op;
 
 /*
@@ -110,6 +112,7 @@ la_status la_workspace_size(la_op op, int B, int H, int N, int Dk, int Dv, la_dt
  * graph planning and for counting launches in a timed region.
  * LA_OP_SELECTIVE_SCAN: for one group and 16-byte aligned rows; a call with more
  * groups or unaligned rows makes one launch or three by its own cut.
+ * LA_OP_DECAY_ATTN(_BWD): for 16-byte aligned rows.
  */
 la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtype dt,
                           int* launches);
@@ -546,6 +549,107 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
                                  const void* z, int64_t z_batch, const float* step_bias,
                                  int softplus, float* S_inout, void* y, int64_t y_batch, int B,
                                  int H, int G, int S, int P, la_dtype dt, la_stream_t stream);
+
+/*
+ * Causal linear attention whose state decays by a factor of its head per token: the
+ * recurrence of "Why Replace Attention? The Softmax Bottleneck and the Path to Linear
+ * Time", section 7.2, steps 1-4, with a decay, and without feature map (features are
+ * the caller's, as with LA_PHI_IDENTITY) and denominator, whose place a norm of the
+ * outputs takes (la_group_norm_fwd). Per head h, f_h = exp(decay_h):
+ *   S_t = f_h S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *  - q, k: rows of [B, H, N, Dk], v, o: rows of [B, H, N, Dv], dtype dt, each row's values
+ *    adjacent. strides: HOST array of (batch, head, token) strides in elements of q, k, v
+ *    and o, in this order: head-major tensors, column ranges of a token-major projection,
+ *    and (inputs) strides of 0 for what heads or sequences share. 1 <= Dk, Dv <= 128;
+ *    B H <= 65535; N <= 2^30.
+ *  - decay: [H] float32, device, the logarithm of the factor per token, <= 0 (minus
+ *    infinity: no token reaches another). Nothing checks it. scale: finite.
+ *  - S0 [B, H, Dk, Dv] float32 (nullable: zero): state before the first token; S_out
+ *    (nullable): state after the last. S_out == S0 updates it in place; any other
+ *    overlap is LA_ERR_INVALID_ARG. The state has the layout of la_decode_step's S.
+ *  - lengths [B] int32, device (nullable): sequence b has lengths[b] tokens (clamped to
+ *    0..N). Rows past it are not written and nothing in them counts, but they may be read,
+ *    in whole tiles of 128: nothing else may write them meanwhile. A sequence of no tokens
+ *    keeps its state.
+ *  - Arithmetic is fp32, and o is rounded once, but for bf16 with Dk and Dv multiples of 8
+ *    and 16-byte aligned rows and states, which runs on the tensor cores: there the weighted
+ *    scores within 128 tokens, and the state where o reads it, are rounded to bf16 as well
+ *    (half a step, 2^-8, of each term). The state is held in fp32; what a token adds to it
+ *    enters S_out as three bf16 terms and what only o reads as two.
+ *  - An infinity or NaN in a token's row reaches no output of an earlier token.
+ *  - o and S_out must not overlap an input (but S_out == S0), one another or the workspace,
+ *    and o's rows must not overlap among themselves (LA_ERR_INVALID_ARG).
+ *  - workspace: la_workspace_size(LA_OP_DECAY_ATTN, B, H, N, Dk, Dv, dt, ...) bytes,
+ *    256-byte aligned, initialised once with la_workspace_init. Calls that overlap in time
+ *    need workspaces of their own.
+ */
+la_status la_decay_attn_fwd(const void* q, const void* k, const void* v, const float* decay, float scale,
+                            const int32_t* lengths, const float* S0, float* S_out, void* o,
+                            const int64_t* strides, int B, int H, int N, int Dk, int Dv, la_dtype dt,
+                            void* workspace, size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * Backward, for sequences that start from a state of zero: from dout = dL/do
+ *   dq_i = scale sum_{j <= i} f^(i-j) (dout_i . v_j) k_j
+ *   dk_j = scale sum_{i >= j} f^(i-j) (dout_i . v_j) q_i
+ *   dv_j = scale sum_{i >= j} f^(i-j) (q_i . k_j) dout_i
+ * three sums of the forward pass's form, two of them backwards in time; no state and no
+ * output of the forward pass is needed. The decay is taken as a constant.
+ *  - strides: HOST array of (batch, head, token) of q, k, v, dout, dq, dk, dv, in this order.
+ *  - lengths, arithmetic and refusals as above; rows of dq, dk and dv past a sequence's
+ *    length are not written. dq, dk and dv must not overlap an input or one another.
+ *  - workspace: la_workspace_size(LA_OP_DECAY_ATTN_BWD, ...).
+ */
+la_status la_decay_attn_bwd(const void* q, const void* k, const void* v, const void* dout, const float* decay,
+                            float scale, const int32_t* lengths, void* dq, void* dk, void* dv,
+                            const int64_t* strides, int B, int H, int N, int Dk, int Dv, la_dtype dt,
+                            void* workspace, size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * One token per sequence: q, k rows of [B, H, Dk], v, o of [B, H, Dv]; strides: HOST array
+ * of (batch, head) of q, k, v, o. S [B, H, Dk, Dv] float32 is updated in place, 16-byte
+ * aligned where Dv is a multiple of 4. o may be q, k or v itself (the same rows); nothing
+ * else may overlap o or S. Needs no workspace; asynchronous on `stream`.
+ */
+la_status la_decay_attn_step(const void* q, const void* k, const void* v, const float* decay, float scale,
+                             float* S_inout, void* o, const int64_t* strides, int B, int H, int Dk, int Dv,
+                             la_dtype dt, la_stream_t stream);
+
+/*
+ * Group norm over channels-last rows, with an optional silu and an optional gate. The pages
+ * have no counterpart: it is the norm behind attention without a denominator (N = 1: every
+ * row a sample, a group per head), and that of images in front of it (N = height x width).
+ * Per sample and group of C / G neighbouring channels, mean and var over N C / G values:
+ *   xh = (x - mean) r, r = 1 / sqrt(var + eps),  u = w_c xh + b_c,  y = act(u) silu(z)
+ *   (w null: 1; b null: 0; act = silu or identity; z null: factor 1)
+ *  - x, z, y: rows of [B, N, C] with batch and token strides in elements (a row's values
+ *    adjacent); w, b: [C]; all dtype dt. stats [B, G, 2] float32 (nullable): (mean, r), which
+ *    the backward takes. C a multiple of G; B N <= 2^30; C / G <= 1024, and with N = 1 and
+ *    rows that are not whole 16-byte pieces C / G <= 128 (LA_ERR_UNSUPPORTED).
+ *  - fp32 arithmetic, one rounding; statistics about the means, so that a large mean costs
+ *    no digits. Sums in a fixed order: the same inputs give the same bits.
+ *  - y and stats must not overlap an input, one another or the workspace (LA_ERR_INVALID_ARG).
+ *  - workspace: la_group_norm_workspace_size() bytes (both directions), 256-byte aligned, no
+ *    initialisation; the forward pass needs none for N = 1. Asynchronous on `stream`.
+ * Backward, from dy = dL/dy with h = dy silu(z) act'(u), means over the group:
+ *   dx = r (w h - mean(w h) - xh mean(w h xh)),  dz = dy act(u) silu'(z),
+ *   dw = sum h xh,  db = sum h   (float32 [C], nullable)
+ *  - dx, dz: rows with strides of their own (dz exactly where z is); no output may overlap
+ *    an input or another output. Without samples or tokens dw and db are zero.
+ */
+la_status la_group_norm_workspace_size(int B, int N, int C, int G, size_t* bytes);
+
+la_status la_group_norm_fwd(const void* x, int64_t x_batch, int64_t x_token, const void* w, const void* b,
+                            const void* z, int64_t z_batch, int64_t z_token, void* y, int64_t y_batch,
+                            int64_t y_token, float* stats, int B, int N, int C, int G, la_dtype dt, int silu,
+                            float eps, void* workspace, size_t workspace_bytes, la_stream_t stream);
+
+la_status la_group_norm_bwd(const void* x, int64_t x_batch, int64_t x_token, const void* w, const void* b,
+                            const void* z, int64_t z_batch, int64_t z_token, const void* dy, int64_t dy_batch,
+                            int64_t dy_token, const float* stats, void* dx, int64_t dx_batch, int64_t dx_token,
+                            void* dz, int64_t dz_batch, int64_t dz_token, float* dw, float* db, int B, int N,
+                            int C, int G, la_dtype dt, int silu, void* workspace, size_t workspace_bytes,
+                            la_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears the workspace status word.

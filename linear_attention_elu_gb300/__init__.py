@@ -29,11 +29,15 @@ __all__ = [
     "la_qk_norm_rope_fwd", "la_qk_norm_rope_bwd", "la_qk_norm_rope_bwd_workspace_size",
     "qk_norm_rope_workspace", "la_short_conv_fwd", "la_short_conv_step",
     "LA_OP_SELECTIVE_SCAN", "la_selective_scan_fwd", "la_selective_scan_step",
+    "LA_OP_DECAY_ATTN", "LA_OP_DECAY_ATTN_BWD", "la_decay_attn_fwd", "la_decay_attn_bwd",
+    "la_decay_attn_step", "la_group_norm_fwd", "la_group_norm_bwd", "la_group_norm_workspace_size",
+    "group_norm_workspace",
 ]
 
 LA_F32, LA_BF16 = 0, 1
 LA_OP_NONCAUSAL, LA_OP_CAUSAL, LA_OP_DECODE, LA_OP_CAUSAL_BWD, LA_OP_NONCAUSAL_BWD = 0, 1, 2, 3, 4
 LA_OP_LAYER_DECODE, LA_OP_SELECTIVE_SCAN = 5, 6
+LA_OP_DECAY_ATTN, LA_OP_DECAY_ATTN_BWD = 8, 9
 LA_PHI_ELU1, LA_PHI_IDENTITY = 0, 1
 LA_ROPE_HALVES, LA_ROPE_INTERLEAVED, LA_ROPE_MAX_AXES = 0, 1, 4
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_WORKSPACE, LA_ERR_CUDA, LA_ERR_TIMEOUT = 0, 1, 2, 3, 4, 5
@@ -126,6 +130,19 @@ def _load():
     lib.la_selective_scan_step.argtypes = [P, L, P, L, P, P, L, P, L, P, P, L, P, I, P, P, L, I, I, I,
                                            I, I, I, P]
     lib.la_selective_scan_step.restype = I
+    lib.la_decay_attn_fwd.argtypes = [P, P, P, P, F, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]
+    lib.la_decay_attn_fwd.restype = I
+    lib.la_decay_attn_bwd.argtypes = [P, P, P, P, P, F, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]
+    lib.la_decay_attn_bwd.restype = I
+    lib.la_decay_attn_step.argtypes = [P, P, P, P, F, P, P, P, I, I, I, I, I, P]
+    lib.la_decay_attn_step.restype = I
+    lib.la_group_norm_workspace_size.argtypes = [I, I, I, I, ctypes.POINTER(Z)]
+    lib.la_group_norm_workspace_size.restype = I
+    lib.la_group_norm_fwd.argtypes = [P, L, L, P, P, P, L, L, P, L, L, P, I, I, I, I, I, I, F, P, Z, P]
+    lib.la_group_norm_fwd.restype = I
+    lib.la_group_norm_bwd.argtypes = [P, L, L, P, P, P, L, L, P, L, L, P, P, L, L, P, L, L, P, P, I, I, I, I, I,
+                                      I, P, Z, P]
+    lib.la_group_norm_bwd.restype = I
     lib.la_query_status.argtypes = [P, P]
     lib.la_query_status.restype = I
     return lib
@@ -836,6 +853,197 @@ def la_selective_scan_step(x, step, A, Bm, Cm, S, D=None, z=None, dt_bias=None, 
             cs[0], _addr(D), _addr(z), zs[0], _addr(dt_bias), 1 if softplus else 0, S.data_ptr(),
             y.data_ptr(), ys[0], B, H, G, Sn, P, _dt(x), _raw_stream(index)), "la_selective_scan_step")
     return y
+
+
+def _decay_args(q, k, v, decay, dims):
+    """Checks shared by the prompt (dims = 4: [B,H,N,D]) and the step (3: [B,H,D]); returns
+    (device index, shape of q, Dv)."""
+    qshape, vshape, dtype = q.shape, v.shape, q.dtype
+    if len(qshape) != dims or k.shape != qshape or len(vshape) != dims or vshape[:-1] != qshape[:-1]:
+        lead = "B,H,N" if dims == 4 else "B,H"
+        raise ValueError(f"expected q, k [{lead},Dk] and v [{lead},Dv]; got {tuple(qshape)}, "
+                         f"{tuple(k.shape)}, {tuple(vshape)}")
+    if k.dtype != dtype or v.dtype != dtype:
+        raise TypeError("q, k and v must share one dtype")
+    _dt(q)
+    index = _device_of(q)
+    if decay.dtype != torch.float32 or decay.dim() != 1 or decay.shape[0] != qshape[1] or not decay.is_contiguous():
+        raise ValueError("decay must be contiguous float32 [H]")
+    _same_device(index, k, v, decay)
+    return index, qshape, vshape[-1]
+
+
+def _row_strides(*named):
+    """The strides of all axes but the last (whose values must be adjacent), as the C entries take them."""
+    out = []
+    for t, what in named:
+        out += _inner_adjacent(t, what, 1)[:-1]
+    return (ctypes.c_int64 * len(out))(*out)
+
+
+def _typed_like(t, ref, what):
+    if t.shape != ref.shape or t.dtype != ref.dtype:
+        raise ValueError(f"{what} must be shaped and typed like its input")
+
+
+def la_decay_attn_fwd(q, k, v, decay, scale=1.0, lengths=None, S0=None, S_out=None, o=None, ws=None, stream=None):
+    """Causal linear attention with a decay per head: o_t = scale S_t^T q_t, S_t = e^decay S_{t-1} + k_t v_t^T.
+
+    q, k [B,H,N,Dk], v [B,H,N,Dv]: any batch, head and token strides (column ranges of a projection,
+    transposed to head-major; a row's values adjacent). decay: float32 [H], the logarithm of the factor
+    per token. S0, S_out [B,H,Dk,Dv] float32 (S_out may be S0). lengths (int32 [B]): rows past them are
+    left as they are (zero where the call makes o). Returns o [B,H,N,Dv]."""
+    index, (B, H, N, Dk), Dv = _decay_args(q, k, v, decay, 4)
+    _f32_state(S0, (B, H, Dk, Dv), "S0")
+    _f32_state(S_out, (B, H, Dk, Dv), "S_out")
+    _check_lengths(lengths, B)
+    with _scope(index, stream):
+        if o is None:
+            make = torch.empty if lengths is None else torch.zeros
+            o = make((B, H, N, Dv), dtype=q.dtype, device=q.device)
+        _typed_like(o, v, "o")
+        if ws is None:
+            ws = workspace(LA_OP_DECAY_ATTN, B, H, N, Dk, Dv, q.dtype, q.device)
+        _same_device(index, lengths, S0, S_out, o, ws)
+        _check(_lib.la_decay_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), scale, _addr(lengths), _addr(S0),
+            _addr(S_out), o.data_ptr(), _row_strides((q, "q"), (k, "k"), (v, "v"), (o, "o")), B, H, N, Dk, Dv,
+            _dt(q), ws.data_ptr(), _bytes(ws), _raw_stream(index)), "la_decay_attn_fwd")
+    return o
+
+
+def la_decay_attn_bwd(q, k, v, dout, decay, scale=1.0, lengths=None, dq=None, dk=None, dv=None, ws=None,
+                      stream=None):
+    """Gradients (dq, dk, dv) of sum(o * dout) of la_decay_attn_fwd without states (decay a constant).
+
+    Strides as there; dq, dk and dv may be given as column ranges of one projection gradient. Rows past
+    the lengths are left as they are (zero where the call makes them)."""
+    index, (B, H, N, Dk), Dv = _decay_args(q, k, v, decay, 4)
+    _typed_like(dout, v, "dout")
+    _check_lengths(lengths, B)
+    with _scope(index, stream):
+        make = torch.empty if lengths is None else torch.zeros
+        grads = [make(x.shape, dtype=x.dtype, device=x.device) if t is None else t
+                 for t, x in ((dq, q), (dk, k), (dv, v))]
+        for t, x, what in zip(grads, (q, k, v), ("dq", "dk", "dv")):
+            _typed_like(t, x, what)
+        dq, dk, dv = grads
+        if ws is None:
+            ws = workspace(LA_OP_DECAY_ATTN_BWD, B, H, N, Dk, Dv, q.dtype, q.device)
+        _same_device(index, dout, lengths, dq, dk, dv, ws)
+        strides = _row_strides((q, "q"), (k, "k"), (v, "v"), (dout, "dout"), (dq, "dq"), (dk, "dk"), (dv, "dv"))
+        _check(_lib.la_decay_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), decay.data_ptr(), scale, _addr(lengths),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), strides, B, H, N, Dk, Dv, _dt(q), ws.data_ptr(), _bytes(ws),
+            _raw_stream(index)), "la_decay_attn_bwd")
+    return dq, dk, dv
+
+
+def la_decay_attn_step(q, k, v, decay, S, scale=1.0, o=None, stream=None):
+    """One token of la_decay_attn_fwd: q, k [B,H,Dk], v [B,H,Dv]; S [B,H,Dk,Dv] in place; returns o [B,H,Dv]."""
+    index, (B, H, Dk), Dv = _decay_args(q, k, v, decay, 3)
+    if S is None:
+        raise ValueError("S must be given")
+    _f32_state(S, (B, H, Dk, Dv), "S")
+    with _scope(index, stream):
+        if o is None:
+            o = torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
+        _typed_like(o, v, "o")
+        _same_device(index, S, o)
+        _check(_lib.la_decay_attn_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), scale, S.data_ptr(), o.data_ptr(),
+            _row_strides((q, "q"), (k, "k"), (v, "v"), (o, "o")), B, H, Dk, Dv, _dt(q), _raw_stream(index)),
+            "la_decay_attn_step")
+    return o
+
+
+def la_group_norm_workspace_size(B, N, C, G):
+    """Workspace bytes of la_group_norm_fwd and la_group_norm_bwd."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.la_group_norm_workspace_size(B, N, C, G, ctypes.byref(n)), "la_group_norm_workspace_size")
+    return int(n.value)
+
+
+def group_norm_workspace(B, N, C, G, device=None):
+    """Allocates (through PyTorch) the workspace of the group norm, both directions; it needs no initialisation."""
+    n = la_group_norm_workspace_size(B, N, C, G)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def _norm_args(x, groups, w, b, z):
+    """Checks shared by both directions; returns (device index, B, N, C)."""
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 3 or groups < 1 or shape[2] % groups:
+        raise ValueError(f"expected x [B,N,C] with C a multiple of groups; got {tuple(shape)}, {groups} groups")
+    _dt(x)
+    index = _device_of(x)
+    for t, what in ((w, "w"), (b, "b")):
+        if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != shape[2] or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous [C] in x's dtype")
+    if z is not None:
+        _typed_like(z, x, "z")
+    _same_device(index, w, b, z)
+    return index, shape[0], shape[1], shape[2]
+
+
+def la_group_norm_fwd(x, groups, w=None, b=None, z=None, silu=False, eps=1e-5, y=None, stats=None,
+                      return_stats=False, ws=None, stream=None):
+    """Group norm of channels-last rows x [B,N,C]: y = act(w xh + b) silu(z), statistics over N and C / groups.
+
+    silu: act is the silu (else the identity); z [B,N,C]: the gate. A row of its own per sample (the
+    heads of an attention output, tokens as samples) is N = 1. Rows may be strided. Returns y, or
+    (y, stats) with return_stats=True: stats [B,groups,2] float32 (mean, inverse deviation)."""
+    index, B, N, C = _norm_args(x, groups, w, b, z)
+    xs = _inner_adjacent(x, "x", 1)
+    zs = _inner_adjacent(z, "z", 1) if z is not None else (0, 0)
+    with _scope(index, stream):
+        if y is None:
+            y = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+        ys = _like(y, x, 1)
+        if stats is None and return_stats:
+            stats = torch.empty((B, groups, 2), dtype=torch.float32, device=x.device)
+        _f32_state(stats, (B, groups, 2), "stats")
+        if ws is None and N != 1:
+            ws = group_norm_workspace(B, N, C, groups, x.device)
+        _same_device(index, y, stats, ws)
+        _check(_lib.la_group_norm_fwd(
+            x.data_ptr(), xs[0], xs[1], _addr(w), _addr(b), _addr(z), zs[0], zs[1], y.data_ptr(), ys[0], ys[1],
+            _addr(stats), B, N, C, groups, _dt(x), 1 if silu else 0, eps, _addr(ws), _bytes(ws),
+            _raw_stream(index)), "la_group_norm_fwd")
+    return (y, stats) if return_stats else y
+
+
+def la_group_norm_bwd(x, groups, dy, stats, w=None, b=None, z=None, silu=False, dx=None, dz=None, ws=None,
+                      stream=None):
+    """Gradients (dx, dw, db, dz) of sum(y * dy) of la_group_norm_fwd; stats: as it returns them.
+
+    dx, dz [B,N,C] in x's dtype (dz None without a gate); dw, db float32 [C] (None without w, b)."""
+    index, B, N, C = _norm_args(x, groups, w, b, z)
+    _typed_like(dy, x, "dy")
+    if stats is None:
+        raise ValueError("stats must be given")
+    _f32_state(stats, (B, groups, 2), "stats")
+    if dz is not None and z is None:
+        raise ValueError("dz needs z")
+    xs, gs = _inner_adjacent(x, "x", 1), _inner_adjacent(dy, "dy", 1)
+    zs = _inner_adjacent(z, "z", 1) if z is not None else (0, 0)
+    with _scope(index, stream):
+        if dx is None:
+            dx = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+        if dz is None and z is not None:
+            dz = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
+        dxs = _like(dx, x, 1)
+        dzs = _like(dz, x, 1) if dz is not None else (0, 0)
+        dw = torch.empty(C, dtype=torch.float32, device=x.device) if w is not None else None
+        db = torch.empty(C, dtype=torch.float32, device=x.device) if b is not None else None
+        if ws is None:
+            ws = group_norm_workspace(B, N, C, groups, x.device)
+        _same_device(index, dy, stats, dx, dz, ws)
+        _check(_lib.la_group_norm_bwd(
+            x.data_ptr(), xs[0], xs[1], _addr(w), _addr(b), _addr(z), zs[0], zs[1], dy.data_ptr(), gs[0], gs[1],
+            stats.data_ptr(), dx.data_ptr(), dxs[0], dxs[1], _addr(dz), dzs[0], dzs[1], _addr(dw), _addr(db), B, N,
+            C, groups, _dt(x), 1 if silu else 0, _addr(ws), _bytes(ws), _raw_stream(index)), "la_group_norm_bwd")
+    return dx, dw, db, dz
 
 
 def la_query_status(ws, stream=None):

@@ -37,6 +37,8 @@ la_status check_eps(float eps) {
     return (isfinite(eps) && eps >= 0.f) ? LA_OK : LA_ERR_INVALID_ARG;
 }
 
+bool is_decay(la_op op) { return op == LA_OP_DECAY_ATTN || op == LA_OP_DECAY_ATTN_BWD; }
+
 size_t body_bytes(la_op op, int B, int H, int N, int Dk, int Dv, la_dtype dt) {
     const int64_t BH = (int64_t)B * H;
     if (BH == 0 || N == 0) return 0;
@@ -54,6 +56,9 @@ size_t body_bytes(la_op op, int B, int H, int N, int Dk, int Dv, la_dtype dt) {
             return la::layer_workspace(B, H, Dk, dt);
         case LA_OP_SELECTIVE_SCAN:
             return la::scan_workspace(B, H, N, Dk, Dv, dt);
+        case LA_OP_DECAY_ATTN:
+        case LA_OP_DECAY_ATTN_BWD:
+            return la::decay_workspace(B, H, N, Dk, Dv, dt, op == LA_OP_DECAY_ATTN_BWD);
         default:
             return 0;
     }
@@ -152,12 +157,12 @@ la_status la_workspace_size(la_op op, int B, int H, int N, int Dk, int Dv, la_dt
     if (!bytes) return LA_ERR_INVALID_ARG;
     if (op != LA_OP_CAUSAL && op != LA_OP_NONCAUSAL && op != LA_OP_DECODE &&
         op != LA_OP_CAUSAL_BWD && op != LA_OP_NONCAUSAL_BWD && op != LA_OP_LAYER_DECODE &&
-        op != LA_OP_SELECTIVE_SCAN)
+        op != LA_OP_SELECTIVE_SCAN && !is_decay(op))
         return LA_ERR_INVALID_ARG;
     const bool one_token = op == LA_OP_DECODE || op == LA_OP_LAYER_DECODE;
     la_status s = check_common(B, H, one_token ? 1 : N, Dk, Dv, dt);
     if (s != LA_OK) return s;
-    if (op == LA_OP_SELECTIVE_SCAN && N > la::kScanMaxTokens) return LA_ERR_UNSUPPORTED;
+    if ((op == LA_OP_SELECTIVE_SCAN || is_decay(op)) && N > la::kScanMaxTokens) return LA_ERR_UNSUPPORTED;
     if (op == LA_OP_LAYER_DECODE) {
         if (Dk != Dv) return LA_ERR_UNSUPPORTED;
         *bytes = kHeaderBytes + round_up(body_bytes(op, B, H, 1, Dk, Dv, dt), 256);
@@ -179,12 +184,12 @@ la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtyp
     if (!launches) return LA_ERR_INVALID_ARG;
     if (op != LA_OP_CAUSAL && op != LA_OP_NONCAUSAL && op != LA_OP_DECODE &&
         op != LA_OP_CAUSAL_BWD && op != LA_OP_NONCAUSAL_BWD && op != LA_OP_LAYER_DECODE &&
-        op != LA_OP_SELECTIVE_SCAN)
+        op != LA_OP_SELECTIVE_SCAN && !is_decay(op))
         return LA_ERR_INVALID_ARG;
     const bool one_token = op == LA_OP_DECODE || op == LA_OP_LAYER_DECODE;
     la_status s = check_common(B, H, one_token ? 1 : N, Dk, Dv, dt);
     if (s != LA_OK) return s;
-    if (op == LA_OP_SELECTIVE_SCAN && N > la::kScanMaxTokens) return LA_ERR_UNSUPPORTED;
+    if ((op == LA_OP_SELECTIVE_SCAN || is_decay(op)) && N > la::kScanMaxTokens) return LA_ERR_UNSUPPORTED;
     const int64_t BH = (int64_t)B * H;
     if (BH == 0 || (!one_token && N == 0)) {
         *launches = 0;
@@ -196,6 +201,8 @@ la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtyp
         *launches = 1;
     else if (op == LA_OP_SELECTIVE_SCAN)
         *launches = la::scan_launches(B, H, N, Dk, Dv, dt);
+    else if (is_decay(op))
+        *launches = la::decay_launches(B, H, N, Dk, Dv, dt, op == LA_OP_DECAY_ATTN_BWD);
     else if (op == LA_OP_CAUSAL_BWD || op == LA_OP_NONCAUSAL_BWD)
         *launches = 5;
     else if (op == LA_OP_CAUSAL && la::tc_causal_supported(Dk, Dv, dt))

@@ -1,0 +1,593 @@
+// Causal linear attention whose state decays by a factor of its head per token:
+//   S_t = e^{l_h} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+// ("Why Replace Attention? The Softmax Bottleneck and the Path to Linear Time",
+// section 7.2, steps 1-4, with a decay of the state; features are the caller's and
+// there is no denominator: a norm of the outputs takes its place).
+//
+// With o = F(q, k, v), F(a, b, c)_t = scale sum_{u <= t} e^{l (t - u)} (a_t . b_u) c_u,
+// the gradients are sums of the same form:
+//   dq = F(dout, v, k),  dk = F'(v, dout, q),  dv = F'(k, q, dout)
+// with F' the sum over u >= t: so one kernel, run forwards or backwards in time, is
+// the forward pass and its whole gradient, and no state is stored.
+//
+// This file: fp32 arithmetic on the CUDA cores for every type, width and stride, the
+// single-token step, the chaining of segments and the entry points. bf16 with whole
+// 16-byte rows runs on the tensor cores instead (csrc/decay_tc.cu).
+//
+// Chunks of 64 tokens in shared memory, 64 columns of c per block, 256 threads of 4 x 4
+// outputs each:
+//   P = weighted, masked A B^T;   O = P C + e^{l (i + 1)} A S;   S = e^{64 l} S + (w B)^T C
+// with S in registers between chunks. What bounds it: the products' operand reads from
+// shared memory (two 16-byte reads per 16 multiply-adds). Sequences are cut into segments
+// when there are too few heads for the SMs: a first pass gives each segment's end state
+// from zero, a chain over the segments their start states, and the second pass starts
+// from those.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "decay.cuh"
+#include "kernels.h"
+#include "overlap.h"
+#include "scan.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+
+using namespace decay;
+
+namespace {
+
+constexpr int kL = 64;              // tokens per chunk, columns per block
+constexpr int kRow = kL + 4;        // floats of a row in shared memory
+
+// kD: 64-row tiles of the state. Tokens and widths past the end are zero.
+template <int kD> struct Shared {
+    float at[64 * kD * kRow];       // A^T, [d][token]
+    float bt[64 * kD * kRow];       // B^T
+    float sm[64 * kD * kRow];       // S, [d][column]
+    float pt[kL * kRow];            // P^T, [u][t]
+};
+template <int kD> struct Common {
+    float bn[kL * (64 * kD + 4)];   // w B, [token][d]
+    float cn[kL * kRow];            // C, [token][column]
+    float pw[kL + 4];               // e^{l k}
+};
+
+// Rows [tok][col0 .. col0 + 8 nblk) of x, transposed to dst[col][tok] or as they are. A
+// warp takes 4 tokens x 8 columns at a time: whole 32-byte pieces, and no two lanes of
+// a transposed store in one bank.
+template <typename T, bool kTransposed, typename Place>
+__device__ __forceinline__ void stage(const T* x, Place row, int m, int width, int cols, float* dst, int stride,
+                                      const float* weight) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = cols / 8;
+    for (int it = warp; it < blocks * (kL / 4); it += 8) {
+        const int d = 8 * (it % blocks) + (lane & 7), t = 4 * (it / blocks) + (lane >> 3);
+        float v = t < m && d < width ? to_f(x[row(t) + d]) : 0.f;
+        if (weight) v *= weight[t < m ? m - 1 - t : 0];
+        if (kTransposed) dst[d * stride + t] = v;
+        else dst[t * stride + d] = v;
+    }
+}
+
+__device__ __forceinline__ void outer(float (&acc)[4][4], const float* x, const float* y) {
+    const float4 u = *reinterpret_cast<const float4*>(x), v = *reinterpret_cast<const float4*>(y);
+    const float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+}
+
+// Grid: (segments, 64-column blocks, B H). kState: only the segment's end state from zero
+// (first pass, every segment but the last).
+template <typename T, int kD, bool kState>
+__global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args a) {
+    extern __shared__ float smem[];
+    Common<kD>& s = *reinterpret_cast<Common<kD>*>(smem);
+    Shared<kD>& x = *reinterpret_cast<Shared<kD>*>(smem + sizeof(Common<kD>) / sizeof(float));
+    constexpr int kB = 64 * kD + 4;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int seg = blockIdx.x, col0 = kL * blockIdx.y;
+    const int64_t bh = blockIdx.z, b = bh / a.H, h = bh - b * a.H;
+    const int n = tokens_of(a, (int)b);
+    const int t0 = min(seg * a.seg_len, n), t1 = min(t0 + a.seg_len, n);
+    const int width = min(kL, a.Dc - col0);
+    const T* A = static_cast<const T*>(a.a.p) + b * a.a.bs + h * a.a.hs;
+    const T* Bp = static_cast<const T*>(a.b.p) + b * a.b.bs + h * a.b.hs;
+    const T* C = static_cast<const T*>(a.c.p) + b * a.c.bs + h * a.c.hs + col0;
+    T* O = static_cast<T*>(const_cast<void*>(a.o.p)) + b * a.o.bs + h * a.o.hs + col0;
+    const float l = a.decay[h], l2 = log2_decay(l);
+    const int64_t state = (int64_t)a.Da * a.Dc;
+
+    tcc::pdl_launch_dependents();
+    tcc::pdl_wait();                    // the second pass follows the chaining kernel
+    float st[kD][4][4];                 // rows 64 t + 4 ty + i, columns col0 + 4 tx + j
+    const float* from = kState ? nullptr : (a.nseg > 1 ? a.seeds + (bh * a.nseg + seg) * state
+                                                       : (a.S0 ? a.S0 + bh * state : nullptr));
+#pragma unroll
+    for (int k = 0; k < kD; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 64 * k + 4 * ty + i, c = 4 * tx + j;
+                st[k][i][j] = from && r < a.Da && c < width ? from[(int64_t)r * a.Dc + col0 + c] : 0.f;
+            }
+    if (tid <= kL) s.pw[tid] = pow2(tid * l2);
+    const int d4 = (a.Da + 3) & ~3, d8 = (a.Da + 7) & ~7;
+    for (int c0 = t0; c0 < t1; c0 += kL) {
+        const int m = min(kL, t1 - c0);
+        // Tokens count from the last one where time is reversed.
+        auto place = [&](const Tensor& t) {
+            const int64_t ts = t.ts;
+            const int64_t at = a.rev ? (int64_t)(n - 1 - c0) * ts : (int64_t)c0 * ts, step = a.rev ? -ts : ts;
+            return [=](int i) { return at + i * step; };
+        };
+        __syncthreads();
+        if constexpr (!kState) {
+            stage<T, true>(A, place(a.a), m, a.Da, d8, x.at, kRow, nullptr);
+            stage<T, true>(Bp, place(a.b), m, a.Da, d8, x.bt, kRow, nullptr);
+#pragma unroll
+            for (int k = 0; k < kD; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4*>(x.sm + (64 * k + 4 * ty + i) * kRow + 4 * tx) =
+                        make_float4(st[k][i][0], st[k][i][1], st[k][i][2], st[k][i][3]);
+        }
+        stage<T, false>(Bp, place(a.b), m, a.Da, 64 * kD, s.bn, kB, s.pw);
+        stage<T, false>(C, place(a.c), m, width, kL, s.cn, kRow, nullptr);
+        __syncthreads();
+        if constexpr (!kState) {
+            if (tx <= ty) {             // the other tiles are masked
+                float p[4][4] = {};
+                for (int d = 0; d < d4; ++d) outer(p, x.at + d * kRow + 4 * ty, x.bt + d * kRow + 4 * tx);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int gap = 4 * (ty - tx) + i - j;
+                        v[i] = gap >= 0 ? p[i][j] * s.pw[max(gap, 0)] : 0.f;
+                    }
+                    *reinterpret_cast<float4*>(x.pt + (4 * tx + j) * kRow + 4 * ty) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            }
+            __syncthreads();
+            float o[4][4] = {};
+            for (int d = 0; d < d4; ++d) outer(o, x.at + d * kRow + 4 * ty, x.sm + d * kRow + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][j] *= s.pw[4 * ty + i + 1];
+            // Tokens after the tile's own take no part: each row adds its own terms only, so
+            // that an infinity or NaN reaches no earlier token.
+            for (int u = 0; u < 4 * ty; ++u) outer(o, x.pt + u * kRow + 4 * ty, s.cn + u * kRow + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                for (int u = 4 * ty; u <= 4 * ty + i; ++u) {
+                    const float w = x.pt[u * kRow + 4 * ty + i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[i][j] = fmaf(w, s.cn[u * kRow + 4 * tx + j], o[i][j]);
+                }
+            const auto row = place(a.o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * ty + i < m && 4 * tx + j < width) O[row(4 * ty + i) + 4 * tx + j] = from_f<T>(a.scale * o[i][j]);
+        }
+        const Factor f = factor(m * log_decay(l));
+#pragma unroll
+        for (int k = 0; k < kD; ++k) {
+            if (64 * k >= a.Da) break;
+            float add[4][4] = {};
+#pragma unroll 4
+            for (int u = 0; u < m; ++u) outer(add, s.bn + u * kB + 64 * k + 4 * ty, s.cn + u * kRow + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) st[k][i][j] = fmaf(f.hi, st[k][i][j], fmaf(f.lo, st[k][i][j], add[i][j]));
+        }
+    }
+    float* to = kState ? a.seeds + (bh * a.nseg + seg) * state
+                       : (seg == a.nseg - 1 && a.S_out ? a.S_out + bh * state : nullptr);
+    if (to)
+#pragma unroll
+        for (int k = 0; k < kD; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 64 * k + 4 * ty + i, c = 4 * tx + j;
+                    if (r < a.Da && c < width) to[(int64_t)r * a.Dc + col0 + c] = st[k][i][j];
+                }
+}
+
+// In place over a head's segments: the end states (from zero) become the states that the
+// segments start from, seed_0 = S0, seed_{i+1} = e^{l tokens_i} seed_i + end_i. A thread
+// chains one element, eight segments in flight.
+constexpr int kMaxSegments = 64;
+__global__ void __launch_bounds__(128) chain_kernel(const __grid_constant__ Args a, int chunk) {
+    __shared__ Factor f[kMaxSegments];
+    __shared__ int empty[kMaxSegments];
+    const int64_t bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
+    tcc::pdl_launch_dependents();
+    tcc::pdl_wait();
+    if (threadIdx.x < a.nseg) {
+        int n = tokens_of(a, (int)b);
+        if (a.rev) n = (n + chunk - 1) / chunk * chunk;
+        const int m = min(max(n - (int)threadIdx.x * a.seg_len, 0), a.seg_len);
+        f[threadIdx.x] = factor(m * log_decay(a.decay[h]));
+        empty[threadIdx.x] = m == 0;
+    }
+    __syncthreads();
+    const int e = blockIdx.x * 128 + threadIdx.x, E = a.Da * a.Dc;
+    if (e >= E) return;
+    float carry = a.S0 ? a.S0[bh * E + e] : 0.f;
+    float* p = a.seeds + bh * a.nseg * E + e;
+    for (int i0 = 0; i0 < a.nseg; i0 += 8) {
+        float end[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i0 + u < a.nseg - 1 && !empty[i0 + u]) end[u] = p[(int64_t)(i0 + u) * E];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u;
+            if (i >= a.nseg) break;
+            p[(int64_t)i * E] = carry;
+            if (i < a.nseg - 1 && !empty[i]) carry = fmaf(f[i].hi, carry, fmaf(f[i].lo, carry, end[u]));
+        }
+    }
+}
+
+struct StepArgs {
+    const void *q, *k, *v;
+    void* o;
+    int64_t q_bs, q_hs, k_bs, k_hs, v_bs, v_hs, o_bs, o_hs;
+    const float* decay;
+    float* S;                   // [B, H, Dk, Dv]
+    int H, Dk, Dv;
+    float scale;
+};
+
+// One token per sequence, the state updated in place. It is read and written once (8
+// bytes per element against five operations): HBM bandwidth bounds it. A block owns one
+// head; a thread owns kV columns of every rows-per-pass-th row and keeps kU rows in flight.
+template <typename T, int kV>
+__global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__ StepArgs a) {
+    constexpr int kU = 8;
+    __shared__ float ks[kMaxDim], qs[kMaxDim];
+    __shared__ float red[256 * kV];
+    const int tid = threadIdx.x;
+    const int64_t bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
+    const int lpr = (a.Dv + kV - 1) / kV, rpp = 256 / lpr;   // lanes per row, rows per pass
+    const int r0 = tid / lpr, c0 = (tid - r0 * lpr) * kV;
+    const bool mine = r0 < rpp;
+    float* S = a.S + bh * a.Dk * a.Dv + c0;
+    float s[kU][kV];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int r = base + u * rpp + r0;
+            if (!mine || r >= a.Dk) continue;
+            if constexpr (kV == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(S + (int64_t)r * a.Dv);
+                s[u][0] = v.x, s[u][1] = v.y, s[u][2] = v.z, s[u][3] = v.w;
+            } else {
+                s[u][0] = S[(int64_t)r * a.Dv];
+            }
+        }
+    };
+    load(0);
+    if (tid < a.Dk) {
+        qs[tid] = to_f(static_cast<const T*>(a.q)[b * a.q_bs + h * a.q_hs + tid]);
+        ks[tid] = to_f(static_cast<const T*>(a.k)[b * a.k_bs + h * a.k_hs + tid]);
+    }
+    const T* vp = static_cast<const T*>(a.v) + b * a.v_bs + h * a.v_hs;
+    float vv[kV], acc[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) vv[v] = mine ? to_f(vp[c0 + v]) : 0.f, acc[v] = 0.f;
+    const float f = expf(log_decay(a.decay[h]));
+    __syncthreads();
+    for (int base = 0; base < a.Dk; base += kU * rpp) {
+        if (base > 0) load(base);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int r = base + u * rpp + r0;
+            if (!mine || r >= a.Dk) continue;
+            const float kr = ks[r], qr = qs[r];
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                s[u][v] = fmaf(kr, vv[v], f * s[u][v]);
+                acc[v] = fmaf(qr, s[u][v], acc[v]);
+            }
+            if constexpr (kV == 4)
+                *reinterpret_cast<float4*>(S + (int64_t)r * a.Dv) = make_float4(s[u][0], s[u][1], s[u][2], s[u][3]);
+            else
+                S[(int64_t)r * a.Dv] = s[u][0];
+        }
+    }
+    if (mine)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) red[r0 * a.Dv + c0 + v] = acc[v];
+    __syncthreads();
+    if (tid < a.Dv) {
+        float v = 0.f;
+        for (int r = 0; r < rpp; ++r) v += red[r * a.Dv + tid];
+        static_cast<T*>(a.o)[b * a.o_bs + h * a.o_hs + tid] = from_f<T>(a.scale * v);
+    }
+}
+
+template <typename T, int kD>
+cudaError_t run_width(const Args& a, cudaStream_t st) {
+    static std::atomic<int> optin[2][tcc::kMaxDevices];
+    constexpr int kSums = sizeof(Common<kD>), kMain = kSums + sizeof(Shared<kD>);
+    cudaError_t e = tcc::ensure_smem_optin(decay_kernel<T, kD, false>, kMain, optin[0]);
+    if (e != cudaSuccess) return e;
+    const unsigned BH = (unsigned)(a.B * a.H), blocks = (a.Dc + kL - 1) / kL;
+    if (a.nseg > 1) {
+        if ((e = tcc::ensure_smem_optin(decay_kernel<T, kD, true>, kSums, optin[1])) != cudaSuccess) return e;
+        decay_kernel<T, kD, true><<<dim3(a.nseg - 1, blocks, BH), 256, kSums, st>>>(a);
+        if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
+        if ((e = launch_chain(a, 1, st)) != cudaSuccess) return e;
+    }
+    return scan::launch_after(decay_kernel<T, kD, false>, dim3(a.nseg, blocks, BH), 256, kMain, st, a.nseg > 1, a);
+}
+
+template <typename T>
+cudaError_t run_simt(const Args& a, cudaStream_t st) {
+    return a.Da <= 64 ? run_width<T, 1>(a, st) : run_width<T, 2>(a, st);
+}
+
+// Segments of the CUDA-core path: one while there are blocks for every SM or fewer than four
+// chunks.
+int simt_segments(int64_t BH, int N, int Da, int Dc) {
+    const int64_t blocks = BH * ((Dc + kL - 1) / kL), slots = (int64_t)tcc::sm_count() * (Da <= 64 ? 2 : 1);
+    const int64_t most = (N + kL - 1) / kL / 2;
+    int64_t n = blocks > 0 ? slots / blocks : 1;
+    n = n < most ? n : most;
+    n = n < kMaxSegments ? n : kMaxSegments;
+    return n < 2 ? 1 : (int)n;
+}
+
+cudaError_t run(Args a, la_dtype dt, void* workspace, cudaStream_t st) {
+    const int64_t BH = (int64_t)a.B * a.H;
+    const bool tc = tc_supported(a, dt);
+    const int chunk = tc ? tcc::kC : kL, chunks = (a.N + chunk - 1) / chunk;
+    a.nseg = tc ? tc_segments(BH, a.N, a.Da, a.Dc) : simt_segments(BH, a.N, a.Da, a.Dc);
+    const int per = (chunks + a.nseg - 1) / a.nseg;
+    a.nseg = (chunks + per - 1) / per;
+    a.seg_len = per * chunk;
+    a.seeds = reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(WsHeader));
+    return tc ? tc_run(a, workspace, st) : dt == LA_BF16 ? run_simt<__nv_bfloat16>(a, st) : run_simt<float>(a, st);
+}
+
+constexpr int64_t kPromptHeads = 65535, kStepHeads = 2147483647;   // grid axes
+la_status check_shape(int B, int H, int N, int Dk, int Dv, la_dtype dt, float scale, int64_t most_heads) {
+    if (B < 0 || H < 0 || N < 0 || Dk < 1 || Dv < 1) return LA_ERR_INVALID_ARG;
+    if ((dt != LA_F32 && dt != LA_BF16) || !isfinite(scale)) return LA_ERR_INVALID_ARG;
+    if (Dk > kMaxDim || Dv > kMaxDim) return LA_ERR_UNSUPPORTED;
+    if ((int64_t)B * H > most_heads || N > kScanMaxTokens) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+bool bad(const void* p, la_dtype dt) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (dt == LA_BF16 ? 1 : 3));
+}
+bool bad4(const void* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
+
+// Rows [B, H, N, D] as the overlap checks take them: two strided axes over whole rows, and
+// what is left as a list of such sets (one, unless the strides of all three axes are their own).
+struct Rows3 {
+    Rows r;
+    int64_t more, stride;       // sets and bytes between them
+};
+Rows3 rows3(const void* p, int64_t B, int64_t H, int64_t N, int64_t D, const int64_t* s, int64_t eb) {
+    const int64_t bs = s[0] * eb, hs = s[1] * eb, ts = s[2] * eb, row = D * eb;
+    if (H == 1) return {{p, B, N, row, bs, ts}, 1, 0};
+    if (N == 1) return {{p, B, H, row, bs, hs}, 1, 0};
+    if (B == 1) return {{p, H, N, row, hs, ts}, 1, 0};
+    if (hs == row) return {{p, B, N, H * row, bs, ts}, 1, 0};
+    if (bs == H * hs) return {{p, B * H, N, row, hs, ts}, 1, 0};
+    if (hs == N * ts) return {{p, B, H * N, row, bs, ts}, 1, 0};
+    return {{p, H, N, row, hs, ts}, B, bs};
+}
+Rows3 whole(const void* p, int64_t bytes) { return {block_of(p, bytes), 1, 0}; }
+
+bool overlap3(const Rows3& x, const Rows3& y) {
+    if (!x.r.p || !y.r.p || x.more * y.more > 65536) return false;
+    for (int64_t i = 0; i < x.more; ++i)
+        for (int64_t j = 0; j < y.more; ++j) {
+            Rows u = x.r, v = y.r;
+            u.p = static_cast<const char*>(u.p) + i * x.stride;
+            v.p = static_cast<const char*>(v.p) + j * y.stride;
+            if (overlap(u, v)) return true;
+        }
+    return false;
+}
+bool overlaps_any3(const Rows3& out, std::initializer_list<Rows3> others) {
+    for (const Rows3& r : others)
+        if (overlap3(out, r)) return true;
+    return false;
+}
+
+// Whether an output's rows are disjoint: each axis steps over all that the axes with smaller
+// strides cover.
+bool disjoint(int64_t B, int64_t H, int64_t N, int64_t D, const int64_t* s) {
+    int64_t size[3] = {B, H, N}, stride[3] = {s[0], s[1], s[2]}, reach = D;
+    for (int k = 0; k < 3; ++k) {
+        int best = -1;
+        for (int i = 0; i < 3; ++i)
+            if (size[i] > 1 && (best < 0 || stride[i] < stride[best])) best = i;
+        if (best < 0) return true;
+        if (stride[best] < reach) return false;
+        reach += (size[best] - 1) * stride[best];
+        size[best] = 1;
+    }
+    return true;
+}
+
+Tensor tensor(const void* p, const int64_t* s) { return {p, s[0], s[1], s[2]}; }
+
+}  // namespace
+
+namespace decay {
+
+cudaError_t launch_chain(const Args& a, int chunk, cudaStream_t st) {
+    return scan::launch_after(chain_kernel, dim3((a.Da * a.Dc + 127) / 128, (unsigned)(a.B * a.H)), 128, 0, st, true, a,
+                              chunk);
+}
+
+}  // namespace decay
+
+namespace {
+
+// Segments of one sum, whichever path its strides let it take.
+int most_segments(int64_t BH, int N, int Da, int Dc, la_dtype dt) {
+    const int x = simt_segments(BH, N, Da, Dc);
+    const int y = dt == LA_BF16 && Da % 8 == 0 && Dc % 8 == 0 ? tc_segments(BH, N, Da, Dc) : 1;
+    return x > y ? x : y;
+}
+
+}  // namespace
+
+size_t decay_workspace(int B, int H, int N, int Dk, int Dv, la_dtype dt, bool backward) {
+    const int64_t BH = (int64_t)B * H;
+    int n = most_segments(BH, N, Dk, Dv, dt);
+    if (backward) {
+        const int m = most_segments(BH, N, Dv, Dk, dt);
+        n = m > n ? m : n;
+    }
+    return n > 1 ? (size_t)BH * n * Dk * Dv * sizeof(float) : 0;
+}
+
+int decay_launches(int B, int H, int N, int Dk, int Dv, la_dtype dt, bool backward) {
+    auto one = [&](int Da, int Dc) {
+        const bool tc = dt == LA_BF16 && Da % 8 == 0 && Dc % 8 == 0;
+        const int64_t BH = (int64_t)B * H;
+        return (tc ? tc_segments(BH, N, Da, Dc) : simt_segments(BH, N, Da, Dc)) > 1 ? 3 : 1;
+    };
+    return backward ? 2 * one(Dv, Dk) + one(Dk, Dv) : one(Dk, Dv);
+}
+
+}  // namespace la
+
+extern "C" {
+
+la_status la_decay_attn_fwd(const void* q, const void* k, const void* v, const float* decay, float scale,
+                            const int32_t* lengths, const float* S0, float* S_out, void* o,
+                            const int64_t* strides, int B, int H, int N, int Dk, int Dv, la_dtype dt,
+                            void* workspace, size_t workspace_bytes, la_stream_t stream) {
+    la_status s = la::check_shape(B, H, N, Dk, Dv, dt, scale, la::kPromptHeads);
+    if (s != LA_OK) return s;
+    const int64_t BH = (int64_t)B * H;
+    if (BH == 0) return LA_OK;
+    if (!decay || la::bad4(decay) || la::bad4(lengths) || la::bad4(S0) || la::bad4(S_out)) return LA_ERR_INVALID_ARG;
+    const size_t state = sizeof(float) * (size_t)BH * Dk * Dv;
+    const la::Rows s0 = la::block_of(S0, state), s1 = la::block_of(S_out, state);
+    if (S0 != S_out && la::overlap(s0, s1)) return LA_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (N == 0) {
+        if (!S_out || S_out == S0) return LA_OK;
+        const cudaError_t e = S0 ? cudaMemcpyAsync(S_out, S0, state, cudaMemcpyDeviceToDevice, st)
+                                 : cudaMemsetAsync(S_out, 0, state, st);
+        return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    }
+    if (la::bad(q, dt) || la::bad(k, dt) || la::bad(v, dt) || la::bad(o, dt) || !strides) return LA_ERR_INVALID_ARG;
+    if (!la::disjoint(B, H, N, Dv, strides + 9)) return LA_ERR_INVALID_ARG;
+    const size_t need = sizeof(la::WsHeader) + la::decay_workspace(B, H, N, Dk, Dv, dt, false);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return LA_ERR_WORKSPACE;
+    const int64_t eb = dt == LA_BF16 ? 2 : 4;
+    const la::Rows3 qr = la::rows3(q, B, H, N, Dk, strides, eb), kr = la::rows3(k, B, H, N, Dk, strides + 3, eb);
+    const la::Rows3 vr = la::rows3(v, B, H, N, Dv, strides + 6, eb), orr = la::rows3(o, B, H, N, Dv, strides + 9, eb);
+    const la::Rows3 dr = la::whole(decay, 4 * (int64_t)H), nr = la::whole(lengths, 4 * (int64_t)B);
+    const la::Rows3 s0r = la::whole(S0, state), s1r = la::whole(S_out, state), wr = la::whole(workspace, need);
+    if (la::overlaps_any3(orr, {qr, kr, vr, dr, nr, s0r, s1r, wr}) || la::overlaps_any3(s1r, {qr, kr, vr, dr, nr, wr}) ||
+        la::overlaps_any3(wr, {qr, kr, vr, dr, nr, s0r}))
+        return LA_ERR_INVALID_ARG;
+    la::decay::Args a = {};
+    a.a = la::tensor(q, strides), a.b = la::tensor(k, strides + 3), a.c = la::tensor(v, strides + 6);
+    a.o = la::tensor(o, strides + 9);
+    a.decay = decay, a.lengths = lengths, a.S0 = S0, a.S_out = S_out;
+    a.B = B, a.H = H, a.N = N, a.Da = Dk, a.Dc = Dv, a.scale = scale;
+    return la::run(a, dt, workspace, st) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+la_status la_decay_attn_bwd(const void* q, const void* k, const void* v, const void* dout, const float* decay,
+                            float scale, const int32_t* lengths, void* dq, void* dk, void* dv,
+                            const int64_t* strides, int B, int H, int N, int Dk, int Dv, la_dtype dt,
+                            void* workspace, size_t workspace_bytes, la_stream_t stream) {
+    la_status s = la::check_shape(B, H, N, Dk, Dv, dt, scale, la::kPromptHeads);
+    if (s != LA_OK) return s;
+    if (B == 0 || H == 0 || N == 0) return LA_OK;
+    if (!decay || la::bad4(decay) || la::bad4(lengths) || !strides) return LA_ERR_INVALID_ARG;
+    for (const void* p : {q, k, v, dout, (const void*)dq, (const void*)dk, (const void*)dv})
+        if (la::bad(p, dt)) return LA_ERR_INVALID_ARG;
+    const int64_t *sq = strides, *sk = strides + 3, *sv = strides + 6, *sg = strides + 9;
+    const int64_t *tq = strides + 12, *tk = strides + 15, *tv = strides + 18;
+    if (!la::disjoint(B, H, N, Dk, tq) || !la::disjoint(B, H, N, Dk, tk) || !la::disjoint(B, H, N, Dv, tv))
+        return LA_ERR_INVALID_ARG;
+    const size_t need = sizeof(la::WsHeader) + la::decay_workspace(B, H, N, Dk, Dv, dt, true);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return LA_ERR_WORKSPACE;
+    const int64_t eb = dt == LA_BF16 ? 2 : 4;
+    const la::Rows3 qr = la::rows3(q, B, H, N, Dk, sq, eb), kr = la::rows3(k, B, H, N, Dk, sk, eb);
+    const la::Rows3 vr = la::rows3(v, B, H, N, Dv, sv, eb), gr = la::rows3(dout, B, H, N, Dv, sg, eb);
+    const la::Rows3 dr = la::whole(decay, 4 * (int64_t)H), nr = la::whole(lengths, 4 * (int64_t)B);
+    const la::Rows3 wr = la::whole(workspace, need);
+    const la::Rows3 oq = la::rows3(dq, B, H, N, Dk, tq, eb), ok = la::rows3(dk, B, H, N, Dk, tk, eb);
+    const la::Rows3 ov = la::rows3(dv, B, H, N, Dv, tv, eb);
+    for (const la::Rows3* out : {&oq, &ok, &ov, &wr})
+        if (la::overlaps_any3(*out, {qr, kr, vr, gr, dr, nr})) return LA_ERR_INVALID_ARG;
+    if (la::overlap3(oq, ok) || la::overlap3(oq, ov) || la::overlap3(ok, ov) || la::overlaps_any3(wr, {oq, ok, ov}))
+        return LA_ERR_INVALID_ARG;
+    la::decay::Args a = {};
+    a.decay = decay, a.lengths = lengths, a.B = B, a.H = H, a.N = N, a.scale = scale;
+    const la::decay::Tensor Q = la::tensor(q, sq), K = la::tensor(k, sk), V = la::tensor(v, sv), G = la::tensor(dout, sg);
+    struct { la::decay::Tensor a, b, c, o; int Da, Dc, rev; } sums[3] = {
+        {G, V, K, la::tensor(dq, tq), Dv, Dk, 0}, {V, G, Q, la::tensor(dk, tk), Dv, Dk, 1}, {K, Q, G, la::tensor(dv, tv), Dk, Dv, 1}};
+    for (const auto& u : sums) {
+        a.a = u.a, a.b = u.b, a.c = u.c, a.o = u.o, a.Da = u.Da, a.Dc = u.Dc, a.rev = u.rev;
+        if (la::run(a, dt, workspace, (cudaStream_t)stream) != cudaSuccess) return LA_ERR_CUDA;
+    }
+    return LA_OK;
+}
+
+la_status la_decay_attn_step(const void* q, const void* k, const void* v, const float* decay, float scale,
+                             float* S_inout, void* o, const int64_t* strides, int B, int H, int Dk, int Dv,
+                             la_dtype dt, la_stream_t stream) {
+    la_status s = la::check_shape(B, H, 1, Dk, Dv, dt, scale, la::kStepHeads);
+    if (s != LA_OK) return s;
+    const int64_t BH = (int64_t)B * H;
+    if (BH == 0) return LA_OK;
+    if (la::bad(q, dt) || la::bad(k, dt) || la::bad(v, dt) || la::bad(o, dt) || !decay || la::bad4(decay) || !strides ||
+        !S_inout || (reinterpret_cast<uintptr_t>(S_inout) & (Dv % 4 ? 3 : 15)))   // 16-byte accesses of four columns
+        return LA_ERR_INVALID_ARG;
+    const int64_t *sq = strides, *sk = strides + 2, *sv = strides + 4, *so = strides + 6;
+    const int64_t no[3] = {so[0], so[1], 0};
+    if (!la::disjoint(B, H, 1, Dv, no)) return LA_ERR_INVALID_ARG;
+    const int64_t eb = dt == LA_BF16 ? 2 : 4;
+    auto rows = [&](const void* p, int D, const int64_t* t) { return la::Rows{p, B, H, D * eb, t[0] * eb, t[1] * eb}; };
+    const la::Rows qr = rows(q, Dk, sq), kr = rows(k, Dk, sk), vr = rows(v, Dv, sv), outr = rows(o, Dv, so);
+    const la::Rows dr = la::block_of(decay, 4 * (int64_t)H);
+    const la::Rows sr = la::block_of(S_inout, (int64_t)(sizeof(float) * (size_t)BH * Dk * Dv));
+    // o may be q, k or v itself (the same rows): a block reads what it replaces.
+    for (const la::Rows* r : {&qr, &kr, &vr})
+        if (!la::same_rows(*r, outr) && la::overlap(*r, outr)) return LA_ERR_INVALID_ARG;
+    if (la::overlap(outr, dr) || la::overlaps_any(sr, {qr, kr, vr, outr, dr})) return LA_ERR_INVALID_ARG;
+    const la::StepArgs a = {q, k, v, o, sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1], decay, S_inout, H, Dk, Dv, scale};
+    cudaStream_t st = (cudaStream_t)stream;
+    const unsigned blocks = (unsigned)BH;
+    if (dt == LA_BF16) {
+        if (Dv % 4 == 0) la::decay_step_kernel<__nv_bfloat16, 4><<<blocks, 256, 0, st>>>(a);
+        else la::decay_step_kernel<__nv_bfloat16, 1><<<blocks, 256, 0, st>>>(a);
+    } else {
+        if (Dv % 4 == 0) la::decay_step_kernel<float, 4><<<blocks, 256, 0, st>>>(a);
+        else la::decay_step_kernel<float, 1><<<blocks, 256, 0, st>>>(a);
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+}  // extern "C"

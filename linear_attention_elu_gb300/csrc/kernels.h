@@ -103,6 +103,11 @@ constexpr int kScanMaxTokens = 1 << 30;
 size_t scan_workspace(int B, int H, int N, int S, int P, la_dtype dt);
 int scan_launches(int B, int H, int N, int S, int P, la_dtype dt);
 
+// Linear attention with a decay per head (csrc/decay.cu): workspace bytes after the header,
+// launches, for rows that are 16-byte aligned.
+size_t decay_workspace(int B, int H, int N, int Dk, int Dv, la_dtype dt, bool backward);
+int decay_launches(int B, int H, int N, int Dk, int Dv, la_dtype dt, bool backward);
+
 // Whether the rows of an output (`row` values each, batch stride bs, token stride
 // ts) are disjoint.
 inline bool rows_disjoint(int B, int N, int64_t row, int64_t bs, int64_t ts) {
