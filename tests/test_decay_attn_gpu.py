@@ -143,7 +143,9 @@ def test_lengths_leave_rows_behind_them(la, N, lengths, dt):
             t[b, :, n:] = float("nan")
     o = torch.full((B, N, 2, 64), 7.0, device="cuda").to(DT[dt]).transpose(1, 2)
     clean = [torch.nan_to_num(t) for t in x]
-    got = la.la_decay_attn_fwd(*x[:3], decay, 0.125, torch.tensor(lengths, dtype=torch.int32, device="cuda"), S0, o=o)
+    # (A call that returns the state sums it in more terms: both calls here do.)
+    got = la.la_decay_attn_fwd(*x[:3], decay, 0.125, torch.tensor(lengths, dtype=torch.int32, device="cuda"), S0,
+                               torch.empty_like(S0), o=o)
     assert got is o
     want = check_fwd(la, clean, decay, S0, dt, lengths=lengths)
     grads = [torch.full((B, 2, N, 64), 7.0, device="cuda").to(DT[dt]) for _ in range(3)]
