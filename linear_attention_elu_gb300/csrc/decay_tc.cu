@@ -10,7 +10,8 @@
 //   (2) read of the state A S_bf16        M = 128, N = 64,  K = Da
 //   (3) P C, P = bf16 of the weighted, masked scores (in TMEM)    K = 128
 //   (4) B^T (w C), C weighted             M = Da,  N = 64,  K = 128
-// A CTA owns a "unit", 64 columns of C and of the state, and walks the chunks of a segment.
+// A CTA walks the chunks of a segment of one head, for one or two "units" of 64 columns of
+// C and of the state ((1) and P serve both).
 //
 // Roundings. A, B, C enter as they are. P and the state of (2) are rounded to bf16 once each
 // (half a step, 2^-8, of a term, as the output itself). The state is held in fp32 in
@@ -21,9 +22,12 @@
 // row and one of the column; the diagonal blocks take an exponential per score. Every
 // factor's exponent is a count of tokens times l, so none is a difference of larger ones.
 //
-// Schedule. 8 working warps and one that issues loads, products and stores; two CTAs per SM
-// (113 KB of shared memory, 256 TMEM columns each), so that one CTA's steps run under the
-// other's waits. A working warp owns 32 rows and half of the columns. Hand-offs are
+// Schedule. Eight working warps per unit and one warp that issues loads, products and stores.
+// A working warp owns 32 rows and half of a unit's columns. Within a chunk: state to bf16 and
+// w C to shared memory; (2) and (4) run under the step from scores to P; the sums of (4) join
+// the state and (3) takes their TMEM columns; the output is staged where C was. A, B and the
+// next scores are on the way from the middle of the chunk on, C from the chunk before. With
+// one unit and Da <= 64 two CTAs share an SM, each under the other's waits. Hand-offs are
 // mbarriers; every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -49,42 +53,47 @@ using namespace tc;
 using namespace tcc;
 
 constexpr uint32_t kTile = kTileBytes;         // [128 tokens x 64] bf16
-constexpr int kWork = 8;                       // working warps
-constexpr int kThreads = 32 * (kWork + 1);
+constexpr int kWork = 8;                       // working warps of a unit
 constexpr int kNone = 0x7fffffff;
 
-// TMEM columns: scores, whose first half then holds P and whose second half (4), and the two
-// parts of the output.
-constexpr uint32_t kTmP = 0, kTmSt = 64, kTmO1 = 128, kTmO2 = 192;
+// TMEM columns: scores, P of each 32 of them over their first 16; per unit the sums of (4),
+// then (3)'s part of the output, and (2)'s part.
+constexpr uint32_t kTmP = 0, kTmX = 128, kTmO2 = 192, kTmUnit = 128;
 
 struct Misc {
-    uint64_t a_full, b_full[2], c_full[2], p_full, o2_full, o_full;
-    uint64_t prep, pt, sread, staged, hfree, pair[4], drain;
+    uint64_t a_full, b_full, c_full[2], p_full, s_full, o_full;
+    uint64_t prep, pt, staged, drain;
     uint32_t tmem_slot;
     int any;                    // values of C that are not finite: the first token that has one,
-    int first[64];              // and that of each column, counted over the segment
+    int first[128];             // and that of each column, counted over the segment
     alignas(16) float tab[32];  // f^(31 - j), by the column's place in its block; read 16 bytes at a time
+    alignas(16) uint32_t mask[512];   // diagonal block, [pair of columns / 2][row][2]: which scores take part
 };
-static_assert(sizeof(Misc) <= 1024, "the last kilobyte");
+constexpr uint32_t kMiscBytes = 3 * 1024;
+static_assert(sizeof(Misc) <= kMiscBytes, "barriers and tables");
 
-// Shared memory from a 1024-byte boundary. The bf16 state of (2) lies where the second term
-// of w C is written once (2) has read it, the output where the first term was.
-template <int kT, int kTerms> struct Smem {
-    static constexpr int kStages = kT == 1 && kTerms == 2 ? 2 : 1;   // of B and C
-    static constexpr uint32_t kA = 0, kB = kT * kTile, kC0 = kB + kStages * kT * kTile;
-    static constexpr uint32_t kW = kC0 + kStages * kTile, kS = kW + kTile;
-    static constexpr uint32_t kMisc = kW + kTerms * kTile;
-    static constexpr int kBytes = kMisc + 1024;
+// Shared memory from a 1024-byte boundary.
+template <int kT, int kU, int kTerms> struct Smem {
+    static constexpr int kStages = kTerms == 2 ? 2 : 1;               // of C
+    static constexpr uint32_t kA = 0, kB = kT * kTile, kC0 = 2 * kT * kTile;
+    static constexpr uint32_t kW = kC0 + kStages * kU * kTile;        // [unit][term]
+    static constexpr uint32_t kS = kW + kU * kTerms * kTile;          // [unit], 64 kT rows
+    static constexpr uint32_t kMisc = kS + kU * kT * kTile / 2;
+    static constexpr int kBytes = kMisc + kMiscBytes;
+    static constexpr int kPerSm = kBytes <= 113 * 1024 && kU == 1 ? 2 : 1;
 };
-static_assert(Smem<1, 2>::kBytes == 113 * 1024 && Smem<2, 2>::kBytes == 113 * 1024, "two CTAs per SM");
+static_assert(Smem<1, 1, 2>::kPerSm == 2 && Smem<1, 1, 3>::kPerSm == 2, "two CTAs per SM");
+static_assert(Smem<2, 2, 2>::kBytes <= 227 * 1024 && Smem<2, 2, 3>::kBytes <= 227 * 1024, "shared memory");
 
 // The first pass: B and C, the terms of w C.
-template <int kT, int kTerms> struct SumSmem {
-    static constexpr int kStages = kT == 1 ? 2 : 1;
-    static constexpr uint32_t kB = 0, kC0 = kStages * kT * kTile, kW = kC0 + kStages * kTile;
-    static constexpr uint32_t kMisc = kW + kTerms * kTile;
-    static constexpr int kBytes = kMisc + 1024;
+template <int kT, int kU, int kTerms> struct SumSmem {
+    static constexpr int kStages = kT + kU < 4 || kTerms == 2 ? 2 : 1;
+    static constexpr uint32_t kB = 0, kC0 = kStages * kT * kTile, kW = kC0 + kStages * kU * kTile;
+    static constexpr uint32_t kMisc = kW + kU * kTerms * kTile;
+    static constexpr int kBytes = kMisc + kMiscBytes;
+    static constexpr int kPerSm = kBytes <= 113 * 1024 && kU == 1 ? 2 : 1;
 };
+static_assert(SumSmem<2, 2, 2>::kBytes <= 227 * 1024 && SumSmem<1, 2, 3>::kBytes <= 227 * 1024, "shared memory");
 
 // Coordinate factors of the tensor maps: 0 for an axis of stride 0, whose map has one entry.
 struct Geo {
@@ -156,11 +165,11 @@ struct Place {
     int b, h, col0, seg, n, nch, v0, nc;
     template <bool kRev> __device__ int chunk(int i) const { return kRev ? nch - 1 - v0 - i : v0 + i; }
 };
-__device__ __forceinline__ Place place(const Args& a, const Geo& geo) {
+__device__ __forceinline__ Place place(const Args& a, const Geo& geo, int units) {
     Place p;
     p.b = blockIdx.z / a.H;
     p.h = blockIdx.z - p.b * a.H;
-    p.col0 = 64 * blockIdx.x;
+    p.col0 = 64 * units * blockIdx.x;
     p.seg = blockIdx.y;
     p.n = tokens_of(a, p.b);
     p.nch = (p.n + kC - 1) / kC;
@@ -189,20 +198,20 @@ __device__ __forceinline__ void next_term(uint64_t (&rest)[4], uint32_t (&t)[4])
 
 // Columns 32 g .. of row `row` of a C tile: notes the values that are not finite, and clears
 // them: (3) would add 0 times them to the tokens before them. (4) has them from the terms.
-__device__ __noinline__ void take_out(uint8_t* tile, int row, int g, int token, Misc* m) {
+__device__ __noinline__ void take_out(uint8_t* tile, int row, int g, int token, int* any, int* first) {
     for (int c = 32 * g; c < 32 * g + 32; ++c) {
         unsigned short* v = reinterpret_cast<unsigned short*>(tile + row * 128 + (((c >> 3) ^ (row & 7)) << 4)) + (c & 7);
         if ((*v & 0x7F80u) != 0x7F80u) continue;
         *v = 0;
-        atomicMin(&m->first[c], token);
-        atomicMin(&m->any, token);
+        atomicMin(first + c, token);
+        atomicMin(any, token);
     }
 }
 
-// The outputs that such values reach, set to NaN: columns c .. c + 7 of a row.
-__device__ __noinline__ uint4 put_nan(const Misc* m, int c, int token, uint4 o) {
+// The outputs that such values reach, set to NaN: eight columns of a row.
+__device__ __noinline__ uint4 put_nan(const int* firsts, int token, uint4 o) {
     auto one = [&](uint32_t w, int k) {
-        const volatile int* first = m->first + c + k;
+        const volatile int* first = firsts + k;
         if (first[0] <= token) w = (w & 0xFFFF0000u) | 0x7FFFu;
         if (first[1] <= token) w = (w & 0xFFFFu) | 0x7FFF0000u;
         return w;
@@ -210,18 +219,175 @@ __device__ __noinline__ uint4 put_nan(const Misc* m, int c, int token, uint4 o) 
     return make_uint4(one(o.x, 0), one(o.y, 2), one(o.z, 4), one(o.w, 6));
 }
 
-template <int kT, int kTerms, bool kRev>
-__global__ void __launch_bounds__(kThreads, kT == 2 && kTerms == 3 ? 1 : 2)
+// ------------------------------------------------------------ steps of a working warp
+// Row `row` = 32 q + lane of the tiles; half g of a unit's 64 columns.
+
+// A state row (32 fp32 columns) to the bf16 tile that (2) reads.
+__device__ __forceinline__ void write_state(uint8_t* tile, const float (&st)[32], int row, int g) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(tile + row * 128 + (((4 * g + j) ^ (row & 7)) << 4)) =
+            make_uint4(pack_bf16(st[8 * j], st[8 * j + 1]), pack_bf16(st[8 * j + 2], st[8 * j + 3]),
+                       pack_bf16(st[8 * j + 4], st[8 * j + 5]), pack_bf16(st[8 * j + 6], st[8 * j + 7]));
+}
+
+// w C of a row: its terms, kTile apart. Returns whether all values are finite.
+template <int kTerms>
+__device__ __forceinline__ bool write_weighted(const uint8_t* c_tile, uint8_t* terms, float w, int row, int g) {
+    const uint64_t w2 = pk2(w, w);
+    uint64_t bad = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t at = row * 128 + (((4 * g + j) ^ (row & 7)) << 4);
+        const uint4 c = *reinterpret_cast<const uint4*>(c_tile + at);
+        uint32_t t[4];
+        uint64_t rest[4];
+        weigh8(c, w2, t, rest);
+        *reinterpret_cast<uint4*>(terms + at) = make_uint4(t[0], t[1], t[2], t[3]);
+        // The remainder of a value that is not finite is NaN.
+        bad = fma2(rest[0], 0, fma2(rest[1], 0, fma2(rest[2], 0, fma2(rest[3], 0, bad))));
+#pragma unroll
+        for (int k = 1; k < kTerms; ++k) {
+            next_term(rest, t);
+            *reinterpret_cast<uint4*>(terms + k * kTile + at) = make_uint4(t[0], t[1], t[2], t[3]);
+        }
+    }
+    float b0, b1;
+    unpk2(bad, &b0, &b1);
+    return b0 == 0.f && b1 == 0.f;
+}
+
+// Rows past a sequence's end may hold anything: four pieces of one row set to 0.
+__device__ __forceinline__ void clear_pieces(uint8_t* tile, int row, int g) {
+#pragma unroll
+    for (int j = 4 * g; j < 4 * g + 4; ++j)
+        *reinterpret_cast<uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+}
+
+// Decay factors of a warp's rows, for every chunk.
+struct RowFactors {
+    float l2, diag;     // log2 f, and its leading 19 bits: times a count below 32 it is exact, so that
+                        // the diagonal's exponents are differences without error (2^-19 of them is lost)
+    int im;             // the row in the order of summation
+};
+
+// 32 lanes x 32 bits, 8 consecutive columns: thread t of the warp writes lane (base + t).
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// Scores of block column `blk` (bm in the order of summation) to packed P, over the first
+// half of their columns: no other warp reads or writes those. Loops are kept rolled: what
+// the compiler keeps of unrolled ones from chunk to chunk does not fit the registers, and
+// what it spills does not fit the little L1 that two CTAs leave (backwards in time the call
+// took 1.8 times as long).
+template <bool kRev>
+__device__ __forceinline__ void scores_to_p(uint32_t tm, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
+    const int lane = threadIdx.x & 31;
+    const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane * rf.diag;
+    const uint64_t r2 = pk2(r, r);
+    const uint32_t at = tm + kTmP + 32 * blk;
+#pragma unroll 1
+    for (int half = 0; half < 32; half += 16) {
+        uint32_t v[16], p[8];
+        if (bm > qm) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = 0u;
+            tmem_st8(at + half / 2, p);
+            continue;
+        }
+        tmem_ld16(at + half, v);
+        tmem_ld_wait();
+        if (kRev && 32 * blk + half + 16 > cut)        // later tokens that the sequence does not have
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (32 * blk + half + e >= cut) v[e] = 0u;
+        if (bm < qm) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.tab + half + 2 * e);
+                p[e] = pack2(mul2(mul2(pair2(v + 2 * e), f.x), r2));
+                p[e + 1] = pack2(mul2(mul2(pair2(v + 2 * e + 2), f.y), r2));
+            }
+        } else {
+            const float first = (float)half;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                // Scores that take no part are cleared as bits: their products may be anything.
+                const uint2 keep = *reinterpret_cast<const uint2*>(m.mask + 32 * (half / 2 + e) + 2 * lane);
+                float x[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float j = first + (float)(2 * e + u);
+                    x[u] = __uint_as_float(v[2 * e + u]) * pow2(kRev ? fmaf(j, rf.diag, -own) : fmaf(-j, rf.diag, own));
+                }
+                p[e] = pack_bf16(x[0], x[1]) & keep.x;
+                p[e + 1] = pack_bf16(x[2], x[3]) & keep.y;
+            }
+        }
+        tmem_st8(at + half / 2, p);
+    }
+}
+
+// The chunk's sums join the state: st = f st + sums.
+__device__ __forceinline__ void join_state(uint32_t tm, const Factor& f, float (&st)[32]) {
+    const uint64_t hi = pk2(f.hi, f.hi), lo = pk2(f.lo, f.lo);
+#pragma unroll
+    for (int half = 0; half < 32; half += 16) {
+        uint32_t v[16];
+        tmem_ld16(tm + half, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            const uint64_t s = pk2(st[half + k], st[half + k + 1]);
+            unpk2(fma2(hi, s, fma2(lo, s, pair2(v + k))), &st[half + k], &st[half + k + 1]);
+        }
+    }
+}
+
+// 16 output columns of a row from the two parts.
+__device__ __forceinline__ void join_output(uint32_t tm1, uint32_t tm2, float scale, float read, uint4* x, uint4* y) {
+    uint32_t u[16], v[16], o[8];
+    tmem_ld16(tm1, u);
+    tmem_ld16(tm2, v);
+    tmem_ld_wait();
+    const uint64_t s2 = pk2(scale, scale), r2 = pk2(read, read);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = pack2(fma2(pair2(u + 2 * e), s2, mul2(pair2(v + 2 * e), r2)));
+    *x = make_uint4(o[0], o[1], o[2], o[3]);
+    *y = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Tables of a head: the columns' factors, and which scores of a diagonal block take part.
+template <bool kRev> __device__ __forceinline__ void init_tables(Misc& m, float l2) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid < 32) m.tab[tid] = pow2((float)(kRev ? tid : 31 - tid) * l2);
+    if (tid < 256)
+        for (int e = 2 * (tid >> 5); e < 2 * (tid >> 5) + 2; ++e) {
+            const bool a = kRev ? 2 * e >= lane : 2 * e <= lane, b = kRev ? 2 * e + 1 >= lane : 2 * e + 1 <= lane;
+            m.mask[32 * (e & ~1) + 2 * lane + (e & 1)] = (a ? 0xFFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
+        }
+}
+
+__device__ __forceinline__ RowFactors row_factors(float l2, int im) {
+    return {l2, __uint_as_float(__float_as_uint(l2) & ~31u), im};
+}
+
+template <int kT, int kU, int kTerms, bool kRev>
+__global__ void __launch_bounds__(32 * (kU * kWork + 1), Smem<kT, kU, kTerms>::kPerSm)
 decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap omap,
                 const __grid_constant__ Args a, const __grid_constant__ Geo geo, WsHeader* hdr) {
-    using L = Smem<kT, kTerms>;
+    using L = Smem<kT, kU, kTerms>;
+    constexpr int kWarps = kU * kWork;
+    constexpr uint32_t kCols = kU == 1 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t base[];
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
-    auto btile = [&](int i) { return base + L::kB + (i % L::kStages) * kT * kTile; };
-    auto ctile = [&](int i) { return base + L::kC0 + (i % L::kStages) * kTile; };
+    auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, geo);
+    const Place pl = place(a, geo, kU);
     const bool returns = a.S_out && pl.seg == a.nseg - 1;
     if (pl.nc == 0 && !returns) {
         pdl_wait();                            // a dependent launch never ends before what it follows
@@ -232,22 +398,17 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         return;
     }
     if (tid == 0) {
-        mbar_init(&m.a_full, 1);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&m.b_full[s], 1);
-            mbar_init(&m.c_full[s], 1);
-        }
-        for (uint64_t* bar : {&m.p_full, &m.o2_full, &m.o_full, &m.hfree, &m.drain}) mbar_init(bar, 1);
-        for (uint64_t* bar : {&m.prep, &m.pt, &m.sread, &m.staged}) mbar_init(bar, kWork);
-        for (int s = 0; s < 4; ++s) mbar_init(&m.pair[s], 2);
+        for (uint64_t* bar : {&m.a_full, &m.b_full, &m.c_full[0], &m.c_full[1], &m.p_full, &m.s_full, &m.o_full, &m.drain})
+            mbar_init(bar, 1);
+        for (uint64_t* bar : {&m.prep, &m.pt, &m.staged}) mbar_init(bar, kWarps);
         fence_mbar_init();
         m.any = kNone;
     }
-    if (tid < 64) m.first[tid] = kNone;
+    if (tid < 128) m.first[tid] = kNone;
     const float l = a.decay[pl.h], l2 = log2_decay(l);
-    if (tid < 32) m.tab[tid] = pow2((kRev ? tid : 31 - tid) * l2);
-    if (warp == kWork) {
-        tmem_alloc(&m.tmem_slot, 256);
+    init_tables<kRev>(m, l2);
+    if (warp == kWarps) {
+        tmem_alloc(&m.tmem_slot, kCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -259,7 +420,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     const bool hold = hdr->hold_item != 0;     // test hook: loads never issued
     bool ok = true;
 
-    if (warp == kWork) {
+    if (warp == kWarps) {
         if (lane == 0 && pl.nc > 0) {
             const uint32_t base_a = smem_u32(base);
             const uint64_t ak = kmajor_desc(base_a + L::kA), bk = kmajor_desc(base_a + L::kB);
@@ -267,100 +428,111 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             const uint64_t sr = rows_desc(base_a + L::kS), wr = rows_desc(base_a + L::kW);
             constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);
-            int na = 0, nbc = 0;               // chunks of A, of B and C asked for
-            auto load_a = [&]() {
+            int nab = 0, nc = 0;               // chunks of A and B, of C asked for
+            auto load_ab = [&]() {
                 if (hold) return;
-                const int t = pl.chunk<kRev>(na) * kC;
+                const int t = pl.chunk<kRev>(nab) * kC;
                 mbar_arrive_expect_tx(&m.a_full, kT * kTile);
+                mbar_arrive_expect_tx(&m.b_full, kT * kTile);
 #pragma unroll
-                for (int k = 0; k < kT; ++k)
+                for (int k = 0; k < kT; ++k) {
                     tma_load_4d(base + L::kA + k * kTile, &amap, &m.a_full, 64 * k, geo.ah * pl.h, t, geo.ab * pl.b);
-                ++na;
+                    tma_load_4d(base + L::kB + k * kTile, &bmap, &m.b_full, 64 * k, geo.bh * pl.h, t, geo.bb * pl.b);
+                }
+                ++nab;
             };
-            auto load_bc = [&]() {
+            auto load_c = [&]() {
                 if (hold) return;
-                const int t = pl.chunk<kRev>(nbc) * kC, s = nbc % L::kStages;
-                mbar_arrive_expect_tx(&m.b_full[s], kT * kTile);
+                const int t = pl.chunk<kRev>(nc) * kC;
+                uint64_t* bar = &m.c_full[nc % L::kStages];
+                mbar_arrive_expect_tx(bar, kU * kTile);
 #pragma unroll
-                for (int k = 0; k < kT; ++k)
-                    tma_load_4d(btile(nbc) + k * kTile, &bmap, &m.b_full[s], 64 * k, geo.bh * pl.h, t, geo.bb * pl.b);
-                mbar_arrive_expect_tx(&m.c_full[s], kTile);
-                tma_load_4d(ctile(nbc), &cmap, &m.c_full[s], pl.col0, geo.ch * pl.h, t, geo.cb * pl.b);
-                ++nbc;
+                for (int u = 0; u < kU; ++u) tma_load_4d(ctile(nc, u), &cmap, bar, pl.col0 + 64 * u, geo.ch * pl.h, t, geo.cb * pl.b);
+                ++nc;
             };
-            auto scores = [&](int i) -> bool {
-                if (!mbar_wait(&m.a_full, i & 1, max_spin) ||
-                    !mbar_wait(&m.b_full[i % L::kStages], (i / L::kStages) & 1, max_spin))
-                    return false;
+            auto scores = [&](int i) -> bool {                                                          // (1)
+                if (!mbar_wait(&m.a_full, i & 1, max_spin) || !mbar_wait(&m.b_full, i & 1, max_spin)) return false;
                 tc_fence_after();
-                const uint64_t b = step_desc(bk, (i % L::kStages) * kT * kTile);
 #pragma unroll
-                for (int k = 0; k < 4 * kT; ++k) mma_bf16(tmem + kTmP, kmajor_step(ak, k), kmajor_step(b, k), id_sc, k > 0);
+                for (int k = 0; k < 4 * kT; ++k) mma_bf16(tmem + kTmP, kmajor_step(ak, k), kmajor_step(bk, k), id_sc, k > 0);
                 mma_commit(&m.p_full);
                 return true;
             };
-            // The output of chunk i, staged by the working warps; the last, ragged one of a
-            // sequence shorter than N was written row by row.
+            // The output of chunk i, staged by the working warps where C was; the last, ragged
+            // one of a sequence shorter than N was written row by row.
             auto put = [&](int i) -> bool {
                 if (!mbar_wait(&m.staged, i & 1, max_spin)) return false;
                 const int t = pl.chunk<kRev>(i) * kC;
                 if (t + kC <= pl.n || pl.n == a.N) {
-                    tma_store_4d(&omap, base + L::kW, pl.col0, pl.h, t, pl.b);
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) tma_store_4d(&omap, ctile(i, u), pl.col0 + 64 * u, pl.h, t, pl.b);
                     tma_store_commit();
                 }
                 return true;
             };
-            load_a();
-            for (int s = 0; s < L::kStages && s < pl.nc; ++s) load_bc();
+            load_ab();
+            for (int s = 0; s < L::kStages && s < pl.nc; ++s) load_c();
+            ok = scores(0);
             for (int i = 0; i < pl.nc && ok; ++i) {
-                if (i == 0) {
-                    ok = scores(0);
-                } else if ((ok = put(i - 1))) {
+                const int s = i % L::kStages;
+                if (L::kStages == 1 && i > 0) {        // C of this chunk, once the output before it has left its place
                     tma_store_wait_read<0>();
-                    mbar_arrive(&m.hfree);
+                    load_c();
                 }
-                if (!ok || !(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
+                if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4 * kT; ++k)                                                        // (2)
-                    mma_bf16(tmem + kTmO2, kmajor_step(ak, k), step_desc(sr, k * 2048), id_o, k > 0);
-                mma_commit(&m.o2_full);
+                for (int u = 0; u < kU; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4 * kT; ++k)                                                    // (2)
+                        mma_bf16(tmem + kTmO2 + kTmUnit * u, kmajor_step(ak, k),
+                                 step_desc(sr, u * kT * kTile / 2 + k * 2048), id_o, k > 0);
+#pragma unroll
+                for (int u = 0; u < kU; ++u)                                                            // (4)
+                    issue_state<kTerms>(tmem + kTmX + kTmUnit * u, br, step_desc(wr, u * kTerms * kTile));
+                mma_commit(&m.s_full);
+                if (L::kStages == 2 && i > 0 && i + 1 < pl.nc) {
+                    tma_store_wait_read<0>();
+                    load_c();
+                }
+                if (!(ok = mbar_wait(&m.s_full, i & 1, max_spin))) break;
+                if (i + 1 < pl.nc) load_ab();
                 if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
                 tc_fence_after();
-                const int s = i % L::kStages;
-                issue_state<kTerms>(tmem + kTmSt, step_desc(br, s * kT * kTile), wr);                   // (4)
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k)                                                       // (3)
-                    mma_bf16_ts(tmem + kTmO1, tmem + kTmP + 8 * k, step_desc(cr, s * kTile + k * 2048), id_o, k > 0);
+                for (int u = 0; u < kU; ++u)
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)                                                   // (3)
+                        mma_bf16_ts(tmem + kTmX + kTmUnit * u, tmem + kTmP + 32 * (k >> 1) + 8 * (k & 1),
+                                    step_desc(cr, (s * kU + u) * kTile + k * 2048), id_o, k > 0);
                 mma_commit(&m.o_full);
-                if (!(ok = mbar_wait(&m.o2_full, i & 1, max_spin))) break;
-                if (i + 1 < pl.nc) load_a();
                 if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
-                if (i + L::kStages < pl.nc) load_bc();
-                if (i + 1 < pl.nc) ok = mbar_wait(&m.sread, i & 1, max_spin) && scores(i + 1);
+                if (i + 1 < pl.nc && !(ok = scores(i + 1))) break;
+                ok = put(i);
             }
-            if (ok) ok = put(pl.nc - 1);
             tma_store_wait_all<0>();
             // Every load that was asked for lands, and every product completes, before the CTA exits.
-            if (na > 0) mbar_wait(&m.a_full, (na - 1) & 1, kDefaultMaxSpin);
-            for (int j = max(nbc - L::kStages, 0); j < nbc; ++j) {
-                mbar_wait(&m.b_full[j % L::kStages], (j / L::kStages) & 1, kDefaultMaxSpin);
-                mbar_wait(&m.c_full[j % L::kStages], (j / L::kStages) & 1, kDefaultMaxSpin);
+            if (nab > 0) {
+                mbar_wait(&m.a_full, (nab - 1) & 1, kDefaultMaxSpin);
+                mbar_wait(&m.b_full, (nab - 1) & 1, kDefaultMaxSpin);
             }
+            for (int j = max(nc - L::kStages, 0); j < nc; ++j)
+                mbar_wait(&m.c_full[j % L::kStages], (j / L::kStages) & 1, kDefaultMaxSpin);
             mma_commit(&m.drain);
             ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
         }
         __syncwarp();
     } else {
-        const int q = warp & 3, g = warp >> 2, row = 32 * q + lane;
-        const int qm = kRev ? 3 - q : q, im = kRev ? 127 - lane - 32 * q : row;   // in the order of summation
-        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        const int q = warp & 3, g4 = warp >> 2, u = g4 >> 1, g = g4 & 1, row = 32 * q + lane;
+        const int qm = kRev ? 3 - q : q, im = kRev ? 127 - row : row;
+        const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16), tmu = tm + kTmUnit * u + 32 * g;
         const bool has_state = q < 2 * kT;
         const int64_t state = (int64_t)a.Da * a.Dc, bh = (int64_t)pl.b * a.H + pl.h;
-        auto piece = [&](int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); };
-        // State row `row`, columns col0 + 32 g ..
+        const RowFactors rf = row_factors(l2, im);
+        uint8_t *terms = base + L::kW + u * kTerms * kTile, *s_tile = base + L::kS + u * kT * kTile / 2;
+        // State row `row`, columns col0 + 64 u + 32 g ..
         float st[32];
-        const int c0 = pl.col0 + 32 * g;
+        const int c0 = pl.col0 + 64 * u + 32 * g;
         const float* from = a.nseg > 1 ? a.seeds + (bh * a.nseg + pl.seg) * state : (a.S0 ? a.S0 + bh * state : nullptr);
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
@@ -368,150 +540,58 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             if (has_state && from && row < a.Da && c0 + k < a.Dc) v = *reinterpret_cast<const float4*>(from + (int64_t)row * a.Dc + c0 + k);
             st[k] = v.x, st[k + 1] = v.y, st[k + 2] = v.z, st[k + 3] = v.w;
         }
-        const float read = a.scale * pow2((im + 1) * l2);   // weight of the state in this row's output
+        const float read = a.scale * pow2((float)(im + 1) * l2);   // weight of the state in this row's output
+        const Factor whole = factor(kC * log_decay(l));
         for (int i = 0; i < pl.nc; ++i) {
             const int t0 = pl.chunk<kRev>(i) * kC, mt = min(kC, pl.n - t0), s = i % L::kStages, ph = (i / L::kStages) & 1;
-            uint8_t *ct = ctile(i), *w0 = base + L::kW;
-            // ---------------------------------------------------- state to bf16, first term of w C
-            if (has_state)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4*>(base + L::kS + piece(4 * g + j)) =
-                        make_uint4(pack_bf16(st[8 * j], st[8 * j + 1]), pack_bf16(st[8 * j + 2], st[8 * j + 3]),
-                                   pack_bf16(st[8 * j + 4], st[8 * j + 5]), pack_bf16(st[8 * j + 6], st[8 * j + 7]));
-            if (i > 0 && !(ok = warp_wait(&m.hfree, (i - 1) & 1, max_spin))) break;
+            uint8_t* ct = ctile(i, u);
+            // ---------------------------------------------------- state to bf16, w C
+            if (has_state) write_state(s_tile, st, row, g);
             if (!(ok = warp_wait(&m.c_full[s], ph, max_spin))) break;
-            // Rows at or past a sequence's end may hold anything: cleared in C, and in B for (4).
-            // (Past N the loads filled zeros.)
+            // Rows past the sequence's end are cleared in C, and in B for (4). (Past N the loads
+            // filled zeros.) (1) may read such rows of B, whose scores take no part.
             const bool ragged = mt < kC && pl.n < a.N;
             if (ragged) {
-                if (!(ok = warp_wait(&m.b_full[s], ph, max_spin))) break;
-                if (row >= mt)
-                    for (int j = 4 * g; j < 4 * g + 4; ++j) {
-                        *reinterpret_cast<uint4*>(ct + piece(j)) = make_uint4(0, 0, 0, 0);
-                        for (int k = 0; k < kT; ++k)
-                            *reinterpret_cast<uint4*>(btile(i) + k * kTile + piece(j)) = make_uint4(0, 0, 0, 0);
-                    }
+                if (!(ok = warp_wait(&m.b_full, i & 1, max_spin))) break;
+                if (row >= mt) {
+                    clear_pieces(ct, row, g);
+                    for (int k = 0; k < kT; ++k) clear_pieces(base + L::kB + k * kTile, row, g);
+                }
             }
             const float w = pow2((float)(kRev ? row : max(mt - 1 - row, 0)) * l2);
-            const uint64_t w2 = pk2(w, w);
-            uint64_t bad = 0;
-#pragma unroll
-            for (int j = 4 * g; j < 4 * g + 4; ++j) {
-                const uint4 c = *reinterpret_cast<const uint4*>(ct + piece(j));
-                uint32_t hi[4];
-                uint64_t rest[4];
-                weigh8(c, w2, hi, rest);
-                *reinterpret_cast<uint4*>(w0 + piece(j)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                bad = fma2(bf2(c.x), 0, fma2(bf2(c.y), 0, fma2(bf2(c.z), 0, fma2(bf2(c.w), 0, bad))));
-            }
-            float b0, b1;
-            unpk2(bad, &b0, &b1);
-            if (!(b0 == 0.f && b1 == 0.f)) take_out(ct, row, g, i * kC + im, &m);
+            if (!write_weighted<kTerms>(ct, terms, w, row, g)) take_out(ct, row, g, i * kC + im, &m.any, m.first + 64 * u);
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
             // ---------------------------------------------------- scores to P
             if (!(ok = warp_wait(&m.p_full, i & 1, max_spin))) break;
             tc_fence_after();
-            uint32_t p[2][16];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int bm = g + 2 * k, blk = kRev ? 3 - bm : bm;
-                if (bm > qm) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) p[k][e] = 0u;
-                    continue;
-                }
-                const float r = pow2((float)(im - 32 * bm - 31) * l2);
-                const uint64_t r2 = pk2(r, r);
-#pragma unroll
-                for (int half = 0; half < 32; half += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(tmem + lanes + kTmP + 32 * blk + half, v);
-                    tmem_ld_wait();
-                    if (ragged && kRev && 32 * blk + 32 > mt)   // later tokens that the sequence does not have
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (32 * blk + half + e >= mt) v[e] = 0u;
-                    if (bm < qm) {
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.tab + half + 2 * e);
-                            p[k][half / 2 + e] = pack2(mul2(mul2(pair2(v + 2 * e), f.x), r2));
-                            p[k][half / 2 + e + 1] = pack2(mul2(mul2(pair2(v + 2 * e + 2), f.y), r2));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float x[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int j = half + 2 * e + u, gap = kRev ? j - lane : lane - j;
-                                x[u] = gap >= 0 ? __uint_as_float(v[2 * e + u]) * pow2((float)gap * l2) : 0.f;
-                            }
-                            p[k][half / 2 + e] = pack_bf16(x[0], x[1]);
-                        }
-                    }
-                }
-            }
-            // Both warps of these rows have read their scores before either writes P over them.
-            tc_fence_before();
-            warp_arrive(&m.pair[q]);
-            if (!(ok = warp_wait(&m.pair[q], i & 1, max_spin))) break;
+#pragma unroll 1
+            for (int bm = g4; bm < 4; bm += 2 * kU)
+                scores_to_p<kRev>(tm, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
+            // ---------------------------------------------------- state
+            if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 2; ++k) tmem_st16(tmem + lanes + kTmP + 16 * (kRev ? 3 - g - 2 * k : g + 2 * k), p[k]);
-            // ---------------------------------------------------- the other terms of w C
-            if (!(ok = warp_wait(&m.o2_full, i & 1, max_spin))) break;
-#pragma unroll
-            for (int j = 4 * g; j < 4 * g + 4; ++j) {
-                uint32_t t[4];
-                uint64_t rest[4];
-                weigh8(*reinterpret_cast<const uint4*>(ct + piece(j)), w2, t, rest);
-#pragma unroll
-                for (int k = 1; k < kTerms; ++k) {
-                    next_term(rest, t);
-                    *reinterpret_cast<uint4*>(w0 + k * kTile + piece(j)) = make_uint4(t[0], t[1], t[2], t[3]);
-                }
-            }
+            if (has_state) join_state(tmu + kTmX, kRev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
             tmem_st_wait();
-            fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.pt);
-            // ---------------------------------------------------- state
+            // ---------------------------------------------------- output
             if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
             tc_fence_after();
-            if (has_state) {
-                const Factor f = factor((float)(kRev ? kC : mt) * log_decay(l));
-                uint32_t v[32];
-                tmem_ld16(tmem + lanes + kTmSt + 32 * g, *reinterpret_cast<uint32_t(*)[16]>(v));
-                tmem_ld16(tmem + lanes + kTmSt + 32 * g + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) st[k] = fmaf(f.hi, st[k], fmaf(f.lo, st[k], __uint_as_float(v[k])));
-            }
-            tc_fence_before();
-            warp_arrive(&m.sread);
-            // ---------------------------------------------------- output
             const bool spoiled = *const_cast<volatile int*>(&m.any) != kNone;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                uint32_t u[16], v[16], o[8];
-                tmem_ld16(tmem + lanes + kTmO1 + 32 * g + 16 * k, u);
-                tmem_ld16(tmem + lanes + kTmO2 + 32 * g + 16 * k, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    o[e] = pack2(fma2(pair2(u + 2 * e), pk2(a.scale, a.scale), mul2(pair2(v + 2 * e), pk2(read, read))));
-                uint4 x = make_uint4(o[0], o[1], o[2], o[3]), y = make_uint4(o[4], o[5], o[6], o[7]);
+                uint4 x, y;
+                join_output(tmu + kTmX + 16 * k, tmu + kTmO2 + 16 * k, a.scale, read, &x, &y);
                 if (spoiled) {
-                    x = put_nan(&m, 32 * g + 16 * k, i * kC + im, x);
-                    y = put_nan(&m, 32 * g + 16 * k + 8, i * kC + im, y);
+                    const int* first = m.first + 64 * u + 32 * g + 16 * k;
+                    x = put_nan(first, i * kC + im, x);
+                    y = put_nan(first + 8, i * kC + im, y);
                 }
                 if (!ragged) {
-                    *reinterpret_cast<uint4*>(w0 + piece(4 * g + 2 * k)) = x;
-                    *reinterpret_cast<uint4*>(w0 + piece(4 * g + 2 * k + 1)) = y;
+                    *reinterpret_cast<uint4*>(ct + row * 128 + (((4 * g + 2 * k) ^ (row & 7)) << 4)) = x;
+                    *reinterpret_cast<uint4*>(ct + row * 128 + (((4 * g + 2 * k + 1) ^ (row & 7)) << 4)) = y;
                 } else if (row < mt) {
                     const int c = c0 + 16 * k;
                     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(const_cast<void*>(a.o.p)) + pl.b * a.o.bs + pl.h * a.o.hs +
@@ -535,21 +615,22 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWork) tmem_dealloc(tmem, 256);
+    if (warp == kWarps) tmem_dealloc(tmem, kCols);
 }
 
 // First pass: a segment's end state from zero (every segment but the last).
-template <int kT, int kTerms, bool kRev>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int kT, int kU, int kTerms, bool kRev>
+__global__ void __launch_bounds__(32 * (kU * kWork + 1), SumSmem<kT, kU, kTerms>::kPerSm)
 decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap,
                   const __grid_constant__ Args a, const __grid_constant__ Geo geo, WsHeader* hdr) {
-    using L = SumSmem<kT, kTerms>;
+    using L = SumSmem<kT, kU, kTerms>;
+    constexpr int kWarps = kU * kWork;
     extern __shared__ __align__(1024) uint8_t base[];
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto btile = [&](int i) { return base + L::kB + (i % L::kStages) * kT * kTile; };
-    auto ctile = [&](int i) { return base + L::kC0 + (i % L::kStages) * kTile; };
+    auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, geo);
+    const Place pl = place(a, geo, kU);
     pdl_launch_dependents();
     if (pl.nc == 0) return;                    // the chaining leaves such segments out
     if ((smem_u32(base) & 1023) != 0) {
@@ -557,17 +638,15 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
         return;
     }
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&m.b_full[s], 1);
-            mbar_init(&m.c_full[s], 1);
-        }
-        mbar_init(&m.prep, kWork);
-        mbar_init(&m.o_full, 1);
+        mbar_init(&m.c_full[0], 1);
+        mbar_init(&m.c_full[1], 1);
+        mbar_init(&m.prep, kWarps);
+        mbar_init(&m.s_full, 1);
         mbar_init(&m.drain, 1);
         fence_mbar_init();
     }
-    if (warp == kWork) {
-        tmem_alloc(&m.tmem_slot, 64);
+    if (warp == kWarps) {
+        tmem_alloc(&m.tmem_slot, 64 * kU);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -578,88 +657,64 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
     const bool hold = hdr->hold_item != 0;
     const float l = a.decay[pl.h], l2 = log2_decay(l);
     bool ok = true;
-    if (warp == kWork) {
+    if (warp == kWarps) {
         if (lane == 0) {
             const uint64_t br = rows_desc(smem_u32(base) + L::kB), wr = rows_desc(smem_u32(base) + L::kW);
-            int nbc = 0;
-            auto load_bc = [&]() {
+            int n = 0;
+            auto load = [&]() {
                 if (hold) return;
-                const int t = pl.chunk<kRev>(nbc) * kC, s = nbc % L::kStages;
-                mbar_arrive_expect_tx(&m.c_full[s], kTile);
-                tma_load_4d(ctile(nbc), &cmap, &m.c_full[s], pl.col0, geo.ch * pl.h, t, geo.cb * pl.b);
-                mbar_arrive_expect_tx(&m.b_full[s], kT * kTile);
+                const int t = pl.chunk<kRev>(n) * kC;
+                uint64_t* bar = &m.c_full[n % L::kStages];
+                mbar_arrive_expect_tx(bar, (kT + kU) * kTile);
 #pragma unroll
-                for (int k = 0; k < kT; ++k)
-                    tma_load_4d(btile(nbc) + k * kTile, &bmap, &m.b_full[s], 64 * k, geo.bh * pl.h, t, geo.bb * pl.b);
-                ++nbc;
+                for (int u = 0; u < kU; ++u) tma_load_4d(ctile(n, u), &cmap, bar, pl.col0 + 64 * u, geo.ch * pl.h, t, geo.cb * pl.b);
+#pragma unroll
+                for (int k = 0; k < kT; ++k) tma_load_4d(btile(n) + k * kTile, &bmap, bar, 64 * k, geo.bh * pl.h, t, geo.bb * pl.b);
+                ++n;
             };
-            for (int s = 0; s < L::kStages && s < pl.nc; ++s) load_bc();
+            for (int s = 0; s < L::kStages && s < pl.nc; ++s) load();
             for (int i = 0; i < pl.nc; ++i) {
-                const int s = i % L::kStages;
-                if (!(ok = mbar_wait(&m.b_full[s], (i / L::kStages) & 1, max_spin) && mbar_wait(&m.prep, i & 1, max_spin))) break;
+                if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
                 tc_fence_after();
-                issue_state<kTerms>(tmem, step_desc(br, s * kT * kTile), wr);
-                mma_commit(&m.o_full);
-                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
-                if (i + L::kStages < pl.nc) load_bc();
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    issue_state<kTerms>(tmem + 64 * u, step_desc(br, (i % L::kStages) * kT * kTile), step_desc(wr, u * kTerms * kTile));
+                mma_commit(&m.s_full);
+                if (!(ok = mbar_wait(&m.s_full, i & 1, max_spin))) break;
+                if (i + L::kStages < pl.nc) load();
             }
-            for (int j = max(nbc - L::kStages, 0); j < nbc; ++j) {
-                mbar_wait(&m.b_full[j % L::kStages], (j / L::kStages) & 1, kDefaultMaxSpin);
+            for (int j = max(n - L::kStages, 0); j < n; ++j)
                 mbar_wait(&m.c_full[j % L::kStages], (j / L::kStages) & 1, kDefaultMaxSpin);
-            }
             mma_commit(&m.drain);
             ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
         }
         __syncwarp();
     } else {
-        const int q = warp & 3, g = warp >> 2, row = 32 * q + lane;
-        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        const int q = warp & 3, u = warp >> 3, g = (warp >> 2) & 1, row = 32 * q + lane;
         const bool has_state = q < 2 * kT;
-        auto piece = [&](int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); };
+        uint8_t* terms = base + L::kW + u * kTerms * kTile;
+        const Factor whole = factor(kC * log_decay(l));
         float st[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) st[k] = 0.f;
         for (int i = 0; i < pl.nc; ++i) {
-            const int t0 = pl.chunk<kRev>(i) * kC, mt = min(kC, pl.n - t0), s = i % L::kStages, ph = (i / L::kStages) & 1;
-            uint8_t *ct = ctile(i), *w0 = base + L::kW;
-            if (!(ok = warp_wait(&m.c_full[s], ph, max_spin))) break;
-            const bool ragged = mt < kC && pl.n < a.N;
-            if (ragged && !(ok = warp_wait(&m.b_full[s], ph, max_spin))) break;
-            const float w = pow2((float)(kRev ? row : max(mt - 1 - row, 0)) * l2);
-            const uint64_t w2 = pk2(w, w);
-#pragma unroll
-            for (int j = 4 * g; j < 4 * g + 4; ++j) {
-                uint4 c = *reinterpret_cast<const uint4*>(ct + piece(j));
-                if (ragged && row >= mt) {
-                    c = make_uint4(0, 0, 0, 0);
-                    for (int k = 0; k < kT; ++k) *reinterpret_cast<uint4*>(btile(i) + k * kTile + piece(j)) = c;
-                }
-                uint32_t t[4];
-                uint64_t rest[4];
-                weigh8(c, w2, t, rest);
-                *reinterpret_cast<uint4*>(w0 + piece(j)) = make_uint4(t[0], t[1], t[2], t[3]);
-#pragma unroll
-                for (int k = 1; k < kTerms; ++k) {
-                    next_term(rest, t);
-                    *reinterpret_cast<uint4*>(w0 + k * kTile + piece(j)) = make_uint4(t[0], t[1], t[2], t[3]);
-                }
+            const int mt = min(kC, pl.n - pl.chunk<kRev>(i) * kC);
+            if (!(ok = warp_wait(&m.c_full[i % L::kStages], (i / L::kStages) & 1, max_spin))) break;
+            if (mt < kC && pl.n < a.N && row >= mt) {
+                clear_pieces(ctile(i, u), row, g);
+                for (int k = 0; k < kT; ++k) clear_pieces(btile(i) + k * kTile, row, g);
             }
+            write_weighted<kTerms>(ctile(i, u), terms, pow2((float)(kRev ? row : max(mt - 1 - row, 0)) * l2), row, g);
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
-            if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
+            if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
-            if (has_state) {
-                const Factor f = factor((float)(kRev ? kC : mt) * log_decay(l));
-                uint32_t v[32];
-                tmem_ld16(tmem + lanes + 32 * g, *reinterpret_cast<uint32_t(*)[16]>(v));
-                tmem_ld16(tmem + lanes + 32 * g + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) st[k] = fmaf(f.hi, st[k], fmaf(f.lo, st[k], __uint_as_float(v[k])));
-            }
+            if (has_state)
+                join_state(tmem + ((uint32_t)(32 * q) << 16) + 64 * u + 32 * g,
+                           kRev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
         }
-        const int c0 = pl.col0 + 32 * g;
+        const int c0 = pl.col0 + 64 * u + 32 * g;
         float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc + (int64_t)row * a.Dc + c0;
         if (ok && has_state && row < a.Da)
 #pragma unroll
@@ -670,7 +725,7 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWork) tmem_dealloc(tmem, 64);
+    if (warp == kWarps) tmem_dealloc(tmem, 64 * kU);
 }
 
 // Rows [B, H, N, D] of bf16 as a 4-D map (D, H, N, B) with boxes of 64 values x 128 tokens;
@@ -695,28 +750,29 @@ struct Maps {
     CUtensorMap a, b, c, o;
 };
 
-template <int kT, int kTerms, bool kRev>
+template <int kT, int kU, int kTerms, bool kRev>
 cudaError_t launch(const Maps& maps, const Args& a, const Geo& geo, WsHeader* hdr, cudaStream_t st) {
     static std::atomic<int> optin[2][kMaxDevices];
-    const unsigned units = (a.Dc + 63) / 64, BH = (unsigned)(a.B * a.H);
+    constexpr int threads = 32 * (kU * kWork + 1);
+    const unsigned blocks = (a.Dc + 64 * kU - 1) / (64 * kU), BH = (unsigned)(a.B * a.H);
     cudaError_t e;
     if (a.nseg > 1) {
-        constexpr int bytes = SumSmem<kT, kTerms>::kBytes;
-        if ((e = ensure_smem_optin(decay_sums_kernel<kT, kTerms, kRev>, bytes, optin[0])) != cudaSuccess) return e;
-        decay_sums_kernel<kT, kTerms, kRev><<<dim3(units, a.nseg - 1, BH), kThreads, bytes, st>>>(maps.b, maps.c, a, geo, hdr);
+        constexpr int bytes = SumSmem<kT, kU, kTerms>::kBytes;
+        if ((e = ensure_smem_optin(decay_sums_kernel<kT, kU, kTerms, kRev>, bytes, optin[0])) != cudaSuccess) return e;
+        decay_sums_kernel<kT, kU, kTerms, kRev><<<dim3(blocks, a.nseg - 1, BH), threads, bytes, st>>>(maps.b, maps.c, a, geo, hdr);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         if ((e = launch_chain(a, kC, st)) != cudaSuccess) return e;
     }
-    constexpr int bytes = Smem<kT, kTerms>::kBytes;
-    if ((e = ensure_smem_optin(decay_tc_kernel<kT, kTerms, kRev>, bytes, optin[1])) != cudaSuccess) return e;
-    return scan::launch_after(decay_tc_kernel<kT, kTerms, kRev>, dim3(units, a.nseg, BH), kThreads, bytes, st, a.nseg > 1,
+    constexpr int bytes = Smem<kT, kU, kTerms>::kBytes;
+    if ((e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev>, bytes, optin[1])) != cudaSuccess) return e;
+    return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev>, dim3(blocks, a.nseg, BH), threads, bytes, st, a.nseg > 1,
                               maps.a, maps.b, maps.c, maps.o, a, geo, hdr);
 }
 
-template <int kT>
+template <int kT, int kU>
 cudaError_t launch_form(const Maps& maps, const Args& a, const Geo& geo, WsHeader* hdr, cudaStream_t st) {
-    if (a.rev) return launch<kT, 2, true>(maps, a, geo, hdr, st);
-    return a.S_out ? launch<kT, 3, false>(maps, a, geo, hdr, st) : launch<kT, 2, false>(maps, a, geo, hdr, st);
+    if (a.rev) return launch<kT, kU, 2, true>(maps, a, geo, hdr, st);
+    return a.S_out ? launch<kT, kU, 3, false>(maps, a, geo, hdr, st) : launch<kT, kU, 2, false>(maps, a, geo, hdr, st);
 }
 
 }  // namespace
@@ -737,8 +793,7 @@ bool tc_supported(const Args& a, la_dtype dt) {
 }
 
 int tc_segments(int64_t BH, int N, int Da, int Dc) {
-    (void)Da;
-    const int64_t ctas = BH * ((Dc + 63) / 64), slots = 2 * (int64_t)sm_count();
+    const int64_t ctas = BH, slots = (Da <= 64 && Dc <= 64 ? 2 : 1) * (int64_t)sm_count();
     const int64_t most = (N + kC - 1) / kC / 4;
     int64_t n = ctas > 0 ? slots / ctas : 1;
     n = n < most ? n : most;
@@ -756,7 +811,8 @@ cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
         !encode_rows(&maps.o, a.o, a.Dc, a.B, a.H, a.N, nullptr, nullptr))
         return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
-    return a.Da <= 64 ? launch_form<1>(maps, a, geo, hdr, st) : launch_form<2>(maps, a, geo, hdr, st);
+    if (a.Da <= 64) return a.Dc <= 64 ? launch_form<1, 1>(maps, a, geo, hdr, st) : launch_form<1, 2>(maps, a, geo, hdr, st);
+    return a.Dc <= 64 ? launch_form<2, 1>(maps, a, geo, hdr, st) : launch_form<2, 2>(maps, a, geo, hdr, st);
 }
 
 }  // namespace decay
