@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -210,7 +211,9 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
 // segments start from, seed_0 = S0, seed_{i+1} = e^{l tokens_i} seed_i + end_i. A thread
 // chains one element, eight segments in flight.
 constexpr int kMaxSegments = 64;
-__global__ void __launch_bounds__(128) chain_kernel(const __grid_constant__ Args a, int chunk) {
+__global__ void __launch_bounds__(128)
+chain_kernel(const __grid_constant__ Args first, const __grid_constant__ Args second, int chunk) {
+    const Args& a = blockIdx.z ? second : first;
     __shared__ Factor f[kMaxSegments];
     __shared__ int empty[kMaxSegments];
     const int64_t bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
@@ -332,7 +335,7 @@ cudaError_t run_width(const Args& a, cudaStream_t st) {
         if ((e = tcc::ensure_smem_optin(decay_kernel<T, kD, true>, kSums, optin[1])) != cudaSuccess) return e;
         decay_kernel<T, kD, true><<<dim3(a.nseg - 1, blocks, BH), 256, kSums, st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
-        if ((e = launch_chain(a, 1, st)) != cudaSuccess) return e;
+        if ((e = launch_chain(&a, 1, 1, st)) != cudaSuccess) return e;
     }
     return scan::launch_after(decay_kernel<T, kD, false>, dim3(a.nseg, blocks, BH), 256, kMain, st, a.nseg > 1, a);
 }
@@ -353,16 +356,17 @@ int simt_segments(int64_t BH, int N, int Da, int Dc) {
     return n < 2 ? 1 : (int)n;
 }
 
-cudaError_t run(Args a, la_dtype dt, void* workspace, cudaStream_t st) {
-    const int64_t BH = (int64_t)a.B * a.H;
-    const bool tc = tc_supported(a, dt);
-    const int chunk = tc ? tcc::kC : kL, chunks = (a.N + chunk - 1) / chunk;
-    a.nseg = tc ? tc_segments(BH, a.N, a.Da, a.Dc) : simt_segments(BH, a.N, a.Da, a.Dc);
-    const int per = (chunks + a.nseg - 1) / a.nseg;
-    a.nseg = (chunks + per - 1) / per;
-    a.seg_len = per * chunk;
-    a.seeds = reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(WsHeader));
-    return tc ? tc_run(a, workspace, st) : dt == LA_BF16 ? run_simt<__nv_bfloat16>(a, st) : run_simt<float>(a, st);
+size_t simt_seeds(int64_t BH, int N, int Da, int Dc) {
+    const int n = simt_segments(BH, N, Da, Dc);
+    return n > 1 ? (size_t)BH * n * Da * Dc : 0;
+}
+
+float* seeds_of(void* workspace) { return reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(WsHeader)); }
+
+cudaError_t run_cuda_cores(Args a, la_dtype dt, void* workspace, cudaStream_t st) {
+    cut(&a, simt_segments((int64_t)a.B * a.H, a.N, a.Da, a.Dc), kL);
+    a.seeds = seeds_of(workspace);
+    return dt == LA_BF16 ? run_simt<__nv_bfloat16>(a, st) : run_simt<float>(a, st);
 }
 
 constexpr int64_t kPromptHeads = 65535, kStepHeads = 2147483647;   // grid axes
@@ -436,40 +440,26 @@ Tensor tensor(const void* p, const int64_t* s) { return {p, s[0], s[1], s[2]}; }
 
 namespace decay {
 
-cudaError_t launch_chain(const Args& a, int chunk, cudaStream_t st) {
-    return scan::launch_after(chain_kernel, dim3((a.Da * a.Dc + 127) / 128, (unsigned)(a.B * a.H)), 128, 0, st, true, a,
-                              chunk);
+cudaError_t launch_chain(const Args* a, int count, int chunk, cudaStream_t st) {
+    return scan::launch_after(chain_kernel, dim3((a->Da * a->Dc + 127) / 128, (unsigned)(a->B * a->H), count), 128, 0, st,
+                              true, a[0], a[count - 1], chunk);
 }
 
 }  // namespace decay
 
-namespace {
-
-// Segments of one sum, whichever path its strides let it take.
-int most_segments(int64_t BH, int N, int Da, int Dc, la_dtype dt) {
-    const int x = simt_segments(BH, N, Da, Dc);
-    const int y = dt == LA_BF16 && Da % 8 == 0 && Dc % 8 == 0 ? tc_segments(BH, N, Da, Dc) : 1;
-    return x > y ? x : y;
-}
-
-}  // namespace
-
+// Enough for either path: rows that are not aligned take the CUDA cores.
 size_t decay_workspace(int B, int H, int N, int Dk, int Dv, la_dtype dt, bool backward) {
     const int64_t BH = (int64_t)B * H;
-    int n = most_segments(BH, N, Dk, Dv, dt);
-    if (backward) {
-        const int m = most_segments(BH, N, Dv, Dk, dt);
-        n = m > n ? m : n;
-    }
-    return n > 1 ? (size_t)BH * n * Dk * Dv * sizeof(float) : 0;
+    size_t most = simt_seeds(BH, N, Dk, Dv);
+    if (backward) most = std::max(most, simt_seeds(BH, N, Dv, Dk));
+    if (dt == LA_BF16 && Dk % 8 == 0 && Dv % 8 == 0) most = std::max(most, tc_seeds(BH, N, Dk, Dv, backward));
+    return most * sizeof(float);
 }
 
 int decay_launches(int B, int H, int N, int Dk, int Dv, la_dtype dt, bool backward) {
-    auto one = [&](int Da, int Dc) {
-        const bool tc = dt == LA_BF16 && Da % 8 == 0 && Dc % 8 == 0;
-        const int64_t BH = (int64_t)B * H;
-        return (tc ? tc_segments(BH, N, Da, Dc) : simt_segments(BH, N, Da, Dc)) > 1 ? 3 : 1;
-    };
+    const int64_t BH = (int64_t)B * H;
+    if (dt == LA_BF16 && Dk % 8 == 0 && Dv % 8 == 0) return tc_launches(BH, N, Dk, Dv, backward);
+    auto one = [&](int Da, int Dc) { return simt_segments(BH, N, Da, Dc) > 1 ? 3 : 1; };
     return backward ? 2 * one(Dv, Dk) + one(Dk, Dv) : one(Dk, Dv);
 }
 
@@ -513,7 +503,11 @@ la_status la_decay_attn_fwd(const void* q, const void* k, const void* v, const f
     a.o = la::tensor(o, strides + 9);
     a.decay = decay, a.lengths = lengths, a.S0 = S0, a.S_out = S_out;
     a.B = B, a.H = H, a.N = N, a.Da = Dk, a.Dc = Dv, a.scale = scale;
-    return la::run(a, dt, workspace, st) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    if (la::tc_supported(a, dt)) {
+        a.seeds = la::seeds_of(workspace);
+        return la::tc_run(a, workspace, st) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    }
+    return la::run_cuda_cores(a, dt, workspace, st) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 la_status la_decay_attn_bwd(const void* q, const void* k, const void* v, const void* dout, const float* decay,
@@ -546,12 +540,17 @@ la_status la_decay_attn_bwd(const void* q, const void* k, const void* v, const v
     la::decay::Args a = {};
     a.decay = decay, a.lengths = lengths, a.B = B, a.H = H, a.N = N, a.scale = scale;
     const la::decay::Tensor Q = la::tensor(q, sq), K = la::tensor(k, sk), V = la::tensor(v, sv), G = la::tensor(dout, sg);
-    struct { la::decay::Tensor a, b, c, o; int Da, Dc, rev; } sums[3] = {
-        {G, V, K, la::tensor(dq, tq), Dv, Dk, 0}, {V, G, Q, la::tensor(dk, tk), Dv, Dk, 1}, {K, Q, G, la::tensor(dv, tv), Dk, Dv, 1}};
-    for (const auto& u : sums) {
-        a.a = u.a, a.b = u.b, a.c = u.c, a.o = u.o, a.Da = u.Da, a.Dc = u.Dc, a.rev = u.rev;
-        if (la::run(a, dt, workspace, (cudaStream_t)stream) != cudaSuccess) return LA_ERR_CUDA;
+    la::decay::Args dqs = a, dks = a, dvs = a;
+    dqs.a = G, dqs.b = V, dqs.c = K, dqs.o = la::tensor(dq, tq), dqs.Da = Dv, dqs.Dc = Dk;
+    dks.a = V, dks.b = G, dks.c = Q, dks.o = la::tensor(dk, tk), dks.Da = Dv, dks.Dc = Dk, dks.rev = 1;
+    dvs.a = K, dvs.b = Q, dvs.c = G, dvs.o = la::tensor(dv, tv), dvs.Da = Dk, dvs.Dc = Dv, dvs.rev = 1;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (la::tc_supported(dqs, dt) && la::tc_supported(dks, dt) && la::tc_supported(dvs, dt)) {
+        dqs.seeds = la::seeds_of(workspace);
+        return la::tc_backward(dqs, dks, dvs, workspace, st) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
     }
+    for (const la::decay::Args* sum : {&dqs, &dks, &dvs})
+        if (la::run_cuda_cores(*sum, dt, workspace, st) != cudaSuccess) return LA_ERR_CUDA;
     return LA_OK;
 }
 

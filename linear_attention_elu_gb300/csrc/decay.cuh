@@ -30,6 +30,7 @@ struct Args {
     float* seeds;               // [B H, nseg, Da, Dc]: end states, then the segments' start states
     int B, H, N, Da, Dc, rev;
     int nseg, seg_len;          // segments and their tokens (a multiple of the chunk)
+    int seeds_t;                // seeds are [.., Dc, Da]: those of the sum with b and c exchanged
     float scale;
 };
 
@@ -65,14 +66,24 @@ __device__ __forceinline__ int tokens_of(const Args& a, int b) {
     return a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
 }
 
-// Chains the segments' end states into their start states, in place (csrc/decay.cu).
-// chunk: the tensor-core path's states of reversed sums stand at whole chunks.
-cudaError_t launch_chain(const Args& a, int chunk, cudaStream_t st);
+// Chains the segments' end states of one or two sums into their start states, in place
+// (csrc/decay.cu). chunk: the tensor-core path's states of reversed sums stand at whole chunks.
+cudaError_t launch_chain(const Args* sums, int count, int chunk, cudaStream_t st);
 
-// Tensor-core path (csrc/decay_tc.cu).
+// The cut of a sequence into `nseg` segments or fewer of whole chunks.
+inline void cut(Args* a, int nseg, int chunk) {
+    const int chunks = (a->N + chunk - 1) / chunk, per = (chunks + nseg - 1) / nseg;
+    a->nseg = (chunks + per - 1) / per;
+    a->seg_len = per * chunk;
+}
+
+// Tensor-core path (csrc/decay_tc.cu): whether a sum can take it; one sum; the three sums of
+// the backward pass, dq, dk, dv in this order, and the floats of seeds of either.
 bool tc_supported(const Args& a, la_dtype dt);
-int tc_segments(int64_t BH, int N, int Da, int Dc);
+size_t tc_seeds(int64_t BH, int N, int Dk, int Dv, bool backward);
+int tc_launches(int64_t BH, int N, int Dk, int Dv, bool backward);
 cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st);
+cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t st);
 
 }  // namespace decay
 }  // namespace la

@@ -99,6 +99,8 @@ static_assert(SumSmem<2, 2, 2>::kBytes <= 227 * 1024 && SumSmem<1, 2, 3>::kBytes
 struct Geo {
     int cps;                    // chunks per segment
     uint8_t ah, ab, bh, bb, ch, cb;
+    uint8_t late;               // the launch before it is not waited for until this one's end: it
+                                // started after that launch had seen the chained seeds
 };
 
 __device__ __forceinline__ uint64_t pk2(float lo, float hi) {
@@ -165,10 +167,10 @@ struct Place {
     int b, h, col0, seg, n, nch, v0, nc;
     template <bool kRev> __device__ int chunk(int i) const { return kRev ? nch - 1 - v0 - i : v0 + i; }
 };
-__device__ __forceinline__ Place place(const Args& a, const Geo& geo, int units) {
+__device__ __forceinline__ Place place(const Args& a, const Geo& geo, int units, int bh) {
     Place p;
-    p.b = blockIdx.z / a.H;
-    p.h = blockIdx.z - p.b * a.H;
+    p.b = bh / a.H;
+    p.h = bh - p.b * a.H;
     p.col0 = 64 * units * blockIdx.x;
     p.seg = blockIdx.y;
     p.n = tokens_of(a, p.b);
@@ -196,10 +198,10 @@ __device__ __forceinline__ void next_term(uint64_t (&rest)[4], uint32_t (&t)[4])
     }
 }
 
-// Columns 32 g .. of row `row` of a C tile: notes the values that are not finite, and clears
+// Columns c0 .. c1 of row `row` of a C tile: notes the values that are not finite, and clears
 // them: (3) would add 0 times them to the tokens before them. (4) has them from the terms.
-__device__ __noinline__ void take_out(uint8_t* tile, int row, int g, int token, int* any, int* first) {
-    for (int c = 32 * g; c < 32 * g + 32; ++c) {
+__device__ __noinline__ void take_out(uint8_t* tile, int row, int c0, int c1, int token, int* any, int* first) {
+    for (int c = c0; c < c1; ++c) {
         unsigned short* v = reinterpret_cast<unsigned short*>(tile + row * 128 + (((c >> 3) ^ (row & 7)) << 4)) + (c & 7);
         if ((*v & 0x7F80u) != 0x7F80u) continue;
         *v = 0;
@@ -220,25 +222,26 @@ __device__ __noinline__ uint4 put_nan(const int* firsts, int token, uint4 o) {
 }
 
 // ------------------------------------------------------------ steps of a working warp
-// Row `row` = 32 q + lane of the tiles; half g of a unit's 64 columns.
+// Row `row` = 32 q + lane of the tiles, columns from the 16-byte piece j0 on.
 
-// A state row (32 fp32 columns) to the bf16 tile that (2) reads.
-__device__ __forceinline__ void write_state(uint8_t* tile, const float (&st)[32], int row, int g) {
+// A state row (fp32 columns) to the bf16 tile that (2) reads.
+template <int kCols>
+__device__ __forceinline__ void write_state(uint8_t* tile, const float (&st)[kCols], int row, int j0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(tile + row * 128 + (((4 * g + j) ^ (row & 7)) << 4)) =
+    for (int j = 0; j < kCols / 8; ++j)
+        *reinterpret_cast<uint4*>(tile + row * 128 + (((j0 + j) ^ (row & 7)) << 4)) =
             make_uint4(pack_bf16(st[8 * j], st[8 * j + 1]), pack_bf16(st[8 * j + 2], st[8 * j + 3]),
                        pack_bf16(st[8 * j + 4], st[8 * j + 5]), pack_bf16(st[8 * j + 6], st[8 * j + 7]));
 }
 
 // w C of a row: its terms, kTile apart. Returns whether all values are finite.
-template <int kTerms>
-__device__ __forceinline__ bool write_weighted(const uint8_t* c_tile, uint8_t* terms, float w, int row, int g) {
+template <int kTerms, int kPieces = 4>
+__device__ __forceinline__ bool write_weighted(const uint8_t* c_tile, uint8_t* terms, float w, int row, int j0) {
     const uint64_t w2 = pk2(w, w);
     uint64_t bad = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t at = row * 128 + (((4 * g + j) ^ (row & 7)) << 4);
+    for (int j = 0; j < kPieces; ++j) {
+        const uint32_t at = row * 128 + (((j0 + j) ^ (row & 7)) << 4);
         const uint4 c = *reinterpret_cast<const uint4*>(c_tile + at);
         uint32_t t[4];
         uint64_t rest[4];
@@ -257,10 +260,10 @@ __device__ __forceinline__ bool write_weighted(const uint8_t* c_tile, uint8_t* t
     return b0 == 0.f && b1 == 0.f;
 }
 
-// Rows past a sequence's end may hold anything: four pieces of one row set to 0.
-__device__ __forceinline__ void clear_pieces(uint8_t* tile, int row, int g) {
+// Rows past a sequence's end may hold anything: pieces of one row set to 0.
+template <int kPieces = 4> __device__ __forceinline__ void clear_pieces(uint8_t* tile, int row, int j0) {
 #pragma unroll
-    for (int j = 4 * g; j < 4 * g + 4; ++j)
+    for (int j = j0; j < j0 + kPieces; ++j)
         *reinterpret_cast<uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
 }
 
@@ -284,11 +287,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 // what it spills does not fit the little L1 that two CTAs leave (backwards in time the call
 // took 1.8 times as long).
 template <bool kRev>
-__device__ __forceinline__ void scores_to_p(uint32_t tm, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
+__device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
     const int lane = threadIdx.x & 31;
     const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane * rf.diag;
     const uint64_t r2 = pk2(r, r);
-    const uint32_t at = tm + kTmP + 32 * blk;
+    const uint32_t at = tm_p + 32 * blk;
 #pragma unroll 1
     for (int half = 0; half < 32; half += 16) {
         uint32_t v[16], p[8];
@@ -332,10 +335,10 @@ __device__ __forceinline__ void scores_to_p(uint32_t tm, int blk, int bm, int qm
 }
 
 // The chunk's sums join the state: st = f st + sums.
-__device__ __forceinline__ void join_state(uint32_t tm, const Factor& f, float (&st)[32]) {
+template <int kCols> __device__ __forceinline__ void join_state(uint32_t tm, const Factor& f, float (&st)[kCols]) {
     const uint64_t hi = pk2(f.hi, f.hi), lo = pk2(f.lo, f.lo);
 #pragma unroll
-    for (int half = 0; half < 32; half += 16) {
+    for (int half = 0; half < kCols; half += 16) {
         uint32_t v[16];
         tmem_ld16(tm + half, v);
         tmem_ld_wait();
@@ -387,12 +390,12 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, geo, kU);
+    const Place pl = place(a, geo, kU, blockIdx.z);
     const bool returns = a.S_out && pl.seg == a.nseg - 1;
-    if (pl.nc == 0 && !returns) {
-        pdl_wait();                            // a dependent launch never ends before what it follows
-        return;
-    }
+    // The seeds, where there are segments. A dependent launch never ends before what it follows.
+    if (!geo.late || (pl.nc == 0 && !returns)) pdl_wait();
+    pdl_launch_dependents();
+    if (pl.nc == 0 && !returns) return;
     if ((smem_u32(base) & 1023) != 0) {        // the tiles' swizzle needs it; no static shared memory, so it holds
         if (tid == 0) set_status(hdr, LA_ERR_CUDA);
         return;
@@ -414,7 +417,6 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    pdl_wait();                                // the seeds, where there are segments
     const uint32_t tmem = m.tmem_slot;
     const uint32_t max_spin = hdr->max_spin;
     const bool hold = hdr->hold_item != 0;     // test hook: loads never issued
@@ -537,7 +539,14 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (has_state && from && row < a.Da && c0 + k < a.Dc) v = *reinterpret_cast<const float4*>(from + (int64_t)row * a.Dc + c0 + k);
+            if (has_state && from && row < a.Da && c0 + k < a.Dc) {
+                if (a.seeds_t) {
+                    const float* t = from + (int64_t)(c0 + k) * a.Da + row;
+                    v = make_float4(t[0], t[a.Da], t[2 * a.Da], t[3 * a.Da]);
+                } else {
+                    v = *reinterpret_cast<const float4*>(from + (int64_t)row * a.Dc + c0 + k);
+                }
+            }
             st[k] = v.x, st[k + 1] = v.y, st[k + 2] = v.z, st[k + 3] = v.w;
         }
         const float read = a.scale * pow2((float)(im + 1) * l2);   // weight of the state in this row's output
@@ -546,7 +555,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             const int t0 = pl.chunk<kRev>(i) * kC, mt = min(kC, pl.n - t0), s = i % L::kStages, ph = (i / L::kStages) & 1;
             uint8_t* ct = ctile(i, u);
             // ---------------------------------------------------- state to bf16, w C
-            if (has_state) write_state(s_tile, st, row, g);
+            if (has_state) write_state(s_tile, st, row, 4 * g);
             if (!(ok = warp_wait(&m.c_full[s], ph, max_spin))) break;
             // Rows past the sequence's end are cleared in C, and in B for (4). (Past N the loads
             // filled zeros.) (1) may read such rows of B, whose scores take no part.
@@ -554,12 +563,12 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             if (ragged) {
                 if (!(ok = warp_wait(&m.b_full, i & 1, max_spin))) break;
                 if (row >= mt) {
-                    clear_pieces(ct, row, g);
-                    for (int k = 0; k < kT; ++k) clear_pieces(base + L::kB + k * kTile, row, g);
+                    clear_pieces(ct, row, 4 * g);
+                    for (int k = 0; k < kT; ++k) clear_pieces(base + L::kB + k * kTile, row, 4 * g);
                 }
             }
             const float w = pow2((float)(kRev ? row : max(mt - 1 - row, 0)) * l2);
-            if (!write_weighted<kTerms>(ct, terms, w, row, g)) take_out(ct, row, g, i * kC + im, &m.any, m.first + 64 * u);
+            if (!write_weighted<kTerms>(ct, terms, w, row, 4 * g)) take_out(ct, row, 32 * g, 32 * g + 32, i * kC + im, &m.any, m.first + 64 * u);
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
@@ -568,7 +577,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             tc_fence_after();
 #pragma unroll 1
             for (int bm = g4; bm < 4; bm += 2 * kU)
-                scores_to_p<kRev>(tm, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
+                scores_to_p<kRev>(tm + kTmP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
@@ -612,17 +621,24 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                         make_float4(st[k], st[k + 1], st[k + 2], st[k + 3]);
     }
     if (!ok) report_timeout(hdr);
+    if (geo.late) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == kWarps) tmem_dealloc(tmem, kCols);
 }
 
-// First pass: a segment's end state from zero (every segment but the last).
-template <int kT, int kU, int kTerms, bool kRev>
+// First pass, of one sum or two: a segment's end state from zero (every segment but the last).
+template <int kT, int kU, int kTerms>
 __global__ void __launch_bounds__(32 * (kU * kWork + 1), SumSmem<kT, kU, kTerms>::kPerSm)
-decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap cmap,
-                  const __grid_constant__ Args a, const __grid_constant__ Geo geo, WsHeader* hdr) {
+decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_constant__ CUtensorMap cmap0,
+                  const __grid_constant__ CUtensorMap bmap1, const __grid_constant__ CUtensorMap cmap1,
+                  const __grid_constant__ Args a0, const __grid_constant__ Geo geo0, const __grid_constant__ Args a1,
+                  const __grid_constant__ Geo geo1, WsHeader* hdr) {
+    const bool second = (int)blockIdx.z >= a0.B * a0.H;
+    const Args& a = second ? a1 : a0;
+    const Geo& geo = second ? geo1 : geo0;
+    const CUtensorMap &bmap = second ? bmap1 : bmap0, &cmap = second ? cmap1 : cmap0;
     using L = SumSmem<kT, kU, kTerms>;
     constexpr int kWarps = kU * kWork;
     extern __shared__ __align__(1024) uint8_t base[];
@@ -630,9 +646,11 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
     auto btile = [&](int i) { return base + L::kB + (i % L::kStages) * kT * kTile; };
     auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, geo, kU);
+    const Place pl = place(a, geo, kU, blockIdx.z - (second ? a0.B * a0.H : 0));
+    const bool rev = a.rev != 0;
+    auto chunk = [&](int i) { return rev ? pl.chunk<true>(i) : pl.chunk<false>(i); };
     pdl_launch_dependents();
-    if (pl.nc == 0) return;                    // the chaining leaves such segments out
+    if (pl.nc == 0 || pl.seg >= a.nseg - 1) return;    // the chaining leaves such segments out
     if ((smem_u32(base) & 1023) != 0) {
         if (tid == 0) set_status(hdr, LA_ERR_CUDA);
         return;
@@ -663,7 +681,7 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
             int n = 0;
             auto load = [&]() {
                 if (hold) return;
-                const int t = pl.chunk<kRev>(n) * kC;
+                const int t = chunk(n) * kC;
                 uint64_t* bar = &m.c_full[n % L::kStages];
                 mbar_arrive_expect_tx(bar, (kT + kU) * kTile);
 #pragma unroll
@@ -698,13 +716,13 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
 #pragma unroll
         for (int k = 0; k < 32; ++k) st[k] = 0.f;
         for (int i = 0; i < pl.nc; ++i) {
-            const int mt = min(kC, pl.n - pl.chunk<kRev>(i) * kC);
+            const int mt = min(kC, pl.n - chunk(i) * kC);
             if (!(ok = warp_wait(&m.c_full[i % L::kStages], (i / L::kStages) & 1, max_spin))) break;
             if (mt < kC && pl.n < a.N && row >= mt) {
-                clear_pieces(ctile(i, u), row, g);
-                for (int k = 0; k < kT; ++k) clear_pieces(btile(i) + k * kTile, row, g);
+                clear_pieces(ctile(i, u), row, 4 * g);
+                for (int k = 0; k < kT; ++k) clear_pieces(btile(i) + k * kTile, row, 4 * g);
             }
-            write_weighted<kTerms>(ctile(i, u), terms, pow2((float)(kRev ? row : max(mt - 1 - row, 0)) * l2), row, g);
+            write_weighted<kTerms>(ctile(i, u), terms, pow2((float)(rev ? row : max(mt - 1 - row, 0)) * l2), row, 4 * g);
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
@@ -712,7 +730,7 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
             tc_fence_after();
             if (has_state)
                 join_state(tmem + ((uint32_t)(32 * q) << 16) + 64 * u + 32 * g,
-                           kRev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
+                           rev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
         }
         const int c0 = pl.col0 + 64 * u + 32 * g;
         float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc + (int64_t)row * a.Dc + c0;
@@ -726,6 +744,233 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constan
     __syncthreads();
     tc_fence_after();
     if (warp == kWarps) tmem_dealloc(tmem, 64 * kU);
+}
+
+// dk and dv of one head in one pass backwards in time (Dk, Dv <= 64). The two sums take the
+// same four tiles and the same state R_t = q_t dout_t^T + f R_{t+1}:
+//   unit 0, dv: A = K, B = Q, C = dout, state R;   unit 1, dk: A = V, B = dout, C = Q, state R^T
+// so (4) and the state are unit 0's alone, and unit 1 reads the same bf16 tile transposed.
+// Sixteen working warps, one CTA per SM; every tile double buffered. For the steps that the
+// units share a warp owns 16 columns.
+enum { kTileK, kTileV, kTileQ, kTileG };
+struct KvSmem {
+    static constexpr uint32_t kW = 8 * kTile, kS = kW + 2 * kTile, kMisc = kS + kTile / 2;
+    static constexpr int kBytes = kMisc + kMiscBytes;
+};
+static_assert(KvSmem::kBytes <= 227 * 1024, "shared memory");
+constexpr uint32_t kKvX = 256, kKvO2 = 320;        // TMEM: scores of unit u at 128 u; + 128 u
+
+struct KvMaps {
+    CUtensorMap in[4], dk, dv;
+};
+
+__global__ void __launch_bounds__(32 * (2 * kWork + 1), 1)
+decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Args a, const __grid_constant__ Tensor dk,
+                const __grid_constant__ Geo geo, const __grid_constant__ Geo vgeo, WsHeader* hdr) {
+    using L = KvSmem;
+    constexpr int kWarps = 2 * kWork;
+    extern __shared__ __align__(1024) uint8_t base[];
+    Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
+    auto tile = [&](int i, int k) { return base + ((i & 1) * 4 + k) * kTile; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Place pl = place(a, geo, 1, blockIdx.z);
+    if (pl.nc == 0) {
+        pdl_wait();
+        return;
+    }
+    if ((smem_u32(base) & 1023) != 0) {
+        if (tid == 0) set_status(hdr, LA_ERR_CUDA);
+        return;
+    }
+    if (tid == 0) {
+        for (uint64_t* bar : {&m.c_full[0], &m.c_full[1], &m.p_full, &m.s_full, &m.o_full, &m.drain}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&m.prep, &m.pt, &m.staged}) mbar_init(bar, kWarps);
+        fence_mbar_init();
+        m.any = kNone;
+    }
+    if (tid < 128) m.first[tid] = kNone;
+    const float l = a.decay[pl.h], l2 = log2_decay(l);
+    init_tables<true>(m, l2);
+    if (warp == kWarps) {
+        tmem_alloc(&m.tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m.tmem_slot;
+    const uint32_t max_spin = hdr->max_spin;
+    const bool hold = hdr->hold_item != 0;
+    bool ok = true;
+
+    if (warp == kWarps) {
+        if (lane == 0) {
+            const uint32_t base_a = smem_u32(base);
+            const uint64_t km = kmajor_desc(base_a), rows = rows_desc(base_a);
+            const uint64_t sr = rows_desc(base_a + L::kS), sk = kmajor_desc(base_a + L::kS), wr = rows_desc(base_a + L::kW);
+            constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true), id_t = idesc_bf16_f32(128, 64, false, false);
+            int n = 0;
+            auto load = [&]() {
+                if (hold) return;
+                const int t = pl.chunk<true>(n) * kC;
+                uint64_t* bar = &m.c_full[n & 1];
+                mbar_arrive_expect_tx(bar, 4 * kTile);
+                tma_load_4d(tile(n, kTileK), &maps.in[kTileK], bar, 0, geo.ah * pl.h, t, geo.ab * pl.b);
+                tma_load_4d(tile(n, kTileQ), &maps.in[kTileQ], bar, 0, geo.bh * pl.h, t, geo.bb * pl.b);
+                tma_load_4d(tile(n, kTileV), &maps.in[kTileV], bar, 0, vgeo.ah * pl.h, t, vgeo.ab * pl.b);
+                tma_load_4d(tile(n, kTileG), &maps.in[kTileG], bar, 0, geo.ch * pl.h, t, geo.cb * pl.b);
+                ++n;
+            };
+            auto at = [&](uint64_t d, int i, int k) { return step_desc(d, ((i & 1) * 4 + k) * kTile); };
+            auto scores = [&](int i) -> bool {                                                          // (1)
+                if (!mbar_wait(&m.c_full[i & 1], (i >> 1) & 1, max_spin)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + 128 * u, kmajor_step(at(km, i, u), k), kmajor_step(at(km, i, 2 + u), k), id_sc, k > 0);
+                mma_commit(&m.p_full);
+                return true;
+            };
+            auto put = [&](int i) -> bool {
+                if (!mbar_wait(&m.staged, i & 1, max_spin)) return false;
+                const int t = pl.chunk<true>(i) * kC;
+                if (t + kC <= pl.n || pl.n == a.N) {
+                    tma_store_4d(&maps.dv, tile(i, kTileG), 0, pl.h, t, pl.b);
+                    tma_store_4d(&maps.dk, tile(i, kTileQ), 0, pl.h, t, pl.b);
+                    tma_store_commit();
+                }
+                return true;
+            };
+            load();
+            if (pl.nc > 1) load();
+            ok = scores(0);
+            for (int i = 0; i < pl.nc && ok; ++i) {
+                if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {                                                           // (2)
+                    mma_bf16(tmem + kKvO2, kmajor_step(at(km, i, kTileK), k), step_desc(sr, k * 2048), id_o, k > 0);
+                    mma_bf16(tmem + kKvO2 + 128, kmajor_step(at(km, i, kTileV), k), kmajor_step(sk, k), id_t, k > 0);
+                }
+                issue_state<2>(tmem + kKvX, at(rows, i, kTileQ), wr);                                   // (4)
+                mma_commit(&m.s_full);
+                if (i > 0 && i + 1 < pl.nc) {          // the next chunk, once the output before this one has left its place
+                    tma_store_wait_read<0>();
+                    load();
+                }
+                if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)                                                   // (3)
+                        mma_bf16_ts(tmem + kKvX + 128 * u, tmem + 128 * u + 32 * (k >> 1) + 8 * (k & 1),
+                                    step_desc(at(rows, i, u ? kTileQ : kTileG), k * 2048), id_o, k > 0);
+                mma_commit(&m.o_full);
+                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
+                if (i + 1 < pl.nc && !(ok = scores(i + 1))) break;
+                ok = put(i);
+            }
+            tma_store_wait_all<0>();
+            for (int j = max(n - 2, 0); j < n; ++j) mbar_wait(&m.c_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
+            mma_commit(&m.drain);
+            ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, g4 = warp >> 2, u = g4 >> 1, g = g4 & 1, row = 32 * q + lane, im = 127 - row;
+        const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16), tmu = tm + kKvX + 128 * u + 32 * g;
+        const bool has_state = q < 2;
+        const RowFactors rf = row_factors(l2, im);
+        // State row `row`, columns 16 g4 ..
+        float st[16];
+        const float* from = a.nseg > 1 ? a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc : nullptr;
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (has_state && from && row < a.Da && 16 * g4 + k < a.Dc)
+                v = *reinterpret_cast<const float4*>(from + (int64_t)row * a.Dc + 16 * g4 + k);
+            st[k] = v.x, st[k + 1] = v.y, st[k + 2] = v.z, st[k + 3] = v.w;
+        }
+        const float read = a.scale * pow2((float)(im + 1) * l2), w = pow2((float)row * l2);
+        const Factor whole = factor(kC * log_decay(l));
+        const Tensor& out = u ? dk : a.o;
+        const int width = u ? a.Da : a.Dc;
+        for (int i = 0; i < pl.nc; ++i) {
+            const int t0 = pl.chunk<true>(i) * kC, mt = min(kC, pl.n - t0);
+            uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ), *ct = u ? qt : gt;
+            // ---------------------------------------------------- state to bf16, w dout
+            if (has_state) write_state(base + L::kS, st, row, 2 * g4);
+            if (!(ok = warp_wait(&m.c_full[i & 1], (i >> 1) & 1, max_spin))) break;
+            const bool ragged = mt < kC && pl.n < a.N;
+            if (ragged && row >= mt) {
+                clear_pieces<2>(gt, row, 2 * g4);
+                clear_pieces<2>(qt, row, 2 * g4);
+            }
+            const bool fine_g = write_weighted<2, 2>(gt, base + L::kW, w, row, 2 * g4);
+            bool fine_q = true;
+#pragma unroll
+            for (int j = 2 * g4; j < 2 * g4 + 2; ++j) {
+                const uint4 x = *reinterpret_cast<const uint4*>(qt + row * 128 + ((j ^ (row & 7)) << 4));
+                for (uint32_t v : {x.x, x.y, x.z, x.w}) fine_q = fine_q && (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            warp_arrive(&m.prep);
+            // ---------------------------------------------------- scores to P
+            if (!(ok = warp_wait(&m.p_full, i & 1, max_spin))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int bm = g; bm < 4; bm += 2) scores_to_p<true>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
+            // ---------------------------------------------------- state
+            if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
+            tc_fence_after();
+            if (has_state) join_state(tm + kKvX + 16 * g4, whole, st);
+            // (1) and (4) have read the tiles as they came; (3) must not read values that are not finite.
+            if (!fine_g) take_out(gt, row, 16 * g4, 16 * g4 + 16, i * kC + im, &m.any, m.first);
+            if (!fine_q) take_out(qt, row, 16 * g4, 16 * g4 + 16, i * kC + im, &m.any, m.first + 64);
+            fence_proxy_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&m.pt);
+            // ---------------------------------------------------- output
+            if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
+            tc_fence_after();
+            const bool spoiled = *const_cast<volatile int*>(&m.any) != kNone;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint4 x, y;
+                join_output(tmu + 16 * k, tmu + 64 + 16 * k, a.scale, read, &x, &y);
+                if (spoiled) {
+                    const int* first = m.first + 64 * u + 32 * g + 16 * k;
+                    x = put_nan(first, i * kC + im, x);
+                    y = put_nan(first + 8, i * kC + im, y);
+                }
+                if (!ragged) {
+                    *reinterpret_cast<uint4*>(ct + row * 128 + (((4 * g + 2 * k) ^ (row & 7)) << 4)) = x;
+                    *reinterpret_cast<uint4*>(ct + row * 128 + (((4 * g + 2 * k + 1) ^ (row & 7)) << 4)) = y;
+                } else if (row < mt) {
+                    const int c = 32 * g + 16 * k;
+                    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)) + pl.b * out.bs + pl.h * out.hs +
+                                        (int64_t)(t0 + row) * out.ts + c;
+                    if (c < width) *reinterpret_cast<uint4*>(to) = x;
+                    if (c + 8 < width) *reinterpret_cast<uint4*>(to + 8) = y;
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            warp_arrive(&m.staged);
+        }
+    }
+    if (!ok) report_timeout(hdr);
+    pdl_wait();                                // as `late` of decay_tc_kernel
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarps) tmem_dealloc(tmem, 512);
 }
 
 // Rows [B, H, N, D] of bf16 as a 4-D map (D, H, N, B) with boxes of 64 values x 128 tokens;
@@ -746,34 +991,77 @@ bool encode_rows(CUtensorMap* map, const Tensor& t, int D, int B, int H, int N, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Maps {
-    CUtensorMap a, b, c, o;
+// One sum with its tensor maps.
+struct Sum {
+    Args a;
+    Geo geo;
+    CUtensorMap am, bm, cm, om;
+    bool encode() {
+        geo = {};
+        geo.cps = a.seg_len / kC;
+        return encode_rows(&am, a.a, a.Da, a.B, a.H, a.N, &geo.ah, &geo.ab) &&
+               encode_rows(&bm, a.b, a.Da, a.B, a.H, a.N, &geo.bh, &geo.bb) &&
+               encode_rows(&cm, a.c, a.Dc, a.B, a.H, a.N, &geo.ch, &geo.cb) &&
+               encode_rows(&om, a.o, a.Dc, a.B, a.H, a.N, nullptr, nullptr);
+    }
+    unsigned heads() const { return (unsigned)(a.B * a.H); }
 };
 
-template <int kT, int kU, int kTerms, bool kRev>
-cudaError_t launch(const Maps& maps, const Args& a, const Geo& geo, WsHeader* hdr, cudaStream_t st) {
-    static std::atomic<int> optin[2][kMaxDevices];
-    constexpr int threads = 32 * (kU * kWork + 1);
-    const unsigned blocks = (a.Dc + 64 * kU - 1) / (64 * kU), BH = (unsigned)(a.B * a.H);
-    cudaError_t e;
-    if (a.nseg > 1) {
-        constexpr int bytes = SumSmem<kT, kU, kTerms>::kBytes;
-        if ((e = ensure_smem_optin(decay_sums_kernel<kT, kU, kTerms, kRev>, bytes, optin[0])) != cudaSuccess) return e;
-        decay_sums_kernel<kT, kU, kTerms, kRev><<<dim3(blocks, a.nseg - 1, BH), threads, bytes, st>>>(maps.b, maps.c, a, geo, hdr);
-        if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
-        if ((e = launch_chain(a, kC, st)) != cudaSuccess) return e;
-    }
-    constexpr int bytes = Smem<kT, kU, kTerms>::kBytes;
-    if ((e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev>, bytes, optin[1])) != cudaSuccess) return e;
-    return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev>, dim3(blocks, a.nseg, BH), threads, bytes, st, a.nseg > 1,
-                              maps.a, maps.b, maps.c, maps.o, a, geo, hdr);
+template <int kT, int kU, int kTerms>
+cudaError_t launch_sums(const Sum* s, int count, WsHeader* hdr, cudaStream_t st) {
+    static std::atomic<int> optin[kMaxDevices];
+    constexpr int bytes = SumSmem<kT, kU, kTerms>::kBytes;
+    const cudaError_t e = ensure_smem_optin(decay_sums_kernel<kT, kU, kTerms>, bytes, optin);
+    if (e != cudaSuccess) return e;
+    const Sum &x = s[0], &y = s[count - 1];
+    const int nseg = x.a.nseg > y.a.nseg ? x.a.nseg : y.a.nseg;
+    const dim3 grid((x.a.Dc + 64 * kU - 1) / (64 * kU), nseg - 1, x.heads() * count);
+    decay_sums_kernel<kT, kU, kTerms><<<grid, 32 * (kU * kWork + 1), bytes, st>>>(x.bm, x.cm, y.bm, y.cm, x.a, x.geo, y.a, y.geo, hdr);
+    return cudaPeekAtLastError();
 }
 
-template <int kT, int kU>
-cudaError_t launch_form(const Maps& maps, const Args& a, const Geo& geo, WsHeader* hdr, cudaStream_t st) {
-    if (a.rev) return launch<kT, kU, 2, true>(maps, a, geo, hdr, st);
-    return a.S_out ? launch<kT, kU, 3, false>(maps, a, geo, hdr, st) : launch<kT, kU, 2, false>(maps, a, geo, hdr, st);
+template <int kT, int kU, int kTerms, bool kRev>
+cudaError_t launch_main(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
+    static std::atomic<int> optin[kMaxDevices];
+    constexpr int bytes = Smem<kT, kU, kTerms>::kBytes;
+    const cudaError_t e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev>, bytes, optin);
+    if (e != cudaSuccess) return e;
+    return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev>, dim3((s.a.Dc + 64 * kU - 1) / (64 * kU), s.a.nseg, s.heads()),
+                              32 * (kU * kWork + 1), bytes, st, dependent, s.am, s.bm, s.cm, s.om, s.a, s.geo, hdr);
 }
+
+// By widths: one or two 64-row tiles of the state, one or two column blocks.
+template <int kTerms> cudaError_t sums_of(const Sum* s, int count, WsHeader* hdr, cudaStream_t st) {
+    if (s->a.Da <= 64) return s->a.Dc <= 64 ? launch_sums<1, 1, kTerms>(s, count, hdr, st) : launch_sums<1, 2, kTerms>(s, count, hdr, st);
+    return s->a.Dc <= 64 ? launch_sums<2, 1, kTerms>(s, count, hdr, st) : launch_sums<2, 2, kTerms>(s, count, hdr, st);
+}
+template <int kTerms, bool kRev> cudaError_t main_of(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
+    if (s.a.Da <= 64)
+        return s.a.Dc <= 64 ? launch_main<1, 1, kTerms, kRev>(s, dependent, hdr, st) : launch_main<1, 2, kTerms, kRev>(s, dependent, hdr, st);
+    return s.a.Dc <= 64 ? launch_main<2, 1, kTerms, kRev>(s, dependent, hdr, st) : launch_main<2, 2, kTerms, kRev>(s, dependent, hdr, st);
+}
+
+bool narrow(int Dk, int Dv) { return Dk <= 64 && Dv <= 64; }
+
+// Segments of a pass with `per_sm` CTAs per SM. CTAs run in waves, so the cut is the one
+// whose waves times chunks is least; in chunks: starting and ending a CTA 1, the first pass
+// 0.4 of the main pass, and with segments two further launches 2.
+int segments(int64_t BH, int N, int per_sm) {
+    const int chunks = (N + kC - 1) / kC;
+    const int64_t slots = (int64_t)per_sm * sm_count();
+    int best = 1;
+    double least = 1e30;
+    for (int n = 1; n <= 64 && n <= chunks; ++n) {
+        const int per = (chunks + n - 1) / n;
+        if ((chunks + per - 1) / per != n) continue;       // the same split with empty segments
+        const double waves = (double)((BH * n + slots - 1) / slots);
+        const double cost = waves * (per + 1.0) + (n > 1 ? 0.4 * waves * per + 2.0 : 0.0);
+        if (cost < least) least = cost, best = n;
+    }
+    return best;
+}
+int forward_segments(int64_t BH, int N, int Dk, int Dv) { return segments(BH, N, narrow(Dk, Dv) ? 2 : 1); }
+int reverse_segments(int64_t BH, int N) { return segments(BH, N, 1); }   // of dk and dv, which share their seeds
 
 }  // namespace
 
@@ -792,27 +1080,66 @@ bool tc_supported(const Args& a, la_dtype dt) {
     return rows(a.a, true) && rows(a.b, true) && rows(a.c, true) && rows(a.o, false);
 }
 
-int tc_segments(int64_t BH, int N, int Da, int Dc) {
-    const int64_t ctas = BH, slots = (Da <= 64 && Dc <= 64 ? 2 : 1) * (int64_t)sm_count();
-    const int64_t most = (N + kC - 1) / kC / 4;
-    int64_t n = ctas > 0 ? slots / ctas : 1;
-    n = n < most ? n : most;
-    n = n < 64 ? n : 64;
-    return n < 2 ? 1 : (int)n;
+size_t tc_seeds(int64_t BH, int N, int Dk, int Dv, bool backward) {
+    const int f = forward_segments(BH, N, Dk, Dv), r = backward ? reverse_segments(BH, N) : 1;
+    return (size_t)BH * Dk * Dv * ((f > 1 ? f : 0) + (r > 1 ? r : 0));
+}
+
+int tc_launches(int64_t BH, int N, int Dk, int Dv, bool backward) {
+    const bool f = forward_segments(BH, N, Dk, Dv) > 1;
+    if (!backward) return f ? 3 : 1;
+    const bool r = reverse_segments(BH, N) > 1, together = (Dk <= 64) == (Dv <= 64);
+    return (narrow(Dk, Dv) ? 2 : 3) + (f || r ? 1 + (f && r && !together ? 2 : 1) : 0);
 }
 
 cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
-    Geo geo = {};
-    geo.cps = a.seg_len / kC;
-    Maps maps;
-    if (!encode_rows(&maps.a, a.a, a.Da, a.B, a.H, a.N, &geo.ah, &geo.ab) ||
-        !encode_rows(&maps.b, a.b, a.Da, a.B, a.H, a.N, &geo.bh, &geo.bb) ||
-        !encode_rows(&maps.c, a.c, a.Dc, a.B, a.H, a.N, &geo.ch, &geo.cb) ||
-        !encode_rows(&maps.o, a.o, a.Dc, a.B, a.H, a.N, nullptr, nullptr))
-        return cudaErrorInvalidValue;
+    cut(&a, forward_segments((int64_t)a.B * a.H, a.N, a.Da, a.Dc), kC);
+    Sum s = {a};
+    if (!s.encode()) return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
-    if (a.Da <= 64) return a.Dc <= 64 ? launch_form<1, 1>(maps, a, geo, hdr, st) : launch_form<1, 2>(maps, a, geo, hdr, st);
-    return a.Dc <= 64 ? launch_form<2, 1>(maps, a, geo, hdr, st) : launch_form<2, 2>(maps, a, geo, hdr, st);
+    cudaError_t e;
+    if (a.nseg > 1) {
+        if ((e = a.S_out ? sums_of<3>(&s, 1, hdr, st) : sums_of<2>(&s, 1, hdr, st)) != cudaSuccess) return e;
+        if ((e = launch_chain(&a, 1, kC, st)) != cudaSuccess) return e;
+    }
+    return a.S_out ? main_of<3, false>(s, a.nseg > 1, hdr, st) : main_of<2, false>(s, a.nseg > 1, hdr, st);
+}
+
+// First passes of S (for dq) and of R (for dk and dv), one chaining, then dq and dk and dv: the
+// last two in one pass where the heads are narrow enough for its tiles.
+cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t st) {
+    const int64_t BH = (int64_t)dq.B * dq.H;
+    cut(&dq, forward_segments(BH, dq.N, dv.Da, dv.Dc), kC);
+    cut(&dv, reverse_segments(BH, dv.N), kC);
+    dv.seeds = dq.seeds + (dq.nseg > 1 ? (size_t)BH * dq.nseg * dq.Da * dq.Dc : 0);
+    dk.seeds = dv.seeds, dk.nseg = dv.nseg, dk.seg_len = dv.seg_len, dk.seeds_t = 1;
+    Sum s[3] = {{dq}, {dv}, {dk}};
+    for (Sum& x : s)
+        if (!x.encode()) return cudaErrorInvalidValue;
+    WsHeader* hdr = static_cast<WsHeader*>(ws_header);
+    cudaError_t e;
+    const bool f = dq.nseg > 1, r = dv.nseg > 1;
+    if (f || r) {
+        if (f && r && (dq.Da <= 64) == (dq.Dc <= 64)) {
+            if ((e = sums_of<2>(s, 2, hdr, st)) != cudaSuccess) return e;
+        } else {
+            if (f && (e = sums_of<2>(s, 1, hdr, st)) != cudaSuccess) return e;
+            if (r && (e = sums_of<2>(s + 1, 1, hdr, st)) != cudaSuccess) return e;
+        }
+        const Args chained[2] = {f ? dq : dv, dv};
+        if ((e = launch_chain(chained, f && r ? 2 : 1, kC, st)) != cudaSuccess) return e;
+    }
+    if ((e = main_of<2, false>(s[0], f || r, hdr, st)) != cudaSuccess) return e;
+    if (narrow(dv.Da, dv.Dc)) {
+        static std::atomic<int> optin[kMaxDevices];
+        if ((e = ensure_smem_optin(decay_kv_kernel, KvSmem::kBytes, optin)) != cudaSuccess) return e;
+        const KvMaps maps = {{s[1].am, s[2].am, s[1].bm, s[1].cm}, s[2].om, s[1].om};
+        return scan::launch_after(decay_kv_kernel, dim3(1, dv.nseg, s[1].heads()), 32 * (2 * kWork + 1), KvSmem::kBytes, st,
+                                  true, maps, dv, dk.o, s[1].geo, s[2].geo, hdr);
+    }
+    s[1].geo.late = s[2].geo.late = 1;
+    if ((e = main_of<2, true>(s[1], true, hdr, st)) != cudaSuccess) return e;
+    return main_of<2, true>(s[2], true, hdr, st);
 }
 
 }  // namespace decay
