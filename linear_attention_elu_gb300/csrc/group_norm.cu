@@ -20,6 +20,9 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "mixing.cuh"
@@ -43,7 +46,7 @@ struct NormArgs {
     int chunks, per, gb;                            // other form: blocks of rows, their rows, groups per block
 };
 
-// V adjacent values as stored, and as floats.
+// V adjacent values as stored.
 template <typename T, int V> struct Raw { T v[V]; };
 template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
 template <> struct Raw<float, 4> { float4 v; };
@@ -55,59 +58,162 @@ template <typename T, int V> __device__ __forceinline__ Raw<T, V> load(const T* 
     else r.v = __ldg(reinterpret_cast<const float4*>(p));
     return r;
 }
-template <typename T, int V> __device__ __forceinline__ void floats(const Raw<T, V>& r, float (&f)[V]) {
+
+// V values in fp32, as packed pairs: half the instructions, which bound these kernels next to
+// memory.
+__device__ __forceinline__ uint64_t pk(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a;
+}
+__device__ __forceinline__ float hi_of(uint64_t v) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return b;
+}
+__device__ __forceinline__ uint64_t add1(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul1(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma1(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float add1(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul1(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma1(float a, float b, float c) { return fmaf(a, b, c); }
+
+template <int V> struct Vals {
+    static constexpr int n = V / 2;
+    uint64_t p[n];
+    __device__ __forceinline__ float get(int i) const { return i & 1 ? hi_of(p[i >> 1]) : lo_of(p[i >> 1]); }
+    template <typename F> __device__ __forceinline__ void make(F f) {       // value i = f(i)
+#pragma unroll
+        for (int i = 0; i < n; ++i) p[i] = pk(f(2 * i), f(2 * i + 1));
+    }
+};
+template <> struct Vals<1> {
+    static constexpr int n = 1;
+    float p[1];
+    __device__ __forceinline__ float get(int) const { return p[0]; }
+    template <typename F> __device__ __forceinline__ void make(F f) { p[0] = f(0); }
+};
+template <int V> __device__ __forceinline__ Vals<V> all(float v) {
+    Vals<V> r;
+    r.make([=](int) { return v; });
+    return r;
+}
+template <int V> __device__ __forceinline__ Vals<V> operator+(const Vals<V>& a, const Vals<V>& b) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < r.n; ++i) r.p[i] = add1(a.p[i], b.p[i]);
+    return r;
+}
+template <int V> __device__ __forceinline__ Vals<V> operator*(const Vals<V>& a, const Vals<V>& b) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < r.n; ++i) r.p[i] = mul1(a.p[i], b.p[i]);
+    return r;
+}
+template <int V> __device__ __forceinline__ Vals<V> fma(const Vals<V>& a, const Vals<V>& b, const Vals<V>& c) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < r.n; ++i) r.p[i] = fma1(a.p[i], b.p[i], c.p[i]);
+    return r;
+}
+template <int V> __device__ __forceinline__ float total(const Vals<V>& a) {
+    if constexpr (V == 8) {
+        const uint64_t s = add1(add1(a.p[0], a.p[1]), add1(a.p[2], a.p[3]));
+        return lo_of(s) + hi_of(s);
+    } else if constexpr (V == 4) {
+        const uint64_t s = add1(a.p[0], a.p[1]);
+        return lo_of(s) + hi_of(s);
+    } else {
+        return a.p[0];
+    }
+}
+template <typename T, int V> __device__ __forceinline__ Vals<V> floats(const Raw<T, V>& r) {
+    Vals<V> f;
     if constexpr (V == 1) {
-        f[0] = to_f(r.v[0]);
+        f.p[0] = to_f(r.v[0]);
     } else if constexpr (sizeof(T) == 2) {
         const uint32_t u[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 4; ++i) f.p[i] = pk(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
     } else {
-        f[0] = r.v.x, f[1] = r.v.y, f[2] = r.v.z, f[3] = r.v.w;
+        f.p[0] = pk(r.v.x, r.v.y), f.p[1] = pk(r.v.z, r.v.w);
     }
+    return f;
 }
-template <typename T, int V> __device__ __forceinline__ void store(T* p, const float (&f)[V]) {
+template <typename T, int V> __device__ __forceinline__ void store(T* p, const Vals<V>& f) {
     if constexpr (V == 1) {
-        *p = from_f<T>(f[0]);
+        *p = from_f<T>(f.p[0]);
     } else if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(tcc::pack_bf16(f[0], f[1]), tcc::pack_bf16(f[2], f[3]),
-                                                  tcc::pack_bf16(f[4], f[5]), tcc::pack_bf16(f[6], f[7]));
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = tcc::pack_bf16(lo_of(f.p[i]), hi_of(f.p[i]));
+        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
-        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(p) = make_float4(lo_of(f.p[0]), hi_of(f.p[0]), lo_of(f.p[1]), hi_of(f.p[1]));
     }
 }
 
-__device__ __forceinline__ float sigmoid(float v) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
+// 1 / (1 + e^-v): hardware exponential and reciprocal, a few 2^-23 in all; e^-v overflows to
+// infinity below -88.7, and its reciprocal is then 0: the limit.
+template <int V> __device__ __forceinline__ Vals<V> sigmoid(const Vals<V>& v) {
+    const Vals<V> t = v * all<V>(-1.4426950408889634f);
+    Vals<V> e;
+    e.make([&](int i) {
+        float r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t.get(i)));
+        return r;
+    });
+    e = e + all<V>(1.f);
+    Vals<V> s;
+    s.make([&](int i) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e.get(i)));
+        return r;
+    });
+    return s;
 }
 
-// y of one value from xh.
-__device__ __forceinline__ float forward(float u, bool act, bool gate, float z) {
-    const float v = act ? silu(u) : u;
-    return gate ? v * silu(z) : v;
+// y from u.
+template <int V> __device__ __forceinline__ Vals<V> forward(Vals<V> u, bool act, bool gate, const Vals<V>& z) {
+    if (act) u = u * sigmoid(u);
+    if (gate) u = u * (z * sigmoid(z));
+    return u;
 }
 
-// h = dL/du of one value, and dz.
-__device__ __forceinline__ float backward(float u, float dy, bool act, bool gate, float z, float* dz) {
-    float v = u, slope = 1.f;
+// h = dL/du from u and dy, and dz (in z's place). With s = sigmoid(u), the slope of u s is
+// s + u s (1 - s).
+template <int V>
+__device__ __forceinline__ Vals<V> backward(const Vals<V>& u, const Vals<V>& dy, bool act, bool gate, Vals<V>& z) {
+    const Vals<V> one = all<V>(1.f), minus = all<V>(-1.f);
+    Vals<V> v = u, h = dy, slope;
     if (act) {
-        const float s = sigmoid(u);
+        const Vals<V> s = sigmoid(u);
         v = u * s;
-        slope = s * fmaf(u, 1.f - s, 1.f);
+        slope = fma(v, fma(s, minus, one), s);
     }
-    float g = dy;
     if (gate) {
-        const float s = sigmoid(z);
-        *dz = dy * v * (s * fmaf(z, 1.f - s, 1.f));
-        g = dy * z * s;
+        const Vals<V> s = sigmoid(z), g = z * s;
+        z = v * dy * fma(g, fma(s, minus, one), s);
+        h = dy * g;
     }
-    return g * slope;
+    return act ? h * slope : h;
 }
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
@@ -115,195 +221,243 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
     return v;
 }
 
+// Neighbouring lanes' sum, kL of them (0: `lanes`, any power of two).
+template <int kL> __device__ __forceinline__ float group_sum(float v, int lanes) {
+    if constexpr (kL == 0) {
+        return lanes_sum(v, lanes);
+    } else {
+#pragma unroll
+        for (int o = kL / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+}
+
+template <typename T, int V> __device__ __forceinline__ Vals<V> weights_of(const void* p, int64_t c, bool in, float other) {
+    Vals<V> r;
+    r.make([&](int i) { return in && p ? to_f(static_cast<const T*>(p)[c + i]) : other; });
+    return r;
+}
+
 constexpr int kThreads = 256;
 
+// A thread's own vectors on the way: copied asynchronously to its places in shared memory, some
+// steps ahead of their use, so that what is in flight costs no registers. (Loads into registers
+// one step ahead left memory idle: 131072 rows of 1024 gated bf16 values 182 us.) Single
+// values (V = 1) are loaded when they are used.
+template <typename T, int V> struct Ring {
+    uint4* own;
+    __device__ __forceinline__ explicit Ring(void* smem) : own(static_cast<uint4*>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ void fetch(int slot, const T* p) const {
+        if constexpr (V > 1)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(own + slot * blockDim.x)), "l"(p) : "memory");
+    }
+    __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    template <int kLeft> __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+    __device__ __forceinline__ Vals<V> get(int slot, const T* p) const {
+        Raw<T, V> r;
+        if constexpr (V == 1) r = load<T, V>(p);
+        else r = *reinterpret_cast<const Raw<T, V>*>(own + slot * blockDim.x);
+        return floats<T, V>(r);
+    }
+};
+
 // One-token form. A row's groups lie side by side over the slots of a block, `lanes` each
-// (a power of two; a lane past the group's end holds nothing), K vectors of V values per
-// lane; rows side by side where several fit, kU times that many in flight.
-template <typename T, int V, int K, int kU>
-__global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constant__ NormArgs a) {
-    const int tid = threadIdx.x, S = a.slots, R = S <= kThreads ? kThreads / S : 1;
-    const int sub = S <= kThreads ? tid / S : 0, slot = S <= kThreads ? tid - sub * S : blockIdx.y * kThreads + tid;
-    const int g = slot / a.lanes, l = slot - g * a.lanes;
-    const bool act = a.silu != 0, gate = a.z != nullptr;
-    float w[K][V], b[K][V];
+// (a power of two), K vectors of V values per lane; rows side by side where several fit. kL:
+// the lanes, where the groups fill them and the slots whole blocks, so that every thread has
+// values; 0: any number, counted at run time, and a lane past the group's end, or a thread past
+// the last whole row, holds nothing.
+template <int V, int K, int kL> struct RowPlace {
+    int S, R, sub, lanes, g, l, c0, step;
     bool in[K];
-    const int c0 = g * a.Cg + l * V, step = a.lanes * V;
+    __device__ __forceinline__ explicit RowPlace(const NormArgs& a) {
+        const int tid = threadIdx.x;
+        S = a.slots;
+        R = S <= (int)blockDim.x ? blockDim.x / S : 1;
+        sub = S <= (int)blockDim.x ? tid / S : 0;
+        const int slot = S <= (int)blockDim.x ? tid - sub * S : blockIdx.y * blockDim.x + tid;
+        lanes = kL ? kL : a.lanes;
+        g = slot / lanes;
+        l = slot - g * lanes;
+        c0 = g * a.Cg + l * V;
+        step = lanes * V;
+#pragma unroll
+        for (int k = 0; k < K; ++k) in[k] = kL ? true : sub < R && slot < S && l * V + k * step < a.Cg;
+    }
+};
+
+template <int K> constexpr int kStages = K == 1 ? 4 : 2;
+
+template <typename T, int V, int K, int kL>
+__global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) rows_fwd_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ uint4 smem[];                // [stage][x, z][K][thread]
+    constexpr int kS = kStages<K>;
+    const RowPlace<V, K, kL> t(a);
+    const Ring<T, V> ring(smem);
+    const bool act = a.silu != 0, gate = a.z != nullptr;
+    Vals<V> w[K], b[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        in[k] = sub < R && slot < S && l * V + k * step < a.Cg;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            w[k][i] = in[k] && a.w ? to_f(static_cast<const T*>(a.w)[c0 + k * step + i]) : 1.f;
-            b[k][i] = in[k] && a.b ? to_f(static_cast<const T*>(a.b)[c0 + k * step + i]) : 0.f;
-        }
+        w[k] = weights_of<T, V>(a.w, t.c0 + k * t.step, t.in[k], 1.f);
+        b[k] = weights_of<T, V>(a.b, t.c0 + k * t.step, t.in[k], 0.f);
     }
     const float inv = 1.f / a.Cg;
-    for (int64_t base = (int64_t)blockIdx.x * R * kU; base < a.B; base += (int64_t)gridDim.x * R * kU) {
-        Raw<T, V> x[kU][K], z[kU][K];
+    const int stride = gridDim.x * t.R, count = (a.B - (int)blockIdx.x * t.R + stride - 1) / stride;
+    int row = blockIdx.x * t.R + t.sub, ahead = row;
+    const T* x = static_cast<const T*>(a.x) + t.c0;
+    const T* z = static_cast<const T*>(a.z) + (gate ? t.c0 : 0);
+    T* y = static_cast<T*>(a.y) + t.c0;
+    auto fetch = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int64_t row = base + u * R + sub;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!in[k] || row >= a.B) continue;
-                x[u][k] = load<T, V>(static_cast<const T*>(a.x) + row * a.x_bs + c0 + k * step);
-                if (gate) z[u][k] = load<T, V>(static_cast<const T*>(a.z) + row * a.z_bs + c0 + k * step);
+        for (int k = 0; k < K; ++k)
+            if (t.in[k] && ahead < a.B) {
+                ring.fetch(((i % kS) * 2 + 0) * K + k, x + ahead * a.x_bs + k * t.step);
+                if (gate) ring.fetch(((i % kS) * 2 + 1) * K + k, z + ahead * a.z_bs + k * t.step);
             }
-        }
+        ring.commit();
+        ahead += stride;                           // at most B + kS strides: B <= 2^30
+    };
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int64_t row = base + u * R + sub;
-            float f[K][V], sum = 0.f, sq = 0.f;
+    for (int i = 0; i < kS - 1; ++i) fetch(i);
+    for (int i = 0; i < count; ++i, row += stride) {
+        ring.template wait<kS - 2>();
+        fetch(i + kS - 1);
+        const int at = (i % kS) * 2 * K;
+        const bool on = row < a.B;
+        Vals<V> f[K];
+        float sum = 0.f, sq = 0.f;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!in[k] || row >= a.B) continue;
-                floats<T, V>(x[u][k], f[k]);
+        for (int k = 0; k < K; ++k)
+            if (on && t.in[k]) f[k] = ring.get(at + k, x + row * a.x_bs + k * t.step), sum += total(f[k]);
+        const float mean = group_sum<kL>(sum, t.lanes) * inv;
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum += f[k][i];
+        for (int k = 0; k < K; ++k)
+            if (on && t.in[k]) f[k] = f[k] + all<V>(-mean), sq += total(f[k] * f[k]);
+        const float r = rsqrtf(fmaf(group_sum<kL>(sq, t.lanes), inv, a.eps));
+        if (a.stats && t.l == 0 && on && t.in[0])
+            reinterpret_cast<float2*>(a.stats)[(int64_t)row * a.G + t.g] = make_float2(mean, r);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (on && t.in[k]) {
+                Vals<V> zf = f[k];
+                if (gate) zf = ring.get(at + K + k, z + row * a.z_bs + k * t.step);
+                store<T, V>(y + row * a.y_bs + k * t.step, forward(fma(f[k] * all<V>(r), w[k], b[k]), act, gate, zf));
             }
-            const float mean = lanes_sum(sum, a.lanes) * inv;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!in[k] || row >= a.B) continue;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    f[k][i] -= mean;
-                    sq = fmaf(f[k][i], f[k][i], sq);
-                }
-            }
-            const float r = 1.f / sqrtf(fmaf(lanes_sum(sq, a.lanes), inv, a.eps));
-            if (a.stats && l == 0 && in[0] && row < a.B)
-                *reinterpret_cast<float2*>(a.stats + 2 * (row * a.G + g)) = make_float2(mean, r);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!in[k] || row >= a.B) continue;
-                float zf[V], y[V];
-                if (gate) floats<T, V>(z[u][k], zf);
-#pragma unroll
-                for (int i = 0; i < V; ++i) y[i] = forward(fmaf(f[k][i] * r, w[k][i], b[k][i]), act, gate, gate ? zf[i] : 0.f);
-                store<T, V>(static_cast<T*>(a.y) + row * a.y_bs + c0 + k * step, y);
-            }
-        }
     }
 }
 
 // partial: [gridDim.x][2][C], the block's sums of h xh and of h.
-template <typename T, int V, int K, int kU>
-__global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float red[kThreads * V];
-    const int tid = threadIdx.x, S = a.slots, R = S <= kThreads ? kThreads / S : 1;
-    const int sub = S <= kThreads ? tid / S : 0, slot = S <= kThreads ? tid - sub * S : blockIdx.y * kThreads + tid;
-    const int g = slot / a.lanes, l = slot - g * a.lanes;
+template <typename T, int V, int K, int kL>
+__global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) rows_bwd_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ uint4 smem[];                // [stage][x, dy, z][K][thread]; then the rows' sums
+    constexpr int kS = kStages<K>;
+    const RowPlace<V, K, kL> t(a);
+    const Ring<T, V> ring(smem);
     const bool act = a.silu != 0, gate = a.z != nullptr;
-    float w[K][V], b[K][V], dw[K][V], db[K][V];
-    bool in[K];
-    const int c0 = g * a.Cg + l * V, step = a.lanes * V;
+    Vals<V> w[K], b[K], dw[K], db[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        in[k] = sub < R && slot < S && l * V + k * step < a.Cg;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            w[k][i] = in[k] && a.w ? to_f(static_cast<const T*>(a.w)[c0 + k * step + i]) : 1.f;
-            b[k][i] = in[k] && a.b ? to_f(static_cast<const T*>(a.b)[c0 + k * step + i]) : 0.f;
-            dw[k][i] = db[k][i] = 0.f;
-        }
+        w[k] = weights_of<T, V>(a.w, t.c0 + k * t.step, t.in[k], 1.f);
+        b[k] = weights_of<T, V>(a.b, t.c0 + k * t.step, t.in[k], 0.f);
+        dw[k] = db[k] = all<V>(0.f);
     }
-    const float inv = 1.f / a.Cg;
-    for (int64_t base = (int64_t)blockIdx.x * R * kU; base < a.B; base += (int64_t)gridDim.x * R * kU) {
-        Raw<T, V> x[kU][K], d[kU][K], z[kU][K];
-        float2 s[kU];
+    const float inv = -1.f / a.Cg;
+    const int stride = gridDim.x * t.R, count = (a.B - (int)blockIdx.x * t.R + stride - 1) / stride;
+    int row = blockIdx.x * t.R + t.sub, ahead = row;
+    const T* x = static_cast<const T*>(a.x) + t.c0;
+    const T* d = static_cast<const T*>(a.dy) + t.c0;
+    const T* z = static_cast<const T*>(a.z) + (gate ? t.c0 : 0);
+    T* y = static_cast<T*>(a.y) + t.c0;
+    T* dz = static_cast<T*>(a.dz) + (gate ? t.c0 : 0);
+    const float2* stats = reinterpret_cast<const float2*>(a.stats) + t.g;
+    auto fetch = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int64_t row = base + u * R + sub;
-            s[u] = make_float2(0.f, 0.f);
-            if (in[0] && row < a.B) s[u] = __ldg(reinterpret_cast<const float2*>(a.stats + 2 * (row * a.G + g)));
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!in[k] || row >= a.B) continue;
-                x[u][k] = load<T, V>(static_cast<const T*>(a.x) + row * a.x_bs + c0 + k * step);
-                d[u][k] = load<T, V>(static_cast<const T*>(a.dy) + row * a.dy_bs + c0 + k * step);
-                if (gate) z[u][k] = load<T, V>(static_cast<const T*>(a.z) + row * a.z_bs + c0 + k * step);
+        for (int k = 0; k < K; ++k)
+            if (t.in[k] && ahead < a.B) {
+                ring.fetch(((i % kS) * 3 + 0) * K + k, x + ahead * a.x_bs + k * t.step);
+                ring.fetch(((i % kS) * 3 + 1) * K + k, d + ahead * a.dy_bs + k * t.step);
+                if (gate) ring.fetch(((i % kS) * 3 + 2) * K + k, z + ahead * a.z_bs + k * t.step);
             }
-        }
+        ring.commit();
+        ahead += stride;
+    };
+    auto stats_of = [&](int n) { return n < a.B && t.in[0] ? __ldg(stats + (int64_t)n * a.G) : make_float2(0.f, 0.f); };
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int64_t row = base + u * R + sub;
-            const float mean = s[u].x, r = s[u].y;
-            float xh[K][V], gw[K][V], s1 = 0.f, s2 = 0.f;
+    for (int i = 0; i < kS - 1; ++i) fetch(i);
+    float2 st = stats_of(row);
+    for (int i = 0; i < count; ++i, row += stride) {
+        ring.template wait<kS - 2>();
+        fetch(i + kS - 1);
+        const float2 next = stats_of(row + stride);
+        const int at = (i % kS) * 3 * K;
+        const bool on = row < a.B;
+        Vals<V> xh[K], gw[K];
+        float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!in[k] || row >= a.B) continue;
-                float df[V], zf[V], dz[V];
-                floats<T, V>(x[u][k], xh[k]);
-                floats<T, V>(d[u][k], df);
-                if (gate) floats<T, V>(z[u][k], zf);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    xh[k][i] = (xh[k][i] - mean) * r;
-                    const float h = backward(fmaf(xh[k][i], w[k][i], b[k][i]), df[i], act, gate, gate ? zf[i] : 0.f, &dz[i]);
-                    dw[k][i] = fmaf(h, xh[k][i], dw[k][i]);
-                    db[k][i] += h;
-                    gw[k][i] = h * w[k][i];
-                    s1 += gw[k][i];
-                    s2 = fmaf(gw[k][i], xh[k][i], s2);
-                }
-                if (gate) store<T, V>(static_cast<T*>(a.dz) + row * a.dz_bs + c0 + k * step, dz);
+        for (int k = 0; k < K; ++k)
+            if (on && t.in[k]) {
+                xh[k] = (ring.get(at + k, x + row * a.x_bs + k * t.step) + all<V>(-st.x)) * all<V>(st.y);
+                Vals<V> zf = xh[k];
+                if (gate) zf = ring.get(at + 2 * K + k, z + row * a.z_bs + k * t.step);
+                const Vals<V> h = backward(fma(xh[k], w[k], b[k]), ring.get(at + K + k, d + row * a.dy_bs + k * t.step), act, gate, zf);
+                if (gate) store<T, V>(dz + row * a.dz_bs + k * t.step, zf);
+                dw[k] = fma(h, xh[k], dw[k]);
+                db[k] = db[k] + h;
+                gw[k] = h * w[k];
+                s1 += total(gw[k]);
+                s2 += total(gw[k] * xh[k]);
             }
-            s1 = lanes_sum(s1, a.lanes) * inv;
-            s2 = lanes_sum(s2, a.lanes) * inv;
+        s1 = group_sum<kL>(s1, t.lanes) * inv;
+        s2 = group_sum<kL>(s2, t.lanes) * inv;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!in[k] || row >= a.B) continue;
-                float dx[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) dx[i] = r * (gw[k][i] - s1 - xh[k][i] * s2);
-                store<T, V>(static_cast<T*>(a.y) + row * a.y_bs + c0 + k * step, dx);
-            }
-        }
+        for (int k = 0; k < K; ++k)
+            if (on && t.in[k])
+                store<T, V>(y + row * a.y_bs + k * t.step, fma(xh[k], all<V>(s2), gw[k] + all<V>(s1)) * all<V>(st.y));
+        st = next;
     }
+    ring.template wait<0>();
     tcc::pdl_launch_dependents();
     // The rows' sums side by side, in order.
+    float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < V; ++i) red[i * kThreads + tid] = which ? db[k][i] : dw[k][i];
+            for (int i = 0; i < V; ++i) red[i * kThreads + threadIdx.x] = which ? db[k].get(i) : dw[k].get(i);
             __syncthreads();
-            if (sub == 0 && in[k])
+            if (t.sub == 0 && t.in[k])
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float v = 0.f;
-                    for (int j = 0; j < R; ++j) v += red[i * kThreads + j * S + tid];
-                    a.partial[((int64_t)blockIdx.x * 2 + which) * a.C + c0 + k * step + i] = v;
+                    for (int j = 0; j < t.R; ++j) v += red[i * kThreads + j * t.S + threadIdx.x];
+                    a.partial[((int64_t)blockIdx.x * 2 + which) * a.C + t.c0 + k * t.step + i] = v;
                 }
         }
 }
 
-// dw, db = sums over the blocks of partial [blocks][2][C], in order within eight slices.
-__global__ void __launch_bounds__(256) weights_kernel(const float* partial, float* dw, float* db, int64_t blocks, int C) {
-    __shared__ float red[8][33];
+// dw, db = sums over the blocks of partial [blocks][2][C], in order within 32 slices.
+__global__ void __launch_bounds__(1024) weights_kernel(const float* partial, float* dw, float* db, int64_t blocks, int C) {
+    __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     tcc::pdl_wait();
     float v = 0.f;
     if (c < C)
 #pragma unroll 8
-        for (int64_t i = warp; i < blocks; i += 8) v += partial[(2 * i + blockIdx.y) * C + c];
+        for (int64_t i = warp; i < blocks; i += 32) v += partial[(2 * i + blockIdx.y) * C + c];
     red[warp][lane] = v;
     __syncthreads();
     float* to = blockIdx.y ? db : dw;
     if (warp == 0 && c < C && to) {
         v = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += red[i][lane];
+        for (int i = 0; i < 32; ++i) v += red[i][lane];
         to[c] = v;
     }
 }
 
 // The other form's block: rows n0 .. n1 of sample b, the channels of gb groups from c0; a
-// thread holds V channels of every sub-th row.
+// thread holds V channels of every subs-th row.
 struct Block {
     int b, chunk, n0, n1, g0, ng, c0, cols, sub, subs, c;
     bool on;
@@ -328,88 +482,97 @@ template <int V> __device__ __forceinline__ Block block_of_rows(const NormArgs& 
 
 constexpr int kMost = 1024;           // threads, and channels of a group
 constexpr int kNarrow = 128;          // channels of a group of single tokens without whole 16-byte pieces
-constexpr int kTileRows = 8;
+constexpr int kTileRows = 8;          // of the statistics: a mean, and squares about it
+constexpr int kRows = 4;              // rows on the way per thread of the other passes
+
+// The group of each of a thread's V channels from c on.
+template <int V> struct Groups {
+    int g[V];
+    __device__ __forceinline__ Groups(int c, int Cg) {
+        g[0] = c / Cg;
+        int next = (g[0] + 1) * Cg - c;                // channels until the next group
+#pragma unroll
+        for (int i = 1; i < V; ++i) {
+            g[i] = g[i - 1];
+            if (i == next) ++g[i], next += Cg;
+        }
+    }
+};
 
 // partial: [B chunks][G][2], mean of the block's values of a group and sum of squares about it.
 template <typename T, int V>
-__global__ void __launch_bounds__(V == 1 ? kMost : kThreads) stats_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ float sm[];                  // [subs][cols] means, then squares
+__global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) stats_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ uint4 smem[];                // [2 tiles][row][thread]; then [subs][cols] means, squares
+    float* sm = reinterpret_cast<float*>(smem);
     const Block k = block_of_rows<V>(a);
-    const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
-    float mean[V], m2[V];
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) mean[i] = m2[i] = 0.f;
-    if (k.on)
-        for (int r0 = k.n0 + k.sub; r0 < k.n1; r0 += kTileRows * k.subs) {
-            Raw<T, V> raw[kTileRows];
-            const int m = min((k.n1 - r0 + k.subs - 1) / k.subs, kTileRows);
+    const Ring<T, V> ring(smem);
+    Vals<V> mean = all<V>(0.f), m2 = all<V>(0.f);
+    if (k.on) {
+        const Vals<V> minus = all<V>(-1.f);
+        const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
+        const int step = k.subs * kTileRows;
+        auto fetch = [&](int i, int row) {
 #pragma unroll
             for (int u = 0; u < kTileRows; ++u)
-                if (u < m) raw[u] = load<T, V>(x + (int64_t)(r0 + u * k.subs) * a.x_ts);
-            float tm[V], tq[V];
+                if (row + u * k.subs < k.n1) ring.fetch((i & 1) * kTileRows + u, x + (row + u * k.subs) * a.x_ts);
+            ring.commit();
+        };
+        int n = 0, row = k.n0 + k.sub;
+        fetch(0, row);
+        for (int i = 0; row < k.n1; ++i, row += step) {
+            fetch(i + 1, row + step);
+            ring.template wait<1>();
+            const int m = min((k.n1 - row + k.subs - 1) / k.subs, kTileRows);
+            // The tile's mean and squares about it, joined to those before.
+            Vals<V> tm = all<V>(0.f), tq = all<V>(0.f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) tm[i] = tq[i] = 0.f;
+            for (int u = 0; u < kTileRows; ++u)
+                if (u < m) tm = tm + ring.get((i & 1) * kTileRows + u, x + (row + u * k.subs) * a.x_ts);
+            tm = tm * all<V>(__fdividef(1.f, (float)m));
+            const Vals<V> off = tm * minus;
 #pragma unroll
             for (int u = 0; u < kTileRows; ++u)
                 if (u < m) {
-                    float f[V];
-                    floats<T, V>(raw[u], f);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) tm[i] += f[i];
+                    const Vals<V> d = ring.get((i & 1) * kTileRows + u, x + (row + u * k.subs) * a.x_ts) + off;
+                    tq = fma(d, d, tq);
                 }
-            const float each = 1.f / m;
-#pragma unroll
-            for (int i = 0; i < V; ++i) tm[i] *= each;
-#pragma unroll
-            for (int u = 0; u < kTileRows; ++u)
-                if (u < m) {
-                    float f[V];
-                    floats<T, V>(raw[u], f);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) tq[i] = fmaf(f[i] - tm[i], f[i] - tm[i], tq[i]);
-                }
-            // Joins the tile's mean and squares to those before it.
-            const float share = (float)m / (n + m), cross = share * n;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = tm[i] - mean[i];
-                mean[i] = fmaf(d, share, mean[i]);
-                m2[i] += fmaf(d * d, cross, tq[i]);
-            }
+            const float share = __fdividef((float)m, (float)(n + m));
+            const Vals<V> d = fma(mean, minus, tm);
+            mean = fma(d, all<V>(share), mean);
+            m2 = m2 + fma(d * d, all<V>(share * n), tq);
             n += m;
         }
+        ring.template wait<0>();
+    }
+    __syncthreads();
     tcc::pdl_launch_dependents();
-    const int rows = k.n1 - k.n0;
+    const int rows = k.n1 - k.n0, whole = rows / k.subs, more = rows - whole * k.subs;   // rows of a thread
     float *sm_mean = sm, *sm_sq = sm + k.subs * k.cols;
     if (k.on)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            sm_mean[k.sub * k.cols + k.c + i] = mean[i];
-            sm_sq[k.sub * k.cols + k.c + i] = m2[i];
+            sm_mean[k.sub * k.cols + k.c + i] = mean.get(i);
+            sm_sq[k.sub * k.cols + k.c + i] = m2.get(i);
         }
     __syncthreads();
+    const float inv = 1.f / rows;
     for (int c = threadIdx.x; c < k.cols; c += blockDim.x) {
         float m = 0.f, q = 0.f;
-        const float inv = 1.f / rows;
+        for (int s = 0; s < k.subs; ++s) m = fmaf((float)(whole + (s < more)) * inv, sm_mean[s * k.cols + c], m);
         for (int s = 0; s < k.subs; ++s) {
-            const int cnt = (rows - s + k.subs - 1) / k.subs;
-            if (cnt > 0) m = fmaf(cnt * inv, sm_mean[s * k.cols + c], m);
-        }
-        for (int s = 0; s < k.subs; ++s) {
-            const int cnt = (rows - s + k.subs - 1) / k.subs;
             const float d = sm_mean[s * k.cols + c] - m;
-            if (cnt > 0) q += fmaf(cnt * d, d, sm_sq[s * k.cols + c]);
+            q += fmaf((float)(whole + (s < more)) * d, d, sm_sq[s * k.cols + c]);
         }
-        sm_mean[c] = m;
+        sm_mean[c] = m;                            // this thread alone reads and writes column c
         sm_sq[c] = q;
     }
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float each = 1.f / a.Cg;
     for (int g = warp; g < k.ng; g += blockDim.x >> 5) {
         float m = 0.f, q = 0.f;
         for (int c = lane; c < a.Cg; c += 32) m += sm_mean[g * a.Cg + c];
-        m = lanes_sum(m, 32) / a.Cg;
+        m = lanes_sum(m, 32) * each;
         for (int c = lane; c < a.Cg; c += 32) {
             const float d = sm_mean[g * a.Cg + c] - m;
             q += fmaf(rows * d, d, sm_sq[g * a.Cg + c]);
@@ -421,122 +584,112 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads) stats_kernel(const 
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(V == 1 ? kMost : kThreads) apply_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ float sm[];                  // [groups][2]: mean, r
+__global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) apply_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ uint4 smem[];                // [stage][x, z][thread]; [groups][2]: -mean, r
     const Block k = block_of_rows<V>(a);
+    const Ring<T, V> ring(smem);
+    float* sm = reinterpret_cast<float*>(smem + (V > 1 ? kRows * 2 * blockDim.x : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool act = a.silu != 0, gate = a.z != nullptr;
+    const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
+    const T* z = static_cast<const T*>(a.z) + (gate ? k.b * a.z_bs + k.c0 + k.c : 0);
+    T* y = static_cast<T*>(a.y) + k.b * a.y_bs + k.c0 + k.c;
+    int row = k.n0 + k.sub;
+    auto fetch = [&](int i, int n) {
+        if (k.on && n < k.n1) {
+            ring.fetch((i % kRows) * 2, x + n * a.x_ts);
+            if (gate) ring.fetch((i % kRows) * 2 + 1, z + n * a.z_ts);
+        }
+        ring.commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kRows - 1; ++i) fetch(i, row + i * k.subs);
     tcc::pdl_wait();
+    const float inv = 1.f / a.N, size = (float)a.N * a.Cg;
     for (int g = warp; g < k.ng; g += blockDim.x >> 5) {
         const float2* p = reinterpret_cast<const float2*>(a.partial) + (int64_t)k.b * a.chunks * a.G + k.g0 + g;
         float m = 0.f, q = 0.f;
-        for (int i = lane; i < a.chunks; i += 32) m = fmaf((float)min(a.per, a.N - i * a.per), p[(int64_t)i * a.G].x, m);
-        m = lanes_sum(m, 32) / a.N;
+        for (int i = lane; i < a.chunks; i += 32) m = fmaf((float)min(a.per, a.N - i * a.per) * inv, p[(int64_t)i * a.G].x, m);
+        m = lanes_sum(m, 32);
         for (int i = lane; i < a.chunks; i += 32) {
             const float2 v = p[(int64_t)i * a.G];
             q += fmaf((float)min(a.per, a.N - i * a.per) * a.Cg * (v.x - m), v.x - m, v.y);
         }
-        const float r = 1.f / sqrtf(lanes_sum(q, 32) / ((float)a.N * a.Cg) + a.eps);
+        const float r = rsqrtf(lanes_sum(q, 32) / size + a.eps);
         if (lane == 0) {
-            sm[2 * g] = m, sm[2 * g + 1] = r;
+            sm[2 * g] = -m, sm[2 * g + 1] = r;
             if (a.stats && k.chunk == 0)
                 *reinterpret_cast<float2*>(a.stats + 2 * ((int64_t)k.b * a.G + k.g0 + g)) = make_float2(m, r);
         }
     }
     __syncthreads();
     if (!k.on) return;
-    const bool act = a.silu != 0, gate = a.z != nullptr;
-    float mean[V], scale[V], bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = k.c + i, g = c / a.Cg;
-        mean[i] = sm[2 * g];
-        scale[i] = sm[2 * g + 1] * (a.w ? to_f(static_cast<const T*>(a.w)[k.c0 + c]) : 1.f);
-        bias[i] = a.b ? to_f(static_cast<const T*>(a.b)[k.c0 + c]) : 0.f;
-    }
-    const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
-    const T* z = static_cast<const T*>(a.z) + (gate ? k.b * a.z_bs + k.c0 + k.c : 0);
-    T* y = static_cast<T*>(a.y) + k.b * a.y_bs + k.c0 + k.c;
-    constexpr int kU = 4;
-    for (int r0 = k.n0 + k.sub; r0 < k.n1; r0 += kU * k.subs) {
-        Raw<T, V> rx[kU], rz[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int r = r0 + u * k.subs;
-            if (r >= k.n1) continue;
-            rx[u] = load<T, V>(x + (int64_t)r * a.x_ts);
-            if (gate) rz[u] = load<T, V>(z + (int64_t)r * a.z_ts);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int r = r0 + u * k.subs;
-            if (r >= k.n1) continue;
-            float f[V], zf[V];
-            floats<T, V>(rx[u], f);
-            if (gate) floats<T, V>(rz[u], zf);
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = forward(fmaf(f[i] - mean[i], scale[i], bias[i]), act, gate, gate ? zf[i] : 0.f);
-            store<T, V>(y + (int64_t)r * a.y_ts, f);
-        }
+    const Groups<V> gr(k.c, a.Cg);
+    Vals<V> mean, scale;
+    mean.make([&](int i) { return sm[2 * gr.g[i]]; });
+    scale.make([&](int i) { return sm[2 * gr.g[i] + 1]; });
+    scale = scale * weights_of<T, V>(a.w, k.c0 + k.c, true, 1.f);
+    const Vals<V> bias = weights_of<T, V>(a.b, k.c0 + k.c, true, 0.f);
+    for (int i = 0; row < k.n1; ++i, row += k.subs) {
+        ring.template wait<kRows - 2>();
+        fetch(i + kRows - 1, row + (kRows - 1) * k.subs);
+        const Vals<V> f = ring.get((i % kRows) * 2, x + row * a.x_ts) + mean;
+        Vals<V> zf = f;
+        if (gate) zf = ring.get((i % kRows) * 2 + 1, z + row * a.z_ts);
+        store<T, V>(y + row * a.y_ts, forward(fma(f, scale, bias), act, gate, zf));
     }
 }
 
 // partial: [B chunks][2][C] sums of h xh and of h, then [B chunks][G][2] of w h and of w h xh.
 template <typename T, int V>
-__global__ void __launch_bounds__(V == 1 ? kMost : kThreads) sums_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ float sm[];                  // [2][subs][cols]
+__global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8 ? 2 : 3) sums_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ uint4 smem[];                // [stage][x, dy, z][thread]; then [2][subs][cols]
+    float* sm = reinterpret_cast<float*>(smem);
     const Block k = block_of_rows<V>(a);
+    const Ring<T, V> ring(smem);
     const bool act = a.silu != 0, gate = a.z != nullptr;
-    float dw[V], db[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.f;
+    Vals<V> dw = all<V>(0.f), db = all<V>(0.f);
     if (k.on) {
-        float mean[V], r[V], w[V], b[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = k.c0 + k.c + i;
-            const float2 s = __ldg(reinterpret_cast<const float2*>(a.stats) + (int64_t)k.b * a.G + c / a.Cg);
-            mean[i] = s.x, r[i] = s.y;
-            w[i] = a.w ? to_f(static_cast<const T*>(a.w)[c]) : 1.f;
-            b[i] = a.b ? to_f(static_cast<const T*>(a.b)[c]) : 0.f;
-        }
         const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
         const T* d = static_cast<const T*>(a.dy) + k.b * a.dy_bs + k.c0 + k.c;
         const T* z = static_cast<const T*>(a.z) + (gate ? k.b * a.z_bs + k.c0 + k.c : 0);
-        constexpr int kU = 4;
-        for (int r0 = k.n0 + k.sub; r0 < k.n1; r0 += kU * k.subs) {
-            Raw<T, V> rx[kU], rd[kU], rz[kU];
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int n = r0 + u * k.subs;
-                if (n >= k.n1) continue;
-                rx[u] = load<T, V>(x + (int64_t)n * a.x_ts);
-                rd[u] = load<T, V>(d + (int64_t)n * a.dy_ts);
-                if (gate) rz[u] = load<T, V>(z + (int64_t)n * a.z_ts);
+        int row = k.n0 + k.sub;
+        auto fetch = [&](int i, int n) {
+            if (n < k.n1) {
+                ring.fetch((i % kRows) * 3, x + n * a.x_ts);
+                ring.fetch((i % kRows) * 3 + 1, d + n * a.dy_ts);
+                if (gate) ring.fetch((i % kRows) * 3 + 2, z + n * a.z_ts);
             }
+            ring.commit();
+        };
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                if (r0 + u * k.subs >= k.n1) continue;
-                float f[V], df[V], zf[V], dz;
-                floats<T, V>(rx[u], f);
-                floats<T, V>(rd[u], df);
-                if (gate) floats<T, V>(rz[u], zf);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = (f[i] - mean[i]) * r[i];
-                    const float h = backward(fmaf(xh, w[i], b[i]), df[i], act, gate, gate ? zf[i] : 0.f, &dz);
-                    dw[i] = fmaf(h, xh, dw[i]);
-                    db[i] += h;
-                }
-            }
+        for (int i = 0; i < kRows - 1; ++i) fetch(i, row + i * k.subs);
+        const float2* s = reinterpret_cast<const float2*>(a.stats) + (int64_t)k.b * a.G + k.g0;
+        const Groups<V> gr(k.c, a.Cg);
+        Vals<V> mean, r;
+        mean.make([&](int i) { return -__ldg(s + gr.g[i]).x; });
+        r.make([&](int i) { return __ldg(s + gr.g[i]).y; });
+        const Vals<V> w = weights_of<T, V>(a.w, k.c0 + k.c, true, 1.f), b = weights_of<T, V>(a.b, k.c0 + k.c, true, 0.f);
+        for (int i = 0; row < k.n1; ++i, row += k.subs) {
+            ring.template wait<kRows - 2>();
+            fetch(i + kRows - 1, row + (kRows - 1) * k.subs);
+            const Vals<V> xh = (ring.get((i % kRows) * 3, x + row * a.x_ts) + mean) * r;
+            Vals<V> zf = xh;
+            if (gate) zf = ring.get((i % kRows) * 3 + 2, z + row * a.z_ts);
+            const Vals<V> h = backward(fma(xh, w, b), ring.get((i % kRows) * 3 + 1, d + row * a.dy_ts), act, gate, zf);
+            dw = fma(h, xh, dw);
+            db = db + h;
         }
+        ring.template wait<0>();
     }
+    __syncthreads();
     tcc::pdl_launch_dependents();
     float *s_w = sm, *s_b = sm + k.subs * k.cols;
     if (k.on)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            s_w[k.sub * k.cols + k.c + i] = dw[i];
-            s_b[k.sub * k.cols + k.c + i] = db[i];
+            s_w[k.sub * k.cols + k.c + i] = dw.get(i);
+            s_b[k.sub * k.cols + k.c + i] = db.get(i);
         }
     __syncthreads();
     float* channel = a.partial + (int64_t)blockIdx.x * 2 * a.C + k.c0;
@@ -562,79 +715,78 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads) sums_kernel(const _
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(V == 1 ? kMost : kThreads) apply_bwd_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ float sm[];                  // [groups][2]: means of w h and of w h xh
+__global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8 ? 2 : 3) apply_bwd_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ uint4 smem[];                // [stage][x, dy, z][thread]; [groups][2]: -means of w h and of w h xh
     const Block k = block_of_rows<V>(a);
+    const Ring<T, V> ring(smem);
+    float* sm = reinterpret_cast<float*>(smem + (V > 1 ? kRows * 3 * blockDim.x : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    tcc::pdl_launch_dependents();
-    tcc::pdl_wait();
-    const float2* parts = reinterpret_cast<const float2*>(a.partial + (int64_t)a.B * a.chunks * 2 * a.C);
-    for (int g = warp; g < k.ng; g += blockDim.x >> 5) {
-        const float2* p = parts + (int64_t)k.b * a.chunks * a.G + k.g0 + g;
-        float u = 0.f, v = 0.f;
-        for (int i = lane; i < a.chunks; i += 32) u += p[(int64_t)i * a.G].x, v += p[(int64_t)i * a.G].y;
-        u = lanes_sum(u, 32);
-        v = lanes_sum(v, 32);
-        if (lane == 0) sm[2 * g] = u / ((float)a.N * a.Cg), sm[2 * g + 1] = v / ((float)a.N * a.Cg);
-    }
-    __syncthreads();
-    if (!k.on) return;
     const bool act = a.silu != 0, gate = a.z != nullptr;
-    float mean[V], r[V], w[V], b[V], s1[V], s2[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = k.c + i, g = c / a.Cg;
-        const float2 s = __ldg(reinterpret_cast<const float2*>(a.stats) + (int64_t)k.b * a.G + k.g0 + g);
-        mean[i] = s.x, r[i] = s.y;
-        w[i] = a.w ? to_f(static_cast<const T*>(a.w)[k.c0 + c]) : 1.f;
-        b[i] = a.b ? to_f(static_cast<const T*>(a.b)[k.c0 + c]) : 0.f;
-        s1[i] = sm[2 * g], s2[i] = sm[2 * g + 1];
-    }
     const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
     const T* d = static_cast<const T*>(a.dy) + k.b * a.dy_bs + k.c0 + k.c;
     const T* z = static_cast<const T*>(a.z) + (gate ? k.b * a.z_bs + k.c0 + k.c : 0);
     T* y = static_cast<T*>(a.y) + k.b * a.y_bs + k.c0 + k.c;
     T* dz = static_cast<T*>(a.dz) + (gate ? k.b * a.dz_bs + k.c0 + k.c : 0);
-    constexpr int kU = 4;
-    for (int r0 = k.n0 + k.sub; r0 < k.n1; r0 += kU * k.subs) {
-        Raw<T, V> rx[kU], rd[kU], rz[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int n = r0 + u * k.subs;
-            if (n >= k.n1) continue;
-            rx[u] = load<T, V>(x + (int64_t)n * a.x_ts);
-            rd[u] = load<T, V>(d + (int64_t)n * a.dy_ts);
-            if (gate) rz[u] = load<T, V>(z + (int64_t)n * a.z_ts);
+    int row = k.n0 + k.sub;
+    auto fetch = [&](int i, int n) {
+        if (k.on && n < k.n1) {
+            ring.fetch((i % kRows) * 3, x + n * a.x_ts);
+            ring.fetch((i % kRows) * 3 + 1, d + n * a.dy_ts);
+            if (gate) ring.fetch((i % kRows) * 3 + 2, z + n * a.z_ts);
         }
+        ring.commit();
+    };
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int n = r0 + u * k.subs;
-            if (n >= k.n1) continue;
-            float f[V], df[V], zf[V], dzf[V];
-            floats<T, V>(rx[u], f);
-            floats<T, V>(rd[u], df);
-            if (gate) floats<T, V>(rz[u], zf);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float xh = (f[i] - mean[i]) * r[i];
-                const float h = backward(fmaf(xh, w[i], b[i]), df[i], act, gate, gate ? zf[i] : 0.f, &dzf[i]);
-                f[i] = r[i] * (h * w[i] - s1[i] - xh * s2[i]);
-            }
-            store<T, V>(y + (int64_t)n * a.y_ts, f);
-            if (gate) store<T, V>(dz + (int64_t)n * a.dz_ts, dzf);
+    for (int i = 0; i < kRows - 1; ++i) fetch(i, row + i * k.subs);
+    tcc::pdl_launch_dependents();
+    tcc::pdl_wait();
+    const float2* parts = reinterpret_cast<const float2*>(a.partial + (int64_t)a.B * a.chunks * 2 * a.C);
+    const float inv = -1.f / ((float)a.N * a.Cg);
+    for (int g = warp; g < k.ng; g += blockDim.x >> 5) {
+        const float2* p = parts + (int64_t)k.b * a.chunks * a.G + k.g0 + g;
+        float u = 0.f, v = 0.f;
+        for (int i = lane; i < a.chunks; i += 32) {
+            const float2 t = p[(int64_t)i * a.G];
+            u += t.x, v += t.y;
         }
+        u = lanes_sum(u, 32);
+        v = lanes_sum(v, 32);
+        if (lane == 0) sm[2 * g] = u * inv, sm[2 * g + 1] = v * inv;
+    }
+    __syncthreads();
+    if (!k.on) return;
+    const Groups<V> gr(k.c, a.Cg);
+    Vals<V> mean, r, s1, s2;
+    const float2* s = reinterpret_cast<const float2*>(a.stats) + (int64_t)k.b * a.G + k.g0;
+    mean.make([&](int i) { return -__ldg(s + gr.g[i]).x; });
+    r.make([&](int i) { return __ldg(s + gr.g[i]).y; });
+    s1.make([&](int i) { return sm[2 * gr.g[i]]; });
+    s2.make([&](int i) { return sm[2 * gr.g[i] + 1]; });
+    const Vals<V> w = weights_of<T, V>(a.w, k.c0 + k.c, true, 1.f), b = weights_of<T, V>(a.b, k.c0 + k.c, true, 0.f);
+    for (int i = 0; row < k.n1; ++i, row += k.subs) {
+        ring.template wait<kRows - 2>();
+        fetch(i + kRows - 1, row + (kRows - 1) * k.subs);
+        const Vals<V> xh = (ring.get((i % kRows) * 3, x + row * a.x_ts) + mean) * r;
+        Vals<V> zf = xh;
+        if (gate) zf = ring.get((i % kRows) * 3 + 2, z + row * a.z_ts);
+        const Vals<V> h = backward(fma(xh, w, b), ring.get((i % kRows) * 3 + 1, d + row * a.dy_ts), act, gate, zf);
+        store<T, V>(y + row * a.y_ts, fma(xh, s2, fma(h, w, s1)) * r);
+        if (gate) store<T, V>(dz + row * a.dz_ts, zf);
     }
 }
 
 // ------------------------------------------------------------------ host side
 
 // Blocks of the one-token backward at most, each of which leaves its sums.
-int row_blocks() { return 4 * tcc::sm_count(); }
+int row_blocks() { return 2 * tcc::sm_count(); }
 
-// Rows of a block of the other form: at least 16, and so many that there are about four
-// blocks for every SM.
-void cut_rows(int B, int N, int* per, int* chunks) {
-    const int64_t want = (4LL * tcc::sm_count() + B - 1) / B;
+// Rows of a block of the other form: at least 16, and so many that the blocks run at once, as
+// many on an SM as its registers hold (a second wave for a few of them would cost as much
+// as the first).
+constexpr int kMostPerSm = 3;
+void cut_rows(int B, int N, int per_sm, int* per, int* chunks) {
+    int64_t want = (int64_t)per_sm * tcc::sm_count() / B;
+    want = want < 1 ? 1 : want;
     int64_t p = (N + want - 1) / want;
     p = p < 16 ? 16 : p;
     *per = (int)p;
@@ -652,49 +804,81 @@ int lanes_of(int Cg, int V, int K) {
     return n;
 }
 
-template <typename T, int V, int K, bool kBackward>
+template <typename T, int V, int K, int kL, bool kBackward>
 cudaError_t launch_rows(NormArgs a, cudaStream_t st) {
-    a.lanes = lanes_of(a.Cg, V, K);
+    static std::atomic<int> optin[tcc::kMaxDevices];
+    a.lanes = kL ? kL : lanes_of(a.Cg, V, K);
     a.slots = a.G * a.lanes;
-    constexpr int kU = kBackward ? (K == 1 ? 2 : 1) : (K == 1 ? 4 : K == 2 ? 2 : 1);
     const int R = a.slots <= kThreads ? kThreads / a.slots : 1;
-    const int64_t tiles = ((int64_t)a.B + R * kU - 1) / (R * kU);
+    // Whole rows where every thread has to have values.
+    const int threads = kL && a.slots <= kThreads ? R * a.slots : kThreads;
+    const int64_t tiles = ((int64_t)a.B + R - 1) / R;
     const unsigned columns = (unsigned)((a.slots + kThreads - 1) / kThreads);
+    constexpr int ring = V > 1 ? kStages<K> * (kBackward ? 3 : 2) * K * kThreads * 16 : 0;
+    constexpr int sums = kBackward ? kThreads * V * 4 : 0, smem = ring > sums ? ring : sums;
+    cudaError_t e;
     if constexpr (!kBackward) {
-        const int64_t most = 8LL * tcc::sm_count();
-        rows_fwd_kernel<T, V, K, kU><<<dim3((unsigned)(tiles < most ? tiles : most), columns), kThreads, 0, st>>>(a);
+        if ((e = tcc::ensure_smem_optin(rows_fwd_kernel<T, V, K, kL>, smem, optin)) != cudaSuccess) return e;
+        const int64_t most = 3LL * tcc::sm_count();
+        rows_fwd_kernel<T, V, K, kL><<<dim3((unsigned)(tiles < most ? tiles : most), columns), threads, smem, st>>>(a);
         return cudaPeekAtLastError();
     } else {
+        if ((e = tcc::ensure_smem_optin(rows_bwd_kernel<T, V, K, kL>, smem, optin)) != cudaSuccess) return e;
         const int64_t most = row_blocks(), blocks = tiles < most ? tiles : most;
-        rows_bwd_kernel<T, V, K, kU><<<dim3((unsigned)blocks, columns), kThreads, 0, st>>>(a);
-        cudaError_t e = cudaPeekAtLastError();
-        if (e != cudaSuccess || (!a.dw && !a.db)) return e;
-        return scan::launch_after(weights_kernel, dim3((a.C + 31) / 32, 2), 256, 0, st, true, a.partial, a.dw, a.db, blocks, a.C);
+        rows_bwd_kernel<T, V, K, kL><<<dim3((unsigned)blocks, columns), threads, smem, st>>>(a);
+        if ((e = cudaPeekAtLastError()) != cudaSuccess || (!a.dw && !a.db)) return e;
+        return scan::launch_after(weights_kernel, dim3((a.C + 31) / 32, 2), 1024, 0, st, true, a.partial, a.dw, a.db, blocks, a.C);
     }
+}
+
+// Groups of 4 V, 8 V, 16 V or 32 V channels whose slots fill whole blocks.
+template <typename T, int V, bool kBackward>
+bool launch_exact(const NormArgs& a, cudaStream_t st, cudaError_t* e) {
+    if (a.Cg % V) return false;
+    const int lanes = a.Cg / V;
+    const int64_t slots = (int64_t)a.G * lanes;
+    if (slots > kThreads ? slots % kThreads != 0 : (kThreads / slots) * slots % 32 != 0) return false;
+    switch (lanes) {
+        case 4: *e = launch_rows<T, V, 1, 4, kBackward>(a, st); return true;
+        case 8: *e = launch_rows<T, V, 1, 8, kBackward>(a, st); return true;
+        case 16: *e = launch_rows<T, V, 1, 16, kBackward>(a, st); return true;
+        case 32: *e = launch_rows<T, V, 1, 32, kBackward>(a, st); return true;
+    }
+    return false;
 }
 
 template <typename T, int V, bool kBackward>
 cudaError_t launch_blocks(NormArgs a, cudaStream_t st) {
-    cut_rows(a.B, a.N, &a.per, &a.chunks);
+    cut_rows(a.B, a.N, kBackward && V == 8 ? 2 : kMostPerSm, &a.per, &a.chunks);
     // Whole groups per block, whole vectors: as many as its threads hold.
     const int unit = V / gcd(a.Cg, V), hold = (V == 1 ? kMost : kThreads) * V / a.Cg;
     a.gb = hold >= a.G ? a.G : hold / unit * unit;
     const int threads = V == 1 && a.gb * a.Cg > kThreads ? kMost : kThreads;
     const int subs = threads / (a.gb * a.Cg / V);
     const dim3 grid((unsigned)(a.B * a.chunks), (unsigned)((a.G + a.gb - 1) / a.gb));
-    const size_t sums = 2 * sizeof(float) * (size_t)subs * a.gb * a.Cg, group = 2 * sizeof(float) * (size_t)a.gb;
+    const int sums = 2 * (int)sizeof(float) * subs * a.gb * a.Cg, group = 2 * (int)sizeof(float) * a.gb;
+    auto ring = [&](int places) { return V > 1 ? places * threads * 16 : 0; };
+    auto larger = [](int p, int q) { return p > q ? p : q; };
+    static std::atomic<int> optin[2][tcc::kMaxDevices];
+    constexpr int kMostRing = V > 1 ? 2 * kTileRows * kThreads * 16 : 0, kMostSums = 2 * 4 * kThreads * V * (V == 1 ? 4 : 1);
+    cudaError_t e;
     if constexpr (!kBackward) {
-        stats_kernel<T, V><<<grid, threads, sums, st>>>(a);
-        const cudaError_t e = cudaPeekAtLastError();
-        return e != cudaSuccess ? e : scan::launch_after(apply_kernel<T, V>, grid, threads, group, st, true, a);
+        if ((e = tcc::ensure_smem_optin(stats_kernel<T, V>, kMostRing + kMostSums, optin[0])) != cudaSuccess ||
+            (e = tcc::ensure_smem_optin(apply_kernel<T, V>, kMostRing + kMostSums, optin[1])) != cudaSuccess)
+            return e;
+        stats_kernel<T, V><<<grid, threads, larger(ring(2 * kTileRows), sums), st>>>(a);
+        if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
+        return scan::launch_after(apply_kernel<T, V>, grid, threads, ring(2 * kRows) + group, st, true, a);
     } else {
-        sums_kernel<T, V><<<grid, threads, sums, st>>>(a);
-        cudaError_t e = cudaPeekAtLastError();
-        if (e != cudaSuccess) return e;
-        if ((e = scan::launch_after(apply_bwd_kernel<T, V>, grid, threads, group, st, true, a)) != cudaSuccess ||
+        if ((e = tcc::ensure_smem_optin(sums_kernel<T, V>, kMostRing + kMostSums, optin[0])) != cudaSuccess ||
+            (e = tcc::ensure_smem_optin(apply_bwd_kernel<T, V>, kMostRing + kMostSums, optin[1])) != cudaSuccess)
+            return e;
+        sums_kernel<T, V><<<grid, threads, larger(ring(3 * kRows), sums), st>>>(a);
+        if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
+        if ((e = scan::launch_after(apply_bwd_kernel<T, V>, grid, threads, ring(3 * kRows) + group, st, true, a)) != cudaSuccess ||
             (!a.dw && !a.db))
             return e;
-        return scan::launch_after(weights_kernel, dim3((a.C + 31) / 32, 2), 256, 0, st, true, a.partial, a.dw, a.db,
+        return scan::launch_after(weights_kernel, dim3((a.C + 31) / 32, 2), 1024, 0, st, true, a.partial, a.dw, a.db,
                                   (int64_t)a.B * a.chunks, a.C);
     }
 }
@@ -704,9 +888,11 @@ template <typename T, bool kBackward>
 cudaError_t launch_norm(const NormArgs& a, bool aligned, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     if (a.N == 1) {
-        if (aligned && lanes_of(a.Cg, V, 1)) return launch_rows<T, V, 1, kBackward>(a, st);
-        if (aligned && a.Cg % V == 0) return launch_rows<T, V, kMost / (32 * V), kBackward>(a, st);
-        return launch_rows<T, 1, kNarrow / 32, kBackward>(a, st);
+        cudaError_t e;
+        if (aligned && launch_exact<T, V, kBackward>(a, st, &e)) return e;
+        if (aligned && lanes_of(a.Cg, V, 1)) return launch_rows<T, V, 1, 0, kBackward>(a, st);
+        if (aligned && a.Cg % V == 0) return launch_rows<T, V, kMost / (32 * V), 0, kBackward>(a, st);
+        return launch_rows<T, 1, kNarrow / 32, 0, kBackward>(a, st);
     }
     const int unit = V / gcd(a.Cg, V);
     const bool whole = a.G * a.Cg <= kThreads * V || kThreads * V / a.Cg >= unit;
@@ -723,7 +909,7 @@ la_status check_norm(int B, int N, int C, int G, la_dtype dt, float eps) {
 size_t norm_workspace(int B, int N, int C, int G) {
     if (B == 0 || N == 0) return 0;
     int per, chunks;
-    cut_rows(B, N, &per, &chunks);
+    cut_rows(B, N, kMostPerSm, &per, &chunks);
     const size_t blocks = sizeof(float) * (size_t)B * chunks * (2 * (size_t)C + 2 * (size_t)G);
     const size_t rows = sizeof(float) * 2 * (size_t)row_blocks() * C;
     return ((N == 1 ? rows : blocks) + 255) & ~(size_t)255;
