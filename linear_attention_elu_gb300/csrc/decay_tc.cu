@@ -56,9 +56,12 @@ constexpr uint32_t kTile = kTileBytes;         // [128 tokens x 64] bf16
 constexpr int kWork = 8;                       // working warps of a unit
 constexpr int kNone = 0x7fffffff;
 
-// TMEM columns: scores, P of each 32 of them over their first 16; per unit the sums of (4),
-// then (3)'s part of the output, and (2)'s part.
-constexpr uint32_t kTmP = 0, kTmX = 128, kTmO2 = 192, kTmUnit = 128;
+// TMEM columns: scores, P of each 32 of them over their first 16; per unit (64 columns on) the
+// sums of (4), (3)'s part of the output and (2)'s part. With one unit, whose CTA leaves half of
+// TMEM to another, (3) takes the columns of (4).
+template <int kU> struct Tm {
+    static constexpr uint32_t kP = 0, kSt = 128, kO1 = kU == 1 ? 128 : 256, kO2 = kU == 1 ? 192 : 384;
+};
 
 struct Misc {
     uint64_t a_full, b_full, c_full[2], p_full, s_full, o_full;
@@ -97,7 +100,6 @@ static_assert(SumSmem<2, 2, 2>::kBytes <= 227 * 1024 && SumSmem<1, 2, 3>::kBytes
 
 // Coordinate factors of the tensor maps: 0 for an axis of stride 0, whose map has one entry.
 struct Geo {
-    int cps;                    // chunks per segment
     uint8_t ah, ab, bh, bb, ch, cb;
     uint8_t late;               // the launch before it is not waited for until this one's end: it
                                 // started after that launch had seen the chained seeds
@@ -150,11 +152,12 @@ __device__ __forceinline__ uint64_t kmajor_step(uint64_t d, int k) {
     return step_desc(d, (k >> 2) * kTile + (k & 3) * 32);
 }
 
-// (4), the smallest terms first. The second 64-row atom of the A operand is the tile after
-// B's (for kT = 1 whatever tile follows: those lanes are unused).
-template <int kTerms>
-__device__ __forceinline__ void issue_state(uint32_t dst, uint64_t bt, uint64_t w) {
-    constexpr uint32_t id = idesc_bf16_f32(128, 64, true, true);
+// (4), the smallest terms first, for kU units side by side (a unit's terms follow one another). The second 64-row atom of the A operand is the tile after B's (for kT = 1 whatever
+// tile follows: those lanes are unused).
+template <int kU, int kTerms>
+__device__ __forceinline__ void issue_state(uint32_t dst, uint64_t bt, uint32_t w_tile) {
+    constexpr uint32_t id = idesc_bf16_f32(128, 64 * kU, true, true);
+    const uint64_t w = smem_desc(w_tile, kTerms * kTile, 1024, kSwizzle128B);
 #pragma unroll
     for (int part = kTerms - 1; part >= 0; --part)
 #pragma unroll
@@ -167,7 +170,7 @@ struct Place {
     int b, h, col0, seg, n, nch, v0, nc;
     template <bool kRev> __device__ int chunk(int i) const { return kRev ? nch - 1 - v0 - i : v0 + i; }
 };
-__device__ __forceinline__ Place place(const Args& a, const Geo& geo, int units, int bh) {
+__device__ __forceinline__ Place place(const Args& a, int chunks, int units, int bh) {   // chunks of a segment, or a part
     Place p;
     p.b = bh / a.H;
     p.h = bh - p.b * a.H;
@@ -175,8 +178,8 @@ __device__ __forceinline__ Place place(const Args& a, const Geo& geo, int units,
     p.seg = blockIdx.y;
     p.n = tokens_of(a, p.b);
     p.nch = (p.n + kC - 1) / kC;
-    p.v0 = p.seg * geo.cps;
-    p.nc = min(max(p.nch - p.v0, 0), geo.cps);
+    p.v0 = p.seg * chunks;
+    p.nc = min(max(p.nch - p.v0, 0), chunks);
     return p;
 }
 
@@ -265,6 +268,47 @@ template <int kPieces = 4> __device__ __forceinline__ void clear_pieces(uint8_t*
 #pragma unroll
     for (int j = j0; j < j0 + kPieces; ++j)
         *reinterpret_cast<uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+}
+
+// kCols columns from c0 of row `row` of a matrix of states [Da, Dc] (transposed: of its transpose).
+template <int kCols>
+__device__ __forceinline__ void load_state(const Args& a, const float* from, int row, int c0, float (&v)[kCols]) {
+#pragma unroll
+    for (int k = 0; k < kCols; k += 4) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < a.Da && c0 + k < a.Dc) {
+            if (a.seeds_t) {
+                const float* t = from + (int64_t)(c0 + k) * a.Da + row;
+                x = make_float4(t[0], t[a.Da], t[2 * a.Da], t[3 * a.Da]);
+            } else {
+                x = *reinterpret_cast<const float4*>(from + (int64_t)row * a.Dc + c0 + k);
+            }
+        }
+        v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
+    }
+}
+
+// The state before a segment: S0, or what the chaining left, or the parts before it joined here.
+template <int kCols>
+__device__ __forceinline__ void start_state(const Args& a, const Place& pl, float l, int row, int c0, float (&st)[kCols]) {
+    const int64_t bh = (int64_t)pl.b * a.H + pl.h, state = (int64_t)a.Da * a.Dc;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) st[k] = 0.f;
+    const bool chained = a.nseg > 1 && !a.fold;
+    const float* from = chained ? a.seeds + (bh * a.parts + pl.seg * a.nsub) * state : (a.S0 ? a.S0 + bh * state : nullptr);
+    if (from) load_state(a, from, row, c0, st);
+    if (!a.fold) return;
+    const int n = a.rev ? pl.nch * kC : pl.n;
+#pragma unroll 1
+    for (int i = 0; i < pl.seg * a.nsub; ++i) {
+        const int m = part_tokens(a, n, i);
+        if (m == 0) break;
+        float v[kCols];
+        load_state(a, a.seeds + (bh * a.parts + i) * state, row, c0, v);
+        const Factor f = factor((float)m * log_decay(l));
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) st[k] = fmaf(f.hi, st[k], fmaf(f.lo, st[k], v[k]));
+    }
 }
 
 // Decay factors of a warp's rows, for every chunk.
@@ -384,13 +428,14 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                 const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap omap,
                 const __grid_constant__ Args a, const __grid_constant__ Geo geo, WsHeader* hdr) {
     using L = Smem<kT, kU, kTerms>;
+    using M = Tm<kU>;
     constexpr int kWarps = kU * kWork;
     constexpr uint32_t kCols = kU == 1 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t base[];
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, geo, kU, blockIdx.z);
+    const Place pl = place(a, a.seg_len / kC, kU, blockIdx.z);
     const bool returns = a.S_out && pl.seg == a.nseg - 1;
     // The seeds, where there are segments. A dependent launch never ends before what it follows.
     if (!geo.late || (pl.nc == 0 && !returns)) pdl_wait();
@@ -427,9 +472,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             const uint32_t base_a = smem_u32(base);
             const uint64_t ak = kmajor_desc(base_a + L::kA), bk = kmajor_desc(base_a + L::kB);
             const uint64_t br = rows_desc(base_a + L::kB), cr = rows_desc(base_a + L::kC0);
-            const uint64_t sr = rows_desc(base_a + L::kS), wr = rows_desc(base_a + L::kW);
+            const uint64_t sr = smem_desc(base_a + L::kS, kT * kTile / 2, 1024, kSwizzle128B);   // units side by side
             constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true);
+            constexpr uint32_t id_o = idesc_bf16_f32(128, 64 * kU, false, true);
             int nab = 0, nc = 0;               // chunks of A and B, of C asked for
             auto load_ab = [&]() {
                 if (hold) return;
@@ -441,7 +486,14 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                     tma_load_4d(base + L::kA + k * kTile, &amap, &m.a_full, 64 * k, geo.ah * pl.h, t, geo.ab * pl.b);
                     tma_load_4d(base + L::kB + k * kTile, &bmap, &m.b_full, 64 * k, geo.bh * pl.h, t, geo.bb * pl.b);
                 }
-                ++nab;
+                if (++nab < pl.nc) {               // the chunk after it comes to L2 ahead of its load
+                    const int next = pl.chunk<kRev>(nab) * kC;
+#pragma unroll
+                    for (int k = 0; k < kT; ++k) {
+                        tma_prefetch_4d(&amap, 64 * k, geo.ah * pl.h, next, geo.ab * pl.b);
+                        tma_prefetch_4d(&bmap, 64 * k, geo.bh * pl.h, next, geo.bb * pl.b);
+                    }
+                }
             };
             auto load_c = [&]() {
                 if (hold) return;
@@ -450,13 +502,16 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                 mbar_arrive_expect_tx(bar, kU * kTile);
 #pragma unroll
                 for (int u = 0; u < kU; ++u) tma_load_4d(ctile(nc, u), &cmap, bar, pl.col0 + 64 * u, geo.ch * pl.h, t, geo.cb * pl.b);
-                ++nc;
+                if (++nc < pl.nc)
+#pragma unroll
+                    for (int u = 0; u < kU; ++u)
+                        tma_prefetch_4d(&cmap, pl.col0 + 64 * u, geo.ch * pl.h, pl.chunk<kRev>(nc) * kC, geo.cb * pl.b);
             };
             auto scores = [&](int i) -> bool {                                                          // (1)
                 if (!mbar_wait(&m.a_full, i & 1, max_spin) || !mbar_wait(&m.b_full, i & 1, max_spin)) return false;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4 * kT; ++k) mma_bf16(tmem + kTmP, kmajor_step(ak, k), kmajor_step(bk, k), id_sc, k > 0);
+                for (int k = 0; k < 4 * kT; ++k) mma_bf16(tmem + M::kP, kmajor_step(ak, k), kmajor_step(bk, k), id_sc, k > 0);
                 mma_commit(&m.p_full);
                 return true;
             };
@@ -484,14 +539,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                 if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int u = 0; u < kU; ++u)
-#pragma unroll
-                    for (int k = 0; k < 4 * kT; ++k)                                                    // (2)
-                        mma_bf16(tmem + kTmO2 + kTmUnit * u, kmajor_step(ak, k),
-                                 step_desc(sr, u * kT * kTile / 2 + k * 2048), id_o, k > 0);
-#pragma unroll
-                for (int u = 0; u < kU; ++u)                                                            // (4)
-                    issue_state<kTerms>(tmem + kTmX + kTmUnit * u, br, step_desc(wr, u * kTerms * kTile));
+                for (int k = 0; k < 4 * kT; ++k)                                                        // (2)
+                    mma_bf16(tmem + M::kO2, kmajor_step(ak, k), step_desc(sr, k * 2048), id_o, k > 0);
+                issue_state<kU, kTerms>(tmem + M::kSt, br, base_a + L::kW);                             // (4)
                 mma_commit(&m.s_full);
                 if (L::kStages == 2 && i > 0 && i + 1 < pl.nc) {
                     tma_store_wait_read<0>();
@@ -502,11 +552,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                 if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int u = 0; u < kU; ++u)
-#pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)                                                   // (3)
-                        mma_bf16_ts(tmem + kTmX + kTmUnit * u, tmem + kTmP + 32 * (k >> 1) + 8 * (k & 1),
-                                    step_desc(cr, (s * kU + u) * kTile + k * 2048), id_o, k > 0);
+                for (int k = 0; k < kC / 16; ++k)                                                       // (3)
+                    mma_bf16_ts(tmem + M::kO1, tmem + M::kP + 32 * (k >> 1) + 8 * (k & 1),
+                                step_desc(cr, s * kU * kTile + k * 2048), id_o, k > 0);
                 mma_commit(&m.o_full);
                 if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
                 if (i + 1 < pl.nc && !(ok = scores(i + 1))) break;
@@ -527,7 +575,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     } else {
         const int q = warp & 3, g4 = warp >> 2, u = g4 >> 1, g = g4 & 1, row = 32 * q + lane;
         const int qm = kRev ? 3 - q : q, im = kRev ? 127 - row : row;
-        const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16), tmu = tm + kTmUnit * u + 32 * g;
+        const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16), tmu = tm + 64 * u + 32 * g;
         const bool has_state = q < 2 * kT;
         const int64_t state = (int64_t)a.Da * a.Dc, bh = (int64_t)pl.b * a.H + pl.h;
         const RowFactors rf = row_factors(l2, im);
@@ -535,33 +583,18 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         // State row `row`, columns col0 + 64 u + 32 g ..
         float st[32];
         const int c0 = pl.col0 + 64 * u + 32 * g;
-        const float* from = a.nseg > 1 ? a.seeds + (bh * a.nseg + pl.seg) * state : (a.S0 ? a.S0 + bh * state : nullptr);
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (has_state && from && row < a.Da && c0 + k < a.Dc) {
-                if (a.seeds_t) {
-                    const float* t = from + (int64_t)(c0 + k) * a.Da + row;
-                    v = make_float4(t[0], t[a.Da], t[2 * a.Da], t[3 * a.Da]);
-                } else {
-                    v = *reinterpret_cast<const float4*>(from + (int64_t)row * a.Dc + c0 + k);
-                }
-            }
-            st[k] = v.x, st[k + 1] = v.y, st[k + 2] = v.z, st[k + 3] = v.w;
-        }
+        if (has_state) start_state(a, pl, l, row, c0, st);
         const float read = a.scale * pow2((float)(im + 1) * l2);   // weight of the state in this row's output
         const Factor whole = factor(kC * log_decay(l));
-        for (int i = 0; i < pl.nc; ++i) {
-            const int t0 = pl.chunk<kRev>(i) * kC, mt = min(kC, pl.n - t0), s = i % L::kStages, ph = (i / L::kStages) & 1;
+        // w C of a chunk, once C is there. Rows past the sequence's end are cleared in C, and in B
+        // for (4). (Past N the loads filled zeros.) (1) may read such rows of B, whose scores take
+        // no part.
+        auto weigh = [&](int i) -> bool {
+            const int mt = min(kC, pl.n - pl.chunk<kRev>(i) * kC);
             uint8_t* ct = ctile(i, u);
-            // ---------------------------------------------------- state to bf16, w C
-            if (has_state) write_state(s_tile, st, row, 4 * g);
-            if (!(ok = warp_wait(&m.c_full[s], ph, max_spin))) break;
-            // Rows past the sequence's end are cleared in C, and in B for (4). (Past N the loads
-            // filled zeros.) (1) may read such rows of B, whose scores take no part.
-            const bool ragged = mt < kC && pl.n < a.N;
-            if (ragged) {
-                if (!(ok = warp_wait(&m.b_full, i & 1, max_spin))) break;
+            if (!warp_wait(&m.c_full[i % L::kStages], (i / L::kStages) & 1, max_spin)) return false;
+            if (mt < kC && pl.n < a.N) {
+                if (!warp_wait(&m.b_full, i & 1, max_spin)) return false;
                 if (row >= mt) {
                     clear_pieces(ct, row, 4 * g);
                     for (int k = 0; k < kT; ++k) clear_pieces(base + L::kB + k * kTile, row, 4 * g);
@@ -569,6 +602,16 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             }
             const float w = pow2((float)(kRev ? row : max(mt - 1 - row, 0)) * l2);
             if (!write_weighted<kTerms>(ct, terms, w, row, 4 * g)) take_out(ct, row, 32 * g, 32 * g + 32, i * kC + im, &m.any, m.first + 64 * u);
+            return true;
+        };
+        if (L::kStages == 2 && pl.nc > 0) ok = weigh(0);
+        for (int i = 0; i < pl.nc && ok; ++i) {
+            const int t0 = pl.chunk<kRev>(i) * kC, mt = min(kC, pl.n - t0);
+            const bool ragged = mt < kC && pl.n < a.N;
+            uint8_t* ct = ctile(i, u);
+            // ---------------------------------------------------- state to bf16, w C
+            if (has_state) write_state(s_tile, st, row, 4 * g);
+            if (L::kStages == 1 && !(ok = weigh(i))) break;
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
@@ -577,14 +620,20 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             tc_fence_after();
 #pragma unroll 1
             for (int bm = g4; bm < 4; bm += 2 * kU)
-                scores_to_p<kRev>(tm + kTmP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
+                scores_to_p<kRev>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
+            auto hand_over = [&]() {
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(&m.pt);
+            };
+            if (kU > 1) hand_over();
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
-            if (has_state) join_state(tmu + kTmX, kRev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&m.pt);
+            if (has_state) join_state(tmu + M::kSt, kRev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
+            if (kU == 1) hand_over();              // (3) takes the columns of (4)
+            // ---------------------------------------------------- the next w C, under (3)
+            if (L::kStages == 2 && i + 1 < pl.nc && !(ok = weigh(i + 1))) break;
             // ---------------------------------------------------- output
             if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
             tc_fence_after();
@@ -592,7 +641,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint4 x, y;
-                join_output(tmu + kTmX + 16 * k, tmu + kTmO2 + 16 * k, a.scale, read, &x, &y);
+                join_output(tmu + M::kO1 + 16 * k, tmu + M::kO2 + 16 * k, a.scale, read, &x, &y);
                 if (spoiled) {
                     const int* first = m.first + 64 * u + 32 * g + 16 * k;
                     x = put_nan(first, i * kC + im, x);
@@ -628,7 +677,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     if (warp == kWarps) tmem_dealloc(tmem, kCols);
 }
 
-// First pass, of one sum or two: a segment's end state from zero (every segment but the last).
+// First pass, of one sum or two: the end state from zero of each part before the last segment.
 template <int kT, int kU, int kTerms>
 __global__ void __launch_bounds__(32 * (kU * kWork + 1), SumSmem<kT, kU, kTerms>::kPerSm)
 decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_constant__ CUtensorMap cmap0,
@@ -646,11 +695,11 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
     auto btile = [&](int i) { return base + L::kB + (i % L::kStages) * kT * kTile; };
     auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, geo, kU, blockIdx.z - (second ? a0.B * a0.H : 0));
+    const Place pl = place(a, a.seg_len / a.nsub / kC, kU, blockIdx.z - (second ? a0.B * a0.H : 0));
     const bool rev = a.rev != 0;
     auto chunk = [&](int i) { return rev ? pl.chunk<true>(i) : pl.chunk<false>(i); };
     pdl_launch_dependents();
-    if (pl.nc == 0 || pl.seg >= a.nseg - 1) return;    // the chaining leaves such segments out
+    if (pl.nc == 0 || pl.seg >= a.parts - 1) return;   // parts without tokens are not read
     if ((smem_u32(base) & 1023) != 0) {
         if (tid == 0) set_status(hdr, LA_ERR_CUDA);
         return;
@@ -677,7 +726,7 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
     bool ok = true;
     if (warp == kWarps) {
         if (lane == 0) {
-            const uint64_t br = rows_desc(smem_u32(base) + L::kB), wr = rows_desc(smem_u32(base) + L::kW);
+            const uint64_t br = rows_desc(smem_u32(base) + L::kB);
             int n = 0;
             auto load = [&]() {
                 if (hold) return;
@@ -688,15 +737,19 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
                 for (int u = 0; u < kU; ++u) tma_load_4d(ctile(n, u), &cmap, bar, pl.col0 + 64 * u, geo.ch * pl.h, t, geo.cb * pl.b);
 #pragma unroll
                 for (int k = 0; k < kT; ++k) tma_load_4d(btile(n) + k * kTile, &bmap, bar, 64 * k, geo.bh * pl.h, t, geo.bb * pl.b);
-                ++n;
+                if (++n + 1 < pl.nc) {             // the chunk after the next comes to L2 ahead of its load
+                    const int later = chunk(n + 1) * kC;
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) tma_prefetch_4d(&cmap, pl.col0 + 64 * u, geo.ch * pl.h, later, geo.cb * pl.b);
+#pragma unroll
+                    for (int k = 0; k < kT; ++k) tma_prefetch_4d(&bmap, 64 * k, geo.bh * pl.h, later, geo.bb * pl.b);
+                }
             };
             for (int s = 0; s < L::kStages && s < pl.nc; ++s) load();
             for (int i = 0; i < pl.nc; ++i) {
                 if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
                 tc_fence_after();
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    issue_state<kTerms>(tmem + 64 * u, step_desc(br, (i % L::kStages) * kT * kTile), step_desc(wr, u * kTerms * kTile));
+                issue_state<kU, kTerms>(tmem, step_desc(br, (i % L::kStages) * kT * kTile), smem_u32(base) + L::kW);
                 mma_commit(&m.s_full);
                 if (!(ok = mbar_wait(&m.s_full, i & 1, max_spin))) break;
                 if (i + L::kStages < pl.nc) load();
@@ -733,7 +786,7 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
                            rev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
         }
         const int c0 = pl.col0 + 64 * u + 32 * g;
-        float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc + (int64_t)row * a.Dc + c0;
+        float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.parts + pl.seg) * a.Da * a.Dc + (int64_t)row * a.Dc + c0;
         if (ok && has_state && row < a.Da)
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
@@ -773,7 +826,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto tile = [&](int i, int k) { return base + ((i & 1) * 4 + k) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, geo, 1, blockIdx.z);
+    const Place pl = place(a, a.seg_len / kC, 1, blockIdx.z);
     if (pl.nc == 0) {
         pdl_wait();
         return;
@@ -807,7 +860,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
         if (lane == 0) {
             const uint32_t base_a = smem_u32(base);
             const uint64_t km = kmajor_desc(base_a), rows = rows_desc(base_a);
-            const uint64_t sr = rows_desc(base_a + L::kS), sk = kmajor_desc(base_a + L::kS), wr = rows_desc(base_a + L::kW);
+            const uint64_t sr = rows_desc(base_a + L::kS), sk = kmajor_desc(base_a + L::kS);
             constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true), id_t = idesc_bf16_f32(128, 64, false, false);
             int n = 0;
@@ -820,7 +873,13 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
                 tma_load_4d(tile(n, kTileQ), &maps.in[kTileQ], bar, 0, geo.bh * pl.h, t, geo.bb * pl.b);
                 tma_load_4d(tile(n, kTileV), &maps.in[kTileV], bar, 0, vgeo.ah * pl.h, t, vgeo.ab * pl.b);
                 tma_load_4d(tile(n, kTileG), &maps.in[kTileG], bar, 0, geo.ch * pl.h, t, geo.cb * pl.b);
-                ++n;
+                if (++n + 1 < pl.nc) {             // the chunk after the next comes to L2 ahead of its load
+                    const int next = pl.chunk<true>(n + 1) * kC;
+                    tma_prefetch_4d(&maps.in[kTileK], 0, geo.ah * pl.h, next, geo.ab * pl.b);
+                    tma_prefetch_4d(&maps.in[kTileQ], 0, geo.bh * pl.h, next, geo.bb * pl.b);
+                    tma_prefetch_4d(&maps.in[kTileV], 0, vgeo.ah * pl.h, next, vgeo.ab * pl.b);
+                    tma_prefetch_4d(&maps.in[kTileG], 0, geo.ch * pl.h, next, geo.cb * pl.b);
+                }
             };
             auto at = [&](uint64_t d, int i, int k) { return step_desc(d, ((i & 1) * 4 + k) * kTile); };
             auto scores = [&](int i) -> bool {                                                          // (1)
@@ -855,7 +914,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
                     mma_bf16(tmem + kKvO2, kmajor_step(at(km, i, kTileK), k), step_desc(sr, k * 2048), id_o, k > 0);
                     mma_bf16(tmem + kKvO2 + 128, kmajor_step(at(km, i, kTileV), k), kmajor_step(sk, k), id_t, k > 0);
                 }
-                issue_state<2>(tmem + kKvX, at(rows, i, kTileQ), wr);                                   // (4)
+                issue_state<1, 2>(tmem + kKvX, at(rows, i, kTileQ), base_a + L::kW);                                   // (4)
                 mma_commit(&m.s_full);
                 if (i > 0 && i + 1 < pl.nc) {          // the next chunk, once the output before this one has left its place
                     tma_store_wait_read<0>();
@@ -887,36 +946,37 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
         const RowFactors rf = row_factors(l2, im);
         // State row `row`, columns 16 g4 ..
         float st[16];
-        const float* from = a.nseg > 1 ? a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc : nullptr;
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (has_state && from && row < a.Da && 16 * g4 + k < a.Dc)
-                v = *reinterpret_cast<const float4*>(from + (int64_t)row * a.Dc + 16 * g4 + k);
-            st[k] = v.x, st[k + 1] = v.y, st[k + 2] = v.z, st[k + 3] = v.w;
-        }
+        if (has_state) start_state(a, pl, l, row, 16 * g4, st);
         const float read = a.scale * pow2((float)(im + 1) * l2), w = pow2((float)row * l2);
         const Factor whole = factor(kC * log_decay(l));
         const Tensor& out = u ? dk : a.o;
         const int width = u ? a.Da : a.Dc;
-        for (int i = 0; i < pl.nc; ++i) {
-            const int t0 = pl.chunk<true>(i) * kC, mt = min(kC, pl.n - t0);
-            uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ), *ct = u ? qt : gt;
-            // ---------------------------------------------------- state to bf16, w dout
-            if (has_state) write_state(base + L::kS, st, row, 2 * g4);
-            if (!(ok = warp_wait(&m.c_full[i & 1], (i >> 1) & 1, max_spin))) break;
-            const bool ragged = mt < kC && pl.n < a.N;
-            if (ragged && row >= mt) {
+        // w dout of a chunk, once its tiles are there; which of its values are finite.
+        bool fine_g = true, fine_q = true;
+        auto weigh = [&](int i) -> bool {
+            const int mt = min(kC, pl.n - pl.chunk<true>(i) * kC);
+            uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ);
+            if (!warp_wait(&m.c_full[i & 1], (i >> 1) & 1, max_spin)) return false;
+            if (mt < kC && pl.n < a.N && row >= mt) {
                 clear_pieces<2>(gt, row, 2 * g4);
                 clear_pieces<2>(qt, row, 2 * g4);
             }
-            const bool fine_g = write_weighted<2, 2>(gt, base + L::kW, w, row, 2 * g4);
-            bool fine_q = true;
+            fine_g = write_weighted<2, 2>(gt, base + L::kW, w, row, 2 * g4);
+            fine_q = true;
 #pragma unroll
             for (int j = 2 * g4; j < 2 * g4 + 2; ++j) {
                 const uint4 x = *reinterpret_cast<const uint4*>(qt + row * 128 + ((j ^ (row & 7)) << 4));
                 for (uint32_t v : {x.x, x.y, x.z, x.w}) fine_q = fine_q && (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
             }
+            return true;
+        };
+        ok = weigh(0);
+        for (int i = 0; i < pl.nc && ok; ++i) {
+            const int t0 = pl.chunk<true>(i) * kC, mt = min(kC, pl.n - t0);
+            const bool ragged = mt < kC && pl.n < a.N;
+            uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ), *ct = u ? qt : gt;
+            // ---------------------------------------------------- state to bf16
+            if (has_state) write_state(base + L::kS, st, row, 2 * g4);
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
@@ -936,6 +996,8 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&m.pt);
+            // ---------------------------------------------------- the next w dout, under (3)
+            if (i + 1 < pl.nc && !(ok = weigh(i + 1))) break;
             // ---------------------------------------------------- output
             if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
             tc_fence_after();
@@ -998,7 +1060,6 @@ struct Sum {
     CUtensorMap am, bm, cm, om;
     bool encode() {
         geo = {};
-        geo.cps = a.seg_len / kC;
         return encode_rows(&am, a.a, a.Da, a.B, a.H, a.N, &geo.ah, &geo.ab) &&
                encode_rows(&bm, a.b, a.Da, a.B, a.H, a.N, &geo.bh, &geo.bb) &&
                encode_rows(&cm, a.c, a.Dc, a.B, a.H, a.N, &geo.ch, &geo.cb) &&
@@ -1014,8 +1075,8 @@ cudaError_t launch_sums(const Sum* s, int count, WsHeader* hdr, cudaStream_t st)
     const cudaError_t e = ensure_smem_optin(decay_sums_kernel<kT, kU, kTerms>, bytes, optin);
     if (e != cudaSuccess) return e;
     const Sum &x = s[0], &y = s[count - 1];
-    const int nseg = x.a.nseg > y.a.nseg ? x.a.nseg : y.a.nseg;
-    const dim3 grid((x.a.Dc + 64 * kU - 1) / (64 * kU), nseg - 1, x.heads() * count);
+    const int parts = x.a.parts > y.a.parts ? x.a.parts : y.a.parts;
+    const dim3 grid((x.a.Dc + 64 * kU - 1) / (64 * kU), parts - 1, x.heads() * count);
     decay_sums_kernel<kT, kU, kTerms><<<grid, 32 * (kU * kWork + 1), bytes, st>>>(x.bm, x.cm, y.bm, y.cm, x.a, x.geo, y.a, y.geo, hdr);
     return cudaPeekAtLastError();
 }
@@ -1060,6 +1121,8 @@ int segments(int64_t BH, int N, int per_sm) {
     }
     return best;
 }
+// Parts that a CTA of the main pass joins itself; more are chained by a launch of their own.
+constexpr int kFold = 6;
 int forward_segments(int64_t BH, int N, int Dk, int Dv) { return segments(BH, N, narrow(Dk, Dv) ? 2 : 1); }
 int reverse_segments(int64_t BH, int N) { return segments(BH, N, 1); }   // of dk and dv, which share their seeds
 
@@ -1080,27 +1143,61 @@ bool tc_supported(const Args& a, la_dtype dt) {
     return rows(a.a, true) && rows(a.b, true) && rows(a.c, true) && rows(a.o, false);
 }
 
+namespace {
+
+// The cuts of a backward pass: S for dq, and R, whose longer segments take parts of about S's
+// length so that the first pass's CTAs end together.
+void cut_backward(Args* dq, Args* dv, int64_t BH, int Dk, int Dv) {
+    cut(dq, forward_segments(BH, dq->N, Dk, Dv), 1, kC);
+    const int nseg = reverse_segments(BH, dv->N);
+    cut(dv, nseg, 1, kC);
+    int nsub = dq->nseg > 1 ? (dv->seg_len + dq->seg_len - 1) / dq->seg_len : 1;
+    while (nsub > 1 && (nseg - 1) * nsub + 1 > 64) --nsub;
+    cut(dv, nseg, nsub, kC);
+    dq->fold = dq->parts - 1 <= kFold && dv->parts - 1 <= kFold;
+    dv->fold = dq->fold;
+}
+void cut_forward(Args* a) {
+    cut(a, forward_segments((int64_t)a->B * a->H, a->N, a->Da, a->Dc), 1, kC);
+    a->fold = a->parts - 1 <= kFold;
+}
+
+size_t seeds_of(const Args& a, int64_t BH, int Dk, int Dv) { return a.nseg > 1 ? (size_t)BH * a.parts * Dk * Dv : 0; }
+
+}  // namespace
+
 size_t tc_seeds(int64_t BH, int N, int Dk, int Dv, bool backward) {
-    const int f = forward_segments(BH, N, Dk, Dv), r = backward ? reverse_segments(BH, N) : 1;
-    return (size_t)BH * Dk * Dv * ((f > 1 ? f : 0) + (r > 1 ? r : 0));
+    Args x = {}, y = {};
+    x.N = y.N = N, x.B = 1, x.H = (int)BH, x.Da = Dk, x.Dc = Dv;
+    if (!backward) {
+        cut_forward(&x);
+        return seeds_of(x, BH, Dk, Dv);
+    }
+    cut_backward(&x, &y, BH, Dk, Dv);
+    return seeds_of(x, BH, Dk, Dv) + seeds_of(y, BH, Dk, Dv);
 }
 
 int tc_launches(int64_t BH, int N, int Dk, int Dv, bool backward) {
-    const bool f = forward_segments(BH, N, Dk, Dv) > 1;
-    if (!backward) return f ? 3 : 1;
-    const bool r = reverse_segments(BH, N) > 1, together = (Dk <= 64) == (Dv <= 64);
-    return (narrow(Dk, Dv) ? 2 : 3) + (f || r ? 1 + (f && r && !together ? 2 : 1) : 0);
+    Args x = {}, y = {};
+    x.N = y.N = N, x.B = 1, x.H = (int)BH, x.Da = Dk, x.Dc = Dv;
+    if (!backward) {
+        cut_forward(&x);
+        return x.nseg == 1 ? 1 : x.fold ? 2 : 3;
+    }
+    cut_backward(&x, &y, BH, Dk, Dv);
+    const bool f = x.nseg > 1, r = y.nseg > 1, together = (Dk <= 64) == (Dv <= 64);
+    return (narrow(Dk, Dv) ? 2 : 3) + (f && r && !together ? 2 : f || r ? 1 : 0) + ((f || r) && !x.fold ? 1 : 0);
 }
 
 cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
-    cut(&a, forward_segments((int64_t)a.B * a.H, a.N, a.Da, a.Dc), kC);
+    cut_forward(&a);
     Sum s = {a};
     if (!s.encode()) return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
     cudaError_t e;
     if (a.nseg > 1) {
         if ((e = a.S_out ? sums_of<3>(&s, 1, hdr, st) : sums_of<2>(&s, 1, hdr, st)) != cudaSuccess) return e;
-        if ((e = launch_chain(&a, 1, kC, st)) != cudaSuccess) return e;
+        if (!a.fold && (e = launch_chain(&a, 1, kC, st)) != cudaSuccess) return e;
     }
     return a.S_out ? main_of<3, false>(s, a.nseg > 1, hdr, st) : main_of<2, false>(s, a.nseg > 1, hdr, st);
 }
@@ -1109,23 +1206,23 @@ cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
 // last two in one pass where the heads are narrow enough for its tiles.
 cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t st) {
     const int64_t BH = (int64_t)dq.B * dq.H;
-    cut(&dq, forward_segments(BH, dq.N, dv.Da, dv.Dc), kC);
-    cut(&dv, reverse_segments(BH, dv.N), kC);
-    dv.seeds = dq.seeds + (dq.nseg > 1 ? (size_t)BH * dq.nseg * dq.Da * dq.Dc : 0);
-    dk.seeds = dv.seeds, dk.nseg = dv.nseg, dk.seg_len = dv.seg_len, dk.seeds_t = 1;
+    cut_backward(&dq, &dv, BH, dv.Da, dv.Dc);
+    dv.seeds = dq.seeds + seeds_of(dq, BH, dq.Da, dq.Dc);
+    dk.seeds = dv.seeds, dk.nseg = dv.nseg, dk.seg_len = dv.seg_len, dk.nsub = dv.nsub, dk.parts = dv.parts;
+    dk.fold = dv.fold, dk.seeds_t = 1;
     Sum s[3] = {{dq}, {dv}, {dk}};
     for (Sum& x : s)
         if (!x.encode()) return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
     cudaError_t e;
     const bool f = dq.nseg > 1, r = dv.nseg > 1;
-    if (f || r) {
-        if (f && r && (dq.Da <= 64) == (dq.Dc <= 64)) {
-            if ((e = sums_of<2>(s, 2, hdr, st)) != cudaSuccess) return e;
-        } else {
-            if (f && (e = sums_of<2>(s, 1, hdr, st)) != cudaSuccess) return e;
-            if (r && (e = sums_of<2>(s + 1, 1, hdr, st)) != cudaSuccess) return e;
-        }
+    if (f && r && (dq.Da <= 64) == (dq.Dc <= 64)) {
+        if ((e = sums_of<2>(s, 2, hdr, st)) != cudaSuccess) return e;
+    } else {
+        if (f && (e = sums_of<2>(s, 1, hdr, st)) != cudaSuccess) return e;
+        if (r && (e = sums_of<2>(s + 1, 1, hdr, st)) != cudaSuccess) return e;
+    }
+    if ((f || r) && !dq.fold) {
         const Args chained[2] = {f ? dq : dv, dv};
         if ((e = launch_chain(chained, f && r ? 2 : 1, kC, st)) != cudaSuccess) return e;
     }
