@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
     tcc::pdl_launch_dependents();
     tcc::pdl_wait();                    // the second pass follows the chaining kernel
     float st[kD][4][4];                 // rows 64 t + 4 ty + i, columns col0 + 4 tx + j
-    const float* from = kState ? nullptr : (a.nseg > 1 ? a.seeds + (bh * a.parts + seg) * state
+    const float* from = kState ? nullptr : (a.nseg > 1 ? a.seeds + (bh * a.nseg + seg) * state
                                                        : (a.S0 ? a.S0 + bh * state : nullptr));
 #pragma unroll
     for (int k = 0; k < kD; ++k)
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
                 for (int j = 0; j < 4; ++j) st[k][i][j] = fmaf(f.hi, st[k][i][j], fmaf(f.lo, st[k][i][j], add[i][j]));
         }
     }
-    float* to = kState ? a.seeds + (bh * a.parts + seg) * state
+    float* to = kState ? a.seeds + (bh * a.nseg + seg) * state
                        : (seg == a.nseg - 1 && a.S_out ? a.S_out + bh * state : nullptr);
     if (to)
 #pragma unroll
@@ -207,22 +207,22 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
                 }
 }
 
-// In place over a head's parts: the end states (from zero) become the states that the parts
-// start from, seed_0 = S0, seed_{i+1} = e^{l tokens_i} seed_i + end_i. A thread chains one
-// element, eight parts in flight.
-constexpr int kMaxParts = 64;
+// In place over a head's segments: the end states (from zero) become the states that the
+// segments start from, seed_0 = S0, seed_{i+1} = e^{l tokens_i} seed_i + end_i. A thread
+// chains one element, eight segments in flight.
+constexpr int kMaxSegments = 64;
 __global__ void __launch_bounds__(128)
 chain_kernel(const __grid_constant__ Args first, const __grid_constant__ Args second, int chunk) {
     const Args& a = blockIdx.z ? second : first;
-    __shared__ Factor f[kMaxParts];
-    __shared__ int empty[kMaxParts];
+    __shared__ Factor f[kMaxSegments];
+    __shared__ int empty[kMaxSegments];
     const int64_t bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
     tcc::pdl_launch_dependents();
     tcc::pdl_wait();
-    if (threadIdx.x < a.parts) {
+    if (threadIdx.x < a.nseg) {
         int n = tokens_of(a, (int)b);
         if (a.rev) n = (n + chunk - 1) / chunk * chunk;
-        const int m = part_tokens(a, n, threadIdx.x);
+        const int m = seg_tokens(a, n, threadIdx.x);
         f[threadIdx.x] = factor(m * log_decay(a.decay[h]));
         empty[threadIdx.x] = m == 0;
     }
@@ -230,18 +230,18 @@ chain_kernel(const __grid_constant__ Args first, const __grid_constant__ Args se
     const int e = blockIdx.x * 128 + threadIdx.x, E = a.Da * a.Dc;
     if (e >= E) return;
     float carry = a.S0 ? a.S0[bh * E + e] : 0.f;
-    float* p = a.seeds + bh * a.parts * E + e;
-    for (int i0 = 0; i0 < a.parts; i0 += 8) {
+    float* p = a.seeds + bh * a.nseg * E + e;
+    for (int i0 = 0; i0 < a.nseg; i0 += 8) {
         float end[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (i0 + u < a.parts - 1 && !empty[i0 + u]) end[u] = p[(int64_t)(i0 + u) * E];
+            if (i0 + u < a.nseg - 1 && !empty[i0 + u]) end[u] = p[(int64_t)(i0 + u) * E];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int i = i0 + u;
-            if (i >= a.parts) break;
+            if (i >= a.nseg) break;
             p[(int64_t)i * E] = carry;
-            if (i < a.parts - 1 && !empty[i]) carry = fmaf(f[i].hi, carry, fmaf(f[i].lo, carry, end[u]));
+            if (i < a.nseg - 1 && !empty[i]) carry = fmaf(f[i].hi, carry, fmaf(f[i].lo, carry, end[u]));
         }
     }
 }
@@ -352,7 +352,7 @@ int simt_segments(int64_t BH, int N, int Da, int Dc) {
     const int64_t most = (N + kL - 1) / kL / 2;
     int64_t n = blocks > 0 ? slots / blocks : 1;
     n = n < most ? n : most;
-    n = n < kMaxParts ? n : kMaxParts;
+    n = n < kMaxSegments ? n : kMaxSegments;
     return n < 2 ? 1 : (int)n;
 }
 
@@ -364,7 +364,7 @@ size_t simt_seeds(int64_t BH, int N, int Da, int Dc) {
 float* seeds_of(void* workspace) { return reinterpret_cast<float*>(static_cast<char*>(workspace) + sizeof(WsHeader)); }
 
 cudaError_t run_cuda_cores(Args a, la_dtype dt, void* workspace, cudaStream_t st) {
-    cut(&a, simt_segments((int64_t)a.B * a.H, a.N, a.Da, a.Dc), 1, kL);
+    cut(&a, simt_segments((int64_t)a.B * a.H, a.N, a.Da, a.Dc), kL);
     a.seeds = seeds_of(workspace);
     return dt == LA_BF16 ? run_simt<__nv_bfloat16>(a, st) : run_simt<float>(a, st);
 }

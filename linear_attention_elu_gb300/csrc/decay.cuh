@@ -27,11 +27,10 @@ struct Args {
     const int32_t* lengths;     // [B] or null
     const float* S0;            // [B, H, Da, Dc] or null
     float* S_out;               // the same or null
-    float* seeds;               // [B H, parts, Da, Dc]: end states of the parts, each from zero; chained: start states
+    float* seeds;               // [B H, nseg, Da, Dc]: the segments' end states from zero; chained: their start states
     int B, H, N, Da, Dc, rev;
     int nseg, seg_len;          // segments and their tokens (a multiple of the chunk)
-    int nsub, parts;            // parts of a segment in the first pass; those before the last segment, and one
-    int fold;                   // the main pass joins the parts before its segment itself: they are not chained
+    int fold;                   // the main pass joins the end states before its segment itself: they are not chained
     int seeds_t;                // seeds are [.., Dc, Da]: those of the sum with b and c exchanged
     float scale;
 };
@@ -72,21 +71,16 @@ __device__ __forceinline__ int tokens_of(const Args& a, int b) {
 // (csrc/decay.cu). chunk: the tensor-core path's states of reversed sums stand at whole chunks.
 cudaError_t launch_chain(const Args* sums, int count, int chunk, cudaStream_t st);
 
-// The cut of a sequence into `nseg` segments or fewer of whole chunks, of nsub parts each.
-inline void cut(Args* a, int nseg, int nsub, int chunk) {
-    const int chunks = (a->N + chunk - 1) / chunk;
-    int per = (chunks + nseg - 1) / nseg;
-    per = (per + nsub - 1) / nsub * nsub;
+// The cut of a sequence into `nseg` segments or fewer of whole chunks.
+inline void cut(Args* a, int nseg, int chunk) {
+    const int chunks = (a->N + chunk - 1) / chunk, per = (chunks + nseg - 1) / nseg;
     a->nseg = (chunks + per - 1) / per;
     a->seg_len = per * chunk;
-    a->nsub = nsub;
-    a->parts = (a->nseg - 1) * nsub + 1;
 }
 
-// Tokens of part i of a sequence that ends after n.
-__device__ __forceinline__ int part_tokens(const Args& a, int n, int i) {
-    const int len = a.seg_len / a.nsub;
-    return min(max(n - i * len, 0), len);
+// Tokens of segment i of a sequence that ends after n.
+__device__ __forceinline__ int seg_tokens(const Args& a, int n, int i) {
+    return min(max(n - i * a.seg_len, 0), a.seg_len);
 }
 
 // Tensor-core path (csrc/decay_tc.cu): whether a sum can take it; one sum; the three sums of

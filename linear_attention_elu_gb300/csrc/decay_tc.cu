@@ -22,7 +22,8 @@
 // row and one of the column; the diagonal blocks take an exponential per score. Every
 // factor's exponent is a count of tokens times l, so none is a difference of larger ones.
 //
-// Schedule. Eight working warps per unit and one warp that issues loads, products and stores.
+// Schedule. Eight working warps per unit, one that issues the products and one for loads and
+// stores.
 // A working warp owns 32 rows and half of a unit's columns. Within a chunk: state to bf16 and
 // w C to shared memory; (2) and (4) run under the step from scores to P; the sums of (4) join
 // the state and (3) takes their TMEM columns; the output is staged where C was. A, B and the
@@ -170,7 +171,7 @@ struct Place {
     int b, h, col0, seg, n, nch, v0, nc;
     template <bool kRev> __device__ int chunk(int i) const { return kRev ? nch - 1 - v0 - i : v0 + i; }
 };
-__device__ __forceinline__ Place place(const Args& a, int chunks, int units, int bh) {   // chunks of a segment, or a part
+__device__ __forceinline__ Place place(const Args& a, int units, int bh) {
     Place p;
     p.b = bh / a.H;
     p.h = bh - p.b * a.H;
@@ -178,8 +179,8 @@ __device__ __forceinline__ Place place(const Args& a, int chunks, int units, int
     p.seg = blockIdx.y;
     p.n = tokens_of(a, p.b);
     p.nch = (p.n + kC - 1) / kC;
-    p.v0 = p.seg * chunks;
-    p.nc = min(max(p.nch - p.v0, 0), chunks);
+    p.v0 = p.seg * (a.seg_len / kC);
+    p.nc = min(max(p.nch - p.v0, 0), a.seg_len / kC);
     return p;
 }
 
@@ -288,23 +289,23 @@ __device__ __forceinline__ void load_state(const Args& a, const float* from, int
     }
 }
 
-// The state before a segment: S0, or what the chaining left, or the parts before it joined here.
+// The state before a segment: S0, or what the chaining left, or the ends of the segments before it joined here.
 template <int kCols>
 __device__ __forceinline__ void start_state(const Args& a, const Place& pl, float l, int row, int c0, float (&st)[kCols]) {
     const int64_t bh = (int64_t)pl.b * a.H + pl.h, state = (int64_t)a.Da * a.Dc;
 #pragma unroll
     for (int k = 0; k < kCols; ++k) st[k] = 0.f;
     const bool chained = a.nseg > 1 && !a.fold;
-    const float* from = chained ? a.seeds + (bh * a.parts + pl.seg * a.nsub) * state : (a.S0 ? a.S0 + bh * state : nullptr);
+    const float* from = chained ? a.seeds + (bh * a.nseg + pl.seg) * state : (a.S0 ? a.S0 + bh * state : nullptr);
     if (from) load_state(a, from, row, c0, st);
     if (!a.fold) return;
     const int n = a.rev ? pl.nch * kC : pl.n;
 #pragma unroll 1
-    for (int i = 0; i < pl.seg * a.nsub; ++i) {
-        const int m = part_tokens(a, n, i);
+    for (int i = 0; i < pl.seg; ++i) {
+        const int m = seg_tokens(a, n, i);
         if (m == 0) break;
         float v[kCols];
-        load_state(a, a.seeds + (bh * a.parts + i) * state, row, c0, v);
+        load_state(a, a.seeds + (bh * a.nseg + i) * state, row, c0, v);
         const Factor f = factor((float)m * log_decay(l));
 #pragma unroll
         for (int k = 0; k < kCols; ++k) st[k] = fmaf(f.hi, st[k], fmaf(f.lo, st[k], v[k]));
@@ -423,7 +424,7 @@ __device__ __forceinline__ RowFactors row_factors(float l2, int im) {
 }
 
 template <int kT, int kU, int kTerms, bool kRev>
-__global__ void __launch_bounds__(32 * (kU * kWork + 1), Smem<kT, kU, kTerms>::kPerSm)
+__global__ void __launch_bounds__(32 * (kU * kWork + 2), Smem<kT, kU, kTerms>::kPerSm)
 decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap omap,
                 const __grid_constant__ Args a, const __grid_constant__ Geo geo, WsHeader* hdr) {
@@ -435,7 +436,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, a.seg_len / kC, kU, blockIdx.z);
+    const Place pl = place(a, kU, blockIdx.z);
     const bool returns = a.S_out && pl.seg == a.nseg - 1;
     // The seeds, where there are segments. A dependent launch never ends before what it follows.
     if (!geo.late || (pl.nc == 0 && !returns)) pdl_wait();
@@ -468,6 +469,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     bool ok = true;
 
     if (warp == kWarps) {
+        // ------------------------------------------------------------ products
         if (lane == 0 && pl.nc > 0) {
             const uint32_t base_a = smem_u32(base);
             const uint64_t ak = kmajor_desc(base_a + L::kA), bk = kmajor_desc(base_a + L::kB);
@@ -475,6 +477,40 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             const uint64_t sr = smem_desc(base_a + L::kS, kT * kTile / 2, 1024, kSwizzle128B);   // units side by side
             constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64 * kU, false, true);
+            auto scores = [&](int i) -> bool {                                                          // (1)
+                if (!mbar_wait(&m.a_full, i & 1, max_spin) || !mbar_wait(&m.b_full, i & 1, max_spin)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4 * kT; ++k) mma_bf16(tmem + M::kP, kmajor_step(ak, k), kmajor_step(bk, k), id_sc, k > 0);
+                mma_commit(&m.p_full);
+                return true;
+            };
+            ok = scores(0);
+            for (int i = 0; i < pl.nc && ok; ++i) {
+                if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4 * kT; ++k)                                                        // (2)
+                    mma_bf16(tmem + M::kO2, kmajor_step(ak, k), step_desc(sr, k * 2048), id_o, k > 0);
+                issue_state<kU, kTerms>(tmem + M::kSt, br, base_a + L::kW);                             // (4)
+                mma_commit(&m.s_full);
+                if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k)                                                       // (3)
+                    mma_bf16_ts(tmem + M::kO1, tmem + M::kP + 32 * (k >> 1) + 8 * (k & 1),
+                                step_desc(cr, (i % L::kStages) * kU * kTile + k * 2048), id_o, k > 0);
+                mma_commit(&m.o_full);
+                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
+                if (i + 1 < pl.nc) ok = scores(i + 1);
+            }
+            mma_commit(&m.drain);              // every product completes before the CTA exits
+            ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
+        }
+        __syncwarp();
+    } else if (warp == kWarps + 1) {
+        // ------------------------------------------------------------ loads and stores
+        if (lane == 0 && pl.nc > 0) {
             int nab = 0, nc = 0;               // chunks of A and B, of C asked for
             auto load_ab = [&]() {
                 if (hold) return;
@@ -507,69 +543,33 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                     for (int u = 0; u < kU; ++u)
                         tma_prefetch_4d(&cmap, pl.col0 + 64 * u, geo.ch * pl.h, pl.chunk<kRev>(nc) * kC, geo.cb * pl.b);
             };
-            auto scores = [&](int i) -> bool {                                                          // (1)
-                if (!mbar_wait(&m.a_full, i & 1, max_spin) || !mbar_wait(&m.b_full, i & 1, max_spin)) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4 * kT; ++k) mma_bf16(tmem + M::kP, kmajor_step(ak, k), kmajor_step(bk, k), id_sc, k > 0);
-                mma_commit(&m.p_full);
-                return true;
-            };
-            // The output of chunk i, staged by the working warps where C was; the last, ragged
-            // one of a sequence shorter than N was written row by row.
-            auto put = [&](int i) -> bool {
-                if (!mbar_wait(&m.staged, i & 1, max_spin)) return false;
+            load_ab();
+            for (int s = 0; s < L::kStages && s < pl.nc; ++s) load_c();
+            for (int i = 0; i < pl.nc; ++i) {
+                if (!(ok = mbar_wait(&m.s_full, i & 1, max_spin))) break;     // (1), (2) and (4) have read A and B
+                if (i + 1 < pl.nc) load_ab();
+                // The output, staged by the working warps where C was; the last, ragged one of a
+                // sequence shorter than N was written row by row.
+                if (!(ok = mbar_wait(&m.staged, i & 1, max_spin))) break;
                 const int t = pl.chunk<kRev>(i) * kC;
                 if (t + kC <= pl.n || pl.n == a.N) {
 #pragma unroll
                     for (int u = 0; u < kU; ++u) tma_store_4d(&omap, ctile(i, u), pl.col0 + 64 * u, pl.h, t, pl.b);
                     tma_store_commit();
                 }
-                return true;
-            };
-            load_ab();
-            for (int s = 0; s < L::kStages && s < pl.nc; ++s) load_c();
-            ok = scores(0);
-            for (int i = 0; i < pl.nc && ok; ++i) {
-                const int s = i % L::kStages;
-                if (L::kStages == 1 && i > 0) {        // C of this chunk, once the output before it has left its place
+                if (i + L::kStages < pl.nc) {      // its place takes C of another chunk
                     tma_store_wait_read<0>();
                     load_c();
                 }
-                if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4 * kT; ++k)                                                        // (2)
-                    mma_bf16(tmem + M::kO2, kmajor_step(ak, k), step_desc(sr, k * 2048), id_o, k > 0);
-                issue_state<kU, kTerms>(tmem + M::kSt, br, base_a + L::kW);                             // (4)
-                mma_commit(&m.s_full);
-                if (L::kStages == 2 && i > 0 && i + 1 < pl.nc) {
-                    tma_store_wait_read<0>();
-                    load_c();
-                }
-                if (!(ok = mbar_wait(&m.s_full, i & 1, max_spin))) break;
-                if (i + 1 < pl.nc) load_ab();
-                if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < kC / 16; ++k)                                                       // (3)
-                    mma_bf16_ts(tmem + M::kO1, tmem + M::kP + 32 * (k >> 1) + 8 * (k & 1),
-                                step_desc(cr, s * kU * kTile + k * 2048), id_o, k > 0);
-                mma_commit(&m.o_full);
-                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
-                if (i + 1 < pl.nc && !(ok = scores(i + 1))) break;
-                ok = put(i);
             }
             tma_store_wait_all<0>();
-            // Every load that was asked for lands, and every product completes, before the CTA exits.
+            // Every load that was asked for lands before the CTA exits.
             if (nab > 0) {
                 mbar_wait(&m.a_full, (nab - 1) & 1, kDefaultMaxSpin);
                 mbar_wait(&m.b_full, (nab - 1) & 1, kDefaultMaxSpin);
             }
             for (int j = max(nc - L::kStages, 0); j < nc; ++j)
                 mbar_wait(&m.c_full[j % L::kStages], (j / L::kStages) & 1, kDefaultMaxSpin);
-            mma_commit(&m.drain);
-            ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
         }
         __syncwarp();
     } else {
@@ -677,7 +677,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     if (warp == kWarps) tmem_dealloc(tmem, kCols);
 }
 
-// First pass, of one sum or two: the end state from zero of each part before the last segment.
+// First pass, of one sum or two: the end state from zero of each segment but the last.
 template <int kT, int kU, int kTerms>
 __global__ void __launch_bounds__(32 * (kU * kWork + 1), SumSmem<kT, kU, kTerms>::kPerSm)
 decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_constant__ CUtensorMap cmap0,
@@ -695,11 +695,11 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
     auto btile = [&](int i) { return base + L::kB + (i % L::kStages) * kT * kTile; };
     auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, a.seg_len / a.nsub / kC, kU, blockIdx.z - (second ? a0.B * a0.H : 0));
+    const Place pl = place(a, kU, blockIdx.z - (second ? a0.B * a0.H : 0));
     const bool rev = a.rev != 0;
     auto chunk = [&](int i) { return rev ? pl.chunk<true>(i) : pl.chunk<false>(i); };
     pdl_launch_dependents();
-    if (pl.nc == 0 || pl.seg >= a.parts - 1) return;   // parts without tokens are not read
+    if (pl.nc == 0 || pl.seg >= a.nseg - 1) return;    // segments without tokens are not read
     if ((smem_u32(base) & 1023) != 0) {
         if (tid == 0) set_status(hdr, LA_ERR_CUDA);
         return;
@@ -786,7 +786,7 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
                            rev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
         }
         const int c0 = pl.col0 + 64 * u + 32 * g;
-        float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.parts + pl.seg) * a.Da * a.Dc + (int64_t)row * a.Dc + c0;
+        float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc + (int64_t)row * a.Dc + c0;
         if (ok && has_state && row < a.Da)
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
@@ -817,7 +817,7 @@ struct KvMaps {
     CUtensorMap in[4], dk, dv;
 };
 
-__global__ void __launch_bounds__(32 * (2 * kWork + 1), 1)
+__global__ void __launch_bounds__(32 * (2 * kWork + 2), 1)
 decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Args a, const __grid_constant__ Tensor dk,
                 const __grid_constant__ Geo geo, const __grid_constant__ Geo vgeo, WsHeader* hdr) {
     using L = KvSmem;
@@ -826,7 +826,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto tile = [&](int i, int k) { return base + ((i & 1) * 4 + k) * kTile; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Place pl = place(a, a.seg_len / kC, 1, blockIdx.z);
+    const Place pl = place(a, 1, blockIdx.z);
     if (pl.nc == 0) {
         pdl_wait();
         return;
@@ -857,12 +857,55 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
     bool ok = true;
 
     if (warp == kWarps) {
+        // ------------------------------------------------------------ products
         if (lane == 0) {
             const uint32_t base_a = smem_u32(base);
             const uint64_t km = kmajor_desc(base_a), rows = rows_desc(base_a);
             const uint64_t sr = rows_desc(base_a + L::kS), sk = kmajor_desc(base_a + L::kS);
             constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true), id_t = idesc_bf16_f32(128, 64, false, false);
+            auto at = [&](uint64_t d, int i, int k) { return step_desc(d, ((i & 1) * 4 + k) * kTile); };
+            auto scores = [&](int i) -> bool {                                                          // (1)
+                if (!mbar_wait(&m.c_full[i & 1], (i >> 1) & 1, max_spin)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + 128 * u, kmajor_step(at(km, i, u), k), kmajor_step(at(km, i, 2 + u), k), id_sc, k > 0);
+                mma_commit(&m.p_full);
+                return true;
+            };
+            ok = scores(0);
+            for (int i = 0; i < pl.nc && ok; ++i) {
+                if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {                                                           // (2)
+                    mma_bf16(tmem + kKvO2, kmajor_step(at(km, i, kTileK), k), step_desc(sr, k * 2048), id_o, k > 0);
+                    mma_bf16(tmem + kKvO2 + 128, kmajor_step(at(km, i, kTileV), k), kmajor_step(sk, k), id_t, k > 0);
+                }
+                issue_state<1, 2>(tmem + kKvX, at(rows, i, kTileQ), base_a + L::kW);                    // (4)
+                mma_commit(&m.s_full);
+                if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)                                                   // (3)
+                        mma_bf16_ts(tmem + kKvX + 128 * u, tmem + 128 * u + 32 * (k >> 1) + 8 * (k & 1),
+                                    step_desc(at(rows, i, u ? kTileQ : kTileG), k * 2048), id_o, k > 0);
+                mma_commit(&m.o_full);
+                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
+                if (i + 1 < pl.nc) ok = scores(i + 1);
+            }
+            mma_commit(&m.drain);
+            ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
+        }
+        __syncwarp();
+    } else if (warp == kWarps + 1) {
+        // ------------------------------------------------------------ loads and stores
+        if (lane == 0) {
             int n = 0;
             auto load = [&]() {
                 if (hold) return;
@@ -881,62 +924,23 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
                     tma_prefetch_4d(&maps.in[kTileG], 0, geo.ch * pl.h, next, geo.cb * pl.b);
                 }
             };
-            auto at = [&](uint64_t d, int i, int k) { return step_desc(d, ((i & 1) * 4 + k) * kTile); };
-            auto scores = [&](int i) -> bool {                                                          // (1)
-                if (!mbar_wait(&m.c_full[i & 1], (i >> 1) & 1, max_spin)) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + 128 * u, kmajor_step(at(km, i, u), k), kmajor_step(at(km, i, 2 + u), k), id_sc, k > 0);
-                mma_commit(&m.p_full);
-                return true;
-            };
-            auto put = [&](int i) -> bool {
-                if (!mbar_wait(&m.staged, i & 1, max_spin)) return false;
+            load();
+            if (pl.nc > 1) load();
+            for (int i = 0; i < pl.nc; ++i) {
+                if (!(ok = mbar_wait(&m.staged, i & 1, max_spin))) break;
                 const int t = pl.chunk<true>(i) * kC;
                 if (t + kC <= pl.n || pl.n == a.N) {
                     tma_store_4d(&maps.dv, tile(i, kTileG), 0, pl.h, t, pl.b);
                     tma_store_4d(&maps.dk, tile(i, kTileQ), 0, pl.h, t, pl.b);
                     tma_store_commit();
                 }
-                return true;
-            };
-            load();
-            if (pl.nc > 1) load();
-            ok = scores(0);
-            for (int i = 0; i < pl.nc && ok; ++i) {
-                if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {                                                           // (2)
-                    mma_bf16(tmem + kKvO2, kmajor_step(at(km, i, kTileK), k), step_desc(sr, k * 2048), id_o, k > 0);
-                    mma_bf16(tmem + kKvO2 + 128, kmajor_step(at(km, i, kTileV), k), kmajor_step(sk, k), id_t, k > 0);
-                }
-                issue_state<1, 2>(tmem + kKvX, at(rows, i, kTileQ), base_a + L::kW);                                   // (4)
-                mma_commit(&m.s_full);
-                if (i > 0 && i + 1 < pl.nc) {          // the next chunk, once the output before this one has left its place
+                if (i + 2 < pl.nc) {               // the tiles' places take another chunk
                     tma_store_wait_read<0>();
                     load();
                 }
-                if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)                                                   // (3)
-                        mma_bf16_ts(tmem + kKvX + 128 * u, tmem + 128 * u + 32 * (k >> 1) + 8 * (k & 1),
-                                    step_desc(at(rows, i, u ? kTileQ : kTileG), k * 2048), id_o, k > 0);
-                mma_commit(&m.o_full);
-                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
-                if (i + 1 < pl.nc && !(ok = scores(i + 1))) break;
-                ok = put(i);
             }
             tma_store_wait_all<0>();
             for (int j = max(n - 2, 0); j < n; ++j) mbar_wait(&m.c_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
-            mma_commit(&m.drain);
-            ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
         }
         __syncwarp();
     } else {
@@ -1075,8 +1079,7 @@ cudaError_t launch_sums(const Sum* s, int count, WsHeader* hdr, cudaStream_t st)
     const cudaError_t e = ensure_smem_optin(decay_sums_kernel<kT, kU, kTerms>, bytes, optin);
     if (e != cudaSuccess) return e;
     const Sum &x = s[0], &y = s[count - 1];
-    const int parts = x.a.parts > y.a.parts ? x.a.parts : y.a.parts;
-    const dim3 grid((x.a.Dc + 64 * kU - 1) / (64 * kU), parts - 1, x.heads() * count);
+    const dim3 grid((x.a.Dc + 64 * kU - 1) / (64 * kU), x.a.nseg - 1, x.heads() * count);
     decay_sums_kernel<kT, kU, kTerms><<<grid, 32 * (kU * kWork + 1), bytes, st>>>(x.bm, x.cm, y.bm, y.cm, x.a, x.geo, y.a, y.geo, hdr);
     return cudaPeekAtLastError();
 }
@@ -1088,7 +1091,7 @@ cudaError_t launch_main(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_
     const cudaError_t e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev>, bytes, optin);
     if (e != cudaSuccess) return e;
     return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev>, dim3((s.a.Dc + 64 * kU - 1) / (64 * kU), s.a.nseg, s.heads()),
-                              32 * (kU * kWork + 1), bytes, st, dependent, s.am, s.bm, s.cm, s.om, s.a, s.geo, hdr);
+                              32 * (kU * kWork + 2), bytes, st, dependent, s.am, s.bm, s.cm, s.om, s.a, s.geo, hdr);
 }
 
 // By widths: one or two 64-row tiles of the state, one or two column blocks.
@@ -1104,12 +1107,12 @@ template <int kTerms, bool kRev> cudaError_t main_of(const Sum& s, bool dependen
 
 bool narrow(int Dk, int Dv) { return Dk <= 64 && Dv <= 64; }
 
-// Segments of a pass with `per_sm` CTAs per SM. CTAs run in waves, so the cut is the one
-// whose waves times chunks is least; in chunks: starting and ending a CTA 1, the first pass
-// 0.4 of the main pass, and with segments two further launches 2.
-int segments(int64_t BH, int N, int per_sm) {
+// Segments of the forward pass. CTAs run in waves, so the cut is the one whose waves times
+// chunks is least; in chunks: starting and ending a CTA 1, the first pass 0.4 of the main
+// pass, and with segments two further launches 2.
+int forward_segments(int64_t BH, int N, int Dk, int Dv) {
     const int chunks = (N + kC - 1) / kC;
-    const int64_t slots = (int64_t)per_sm * sm_count();
+    const int64_t slots = (narrow(Dk, Dv) ? 2 : 1) * (int64_t)sm_count();
     int best = 1;
     double least = 1e30;
     for (int n = 1; n <= 64 && n <= chunks; ++n) {
@@ -1121,10 +1124,35 @@ int segments(int64_t BH, int N, int per_sm) {
     }
     return best;
 }
-// Parts that a CTA of the main pass joins itself; more are chained by a launch of their own.
+
+// Segments of the backward pass, the same for dq and for dk and dv, in chunks of the main
+// passes as above. Those run side by side while their CTAs fit the SMs together (two of dq to
+// one where heads are narrow), else one after the other. B=8 N=4096 H=8 D=64, 32 chunks: not
+// cut 102 us, two segments each 121, four and two 119; B=4 N=2047 H=8 D=128, 16 chunks: not cut
+// 59 us, two segments 81, four 89.
+int backward_segments(int64_t BH, int N, int Dk, int Dv) {
+    const int chunks = (N + kC - 1) / kC;
+    const double sms = sm_count(), shares[3] = {narrow(Dk, Dv) ? 0.5 : 1.0, 1.0, narrow(Dk, Dv) ? 0.0 : 1.0};
+    int best = 1;
+    double least = 1e30;
+    for (int n = 1; n <= 64 && n <= chunks; ++n) {
+        const int per = (chunks + n - 1) / n;
+        if ((chunks + per - 1) / per != n) continue;
+        double used = 0.0, each = 0.0;
+        for (double share : shares) {
+            used += share * BH * n;
+            if (share > 0.0) each += ceil(share * BH * n / sms) * (per + 1.5);
+        }
+        const double cost = (used <= sms ? per + 1.5 : each) +
+                            (n > 1 ? ceil((shares[0] + shares[2]) * BH * (n - 1) / sms) * (0.4 * per + 1.0) + 1.0 : 0.0);
+        if (cost < least) least = cost, best = n;
+    }
+    return best;
+}
+
+// Segments whose end states a CTA of the main pass joins itself; more are chained by a launch
+// of their own.
 constexpr int kFold = 6;
-int forward_segments(int64_t BH, int N, int Dk, int Dv) { return segments(BH, N, narrow(Dk, Dv) ? 2 : 1); }
-int reverse_segments(int64_t BH, int N) { return segments(BH, N, 1); }   // of dk and dv, which share their seeds
 
 }  // namespace
 
@@ -1145,48 +1173,33 @@ bool tc_supported(const Args& a, la_dtype dt) {
 
 namespace {
 
-// The cuts of a backward pass: S for dq, and R, whose longer segments take parts of about S's
-// length so that the first pass's CTAs end together.
-void cut_backward(Args* dq, Args* dv, int64_t BH, int Dk, int Dv) {
-    cut(dq, forward_segments(BH, dq->N, Dk, Dv), 1, kC);
-    const int nseg = reverse_segments(BH, dv->N);
-    cut(dv, nseg, 1, kC);
-    int nsub = dq->nseg > 1 ? (dv->seg_len + dq->seg_len - 1) / dq->seg_len : 1;
-    while (nsub > 1 && (nseg - 1) * nsub + 1 > 64) --nsub;
-    cut(dv, nseg, nsub, kC);
-    dq->fold = dq->parts - 1 <= kFold && dv->parts - 1 <= kFold;
-    dv->fold = dq->fold;
-}
 void cut_forward(Args* a) {
-    cut(a, forward_segments((int64_t)a->B * a->H, a->N, a->Da, a->Dc), 1, kC);
-    a->fold = a->parts - 1 <= kFold;
+    cut(a, forward_segments((int64_t)a->B * a->H, a->N, a->Da, a->Dc), kC);
+    a->fold = a->nseg - 1 <= kFold;
+}
+void cut_backward(Args* a) {
+    cut(a, backward_segments((int64_t)a->B * a->H, a->N, a->Da, a->Dc), kC);
+    a->fold = a->nseg - 1 <= kFold;
 }
 
-size_t seeds_of(const Args& a, int64_t BH, int Dk, int Dv) { return a.nseg > 1 ? (size_t)BH * a.parts * Dk * Dv : 0; }
+Args cut_of(int64_t BH, int N, int Dk, int Dv, bool backward) {
+    Args a = {};
+    a.B = 1, a.H = (int)BH, a.N = N, a.Da = Dk, a.Dc = Dv;
+    backward ? cut_backward(&a) : cut_forward(&a);
+    return a;
+}
 
 }  // namespace
 
 size_t tc_seeds(int64_t BH, int N, int Dk, int Dv, bool backward) {
-    Args x = {}, y = {};
-    x.N = y.N = N, x.B = 1, x.H = (int)BH, x.Da = Dk, x.Dc = Dv;
-    if (!backward) {
-        cut_forward(&x);
-        return seeds_of(x, BH, Dk, Dv);
-    }
-    cut_backward(&x, &y, BH, Dk, Dv);
-    return seeds_of(x, BH, Dk, Dv) + seeds_of(y, BH, Dk, Dv);
+    const Args a = cut_of(BH, N, Dk, Dv, backward);
+    return a.nseg > 1 ? (size_t)BH * a.nseg * Dk * Dv * (backward ? 2 : 1) : 0;
 }
 
 int tc_launches(int64_t BH, int N, int Dk, int Dv, bool backward) {
-    Args x = {}, y = {};
-    x.N = y.N = N, x.B = 1, x.H = (int)BH, x.Da = Dk, x.Dc = Dv;
-    if (!backward) {
-        cut_forward(&x);
-        return x.nseg == 1 ? 1 : x.fold ? 2 : 3;
-    }
-    cut_backward(&x, &y, BH, Dk, Dv);
-    const bool f = x.nseg > 1, r = y.nseg > 1, together = (Dk <= 64) == (Dv <= 64);
-    return (narrow(Dk, Dv) ? 2 : 3) + (f && r && !together ? 2 : f || r ? 1 : 0) + ((f || r) && !x.fold ? 1 : 0);
+    const Args a = cut_of(BH, N, Dk, Dv, backward);
+    const int sums = backward && (Dk <= 64) != (Dv <= 64) ? 2 : 1, main = !backward ? 1 : narrow(Dk, Dv) ? 2 : 3;
+    return main + (a.nseg > 1 ? sums + (a.fold ? 0 : 1) : 0);
 }
 
 cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
@@ -1202,36 +1215,32 @@ cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
     return a.S_out ? main_of<3, false>(s, a.nseg > 1, hdr, st) : main_of<2, false>(s, a.nseg > 1, hdr, st);
 }
 
-// First passes of S (for dq) and of R (for dk and dv), one chaining, then dq and dk and dv: the
-// last two in one pass where the heads are narrow enough for its tiles.
+// With segments the first passes of S (for dq) and of R (for dk and dv) and their chaining; then
+// dq and dk and dv, the last two in one pass where the heads are narrow enough for its tiles.
 cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t st) {
-    const int64_t BH = (int64_t)dq.B * dq.H;
-    cut_backward(&dq, &dv, BH, dv.Da, dv.Dc);
-    dv.seeds = dq.seeds + seeds_of(dq, BH, dq.Da, dq.Dc);
-    dk.seeds = dv.seeds, dk.nseg = dv.nseg, dk.seg_len = dv.seg_len, dk.nsub = dv.nsub, dk.parts = dv.parts;
-    dk.fold = dv.fold, dk.seeds_t = 1;
+    cut_backward(&dv);
+    const bool cut = dv.nseg > 1;
+    for (Args* a : {&dq, &dk}) a->nseg = dv.nseg, a->seg_len = dv.seg_len, a->fold = dv.fold;
+    dk.seeds = dv.seeds = dq.seeds + (cut ? (size_t)dq.B * dq.H * dq.nseg * dq.Da * dq.Dc : 0);
+    dk.seeds_t = 1;
     Sum s[3] = {{dq}, {dv}, {dk}};
     for (Sum& x : s)
         if (!x.encode()) return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
     cudaError_t e;
-    const bool f = dq.nseg > 1, r = dv.nseg > 1;
-    if (f && r && (dq.Da <= 64) == (dq.Dc <= 64)) {
-        if ((e = sums_of<2>(s, 2, hdr, st)) != cudaSuccess) return e;
-    } else {
-        if (f && (e = sums_of<2>(s, 1, hdr, st)) != cudaSuccess) return e;
-        if (r && (e = sums_of<2>(s + 1, 1, hdr, st)) != cudaSuccess) return e;
+    if (cut) {
+        const bool together = (dq.Da <= 64) == (dq.Dc <= 64);   // S and R have the same shape
+        if ((e = sums_of<2>(s, together ? 2 : 1, hdr, st)) != cudaSuccess) return e;
+        if (!together && (e = sums_of<2>(s + 1, 1, hdr, st)) != cudaSuccess) return e;
+        const Args chained[2] = {dq, dv};
+        if (!dq.fold && (e = launch_chain(chained, 2, kC, st)) != cudaSuccess) return e;
     }
-    if ((f || r) && !dq.fold) {
-        const Args chained[2] = {f ? dq : dv, dv};
-        if ((e = launch_chain(chained, f && r ? 2 : 1, kC, st)) != cudaSuccess) return e;
-    }
-    if ((e = main_of<2, false>(s[0], f || r, hdr, st)) != cudaSuccess) return e;
+    if ((e = main_of<2, false>(s[0], cut, hdr, st)) != cudaSuccess) return e;
     if (narrow(dv.Da, dv.Dc)) {
         static std::atomic<int> optin[kMaxDevices];
         if ((e = ensure_smem_optin(decay_kv_kernel, KvSmem::kBytes, optin)) != cudaSuccess) return e;
         const KvMaps maps = {{s[1].am, s[2].am, s[1].bm, s[1].cm}, s[2].om, s[1].om};
-        return scan::launch_after(decay_kv_kernel, dim3(1, dv.nseg, s[1].heads()), 32 * (2 * kWork + 1), KvSmem::kBytes, st,
+        return scan::launch_after(decay_kv_kernel, dim3(1, dv.nseg, s[1].heads()), 32 * (2 * kWork + 2), KvSmem::kBytes, st,
                                   true, maps, dv, dk.o, s[1].geo, s[2].geo, hdr);
     }
     s[1].geo.late = s[2].geo.late = 1;
