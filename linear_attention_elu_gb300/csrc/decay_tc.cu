@@ -19,7 +19,7 @@
 // sums stay short. w C enters it as bf16 terms, each the remainder of those before: two for a
 // state that only o reads (2^-16 of w C is left), three for one that the call returns.
 // Weights below the diagonal 32 x 32 blocks are products of two factors <= 1, one of the
-// row and one of the column; the diagonal blocks take an exponential per score. Every
+// row and one of the column; the diagonal blocks take a factor per score. Every
 // factor's exponent is a count of tokens times l, so none is a difference of larger ones.
 //
 // Schedule. Eight working warps per unit, one that issues the products and one for loads and
@@ -33,6 +33,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
+#include <stddef.h>
 
 #include <atomic>
 
@@ -66,15 +67,18 @@ template <int kU> struct Tm {
 
 struct Misc {
     uint64_t a_full, b_full, c_full[2], p_full, s_full, o_full;
-    uint64_t prep, pt, staged, drain;
+    uint64_t prep, pt, staged, o_free, drain;
     uint32_t tmem_slot;
     int any;                    // values of C that are not finite: the first token that has one,
     int first[128];             // and that of each column, counted over the segment
     alignas(16) float tab[32];  // f^(31 - j), by the column's place in its block; read 16 bytes at a time
     alignas(16) uint32_t mask[512];   // diagonal block, [pair of columns / 2][row][2]: which scores take part
+    alignas(16) float diag[1024];     // where there is room: its factors, [column / 4][row][4]
 };
-constexpr uint32_t kMiscBytes = 3 * 1024;
-static_assert(sizeof(Misc) <= kMiscBytes, "barriers and tables");
+// Two column blocks leave no room for the diagonal's factors.
+constexpr bool diag_table(int kU) { return kU == 1; }
+constexpr uint32_t misc_bytes(bool table) { return table ? 7 * 1024 : 3 * 1024; }
+static_assert(sizeof(Misc) <= misc_bytes(true) && offsetof(Misc, diag) <= misc_bytes(false), "barriers and tables");
 
 // Shared memory from a 1024-byte boundary.
 template <int kT, int kU, int kTerms> struct Smem {
@@ -83,7 +87,7 @@ template <int kT, int kU, int kTerms> struct Smem {
     static constexpr uint32_t kW = kC0 + kStages * kU * kTile;        // [unit][term]
     static constexpr uint32_t kS = kW + kU * kTerms * kTile;          // [unit], 64 kT rows
     static constexpr uint32_t kMisc = kS + kU * kT * kTile / 2;
-    static constexpr int kBytes = kMisc + kMiscBytes;
+    static constexpr int kBytes = kMisc + misc_bytes(diag_table(kU));
     static constexpr int kPerSm = kBytes <= 113 * 1024 && kU == 1 ? 2 : 1;
 };
 static_assert(Smem<1, 1, 2>::kPerSm == 2 && Smem<1, 1, 3>::kPerSm == 2, "two CTAs per SM");
@@ -94,7 +98,7 @@ template <int kT, int kU, int kTerms> struct SumSmem {
     static constexpr int kStages = kT + kU < 4 || kTerms == 2 ? 2 : 1;
     static constexpr uint32_t kB = 0, kC0 = kStages * kT * kTile, kW = kC0 + kStages * kU * kTile;
     static constexpr uint32_t kMisc = kW + kU * kTerms * kTile;
-    static constexpr int kBytes = kMisc + kMiscBytes;
+    static constexpr int kBytes = kMisc + misc_bytes(false);
     static constexpr int kPerSm = kBytes <= 113 * 1024 && kU == 1 ? 2 : 1;
 };
 static_assert(SumSmem<2, 2, 2>::kBytes <= 227 * 1024 && SumSmem<1, 2, 3>::kBytes <= 227 * 1024, "shared memory");
@@ -326,56 +330,68 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// Four scores of a diagonal block, columns j .. j + 3, to packed P: by the table, or by an
+// exponential each. Scores that take no part are cleared as bits: their products may be anything.
+template <bool kRev, bool kTable>
+__device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float own, const Misc& m, uint32_t* p) {
+    const int lane = threadIdx.x & 31;
+    const uint2 keep = *reinterpret_cast<const uint2*>(m.mask + 16 * j + 2 * lane);
+    uint64_t f0, f1;
+    if constexpr (kTable) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.diag + 32 * j + 4 * lane);
+        f0 = f.x, f1 = f.y;
+    } else {
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float c = (float)(j + u);
+            x[u] = pow2(kRev ? fmaf(c, rf.diag, -own) : fmaf(-c, rf.diag, own));
+        }
+        f0 = pk2(x[0], x[1]), f1 = pk2(x[2], x[3]);
+    }
+    p[0] = pack2(mul2(pair2(v), f0)) & keep.x;
+    p[1] = pack2(mul2(pair2(v + 2), f1)) & keep.y;
+}
+
 // Scores of block column `blk` (bm in the order of summation) to packed P, over the first
-// half of their columns: no other warp reads or writes those. Loops are kept rolled: what
-// the compiler keeps of unrolled ones from chunk to chunk does not fit the registers, and
-// what it spills does not fit the little L1 that two CTAs leave (backwards in time the call
-// took 1.8 times as long).
-template <bool kRev>
+// half of their columns: no other warp reads or writes those. kCols at a time: 16, in rolled
+// loops, where the state's registers leave no room for more (what the compiler keeps of
+// unrolled ones from chunk to chunk is spilled, and does not fit the little L1 that two
+// CTAs leave: backwards in time the call took 1.8 times as long).
+template <bool kRev, bool kTable, int kCols>
 __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
     const int lane = threadIdx.x & 31;
     const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane * rf.diag;
     const uint64_t r2 = pk2(r, r);
     const uint32_t at = tm_p + 32 * blk;
 #pragma unroll 1
-    for (int half = 0; half < 32; half += 16) {
-        uint32_t v[16], p[8];
+    for (int first = 0; first < 32; first += kCols) {
+        uint32_t v[kCols], p[kCols / 2];
         if (bm > qm) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = 0u;
-            tmem_st8(at + half / 2, p);
-            continue;
-        }
-        tmem_ld16(at + half, v);
-        tmem_ld_wait();
-        if (kRev && 32 * blk + half + 16 > cut)        // later tokens that the sequence does not have
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (32 * blk + half + e >= cut) v[e] = 0u;
-        if (bm < qm) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.tab + half + 2 * e);
-                p[e] = pack2(mul2(mul2(pair2(v + 2 * e), f.x), r2));
-                p[e + 1] = pack2(mul2(mul2(pair2(v + 2 * e + 2), f.y), r2));
-            }
+            for (int e = 0; e < kCols / 2; ++e) p[e] = 0u;
         } else {
-            const float first = (float)half;
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                // Scores that take no part are cleared as bits: their products may be anything.
-                const uint2 keep = *reinterpret_cast<const uint2*>(m.mask + 32 * (half / 2 + e) + 2 * lane);
-                float x[4];
+            for (int e = 0; e < kCols; e += 16) tmem_ld16(at + first + e, *reinterpret_cast<uint32_t(*)[16]>(v + e));
+            tmem_ld_wait();
+            if (kRev && 32 * blk + first + kCols > cut)        // later tokens that the sequence does not have
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float j = first + (float)(2 * e + u);
-                    x[u] = __uint_as_float(v[2 * e + u]) * pow2(kRev ? fmaf(j, rf.diag, -own) : fmaf(-j, rf.diag, own));
+                for (int e = 0; e < kCols; ++e)
+                    if (32 * blk + first + e >= cut) v[e] = 0u;
+            if (bm < qm) {
+#pragma unroll
+                for (int e = 0; e < kCols; e += 4) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.tab + first + e);
+                    p[e / 2] = pack2(mul2(mul2(pair2(v + e), f.x), r2));
+                    p[e / 2 + 1] = pack2(mul2(mul2(pair2(v + e + 2), f.y), r2));
                 }
-                p[e] = pack_bf16(x[0], x[1]) & keep.x;
-                p[e + 1] = pack_bf16(x[2], x[3]) & keep.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < kCols; e += 4) diagonal4<kRev, kTable>(v + e, first + e, rf, own, m, p + e / 2);
             }
         }
-        tmem_st8(at + half / 2, p);
+        if constexpr (kCols == 16) tmem_st8(at + first / 2, p);
+        else tmem_st16(at, p);
     }
 }
 
@@ -409,8 +425,13 @@ __device__ __forceinline__ void join_output(uint32_t tm1, uint32_t tm2, float sc
 }
 
 // Tables of a head: the columns' factors, and which scores of a diagonal block take part.
-template <bool kRev> __device__ __forceinline__ void init_tables(Misc& m, float l2) {
+template <bool kRev, bool kTable> __device__ __forceinline__ void init_tables(Misc& m, float l2) {
     const int tid = threadIdx.x, lane = tid & 31;
+    if (kTable && tid < 256)
+        for (int j = 4 * (tid >> 5); j < 4 * (tid >> 5) + 4; ++j) {
+            const int gap = kRev ? j - lane : lane - j;
+            m.diag[32 * (j & ~3) + 4 * lane + (j & 3)] = gap >= 0 ? pow2((float)gap * l2) : 0.f;
+        }
     if (tid < 32) m.tab[tid] = pow2((float)(kRev ? tid : 31 - tid) * l2);
     if (tid < 256)
         for (int e = 2 * (tid >> 5); e < 2 * (tid >> 5) + 2; ++e) {
@@ -455,7 +476,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     }
     if (tid < 128) m.first[tid] = kNone;
     const float l = a.decay[pl.h], l2 = log2_decay(l);
-    init_tables<kRev>(m, l2);
+    init_tables<kRev, diag_table(kU)>(m, l2);
     if (warp == kWarps) {
         tmem_alloc(&m.tmem_slot, kCols);
         tmem_relinquish();
@@ -620,7 +641,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             tc_fence_after();
 #pragma unroll 1
             for (int bm = g4; bm < 4; bm += 2 * kU)
-                scores_to_p<kRev>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
+                scores_to_p<kRev, diag_table(kU), 16>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             auto hand_over = [&]() {
                 tmem_st_wait();
@@ -803,12 +824,13 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
 // same four tiles and the same state R_t = q_t dout_t^T + f R_{t+1}:
 //   unit 0, dv: A = K, B = Q, C = dout, state R;   unit 1, dk: A = V, B = dout, C = Q, state R^T
 // so (4) and the state are unit 0's alone, and unit 1 reads the same bf16 tile transposed.
-// Sixteen working warps, one CTA per SM; every tile double buffered. For the steps that the
-// units share a warp owns 16 columns.
+// Sixteen working warps, one CTA per SM; every tile double buffered, and the outputs staged in
+// tiles of their own, so that a chunk's places take the next but one as soon as its products
+// are done. For the steps that the units share a warp owns 16 columns.
 enum { kTileK, kTileV, kTileQ, kTileG };
 struct KvSmem {
-    static constexpr uint32_t kW = 8 * kTile, kS = kW + 2 * kTile, kMisc = kS + kTile / 2;
-    static constexpr int kBytes = kMisc + kMiscBytes;
+    static constexpr uint32_t kW = 8 * kTile, kO = kW + 2 * kTile, kS = kO + 2 * kTile, kMisc = kS + kTile / 2;
+    static constexpr int kBytes = kMisc + misc_bytes(true);
 };
 static_assert(KvSmem::kBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kKvX = 256, kKvO2 = 320;        // TMEM: scores of unit u at 128 u; + 128 u
@@ -836,14 +858,14 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
         return;
     }
     if (tid == 0) {
-        for (uint64_t* bar : {&m.c_full[0], &m.c_full[1], &m.p_full, &m.s_full, &m.o_full, &m.drain}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&m.c_full[0], &m.c_full[1], &m.p_full, &m.s_full, &m.o_full, &m.o_free, &m.drain}) mbar_init(bar, 1);
         for (uint64_t* bar : {&m.prep, &m.pt, &m.staged}) mbar_init(bar, kWarps);
         fence_mbar_init();
         m.any = kNone;
     }
     if (tid < 128) m.first[tid] = kNone;
     const float l = a.decay[pl.h], l2 = log2_decay(l);
-    init_tables<true>(m, l2);
+    init_tables<true, true>(m, l2);
     if (warp == kWarps) {
         tmem_alloc(&m.tmem_slot, 512);
         tmem_relinquish();
@@ -927,17 +949,18 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             load();
             if (pl.nc > 1) load();
             for (int i = 0; i < pl.nc; ++i) {
+                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;     // the last to read a chunk's tiles
+                if (i + 2 < pl.nc) load();
+                // The outputs, staged by the working warps; a ragged chunk's were written row by row.
                 if (!(ok = mbar_wait(&m.staged, i & 1, max_spin))) break;
                 const int t = pl.chunk<true>(i) * kC;
                 if (t + kC <= pl.n || pl.n == a.N) {
-                    tma_store_4d(&maps.dv, tile(i, kTileG), 0, pl.h, t, pl.b);
-                    tma_store_4d(&maps.dk, tile(i, kTileQ), 0, pl.h, t, pl.b);
+                    tma_store_4d(&maps.dv, base + L::kO, 0, pl.h, t, pl.b);
+                    tma_store_4d(&maps.dk, base + L::kO + kTile, 0, pl.h, t, pl.b);
                     tma_store_commit();
-                }
-                if (i + 2 < pl.nc) {               // the tiles' places take another chunk
                     tma_store_wait_read<0>();
-                    load();
                 }
+                mbar_arrive(&m.o_free);
             }
             tma_store_wait_all<0>();
             for (int j = max(n - 2, 0); j < n; ++j) mbar_wait(&m.c_full[j & 1], (j >> 1) & 1, kDefaultMaxSpin);
@@ -978,7 +1001,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
         for (int i = 0; i < pl.nc && ok; ++i) {
             const int t0 = pl.chunk<true>(i) * kC, mt = min(kC, pl.n - t0);
             const bool ragged = mt < kC && pl.n < a.N;
-            uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ), *ct = u ? qt : gt;
+            uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ), *ct = base + L::kO + u * kTile;
             // ---------------------------------------------------- state to bf16
             if (has_state) write_state(base + L::kS, st, row, 2 * g4);
             fence_proxy_async_smem();
@@ -988,7 +1011,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             if (!(ok = warp_wait(&m.p_full, i & 1, max_spin))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int bm = g; bm < 4; bm += 2) scores_to_p<true>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
+            for (int bm = g; bm < 4; bm += 2) scores_to_p<true, true, 32>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
@@ -1005,6 +1028,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             // ---------------------------------------------------- output
             if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
             tc_fence_after();
+            if (i > 0 && !(ok = warp_wait(&m.o_free, (i - 1) & 1, max_spin))) break;
             const bool spoiled = *const_cast<volatile int*>(&m.any) != kNone;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
