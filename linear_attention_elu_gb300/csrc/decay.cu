@@ -18,7 +18,7 @@
 // outputs each:
 //   P = weighted, masked A B^T;   O = P C + e^{l (i + 1)} A S;   S = e^{64 l} S + (w B)^T C
 // with S in registers between chunks. What bounds it: the products' operand reads from
-// shared memory (two 16-byte reads per 16 multiply-adds). Sequences are cut into segments
+// shared memory (two 16-byte reads per 16 multiply-adds) and the instructions around them. Sequences are cut into segments
 // when there are too few heads for the SMs: a first pass gives each segment's end state
 // from zero, a chain over the segments their start states, and the second pass starts
 // from those.
@@ -57,20 +57,34 @@ template <int kD> struct Common {
     float pw[kL + 4];               // e^{l k}
 };
 
-// Rows [tok][col0 .. col0 + 8 nblk) of x, transposed to dst[col][tok] or as they are. A
-// warp takes 4 tokens x 8 columns at a time: whole 32-byte pieces, and no two lanes of
-// a transposed store in one bank.
-template <typename T, bool kTransposed, typename Place>
-__device__ __forceinline__ void stage(const T* x, Place row, int m, int width, int cols, float* dst, int stride,
-                                      const float* weight) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blocks = cols / 8;
-    for (int it = warp; it < blocks * (kL / 4); it += 8) {
-        const int d = 8 * (it % blocks) + (lane & 7), t = 4 * (it / blocks) + (lane >> 3);
-        float v = t < m && d < width ? to_f(x[row(t) + d]) : 0.f;
-        if (weight) v *= weight[t < m ? m - 1 - t : 0];
-        if (kTransposed) dst[d * stride + t] = v;
-        else dst[t * stride + d] = v;
+// Four values of a row from value d on; past `width` they are zero.
+template <typename T> __device__ __forceinline__ float4 load4(const T* p, int d, int width, bool vec) {
+    if (vec) {
+        if (d >= width) return make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (sizeof(T) == 4) {
+            return __ldg(reinterpret_cast<const float4*>(p + d));
+        } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + d));
+            return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+        }
     }
+    return make_float4(d < width ? to_f(p[d]) : 0.f, d + 1 < width ? to_f(p[d + 1]) : 0.f,
+                       d + 2 < width ? to_f(p[d + 2]) : 0.f, d + 3 < width ? to_f(p[d + 3]) : 0.f);
+}
+
+// Whether every row of x can be read four values at a time.
+template <typename T> __device__ __forceinline__ bool whole4(const T* x, const Tensor& t, int width) {
+    return ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(t.ts * (int64_t)sizeof(T))) & (4 * sizeof(T) - 1)) == 0 && width % 4 == 0;
+}
+
+// A thread stages values 4 (lane / 8) + 16 i of token 8 warp + lane mod 8: whole 32-byte
+// pieces of eight rows at a time, and stores of a transposed tile in two banks' reach.
+__device__ __forceinline__ void put_transposed(float* dst, int d, int t, const float4& v) {
+    dst[d * kRow + t] = v.x;
+    dst[(d + 1) * kRow + t] = v.y;
+    dst[(d + 2) * kRow + t] = v.z;
+    dst[(d + 3) * kRow + t] = v.w;
 }
 
 __device__ __forceinline__ void outer(float (&acc)[4][4], const float* x, const float* y) {
@@ -118,32 +132,48 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
                 st[k][i][j] = from && r < a.Da && c < width ? from[(int64_t)r * a.Dc + col0 + c] : 0.f;
             }
     if (tid <= kL) s.pw[tid] = pow2(tid * l2);
-    const int d4 = (a.Da + 3) & ~3, d8 = (a.Da + 7) & ~7;
+    const int d4 = (a.Da + 3) & ~3;
+    const int tok = 8 * (tid >> 5) + (tid & 7), q4 = 4 * ((tid & 31) >> 3);   // staged by this thread
+    const bool vec_a = whole4(A, a.a, a.Da), vec_b = whole4(Bp, a.b, a.Da), vec_c = whole4(C, a.c, width);
+    __syncthreads();
     for (int c0 = t0; c0 < t1; c0 += kL) {
         const int m = min(kL, t1 - c0);
         // Tokens count from the last one where time is reversed.
-        auto place = [&](const Tensor& t) {
-            const int64_t ts = t.ts;
-            const int64_t at = a.rev ? (int64_t)(n - 1 - c0) * ts : (int64_t)c0 * ts, step = a.rev ? -ts : ts;
-            return [=](int i) { return at + i * step; };
-        };
+        auto token = [&](int i) { return (int64_t)(a.rev ? n - 1 - c0 - i : c0 + i); };
+        const int64_t at = token(tok);
+        const bool in = tok < m;
+        const float weight = in ? s.pw[m - 1 - tok] : 0.f;
         __syncthreads();
-        if constexpr (!kState) {
-            stage<T, true>(A, place(a.a), m, a.Da, d8, x.at, kRow, nullptr);
-            stage<T, true>(Bp, place(a.b), m, a.Da, d8, x.bt, kRow, nullptr);
+#pragma unroll
+        for (int d = q4; d < 64 * kD; d += 16) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in) v = load4(Bp + at * a.b.ts, d, a.Da, vec_b);
+            if constexpr (!kState) {
+                put_transposed(x.bt, d, tok, v);
+                float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (in) u = load4(A + at * a.a.ts, d, a.Da, vec_a);
+                put_transposed(x.at, d, tok, u);
+            }
+            *reinterpret_cast<float4*>(s.bn + tok * kB + d) = make_float4(weight * v.x, weight * v.y, weight * v.z, weight * v.w);
+        }
+#pragma unroll
+        for (int d = q4; d < kL; d += 16) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in) v = load4(C + at * a.c.ts, d, width, vec_c);
+            *reinterpret_cast<float4*>(s.cn + tok * kRow + d) = v;
+        }
+        if constexpr (!kState)
 #pragma unroll
             for (int k = 0; k < kD; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<float4*>(x.sm + (64 * k + 4 * ty + i) * kRow + 4 * tx) =
                         make_float4(st[k][i][0], st[k][i][1], st[k][i][2], st[k][i][3]);
-        }
-        stage<T, false>(Bp, place(a.b), m, a.Da, 64 * kD, s.bn, kB, s.pw);
-        stage<T, false>(C, place(a.c), m, width, kL, s.cn, kRow, nullptr);
         __syncthreads();
         if constexpr (!kState) {
             if (tx <= ty) {             // the other tiles are masked
                 float p[4][4] = {};
+#pragma unroll 4
                 for (int d = 0; d < d4; ++d) outer(p, x.at + d * kRow + 4 * ty, x.bt + d * kRow + 4 * tx);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -158,6 +188,7 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
             }
             __syncthreads();
             float o[4][4] = {};
+#pragma unroll 4
             for (int d = 0; d < d4; ++d) outer(o, x.at + d * kRow + 4 * ty, x.sm + d * kRow + 4 * tx);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -165,6 +196,7 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
                 for (int j = 0; j < 4; ++j) o[i][j] *= s.pw[4 * ty + i + 1];
             // Tokens after the tile's own take no part: each row adds its own terms only, so
             // that an infinity or NaN reaches no earlier token.
+#pragma unroll 4
             for (int u = 0; u < 4 * ty; ++u) outer(o, x.pt + u * kRow + 4 * ty, s.cn + u * kRow + 4 * tx);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -173,12 +205,13 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[i][j] = fmaf(w, s.cn[u * kRow + 4 * tx + j], o[i][j]);
                 }
-            const auto row = place(a.o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                T* to = O + token(4 * ty + i) * a.o.ts + 4 * tx;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (4 * ty + i < m && 4 * tx + j < width) O[row(4 * ty + i) + 4 * tx + j] = from_f<T>(a.scale * o[i][j]);
+                    if (4 * ty + i < m && 4 * tx + j < width) to[j] = from_f<T>(a.scale * o[i][j]);
+            }
         }
         const Factor f = factor(m * log_decay(l));
 #pragma unroll

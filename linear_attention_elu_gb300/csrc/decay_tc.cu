@@ -73,10 +73,8 @@ struct Misc {
     int first[128];             // and that of each column, counted over the segment
     alignas(16) float tab[32];  // f^(31 - j), by the column's place in its block; read 16 bytes at a time
     alignas(16) uint32_t mask[512];   // diagonal block, [pair of columns / 2][row][2]: which scores take part
-    alignas(16) float diag[1024];     // where there is room: its factors, [column / 4][row][4]
+    alignas(16) float diag[1024];     // decay_kv_kernel alone: its factors, [column / 4][row][4]
 };
-// Two column blocks leave no room for the diagonal's factors.
-constexpr bool diag_table(int kU) { return kU == 1; }
 constexpr uint32_t misc_bytes(bool table) { return table ? 7 * 1024 : 3 * 1024; }
 static_assert(sizeof(Misc) <= misc_bytes(true) && offsetof(Misc, diag) <= misc_bytes(false), "barriers and tables");
 
@@ -87,7 +85,7 @@ template <int kT, int kU, int kTerms> struct Smem {
     static constexpr uint32_t kW = kC0 + kStages * kU * kTile;        // [unit][term]
     static constexpr uint32_t kS = kW + kU * kTerms * kTile;          // [unit], 64 kT rows
     static constexpr uint32_t kMisc = kS + kU * kT * kTile / 2;
-    static constexpr int kBytes = kMisc + misc_bytes(diag_table(kU));
+    static constexpr int kBytes = kMisc + misc_bytes(false);
     static constexpr int kPerSm = kBytes <= 113 * 1024 && kU == 1 ? 2 : 1;
 };
 static_assert(Smem<1, 1, 2>::kPerSm == 2 && Smem<1, 1, 3>::kPerSm == 2, "two CTAs per SM");
@@ -330,8 +328,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
-// Four scores of a diagonal block, columns j .. j + 3, to packed P: by the table, or by an
-// exponential each. Scores that take no part are cleared as bits: their products may be anything.
+// Four scores of a diagonal block, columns j .. j + 3, to packed P. Scores that take no part are
+// cleared as bits: their products may be anything. kTable: factors from the table (one CTA
+// per SM; with two the table's reads from shared memory cost more than the exponentials: B=1
+// N=65536 H=16 D=64 forward 151 us against 148, the backward of B=8 N=4096 H=8 D=64 with one 91
+// against 92.5).
 template <bool kRev, bool kTable>
 __device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float own, const Misc& m, uint32_t* p) {
     const int lane = threadIdx.x & 31;
@@ -354,44 +355,41 @@ __device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFac
 }
 
 // Scores of block column `blk` (bm in the order of summation) to packed P, over the first
-// half of their columns: no other warp reads or writes those. kCols at a time: 16, in rolled
-// loops, where the state's registers leave no room for more (what the compiler keeps of
-// unrolled ones from chunk to chunk is spilled, and does not fit the little L1 that two
-// CTAs leave: backwards in time the call took 1.8 times as long).
-template <bool kRev, bool kTable, int kCols>
+// half of their columns: no other warp reads or writes those. Loops are kept rolled: what
+// the compiler keeps of unrolled ones from chunk to chunk is spilled, and does not fit the
+// little L1 that two CTAs leave (backwards in time the call took 1.8 times as long).
+template <bool kRev, bool kTable>
 __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
     const int lane = threadIdx.x & 31;
     const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane * rf.diag;
     const uint64_t r2 = pk2(r, r);
     const uint32_t at = tm_p + 32 * blk;
 #pragma unroll 1
-    for (int first = 0; first < 32; first += kCols) {
-        uint32_t v[kCols], p[kCols / 2];
+    for (int half = 0; half < 32; half += 16) {
+        uint32_t v[16], p[8];
         if (bm > qm) {
 #pragma unroll
-            for (int e = 0; e < kCols / 2; ++e) p[e] = 0u;
+            for (int e = 0; e < 8; ++e) p[e] = 0u;
         } else {
-#pragma unroll
-            for (int e = 0; e < kCols; e += 16) tmem_ld16(at + first + e, *reinterpret_cast<uint32_t(*)[16]>(v + e));
+            tmem_ld16(at + half, v);
             tmem_ld_wait();
-            if (kRev && 32 * blk + first + kCols > cut)        // later tokens that the sequence does not have
+            if (kRev && 32 * blk + half + 16 > cut)        // later tokens that the sequence does not have
 #pragma unroll
-                for (int e = 0; e < kCols; ++e)
-                    if (32 * blk + first + e >= cut) v[e] = 0u;
+                for (int e = 0; e < 16; ++e)
+                    if (32 * blk + half + e >= cut) v[e] = 0u;
             if (bm < qm) {
 #pragma unroll
-                for (int e = 0; e < kCols; e += 4) {
-                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.tab + first + e);
+                for (int e = 0; e < 16; e += 4) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.tab + half + e);
                     p[e / 2] = pack2(mul2(mul2(pair2(v + e), f.x), r2));
                     p[e / 2 + 1] = pack2(mul2(mul2(pair2(v + e + 2), f.y), r2));
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < kCols; e += 4) diagonal4<kRev, kTable>(v + e, first + e, rf, own, m, p + e / 2);
+                for (int e = 0; e < 16; e += 4) diagonal4<kRev, kTable>(v + e, half + e, rf, own, m, p + e / 2);
             }
         }
-        if constexpr (kCols == 16) tmem_st8(at + first / 2, p);
-        else tmem_st16(at, p);
+        tmem_st8(at + half / 2, p);
     }
 }
 
@@ -476,7 +474,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     }
     if (tid < 128) m.first[tid] = kNone;
     const float l = a.decay[pl.h], l2 = log2_decay(l);
-    init_tables<kRev, diag_table(kU)>(m, l2);
+    init_tables<kRev, false>(m, l2);
     if (warp == kWarps) {
         tmem_alloc(&m.tmem_slot, kCols);
         tmem_relinquish();
@@ -641,7 +639,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             tc_fence_after();
 #pragma unroll 1
             for (int bm = g4; bm < 4; bm += 2 * kU)
-                scores_to_p<kRev, diag_table(kU), 16>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
+                scores_to_p<kRev, false>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             auto hand_over = [&]() {
                 tmem_st_wait();
@@ -1011,7 +1009,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             if (!(ok = warp_wait(&m.p_full, i & 1, max_spin))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int bm = g; bm < 4; bm += 2) scores_to_p<true, true, 32>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
+            for (int bm = g; bm < 4; bm += 2) scores_to_p<true, true>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
