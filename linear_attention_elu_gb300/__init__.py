@@ -857,7 +857,7 @@ def la_selective_scan_step(x, step, A, Bm, Cm, S, D=None, z=None, dt_bias=None, 
 
 def _decay_args(q, k, v, decay, dims):
     """Checks shared by the prompt (dims = 4: [B,H,N,D]) and the step (3: [B,H,D]); returns
-    (device index, shape of q, Dv)."""
+    (device index, shape of q, Dv, element type)."""
     qshape, vshape, dtype = q.shape, v.shape, q.dtype
     if len(qshape) != dims or k.shape != qshape or len(vshape) != dims or vshape[:-1] != qshape[:-1]:
         lead = "B,H,N" if dims == 4 else "B,H"
@@ -865,20 +865,25 @@ def _decay_args(q, k, v, decay, dims):
                          f"{tuple(k.shape)}, {tuple(vshape)}")
     if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v must share one dtype")
-    _dt(q)
+    dt = _dt(q)
     index = _device_of(q)
-    if decay.dtype != torch.float32 or decay.dim() != 1 or decay.shape[0] != qshape[1] or not decay.is_contiguous():
+    if decay.dtype != torch.float32 or decay.shape != qshape[1:2] or not decay.is_contiguous():
         raise ValueError("decay must be contiguous float32 [H]")
-    _same_device(index, k, v, decay)
-    return index, qshape, vshape[-1]
+    if k.get_device() != index or v.get_device() != index or decay.get_device() != index:
+        raise ValueError("tensors must be on one CUDA device")
+    return index, qshape, vshape[-1], dt
 
 
-def _row_strides(*named):
-    """The strides of all axes but the last (whose values must be adjacent), as the C entries take them."""
-    out = []
-    for t, what in named:
-        out += _inner_adjacent(t, what, 1)[:-1]
-    return (ctypes.c_int64 * len(out))(*out)
+# Host arrays of strides: of the axes but the last, tensor by tensor.
+_I64x8, _I64x12, _I64x21 = (ctypes.c_int64 * n for n in (8, 12, 21))
+
+
+def _rows(t, what):
+    """Strides of a tensor whose last axis' values must be adjacent."""
+    s = t.stride()
+    if s[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: a row's values must be adjacent (strides {s})")
+    return s
 
 
 def _typed_like(t, ref, what):
@@ -893,7 +898,7 @@ def la_decay_attn_fwd(q, k, v, decay, scale=1.0, lengths=None, S0=None, S_out=No
     transposed to head-major; a row's values adjacent). decay: float32 [H], the logarithm of the factor
     per token. S0, S_out [B,H,Dk,Dv] float32 (S_out may be S0). lengths (int32 [B]): rows past them are
     left as they are (zero where the call makes o). Returns o [B,H,N,Dv]."""
-    index, (B, H, N, Dk), Dv = _decay_args(q, k, v, decay, 4)
+    index, (B, H, N, Dk), Dv, dt = _decay_args(q, k, v, decay, 4)
     _f32_state(S0, (B, H, Dk, Dv), "S0")
     _f32_state(S_out, (B, H, Dk, Dv), "S_out")
     _check_lengths(lengths, B)
@@ -905,10 +910,11 @@ def la_decay_attn_fwd(q, k, v, decay, scale=1.0, lengths=None, S0=None, S_out=No
         if ws is None:
             ws = workspace(LA_OP_DECAY_ATTN, B, H, N, Dk, Dv, q.dtype, q.device)
         _same_device(index, lengths, S0, S_out, o, ws)
+        sq, sk, sv, so = _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _rows(o, "o")
         _check(_lib.la_decay_attn_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), scale, _addr(lengths), _addr(S0),
-            _addr(S_out), o.data_ptr(), _row_strides((q, "q"), (k, "k"), (v, "v"), (o, "o")), B, H, N, Dk, Dv,
-            _dt(q), ws.data_ptr(), _bytes(ws), _raw_stream(index)), "la_decay_attn_fwd")
+            _addr(S_out), o.data_ptr(), _I64x12(*sq[:3], *sk[:3], *sv[:3], *so[:3]), B, H, N, Dk, Dv, dt,
+            ws.data_ptr(), _bytes(ws), _raw_stream(index)), "la_decay_attn_fwd")
     return o
 
 
@@ -918,7 +924,7 @@ def la_decay_attn_bwd(q, k, v, dout, decay, scale=1.0, lengths=None, dq=None, dk
 
     Strides as there; dq, dk and dv may be given as column ranges of one projection gradient. Rows past
     the lengths are left as they are (zero where the call makes them)."""
-    index, (B, H, N, Dk), Dv = _decay_args(q, k, v, decay, 4)
+    index, (B, H, N, Dk), Dv, dt = _decay_args(q, k, v, decay, 4)
     _typed_like(dout, v, "dout")
     _check_lengths(lengths, B)
     with _scope(index, stream):
@@ -931,28 +937,33 @@ def la_decay_attn_bwd(q, k, v, dout, decay, scale=1.0, lengths=None, dq=None, dk
         if ws is None:
             ws = workspace(LA_OP_DECAY_ATTN_BWD, B, H, N, Dk, Dv, q.dtype, q.device)
         _same_device(index, dout, lengths, dq, dk, dv, ws)
-        strides = _row_strides((q, "q"), (k, "k"), (v, "v"), (dout, "dout"), (dq, "dq"), (dk, "dk"), (dv, "dv"))
+        strides = _I64x21(*(s for t, what in ((q, "q"), (k, "k"), (v, "v"), (dout, "dout"), (dq, "dq"), (dk, "dk"), (dv, "dv"))
+                            for s in _rows(t, what)[:3]))
         _check(_lib.la_decay_attn_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), decay.data_ptr(), scale, _addr(lengths),
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), strides, B, H, N, Dk, Dv, _dt(q), ws.data_ptr(), _bytes(ws),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), strides, B, H, N, Dk, Dv, dt, ws.data_ptr(), _bytes(ws),
             _raw_stream(index)), "la_decay_attn_bwd")
     return dq, dk, dv
 
 
 def la_decay_attn_step(q, k, v, decay, S, scale=1.0, o=None, stream=None):
     """One token of la_decay_attn_fwd: q, k [B,H,Dk], v [B,H,Dv]; S [B,H,Dk,Dv] in place; returns o [B,H,Dv]."""
-    index, (B, H, Dk), Dv = _decay_args(q, k, v, decay, 3)
+    index, (B, H, Dk), Dv, dt = _decay_args(q, k, v, decay, 3)
     if S is None:
         raise ValueError("S must be given")
     _f32_state(S, (B, H, Dk, Dv), "S")
+    if S.get_device() != index:
+        raise ValueError("tensors must be on one CUDA device")
     with _scope(index, stream):
         if o is None:
             o = torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
-        _typed_like(o, v, "o")
-        _same_device(index, S, o)
+        else:
+            _typed_like(o, v, "o")
+            _same_device(index, o)
+        sq, sk, sv, so = _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _rows(o, "o")
         _check(_lib.la_decay_attn_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), scale, S.data_ptr(), o.data_ptr(),
-            _row_strides((q, "q"), (k, "k"), (v, "v"), (o, "o")), B, H, Dk, Dv, _dt(q), _raw_stream(index)),
+            _I64x8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), B, H, Dk, Dv, dt, _raw_stream(index)),
             "la_decay_attn_step")
     return o
 
@@ -971,19 +982,19 @@ def group_norm_workspace(B, N, C, G, device=None):
 
 
 def _norm_args(x, groups, w, b, z):
-    """Checks shared by both directions; returns (device index, B, N, C)."""
+    """Checks shared by both directions; returns (device index, B, N, C, element type)."""
     shape, dtype = x.shape, x.dtype
     if len(shape) != 3 or groups < 1 or shape[2] % groups:
         raise ValueError(f"expected x [B,N,C] with C a multiple of groups; got {tuple(shape)}, {groups} groups")
-    _dt(x)
+    dt = _dt(x)
     index = _device_of(x)
-    for t, what in ((w, "w"), (b, "b")):
-        if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != shape[2] or not t.is_contiguous()):
-            raise ValueError(f"{what} must be contiguous [C] in x's dtype")
+    for t in (w, b):
+        if t is not None and (t.dtype != dtype or t.shape != shape[2:] or not t.is_contiguous()):
+            raise ValueError("w and b must be contiguous [C] in x's dtype")
     if z is not None:
         _typed_like(z, x, "z")
     _same_device(index, w, b, z)
-    return index, shape[0], shape[1], shape[2]
+    return index, shape[0], shape[1], shape[2], dt
 
 
 def la_group_norm_fwd(x, groups, w=None, b=None, z=None, silu=False, eps=1e-5, y=None, stats=None,
@@ -993,22 +1004,29 @@ def la_group_norm_fwd(x, groups, w=None, b=None, z=None, silu=False, eps=1e-5, y
     silu: act is the silu (else the identity); z [B,N,C]: the gate. A row of its own per sample (the
     heads of an attention output, tokens as samples) is N = 1. Rows may be strided. Returns y, or
     (y, stats) with return_stats=True: stats [B,groups,2] float32 (mean, inverse deviation)."""
-    index, B, N, C = _norm_args(x, groups, w, b, z)
-    xs = _inner_adjacent(x, "x", 1)
-    zs = _inner_adjacent(z, "z", 1) if z is not None else (0, 0)
+    index, B, N, C, dt = _norm_args(x, groups, w, b, z)
+    xs = _rows(x, "x")
+    zs = _rows(z, "z") if z is not None else (0, 0)
     with _scope(index, stream):
         if y is None:
             y = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
-        ys = _like(y, x, 1)
-        if stats is None and return_stats:
+        else:
+            _typed_like(y, x, "y")
+            _same_device(index, y)
+        ys = _rows(y, "y")
+        if stats is not None:
+            _f32_state(stats, (B, groups, 2), "stats")
+            _same_device(index, stats)
+        elif return_stats:
             stats = torch.empty((B, groups, 2), dtype=torch.float32, device=x.device)
-        _f32_state(stats, (B, groups, 2), "stats")
-        if ws is None and N != 1:
-            ws = group_norm_workspace(B, N, C, groups, x.device)
-        _same_device(index, y, stats, ws)
+        if ws is None:
+            if N != 1:
+                ws = group_norm_workspace(B, N, C, groups, x.device)
+        else:
+            _same_device(index, ws)
         _check(_lib.la_group_norm_fwd(
             x.data_ptr(), xs[0], xs[1], _addr(w), _addr(b), _addr(z), zs[0], zs[1], y.data_ptr(), ys[0], ys[1],
-            _addr(stats), B, N, C, groups, _dt(x), 1 if silu else 0, eps, _addr(ws), _bytes(ws),
+            _addr(stats), B, N, C, groups, dt, 1 if silu else 0, eps, _addr(ws), _bytes(ws),
             _raw_stream(index)), "la_group_norm_fwd")
     return (y, stats) if return_stats else y
 
@@ -1018,22 +1036,25 @@ def la_group_norm_bwd(x, groups, dy, stats, w=None, b=None, z=None, silu=False, 
     """Gradients (dx, dw, db, dz) of sum(y * dy) of la_group_norm_fwd; stats: as it returns them.
 
     dx, dz [B,N,C] in x's dtype (dz None without a gate); dw, db float32 [C] (None without w, b)."""
-    index, B, N, C = _norm_args(x, groups, w, b, z)
+    index, B, N, C, dt = _norm_args(x, groups, w, b, z)
     _typed_like(dy, x, "dy")
     if stats is None:
         raise ValueError("stats must be given")
     _f32_state(stats, (B, groups, 2), "stats")
     if dz is not None and z is None:
         raise ValueError("dz needs z")
-    xs, gs = _inner_adjacent(x, "x", 1), _inner_adjacent(dy, "dy", 1)
-    zs = _inner_adjacent(z, "z", 1) if z is not None else (0, 0)
+    xs, gs = _rows(x, "x"), _rows(dy, "dy")
+    zs = _rows(z, "z") if z is not None else (0, 0)
     with _scope(index, stream):
         if dx is None:
             dx = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
         if dz is None and z is not None:
             dz = torch.empty((B, N, C), dtype=x.dtype, device=x.device)
-        dxs = _like(dx, x, 1)
-        dzs = _like(dz, x, 1) if dz is not None else (0, 0)
+        _typed_like(dx, x, "dx")
+        dxs, dzs = _rows(dx, "dx"), (0, 0)
+        if dz is not None:
+            _typed_like(dz, x, "dz")
+            dzs = _rows(dz, "dz")
         dw = torch.empty(C, dtype=torch.float32, device=x.device) if w is not None else None
         db = torch.empty(C, dtype=torch.float32, device=x.device) if b is not None else None
         if ws is None:
@@ -1042,7 +1063,7 @@ def la_group_norm_bwd(x, groups, dy, stats, w=None, b=None, z=None, silu=False, 
         _check(_lib.la_group_norm_bwd(
             x.data_ptr(), xs[0], xs[1], _addr(w), _addr(b), _addr(z), zs[0], zs[1], dy.data_ptr(), gs[0], gs[1],
             stats.data_ptr(), dx.data_ptr(), dxs[0], dxs[1], _addr(dz), dzs[0], dzs[1], _addr(dw), _addr(db), B, N,
-            C, groups, _dt(x), 1 if silu else 0, _addr(ws), _bytes(ws), _raw_stream(index)), "la_group_norm_bwd")
+            C, groups, dt, 1 if silu else 0, _addr(ws), _bytes(ws), _raw_stream(index)), "la_group_norm_bwd")
     return dx, dw, db, dz
 
 

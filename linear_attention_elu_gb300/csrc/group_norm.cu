@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 3 : 1) rows_fwd_kernel(cons
 
 // partial: [gridDim.x][2][C], the block's sums of h xh and of h.
 template <typename T, int V, int K, int kL>
-__global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) rows_bwd_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, K > 1 ? 1 : V == 4 && kL ? 3 : 2) rows_bwd_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ uint4 smem[];                // [stage][x, dy, z][K][thread]; then the rows' sums
     constexpr int kS = kStages<K>;
     const RowPlace<V, K, kL> t(a);
@@ -436,24 +436,27 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) rows_bwd_kernel(cons
         }
 }
 
-// dw, db = sums over the blocks of partial [blocks][2][C], in order within 32 slices.
-__global__ void __launch_bounds__(1024) weights_kernel(const float* partial, float* dw, float* db, int64_t blocks, int C) {
-    __shared__ float red[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    tcc::pdl_wait();
+// dw (which = 0) or db (1), channels 32 block .. of them: sums over the blocks of partial
+// [blocks][2][C], in order within a slice per warp. red: [warps][33].
+__device__ __forceinline__ void sum_weights(const float* partial, float* to, int64_t blocks, int C, int block, int which, float* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, c = block * 32 + lane;
     float v = 0.f;
     if (c < C)
 #pragma unroll 8
-        for (int64_t i = warp; i < blocks; i += 32) v += partial[(2 * i + blockIdx.y) * C + c];
-    red[warp][lane] = v;
+        for (int64_t i = warp; i < blocks; i += warps) v += partial[(2 * i + which) * C + c];
+    red[warp * 33 + lane] = v;
     __syncthreads();
-    float* to = blockIdx.y ? db : dw;
     if (warp == 0 && c < C && to) {
         v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v += red[i][lane];
+        for (int i = 0; i < warps; ++i) v += red[i * 33 + lane];
         to[c] = v;
     }
+}
+
+__global__ void __launch_bounds__(1024) weights_kernel(const float* partial, float* dw, float* db, int64_t blocks, int C) {
+    __shared__ float red[32 * 33];
+    tcc::pdl_wait();
+    sum_weights(partial, blockIdx.y ? db : dw, blocks, C, blockIdx.x, blockIdx.y, red);
 }
 
 // The other form's block: rows n0 .. n1 of sample b, the channels of gb groups from c0; a
@@ -482,8 +485,8 @@ template <int V> __device__ __forceinline__ Block block_of_rows(const NormArgs& 
 
 constexpr int kMost = 1024;           // threads, and channels of a group
 constexpr int kNarrow = 128;          // channels of a group of single tokens without whole 16-byte pieces
-constexpr int kTileRows = 8;          // of the statistics: a mean, and squares about it
-constexpr int kRows = 4;              // rows on the way per thread of the other passes
+constexpr int kStatsRows = 8;         // rows on the way per thread of the statistics
+constexpr int kRows = 4;              // and of the other passes
 
 // The group of each of a thread's V channels from c on.
 template <int V> struct Groups {
@@ -502,48 +505,40 @@ template <int V> struct Groups {
 // partial: [B chunks][G][2], mean of the block's values of a group and sum of squares about it.
 template <typename T, int V>
 __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) stats_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ uint4 smem[];                // [2 tiles][row][thread]; then [subs][cols] means, squares
+    extern __shared__ uint4 smem[];                // [stage][thread]; then [subs][cols] means, squares
     float* sm = reinterpret_cast<float*>(smem);
     const Block k = block_of_rows<V>(a);
     const Ring<T, V> ring(smem);
-    Vals<V> mean = all<V>(0.f), m2 = all<V>(0.f);
+    // Sums of the differences to the thread's first row, and of their squares. That row c is one
+    // of its n values of a channel, so (c - mean)^2 is at most M, the sum of squares about the
+    // mean, and what is subtracted from the squares below at most n M: n 2^-24 of M is lost at
+    // worst, 2^-23 where c is no outlier.
+    Vals<V> first = all<V>(0.f), sum = all<V>(0.f), sq = all<V>(0.f);
+    int n = 0;
     if (k.on) {
-        const Vals<V> minus = all<V>(-1.f);
         const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
-        const int step = k.subs * kTileRows;
-        auto fetch = [&](int i, int row) {
-#pragma unroll
-            for (int u = 0; u < kTileRows; ++u)
-                if (row + u * k.subs < k.n1) ring.fetch((i & 1) * kTileRows + u, x + (row + u * k.subs) * a.x_ts);
+        int row = k.n0 + k.sub;
+        auto fetch = [&](int i, int r) {
+            if (r < k.n1) ring.fetch(i % kStatsRows, x + r * a.x_ts);
             ring.commit();
         };
-        int n = 0, row = k.n0 + k.sub;
-        fetch(0, row);
-        for (int i = 0; row < k.n1; ++i, row += step) {
-            fetch(i + 1, row + step);
-            ring.template wait<1>();
-            const int m = min((k.n1 - row + k.subs - 1) / k.subs, kTileRows);
-            // The tile's mean and squares about it, joined to those before.
-            Vals<V> tm = all<V>(0.f), tq = all<V>(0.f);
 #pragma unroll
-            for (int u = 0; u < kTileRows; ++u)
-                if (u < m) tm = tm + ring.get((i & 1) * kTileRows + u, x + (row + u * k.subs) * a.x_ts);
-            tm = tm * all<V>(__fdividef(1.f, (float)m));
-            const Vals<V> off = tm * minus;
-#pragma unroll
-            for (int u = 0; u < kTileRows; ++u)
-                if (u < m) {
-                    const Vals<V> d = ring.get((i & 1) * kTileRows + u, x + (row + u * k.subs) * a.x_ts) + off;
-                    tq = fma(d, d, tq);
-                }
-            const float share = __fdividef((float)m, (float)(n + m));
-            const Vals<V> d = fma(mean, minus, tm);
-            mean = fma(d, all<V>(share), mean);
-            m2 = m2 + fma(d * d, all<V>(share * n), tq);
-            n += m;
+        for (int i = 0; i < kStatsRows - 1; ++i) fetch(i, row + i * k.subs);
+        if (row < k.n1) {
+            ring.template wait<kStatsRows - 2>();
+            first = ring.get(0, x + row * a.x_ts) * all<V>(-1.f);
+        }
+        for (; row < k.n1; ++n, row += k.subs) {
+            ring.template wait<kStatsRows - 2>();
+            fetch(n + kStatsRows - 1, row + (kStatsRows - 1) * k.subs);
+            const Vals<V> d = ring.get(n % kStatsRows, x + row * a.x_ts) + first;
+            sum = sum + d;
+            sq = fma(d, d, sq);
         }
         ring.template wait<0>();
     }
+    const Vals<V> off = sum * all<V>(n > 0 ? 1.f / n : 0.f), minus = all<V>(-1.f);
+    const Vals<V> mean = fma(first, minus, off), m2 = fma(sum * minus, off, sq);
     __syncthreads();
     tcc::pdl_launch_dependents();
     const int rows = k.n1 - k.n0, whole = rows / k.subs, more = rows - whole * k.subs;   // rows of a thread
@@ -552,7 +547,8 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) sta
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             sm_mean[k.sub * k.cols + k.c + i] = mean.get(i);
-            sm_sq[k.sub * k.cols + k.c + i] = m2.get(i);
+            const float q = m2.get(i);
+            sm_sq[k.sub * k.cols + k.c + i] = q < 0.f ? 0.f : q;   // a comparison, so that NaN stays NaN
         }
     __syncthreads();
     const float inv = 1.f / rows;
@@ -714,9 +710,18 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8
     }
 }
 
+// The blocks past the rows' sum the weights' gradients meanwhile.
 template <typename T, int V>
 __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8 ? 2 : 3) apply_bwd_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ uint4 smem[];                // [stage][x, dy, z][thread]; [groups][2]: -means of w h and of w h xh
+    const int extra = (int)blockIdx.x - a.B * a.chunks;
+    if (extra >= 0) {
+        tcc::pdl_wait();
+        if (blockIdx.y == 0)
+            sum_weights(a.partial, extra & 1 ? a.db : a.dw, (int64_t)a.B * a.chunks, a.C, extra >> 1, extra & 1,
+                        reinterpret_cast<float*>(smem));
+        return;
+    }
     const Block k = block_of_rows<V>(a);
     const Ring<T, V> ring(smem);
     float* sm = reinterpret_cast<float*>(smem + (V > 1 ? kRows * 3 * blockDim.x : 0));
@@ -738,7 +743,6 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8
     };
 #pragma unroll
     for (int i = 0; i < kRows - 1; ++i) fetch(i, row + i * k.subs);
-    tcc::pdl_launch_dependents();
     tcc::pdl_wait();
     const float2* parts = reinterpret_cast<const float2*>(a.partial + (int64_t)a.B * a.chunks * 2 * a.C);
     const float inv = -1.f / ((float)a.N * a.Cg);
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8
 // ------------------------------------------------------------------ host side
 
 // Blocks of the one-token backward at most, each of which leaves its sums.
-int row_blocks() { return 2 * tcc::sm_count(); }
+int row_blocks() { return 3 * tcc::sm_count(); }
 
 // Rows of a block of the other form: at least 16, and so many that the blocks run at once, as
 // many on an SM as its registers hold (a second wave for a few of them would cost as much
@@ -824,7 +828,7 @@ cudaError_t launch_rows(NormArgs a, cudaStream_t st) {
         return cudaPeekAtLastError();
     } else {
         if ((e = tcc::ensure_smem_optin(rows_bwd_kernel<T, V, K, kL>, smem, optin)) != cudaSuccess) return e;
-        const int64_t most = row_blocks(), blocks = tiles < most ? tiles : most;
+        const int64_t most = V == 4 && kL ? row_blocks() : row_blocks() / 3 * 2, blocks = tiles < most ? tiles : most;
         rows_bwd_kernel<T, V, K, kL><<<dim3((unsigned)blocks, columns), threads, smem, st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess || (!a.dw && !a.db)) return e;
         return scan::launch_after(weights_kernel, dim3((a.C + 31) / 32, 2), 1024, 0, st, true, a.partial, a.dw, a.db, blocks, a.C);
@@ -860,13 +864,13 @@ cudaError_t launch_blocks(NormArgs a, cudaStream_t st) {
     auto ring = [&](int places) { return V > 1 ? places * threads * 16 : 0; };
     auto larger = [](int p, int q) { return p > q ? p : q; };
     static std::atomic<int> optin[2][tcc::kMaxDevices];
-    constexpr int kMostRing = V > 1 ? 2 * kTileRows * kThreads * 16 : 0, kMostSums = 2 * 4 * kThreads * V * (V == 1 ? 4 : 1);
+    constexpr int kMostRing = V > 1 ? 3 * kRows * kThreads * 16 : 0, kMostSums = 2 * 4 * kThreads * V * (V == 1 ? 4 : 1);
     cudaError_t e;
     if constexpr (!kBackward) {
         if ((e = tcc::ensure_smem_optin(stats_kernel<T, V>, kMostRing + kMostSums, optin[0])) != cudaSuccess ||
             (e = tcc::ensure_smem_optin(apply_kernel<T, V>, kMostRing + kMostSums, optin[1])) != cudaSuccess)
             return e;
-        stats_kernel<T, V><<<grid, threads, larger(ring(2 * kTileRows), sums), st>>>(a);
+        stats_kernel<T, V><<<grid, threads, larger(ring(kStatsRows), sums), st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         return scan::launch_after(apply_kernel<T, V>, grid, threads, ring(2 * kRows) + group, st, true, a);
     } else {
@@ -875,11 +879,10 @@ cudaError_t launch_blocks(NormArgs a, cudaStream_t st) {
             return e;
         sums_kernel<T, V><<<grid, threads, larger(ring(3 * kRows), sums), st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
-        if ((e = scan::launch_after(apply_bwd_kernel<T, V>, grid, threads, ring(3 * kRows) + group, st, true, a)) != cudaSuccess ||
-            (!a.dw && !a.db))
-            return e;
-        return scan::launch_after(weights_kernel, dim3((a.C + 31) / 32, 2), 1024, 0, st, true, a.partial, a.dw, a.db,
-                                  (int64_t)a.B * a.chunks, a.C);
+        dim3 more = grid;
+        if (a.dw || a.db) more.x += 2 * ((a.C + 31) / 32);
+        return scan::launch_after(apply_bwd_kernel<T, V>, more, threads, larger(ring(3 * kRows) + group, 33 * 4 * threads / 32), st,
+                                  true, a);
     }
 }
 
