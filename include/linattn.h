@@ -112,7 +112,8 @@ la_status la_workspace_size(la_op op, int B, int H, int N, int Dk, int Dv, la_dt
  * graph planning and for counting launches in a timed region.
  * LA_OP_SELECTIVE_SCAN: for one group and 16-byte aligned rows; a call with more
  * groups or unaligned rows makes one launch or three by its own cut.
- * LA_OP_DECAY_ATTN(_BWD): for 16-byte aligned rows.
+ * LA_OP_DECAY_ATTN(_BWD): for 16-byte aligned rows and a state that is not updated in place
+ * (which can make one launch more).
  */
 la_status la_launch_count(la_op op, int B, int H, int N, int Dk, int Dv, la_dtype dt,
                           int* launches);

@@ -80,7 +80,12 @@ def _adjacent(t):
 
 class _DecayAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, decay, scale, lengths, o):
+    def forward(ctx, q, k, v, decay, scale, lengths, token_major):
+        o = None
+        if token_major:
+            B, H, N, Dv = v.shape
+            make = torch.empty if lengths is None else torch.zeros
+            o = make((B, N, H, Dv), dtype=v.dtype, device=v.device).transpose(1, 2)
         o = la_decay_attn_fwd(q, k, v, decay, scale, lengths, o=o)
         ctx.save_for_backward(q, k, v, decay, lengths)
         ctx.scale = scale
@@ -102,12 +107,7 @@ def decay_attention(q, k, v, decay, scale=1.0, lengths=None, token_major=False):
     if decay.requires_grad:
         raise ValueError("the decay is a constant: no gradient with respect to it")
     q, k, v = (_adjacent(t) for t in (q, k, v))
-    o = None
-    if token_major:
-        B, H, N, Dv = v.shape
-        make = torch.empty if lengths is None else torch.zeros
-        o = make((B, N, H, Dv), dtype=v.dtype, device=v.device).transpose(1, 2)
-    return _DecayAttention.apply(q, k, v, decay, float(scale), lengths, o)
+    return _DecayAttention.apply(q, k, v, decay, float(scale), lengths, bool(token_major))
 
 
 class _GroupNorm(torch.autograd.Function):

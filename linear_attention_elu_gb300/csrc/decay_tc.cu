@@ -696,7 +696,11 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     if (warp == kWarps) tmem_dealloc(tmem, kCols);
 }
 
-// First pass, of one sum or two: the end state from zero of each segment but the last.
+// First pass, of one sum or two: the end state from zero of each segment but the last. Shared
+// memory bounds it, the operand reads of (4) before all; so a narrow head's state is summed
+// transposed, the first two terms of w C stacked as the 128 rows of one product (8 products of
+// 6 KB of operands a chunk for 16), and the terms' sums joined at the end. The third term takes
+// columns of its own, with the second in the rows that nobody reads.
 template <int kT, int kU, int kTerms>
 __global__ void __launch_bounds__(32 * (kU * kWork + 1), SumSmem<kT, kU, kTerms>::kPerSm)
 decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_constant__ CUtensorMap cmap0,
@@ -709,6 +713,8 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
     const CUtensorMap &bmap = second ? bmap1 : bmap0, &cmap = second ? cmap1 : cmap0;
     using L = SumSmem<kT, kU, kTerms>;
     constexpr int kWarps = kU * kWork;
+    constexpr bool kStacked = kT == 1 && kU == 1;
+    constexpr uint32_t kCols = kStacked && kTerms == 2 ? 64 : 128;
     extern __shared__ __align__(1024) uint8_t base[];
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto btile = [&](int i) { return base + L::kB + (i % L::kStages) * kT * kTile; };
@@ -732,7 +738,7 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
         fence_mbar_init();
     }
     if (warp == kWarps) {
-        tmem_alloc(&m.tmem_slot, 64 * kU);
+        tmem_alloc(&m.tmem_slot, kCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -768,7 +774,18 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
             for (int i = 0; i < pl.nc; ++i) {
                 if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
                 tc_fence_after();
-                issue_state<kU, kTerms>(tmem, step_desc(br, (i % L::kStages) * kT * kTile), smem_u32(base) + L::kW);
+                const uint64_t bt = step_desc(br, (i % L::kStages) * kT * kTile);
+                if constexpr (kStacked) {
+                    constexpr uint32_t id = idesc_bf16_f32(128, 64, true, true);
+                    const uint64_t w = rows_desc(smem_u32(base) + L::kW);
+#pragma unroll
+                    for (int part = 0; part < kTerms - 1; ++part)
+#pragma unroll
+                        for (int k = 0; k < kC / 16; ++k)
+                            mma_bf16(tmem + 64 * part, step_desc(w, part * kTile + k * 2048), step_desc(bt, k * 2048), id, k > 0);
+                } else {
+                    issue_state<kU, kTerms>(tmem, bt, smem_u32(base) + L::kW);
+                }
                 mma_commit(&m.s_full);
                 if (!(ok = mbar_wait(&m.s_full, i & 1, max_spin))) break;
                 if (i + L::kStages < pl.nc) load();
@@ -781,7 +798,8 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
         __syncwarp();
     } else {
         const int q = warp & 3, u = warp >> 3, g = (warp >> 2) & 1, row = 32 * q + lane;
-        const bool has_state = q < 2 * kT;
+        const bool has_state = kStacked || q < 2 * kT;
+        const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + 64 * u + 32 * g;
         uint8_t* terms = base + L::kW + u * kTerms * kTile;
         const Factor whole = factor(kC * log_decay(l));
         float st[32];
@@ -800,22 +818,34 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
             warp_arrive(&m.prep);
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
-            if (has_state)
-                join_state(tmem + ((uint32_t)(32 * q) << 16) + 64 * u + 32 * g,
-                           rev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
+            if (has_state) join_state(tm, rev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
+            if (kStacked && kTerms == 3 && q >= 2) join_state(tm + 64, {1.f, 0.f}, st);
         }
         const int c0 = pl.col0 + 64 * u + 32 * g;
-        float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc + (int64_t)row * a.Dc + c0;
-        if (ok && has_state && row < a.Da)
+        float* to = a.seeds + (((int64_t)pl.b * a.H + pl.h) * a.nseg + pl.seg) * a.Da * a.Dc;
+        if constexpr (kStacked) {
+            // Rows 64 .. (terms after the first) to those of the first, column 32 g + k of row `row`.
+            float* other = reinterpret_cast<float*>(base + L::kW) + 32 * g * 64 + (row & 63);
+            if (q >= 2)
+#pragma unroll
+                for (int k = 0; k < 32; ++k) other[64 * k] = st[k];
+            named_bar(1, 32 * kWarps);             // every working warp comes here, whatever its waits said
+            if (ok && q < 2 && row < a.Dc)
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    if (32 * g + k < a.Da) to[(int64_t)(32 * g + k) * a.Dc + row] = st[k] + other[64 * k];
+        } else if (ok && has_state && row < a.Da) {
+            to += (int64_t)row * a.Dc + c0;
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
                 if (c0 + k < a.Dc) *reinterpret_cast<float4*>(to + k) = make_float4(st[k], st[k + 1], st[k + 2], st[k + 3]);
+        }
     }
     if (!ok) report_timeout(hdr);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWarps) tmem_dealloc(tmem, 64 * kU);
+    if (warp == kWarps) tmem_dealloc(tmem, kCols);
 }
 
 // dk and dv of one head in one pass backwards in time (Dk, Dv <= 64). The two sums take the
@@ -1159,7 +1189,7 @@ int backward_segments(int64_t BH, int N, int Dk, int Dv) {
     double least = 1e30;
     for (int n = 1; n <= 64 && n <= chunks; ++n) {
         const int per = (chunks + n - 1) / n;
-        if ((chunks + per - 1) / per != n) continue;
+        if ((chunks + per - 1) / per != n || (n > 1 && 2 * BH > 65535)) continue;   // both sums' first passes: grid.z
         double used = 0.0, each = 0.0;
         for (double share : shares) {
             used += share * BH * n;
@@ -1226,6 +1256,8 @@ int tc_launches(int64_t BH, int N, int Dk, int Dv, bool backward) {
 
 cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
     cut_forward(&a);
+    // Where the last segment writes its state over the first one's, only the chaining reads that.
+    if (a.S0 && a.S0 == a.S_out) a.fold = a.nseg == 1;
     Sum s = {a};
     if (!s.encode()) return cudaErrorInvalidValue;
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);

@@ -103,6 +103,11 @@ SHAPES = [
     (3, 5, 257, 8, 8, "tok", 0),
     (1, 1, 64, 65, 66, "head", 0),
     (2, 70, 5, 128, 8, "tok", 0),
+    (1, 1, 1300, 64, 128, "tok", 0),     # segments of every pair of widths
+    (1, 1, 1300, 128, 64, "head", 0),
+    (1, 2, 1500, 24, 56, "tok", 0),
+    (1, 1, 4100, 64, 64, "head", 0),     # more segments than a CTA joins itself
+    (1, 1, 3000, 128, 128, "head", 0),
 ]
 
 
@@ -158,12 +163,33 @@ def test_lengths_leave_rows_behind_them(la, N, lengths, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_lengths_across_segments(la, D, dt):
+    x, decay, S0 = problem(4, 2, 1500, D, D, dt, 12)
+    lengths = [1500, 700, 0, 129]
+    check_fwd(la, x, decay, S0, dt, lengths=lengths)
+    check_bwd(la, x, decay, dt, lengths=lengths)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("B,N,D", [(1, 1500, 64), (1, 4100, 64), (3, 130, 128)])
+def test_state_in_place(la, B, N, D, dt):
+    (q, k, v, _), decay, S0 = problem(B, 2, N, D, D, dt, 14)
+    want, S = torch.empty_like(S0), S0.clone()
+    o = la.la_decay_attn_fwd(q, k, v, decay, S0=S0, S_out=want)
+    for _ in range(3):
+        S.copy_(S0)
+        got = la.la_decay_attn_fwd(q, k, v, decay, S0=S, S_out=S)
+        assert torch.equal(got, o) and torch.equal(S, want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("what", ["q", "k", "v", "do"])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
-def test_values_that_are_not_finite_reach_no_earlier_token(la, what, value, dt):
-    x, decay, _ = problem(1, 2, 300, 64, 64, dt, 13, "head")
-    x[3] = x[3].contiguous()
-    at = 150
+@pytest.mark.parametrize("N,D", [(300, 64), (1100, 64), (300, 128)])
+def test_values_that_are_not_finite_reach_no_earlier_token(la, N, D, what, value, dt):
+    x, decay, _ = problem(1, 2, N, D, D, dt, 13, "head")
+    at = N // 2
     clean = la.la_decay_attn_fwd(*x[:3], decay, 0.125)
     grads = la.la_decay_attn_bwd(*x, decay, 0.125)
     y = [t.clone() for t in x]
