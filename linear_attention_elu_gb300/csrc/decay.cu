@@ -41,19 +41,20 @@ using namespace decay;
 
 namespace {
 
-constexpr int kL = 64;              // tokens per chunk, columns per block
-constexpr int kRow = kL + 4;        // floats of a row in shared memory
+constexpr int kL = 64;              // tokens per chunk
+constexpr int kRow = kL + 4;        // floats of a row of tokens in shared memory
 
-// kD: 64-row tiles of the state. Tokens and widths past the end are zero.
-template <int kD> struct Shared {
+// kD: 64-row tiles of the state; kC: columns per block. Tokens and widths past the end are
+// zero.
+template <int kD, int kC> struct Shared {
     float at[64 * kD * kRow];       // A^T, [d][token]
     float bt[64 * kD * kRow];       // B^T
-    float sm[64 * kD * kRow];       // S, [d][column]
+    float sm[64 * kD * (kC + 4)];   // S, [d][column]
     float pt[kL * kRow];            // P^T, [u][t]
 };
-template <int kD> struct Common {
+template <int kD, int kC> struct Common {
     float bn[kL * (64 * kD + 4)];   // w B, [token][d]
-    float cn[kL * kRow];            // C, [token][column]
+    float cn[kL * (kC + 4)];        // C, [token][column]
     float pw[kL + 4];               // e^{l k}
 };
 
@@ -87,29 +88,45 @@ __device__ __forceinline__ void put_transposed(float* dst, int d, int t, const f
     dst[(d + 3) * kRow + t] = v.w;
 }
 
-__device__ __forceinline__ void outer(float (&acc)[4][4], const float* x, const float* y) {
-    const float4 u = *reinterpret_cast<const float4*>(x), v = *reinterpret_cast<const float4*>(y);
-    const float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+// acc += x y^T from row `from` on, two columns per instruction.
+template <int kI> __device__ __forceinline__ void outer(float (&acc)[kI][4], const float* x, const float* y, int from = 0) {
+    const float4 b = *reinterpret_cast<const float4*>(y);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i0 = 0; i0 < kI; i0 += 4) {
+        if (i0 + 3 < from) continue;
+        const float4 u = *reinterpret_cast<const float4*>(x + i0);
+        const float a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + i < from) continue;
+            float(&r)[4] = acc[i0 + i];
+            asm("{\n.reg .b64 x, y, z, u, v;\nmov.b64 x, {%4, %4};\nmov.b64 y, {%5, %6};\nmov.b64 z, {%7, %8};\n"
+                "mov.b64 u, {%0, %1};\nmov.b64 v, {%2, %3};\n"
+                "fma.rn.f32x2 u, x, y, u;\nfma.rn.f32x2 v, x, z, v;\n"
+                "mov.b64 {%0, %1}, u;\nmov.b64 {%2, %3}, v;\n}"
+                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]) : "f"(a[i]), "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w));
+        }
+    }
 }
 
-// Grid: (segments, 64-column blocks, B H). kState: only the segment's end state from zero
+// Grid: (segments, column blocks, B H). A thread owns kI rows (tokens, or rows of each of
+// the state's tiles) by four columns, a warp 4 kI rows by 32 columns. kState: only the segment's end state from zero
 // (first pass, every segment but the last).
-template <typename T, int kD, bool kState>
-__global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args a) {
+template <typename T, int kD, int kC, bool kState>
+__global__ void __launch_bounds__(256, kC == 64 && (kD == 1 || kState) ? 2 : 1) decay_kernel(const __grid_constant__ Args a) {
     extern __shared__ float smem[];
-    Common<kD>& s = *reinterpret_cast<Common<kD>*>(smem);
-    Shared<kD>& x = *reinterpret_cast<Shared<kD>*>(smem + sizeof(Common<kD>) / sizeof(float));
-    constexpr int kB = 64 * kD + 4;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int seg = blockIdx.x, col0 = kL * blockIdx.y;
+    Common<kD, kC>& s = *reinterpret_cast<Common<kD, kC>*>(smem);
+    Shared<kD, kC>& x = *reinterpret_cast<Shared<kD, kC>*>(smem + sizeof(Common<kD, kC>) / sizeof(float));
+    constexpr int kB = 64 * kD + 4, kRowC = kC + 4, kI = kC / 16, kStripes = kC / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tx = 8 * (warp % kStripes) + (lane & 7), ty = 4 * (warp / kStripes) + (lane >> 3);
+    const int px = tid & 15, py = tid >> 4;     // the thread's 4 x 4 scores
+    const int seg = blockIdx.x, col0 = kC * blockIdx.y;
     const int64_t bh = blockIdx.z, b = bh / a.H, h = bh - b * a.H;
     const int n = tokens_of(a, (int)b);
     const int t0 = min(seg * a.seg_len, n), t1 = min(t0 + a.seg_len, n);
-    const int width = min(kL, a.Dc - col0);
+    const int width = min(kC, a.Dc - col0);
+    const bool working = 32 * (warp % kStripes) < width;
     const T* A = static_cast<const T*>(a.a.p) + b * a.a.bs + h * a.a.hs;
     const T* Bp = static_cast<const T*>(a.b.p) + b * a.b.bs + h * a.b.hs;
     const T* C = static_cast<const T*>(a.c.p) + b * a.c.bs + h * a.c.hs + col0;
@@ -119,16 +136,16 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
 
     tcc::pdl_launch_dependents();
     tcc::pdl_wait();                    // the second pass follows the chaining kernel
-    float st[kD][4][4];                 // rows 64 t + 4 ty + i, columns col0 + 4 tx + j
+    float st[kD][kI][4];                // rows 64 k + kI ty + i, columns col0 + 4 tx + j
     const float* from = kState ? nullptr : (a.nseg > 1 ? a.seeds + (bh * a.nseg + seg) * state
                                                        : (a.S0 ? a.S0 + bh * state : nullptr));
 #pragma unroll
     for (int k = 0; k < kD; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = 64 * k + 4 * ty + i, c = 4 * tx + j;
+                const int r = 64 * k + kI * ty + i, c = 4 * tx + j;
                 st[k][i][j] = from && r < a.Da && c < width ? from[(int64_t)r * a.Dc + col0 + c] : 0.f;
             }
     if (tid <= kL) s.pw[tid] = pow2(tid * l2);
@@ -157,71 +174,69 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
             *reinterpret_cast<float4*>(s.bn + tok * kB + d) = make_float4(weight * v.x, weight * v.y, weight * v.z, weight * v.w);
         }
 #pragma unroll
-        for (int d = q4; d < kL; d += 16) {
+        for (int d = q4; d < kC; d += 16) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (in) v = load4(C + at * a.c.ts, d, width, vec_c);
-            *reinterpret_cast<float4*>(s.cn + tok * kRow + d) = v;
+            *reinterpret_cast<float4*>(s.cn + tok * kRowC + d) = v;
         }
         if constexpr (!kState)
 #pragma unroll
             for (int k = 0; k < kD; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float4*>(x.sm + (64 * k + 4 * ty + i) * kRow + 4 * tx) =
+                for (int i = 0; i < kI; ++i)
+                    *reinterpret_cast<float4*>(x.sm + (64 * k + kI * ty + i) * kRowC + 4 * tx) =
                         make_float4(st[k][i][0], st[k][i][1], st[k][i][2], st[k][i][3]);
         __syncthreads();
         if constexpr (!kState) {
-            if (tx <= ty) {             // the other tiles are masked
+            if (px <= py) {             // the other tiles are masked
                 float p[4][4] = {};
 #pragma unroll 4
-                for (int d = 0; d < d4; ++d) outer(p, x.at + d * kRow + 4 * ty, x.bt + d * kRow + 4 * tx);
+                for (int d = 0; d < d4; ++d) outer(p, x.at + d * kRow + 4 * py, x.bt + d * kRow + 4 * px);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int gap = 4 * (ty - tx) + i - j;
+                        const int gap = 4 * (py - px) + i - j;
                         v[i] = gap >= 0 ? p[i][j] * s.pw[max(gap, 0)] : 0.f;
                     }
-                    *reinterpret_cast<float4*>(x.pt + (4 * tx + j) * kRow + 4 * ty) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(x.pt + (4 * px + j) * kRow + 4 * py) = make_float4(v[0], v[1], v[2], v[3]);
                 }
             }
             __syncthreads();
-            float o[4][4] = {};
+            if (working) {
+                float o[kI][4] = {};
 #pragma unroll 4
-            for (int d = 0; d < d4; ++d) outer(o, x.at + d * kRow + 4 * ty, x.sm + d * kRow + 4 * tx);
+                for (int d = 0; d < d4; ++d) outer(o, x.at + d * kRow + kI * ty, x.sm + d * kRowC + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < kI; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[i][j] *= s.pw[4 * ty + i + 1];
-            // Tokens after the tile's own take no part: each row adds its own terms only, so
-            // that an infinity or NaN reaches no earlier token.
+                    for (int j = 0; j < 4; ++j) o[i][j] *= s.pw[kI * ty + i + 1];
+                // Tokens after a row's own take no part, not even as zeros: an infinity or NaN
+                // reaches no earlier token.
 #pragma unroll 4
-            for (int u = 0; u < 4 * ty; ++u) outer(o, x.pt + u * kRow + 4 * ty, s.cn + u * kRow + 4 * tx);
+                for (int u = 0; u < kI * ty; ++u) outer(o, x.pt + u * kRow + kI * ty, s.cn + u * kRowC + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                for (int u = 4 * ty; u <= 4 * ty + i; ++u) {
-                    const float w = x.pt[u * kRow + 4 * ty + i];
+                for (int u = 0; u < kI; ++u)
+                    outer(o, x.pt + (kI * ty + u) * kRow + kI * ty, s.cn + (kI * ty + u) * kRowC + 4 * tx, u);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[i][j] = fmaf(w, s.cn[u * kRow + 4 * tx + j], o[i][j]);
+                for (int i = 0; i < kI; ++i) {
+                    T* to = O + token(kI * ty + i) * a.o.ts + 4 * tx;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (kI * ty + i < m && 4 * tx + j < width) to[j] = from_f<T>(a.scale * o[i][j]);
                 }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                T* to = O + token(4 * ty + i) * a.o.ts + 4 * tx;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * ty + i < m && 4 * tx + j < width) to[j] = from_f<T>(a.scale * o[i][j]);
             }
         }
         const Factor f = factor(m * log_decay(l));
 #pragma unroll
         for (int k = 0; k < kD; ++k) {
-            if (64 * k >= a.Da) break;
-            float add[4][4] = {};
+            if (64 * k >= a.Da || !working) break;
+            float add[kI][4] = {};
 #pragma unroll 4
-            for (int u = 0; u < m; ++u) outer(add, s.bn + u * kB + 64 * k + 4 * ty, s.cn + u * kRow + 4 * tx);
+            for (int u = 0; u < m; ++u) outer(add, s.bn + u * kB + 64 * k + kI * ty, s.cn + u * kRowC + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kI; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) st[k][i][j] = fmaf(f.hi, st[k][i][j], fmaf(f.lo, st[k][i][j], add[i][j]));
         }
@@ -232,10 +247,10 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Args
 #pragma unroll
         for (int k = 0; k < kD; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kI; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int r = 64 * k + 4 * ty + i, c = 4 * tx + j;
+                    const int r = 64 * k + kI * ty + i, c = 4 * tx + j;
                     if (r < a.Da && c < width) to[(int64_t)r * a.Dc + col0 + c] = st[k][i][j];
                 }
 }
@@ -357,31 +372,36 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
     }
 }
 
-template <typename T, int kD>
+template <typename T, int kD, int kC>
 cudaError_t run_width(const Args& a, cudaStream_t st) {
     static std::atomic<int> optin[2][tcc::kMaxDevices];
-    constexpr int kSums = sizeof(Common<kD>), kMain = kSums + sizeof(Shared<kD>);
-    cudaError_t e = tcc::ensure_smem_optin(decay_kernel<T, kD, false>, kMain, optin[0]);
+    constexpr int kSums = sizeof(Common<kD, kC>), kMain = kSums + sizeof(Shared<kD, kC>);
+    cudaError_t e = tcc::ensure_smem_optin(decay_kernel<T, kD, kC, false>, kMain, optin[0]);
     if (e != cudaSuccess) return e;
-    const unsigned BH = (unsigned)(a.B * a.H), blocks = (a.Dc + kL - 1) / kL;
+    const unsigned BH = (unsigned)(a.B * a.H), blocks = (a.Dc + kC - 1) / kC;
     if (a.nseg > 1) {
-        if ((e = tcc::ensure_smem_optin(decay_kernel<T, kD, true>, kSums, optin[1])) != cudaSuccess) return e;
-        decay_kernel<T, kD, true><<<dim3(a.nseg - 1, blocks, BH), 256, kSums, st>>>(a);
+        if ((e = tcc::ensure_smem_optin(decay_kernel<T, kD, kC, true>, kSums, optin[1])) != cudaSuccess) return e;
+        decay_kernel<T, kD, kC, true><<<dim3(a.nseg - 1, blocks, BH), 256, kSums, st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         if ((e = launch_chain(&a, 1, 1, st)) != cudaSuccess) return e;
     }
-    return scan::launch_after(decay_kernel<T, kD, false>, dim3(a.nseg, blocks, BH), 256, kMain, st, a.nseg > 1, a);
+    return scan::launch_after(decay_kernel<T, kD, kC, false>, dim3(a.nseg, blocks, BH), 256, kMain, st, a.nseg > 1, a);
 }
+
+// Columns per block.
+int columns(int Dc) { return Dc <= 64 ? 64 : 128; }
 
 template <typename T>
 cudaError_t run_simt(const Args& a, cudaStream_t st) {
-    return a.Da <= 64 ? run_width<T, 1>(a, st) : run_width<T, 2>(a, st);
+    if (columns(a.Dc) == 64) return a.Da <= 64 ? run_width<T, 1, 64>(a, st) : run_width<T, 2, 64>(a, st);
+    return a.Da <= 64 ? run_width<T, 1, 128>(a, st) : run_width<T, 2, 128>(a, st);
 }
 
 // Segments of the CUDA-core path: one while there are blocks for every SM or fewer than four
 // chunks.
 int simt_segments(int64_t BH, int N, int Da, int Dc) {
-    const int64_t blocks = BH * ((Dc + kL - 1) / kL), slots = (int64_t)tcc::sm_count() * (Da <= 64 ? 2 : 1);
+    const int64_t blocks = BH * ((Dc + columns(Dc) - 1) / columns(Dc));
+    const int64_t slots = (int64_t)tcc::sm_count() * (Da <= 64 && Dc <= 64 ? 2 : 1);
     const int64_t most = (N + kL - 1) / kL / 2;
     int64_t n = blocks > 0 ? slots / blocks : 1;
     n = n < most ? n : most;
