@@ -14,14 +14,18 @@
 // single-token step, the chaining of segments and the entry points. bf16 with whole
 // 16-byte rows runs on the tensor cores instead (csrc/decay_tc.cu).
 //
-// Chunks of 64 tokens in shared memory, 64 columns of c per block, 256 threads of 4 x 4
-// outputs each:
-//   P = weighted, masked A B^T;   O = P C + e^{l (i + 1)} A S;   S = e^{64 l} S + (w B)^T C
-// with S in registers between chunks. What bounds it: the products' operand reads from
-// shared memory (two 16-byte reads per 16 multiply-adds) and the instructions around them. Sequences are cut into segments
-// when there are too few heads for the SMs: a first pass gives each segment's end state
-// from zero, a chain over the segments their start states, and the second pass starts
-// from those.
+// Chunks of 64 tokens in shared memory, 64 or 128 columns of c per block, 256 threads of
+// 4 x 4 or 8 x 4 outputs each:
+//   O = e^{l (i + 1)} A S;   P = weighted, masked A B^T (in A's place);   O += P C;
+//   S = e^{64 l} S + B^T (w C)
+// with S in registers between chunks. What bounds it: the operands' reads from shared
+// memory, 128 bytes per cycle and SM whether lanes share them or not, so 3 reads of 16
+// bytes for 32 multiply-adds (8 x 4) go further than 2 for 16; and two blocks per SM, which
+// fill one another's waits (P in A's place and no transposed B leave the memory for them).
+// Sequences are cut into segments when there are too few heads for the SMs: a first pass
+// gives each segment's end state from zero, a chain over the segments their start states,
+// and the second pass starts from those. fp32 B=2 N=4000 H=8 Dk=64 Dv=96: 137 us in all
+// (64 columns of 4 x 4 per block: 171; two products per instruction: 171 against 185).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -47,13 +51,11 @@ constexpr int kRow = kL + 4;        // floats of a row of tokens in shared memor
 // kD: 64-row tiles of the state; kC: columns per block. Tokens and widths past the end are
 // zero.
 template <int kD, int kC> struct Shared {
-    float at[64 * kD * kRow];       // A^T, [d][token]
-    float bt[64 * kD * kRow];       // B^T
+    float at[64 * kD * kRow];       // A^T, [d][token]; then P^T, [u][t]
     float sm[64 * kD * (kC + 4)];   // S, [d][column]
-    float pt[kL * kRow];            // P^T, [u][t]
 };
 template <int kD, int kC> struct Common {
-    float bn[kL * (64 * kD + 4)];   // w B, [token][d]
+    float bn[kL * (64 * kD + 4)];   // B, [token][d] (first pass: w B)
     float cn[kL * (kC + 4)];        // C, [token][column]
     float pw[kL + 4];               // e^{l k}
 };
@@ -88,32 +90,37 @@ __device__ __forceinline__ void put_transposed(float* dst, int d, int t, const f
     dst[(d + 3) * kRow + t] = v.w;
 }
 
-// acc += x y^T from row `from` on, two columns per instruction.
-template <int kI> __device__ __forceinline__ void outer(float (&acc)[kI][4], const float* x, const float* y, int from = 0) {
-    const float4 b = *reinterpret_cast<const float4*>(y);
+// r += x y, two columns per instruction.
+__device__ __forceinline__ void add_times(float (&r)[4], float x, const float (&y)[4]) {
+    asm("{\n.reg .b64 x, y, z, u, v;\nmov.b64 x, {%4, %4};\nmov.b64 y, {%5, %6};\nmov.b64 z, {%7, %8};\n"
+        "mov.b64 u, {%0, %1};\nmov.b64 v, {%2, %3};\n"
+        "fma.rn.f32x2 u, x, y, u;\nfma.rn.f32x2 v, x, z, v;\n"
+        "mov.b64 {%0, %1}, u;\nmov.b64 {%2, %3}, v;\n}"
+        : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]) : "f"(x), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+}
+
+// acc += x (w y)^T from row `from` on.
+template <int kI>
+__device__ __forceinline__ void outer(float (&acc)[kI][4], const float* x, const float* y, float w = 1.f, int from = 0) {
+    const float4 v = *reinterpret_cast<const float4*>(y);
+    const float b[4] = {w * v.x, w * v.y, w * v.z, w * v.w};
 #pragma unroll
     for (int i0 = 0; i0 < kI; i0 += 4) {
         if (i0 + 3 < from) continue;
         const float4 u = *reinterpret_cast<const float4*>(x + i0);
         const float a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i0 + i < from) continue;
-            float(&r)[4] = acc[i0 + i];
-            asm("{\n.reg .b64 x, y, z, u, v;\nmov.b64 x, {%4, %4};\nmov.b64 y, {%5, %6};\nmov.b64 z, {%7, %8};\n"
-                "mov.b64 u, {%0, %1};\nmov.b64 v, {%2, %3};\n"
-                "fma.rn.f32x2 u, x, y, u;\nfma.rn.f32x2 v, x, z, v;\n"
-                "mov.b64 {%0, %1}, u;\nmov.b64 {%2, %3}, v;\n}"
-                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]) : "f"(a[i]), "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w));
-        }
+        for (int i = 0; i < 4; ++i)
+            if (i0 + i >= from) add_times(acc[i0 + i], a[i], b);
     }
 }
 
 // Grid: (segments, column blocks, B H). A thread owns kI rows (tokens, or rows of each of
-// the state's tiles) by four columns, a warp 4 kI rows by 32 columns. kState: only the segment's end state from zero
+// the state's tiles) by four columns, a warp 4 kI rows by 32 columns. kBlocks: blocks per
+// SM that the registers leave room for. kState: only the segment's end state from zero
 // (first pass, every segment but the last).
-template <typename T, int kD, int kC, bool kState>
-__global__ void __launch_bounds__(256, kC == 64 && (kD == 1 || kState) ? 2 : 1) decay_kernel(const __grid_constant__ Args a) {
+template <typename T, int kD, int kC, bool kState, int kBlocks>
+__global__ void __launch_bounds__(256, kBlocks) decay_kernel(const __grid_constant__ Args a) {
     extern __shared__ float smem[];
     Common<kD, kC>& s = *reinterpret_cast<Common<kD, kC>*>(smem);
     Shared<kD, kC>& x = *reinterpret_cast<Shared<kD, kC>*>(smem + sizeof(Common<kD, kC>) / sizeof(float));
@@ -159,19 +166,19 @@ __global__ void __launch_bounds__(256, kC == 64 && (kD == 1 || kState) ? 2 : 1) 
         auto token = [&](int i) { return (int64_t)(a.rev ? n - 1 - c0 - i : c0 + i); };
         const int64_t at = token(tok);
         const bool in = tok < m;
-        const float weight = in ? s.pw[m - 1 - tok] : 0.f;
+        const float weight = in && kState ? s.pw[m - 1 - tok] : 0.f;
         __syncthreads();
 #pragma unroll
         for (int d = q4; d < 64 * kD; d += 16) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (in) v = load4(Bp + at * a.b.ts, d, a.Da, vec_b);
             if constexpr (!kState) {
-                put_transposed(x.bt, d, tok, v);
                 float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (in) u = load4(A + at * a.a.ts, d, a.Da, vec_a);
                 put_transposed(x.at, d, tok, u);
             }
-            *reinterpret_cast<float4*>(s.bn + tok * kB + d) = make_float4(weight * v.x, weight * v.y, weight * v.z, weight * v.w);
+            if constexpr (kState) v = make_float4(weight * v.x, weight * v.y, weight * v.z, weight * v.w);
+            *reinterpret_cast<float4*>(s.bn + tok * kB + d) = v;
         }
 #pragma unroll
         for (int d = q4; d < kC; d += 16) {
@@ -188,37 +195,54 @@ __global__ void __launch_bounds__(256, kC == 64 && (kD == 1 || kState) ? 2 : 1) 
                         make_float4(st[k][i][0], st[k][i][1], st[k][i][2], st[k][i][3]);
         __syncthreads();
         if constexpr (!kState) {
-            if (px <= py) {             // the other tiles are masked
-                float p[4][4] = {};
-#pragma unroll 4
-                for (int d = 0; d < d4; ++d) outer(p, x.at + d * kRow + 4 * py, x.bt + d * kRow + 4 * px);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int gap = 4 * (py - px) + i - j;
-                        v[i] = gap >= 0 ? p[i][j] * s.pw[max(gap, 0)] : 0.f;
-                    }
-                    *reinterpret_cast<float4*>(x.pt + (4 * px + j) * kRow + 4 * py) = make_float4(v[0], v[1], v[2], v[3]);
-                }
-            }
-            __syncthreads();
+            float o[kI][4] = {}, p[4][4] = {};      // p: tokens u = px + 16 j by t = 4 py + i
             if (working) {
-                float o[kI][4] = {};
 #pragma unroll 4
                 for (int d = 0; d < d4; ++d) outer(o, x.at + d * kRow + kI * ty, x.sm + d * kRowC + 4 * tx);
 #pragma unroll
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[i][j] *= s.pw[kI * ty + i + 1];
+            }
+            const int last_t = 8 * warp + 7;        // of the warp's scores
+            for (int d = 0; d < d4; d += 4) {
+                float av[4][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 v = *reinterpret_cast<const float4*>(x.at + (d + e) * kRow + 4 * py);
+                    av[e][0] = v.x, av[e][1] = v.y, av[e][2] = v.z, av[e][3] = v.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (16 * j > last_t) break;     // every token is masked
+                    const float4 v = *reinterpret_cast<const float4*>(s.bn + (px + 16 * j) * kB + d);
+                    add_times(p[j], v.x, av[0]);
+                    add_times(p[j], v.y, av[1]);
+                    add_times(p[j], v.z, av[2]);
+                    add_times(p[j], v.w, av[3]);
+                }
+            }
+            __syncthreads();                        // A has been read
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int u = px + 16 * j;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int gap = 4 * py + i - u;
+                    v[i] = gap >= 0 ? p[j][i] * s.pw[max(gap, 0)] : 0.f;
+                }
+                if (16 * j <= last_t) *reinterpret_cast<float4*>(x.at + u * kRow + 4 * py) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            __syncthreads();
+            if (working) {
                 // Tokens after a row's own take no part, not even as zeros: an infinity or NaN
                 // reaches no earlier token.
 #pragma unroll 4
-                for (int u = 0; u < kI * ty; ++u) outer(o, x.pt + u * kRow + kI * ty, s.cn + u * kRowC + 4 * tx);
+                for (int u = 0; u < kI * ty; ++u) outer(o, x.at + u * kRow + kI * ty, s.cn + u * kRowC + 4 * tx);
 #pragma unroll
                 for (int u = 0; u < kI; ++u)
-                    outer(o, x.pt + (kI * ty + u) * kRow + kI * ty, s.cn + (kI * ty + u) * kRowC + 4 * tx, u);
+                    outer(o, x.at + (kI * ty + u) * kRow + kI * ty, s.cn + (kI * ty + u) * kRowC + 4 * tx, 1.f, u);
 #pragma unroll
                 for (int i = 0; i < kI; ++i) {
                     T* to = O + token(kI * ty + i) * a.o.ts + 4 * tx;
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(256, kC == 64 && (kD == 1 || kState) ? 2 : 1) 
             if (64 * k >= a.Da || !working) break;
             float add[kI][4] = {};
 #pragma unroll 4
-            for (int u = 0; u < m; ++u) outer(add, s.bn + u * kB + 64 * k + kI * ty, s.cn + u * kRowC + 4 * tx);
+            for (int u = 0; u < m; ++u) outer(add, s.bn + u * kB + 64 * k + kI * ty, s.cn + u * kRowC + 4 * tx, kState ? 1.f : s.pw[m - 1 - u]);
 #pragma unroll
             for (int i = 0; i < kI; ++i)
 #pragma unroll
@@ -374,18 +398,27 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
 
 template <typename T, int kD, int kC>
 cudaError_t run_width(const Args& a, cudaStream_t st) {
-    static std::atomic<int> optin[2][tcc::kMaxDevices];
+    static std::atomic<int> optin[3][tcc::kMaxDevices];
     constexpr int kSums = sizeof(Common<kD, kC>), kMain = kSums + sizeof(Shared<kD, kC>);
-    cudaError_t e = tcc::ensure_smem_optin(decay_kernel<T, kD, kC, false>, kMain, optin[0]);
-    if (e != cudaSuccess) return e;
     const unsigned BH = (unsigned)(a.B * a.H), blocks = (a.Dc + kC - 1) / kC;
+    cudaError_t e;
     if (a.nseg > 1) {
-        if ((e = tcc::ensure_smem_optin(decay_kernel<T, kD, kC, true>, kSums, optin[1])) != cudaSuccess) return e;
-        decay_kernel<T, kD, kC, true><<<dim3(a.nseg - 1, blocks, BH), 256, kSums, st>>>(a);
+        if ((e = tcc::ensure_smem_optin(decay_kernel<T, kD, kC, true, 2>, kSums, optin[0])) != cudaSuccess) return e;
+        decay_kernel<T, kD, kC, true, 2><<<dim3(a.nseg - 1, blocks, BH), 256, kSums, st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         if ((e = launch_chain(&a, 1, 1, st)) != cudaSuccess) return e;
     }
-    return scan::launch_after(decay_kernel<T, kD, kC, false>, dim3(a.nseg, blocks, BH), 256, kMain, st, a.nseg > 1, a);
+    auto main_pass = [&](auto kernel, std::atomic<int>* in) {
+        e = tcc::ensure_smem_optin(kernel, kMain, in);
+        return e != cudaSuccess ? e : scan::launch_after(kernel, dim3(a.nseg, blocks, BH), 256, kMain, st, a.nseg > 1, a);
+    };
+    // Two blocks per SM leave a thread 128 registers: fp32 N=4000 Dk=64 Dv=96, 16 heads 137 us
+    // against 193 with one. With no second block to share the SM, more registers hold more
+    // loads in flight: two heads 85 us against 109.
+    if constexpr (kD == 1) {
+        if ((int64_t)a.nseg * blocks * BH > tcc::sm_count()) return main_pass(decay_kernel<T, kD, kC, false, 2>, optin[1]);
+    }
+    return main_pass(decay_kernel<T, kD, kC, false, 1>, optin[2]);
 }
 
 // Columns per block.
@@ -401,7 +434,7 @@ cudaError_t run_simt(const Args& a, cudaStream_t st) {
 // chunks.
 int simt_segments(int64_t BH, int N, int Da, int Dc) {
     const int64_t blocks = BH * ((Dc + columns(Dc) - 1) / columns(Dc));
-    const int64_t slots = (int64_t)tcc::sm_count() * (Da <= 64 && Dc <= 64 ? 2 : 1);
+    const int64_t slots = (int64_t)tcc::sm_count() * (Da <= 64 ? 2 : 1);
     const int64_t most = (N + kL - 1) / kL / 2;
     int64_t n = blocks > 0 ? slots / blocks : 1;
     n = n < most ? n : most;
