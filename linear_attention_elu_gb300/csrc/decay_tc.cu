@@ -155,8 +155,9 @@ __device__ __forceinline__ uint64_t kmajor_step(uint64_t d, int k) {
     return step_desc(d, (k >> 2) * kTile + (k & 3) * 32);
 }
 
-// (4), the smallest terms first, for kU units side by side (a unit's terms follow one another). The second 64-row atom of the A operand is the tile after B's (for kT = 1 whatever
-// tile follows: those lanes are unused).
+// (4), the smallest terms first, for kU units side by side (a unit's terms follow one another).
+// The second 64-row atom of the A operand is the tile after B's (for kT = 1 whatever tile
+// follows: those lanes are unused).
 template <int kU, int kTerms>
 __device__ __forceinline__ void issue_state(uint32_t dst, uint64_t bt, uint32_t w_tile) {
     constexpr uint32_t id = idesc_bf16_f32(128, 64 * kU, true, true);
@@ -1179,9 +1180,9 @@ int forward_segments(int64_t BH, int N, int Dk, int Dv) {
 
 // Segments of the backward pass, the same for dq and for dk and dv, in chunks of the main
 // passes as above. Those run side by side while their CTAs fit the SMs together (two of dq to
-// one where heads are narrow), else one after the other. B=8 N=4096 H=8 D=64, 32 chunks: not
-// cut 102 us, two segments each 121, four and two 119; B=4 N=2047 H=8 D=128, 16 chunks: not cut
-// 59 us, two segments 81, four 89.
+// one where heads are narrow), else one after the other. Single calls on a cold L2, B=8 N=4096 H=8
+// D=64, 32 chunks: not cut 100 us, two segments 120, four 130; B=4 N=2047 H=8 D=128, 16 chunks:
+// 65, 89, 99.
 int backward_segments(int64_t BH, int N, int Dk, int Dv) {
     const int chunks = (N + kC - 1) / kC;
     const double sms = sm_count(), shares[3] = {narrow(Dk, Dv) ? 0.5 : 1.0, 1.0, narrow(Dk, Dv) ? 0.0 : 1.0};
