@@ -14,8 +14,12 @@
 // the second time mostly from L2), two or three dozen operations each. Two forms:
 //  - N = 1: 2^k lanes hold one group of one row in registers; mean and variance in two
 //    passes over them; a thread keeps its channels, and their weights, over all its rows.
+//    131072 rows of 1024 gated bf16 values: 126 us, 0.97 of a copy's rate; backward of 32765
+//    rows of 512: 38 us, 0.67 (instructions, and the sums of the weights in registers).
 //  - else: a first kernel leaves each block of rows' mean and sum of squares about it (so
 //    that a large mean costs no digits), a second one joins them and writes the outputs.
+//    B=16 N=4096 C=320 bf16 silu: 31 us, 0.41 (both passes' instructions, and two launches);
+//    backward of B=16 N=1024 C=256 fp32: 18 us, 0.42.
 // Sums are fp32 in a fixed order: the same inputs give the same bits.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -383,11 +387,12 @@ __global__ void __launch_bounds__(kThreads, K > 1 ? 1 : V == 4 && kL ? 3 : 2) ro
     auto stats_of = [&](int n) { return n < a.B && t.in[0] ? __ldg(stats + (int64_t)n * a.G) : make_float2(0.f, 0.f); };
 #pragma unroll
     for (int i = 0; i < kS - 1; ++i) fetch(i);
-    float2 st = stats_of(row);
+    // Two rows ahead: one ahead, the 32765 rows of 512 gated bf16 values took 43 us, not 38.
+    float2 st = stats_of(row), st1 = stats_of(row + stride);
     for (int i = 0; i < count; ++i, row += stride) {
         ring.template wait<kS - 2>();
         fetch(i + kS - 1);
-        const float2 next = stats_of(row + stride);
+        const float2 next = stats_of(row + 2 * stride);
         const int at = (i % kS) * 3 * K;
         const bool on = row < a.B;
         Vals<V> xh[K], gw[K];
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, K > 1 ? 1 : V == 4 && kL ? 3 : 2) ro
         for (int k = 0; k < K; ++k)
             if (on && t.in[k])
                 store<T, V>(y + row * a.y_bs + k * t.step, fma(xh[k], all<V>(s2), gw[k] + all<V>(s1)) * all<V>(st.y));
-        st = next;
+        st = st1, st1 = next;
     }
     ring.template wait<0>();
     tcc::pdl_launch_dependents();
