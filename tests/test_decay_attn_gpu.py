@@ -129,6 +129,14 @@ def test_backward_matches_oracle(la, shape, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(80, 4, 70, 64, 96), (60, 3, 131, 33, 40), (45, 4, 66, 100, 127), (2, 90, 65, 128, 31)])
+def test_more_heads_than_sms(la, shape, dt):
+    x, decay, S0 = problem(*shape, dt, 41, lead=1)
+    check_fwd(la, x, decay, S0, dt)
+    check_bwd(la, x, decay, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_slow_and_fast_decays(la, dt):
     # Factors of one (no decay), almost one, tiny, and exactly zero.
     x, _, S0 = problem(1, 6, 520, 64, 64, dt, 3)
