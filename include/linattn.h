@@ -575,8 +575,9 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
  *  - Arithmetic is fp32, and o is rounded once, but for bf16 with Dk and Dv multiples of 8
  *    and 16-byte aligned rows and states, which runs on the tensor cores: there the weighted
  *    scores within 128 tokens, and the state where o reads it, are rounded to bf16 as well
- *    (half a step, 2^-8, of each term). The state is held in fp32; what a token adds to it
- *    enters S_out as three bf16 terms and what only o reads as two.
+ *    (half a step, 2^-8, of each term; the scores 2^-16 where the call has
+ *    B H N <= 1024 rows). The state is held in fp32; what a token adds to it enters S_out
+ *    as three bf16 terms and what only o reads as two, or three in calls of few rows.
  *  - An infinity or NaN in a token's row reaches no output of an earlier token.
  *  - o and S_out must not overlap an input (but S_out == S0), one another or the workspace,
  *    and o's rows must not overlap among themselves (LA_ERR_INVALID_ARG).

@@ -14,7 +14,8 @@
 // C and of the state ((1) and P serve both).
 //
 // Roundings. A, B, C enter as they are. P and the state of (2) are rounded to bf16 once each
-// (half a step, 2^-8, of a term, as the output itself). The state is held in fp32 in
+// (half a step, 2^-8, of a term, as the output itself); in calls of few rows P is
+// two terms, and only the state is. The state is held in fp32 in
 // registers; (4) is summed per chunk from zero and added there, so that the tensor core's
 // sums stay short. w C enters it as bf16 terms, each the remainder of those before: two for a
 // state that only o reads (2^-16 of w C is left), three for one that the call returns.
@@ -58,7 +59,7 @@ constexpr uint32_t kTile = kTileBytes;         // [128 tokens x 64] bf16
 constexpr int kWork = 8;                       // working warps of a unit
 constexpr int kNone = 0x7fffffff;
 
-// TMEM columns: scores, P of each 32 of them over their first 16; per unit (64 columns on) the
+// TMEM columns: scores, P of each 16 of them over their first 8; per unit (64 columns on) the
 // sums of (4), (3)'s part of the output and (2)'s part. With one unit, whose CTA leaves half of
 // TMEM to another, (3) takes the columns of (4).
 template <int kU> struct Tm {
@@ -134,6 +135,8 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
     unpk2(v, &a, &b);
     return pack_bf16(a, b);
 }
+// What packing left of x, packed.
+__device__ __forceinline__ uint32_t remainder2(uint64_t x, uint32_t hi) { return pack2(fma2(bf2(hi), pk2(-1.f, -1.f), x)); }
 __device__ __forceinline__ uint64_t pair2(const uint32_t* v) { return pk2(__uint_as_float(v[0]), __uint_as_float(v[1])); }
 
 // Bounded wait of a whole warp: every lane gets the same answer.
@@ -334,8 +337,8 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 // per SM; with two the table's reads from shared memory cost more than the exponentials: B=1
 // N=65536 H=16 D=64 forward 151 us against 148, the backward of B=8 N=4096 H=8 D=64 with one 91
 // against 92.5).
-template <bool kRev, bool kTable>
-__device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float own, const Misc& m, uint32_t* p) {
+template <bool kRev, bool kTable, bool kFine>
+__device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float own, const Misc& m, uint32_t* p, uint32_t* rest) {
     const int lane = threadIdx.x & 31;
     const uint2 keep = *reinterpret_cast<const uint2*>(m.mask + 16 * j + 2 * lane);
     uint64_t f0, f1;
@@ -351,15 +354,21 @@ __device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFac
         }
         f0 = pk2(x[0], x[1]), f1 = pk2(x[2], x[3]);
     }
-    p[0] = pack2(mul2(pair2(v), f0)) & keep.x;
-    p[1] = pack2(mul2(pair2(v + 2), f1)) & keep.y;
+    const uint64_t x0 = mul2(pair2(v), f0), x1 = mul2(pair2(v + 2), f1);
+    p[0] = pack2(x0) & keep.x;
+    p[1] = pack2(x1) & keep.y;
+    if constexpr (kFine) {
+        rest[0] = remainder2(x0, pack2(x0)) & keep.x;
+        rest[1] = remainder2(x1, pack2(x1)) & keep.y;
+    }
 }
 
-// Scores of block column `blk` (bm in the order of summation) to packed P, over the first
-// half of their columns: no other warp reads or writes those. Loops are kept rolled: what
+// Scores of block column `blk` (bm in the order of summation) to packed P: 16 of them over the
+// first 8 of their columns, with kFine what the packing leaves over the other 8. No other warp
+// reads or writes those. Loops are kept rolled: what
 // the compiler keeps of unrolled ones from chunk to chunk is spilled, and does not fit the
 // little L1 that two CTAs leave (backwards in time the call took 1.8 times as long).
-template <bool kRev, bool kTable>
+template <bool kRev, bool kTable, bool kFine>
 __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
     const int lane = threadIdx.x & 31;
     const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane * rf.diag;
@@ -367,10 +376,10 @@ __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int 
     const uint32_t at = tm_p + 32 * blk;
 #pragma unroll 1
     for (int half = 0; half < 32; half += 16) {
-        uint32_t v[16], p[8];
+        uint32_t v[16], p[8], rest[8];
         if (bm > qm) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = 0u;
+            for (int e = 0; e < 8; ++e) p[e] = rest[e] = 0u;
         } else {
             tmem_ld16(at + half, v);
             tmem_ld_wait();
@@ -382,15 +391,18 @@ __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int 
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.tab + half + e);
-                    p[e / 2] = pack2(mul2(mul2(pair2(v + e), f.x), r2));
-                    p[e / 2 + 1] = pack2(mul2(mul2(pair2(v + e + 2), f.y), r2));
+                    const uint64_t x0 = mul2(mul2(pair2(v + e), f.x), r2), x1 = mul2(mul2(pair2(v + e + 2), f.y), r2);
+                    p[e / 2] = pack2(x0);
+                    p[e / 2 + 1] = pack2(x1);
+                    if constexpr (kFine) rest[e / 2] = remainder2(x0, p[e / 2]), rest[e / 2 + 1] = remainder2(x1, p[e / 2 + 1]);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) diagonal4<kRev, kTable>(v + e, half + e, rf, own, m, p + e / 2);
+                for (int e = 0; e < 16; e += 4) diagonal4<kRev, kTable, kFine>(v + e, half + e, rf, own, m, p + e / 2, rest + e / 2);
             }
         }
-        tmem_st8(at + half / 2, p);
+        tmem_st8(at + half, p);
+        if constexpr (kFine) tmem_st8(at + half + 8, rest);
     }
 }
 
@@ -443,7 +455,8 @@ __device__ __forceinline__ RowFactors row_factors(float l2, int im) {
     return {l2, __uint_as_float(__float_as_uint(l2) & ~31u), im};
 }
 
-template <int kT, int kU, int kTerms, bool kRev>
+// kFine: P in two terms.
+template <int kT, int kU, int kTerms, bool kRev, bool kFine>
 __global__ void __launch_bounds__(32 * (kU * kWork + 2), Smem<kT, kU, kTerms>::kPerSm)
 decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap omap,
@@ -517,9 +530,11 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                 if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k)                                                       // (3)
-                    mma_bf16_ts(tmem + M::kO1, tmem + M::kP + 32 * (k >> 1) + 8 * (k & 1),
-                                step_desc(cr, (i % L::kStages) * kU * kTile + k * 2048), id_o, k > 0);
+                for (int part = kFine ? 1 : 0; part >= 0; --part)                                       // (3)
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_bf16_ts(tmem + M::kO1, tmem + M::kP + 16 * k + 8 * part,
+                                    step_desc(cr, (i % L::kStages) * kU * kTile + k * 2048), id_o, part < (kFine ? 1 : 0) || k > 0);
                 mma_commit(&m.o_full);
                 if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
                 if (i + 1 < pl.nc) ok = scores(i + 1);
@@ -640,7 +655,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             tc_fence_after();
 #pragma unroll 1
             for (int bm = g4; bm < 4; bm += 2 * kU)
-                scores_to_p<kRev, false>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
+                scores_to_p<kRev, false, kFine>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             auto hand_over = [&]() {
                 tmem_st_wait();
@@ -944,7 +959,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k)                                                   // (3)
-                        mma_bf16_ts(tmem + kKvX + 128 * u, tmem + 128 * u + 32 * (k >> 1) + 8 * (k & 1),
+                        mma_bf16_ts(tmem + kKvX + 128 * u, tmem + 128 * u + 16 * k,
                                     step_desc(at(rows, i, u ? kTileQ : kTileG), k * 2048), id_o, k > 0);
                 mma_commit(&m.o_full);
                 if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
@@ -1040,7 +1055,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             if (!(ok = warp_wait(&m.p_full, i & 1, max_spin))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int bm = g; bm < 4; bm += 2) scores_to_p<true, true>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
+            for (int bm = g; bm < 4; bm += 2) scores_to_p<true, true, false>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
@@ -1137,13 +1152,13 @@ cudaError_t launch_sums(const Sum* s, int count, WsHeader* hdr, cudaStream_t st)
     return cudaPeekAtLastError();
 }
 
-template <int kT, int kU, int kTerms, bool kRev>
+template <int kT, int kU, int kTerms, bool kRev, bool kFine>
 cudaError_t launch_main(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
     static std::atomic<int> optin[kMaxDevices];
     constexpr int bytes = Smem<kT, kU, kTerms>::kBytes;
-    const cudaError_t e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev>, bytes, optin);
+    const cudaError_t e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev, kFine>, bytes, optin);
     if (e != cudaSuccess) return e;
-    return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev>, dim3((s.a.Dc + 64 * kU - 1) / (64 * kU), s.a.nseg, s.heads()),
+    return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev, kFine>, dim3((s.a.Dc + 64 * kU - 1) / (64 * kU), s.a.nseg, s.heads()),
                               32 * (kU * kWork + 2), bytes, st, dependent, s.am, s.bm, s.cm, s.om, s.a, s.geo, hdr);
 }
 
@@ -1152,10 +1167,12 @@ template <int kTerms> cudaError_t sums_of(const Sum* s, int count, WsHeader* hdr
     if (s->a.Da <= 64) return s->a.Dc <= 64 ? launch_sums<1, 1, kTerms>(s, count, hdr, st) : launch_sums<1, 2, kTerms>(s, count, hdr, st);
     return s->a.Dc <= 64 ? launch_sums<2, 1, kTerms>(s, count, hdr, st) : launch_sums<2, 2, kTerms>(s, count, hdr, st);
 }
-template <int kTerms, bool kRev> cudaError_t main_of(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
+template <int kTerms, bool kRev, bool kFine = false> cudaError_t main_of(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
     if (s.a.Da <= 64)
-        return s.a.Dc <= 64 ? launch_main<1, 1, kTerms, kRev>(s, dependent, hdr, st) : launch_main<1, 2, kTerms, kRev>(s, dependent, hdr, st);
-    return s.a.Dc <= 64 ? launch_main<2, 1, kTerms, kRev>(s, dependent, hdr, st) : launch_main<2, 2, kTerms, kRev>(s, dependent, hdr, st);
+        return s.a.Dc <= 64 ? launch_main<1, 1, kTerms, kRev, kFine>(s, dependent, hdr, st)
+                            : launch_main<1, 2, kTerms, kRev, kFine>(s, dependent, hdr, st);
+    return s.a.Dc <= 64 ? launch_main<2, 1, kTerms, kRev, kFine>(s, dependent, hdr, st)
+                        : launch_main<2, 2, kTerms, kRev, kFine>(s, dependent, hdr, st);
 }
 
 bool narrow(int Dk, int Dv) { return Dk <= 64 && Dv <= 64; }
@@ -1235,6 +1252,12 @@ void cut_backward(Args* a) {
     a->fold = a->nseg - 1 <= kFold;
 }
 
+// Calls of few rows take P in two bf16 terms and w C in three. A score's
+// rounding is shared by a whole row of outputs, and a row has few scores that count where the
+// sequence is short or the decay fast: over few rows such errors do not average out. They
+// are bound by their launches either way.
+bool few_rows(int64_t BH, int N) { return BH * N <= 1024; }
+
 Args cut_of(int64_t BH, int N, int Dk, int Dv, bool backward) {
     Args a = {};
     a.B = 1, a.H = (int)BH, a.N = N, a.Da = Dk, a.Dc = Dv;
@@ -1251,7 +1274,7 @@ size_t tc_seeds(int64_t BH, int N, int Dk, int Dv, bool backward) {
 
 int tc_launches(int64_t BH, int N, int Dk, int Dv, bool backward) {
     const Args a = cut_of(BH, N, Dk, Dv, backward);
-    const int sums = backward && (Dk <= 64) != (Dv <= 64) ? 2 : 1, main = !backward ? 1 : narrow(Dk, Dv) ? 2 : 3;
+    const int sums = backward && (Dk <= 64) != (Dv <= 64) ? 2 : 1, main = !backward ? 1 : narrow(Dk, Dv) && !few_rows(BH, N) ? 2 : 3;
     return main + (a.nseg > 1 ? sums + (a.fold ? 0 : 1) : 0);
 }
 
@@ -1267,6 +1290,7 @@ cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
         if ((e = a.S_out ? sums_of<3>(&s, 1, hdr, st) : sums_of<2>(&s, 1, hdr, st)) != cudaSuccess) return e;
         if (!a.fold && (e = launch_chain(&a, 1, kC, st)) != cudaSuccess) return e;
     }
+    if (few_rows(s.heads(), a.N)) return main_of<3, false, true>(s, a.nseg > 1, hdr, st);
     return a.S_out ? main_of<3, false>(s, a.nseg > 1, hdr, st) : main_of<2, false>(s, a.nseg > 1, hdr, st);
 }
 
@@ -1290,8 +1314,9 @@ cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t
         const Args chained[2] = {dq, dv};
         if (!dq.fold && (e = launch_chain(chained, 2, kC, st)) != cudaSuccess) return e;
     }
-    if ((e = main_of<2, false>(s[0], cut, hdr, st)) != cudaSuccess) return e;
-    if (narrow(dv.Da, dv.Dc)) {
+    const bool few = few_rows(s[0].heads(), dq.N);
+    if ((e = few ? main_of<3, false, true>(s[0], cut, hdr, st) : main_of<2, false>(s[0], cut, hdr, st)) != cudaSuccess) return e;
+    if (narrow(dv.Da, dv.Dc) && !few) {
         static std::atomic<int> optin[kMaxDevices];
         if ((e = ensure_smem_optin(decay_kv_kernel, KvSmem::kBytes, optin)) != cudaSuccess) return e;
         const KvMaps maps = {{s[1].am, s[2].am, s[1].bm, s[1].cm}, s[2].om, s[1].om};
@@ -1299,8 +1324,9 @@ cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t
                                   true, maps, dv, dk.o, s[1].geo, s[2].geo, hdr);
     }
     s[1].geo.late = s[2].geo.late = 1;
-    if ((e = main_of<2, true>(s[1], true, hdr, st)) != cudaSuccess) return e;
-    return main_of<2, true>(s[2], true, hdr, st);
+    for (int i = 1; i < 3; ++i)
+        if ((e = few ? main_of<3, true, true>(s[i], true, hdr, st) : main_of<2, true>(s[i], true, hdr, st)) != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 }  // namespace decay

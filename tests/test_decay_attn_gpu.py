@@ -108,6 +108,11 @@ SHAPES = [
     (1, 2, 1500, 24, 56, "tok", 0),
     (1, 1, 4100, 64, 64, "head", 0),     # more segments than a CTA joins itself
     (1, 1, 3000, 128, 128, "head", 0),
+    (9, 4, 40, 64, 64, "tok", 0),        # short sequences, more than 1024 rows in all
+    (4, 4, 130, 64, 48, "head", 0),
+    (550, 2, 1, 64, 64, "tok", 0),
+    (5, 2, 129, 128, 64, "tok", 0),
+    (3, 3, 129, 40, 128, "head", 0),
 ]
 
 
@@ -126,6 +131,28 @@ def test_backward_matches_oracle(la, shape, dt):
     B, H, N, Dk, Dv, layout, lead = shape
     x, decay, _ = problem(B, H, N, Dk, Dv, dt, 7 + N + Dk + Dv, layout, lead)
     check_bwd(la, x, decay, dt)
+
+
+# At most 1024 rows: the scores are two bf16 terms, so that what is lost of a term is 2^-16 of it
+# (half a step twice: 2^-8 of 2^-8), beside o's own rounding. Sequences of one chunk, from zero:
+# the state plays no part.
+@pytest.mark.parametrize("shape", [(1, 1, 1, 64, 64), (1, 2, 3, 64, 128), (2, 8, 4, 128, 64), (1, 8, 128, 64, 64),
+                                   (1, 3, 100, 128, 128), (3, 4, 20, 32, 48)])
+def test_few_rows_lose_nothing_but_the_rounding_of_the_output(la, shape):
+    x, decay, _ = problem(*shape, "bf16", 43)
+    a, d = [to_f64(t) for t in x], to_f64(decay)
+    N = shape[2]
+
+    def check(got, ref, mag, D, what):
+        f = (D + N / 16 + 192) * 2.0 ** -24
+        near(got, ref, (2.0 ** -16 + f) * 1.01 * mag + 2.0 ** -8 * np.abs(ref), what)
+
+    ref, mag = (tm.decay_attn(*(f(t) for t in a[:3]), d, 0.125)[0] for f in (np.asarray, np.abs))
+    check(la.la_decay_attn_fwd(*x[:3], decay, 0.125), ref, mag, shape[3], "o")
+    got = la.la_decay_attn_bwd(*x, decay, 0.125)
+    ref, mag = (tm.decay_attn_bwd(*(f(t) for t in a), d, 0.125) for f in (np.asarray, np.abs))
+    for g, r, m, D, what in zip(got, ref, mag, (shape[4], shape[4], shape[3]), ("dq", "dk", "dv")):
+        check(g, r, m, D, what)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])

@@ -97,7 +97,8 @@ def test_workspace_and_launches(la):
             assert la.la_workspace_size(op, 1, 2, 9000, 64, 128, dt) % 256 == 0
             assert la.la_launch_count(op, 2, 8, 0, 64, 64, dt) == 0
             # (On the tensor cores dk and dv of heads up to 64 wide come from one launch.)
-            assert la.la_launch_count(op, 2, 8, 1, 64, 64, dt) == most // 3 - (most == 9 and dt == la.LA_BF16)
+            assert la.la_launch_count(op, 2, 8, 1, 64, 64, dt) == most // 3
+            assert la.la_launch_count(op, 20, 8, 100, 64, 64, dt) >= most // 3 - (most == 9 and dt == la.LA_BF16)
             assert la.la_launch_count(op, 2, 8, 1, 128, 128, dt) == most // 3
             assert la.la_launch_count(op, 1, 1, 9000, 64, 64, dt) <= most
             for bad in ((1, 1, 10, 129, 64), (1, 1, (1 << 30) + 1, 64, 64), (70000, 1, 4, 64, 64)):
