@@ -580,7 +580,9 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
  *    as three bf16 terms and what only o reads as two, or three in calls of few rows.
  *  - An infinity or NaN in a token's row reaches no output of an earlier token.
  *  - o and S_out must not overlap an input (but S_out == S0), one another or the workspace,
- *    and o's rows must not overlap among themselves (LA_ERR_INVALID_ARG).
+ *    and o's rows must not overlap among themselves (LA_ERR_INVALID_ARG). That is decided
+ *    from the strides, exactly for the views of a tensor; of rows that interleave otherwise
+ *    what 2^14 steps do not show counts as apart.
  *  - workspace: la_workspace_size(LA_OP_DECAY_ATTN, B, H, N, Dk, Dv, dt, ...) bytes,
  *    256-byte aligned, initialised once with la_workspace_init. Calls that overlap in time
  *    need workspaces of their own.

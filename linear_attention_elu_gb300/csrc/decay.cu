@@ -483,40 +483,11 @@ bool bad(const void* p, la_dtype dt) {
 }
 bool bad4(const void* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
 
-// Rows [B, H, N, D] as the overlap checks take them: two strided axes over whole rows, and
-// what is left as a list of such sets (one, unless the strides of all three axes are their own).
-struct Rows3 {
-    Rows r;
-    int64_t more, stride;       // sets and bytes between them
-};
+// Rows [B, H, N, D], and a whole range, as the overlap checks take them.
 Rows3 rows3(const void* p, int64_t B, int64_t H, int64_t N, int64_t D, const int64_t* s, int64_t eb) {
-    const int64_t bs = s[0] * eb, hs = s[1] * eb, ts = s[2] * eb, row = D * eb;
-    if (H == 1) return {{p, B, N, row, bs, ts}, 1, 0};
-    if (N == 1) return {{p, B, H, row, bs, hs}, 1, 0};
-    if (B == 1) return {{p, H, N, row, hs, ts}, 1, 0};
-    if (hs == row) return {{p, B, N, H * row, bs, ts}, 1, 0};
-    if (bs == H * hs) return {{p, B * H, N, row, hs, ts}, 1, 0};
-    if (hs == N * ts) return {{p, B, H * N, row, bs, ts}, 1, 0};
-    return {{p, H, N, row, hs, ts}, B, bs};
+    return {p, D * eb, {B, H, N}, {s[0] * eb, s[1] * eb, s[2] * eb}};
 }
-Rows3 whole(const void* p, int64_t bytes) { return {block_of(p, bytes), 1, 0}; }
-
-bool overlap3(const Rows3& x, const Rows3& y) {
-    if (!x.r.p || !y.r.p || x.more * y.more > 65536) return false;
-    for (int64_t i = 0; i < x.more; ++i)
-        for (int64_t j = 0; j < y.more; ++j) {
-            Rows u = x.r, v = y.r;
-            u.p = static_cast<const char*>(u.p) + i * x.stride;
-            v.p = static_cast<const char*>(v.p) + j * y.stride;
-            if (overlap(u, v)) return true;
-        }
-    return false;
-}
-bool overlaps_any3(const Rows3& out, std::initializer_list<Rows3> others) {
-    for (const Rows3& r : others)
-        if (overlap3(out, r)) return true;
-    return false;
-}
+Rows3 whole(const void* p, int64_t bytes) { return {p, bytes, {1, 1, 1}, {0, 0, 0}}; }
 
 // Whether an output's rows are disjoint: each axis steps over all that the axes with smaller
 // strides cover.
@@ -595,8 +566,8 @@ la_status la_decay_attn_fwd(const void* q, const void* k, const void* v, const f
     const la::Rows3 vr = la::rows3(v, B, H, N, Dv, strides + 6, eb), orr = la::rows3(o, B, H, N, Dv, strides + 9, eb);
     const la::Rows3 dr = la::whole(decay, 4 * (int64_t)H), nr = la::whole(lengths, 4 * (int64_t)B);
     const la::Rows3 s0r = la::whole(S0, state), s1r = la::whole(S_out, state), wr = la::whole(workspace, need);
-    if (la::overlaps_any3(orr, {qr, kr, vr, dr, nr, s0r, s1r, wr}) || la::overlaps_any3(s1r, {qr, kr, vr, dr, nr, wr}) ||
-        la::overlaps_any3(wr, {qr, kr, vr, dr, nr, s0r}))
+    if (la::overlaps_any(orr, {qr, kr, vr, dr, nr, s0r, s1r, wr}) || la::overlaps_any(s1r, {qr, kr, vr, dr, nr, wr}) ||
+        la::overlaps_any(wr, {qr, kr, vr, dr, nr, s0r}))
         return LA_ERR_INVALID_ARG;
     la::decay::Args a = {};
     a.a = la::tensor(q, strides), a.b = la::tensor(k, strides + 3), a.c = la::tensor(v, strides + 6);
@@ -634,8 +605,8 @@ la_status la_decay_attn_bwd(const void* q, const void* k, const void* v, const v
     const la::Rows3 oq = la::rows3(dq, B, H, N, Dk, tq, eb), ok = la::rows3(dk, B, H, N, Dk, tk, eb);
     const la::Rows3 ov = la::rows3(dv, B, H, N, Dv, tv, eb);
     for (const la::Rows3* out : {&oq, &ok, &ov, &wr})
-        if (la::overlaps_any3(*out, {qr, kr, vr, gr, dr, nr})) return LA_ERR_INVALID_ARG;
-    if (la::overlap3(oq, ok) || la::overlap3(oq, ov) || la::overlap3(ok, ov) || la::overlaps_any3(wr, {oq, ok, ov}))
+        if (la::overlaps_any(*out, {qr, kr, vr, gr, dr, nr})) return LA_ERR_INVALID_ARG;
+    if (la::overlap(oq, ok) || la::overlap(oq, ov) || la::overlap(ok, ov) || la::overlaps_any(wr, {oq, ok, ov}))
         return LA_ERR_INVALID_ARG;
     la::decay::Args a = {};
     a.decay = decay, a.lengths = lengths, a.B = B, a.H = H, a.N = N, a.scale = scale;

@@ -87,4 +87,69 @@ inline bool same_rows(const Rows& x, const Rows& y) {
     return x.p == y.p && x.row == y.row && (x.B <= 1 || x.bs == y.bs) && (x.N <= 1 || x.ts == y.ts);
 }
 
+// Rows with three strided axes: count[i] steps of stride[i] bytes each, `row` bytes.
+struct Rows3 {
+    const void* p;
+    int64_t row, count[3], stride[3];
+};
+
+// Whether rows of x and of y share a byte. The rows of x lie at p + sum of c s (0 <= c < count),
+// so the question is whether the distance of two rows, d + sum of c s over the axes of both
+// (those of x with -count < c <= 0, axes of one stride counted together), can come between -y.row
+// and x.row: sought from the largest stride down, trying only what the smaller strides can still
+// make up for. Where strides nest, which those of a tensor's views do, that is two or three
+// steps per axis. What 2^14 steps do not show counts as apart.
+inline bool overlap(const Rows3& x, const Rows3& y) {
+    struct Axis {
+        int64_t s, lo, hi;
+    } axis[6];
+    int n = 0;
+    int64_t row[2] = {x.row, y.row}, base[2] = {};
+    for (int which = 0; which < 2; ++which) {
+        const Rows3& r = which ? y : x;
+        if (!r.p || r.row < 1) return false;
+        int64_t count[3], stride[3];
+        for (int i = 0; i < 3; ++i) {
+            if (r.count[i] < 1) return false;
+            count[i] = r.stride[i] == 0 ? 1 : r.count[i], stride[i] = r.stride[i];   // 0: the same rows again
+            if (stride[i] < 0) base[which] += (count[i] - 1) * stride[i], stride[i] = -stride[i];   // from the other end
+        }
+        for (int pass = 0; pass < 3; ++pass)                 // rows without a gap between them are one row
+            for (int i = 0; i < 3; ++i)
+                if (count[i] > 1 && stride[i] <= row[which]) row[which] += (count[i] - 1) * stride[i], count[i] = 1;
+        for (int i = 0; i < 3; ++i) {
+            if (count[i] == 1) continue;
+            int k = 0;
+            while (k < n && axis[k].s > stride[i]) ++k;
+            if (k == n || axis[k].s != stride[i]) {
+                for (int j = n++; j > k; --j) axis[j] = axis[j - 1];
+                axis[k] = {stride[i], 0, 0};
+            }
+            (which ? axis[k].hi : axis[k].lo) += which ? count[i] - 1 : 1 - count[i];
+        }
+    }
+    int64_t lo[7] = {}, hi[7] = {};                          // what axes k .. add at least and at most
+    for (int k = n - 1; k >= 0; --k) lo[k] = lo[k + 1] + axis[k].lo * axis[k].s, hi[k] = hi[k + 1] + axis[k].hi * axis[k].s;
+    auto below = [](int64_t v, int64_t s) { return v >= 0 ? v / s : -((-v + s - 1) / s); };   // the floor of v / s
+    int left = 1 << 14;
+    auto meet = [&](auto& self, int k, int64_t d) -> bool {
+        if (k == n) return -row[1] < d && d < row[0];
+        const int64_t s = axis[k].s;
+        int64_t from = below(-row[1] - hi[k + 1] - d, s) + 1, to = below(row[0] - lo[k + 1] - d - 1, s);
+        if (from < axis[k].lo) from = axis[k].lo;
+        if (to > axis[k].hi) to = axis[k].hi;
+        for (int64_t c = from; c <= to && left > 0; ++c, --left)
+            if (self(self, k + 1, d + c * s)) return true;
+        return false;
+    };
+    const int64_t apart = (int64_t)(reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p));
+    return meet(meet, 0, apart + base[1] - base[0]);
+}
+
+inline bool overlaps_any(const Rows3& out, std::initializer_list<Rows3> others) {
+    for (const Rows3& r : others)
+        if (overlap(out, r)) return true;
+    return false;
+}
+
 }  // namespace la
