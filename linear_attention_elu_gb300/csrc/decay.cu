@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
     float vv[kV], acc[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) vv[v] = mine ? to_f(vp[c0 + v]) : 0.f, acc[v] = 0.f;
-    const float f = expf(log_decay(a.decay[h]));
+    const Factor f = factor(log_decay(a.decay[h]));   // a state passes it once per token
     __syncthreads();
     for (int base = 0; base < a.Dk; base += kU * rpp) {
         if (base > 0) load(base);
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const __grid_constant__
             const float kr = ks[r], qr = qs[r];
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
-                s[u][v] = fmaf(kr, vv[v], f * s[u][v]);
+                s[u][v] = fmaf(f.hi, s[u][v], fmaf(f.lo, s[u][v], kr * vv[v]));
                 acc[v] = fmaf(qr, s[u][v], acc[v]);
             }
             if constexpr (kV == 4)
