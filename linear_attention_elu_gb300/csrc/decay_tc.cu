@@ -320,8 +320,7 @@ __device__ __forceinline__ void start_state(const Args& a, const Place& pl, floa
 
 // Decay factors of a warp's rows, for every chunk.
 struct RowFactors {
-    float l2, diag;     // log2 f, and its leading 19 bits: times a count below 32 it is exact, so that
-                        // the diagonal's exponents are differences without error (2^-19 of them is lost)
+    float l2;           // log2 f
     int im;             // the row in the order of summation
 };
 
@@ -350,7 +349,7 @@ __device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFac
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const float c = (float)(j + u);
-            x[u] = pow2(kRev ? fmaf(c, rf.diag, -own) : fmaf(-c, rf.diag, own));
+            x[u] = pow2((kRev ? c - own : own - c) * rf.l2);   // a count: times l2 it is rounded once
         }
         f0 = pk2(x[0], x[1]), f1 = pk2(x[2], x[3]);
     }
@@ -371,7 +370,7 @@ __device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFac
 template <bool kRev, bool kTable, bool kFine>
 __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
     const int lane = threadIdx.x & 31;
-    const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane * rf.diag;
+    const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane;
     const uint64_t r2 = pk2(r, r);
     const uint32_t at = tm_p + 32 * blk;
 #pragma unroll 1
@@ -452,7 +451,7 @@ template <bool kRev, bool kTable> __device__ __forceinline__ void init_tables(Mi
 }
 
 __device__ __forceinline__ RowFactors row_factors(float l2, int im) {
-    return {l2, __uint_as_float(__float_as_uint(l2) & ~31u), im};
+    return {l2, im};
 }
 
 // kFine: P in two terms.
