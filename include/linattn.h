@@ -574,10 +574,10 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
  *    keeps its state.
  *  - Arithmetic is fp32, and o is rounded once, but for bf16 with Dk and Dv multiples of 8
  *    and 16-byte aligned rows and states, which runs on the tensor cores: there the weighted
- *    scores within 128 tokens, and the state where o reads it, are rounded to bf16 as well
- *    (half a step, 2^-8, of each term; the scores 2^-16 where the call has
- *    B H N <= 1024 rows). The state is held in fp32; what a token adds to it enters S_out
- *    as three bf16 terms and what only o reads as two, or three in calls of few rows.
+ *    scores within 128 tokens, the state where o reads it, and what a token adds to a state that
+ *    only o reads are sums of two bf16 terms (2^-16 of each value is left at most), whatever the
+ *    call's size. Where Dk and Dv are both above 64 the state where o reads it is one bf16
+ *    value (2^-8). The state is held in fp32; what a token adds to it enters S_out as three terms.
  *  - An infinity or NaN in a token's row reaches no output of an earlier token.
  *  - o and S_out must not overlap an input (but S_out == S0), one another or the workspace,
  *    and o's rows must not overlap among themselves (LA_ERR_INVALID_ARG). That is decided

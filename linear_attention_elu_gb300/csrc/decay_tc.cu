@@ -7,27 +7,30 @@
 //   S_new = f^m S + sum_j B_j (f^(m-1-j) C_j)^T          (m tokens in the chunk)
 // as products of 128-row tiles:
 //   (1) scores A B^T                      M = 128, N = 128, K = Da
-//   (2) read of the state A S_bf16        M = 128, N = 64,  K = Da
-//   (3) P C, P = bf16 of the weighted, masked scores (in TMEM)    K = 128
+//   (2) read of the state A S             M = 128, N = 64,  K = Da
+//   (3) P C, P the weighted, masked scores (in TMEM)              K = 128
 //   (4) B^T (w C), C weighted             M = Da,  N = 64,  K = 128
 // A CTA walks the chunks of a segment of one head, for one or two "units" of 64 columns of
 // C and of the state ((1) and P serve both).
 //
-// Roundings. A, B, C enter as they are. P and the state of (2) are rounded to bf16 once each
-// (half a step, 2^-8, of a term, as the output itself); in calls of few rows P is
-// two terms, and only the state is. The state is held in fp32 in
+// Roundings. A, B, C enter as they are. P and the state of (2) enter as two bf16 terms, the second the
+// remainder of the first: 2^-16 of a value is left at most, so that what an output loses beside its own
+// rounding depends neither on how many scores make it nor on the call's size. (One term of each: 2.3e-3
+// to 2.4e-3 off in all where the output's rounding is 1.7e-3. What the second terms cost: B=1 N=65536 H=16
+// D=64 154 us for 143, B=8 N=4096 H=8 D=64 backward 105 for 90.) Where both widths are above 64 the state has
+// one term, see Smem. The state is held in fp32 in
 // registers; (4) is summed per chunk from zero and added there, so that the tensor core's
-// sums stay short. w C enters it as bf16 terms, each the remainder of those before: two for a
-// state that only o reads (2^-16 of w C is left), three for one that the call returns.
+// sums stay short. w C enters it as bf16 terms as well: two for a
+// state that only o reads, three for one that the call returns.
 // Weights below the diagonal 32 x 32 blocks are products of two factors <= 1, one of the
 // row and one of the column; the diagonal blocks take a factor per score. Every
 // factor's exponent is a count of tokens times l, so none is a difference of larger ones.
 //
 // Schedule. Eight working warps per unit, one that issues the products and one for loads and
 // stores.
-// A working warp owns 32 rows and half of a unit's columns. Within a chunk: state to bf16 and
-// w C to shared memory; (2) and (4) run under the step from scores to P; the sums of (4) join
-// the state and (3) takes their TMEM columns; the output is staged where C was. A, B and the
+// A working warp owns 32 rows and half of a unit's columns. Within a chunk: (2) and (4) run under
+// the step from scores to P; the sums of (4) join the state and (3) takes their TMEM columns; under
+// (3) the next w C and the new state go to shared memory; the output is staged where C was. A, B and the
 // next scores are on the way from the middle of the chunk on, C from the chunk before. With
 // one unit and Da <= 64 two CTAs share an SM, each under the other's waits. Hand-offs are
 // mbarriers; every wait is bounded.
@@ -59,7 +62,8 @@ constexpr uint32_t kTile = kTileBytes;         // [128 tokens x 64] bf16
 constexpr int kWork = 8;                       // working warps of a unit
 constexpr int kNone = 0x7fffffff;
 
-// TMEM columns: scores, P of each 16 of them over their first 8; per unit (64 columns on) the
+// TMEM columns: scores, P of each 16 of them over their first 8 and its second term over the
+// others; per unit (64 columns on) the
 // sums of (4), (3)'s part of the output and (2)'s part. With one unit, whose CTA leaves half of
 // TMEM to another, (3) takes the columns of (4).
 template <int kU> struct Tm {
@@ -67,16 +71,17 @@ template <int kU> struct Tm {
 };
 
 struct Misc {
-    uint64_t a_full, b_full, c_full[2], p_full, s_full, o_full;
-    uint64_t prep, pt, staged, o_free, drain;
+    uint64_t a_full, b_full, c_full[2], p_full[2], s_full, o_full[2];
+    uint64_t prep, pt[2], staged, o_free, drain;
     uint32_t tmem_slot;
     int any;                    // values of C that are not finite: the first token that has one,
     int first[128];             // and that of each column, counted over the segment
     alignas(16) float tab[32];  // f^(31 - j), by the column's place in its block; read 16 bytes at a time
-    alignas(16) uint32_t mask[512];   // diagonal block, [pair of columns / 2][row][2]: which scores take part
-    alignas(16) float diag[1024];     // decay_kv_kernel alone: its factors, [column / 4][row][4]
+    // decay_kv_kernel alone, of a diagonal block:
+    alignas(16) float diag[1024];     // its factors, [column / 4][row][4]
+    uint32_t mask[512];               // which scores take part, [pair of columns / 2][row][2]
 };
-constexpr uint32_t misc_bytes(bool table) { return table ? 7 * 1024 : 3 * 1024; }
+constexpr uint32_t misc_bytes(bool table) { return table ? 7 * 1024 : 1024; }
 static_assert(sizeof(Misc) <= misc_bytes(true) && offsetof(Misc, diag) <= misc_bytes(false), "barriers and tables");
 
 // Shared memory from a 1024-byte boundary.
@@ -85,7 +90,11 @@ template <int kT, int kU, int kTerms> struct Smem {
     static constexpr uint32_t kA = 0, kB = kT * kTile, kC0 = 2 * kT * kTile;
     static constexpr uint32_t kW = kC0 + kStages * kU * kTile;        // [unit][term]
     static constexpr uint32_t kS = kW + kU * kTerms * kTile;          // [unit], 64 kT rows
-    static constexpr uint32_t kMisc = kS + kU * kT * kTile / 2;
+    // Terms of the state in (2). Where both widths are above 64 a second one would take the place
+    // of C's second stage, or of a unit: B=4 N=2047 H=8 D=128 backward 79 us against 60, forward
+    // with S_out B=4 N=4096 H=16 187 against 134.
+    static constexpr int kReads = kT * kU < 4 ? 2 : 1;
+    static constexpr uint32_t kMisc = kS + kReads * kU * kT * kTile / 2;
     static constexpr int kBytes = kMisc + misc_bytes(false);
     static constexpr int kPerSm = kBytes <= 113 * 1024 && kU == 1 ? 2 : 1;
 };
@@ -234,14 +243,22 @@ __device__ __noinline__ uint4 put_nan(const int* firsts, int token, uint4 o) {
 // ------------------------------------------------------------ steps of a working warp
 // Row `row` = 32 q + lane of the tiles, columns from the 16-byte piece j0 on.
 
-// A state row (fp32 columns) to the bf16 tile that (2) reads.
-template <int kCols>
-__device__ __forceinline__ void write_state(uint8_t* tile, const float (&st)[kCols], int row, int j0) {
+// A state row (fp32 columns) to the bf16 tiles that (2) reads, its terms `term` bytes apart.
+template <int kReads, int kCols>
+__device__ __forceinline__ void write_state(uint8_t* tile, uint32_t term, const float (&st)[kCols], int row, int j0) {
 #pragma unroll
-    for (int j = 0; j < kCols / 8; ++j)
-        *reinterpret_cast<uint4*>(tile + row * 128 + (((j0 + j) ^ (row & 7)) << 4)) =
-            make_uint4(pack_bf16(st[8 * j], st[8 * j + 1]), pack_bf16(st[8 * j + 2], st[8 * j + 3]),
-                       pack_bf16(st[8 * j + 4], st[8 * j + 5]), pack_bf16(st[8 * j + 6], st[8 * j + 7]));
+    for (int j = 0; j < kCols / 8; ++j) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t v = pk2(st[8 * j + 2 * k], st[8 * j + 2 * k + 1]);
+            hi[k] = pack2(v);
+            if (kReads > 1) lo[k] = remainder2(v, hi[k]);
+        }
+        uint8_t* to = tile + row * 128 + (((j0 + j) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (kReads > 1) *reinterpret_cast<uint4*>(to + term) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
 }
 
 // w C of a row: its terms, kTile apart. Returns whether all values are finite.
@@ -275,6 +292,17 @@ template <int kPieces = 4> __device__ __forceinline__ void clear_pieces(uint8_t*
 #pragma unroll
     for (int j = j0; j < j0 + kPieces; ++j)
         *reinterpret_cast<uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+}
+
+// Whether the values of four 16-byte pieces of a row are finite, for the warp as a whole.
+__device__ __forceinline__ bool finite_pieces(const uint8_t* tile, int row, int j0) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int j = j0; j < j0 + 4; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4));
+        for (uint32_t v : {x.x, x.y, x.z, x.w}) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(bad) : "r"(v), "r"(0u));
+    }
+    return __all_sync(0xffffffffu, (bad & 0x7FFF7FFFu) == 0);
 }
 
 // kCols columns from c0 of row `row` of a matrix of states [Da, Dc] (transposed: of its transpose).
@@ -336,43 +364,44 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 // per SM; with two the table's reads from shared memory cost more than the exponentials: B=1
 // N=65536 H=16 D=64 forward 151 us against 148, the backward of B=8 N=4096 H=8 D=64 with one 91
 // against 92.5).
-template <bool kRev, bool kTable, bool kFine>
-__device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float own, const Misc& m, uint32_t* p, uint32_t* rest) {
-    const int lane = threadIdx.x & 31;
-    const uint2 keep = *reinterpret_cast<const uint2*>(m.mask + 16 * j + 2 * lane);
+template <bool kRev, bool kTable>
+__device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float gap, uint32_t keep, const Misc& m, uint32_t* p, uint32_t* rest) {
     uint64_t f0, f1;
+    uint32_t k0, k1;
     if constexpr (kTable) {
+        const int lane = threadIdx.x & 31;
         const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(m.diag + 32 * j + 4 * lane);
-        f0 = f.x, f1 = f.y;
+        const uint2 k = *reinterpret_cast<const uint2*>(m.mask + 16 * j + 2 * lane);
+        f0 = f.x, f1 = f.y, k0 = k.x, k1 = k.y;
     } else {
         float x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float c = (float)(j + u);
-            x[u] = pow2((kRev ? c - own : own - c) * rf.l2);   // a count: times l2 it is rounded once
-        }
+        for (int u = 0; u < 4; ++u) x[u] = pow2((kRev ? gap + (float)u : gap - (float)u) * rf.l2);
         f0 = pk2(x[0], x[1]), f1 = pk2(x[2], x[3]);
+        // Bits k and k + 1 of keep to the halves of a word.
+        auto halves = [=](int k) { return ((((keep >> k) & 3u) * 0x8001u) & 0x10001u) * 0xFFFFu; };
+        k0 = halves(0), k1 = halves(2);
     }
     const uint64_t x0 = mul2(pair2(v), f0), x1 = mul2(pair2(v + 2), f1);
-    p[0] = pack2(x0) & keep.x;
-    p[1] = pack2(x1) & keep.y;
-    if constexpr (kFine) {
-        rest[0] = remainder2(x0, pack2(x0)) & keep.x;
-        rest[1] = remainder2(x1, pack2(x1)) & keep.y;
-    }
+    p[0] = pack2(x0);
+    p[1] = pack2(x1);
+    rest[0] = remainder2(x0, p[0]) & k0;
+    rest[1] = remainder2(x1, p[1]) & k1;
+    p[0] &= k0;
+    p[1] &= k1;
 }
 
 // Scores of block column `blk` (bm in the order of summation) to packed P: 16 of them over the
-// first 8 of their columns, with kFine what the packing leaves over the other 8. No other warp
+// first 8 of their columns, what the packing leaves over the other 8. No other warp
 // reads or writes those. Loops are kept rolled: what
 // the compiler keeps of unrolled ones from chunk to chunk is spilled, and does not fit the
 // little L1 that two CTAs leave (backwards in time the call took 1.8 times as long).
-template <bool kRev, bool kTable, bool kFine>
+template <bool kRev, bool kTable>
 __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
     const int lane = threadIdx.x & 31;
-    const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2), own = (float)lane;
+    const float r = pow2((float)(rf.im - 32 * bm - 31) * rf.l2);
     const uint64_t r2 = pk2(r, r);
-    const uint32_t at = tm_p + 32 * blk;
+    const uint32_t at = tm_p + 32 * blk, keep = kRev ? 0xFFFFFFFFu << lane : 0xFFFFFFFFu >> (31 - lane);
 #pragma unroll 1
     for (int half = 0; half < 32; half += 16) {
         uint32_t v[16], p[8], rest[8];
@@ -393,15 +422,19 @@ __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int 
                     const uint64_t x0 = mul2(mul2(pair2(v + e), f.x), r2), x1 = mul2(mul2(pair2(v + e + 2), f.y), r2);
                     p[e / 2] = pack2(x0);
                     p[e / 2 + 1] = pack2(x1);
-                    if constexpr (kFine) rest[e / 2] = remainder2(x0, p[e / 2]), rest[e / 2 + 1] = remainder2(x1, p[e / 2 + 1]);
+                    rest[e / 2] = remainder2(x0, p[e / 2]);
+                    rest[e / 2 + 1] = remainder2(x1, p[e / 2 + 1]);
                 }
             } else {
+                const float gap = (float)(kRev ? half - lane : lane - half);   // a count: times l2 it is rounded once
+                const uint32_t bits = keep >> half;
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) diagonal4<kRev, kTable, kFine>(v + e, half + e, rf, own, m, p + e / 2, rest + e / 2);
+                for (int e = 0; e < 16; e += 4)
+                    diagonal4<kRev, kTable>(v + e, half + e, rf, kRev ? gap + (float)e : gap - (float)e, bits >> e, m, p + e / 2, rest + e / 2);
             }
         }
         tmem_st8(at + half, p);
-        if constexpr (kFine) tmem_st8(at + half + 8, rest);
+        tmem_st8(at + half + 8, rest);
     }
 }
 
@@ -443,7 +476,7 @@ template <bool kRev, bool kTable> __device__ __forceinline__ void init_tables(Mi
             m.diag[32 * (j & ~3) + 4 * lane + (j & 3)] = gap >= 0 ? pow2((float)gap * l2) : 0.f;
         }
     if (tid < 32) m.tab[tid] = pow2((float)(kRev ? tid : 31 - tid) * l2);
-    if (tid < 256)
+    if (kTable && tid < 256)
         for (int e = 2 * (tid >> 5); e < 2 * (tid >> 5) + 2; ++e) {
             const bool a = kRev ? 2 * e >= lane : 2 * e <= lane, b = kRev ? 2 * e + 1 >= lane : 2 * e + 1 <= lane;
             m.mask[32 * (e & ~1) + 2 * lane + (e & 1)] = (a ? 0xFFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
@@ -454,8 +487,7 @@ __device__ __forceinline__ RowFactors row_factors(float l2, int im) {
     return {l2, im};
 }
 
-// kFine: P in two terms.
-template <int kT, int kU, int kTerms, bool kRev, bool kFine>
+template <int kT, int kU, int kTerms, bool kRev>
 __global__ void __launch_bounds__(32 * (kU * kWork + 2), Smem<kT, kU, kTerms>::kPerSm)
 decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap omap,
@@ -464,6 +496,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     using M = Tm<kU>;
     constexpr int kWarps = kU * kWork;
     constexpr uint32_t kCols = kU == 1 ? 256 : 512;
+    constexpr int kLow = kRev && kT == 1 ? 64 : 0;     // the state's first lane: where the warps have few scores to convert
     extern __shared__ __align__(1024) uint8_t base[];
     Misc& m = *reinterpret_cast<Misc*>(base + L::kMisc);
     auto ctile = [&](int i, int u) { return base + L::kC0 + ((i % L::kStages) * kU + u) * kTile; };
@@ -479,9 +512,9 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         return;
     }
     if (tid == 0) {
-        for (uint64_t* bar : {&m.a_full, &m.b_full, &m.c_full[0], &m.c_full[1], &m.p_full, &m.s_full, &m.o_full, &m.drain})
+        for (uint64_t* bar : {&m.a_full, &m.b_full, &m.c_full[0], &m.c_full[1], &m.p_full[0], &m.s_full, &m.o_full[0], &m.drain})
             mbar_init(bar, 1);
-        for (uint64_t* bar : {&m.prep, &m.pt, &m.staged}) mbar_init(bar, kWarps);
+        for (uint64_t* bar : {&m.prep, &m.pt[0], &m.staged}) mbar_init(bar, kWarps);
         fence_mbar_init();
         m.any = kNone;
     }
@@ -514,7 +547,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 4 * kT; ++k) mma_bf16(tmem + M::kP, kmajor_step(ak, k), kmajor_step(bk, k), id_sc, k > 0);
-                mma_commit(&m.p_full);
+                mma_commit(&m.p_full[0]);
                 return true;
             };
             ok = scores(0);
@@ -522,20 +555,23 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                 if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4 * kT; ++k)                                                        // (2)
-                    mma_bf16(tmem + M::kO2, kmajor_step(ak, k), step_desc(sr, k * 2048), id_o, k > 0);
-                issue_state<kU, kTerms>(tmem + M::kSt, br, base_a + L::kW);                             // (4)
+                for (int part = L::kReads - 1; part >= 0; --part)                                       // (2)
+#pragma unroll
+                    for (int k = 0; k < 4 * kT; ++k)
+                        mma_bf16(tmem + M::kO2, kmajor_step(ak, k), step_desc(sr, part * kU * kT * kTile / 2 + k * 2048), id_o,
+                                 part < L::kReads - 1 || k > 0);
+                issue_state<kU, kTerms>(tmem + M::kSt, kLow ? br - (kTile >> 4) : br, base_a + L::kW);                             // (4)
                 mma_commit(&m.s_full);
-                if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
+                if (!(ok = mbar_wait(&m.pt[0], i & 1, max_spin))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int part = kFine ? 1 : 0; part >= 0; --part)                                       // (3)
+                for (int part = 1; part >= 0; --part)                                                   // (3)
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k)
                         mma_bf16_ts(tmem + M::kO1, tmem + M::kP + 16 * k + 8 * part,
-                                    step_desc(cr, (i % L::kStages) * kU * kTile + k * 2048), id_o, part < (kFine ? 1 : 0) || k > 0);
-                mma_commit(&m.o_full);
-                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
+                                    step_desc(cr, (i % L::kStages) * kU * kTile + k * 2048), id_o, part < 1 || k > 0);
+                mma_commit(&m.o_full[0]);
+                if (!(ok = mbar_wait(&m.o_full[0], i & 1, max_spin))) break;
                 if (i + 1 < pl.nc) ok = scores(i + 1);
             }
             mma_commit(&m.drain);              // every product completes before the CTA exits
@@ -610,14 +646,15 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         const int q = warp & 3, g4 = warp >> 2, u = g4 >> 1, g = g4 & 1, row = 32 * q + lane;
         const int qm = kRev ? 3 - q : q, im = kRev ? 127 - row : row;
         const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16), tmu = tm + 64 * u + 32 * g;
-        const bool has_state = q < 2 * kT;
+        const bool has_state = row >= kLow && row < kLow + 64 * kT;
+        const int srow = row - kLow;
         const int64_t state = (int64_t)a.Da * a.Dc, bh = (int64_t)pl.b * a.H + pl.h;
         const RowFactors rf = row_factors(l2, im);
         uint8_t *terms = base + L::kW + u * kTerms * kTile, *s_tile = base + L::kS + u * kT * kTile / 2;
-        // State row `row`, columns col0 + 64 u + 32 g ..
+        // State row `srow`, columns col0 + 64 u + 32 g ..
         float st[32];
         const int c0 = pl.col0 + 64 * u + 32 * g;
-        if (has_state) start_state(a, pl, l, row, c0, st);
+        if (has_state) start_state(a, pl, l, srow, c0, st);
         const float read = a.scale * pow2((float)(im + 1) * l2);   // weight of the state in this row's output
         const Factor whole = factor(kC * log_decay(l));
         // w C of a chunk, once C is there. Rows past the sequence's end are cleared in C, and in B
@@ -638,38 +675,42 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             if (!write_weighted<kTerms>(ct, terms, w, row, 4 * g)) take_out(ct, row, 32 * g, 32 * g + 32, i * kC + im, &m.any, m.first + 64 * u);
             return true;
         };
-        if (L::kStages == 2 && pl.nc > 0) ok = weigh(0);
+        auto put_state = [&]() {
+            if (has_state) write_state<L::kReads>(s_tile, kU * kT * kTile / 2, st, srow, 4 * g);
+        };
+        if (pl.nc > 0) ok = weigh(0);              // S0 on its way meanwhile
+        put_state();
         for (int i = 0; i < pl.nc && ok; ++i) {
             const int t0 = pl.chunk<kRev>(i) * kC, mt = min(kC, pl.n - t0);
             const bool ragged = mt < kC && pl.n < a.N;
             uint8_t* ct = ctile(i, u);
-            // ---------------------------------------------------- state to bf16, w C
-            if (has_state) write_state(s_tile, st, row, 4 * g);
-            if (L::kStages == 1 && !(ok = weigh(i))) break;
+            // ---------------------------------------------------- the operands of (2) and (4) are there
+            if (L::kStages == 1 && i > 0 && !(ok = weigh(i))) break;
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
             // ---------------------------------------------------- scores to P
-            if (!(ok = warp_wait(&m.p_full, i & 1, max_spin))) break;
+            if (!(ok = warp_wait(&m.p_full[0], i & 1, max_spin))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int bm = g4; bm < 4; bm += 2 * kU)
-                scores_to_p<kRev, false, kFine>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
+                scores_to_p<kRev, false>(tm + M::kP, kRev ? 3 - bm : bm, bm, qm, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
             auto hand_over = [&]() {
                 tmem_st_wait();
                 tc_fence_before();
-                warp_arrive(&m.pt);
+                warp_arrive(&m.pt[0]);
             };
             if (kU > 1) hand_over();
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
             if (has_state) join_state(tmu + M::kSt, kRev || mt == kC ? whole : factor((float)mt * log_decay(l)), st);
             if (kU == 1) hand_over();              // (3) takes the columns of (4)
-            // ---------------------------------------------------- the next w C, under (3)
+            // ---------------------------------------------------- the next w C and state, under (3)
             if (L::kStages == 2 && i + 1 < pl.nc && !(ok = weigh(i + 1))) break;
+            put_state();
             // ---------------------------------------------------- output
-            if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
+            if (!(ok = warp_wait(&m.o_full[0], i & 1, max_spin))) break;
             tc_fence_after();
             const bool spoiled = *const_cast<volatile int*>(&m.any) != kNone;
 #pragma unroll
@@ -696,11 +737,11 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             tc_fence_before();
             warp_arrive(&m.staged);
         }
-        if (ok && returns && has_state && row < a.Da)
+        if (ok && returns && has_state && srow < a.Da)
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
                 if (c0 + k < a.Dc)
-                    *reinterpret_cast<float4*>(a.S_out + bh * state + (int64_t)row * a.Dc + c0 + k) =
+                    *reinterpret_cast<float4*>(a.S_out + bh * state + (int64_t)srow * a.Dc + c0 + k) =
                         make_float4(st[k], st[k + 1], st[k + 2], st[k + 3]);
     }
     if (!ok) report_timeout(hdr);
@@ -869,10 +910,16 @@ decay_sums_kernel(const __grid_constant__ CUtensorMap bmap0, const __grid_consta
 // so (4) and the state are unit 0's alone, and unit 1 reads the same bf16 tile transposed.
 // Sixteen working warps, one CTA per SM; every tile double buffered, and the outputs staged in
 // tiles of their own, so that a chunk's places take the next but one as soon as its products
-// are done. For the steps that the units share a warp owns 16 columns.
+// are done. For the steps that the units share a warp owns 16 columns. Backwards in time the rows
+// of low lanes have the most scores to convert: the state lies in the high ones, (4) taking the
+// tile before Q's for the rows that nobody reads. (1), P, (3) and the output of the units are handed
+// on separately, unit 1 ahead, whose (3) waits for no sum of (4): one unit's steps run under the
+// other's products. (Handed on together, with the state in the low lanes: B=8 N=4096 H=8 D=64 122 us
+// in all, not 105.)
 enum { kTileK, kTileV, kTileQ, kTileG };
 struct KvSmem {
-    static constexpr uint32_t kW = 8 * kTile, kO = kW + 2 * kTile, kS = kO + 2 * kTile, kMisc = kS + kTile / 2;
+    static constexpr int kReads = 2;
+    static constexpr uint32_t kW = 8 * kTile, kO = kW + 2 * kTile, kS = kO + 2 * kTile, kMisc = kS + kReads * kTile / 2;
     static constexpr int kBytes = kMisc + misc_bytes(true);
 };
 static_assert(KvSmem::kBytes <= 227 * 1024, "shared memory");
@@ -901,8 +948,9 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
         return;
     }
     if (tid == 0) {
-        for (uint64_t* bar : {&m.c_full[0], &m.c_full[1], &m.p_full, &m.s_full, &m.o_full, &m.o_free, &m.drain}) mbar_init(bar, 1);
-        for (uint64_t* bar : {&m.prep, &m.pt, &m.staged}) mbar_init(bar, kWarps);
+        for (uint64_t* bar : {&m.c_full[0], &m.c_full[1], &m.p_full[0], &m.p_full[1], &m.s_full, &m.o_full[0], &m.o_full[1], &m.o_free, &m.drain}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&m.prep, &m.pt[0], &m.staged}) mbar_init(bar, kWarps);
+        mbar_init(&m.pt[1], kWork);
         fence_mbar_init();
         m.any = kNone;
     }
@@ -930,39 +978,52 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             constexpr uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, 64, false, true), id_t = idesc_bf16_f32(128, 64, false, false);
             auto at = [&](uint64_t d, int i, int k) { return step_desc(d, ((i & 1) * 4 + k) * kTile); };
-            auto scores = [&](int i) -> bool {                                                          // (1)
-                if (!mbar_wait(&m.c_full[i & 1], (i >> 1) & 1, max_spin)) return false;
-                tc_fence_after();
+            auto scores = [&](int i, int u) {                                                           // (1)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + 128 * u, kmajor_step(at(km, i, u), k), kmajor_step(at(km, i, 2 + u), k), id_sc, k > 0);
-                mma_commit(&m.p_full);
-                return true;
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(tmem + 128 * u, kmajor_step(at(km, i, u), k), kmajor_step(at(km, i, 2 + u), k), id_sc, k > 0);
+                mma_commit(&m.p_full[u]);
             };
-            ok = scores(0);
+            auto outputs = [&](int i, int u) {                                                          // (3)
+#pragma unroll
+                for (int part = 1; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_bf16_ts(tmem + kKvX + 128 * u, tmem + 128 * u + 16 * k + 8 * part,
+                                    step_desc(at(rows, i, u ? kTileQ : kTileG), k * 2048), id_o, part < 1 || k > 0);
+                mma_commit(&m.o_full[u]);
+            };
+            if ((ok = mbar_wait(&m.c_full[0], 0, max_spin))) {
+                tc_fence_after();
+                scores(0, 1);
+                scores(0, 0);
+            }
             for (int i = 0; i < pl.nc && ok; ++i) {
                 if (!(ok = mbar_wait(&m.prep, i & 1, max_spin))) break;
                 tc_fence_after();
+                issue_state<1, 2>(tmem + kKvX, at(rows, i, kTileQ - 1), base_a + L::kW);                // (4)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {                                                           // (2)
-                    mma_bf16(tmem + kKvO2, kmajor_step(at(km, i, kTileK), k), step_desc(sr, k * 2048), id_o, k > 0);
-                    mma_bf16(tmem + kKvO2 + 128, kmajor_step(at(km, i, kTileV), k), kmajor_step(sk, k), id_t, k > 0);
-                }
-                issue_state<1, 2>(tmem + kKvX, at(rows, i, kTileQ), base_a + L::kW);                    // (4)
+                for (int part = L::kReads - 1; part >= 0; --part)                                       // (2)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t more = part < L::kReads - 1 || k > 0, term = part * kTile / 2;
+                        mma_bf16(tmem + kKvO2 + 128, kmajor_step(at(km, i, kTileV), k), step_desc(kmajor_step(sk, k), term), id_t, more);
+                        mma_bf16(tmem + kKvO2, kmajor_step(at(km, i, kTileK), k), step_desc(sr, term + k * 2048), id_o, more);
+                    }
                 mma_commit(&m.s_full);
-                if (!(ok = mbar_wait(&m.pt, i & 1, max_spin))) break;
+                if (!(ok = mbar_wait(&m.pt[1], i & 1, max_spin))) break;
                 tc_fence_after();
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)                                                   // (3)
-                        mma_bf16_ts(tmem + kKvX + 128 * u, tmem + 128 * u + 16 * k,
-                                    step_desc(at(rows, i, u ? kTileQ : kTileG), k * 2048), id_o, k > 0);
-                mma_commit(&m.o_full);
-                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;
-                if (i + 1 < pl.nc) ok = scores(i + 1);
+                outputs(i, 1);
+                if (!(ok = mbar_wait(&m.pt[0], i & 1, max_spin))) break;
+                tc_fence_after();
+                outputs(i, 0);
+                const bool more = i + 1 < pl.nc;
+                if (more && !(ok = mbar_wait(&m.c_full[(i + 1) & 1], ((i + 1) >> 1) & 1, max_spin))) break;
+                for (int u = 1; u >= 0; --u) {
+                    if (!(ok = mbar_wait(&m.o_full[u], i & 1, max_spin))) break;
+                    tc_fence_after();
+                    if (more) scores(i + 1, u);
+                }
             }
             mma_commit(&m.drain);
             ok = mbar_wait(&m.drain, 0, kDefaultMaxSpin) && ok;
@@ -992,7 +1053,7 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             load();
             if (pl.nc > 1) load();
             for (int i = 0; i < pl.nc; ++i) {
-                if (!(ok = mbar_wait(&m.o_full, i & 1, max_spin))) break;     // the last to read a chunk's tiles
+                if (!(ok = mbar_wait(&m.o_full[0], i & 1, max_spin))) break;  // the last to read a chunk's tiles
                 if (i + 2 < pl.nc) load();
                 // The outputs, staged by the working warps; a ragged chunk's were written row by row.
                 if (!(ok = mbar_wait(&m.staged, i & 1, max_spin))) break;
@@ -1012,17 +1073,18 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
     } else {
         const int q = warp & 3, g4 = warp >> 2, u = g4 >> 1, g = g4 & 1, row = 32 * q + lane, im = 127 - row;
         const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16), tmu = tm + kKvX + 128 * u + 32 * g;
-        const bool has_state = q < 2;
+        const bool has_state = q >= 2;             // few scores to convert there
         const RowFactors rf = row_factors(l2, im);
-        // State row `row`, columns 16 g4 ..
+        // State row `row - 64`, columns 16 g4 ..
         float st[16];
-        if (has_state) start_state(a, pl, l, row, 16 * g4, st);
+        if (has_state) start_state(a, pl, l, row - 64, 16 * g4, st);
         const float read = a.scale * pow2((float)(im + 1) * l2), w = pow2((float)row * l2);
         const Factor whole = factor(kC * log_decay(l));
         const Tensor& out = u ? dk : a.o;
         const int width = u ? a.Da : a.Dc;
-        // w dout of a chunk, once its tiles are there; which of its values are finite.
-        bool fine_g = true, fine_q = true;
+        // w dout of a chunk, once its tiles are there; whether the values that this unit's (3)
+        // reads are finite.
+        bool fine = true;
         auto weigh = [&](int i) -> bool {
             const int mt = min(kC, pl.n - pl.chunk<true>(i) * kC);
             uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ);
@@ -1031,45 +1093,51 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
                 clear_pieces<2>(gt, row, 2 * g4);
                 clear_pieces<2>(qt, row, 2 * g4);
             }
-            fine_g = write_weighted<2, 2>(gt, base + L::kW, w, row, 2 * g4);
-            fine_q = true;
-#pragma unroll
-            for (int j = 2 * g4; j < 2 * g4 + 2; ++j) {
-                const uint4 x = *reinterpret_cast<const uint4*>(qt + row * 128 + ((j ^ (row & 7)) << 4));
-                for (uint32_t v : {x.x, x.y, x.z, x.w}) fine_q = fine_q && (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
-            }
+            write_weighted<2, 2>(gt, base + L::kW, w, row, 2 * g4);
+            // (Rows past the sequence's end may not be clear yet: taking values out of them does no harm.)
+            fine = finite_pieces(u ? qt : gt, row, 4 * g);
             return true;
         };
+        auto put_state = [&]() {
+            if (has_state) write_state<L::kReads>(base + L::kS, kTile / 2, st, row - 64, 2 * g4);
+        };
         ok = weigh(0);
+        put_state();
         for (int i = 0; i < pl.nc && ok; ++i) {
             const int t0 = pl.chunk<true>(i) * kC, mt = min(kC, pl.n - t0);
             const bool ragged = mt < kC && pl.n < a.N;
             uint8_t *gt = tile(i, kTileG), *qt = tile(i, kTileQ), *ct = base + L::kO + u * kTile;
-            // ---------------------------------------------------- state to bf16
-            if (has_state) write_state(base + L::kS, st, row, 2 * g4);
+            // ---------------------------------------------------- the operands of (2) and (4) are there
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&m.prep);
             // ---------------------------------------------------- scores to P
-            if (!(ok = warp_wait(&m.p_full, i & 1, max_spin))) break;
+            if (!(ok = warp_wait(&m.p_full[u], i & 1, max_spin))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int bm = g; bm < 4; bm += 2) scores_to_p<true, true, false>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
+            for (int bm = g; bm < 4; bm += 2) scores_to_p<true, true>(tm + 128 * u, 3 - bm, bm, 3 - q, rf, m, ragged ? mt : kC);
             // ---------------------------------------------------- state
+            auto hand_over = [&](uint64_t* to) {
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(to);
+            };
+            if (u == 1 && fine) hand_over(&m.pt[1]);
             if (!(ok = warp_wait(&m.s_full, i & 1, max_spin))) break;
             tc_fence_after();
             if (has_state) join_state(tm + kKvX + 16 * g4, whole, st);
             // (1) and (4) have read the tiles as they came; (3) must not read values that are not finite.
-            if (!fine_g) take_out(gt, row, 16 * g4, 16 * g4 + 16, i * kC + im, &m.any, m.first);
-            if (!fine_q) take_out(qt, row, 16 * g4, 16 * g4 + 16, i * kC + im, &m.any, m.first + 64);
-            fence_proxy_async_smem();
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&m.pt);
-            // ---------------------------------------------------- the next w dout, under (3)
+            if (!fine) {
+                take_out(u ? qt : gt, row, 32 * g, 32 * g + 32, i * kC + im, &m.any, m.first + 64 * u);
+                fence_proxy_async_smem();
+                if (u == 1) hand_over(&m.pt[1]);
+            }
+            hand_over(&m.pt[0]);                       // its (3) takes the columns of (4)
+            // ---------------------------------------------------- the next w dout and state, under (3)
             if (i + 1 < pl.nc && !(ok = weigh(i + 1))) break;
+            put_state();
             // ---------------------------------------------------- output
-            if (!(ok = warp_wait(&m.o_full, i & 1, max_spin))) break;
+            if (!(ok = warp_wait(&m.o_full[u], i & 1, max_spin))) break;
             tc_fence_after();
             if (i > 0 && !(ok = warp_wait(&m.o_free, (i - 1) & 1, max_spin))) break;
             const bool spoiled = *const_cast<volatile int*>(&m.any) != kNone;
@@ -1151,13 +1219,13 @@ cudaError_t launch_sums(const Sum* s, int count, WsHeader* hdr, cudaStream_t st)
     return cudaPeekAtLastError();
 }
 
-template <int kT, int kU, int kTerms, bool kRev, bool kFine>
+template <int kT, int kU, int kTerms, bool kRev>
 cudaError_t launch_main(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
     static std::atomic<int> optin[kMaxDevices];
     constexpr int bytes = Smem<kT, kU, kTerms>::kBytes;
-    const cudaError_t e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev, kFine>, bytes, optin);
+    const cudaError_t e = ensure_smem_optin(decay_tc_kernel<kT, kU, kTerms, kRev>, bytes, optin);
     if (e != cudaSuccess) return e;
-    return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev, kFine>, dim3((s.a.Dc + 64 * kU - 1) / (64 * kU), s.a.nseg, s.heads()),
+    return scan::launch_after(decay_tc_kernel<kT, kU, kTerms, kRev>, dim3((s.a.Dc + 64 * kU - 1) / (64 * kU), s.a.nseg, s.heads()),
                               32 * (kU * kWork + 2), bytes, st, dependent, s.am, s.bm, s.cm, s.om, s.a, s.geo, hdr);
 }
 
@@ -1166,15 +1234,20 @@ template <int kTerms> cudaError_t sums_of(const Sum* s, int count, WsHeader* hdr
     if (s->a.Da <= 64) return s->a.Dc <= 64 ? launch_sums<1, 1, kTerms>(s, count, hdr, st) : launch_sums<1, 2, kTerms>(s, count, hdr, st);
     return s->a.Dc <= 64 ? launch_sums<2, 1, kTerms>(s, count, hdr, st) : launch_sums<2, 2, kTerms>(s, count, hdr, st);
 }
-template <int kTerms, bool kRev, bool kFine = false> cudaError_t main_of(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
+template <int kTerms, bool kRev> cudaError_t main_of(const Sum& s, bool dependent, WsHeader* hdr, cudaStream_t st) {
     if (s.a.Da <= 64)
-        return s.a.Dc <= 64 ? launch_main<1, 1, kTerms, kRev, kFine>(s, dependent, hdr, st)
-                            : launch_main<1, 2, kTerms, kRev, kFine>(s, dependent, hdr, st);
-    return s.a.Dc <= 64 ? launch_main<2, 1, kTerms, kRev, kFine>(s, dependent, hdr, st)
-                        : launch_main<2, 2, kTerms, kRev, kFine>(s, dependent, hdr, st);
+        return s.a.Dc <= 64 ? launch_main<1, 1, kTerms, kRev>(s, dependent, hdr, st)
+                            : launch_main<1, 2, kTerms, kRev>(s, dependent, hdr, st);
+    return s.a.Dc <= 64 ? launch_main<2, 1, kTerms, kRev>(s, dependent, hdr, st)
+                        : launch_main<2, 2, kTerms, kRev>(s, dependent, hdr, st);
 }
 
 bool narrow(int Dk, int Dv) { return Dk <= 64 && Dv <= 64; }
+
+// Whether dk and dv come from one pass: narrow heads of more than one chunk. One chunk has no next
+// to prepare under its products, and two CTAs per SM do more: the whole backward of N=100 D=64,
+// 160 heads 18.1 us against 20.1, 2048 heads 144 against 151 (16 heads of N=64 9.4 against 8.8).
+bool together(int N, int Dk, int Dv) { return narrow(Dk, Dv) && N > kC; }
 
 // Segments of the forward pass. CTAs run in waves, so the cut is the one whose waves times
 // chunks is least; in chunks: starting and ending a CTA 1, the first pass 0.4 of the main
@@ -1251,12 +1324,6 @@ void cut_backward(Args* a) {
     a->fold = a->nseg - 1 <= kFold;
 }
 
-// Calls of few rows take P in two bf16 terms and w C in three. A score's
-// rounding is shared by a whole row of outputs, and a row has few scores that count where the
-// sequence is short or the decay fast: over few rows such errors do not average out. They
-// are bound by their launches either way.
-bool few_rows(int64_t BH, int N) { return BH * N <= 1024; }
-
 Args cut_of(int64_t BH, int N, int Dk, int Dv, bool backward) {
     Args a = {};
     a.B = 1, a.H = (int)BH, a.N = N, a.Da = Dk, a.Dc = Dv;
@@ -1273,7 +1340,7 @@ size_t tc_seeds(int64_t BH, int N, int Dk, int Dv, bool backward) {
 
 int tc_launches(int64_t BH, int N, int Dk, int Dv, bool backward) {
     const Args a = cut_of(BH, N, Dk, Dv, backward);
-    const int sums = backward && (Dk <= 64) != (Dv <= 64) ? 2 : 1, main = !backward ? 1 : narrow(Dk, Dv) && !few_rows(BH, N) ? 2 : 3;
+    const int sums = backward && (Dk <= 64) != (Dv <= 64) ? 2 : 1, main = !backward ? 1 : together(N, Dk, Dv) ? 2 : 3;
     return main + (a.nseg > 1 ? sums + (a.fold ? 0 : 1) : 0);
 }
 
@@ -1289,12 +1356,11 @@ cudaError_t tc_run(Args a, void* ws_header, cudaStream_t st) {
         if ((e = a.S_out ? sums_of<3>(&s, 1, hdr, st) : sums_of<2>(&s, 1, hdr, st)) != cudaSuccess) return e;
         if (!a.fold && (e = launch_chain(&a, 1, kC, st)) != cudaSuccess) return e;
     }
-    if (few_rows(s.heads(), a.N)) return main_of<3, false, true>(s, a.nseg > 1, hdr, st);
     return a.S_out ? main_of<3, false>(s, a.nseg > 1, hdr, st) : main_of<2, false>(s, a.nseg > 1, hdr, st);
 }
 
 // With segments the first passes of S (for dq) and of R (for dk and dv) and their chaining; then
-// dq and dk and dv, the last two in one pass where the heads are narrow enough for its tiles.
+// dq and dk and dv, the last two in one pass where it pays.
 cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t st) {
     cut_backward(&dv);
     const bool cut = dv.nseg > 1;
@@ -1307,15 +1373,14 @@ cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t
     WsHeader* hdr = static_cast<WsHeader*>(ws_header);
     cudaError_t e;
     if (cut) {
-        const bool together = (dq.Da <= 64) == (dq.Dc <= 64);   // S and R have the same shape
-        if ((e = sums_of<2>(s, together ? 2 : 1, hdr, st)) != cudaSuccess) return e;
-        if (!together && (e = sums_of<2>(s + 1, 1, hdr, st)) != cudaSuccess) return e;
+        const bool alike = (dq.Da <= 64) == (dq.Dc <= 64);   // S and R have the same shape
+        if ((e = sums_of<2>(s, alike ? 2 : 1, hdr, st)) != cudaSuccess) return e;
+        if (!alike && (e = sums_of<2>(s + 1, 1, hdr, st)) != cudaSuccess) return e;
         const Args chained[2] = {dq, dv};
         if (!dq.fold && (e = launch_chain(chained, 2, kC, st)) != cudaSuccess) return e;
     }
-    const bool few = few_rows(s[0].heads(), dq.N);
-    if ((e = few ? main_of<3, false, true>(s[0], cut, hdr, st) : main_of<2, false>(s[0], cut, hdr, st)) != cudaSuccess) return e;
-    if (narrow(dv.Da, dv.Dc) && !few) {
+    if ((e = main_of<2, false>(s[0], cut, hdr, st)) != cudaSuccess) return e;
+    if (together(dv.N, dv.Da, dv.Dc)) {
         static std::atomic<int> optin[kMaxDevices];
         if ((e = ensure_smem_optin(decay_kv_kernel, KvSmem::kBytes, optin)) != cudaSuccess) return e;
         const KvMaps maps = {{s[1].am, s[2].am, s[1].bm, s[1].cm}, s[2].om, s[1].om};
@@ -1324,7 +1389,7 @@ cudaError_t tc_backward(Args dq, Args dk, Args dv, void* ws_header, cudaStream_t
     }
     s[1].geo.late = s[2].geo.late = 1;
     for (int i = 1; i < 3; ++i)
-        if ((e = few ? main_of<3, true, true>(s[i], true, hdr, st) : main_of<2, true>(s[i], true, hdr, st)) != cudaSuccess) return e;
+        if ((e = main_of<2, true>(s[i], true, hdr, st)) != cudaSuccess) return e;
     return cudaSuccess;
 }
 

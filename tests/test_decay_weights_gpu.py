@@ -18,7 +18,7 @@ def la():
     return m
 
 
-@pytest.mark.parametrize("B", [1])
+@pytest.mark.parametrize("B", [1, 40])
 @pytest.mark.parametrize("l", [-0.5, -0.9, -1.0, -1.3])
 def test_weights_within_a_block_of_tokens(la, l, B):
     """Two terms that cancel, so that the weight of one shows: a token `gap` back, and the token itself
