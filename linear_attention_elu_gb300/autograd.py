@@ -78,6 +78,19 @@ def _adjacent(t):
     return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
 
 
+def _whole_pieces(t):
+    """A gradient in rows of whole 16-byte pieces: t itself, or a copy where only its strides or its
+    place in memory stand against that (behind a torch.cat, say). Without them the tensor-core kernels
+    of the decayed attention and the wide groups of the norm, which the forward pass had, are closed to it."""
+    e = t.element_size()
+    if t.shape[-1] * e % 16 or t.numel() == 0:
+        return _adjacent(t)
+    rows = zip(t.shape[:-1], t.stride()[:-1])
+    if t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(n == 1 or s * e % 16 == 0 for n, s in rows):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class _DecayAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, decay, scale, lengths, token_major):
@@ -95,7 +108,10 @@ class _DecayAttention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, do):
         q, k, v, decay, lengths = ctx.saved_tensors
-        dq, dk, dv = la_decay_attn_bwd(q, k, v, _adjacent(do.to(v.dtype)), decay, ctx.scale, lengths)
+        do = _whole_pieces(do.to(v.dtype))
+        if do.stride(2) == 0:                   # one row for all tokens (a sum over them): rows of their own
+            do = do.contiguous()
+        dq, dk, dv = la_decay_attn_bwd(q, k, v, do, decay, ctx.scale, lengths)
         return dq, dk, dv, None, None, None, None
 
 
@@ -122,7 +138,7 @@ class _GroupNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, w, b, z, stats = ctx.saved_tensors
-        dx, dw, db, dz = la_group_norm_bwd(x, ctx.groups, _adjacent(dy.to(x.dtype)), stats, w, b, z, ctx.silu)
+        dx, dw, db, dz = la_group_norm_bwd(x, ctx.groups, _whole_pieces(dy.to(x.dtype)), stats, w, b, z, ctx.silu)
         return (dx, None, dw.to(w.dtype) if dw is not None else None, db.to(b.dtype) if db is not None else None,
                 dz, None, None)
 
