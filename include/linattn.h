@@ -628,8 +628,9 @@ la_status la_decay_attn_step(const void* q, const void* k, const void* v, const 
  *   (w null: 1; b null: 0; act = silu or identity; z null: factor 1)
  *  - x, z, y: rows of [B, N, C] with batch and token strides in elements (a row's values
  *    adjacent); w, b: [C]; all dtype dt. stats [B, G, 2] float32 (nullable): (mean, r), which
- *    the backward takes. C a multiple of G; B N <= 2^30; C / G <= 1024, and with N = 1 and
- *    rows that are not whole 16-byte pieces C / G <= 128 (LA_ERR_UNSUPPORTED).
+ *    the backward takes; without tokens (N = 0) nothing is written, stats neither. C a multiple
+ *    of G; B N <= 2^30; C / G <= 1024, and with N = 1 and rows that are not whole 16-byte
+ *    pieces C / G <= 128 (LA_ERR_UNSUPPORTED).
  *  - fp32 arithmetic, one rounding; statistics about the means, so that a large mean costs
  *    no digits. Sums in a fixed order: the same inputs give the same bits.
  *  - y and stats must not overlap an input, one another or the workspace (LA_ERR_INVALID_ARG).

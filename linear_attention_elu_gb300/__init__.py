@@ -1003,7 +1003,8 @@ def la_group_norm_fwd(x, groups, w=None, b=None, z=None, silu=False, eps=1e-5, y
 
     silu: act is the silu (else the identity); z [B,N,C]: the gate. A row of its own per sample (the
     heads of an attention output, tokens as samples) is N = 1. Rows may be strided. Returns y, or
-    (y, stats) with return_stats=True: stats [B,groups,2] float32 (mean, inverse deviation)."""
+    (y, stats) with return_stats=True: stats [B,groups,2] float32 (mean, inverse deviation; zeros
+    where there are no tokens)."""
     index, B, N, C, dt = _norm_args(x, groups, w, b, z)
     xs = _rows(x, "x")
     zs = _rows(z, "z") if z is not None else (0, 0)
@@ -1019,6 +1020,8 @@ def la_group_norm_fwd(x, groups, w=None, b=None, z=None, silu=False, eps=1e-5, y
             _same_device(index, stats)
         elif return_stats:
             stats = torch.empty((B, groups, 2), dtype=torch.float32, device=x.device)
+        if N == 0 and stats is not None:
+            stats.zero_()                       # the library writes nothing then
         if ws is None:
             if N != 1:
                 ws = group_norm_workspace(B, N, C, groups, x.device)
