@@ -48,6 +48,7 @@ struct NormArgs {
     float eps;
     int lanes, slots;                               // one-token form: lanes per group, per row
     int chunks, per, gb;                            // other form: blocks of rows, their rows, groups per block
+    int blocks, over;                               // its backward: blocks of sums, floats before those over a block's parts
 };
 
 // V adjacent values as stored.
@@ -470,10 +471,10 @@ struct Block {
     int b, chunk, n0, n1, g0, ng, c0, cols, sub, subs, c;
     bool on;
 };
-template <int V> __device__ __forceinline__ Block block_of_rows(const NormArgs& a) {
+template <int V> __device__ __forceinline__ Block block_of_rows(const NormArgs& a, int part) {
     Block k;
-    k.b = blockIdx.x / a.chunks;
-    k.chunk = blockIdx.x - k.b * a.chunks;
+    k.b = part / a.chunks;
+    k.chunk = part - k.b * a.chunks;
     k.n0 = k.chunk * a.per;
     k.n1 = min(k.n0 + a.per, a.N);
     k.g0 = blockIdx.y * a.gb;
@@ -512,7 +513,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) stats_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ uint4 smem[];                // [stage][thread]; then [subs][cols] means, squares
     float* sm = reinterpret_cast<float*>(smem);
-    const Block k = block_of_rows<V>(a);
+    const Block k = block_of_rows<V>(a, blockIdx.x);
     const Ring<T, V> ring(smem);
     // Sums of the differences to the thread's first row, and of their squares. That row c is one
     // of its n values of a channel, so (c - mean)^2 is at most M, the sum of squares about the
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) sta
 template <typename T, int V>
 __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) apply_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ uint4 smem[];                // [stage][x, z][thread]; [groups][2]: -mean, r
-    const Block k = block_of_rows<V>(a);
+    const Block k = block_of_rows<V>(a, blockIdx.x);
     const Ring<T, V> ring(smem);
     float* sm = reinterpret_cast<float*>(smem + (V > 1 ? kRows * 2 * blockDim.x : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -641,77 +642,95 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : 3) app
     }
 }
 
-// partial: [B chunks][2][C] sums of h xh and of h, then [B chunks][G][2] of w h and of w h xh.
-template <typename T, int V>
+// partial: [blocks][2][C] sums of h xh and of h, then [B chunks][G][2] of w h and of w h xh. kMany:
+// more samples than blocks that run at once. A block then takes every blocks-th of them, its channels'
+// sums over them in shared memory: what the weights' gradients are summed from stays a few blocks
+// per SM however many samples there are. (With a block per sample the backward of B=65536 N=4 C=320
+// bf16 took 2357 us, now 1741, and N=16 C=64 1786, now 1128. The loop costs a call without
+// it 6 %, B=16 N=1024 C=256 fp32 18.4 us for 17.3: hence two kernels.)
+template <typename T, int V, bool kMany>
 __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8 ? 2 : 3) sums_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ uint4 smem[];                // [stage][x, dy, z][thread]; then [2][subs][cols]
+    extern __shared__ uint4 smem[];                // [stage][x, dy, z][thread]; then [2][subs][cols]; behind both [2][cols]
     float* sm = reinterpret_cast<float*>(smem);
-    const Block k = block_of_rows<V>(a);
     const Ring<T, V> ring(smem);
     const bool act = a.silu != 0, gate = a.z != nullptr;
-    Vals<V> dw = all<V>(0.f), db = all<V>(0.f);
-    if (k.on) {
-        const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
-        const T* d = static_cast<const T*>(a.dy) + k.b * a.dy_bs + k.c0 + k.c;
-        const T* z = static_cast<const T*>(a.z) + (gate ? k.b * a.z_bs + k.c0 + k.c : 0);
-        int row = k.n0 + k.sub;
-        auto fetch = [&](int i, int n) {
-            if (n < k.n1) {
-                ring.fetch((i % kRows) * 3, x + n * a.x_ts);
-                ring.fetch((i % kRows) * 3 + 1, d + n * a.dy_ts);
-                if (gate) ring.fetch((i % kRows) * 3 + 2, z + n * a.z_ts);
+    for (int part = blockIdx.x;; part += gridDim.x) {
+        const bool more = kMany && part + (int)gridDim.x < a.B * a.chunks;
+        const Block k = block_of_rows<V>(a, part);
+        Vals<V> dw = all<V>(0.f), db = all<V>(0.f);
+        if (k.on) {
+            const T* x = static_cast<const T*>(a.x) + k.b * a.x_bs + k.c0 + k.c;
+            const T* d = static_cast<const T*>(a.dy) + k.b * a.dy_bs + k.c0 + k.c;
+            const T* z = static_cast<const T*>(a.z) + (gate ? k.b * a.z_bs + k.c0 + k.c : 0);
+            int row = k.n0 + k.sub;
+            auto fetch = [&](int i, int n) {
+                if (n < k.n1) {
+                    ring.fetch((i % kRows) * 3, x + n * a.x_ts);
+                    ring.fetch((i % kRows) * 3 + 1, d + n * a.dy_ts);
+                    if (gate) ring.fetch((i % kRows) * 3 + 2, z + n * a.z_ts);
+                }
+                ring.commit();
+            };
+#pragma unroll
+            for (int i = 0; i < kRows - 1; ++i) fetch(i, row + i * k.subs);
+            const float2* s = reinterpret_cast<const float2*>(a.stats) + (int64_t)k.b * a.G + k.g0;
+            const Groups<V> gr(k.c, a.Cg);
+            Vals<V> mean, r;
+            mean.make([&](int i) { return -__ldg(s + gr.g[i]).x; });
+            r.make([&](int i) { return __ldg(s + gr.g[i]).y; });
+            const Vals<V> w = weights_of<T, V>(a.w, k.c0 + k.c, true, 1.f), b = weights_of<T, V>(a.b, k.c0 + k.c, true, 0.f);
+            for (int i = 0; row < k.n1; ++i, row += k.subs) {
+                ring.template wait<kRows - 2>();
+                fetch(i + kRows - 1, row + (kRows - 1) * k.subs);
+                const Vals<V> xh = (ring.get((i % kRows) * 3, x + row * a.x_ts) + mean) * r;
+                Vals<V> zf = xh;
+                if (gate) zf = ring.get((i % kRows) * 3 + 2, z + row * a.z_ts);
+                const Vals<V> h = backward(fma(xh, w, b), ring.get((i % kRows) * 3 + 1, d + row * a.dy_ts), act, gate, zf);
+                dw = fma(h, xh, dw);
+                db = db + h;
             }
-            ring.commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kRows - 1; ++i) fetch(i, row + i * k.subs);
-        const float2* s = reinterpret_cast<const float2*>(a.stats) + (int64_t)k.b * a.G + k.g0;
-        const Groups<V> gr(k.c, a.Cg);
-        Vals<V> mean, r;
-        mean.make([&](int i) { return -__ldg(s + gr.g[i]).x; });
-        r.make([&](int i) { return __ldg(s + gr.g[i]).y; });
-        const Vals<V> w = weights_of<T, V>(a.w, k.c0 + k.c, true, 1.f), b = weights_of<T, V>(a.b, k.c0 + k.c, true, 0.f);
-        for (int i = 0; row < k.n1; ++i, row += k.subs) {
-            ring.template wait<kRows - 2>();
-            fetch(i + kRows - 1, row + (kRows - 1) * k.subs);
-            const Vals<V> xh = (ring.get((i % kRows) * 3, x + row * a.x_ts) + mean) * r;
-            Vals<V> zf = xh;
-            if (gate) zf = ring.get((i % kRows) * 3 + 2, z + row * a.z_ts);
-            const Vals<V> h = backward(fma(xh, w, b), ring.get((i % kRows) * 3 + 1, d + row * a.dy_ts), act, gate, zf);
-            dw = fma(h, xh, dw);
-            db = db + h;
+            ring.template wait<0>();
         }
-        ring.template wait<0>();
-    }
-    __syncthreads();
-    tcc::pdl_launch_dependents();
-    float *s_w = sm, *s_b = sm + k.subs * k.cols;
-    if (k.on)
+        __syncthreads();
+        if (!more) tcc::pdl_launch_dependents();
+        float *s_w = sm, *s_b = sm + k.subs * k.cols;
+        if (k.on)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            s_w[k.sub * k.cols + k.c + i] = dw.get(i);
-            s_b[k.sub * k.cols + k.c + i] = db.get(i);
+            for (int i = 0; i < V; ++i) {
+                s_w[k.sub * k.cols + k.c + i] = dw.get(i);
+                s_b[k.sub * k.cols + k.c + i] = db.get(i);
+            }
+        __syncthreads();
+        float* channel = a.partial + (int64_t)blockIdx.x * 2 * a.C + k.c0;
+        float* over = sm + a.over;                 // the sums over the block's parts, a thread's own channels
+        const bool first = !kMany || part == (int)blockIdx.x;
+        for (int c = threadIdx.x; c < k.cols; c += blockDim.x) {
+            float u = 0.f, v = 0.f;
+            for (int s = 0; s < k.subs; ++s) u += s_w[s * k.cols + c], v += s_b[s * k.cols + c];
+            if (first && !more) {
+                channel[c] = u;
+                channel[a.C + c] = v;
+            } else {
+                const float du = first ? u : over[c] + u, dv = first ? v : over[k.cols + c] + v;
+                (more ? over : channel)[c] = du;
+                (more ? over + k.cols : channel + a.C)[c] = dv;
+            }
+            const float w = a.w ? to_f(static_cast<const T*>(a.w)[k.c0 + c]) : 1.f;
+            s_w[c] = w * u;
+            s_b[c] = w * v;
         }
-    __syncthreads();
-    float* channel = a.partial + (int64_t)blockIdx.x * 2 * a.C + k.c0;
-    for (int c = threadIdx.x; c < k.cols; c += blockDim.x) {
-        float u = 0.f, v = 0.f;
-        for (int s = 0; s < k.subs; ++s) u += s_w[s * k.cols + c], v += s_b[s * k.cols + c];
-        channel[c] = u;
-        channel[a.C + c] = v;
-        const float w = a.w ? to_f(static_cast<const T*>(a.w)[k.c0 + c]) : 1.f;
-        s_w[c] = w * u;
-        s_b[c] = w * v;
-    }
-    __syncthreads();
-    float2* group = reinterpret_cast<float2*>(a.partial + (int64_t)a.B * a.chunks * 2 * a.C) + (int64_t)blockIdx.x * a.G + k.g0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int g = warp; g < k.ng; g += blockDim.x >> 5) {
-        float u = 0.f, v = 0.f;
-        for (int c = lane; c < a.Cg; c += 32) u += s_b[g * a.Cg + c], v += s_w[g * a.Cg + c];
-        u = lanes_sum(u, 32);
-        v = lanes_sum(v, 32);
-        if (lane == 0) group[g] = make_float2(u, v);
+        __syncthreads();
+        float2* group = reinterpret_cast<float2*>(a.partial + (int64_t)a.blocks * 2 * a.C) + (int64_t)part * a.G + k.g0;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        for (int g = warp; g < k.ng; g += blockDim.x >> 5) {
+            float u = 0.f, v = 0.f;
+            for (int c = lane; c < a.Cg; c += 32) u += s_b[g * a.Cg + c], v += s_w[g * a.Cg + c];
+            u = lanes_sum(u, 32);
+            v = lanes_sum(v, 32);
+            if (lane == 0) group[g] = make_float2(u, v);
+        }
+        if (!more) break;
+        __syncthreads();                           // the next rows take the place of the sums
     }
 }
 
@@ -723,11 +742,11 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8
     if (extra >= 0) {
         tcc::pdl_wait();
         if (blockIdx.y == 0)
-            sum_weights(a.partial, extra & 1 ? a.db : a.dw, (int64_t)a.B * a.chunks, a.C, extra >> 1, extra & 1,
+            sum_weights(a.partial, extra & 1 ? a.db : a.dw, a.blocks, a.C, extra >> 1, extra & 1,
                         reinterpret_cast<float*>(smem));
         return;
     }
-    const Block k = block_of_rows<V>(a);
+    const Block k = block_of_rows<V>(a, blockIdx.x);
     const Ring<T, V> ring(smem);
     float* sm = reinterpret_cast<float*>(smem + (V > 1 ? kRows * 3 * blockDim.x : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -749,7 +768,7 @@ __global__ void __launch_bounds__(V == 1 ? kMost : kThreads, V == 1 ? 1 : V == 8
 #pragma unroll
     for (int i = 0; i < kRows - 1; ++i) fetch(i, row + i * k.subs);
     tcc::pdl_wait();
-    const float2* parts = reinterpret_cast<const float2*>(a.partial + (int64_t)a.B * a.chunks * 2 * a.C);
+    const float2* parts = reinterpret_cast<const float2*>(a.partial + (int64_t)a.blocks * 2 * a.C);
     const float inv = -1.f / ((float)a.N * a.Cg);
     for (int g = warp; g < k.ng; g += blockDim.x >> 5) {
         const float2* p = parts + (int64_t)k.b * a.chunks * a.G + k.g0 + g;
@@ -800,6 +819,12 @@ void cut_rows(int B, int N, int per_sm, int* per, int* chunks) {
     p = p < 16 ? 16 : p;
     *per = (int)p;
     *chunks = (int)((N + p - 1) / p);
+}
+
+// Blocks of the backward's sums: as many as run at once.
+int sum_blocks(int64_t parts, int per_sm) {
+    const int64_t most = (int64_t)per_sm * tcc::sm_count();
+    return (int)(parts < most ? parts : most);
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -858,7 +883,8 @@ bool launch_exact(const NormArgs& a, cudaStream_t st, cudaError_t* e) {
 
 template <typename T, int V, bool kBackward>
 cudaError_t launch_blocks(NormArgs a, cudaStream_t st) {
-    cut_rows(a.B, a.N, kBackward && V == 8 ? 2 : kMostPerSm, &a.per, &a.chunks);
+    const int per_sm = kBackward && V == 8 ? 2 : kMostPerSm;
+    cut_rows(a.B, a.N, per_sm, &a.per, &a.chunks);
     // Whole groups per block, whole vectors: as many as its threads hold.
     const int unit = V / gcd(a.Cg, V), hold = (V == 1 ? kMost : kThreads) * V / a.Cg;
     a.gb = hold >= a.G ? a.G : hold / unit * unit;
@@ -868,8 +894,8 @@ cudaError_t launch_blocks(NormArgs a, cudaStream_t st) {
     const int sums = 2 * (int)sizeof(float) * subs * a.gb * a.Cg, group = 2 * (int)sizeof(float) * a.gb;
     auto ring = [&](int places) { return V > 1 ? places * threads * 16 : 0; };
     auto larger = [](int p, int q) { return p > q ? p : q; };
-    static std::atomic<int> optin[2][tcc::kMaxDevices];
-    constexpr int kMostRing = V > 1 ? 3 * kRows * kThreads * 16 : 0, kMostSums = 2 * 4 * kThreads * V * (V == 1 ? 4 : 1);
+    static std::atomic<int> optin[3][tcc::kMaxDevices];
+    constexpr int kMostRing = V > 1 ? 3 * kRows * kThreads * 16 : 0, kMostSums = 2 * 2 * 4 * kThreads * V * (V == 1 ? 4 : 1);
     cudaError_t e;
     if constexpr (!kBackward) {
         if ((e = tcc::ensure_smem_optin(stats_kernel<T, V>, kMostRing + kMostSums, optin[0])) != cudaSuccess ||
@@ -879,10 +905,16 @@ cudaError_t launch_blocks(NormArgs a, cudaStream_t st) {
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         return scan::launch_after(apply_kernel<T, V>, grid, threads, ring(2 * kRows) + group, st, true, a);
     } else {
-        if ((e = tcc::ensure_smem_optin(sums_kernel<T, V>, kMostRing + kMostSums, optin[0])) != cudaSuccess ||
+        if ((e = tcc::ensure_smem_optin(sums_kernel<T, V, false>, kMostRing + kMostSums, optin[0])) != cudaSuccess ||
+            (e = tcc::ensure_smem_optin(sums_kernel<T, V, true>, kMostRing + kMostSums, optin[2])) != cudaSuccess ||
             (e = tcc::ensure_smem_optin(apply_bwd_kernel<T, V>, kMostRing + kMostSums, optin[1])) != cudaSuccess)
             return e;
-        sums_kernel<T, V><<<grid, threads, larger(ring(3 * kRows), sums), st>>>(a);
+        const int parts = a.B * a.chunks, room = larger(ring(3 * kRows), sums);
+        a.blocks = sum_blocks(parts, per_sm);
+        a.over = room / (int)sizeof(float);
+        const dim3 sum_grid((unsigned)a.blocks, grid.y);
+        if (parts > a.blocks) sums_kernel<T, V, true><<<sum_grid, threads, room + 2 * (int)sizeof(float) * a.gb * a.Cg, st>>>(a);
+        else sums_kernel<T, V, false><<<sum_grid, threads, room, st>>>(a);
         if ((e = cudaPeekAtLastError()) != cudaSuccess) return e;
         dim3 more = grid;
         if (a.dw || a.db) more.x += 2 * ((a.C + 31) / 32);
@@ -918,7 +950,8 @@ size_t norm_workspace(int B, int N, int C, int G) {
     if (B == 0 || N == 0) return 0;
     int per, chunks;
     cut_rows(B, N, kMostPerSm, &per, &chunks);
-    const size_t blocks = sizeof(float) * (size_t)B * chunks * (2 * (size_t)C + 2 * (size_t)G);
+    const int64_t parts = (int64_t)B * chunks;
+    const size_t blocks = sizeof(float) * 2 * ((size_t)sum_blocks(parts, kMostPerSm) * C + (size_t)parts * G);
     const size_t rows = sizeof(float) * 2 * (size_t)row_blocks() * C;
     return ((N == 1 ? rows : blocks) + 255) & ~(size_t)255;
 }
