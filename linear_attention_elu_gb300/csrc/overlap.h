@@ -100,6 +100,17 @@ struct Rows3 {
 // make up for. Where strides nest, which those of a tensor's views do, that is two or three
 // steps per axis. What 2^14 steps do not show counts as apart.
 inline bool overlap(const Rows3& x, const Rows3& y) {
+    const int64_t apart = (int64_t)(reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p));
+    int64_t low[2] = {}, high[2] = {x.row, y.row};
+    for (int which = 0; which < 2; ++which) {
+        const Rows3& r = which ? y : x;
+        if (!r.p || r.row < 1) return false;
+        for (int i = 0; i < 3; ++i) {
+            if (r.count[i] < 1) return false;
+            (r.stride[i] < 0 ? low : high)[which] += (r.count[i] - 1) * r.stride[i];
+        }
+    }
+    if (apart + low[1] >= high[0] || low[0] >= apart + high[1]) return false;
     struct Axis {
         int64_t s, lo, hi;
     } axis[6];
@@ -107,10 +118,8 @@ inline bool overlap(const Rows3& x, const Rows3& y) {
     int64_t row[2] = {x.row, y.row}, base[2] = {};
     for (int which = 0; which < 2; ++which) {
         const Rows3& r = which ? y : x;
-        if (!r.p || r.row < 1) return false;
         int64_t count[3], stride[3];
         for (int i = 0; i < 3; ++i) {
-            if (r.count[i] < 1) return false;
             count[i] = r.stride[i] == 0 ? 1 : r.count[i], stride[i] = r.stride[i];   // 0: the same rows again
             if (stride[i] < 0) base[which] += (count[i] - 1) * stride[i], stride[i] = -stride[i];   // from the other end
         }
@@ -142,7 +151,6 @@ inline bool overlap(const Rows3& x, const Rows3& y) {
             if (self(self, k + 1, d + c * s)) return true;
         return false;
     };
-    const int64_t apart = (int64_t)(reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p));
     return meet(meet, 0, apart + base[1] - base[0]);
 }
 
