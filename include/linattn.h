@@ -578,7 +578,9 @@ la_status la_selective_scan_step(const void* x, int64_t x_batch, const void* ste
  *    only o reads are sums of two bf16 terms (2^-16 of each value is left at most), whatever the
  *    call's size. Where Dk and Dv are both above 64 the state where o reads it is one bf16
  *    value (2^-8). The state is held in fp32; what a token adds to it enters S_out as three terms.
- *  - An infinity or NaN in a token's row reaches no output of an earlier token.
+ *  - An infinity or NaN in a token's row reaches no output of an earlier token. Its own and the
+ *    later ones, and S_out, hold an infinity or NaN, on the tensor cores NaN for either (an
+ *    infinity has no second term); one in v stays in its column.
  *  - o and S_out must not overlap an input (but S_out == S0), one another or the workspace,
  *    and o's rows must not overlap among themselves (LA_ERR_INVALID_ARG). That is decided
  *    from the strides, exactly for the views of a tensor; of rows that interleave otherwise
