@@ -118,32 +118,6 @@ struct Geo {
                                 // started after that launch had seen the chained seeds
 };
 
-__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpk2(uint64_t v, float* lo, float* hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t bf2(uint32_t u) {   // two packed bf16 as fp32 pair
-    return pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t pack2(uint64_t v) {
-    float a, b;
-    unpk2(v, &a, &b);
-    return pack_bf16(a, b);
-}
 // What packing left of x, packed.
 __device__ __forceinline__ uint32_t remainder2(uint64_t x, uint32_t hi) { return pack2(fma2(bf2(hi), pk2(-1.f, -1.f), x)); }
 __device__ __forceinline__ uint64_t pair2(const uint32_t* v) { return pk2(__uint_as_float(v[0]), __uint_as_float(v[1])); }

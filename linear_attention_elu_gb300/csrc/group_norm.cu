@@ -66,36 +66,19 @@ template <typename T, int V> __device__ __forceinline__ Raw<T, V> load(const T* 
 
 // V values in fp32, as packed pairs: half the instructions, which bound these kernels next to
 // memory.
-__device__ __forceinline__ uint64_t pk(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
 __device__ __forceinline__ float lo_of(uint64_t v) {
     float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    unpk2(v, &a, &b);
     return a;
 }
 __device__ __forceinline__ float hi_of(uint64_t v) {
     float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    unpk2(v, &a, &b);
     return b;
 }
-__device__ __forceinline__ uint64_t add1(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul1(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma1(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
+__device__ __forceinline__ uint64_t add1(uint64_t a, uint64_t b) { return add2(a, b); }
+__device__ __forceinline__ uint64_t mul1(uint64_t a, uint64_t b) { return mul2(a, b); }
+__device__ __forceinline__ uint64_t fma1(uint64_t a, uint64_t b, uint64_t c) { return fma2(a, b, c); }
 __device__ __forceinline__ float add1(float a, float b) { return a + b; }
 __device__ __forceinline__ float mul1(float a, float b) { return a * b; }
 __device__ __forceinline__ float fma1(float a, float b, float c) { return fmaf(a, b, c); }
@@ -106,7 +89,7 @@ template <int V> struct Vals {
     __device__ __forceinline__ float get(int i) const { return i & 1 ? hi_of(p[i >> 1]) : lo_of(p[i >> 1]); }
     template <typename F> __device__ __forceinline__ void make(F f) {       // value i = f(i)
 #pragma unroll
-        for (int i = 0; i < n; ++i) p[i] = pk(f(2 * i), f(2 * i + 1));
+        for (int i = 0; i < n; ++i) p[i] = pk2(f(2 * i), f(2 * i + 1));
     }
 };
 template <> struct Vals<1> {
@@ -156,9 +139,9 @@ template <typename T, int V> __device__ __forceinline__ Vals<V> floats(const Raw
     } else if constexpr (sizeof(T) == 2) {
         const uint32_t u[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f.p[i] = pk(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+        for (int i = 0; i < 4; ++i) f.p[i] = pk2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
     } else {
-        f.p[0] = pk(r.v.x, r.v.y), f.p[1] = pk(r.v.z, r.v.w);
+        f.p[0] = pk2(r.v.x, r.v.y), f.p[1] = pk2(r.v.z, r.v.w);
     }
     return f;
 }

@@ -1,12 +1,13 @@
 // Device helpers of the token-mixing operators (norm and rotation, convolution,
-// selective scan) beyond those of the attention kernels: the silu and the 4-D TMA
-// copies of strided rows.
+// selective scan, decayed attention, group norm) beyond those of the attention kernels: the silu,
+// pairs of fp32 values in one register pair, and the 4-D TMA copies of strided rows.
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "tc_common.cuh"
 #include "tc_util.cuh"
 
 namespace la {
@@ -19,6 +20,39 @@ __device__ __forceinline__ float silu(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return v * r;
+}
+
+// Two fp32 values as one operand: half the instructions of a pair's operations.
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpk2(uint64_t v, float* lo, float* hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t bf2(uint32_t u) {   // two packed bf16 as fp32 pair
+    return pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+    float a, b;
+    unpk2(v, &a, &b);
+    return tcc::pack_bf16(a, b);
 }
 
 namespace tc {
