@@ -1027,10 +1027,12 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
             load();
             if (pl.nc > 1) load();
             for (int i = 0; i < pl.nc; ++i) {
-                if (!(ok = mbar_wait(&m.o_full[0], i & 1, max_spin))) break;  // the last to read a chunk's tiles
-                if (i + 2 < pl.nc) load();
-                // The outputs, staged by the working warps; a ragged chunk's were written row by row.
+                // The outputs, staged by the working warps; a ragged chunk's were written row by row. They
+                // are there after (3), the last to read a chunk's tiles. (The barrier of (3) itself could
+                // complete the next chunk's phase before it is looked at here: the next but one
+                // needs these loads, the next does not. This one's next phase needs o_free.)
                 if (!(ok = mbar_wait(&m.staged, i & 1, max_spin))) break;
+                if (i + 2 < pl.nc) load();
                 const int t = pl.chunk<true>(i) * kC;
                 if (t + kC <= pl.n || pl.n == a.N) {
                     tma_store_4d(&maps.dv, base + L::kO, 0, pl.h, t, pl.b);
