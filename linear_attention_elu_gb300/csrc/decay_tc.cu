@@ -13,15 +13,15 @@
 // A CTA walks the chunks of a segment of one head, for one or two "units" of 64 columns of
 // C and of the state ((1) and P serve both).
 //
-// Roundings. A, B, C enter as they are. P and the state of (2) enter as two bf16 terms, the second the
-// remainder of the first: 2^-16 of a value is left at most, so that what an output loses beside its own
-// rounding depends neither on how many scores make it nor on the call's size. (One term of each: 2.3e-3
-// to 2.4e-3 off in all where the output's rounding is 1.7e-3. What the second terms cost: B=1 N=65536 H=16
-// D=64 154 us for 143, B=8 N=4096 H=8 D=64 backward 105 for 90.) Where both widths are above 64 the state has
-// one term, see Smem. The state is held in fp32 in
-// registers; (4) is summed per chunk from zero and added there, so that the tensor core's
-// sums stay short. w C enters it as bf16 terms as well: two for a
-// state that only o reads, three for one that the call returns.
+// Roundings. A, B, C enter as they are. P and the state of (2) enter as two bf16 terms, the second
+// the remainder of the first: 2^-16 of a value is left at most, so that what an output loses beside
+// its own rounding depends neither on how many scores make it nor on the call's size. (One term of
+// each: 2.3e-3 to 2.4e-3 off in all where the output's rounding is 1.7e-3. What the second terms
+// cost, replayed from a graph: B=1 N=65536 H=16 D=64 154 us for 143, B=8 N=4096 H=8 D=64 backward
+// 105 for 90.) Where both widths are above 64 the state has one term, see Smem. The state is held
+// in fp32 in registers; (4) is summed per chunk from zero and added there, so that the tensor core's
+// sums stay short. w C enters it as bf16 terms as well: two for a state that only o reads, three
+// for one that the call returns.
 // Weights below the diagonal 32 x 32 blocks are products of two factors <= 1, one of the
 // row and one of the column; the diagonal blocks take a factor per score. Every
 // factor's exponent is a count of tokens times l, so none is a difference of larger ones.
@@ -335,11 +335,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 
 // Four scores of a diagonal block, columns j .. j + 3, to packed P. Scores that take no part are
 // cleared as bits: their products may be anything. kTable: factors from the table (one CTA
-// per SM; with two the table's reads from shared memory cost more than the exponentials: B=1
-// N=65536 H=16 D=64 forward 151 us against 148, the backward of B=8 N=4096 H=8 D=64 with one 91
-// against 92.5).
+// per SM; with two the table's reads from shared memory cost more than the exponentials: with P in
+// one term, B=1 N=65536 H=16 D=64 forward 151 us against 148, the backward of B=8 N=4096 H=8 D=64
+// with one 91 against 92.5).
 template <bool kRev, bool kTable>
-__device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float gap, uint32_t keep, const Misc& m, uint32_t* p, uint32_t* rest) {
+__device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFactors& rf, float gap, uint32_t keep,
+                                          const Misc& m, uint32_t* p, uint32_t* rest) {
     uint64_t f0, f1;
     uint32_t k0, k1;
     if constexpr (kTable) {
@@ -366,10 +367,10 @@ __device__ __forceinline__ void diagonal4(const uint32_t* v, int j, const RowFac
 }
 
 // Scores of block column `blk` (bm in the order of summation) to packed P: 16 of them over the
-// first 8 of their columns, what the packing leaves over the other 8. No other warp
-// reads or writes those. Loops are kept rolled: what
-// the compiler keeps of unrolled ones from chunk to chunk is spilled, and does not fit the
-// little L1 that two CTAs leave (backwards in time the call took 1.8 times as long).
+// first 8 of their columns, what the packing leaves over the other 8. No other warp reads or
+// writes those. Loops are kept rolled: what the compiler keeps of unrolled ones from chunk to chunk
+// is spilled, and does not fit the little L1 that two CTAs leave (backwards in time the call took
+// 1.8 times as long).
 template <bool kRev, bool kTable>
 __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int qm, const RowFactors& rf, const Misc& m, int cut) {
     const int lane = threadIdx.x & 31;
@@ -404,7 +405,8 @@ __device__ __forceinline__ void scores_to_p(uint32_t tm_p, int blk, int bm, int 
                 const uint32_t bits = keep >> half;
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
-                    diagonal4<kRev, kTable>(v + e, half + e, rf, kRev ? gap + (float)e : gap - (float)e, bits >> e, m, p + e / 2, rest + e / 2);
+                    diagonal4<kRev, kTable>(v + e, half + e, rf, kRev ? gap + (float)e : gap - (float)e, bits >> e, m,
+                                            p + e / 2, rest + e / 2);
             }
         }
         tmem_st8(at + half, p);
@@ -534,7 +536,7 @@ decay_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                     for (int k = 0; k < 4 * kT; ++k)
                         mma_bf16(tmem + M::kO2, kmajor_step(ak, k), step_desc(sr, part * kU * kT * kTile / 2 + k * 2048), id_o,
                                  part < L::kReads - 1 || k > 0);
-                issue_state<kU, kTerms>(tmem + M::kSt, kLow ? br - (kTile >> 4) : br, base_a + L::kW);                             // (4)
+                issue_state<kU, kTerms>(tmem + M::kSt, kLow ? br - (kTile >> 4) : br, base_a + L::kW);  // (4)
                 mma_commit(&m.s_full);
                 if (!(ok = mbar_wait(&m.pt[0], i & 1, max_spin))) break;
                 tc_fence_after();
@@ -922,7 +924,9 @@ decay_kv_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ Arg
         return;
     }
     if (tid == 0) {
-        for (uint64_t* bar : {&m.c_full[0], &m.c_full[1], &m.p_full[0], &m.p_full[1], &m.s_full, &m.o_full[0], &m.o_full[1], &m.o_free, &m.drain}) mbar_init(bar, 1);
+        for (uint64_t* bar : {&m.c_full[0], &m.c_full[1], &m.p_full[0], &m.p_full[1], &m.s_full, &m.o_full[0],
+                              &m.o_full[1], &m.o_free, &m.drain})
+            mbar_init(bar, 1);
         for (uint64_t* bar : {&m.prep, &m.pt[0], &m.staged}) mbar_init(bar, kWarps);
         mbar_init(&m.pt[1], kWork);
         fence_mbar_init();
@@ -1246,8 +1250,8 @@ int forward_segments(int64_t BH, int N, int Dk, int Dv) {
 // Segments of the backward pass, the same for dq and for dk and dv, in chunks of the main
 // passes as above. Those run side by side while their CTAs fit the SMs together (two of dq to
 // one where heads are narrow), else one after the other. Single calls on a cold L2, B=8 N=4096 H=8
-// D=64, 32 chunks: not cut 100 us, two segments 120, four 130; B=4 N=2047 H=8 D=128, 16 chunks:
-// 65, 89, 99.
+// D=64, 32 chunks, P in one term: not cut 100 us, two segments 120, four 130; B=4 N=2047 H=8
+// D=128, 16 chunks: 65, 89, 99.
 int backward_segments(int64_t BH, int N, int Dk, int Dv) {
     const int chunks = (N + kC - 1) / kC;
     const double sms = sm_count(), shares[3] = {narrow(Dk, Dv) ? 0.5 : 1.0, 1.0, narrow(Dk, Dv) ? 0.0 : 1.0};
